@@ -422,7 +422,7 @@ def _fork_own(s):
     kv, tab, ws = s["kv"], s["tab"], s["workspace"]
     qp.qpack_kv_free(tab, s["dst"])
     qp.qpack_kv_fork(kv, tab, s["src"], s["dst"], workspace=ws)
-    qp.qpack_kv_reserve(tab, s["dst"], s["add"])
+    qp.qpack_kv_reserve(kv, tab, s["dst"], s["add"])
     return {"tables": s["tables"], "lens": s["lens"], "refs": s["refs"], "k": s["pool"]["k"], "v": s["pool"]["v"]}
 
 
