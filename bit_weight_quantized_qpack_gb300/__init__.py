@@ -20,6 +20,8 @@ FORMATS = {"Q4G32": Q4G32, "Q2S": Q2S, "Q3S": Q3S, "Q5S": Q5S, "Q6S": Q6S, "Q4G3
 F32, F16, BF16 = 0, 1, 2
 FLAG_RANGE = 1
 FAULT_NONFINITE_X = 16
+FAULT_PAGE, FAULT_NO_PAGES = 32, 64
+KV_I8, KV_F16, KV_BF16 = 0, 1, 2
 # (sub-blocks per super-block, asymmetric) for the super-block formats
 _SB = {Q2S: (16, True), Q3S: (16, False), Q5S: (8, True), Q6S: (16, False)}
 
@@ -38,6 +40,21 @@ class Layout(ctypes.Structure):
                 ("scale_stride", ctypes.c_int64), ("scale_bytes", ctypes.c_int64),
                 ("block_bytes", ctypes.c_int64), ("nsub", ctypes.c_int64),
                 ("weight_bytes", ctypes.c_int64)]
+
+
+class _Pool(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("layer_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("scale_layer_stride", ctypes.c_int64), ("scale_page_stride", ctypes.c_int64),
+                ("pages", ctypes.c_int64), ("layers", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("dim", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class _Tables(ctypes.Structure):
+    _fields_ = [("tables", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("stride", ctypes.c_int64), ("pages", ctypes.c_int64), ("seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
 
 
 def lib():
@@ -61,6 +78,17 @@ def lib():
                 "qgemm_prefill": ([I, P, P, I64, I64, I64, P, I64, P, I64, P], I),
                 "qpack_kv_quantize": ([P, I64, P, P, P], I),
                 "qpack_kv_dequant": ([P, P, I64, P, P], I),
+                "qpack_kv_append": ([P, I, P, P, P, I64, P, P, I, I64, I64, P, I64, P], I),
+                "qpack_kv_read": ([P, I, P, P, P, I64, P, P, I, I64, I64, P], I),
+                "qpack_kv_attend": ([P, I, P, P, I, P, I, I64, I, ctypes.c_float, I64, P, I64, P, I, I64, P, P, I64, P],
+                                    I),
+                "qpack_kv_attend_workspace": ([P, I, I, ctypes.POINTER(I64)], I),
+                "qpack_kv_reserve": ([P, P, P, P, I64, P], I),
+                "qpack_kv_fork": ([P, P, P, P, I64, P, I64, P], I),
+                "qpack_kv_free": ([P, P, I64, P], I),
+                "qpack_kv_compact": ([P, P, P, P, P, P, I64, P], I),
+                "qpack_kv_copy_pages": ([P, P, P, I64, P], I),
+                "qpack_kv_page_workspace": ([P, P, ctypes.POINTER(I64)], I),
                 "qpack_status_string": ([I], ctypes.c_char_p),
                 "qpack_fetch_fault_flags": ([ctypes.POINTER(ctypes.c_int32)], I),
                 "qpack_version": ([], I),
@@ -267,6 +295,278 @@ def qpack_kv_dequant(codes, scales, out=None, stream=None):
     _check(lib().qpack_kv_dequant(_ptr(codes), _ptr(scales), codes.numel(), _ptr(out), _stream(stream)),
            "qpack_kv_dequant")
     return out
+
+
+class KVPool:
+    """A paged KV cache: keys and values [layers, pages, heads, page_tokens, dim], int8 codes with fp16 scales
+    [layers, pages, heads, page_tokens, dim / 32], or fp16 / bf16 without scales. The layer and page strides are free (a
+    slice of a larger buffer will do), everything inside a page is contiguous. Holds its tensors; it can be kept for as
+    long as they live."""
+
+    def __init__(self, k, v, k_scales=None, v_scales=None):
+        kind = {torch.int8: KV_I8, torch.float16: KV_F16, torch.bfloat16: KV_BF16}.get(k.dtype)
+        if kind is None:
+            raise QpackError(f"k: expected int8, float16 or bfloat16, got {k.dtype}")
+        if (kind == KV_I8) != (k_scales is not None) or (kind == KV_I8) != (v_scales is not None):
+            raise QpackError("k_scales, v_scales: given for int8 pools and for no other")
+        sets = [("k", k, k.dtype, 0), ("v", v, k.dtype, 0)]
+        if kind == KV_I8:
+            sets += [("k_scales", k_scales, torch.float16, 1), ("v_scales", v_scales, torch.float16, 1)]
+        for name, t, dtype, scales in sets:
+            if t.dtype != dtype:
+                raise QpackError(f"{name}: expected {dtype}, got {t.dtype}")
+            shape = tuple(k.shape[:-1]) + ((k.shape[-1] // 32,) if scales else (k.shape[-1],))
+            if t.dim() != 5 or tuple(t.shape) != shape:
+                raise QpackError(f"{name}: expected [layers, pages, heads, page_tokens, dim{' / 32' if scales else ''}] "
+                                 f"of {shape}, got {tuple(t.shape)}")
+            inner = (t.shape[3] * t.shape[4], t.shape[4], 1)
+            if any(n > 1 and st != want for n, st, want in zip(t.shape[2:], t.stride()[2:], inner)):
+                raise QpackError(f"{name}: pages are not contiguous, strides {tuple(t.stride())}")
+            same = (k if not scales else k_scales).stride()
+            if any(n > 1 and a != b for n, a, b in zip(t.shape[:2], t.stride()[:2], same)):
+                raise QpackError(f"{name}: layer and page strides differ from {'k_scales' if scales else 'k'}'s")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        layers, pages, heads, page_tokens, dim = k.shape
+        self.layers, self.pages, self.heads, self.page_tokens, self.dim = layers, pages, heads, page_tokens, dim
+
+        def strides(t):                                         # of an extent of one they mean nothing
+            page = t[0, 0].numel() if t.numel() else 0
+            ps = t.stride(1) if t.shape[1] > 1 else page
+            return (t.stride(0) if t.shape[0] > 1 else 0), ps
+
+        ls, ps = strides(k)
+        sls, sps = strides(k_scales) if kind == KV_I8 else (0, 0)
+        self._c = _Pool(_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales), ls, ps, sls, sps, pages, layers, heads,
+                        page_tokens, dim, kind, 0)
+        self._ref = ctypes.byref(self._c)
+
+
+def alloc_kv_pool(kind, layers, pages, heads, page_tokens, dim, device="cuda") -> KVPool:
+    """An empty pool of the kind KV_I8, KV_F16 or KV_BF16."""
+    dt = {KV_I8: torch.int8, KV_F16: torch.float16, KV_BF16: torch.bfloat16}[kind]
+    shape = (layers, pages, heads, page_tokens, dim)
+    k, v = (torch.zeros(shape, dtype=dt, device=device) for _ in range(2))
+    if kind != KV_I8:
+        return KVPool(k, v)
+    ks, vs = (torch.zeros(shape[:-1] + (dim // 32,), dtype=torch.float16, device=device) for _ in range(2))
+    return KVPool(k, v, ks, vs)
+
+
+class KVTables:
+    """The sequences of a pool: page table int32 [seqs, max_pages] (-1: no page), lengths int32 [seqs] and reference
+    counts int32 [pages] (not needed by append, read and attend). Holds its tensors."""
+
+    def __init__(self, tables, lens, refs=None):
+        if tables.dtype != torch.int32 or tables.dim() != 2 or (tables.shape[1] > 1 and tables.stride(1) != 1):
+            raise QpackError(f"tables: expected a row-major int32 matrix, got {tables.dtype} {tuple(tables.shape)} with "
+                             f"strides {tuple(tables.stride())}")
+        _need(lens, torch.int32, "lens", numel=tables.shape[0])
+        if refs is not None:
+            _need(refs, torch.int32, "refs", numel=0)
+        self.tables, self.lens, self.refs = tables, lens, refs
+        stride = tables.stride(0) if tables.shape[0] > 1 else tables.shape[1]
+        self._c = _Tables(_ptr(tables), _ptr(lens), _ptr(refs), stride, 0 if refs is None else refs.numel(),
+                          tables.shape[0], tables.shape[1])
+        self._ref = ctypes.byref(self._c)
+
+
+def alloc_kv_tables(seqs, max_pages, pages, device="cuda") -> KVTables:
+    """Empty sequences over a pool of `pages` free pages."""
+    return KVTables(torch.full((seqs, max_pages), -1, dtype=torch.int32, device=device),
+                    torch.zeros(seqs, dtype=torch.int32, device=device),
+                    torch.zeros(pages, dtype=torch.int32, device=device))
+
+
+_DTYPE_CODE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+
+
+def _need_rows(t, what, heads, dim):
+    """Token rows: [n, heads * dim] or [n, heads, dim], a row contiguous. Returns (dtype code, row stride)."""
+    code = _DTYPE_CODE.get(t.dtype)
+    if code is None:
+        raise QpackError(f"{what}: expected float32, float16 or bfloat16, got {t.dtype}")
+    shape, st, nd = t.shape, t.stride(), t.dim()
+    if nd == 2:
+        ok = shape[1] == heads * dim and st[1] == 1
+    else:
+        ok = nd == 3 and shape[1] == heads and shape[2] == dim and st[2] == 1 and (heads == 1 or st[1] == dim)
+    if not ok:
+        raise QpackError(f"{what}: expected rows of {heads} x {dim}, got {tuple(shape)} with strides {tuple(st)}")
+    return code, (st[0] if shape[0] > 1 else heads * dim)
+
+
+def _need_i32(t, what, n):
+    if t is not None:
+        _need(t, torch.int32, what, numel=n)
+
+
+def _need_rope(rope, dim):
+    """Rows of the rotation table."""
+    if rope is None:
+        return 0
+    if rope.dtype != torch.float32 or rope.dim() != 2 or rope.shape[1] != dim or not rope.is_contiguous():
+        raise QpackError(f"rope: expected a contiguous float32 [positions, {dim}] table, got {rope.dtype} "
+                         f"{tuple(rope.shape)}")
+    return rope.shape[0]
+
+
+def qpack_kv_append(pool, layer, tables, k, v, seqs=None, pos=None, rope=None, stream=None):
+    """Write new tokens' keys and values (rows [n, heads, dim], float32, float16 or bfloat16) into a layer of the cache:
+    token i at position pos[i] of sequence seqs[i] (default: the last token of sequence i). Keys are rotated first
+    where `rope` (float32 [positions, dim]: cos | sin) is given; int8 pools quantize by qpack_kv_quantize's rule."""
+    dt, ldk = _need_rows(k, "k", pool.heads, pool.dim)
+    dtv, ldv = _need_rows(v, "v", pool.heads, pool.dim)
+    n = k.shape[0]
+    if dtv != dt or v.shape[0] != n:
+        raise QpackError("k, v: expected the same type and number of rows")
+    _need_i32(seqs, "seqs", n)
+    _need_i32(pos, "pos", n)
+    rows = _need_rope(rope, pool.dim)
+    rc = lib().qpack_kv_append(pool._ref, layer, tables._ref, _ptr(seqs), _ptr(pos), n, _ptr(k), _ptr(v), dt, ldk, ldv,
+                               _ptr(rope), rows, _stream(stream))
+    _check(rc, "qpack_kv_append")
+
+
+def qpack_kv_read(pool, layer, tables, seqs=None, pos=None, k_out=None, v_out=None, n=None, stream=None):
+    """Rows of the cache: token i from position pos[i] of sequence seqs[i] (as in qpack_kv_append). Returns (k, v),
+    [n, heads, dim], float16 (bfloat16 for a bfloat16 pool) unless given."""
+    given = next((t for t in (seqs, pos, k_out, v_out) if t is not None), None)
+    if n is None:
+        if given is None:
+            raise QpackError("n: needed where neither seqs, pos nor an output is given")
+        n = given.shape[0]
+    if k_out is None and v_out is None:
+        dt = torch.bfloat16 if pool.k.dtype == torch.bfloat16 else torch.float16
+        k_out, v_out = (torch.empty((n, pool.heads, pool.dim), dtype=dt, device=pool.k.device) for _ in range(2))
+    ld = {}
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None:
+            ld[name] = _need_rows(t, name, pool.heads, pool.dim)
+            if t.shape[0] < n:
+                raise QpackError(f"{name}: expected at least {n} rows, got {t.shape[0]}")
+    if len({c for c, _ in ld.values()}) != 1:
+        raise QpackError("k_out, v_out: expected the same type")
+    _need_i32(seqs, "seqs", n)
+    _need_i32(pos, "pos", n)
+    dt = next(iter(ld.values()))[0]
+    rc = lib().qpack_kv_read(pool._ref, layer, tables._ref, _ptr(seqs), _ptr(pos), n, _ptr(k_out), _ptr(v_out), dt,
+                             ld.get("k_out", (0, 0))[1], ld.get("v_out", (0, 0))[1], _stream(stream))
+    _check(rc, "qpack_kv_read")
+    return k_out, v_out
+
+
+class KVWorkspace:
+    """Scratch memory of a call, laid out once. Attention's is zeroed here and left ready by every call; calls that may
+    run at the same time need one each."""
+
+    def __init__(self, bytes, device):
+        self.buffer = torch.zeros(bytes, dtype=torch.uint8, device=device)
+        self._p = _ptr(self.buffer)
+        self.bytes = bytes
+
+
+def alloc_kv_workspace(pool, batch, q_heads) -> KVWorkspace:
+    """For qpack_kv_attend with up to `batch` rows."""
+    n = ctypes.c_int64(0)
+    _check(lib().qpack_kv_attend_workspace(pool._ref, batch, q_heads, ctypes.byref(n)), "qpack_kv_attend_workspace")
+    return KVWorkspace(n.value, pool.k.device)
+
+
+def alloc_kv_page_workspace(pool, tables) -> KVWorkspace:
+    """For qpack_kv_fork and qpack_kv_compact."""
+    n = ctypes.c_int64(0)
+    _check(lib().qpack_kv_page_workspace(pool._ref, tables._ref, ctypes.byref(n)), "qpack_kv_page_workspace")
+    return KVWorkspace(n.value, pool.k.device)
+
+
+def qpack_kv_attend(pool, layer, tables, q, seqs=None, scale=None, window=0, rope=None, out=None, lse=None,
+                    workspace=None, stream=None):
+    """Attention of one new token a row: q [B, q_heads, dim] or [B, q_heads * dim] (float32, float16 or bfloat16) over the
+    cache of sequence seqs[b] (default b), its last `window` tokens where that is not 0. scale defaults to dim ** -0.5.
+    Returns out, of q's shape, float16 unless given (float32 and bfloat16 too); lse, a float32 [B, q_heads] tensor if
+    wanted, gets the log-sum-exp. A kept workspace (alloc_kv_workspace) saves its allocation."""
+    D = pool.dim
+    B = q.shape[0]
+    width = q.shape[1] * (D if q.dim() == 3 else 1)
+    q_heads = width // D
+    qdt, ldq = _need_rows(q, "q", q_heads, D)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+    odt, ldo = _need_rows(out, "out", q_heads, D)
+    if out.shape[0] < B:
+        raise QpackError(f"out: expected at least {B} rows, got {out.shape[0]}")
+    _need_i32(seqs, "seqs", B)
+    if seqs is None and tables.tables.shape[0] < B:
+        raise QpackError(f"q: {B} rows, but the table has {tables.tables.shape[0]} sequences")
+    if lse is not None:
+        _need(lse, torch.float32, "lse", numel=B * q_heads)
+    if workspace is None:
+        workspace = alloc_kv_workspace(pool, B, q_heads)
+    rows = _need_rope(rope, D)
+    rc = lib().qpack_kv_attend(pool._ref, layer, tables._ref, _ptr(seqs), B, _ptr(q), qdt, ldq, q_heads,
+                               D ** -0.5 if scale is None else scale, window, _ptr(rope), rows, _ptr(out), odt, ldo,
+                               _ptr(lse), workspace._p, workspace.bytes, _stream(stream))
+    _check(rc, "qpack_kv_attend")
+    return out
+
+
+def _need_refs(tables):
+    if tables.refs is None:
+        raise QpackError("tables: this call needs the reference counts")
+
+
+def qpack_kv_reserve(pool, tables, seqs, add, stream=None):
+    """Extend sequence seqs[i] by add[i] tokens, taking the lowest-numbered free pages in the order of the requests. A
+    request without enough pages is left as it was and sets FAULT_NO_PAGES."""
+    _need_refs(tables)
+    n = seqs.numel()
+    _need_i32(seqs, "seqs", n)
+    _need_i32(add, "add", n)
+    _check(lib().qpack_kv_reserve(pool._ref, tables._ref, _ptr(seqs), _ptr(add), n, _stream(stream)), "qpack_kv_reserve")
+
+
+def qpack_kv_fork(pool, tables, src, dst, workspace=None, stream=None):
+    """Make the empty sequences dst[i] copies of src[i]: full pages are shared, a part-filled last page is copied."""
+    _need_refs(tables)
+    n = src.numel()
+    _need_i32(src, "src", n)
+    _need_i32(dst, "dst", n)
+    workspace = alloc_kv_page_workspace(pool, tables) if workspace is None else workspace
+    _check(lib().qpack_kv_fork(pool._ref, tables._ref, _ptr(src), _ptr(dst), n, workspace._p, workspace.bytes,
+                               _stream(stream)), "qpack_kv_fork")
+
+
+def qpack_kv_free(tables, seqs, stream=None):
+    """Release the pages of sequences seqs[i]; they become empty."""
+    _need_refs(tables)
+    n = seqs.numel()
+    _need_i32(seqs, "seqs", n)
+    _check(lib().qpack_kv_free(tables._ref, _ptr(seqs), n, _stream(stream)), "qpack_kv_free")
+
+
+def qpack_kv_compact(pool, tables, tables_out=None, refs_out=None, moved=None, workspace=None, stream=None):
+    """Move the live pages to the lowest numbers and renumber the tables and reference counts (in place unless outputs
+    of the same layout are given). moved, an int32 tensor if wanted, gets the number of pages moved."""
+    _need_refs(tables)
+    tables_out = tables.tables if tables_out is None else tables_out
+    refs_out = tables.refs if refs_out is None else refs_out
+    if tables_out.dtype != torch.int32 or tables_out.shape != tables.tables.shape or \
+            tables_out.stride() != tables.tables.stride():
+        raise QpackError("tables_out: expected the tables' type, shape and strides")
+    _need(refs_out, torch.int32, "refs_out", numel=tables.refs.numel())
+    _need_i32(moved, "moved", 1)
+    workspace = alloc_kv_page_workspace(pool, tables) if workspace is None else workspace
+    _check(lib().qpack_kv_compact(pool._ref, tables._ref, _ptr(tables_out), _ptr(refs_out), _ptr(moved), workspace._p,
+                                  workspace.bytes, _stream(stream)), "qpack_kv_compact")
+    return tables_out, refs_out
+
+
+def qpack_kv_copy_pages(pool, src, dst, stream=None):
+    """Copy page src[i] to page dst[i] over all layers."""
+    n = src.numel()
+    _need_i32(src, "src", n)
+    _need_i32(dst, "dst", n)
+    _check(lib().qpack_kv_copy_pages(pool._ref, _ptr(src), _ptr(dst), n, _stream(stream)), "qpack_kv_copy_pages")
 
 
 def qpack_fetch_fault_flags() -> int:

@@ -150,6 +150,58 @@ int check_packed(int fmt, const void *packed, const void *gs) {
     return QPACK_OK;
 }
 
+// A pool's shape, alignment and strides. `data`: whether the call reads or writes its pages.
+int check_pool(const qpack_kv_pool_t *p, bool data = true) {
+    if (!p) return QPACK_ERR_ARG;
+    if (p->type < QPACK_KV_I8 || p->type > QPACK_KV_BF16 || p->layers < 0 || p->pages < 0) return QPACK_ERR_ARG;
+    if (p->dim != 64 && p->dim != 128 && p->dim != 256) return QPACK_ERR_SHAPE;
+    if (p->page_tokens < 1 || p->page_tokens > 1024 || (p->page_tokens & (p->page_tokens - 1))) return QPACK_ERR_SHAPE;
+    if (p->heads < 1 || p->heads > 4096 || p->pages > 0x7FFFFFFF) return QPACK_ERR_SHAPE;
+    const int64_t page = int64_t(p->heads) * p->page_tokens * p->dim;
+    const bool i8 = p->type == QPACK_KV_I8;
+    if (p->pages > 1 && p->page_stride < page) return QPACK_ERR_SHAPE;
+    if (i8 && p->pages > 1 && p->scale_page_stride < page / 32) return QPACK_ERR_SHAPE;
+    if (!data) return QPACK_OK;
+    if (p->pages > 0 && p->layers > 0 && (!p->k || !p->v || (i8 && (!p->k_scales || !p->v_scales)))) return QPACK_ERR_ARG;
+    if (!aligned(p->k, 16) || !aligned(p->v, 16) || p->page_stride % 16 || p->layer_stride % 16) return QPACK_ERR_ALIGN;
+    if (i8 && (!aligned(p->k_scales, 16) || !aligned(p->v_scales, 16) || p->scale_page_stride % (p->dim / 32) ||
+               p->scale_layer_stride % (p->dim / 32)))
+        return QPACK_ERR_ALIGN;
+    return QPACK_OK;
+}
+
+int check_tables(const qpack_kv_tables_t *t, bool need_refs) {
+    if (!t || t->seqs < 0 || t->max_pages < 0 || t->pages < 0) return QPACK_ERR_ARG;
+    if (t->seqs > 0 && (!t->lens || (t->max_pages > 0 && !t->tables))) return QPACK_ERR_ARG;
+    if (t->seqs > 1 && t->stride < t->max_pages) return QPACK_ERR_SHAPE;
+    if (need_refs && t->pages > 0 && !t->refs) return QPACK_ERR_ARG;
+    if (need_refs && t->pages > 0x7FFFFFFF) return QPACK_ERR_SHAPE;
+    if (!aligned(t->tables, 4) || !aligned(t->lens, 4) || !aligned(t->refs, 4)) return QPACK_ERR_ALIGN;
+    return QPACK_OK;
+}
+
+// Rows of token vectors: `width` elements, 16-byte aligned, a row stride of whole 8-element pieces.
+int check_rows(const void *p, int64_t ld, int64_t width) {
+    if (!p) return QPACK_ERR_ARG;
+    if (ld < width) return QPACK_ERR_SHAPE;
+    if (!aligned(p, 16) || ld % 8) return QPACK_ERR_ALIGN;
+    return QPACK_OK;
+}
+
+int check_rope(const float *rope, int64_t rows) {
+    if (rows < 0) return QPACK_ERR_ARG;
+    return aligned(rope, 16) ? QPACK_OK : QPACK_ERR_ALIGN;
+}
+
+// The page operators: a pool that covers the reference counts, and n sequences.
+int check_page_op(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, int64_t n) {
+    if (int rc = check_pool(pool)) return rc;
+    if (int rc = check_tables(t, true)) return rc;
+    if (n < 0) return QPACK_ERR_ARG;
+    if (n > 4096 || t->pages > pool->pages) return QPACK_ERR_SHAPE;
+    return QPACK_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -332,6 +384,121 @@ int qpack_kv_dequant(const int8_t *codes, const uint16_t *scales, int64_t n, uin
     return cuda_status(launch_kv_dequant(codes, scales, n, out, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int qpack_kv_append(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_t *t, const int32_t *seqs,
+                    const int32_t *pos, int64_t n, const void *k, const void *v, int dt, int64_t ldk, int64_t ldv,
+                    const float *rope, int64_t rope_rows, qpack_stream_t stream) {
+    int rc;
+    if ((rc = check_pool(pool)) || (rc = check_tables(t, false))) return rc;
+    if (layer < 0 || layer >= pool->layers || n < 0 || dt < QPACK_F32 || dt > QPACK_BF16) return QPACK_ERR_ARG;
+    if (n == 0) return QPACK_OK;
+    const int64_t width = int64_t(pool->heads) * pool->dim;
+    if ((rc = check_rows(k, ldk, width)) || (rc = check_rows(v, ldv, width)) || (rc = check_rope(rope, rope_rows)))
+        return rc;
+    if (!aligned(seqs, 4) || !aligned(pos, 4)) return QPACK_ERR_ALIGN;
+    AppendArgs a = {*pool, *t, seqs, pos, n, const_cast<void *>(k), const_cast<void *>(v), ldk, ldv, rope, rope_rows,
+                    layer, dt};
+    return cuda_status(launch_kv_append(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qpack_kv_read(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_t *t, const int32_t *seqs,
+                  const int32_t *pos, int64_t n, void *k, void *v, int dt, int64_t ldk, int64_t ldv,
+                  qpack_stream_t stream) {
+    int rc;
+    if ((rc = check_pool(pool)) || (rc = check_tables(t, false))) return rc;
+    if (layer < 0 || layer >= pool->layers || n < 0 || dt < QPACK_F32 || dt > QPACK_BF16) return QPACK_ERR_ARG;
+    if (n == 0 || (!k && !v)) return QPACK_OK;
+    const int64_t width = int64_t(pool->heads) * pool->dim;
+    if ((k && (rc = check_rows(k, ldk, width))) || (v && (rc = check_rows(v, ldv, width)))) return rc;
+    if (!aligned(seqs, 4) || !aligned(pos, 4)) return QPACK_ERR_ALIGN;
+    AppendArgs a = {*pool, *t, seqs, pos, n, k, v, ldk, ldv, nullptr, 0, layer, dt};
+    return cuda_status(launch_kv_read(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qpack_kv_attend_workspace(const qpack_kv_pool_t *pool, int B, int q_heads, int64_t *bytes) {
+    if (!bytes || B < 0 || q_heads < 1) return QPACK_ERR_ARG;
+    if (int rc = check_pool(pool, false)) return rc;
+    if (B > 4096 || q_heads % pool->heads) return QPACK_ERR_SHAPE;
+    *bytes = kv_attend_workspace(*pool, B, q_heads);
+    return QPACK_OK;
+}
+
+int qpack_kv_attend(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_t *t, const int32_t *seqs, int B,
+                    const void *q, int qdt, int64_t ldq, int q_heads, float scale, int64_t window, const float *rope,
+                    int64_t rope_rows, void *out, int odt, int64_t ldo, float *lse, void *ws, int64_t ws_bytes,
+                    qpack_stream_t stream) {
+    int rc;
+    if ((rc = check_pool(pool)) || (rc = check_tables(t, false))) return rc;
+    if (layer < 0 || layer >= pool->layers || B < 0 || q_heads < 1 || window < 0) return QPACK_ERR_ARG;
+    if (qdt < QPACK_F32 || qdt > QPACK_BF16 || odt < QPACK_F32 || odt > QPACK_BF16) return QPACK_ERR_ARG;
+    if (q_heads % pool->heads || B > 4096) return QPACK_ERR_SHAPE;
+    if (B == 0) return QPACK_OK;
+    const int64_t width = int64_t(q_heads) * pool->dim;
+    if ((rc = check_rows(q, ldq, width)) || (rc = check_rows(out, ldo, width)) || (rc = check_rope(rope, rope_rows)))
+        return rc;
+    if (!aligned(seqs, 4) || !aligned(lse, 4) || !aligned(ws, 16)) return QPACK_ERR_ALIGN;
+    if (!ws) return QPACK_ERR_ARG;
+    if (ws_bytes < kv_attend_workspace(*pool, B, q_heads)) return QPACK_ERR_SHAPE;
+    AttendArgs a = {*pool, *t, seqs, q, ldq, rope, rope_rows, out, ldo, lse, ws, window, scale, layer, B, q_heads, qdt,
+                    odt};
+    return cuda_status(launch_kv_attend(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qpack_kv_page_workspace(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, int64_t *bytes) {
+    if (!bytes) return QPACK_ERR_ARG;
+    int rc;
+    if ((rc = check_pool(pool, false)) || (rc = check_tables(t, false))) return rc;
+    *bytes = kv_page_workspace(*pool, *t);
+    return QPACK_OK;
+}
+
+int qpack_kv_reserve(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, const int32_t *seqs, const int32_t *add,
+                     int64_t n, qpack_stream_t stream) {
+    if (int rc = check_page_op(pool, t, n)) return rc;
+    if (n == 0) return QPACK_OK;
+    if (!seqs || !add) return QPACK_ERR_ARG;
+    if (!aligned(seqs, 4) || !aligned(add, 4)) return QPACK_ERR_ALIGN;
+    return cuda_status(launch_kv_reserve(*pool, *t, seqs, add, int(n), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qpack_kv_fork(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, const int32_t *src, const int32_t *dst,
+                  int64_t n, void *ws, int64_t ws_bytes, qpack_stream_t stream) {
+    if (int rc = check_page_op(pool, t, n)) return rc;
+    if (n == 0) return QPACK_OK;
+    if (!src || !dst || !ws) return QPACK_ERR_ARG;
+    if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(ws, 16)) return QPACK_ERR_ALIGN;
+    if (ws_bytes < kv_page_workspace(*pool, *t)) return QPACK_ERR_SHAPE;
+    return cuda_status(launch_kv_fork(*pool, *t, src, dst, int(n), ws, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qpack_kv_free(const qpack_kv_tables_t *t, const int32_t *seqs, int64_t n, qpack_stream_t stream) {
+    if (int rc = check_tables(t, true)) return rc;
+    if (n < 0) return QPACK_ERR_ARG;
+    if (n > 4096) return QPACK_ERR_SHAPE;
+    if (n == 0) return QPACK_OK;
+    if (!seqs) return QPACK_ERR_ARG;
+    if (!aligned(seqs, 4)) return QPACK_ERR_ALIGN;
+    return cuda_status(launch_kv_free(*t, seqs, int(n), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qpack_kv_compact(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, int32_t *tables_out, int32_t *refs_out,
+                     int32_t *moved, void *ws, int64_t ws_bytes, qpack_stream_t stream) {
+    if (int rc = check_page_op(pool, t, 0)) return rc;
+    if (!ws || (t->pages > 0 && !refs_out) || (t->seqs > 0 && t->max_pages > 0 && !tables_out)) return QPACK_ERR_ARG;
+    if (!aligned(tables_out, 4) || !aligned(refs_out, 4) || !aligned(moved, 4) || !aligned(ws, 16)) return QPACK_ERR_ALIGN;
+    if (ws_bytes < kv_page_workspace(*pool, *t)) return QPACK_ERR_SHAPE;
+    return cuda_status(launch_kv_compact(*pool, *t, tables_out, refs_out, moved, ws, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qpack_kv_copy_pages(const qpack_kv_pool_t *pool, const int32_t *src, const int32_t *dst, int64_t n,
+                        qpack_stream_t stream) {
+    if (int rc = check_pool(pool)) return rc;
+    if (n < 0) return QPACK_ERR_ARG;
+    if (n == 0) return QPACK_OK;
+    if (!src || !dst) return QPACK_ERR_ARG;
+    if (!aligned(src, 4) || !aligned(dst, 4)) return QPACK_ERR_ALIGN;
+    return cuda_status(launch_kv_copy_pages(*pool, src, dst, n, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 const char *qpack_status_string(int status) {
     switch (status) {
         case QPACK_OK: return "QPACK_OK";
@@ -350,6 +517,8 @@ int qpack_fetch_fault_flags(int32_t *flags) {
     *flags = 0;
     cudaError_t e = fetch_fault_gemv(flags);
     if (e == cudaSuccess) e = fetch_fault_prefill(flags);
+    if (e == cudaSuccess) e = fetch_fault_paged(flags);
+    if (e == cudaSuccess) e = fetch_fault_attend(flags);
     return cuda_status(e);
 }
 

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "qpack.h"
+
 namespace qpack {
 
 // Arguments of the per-256-weight-block kernels (quantize / pack / unpack / dequant). Unused pointers are null.
@@ -72,6 +74,53 @@ cudaError_t launch_kv_quantize(const uint16_t *v, int64_t n, int8_t *q, uint16_t
 cudaError_t launch_kv_dequant(const int8_t *q, const uint16_t *scales, int64_t n, uint16_t *out, cudaStream_t s);
 cudaError_t fetch_fault_gemv(int32_t *flags);
 cudaError_t fetch_fault_prefill(int32_t *flags);
+
+// Paged KV cache (qpack_paged.cu, qpack_attend.cu). The pool and the tables as the C ABI has them, checked.
+struct AppendArgs {
+    qpack_kv_pool_t pool;
+    qpack_kv_tables_t t;
+    const int32_t *seqs, *pos;   // null: token i of sequence i / its last token
+    int64_t n;
+    void *k, *v;                 // read by append, written by read (either may then be null)
+    int64_t ldk, ldv;
+    const float *rope;           // null: no rotation
+    int64_t rope_rows;
+    int layer, dt;
+};
+cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t s);
+cudaError_t launch_kv_read(const AppendArgs &a, cudaStream_t s);
+
+struct AttendArgs {
+    qpack_kv_pool_t pool;
+    qpack_kv_tables_t t;
+    const int32_t *seqs;
+    const void *q;
+    int64_t ldq;
+    const float *rope;
+    int64_t rope_rows;
+    void *out;
+    int64_t ldo;
+    float *lse;
+    void *ws;
+    int64_t window;
+    float scale;
+    int layer, B, q_heads, qdt, odt;
+};
+cudaError_t launch_kv_attend(const AttendArgs &a, cudaStream_t s);
+int64_t kv_attend_workspace(const qpack_kv_pool_t &pool, int B, int q_heads);
+
+cudaError_t launch_kv_reserve(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t, const int32_t *seqs,
+                              const int32_t *add, int n, cudaStream_t s);
+cudaError_t launch_kv_fork(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t, const int32_t *src, const int32_t *dst,
+                           int n, void *ws, cudaStream_t s);
+cudaError_t launch_kv_free(const qpack_kv_tables_t &t, const int32_t *seqs, int n, cudaStream_t s);
+cudaError_t launch_kv_compact(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t, int32_t *tables_out,
+                              int32_t *refs_out, int32_t *moved, void *ws, cudaStream_t s);
+cudaError_t launch_kv_copy_pages(const qpack_kv_pool_t &p, const int32_t *src, const int32_t *dst, int64_t n,
+                                 cudaStream_t s);
+int64_t kv_page_workspace(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t);
+cudaError_t fetch_fault_paged(int32_t *flags);
+cudaError_t fetch_fault_attend(int32_t *flags);
 
 int num_sms();
 int weight_prefetch_enabled();   // per-device option QPACK_OPT_WEIGHT_PREFETCH

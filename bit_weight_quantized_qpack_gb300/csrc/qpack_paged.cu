@@ -1,0 +1,589 @@
+// qpack_paged.cu — the paged KV cache: appending new tokens (rotary embedding, 8-bit quantization or rounding to 16
+// bits, scatter into pages), reading rows back, and the page operators (reserve, fork, free, compact, copy).
+//
+// Append and read are streams: every element is read and written once, so HBM bounds them at length and the launch at
+// a decode step's few tokens. The page operators move the pages that they have to (HBM bound) after a plan on the
+// tables alone. All of it is deterministic: pages are ranked by number and requests by place, never by arrival.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "qpack_dev.cuh"
+#include "qpack_launch.h"
+#include "qpack_quot.cuh"
+
+namespace qpack {
+namespace {
+
+__device__ int g_fault_paged = 0;
+
+// ------------------------------------------------------------------------------------------------------------
+// Append and read back
+// ------------------------------------------------------------------------------------------------------------
+constexpr int ROW_THREADS = 256;
+
+template <int DT> struct Elem { using type = uint16_t; };
+template <> struct Elem<DT_F32> { using type = float; };
+
+// Where token i of the call lives: its sequence and position, and the element offset of its page's first head.
+struct Place {
+    int64_t page;      // -1: nowhere (a skipped token, or one out of range)
+    int pos, slot;
+};
+
+__device__ __forceinline__ Place place_of(const AppendArgs &a, int64_t i) {
+    Place p = {-1, -1, 0};
+    const int64_t seq = a.seqs ? int64_t(__ldg(a.seqs + i)) : i;
+    if (seq < 0 || seq >= a.t.seqs) {
+        atomicOr(&g_fault_paged, FAULT_PAGE);
+        return p;
+    }
+    p.pos = a.pos ? __ldg(a.pos + i) : __ldg(a.t.lens + seq) - 1;
+    if (p.pos < 0) return p;
+    const int shift = 31 - __clz(a.pool.page_tokens);
+    const int col = p.pos >> shift;
+    p.slot = p.pos & (a.pool.page_tokens - 1);
+    const int page = col < a.t.max_pages ? __ldg(a.t.tables + seq * a.t.stride + col) : -1;
+    if (page < 0 || page >= a.pool.pages) {
+        atomicOr(&g_fault_paged, FAULT_PAGE);
+        return p;
+    }
+    p.page = page;
+    return p;
+}
+
+// Eight consecutive elements a lane, so a row of D takes D / 8 lanes: 32 / (D / 8) rows a warp. The rotation's partner
+// (i +- D/2) is D/16 lanes away, and the four lanes of a 32-element group reduce its maximum with two shuffles.
+template <int KT, int D, int DT>
+__global__ void __launch_bounds__(ROW_THREADS) kv_append_kernel(AppendArgs a, int64_t rows) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR;
+    const int lane = threadIdx.x & 31, sub = lane % LPR;
+    const int64_t warps = int64_t(gridDim.x) * (ROW_THREADS / 32);
+    const int H = a.pool.heads;
+    for (int64_t r0 = (int64_t(blockIdx.x) * (ROW_THREADS / 32) + (threadIdx.x >> 5)) * RPW; r0 < rows; r0 += warps * RPW) {
+        const int64_t r = r0 + lane / LPR;
+        const bool live = r < rows;
+        const int64_t tok = live ? r / (2 * H) : 0;
+        const int kh = live ? int(r - tok * 2 * H) : 0;
+        const bool is_v = kh >= H;
+        const int head = is_v ? kh - H : kh;
+        Place pl = {-1, -1, 0};
+        if (live) pl = place_of(a, tok);
+        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (pl.page >= 0) load8<DT>(is_v ? a.v : a.k, tok * (is_v ? a.ldv : a.ldk) + int64_t(head) * D + sub * 8, x);
+        if (a.rope) {                                      // uniform: the shuffles are the warp's
+            const bool turn = pl.page >= 0 && !is_v;
+            const bool in = turn && pl.pos < a.rope_rows;
+            if (turn && !in) atomicOr(&g_fault_paged, FAULT_PAGE);
+            const bool lower = sub < LPR / 2;
+            float c[8] = {1, 1, 1, 1, 1, 1, 1, 1}, s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (in) {
+                const int64_t row = int64_t(pl.pos) * D + (sub % (LPR / 2)) * 8;
+                load8<DT_F32>(a.rope, row, c);
+                load8<DT_F32>(a.rope, row + D / 2, s);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float y = __shfl_xor_sync(0xffffffffu, x[e], LPR / 2);
+                // lower half: x c - y s; upper half: x c + y s; each operation rounded
+                const float ys = __fmul_rn(y, s[e]);
+                if (in) x[e] = lower ? __fsub_rn(__fmul_rn(x[e], c[e]), ys) : __fadd_rn(__fmul_rn(x[e], c[e]), ys);
+            }
+        }
+        const int64_t in_page = (int64_t(head) * a.pool.page_tokens + pl.slot) * D + sub * 8;
+        if (KT == QPACK_KV_I8) {
+            float m = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const uint16_t d16 = f2h_bits(fminf(__fdiv_rn(m, 127.0f), 65504.0f));
+            const float d = h2f_bits(d16);
+            uint8_t cb[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (d > 0.0f) rint_codes<8>(x, d, __frcp_rn(d), 0, -127, 127, 0, cb);
+            uint32_t w[2] = {0u, 0u};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e >> 2] |= uint32_t(cb[e]) << (8 * (e & 3));
+            if (pl.page >= 0) {
+                int8_t *base = static_cast<int8_t *>(is_v ? a.pool.v : a.pool.k);
+                const int64_t at = a.layer * a.pool.layer_stride + pl.page * a.pool.page_stride + in_page;
+                *reinterpret_cast<uint2 *>(base + at) = make_uint2(w[0], w[1]);
+                if ((sub & 3) == 0) {
+                    uint16_t *sc = is_v ? a.pool.v_scales : a.pool.k_scales;
+                    sc[a.layer * a.pool.scale_layer_stride + pl.page * a.pool.scale_page_stride + in_page / 32] = d16;
+                }
+            }
+        } else if (pl.page >= 0) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (KT == QPACK_KV_F16) {
+                    w[e] = uint32_t(f2h_bits(x[2 * e])) | (uint32_t(f2h_bits(x[2 * e + 1])) << 16);
+                } else {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+                    w[e] = *reinterpret_cast<const uint32_t *>(&b);
+                }
+            }
+            uint16_t *base = static_cast<uint16_t *>(is_v ? a.pool.v : a.pool.k);
+            const int64_t at = a.layer * a.pool.layer_stride + pl.page * a.pool.page_stride + in_page;
+            *reinterpret_cast<uint4 *>(base + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+template <int DT> __device__ __forceinline__ void store8(void *p, int64_t idx, const float *x) {
+    if (DT == DT_F32) {
+        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p) + idx);
+        o[0] = make_float4(x[0], x[1], x[2], x[3]);
+        o[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (DT == DT_F16) {
+                w[e] = uint32_t(f2h_bits(x[2 * e])) | (uint32_t(f2h_bits(x[2 * e + 1])) << 16);
+            } else {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+                w[e] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+        }
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + idx) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Rows of the cache as they stand for: code x scale rounded to fp16 (the definition of the 8-bit cache), then to DT.
+template <int KT, int D, int DT>
+__global__ void __launch_bounds__(ROW_THREADS) kv_read_kernel(AppendArgs a, int64_t rows) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR;
+    const int lane = threadIdx.x & 31, sub = lane % LPR;
+    const int64_t warps = int64_t(gridDim.x) * (ROW_THREADS / 32);
+    const int H = a.pool.heads;
+    for (int64_t r0 = (int64_t(blockIdx.x) * (ROW_THREADS / 32) + (threadIdx.x >> 5)) * RPW; r0 < rows; r0 += warps * RPW) {
+        const int64_t r = r0 + lane / LPR;
+        if (r >= rows) continue;
+        const int64_t tok = r / (2 * H);
+        const int kh = int(r - tok * 2 * H);
+        const bool is_v = kh >= H;
+        const int head = is_v ? kh - H : kh;
+        void *out = is_v ? a.v : a.k;
+        if (!out) continue;
+        const Place pl = place_of(a, tok);
+        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (pl.page >= 0) {
+            const int64_t in_page = (int64_t(head) * a.pool.page_tokens + pl.slot) * D + sub * 8;
+            const int64_t at = a.layer * a.pool.layer_stride + pl.page * a.pool.page_stride + in_page;
+            const void *base = is_v ? a.pool.v : a.pool.k;
+            if (KT == QPACK_KV_I8) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const int8_t *>(base) + at);
+                const uint16_t *sc = is_v ? a.pool.v_scales : a.pool.k_scales;
+                const float d = h2f_bits(
+                    sc[a.layer * a.pool.scale_layer_stride + pl.page * a.pool.scale_page_stride + in_page / 32]);
+                const uint32_t ww[2] = {w.x, w.y};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    x[e] = h2f_bits(f2h_bits(d * float(int8_t(uint8_t(ww[e >> 2] >> (8 * (e & 3)))))));
+            } else {
+                load8<KT == QPACK_KV_F16 ? DT_F16 : DT_BF16>(base, at, x);
+            }
+        }
+        store8<DT>(out, tok * (is_v ? a.ldv : a.ldk) + int64_t(head) * D + sub * 8, x);
+    }
+}
+
+template <int KT, int D, int DT> cudaError_t run_rows(const AppendArgs &a, bool read, cudaStream_t s) {
+    const int64_t rows = a.n * 2 * a.pool.heads;
+    constexpr int per_block = (ROW_THREADS / 32) * (32 / (D / 8));
+    const int64_t need = (rows + per_block - 1) / per_block, cap = int64_t(num_sms()) * 8;
+    const int grid = int(need < cap ? need : cap);
+    if (read)
+        kv_read_kernel<KT, D, DT><<<grid, ROW_THREADS, 0, s>>>(a, rows);
+    else
+        kv_append_kernel<KT, D, DT><<<grid, ROW_THREADS, 0, s>>>(a, rows);
+    return cudaGetLastError();
+}
+
+template <int KT, int D> cudaError_t rows_dt(const AppendArgs &a, bool read, cudaStream_t s) {
+    if (a.dt == DT_F32) return run_rows<KT, D, DT_F32>(a, read, s);
+    if (a.dt == DT_F16) return run_rows<KT, D, DT_F16>(a, read, s);
+    return run_rows<KT, D, DT_BF16>(a, read, s);
+}
+
+template <int KT> cudaError_t rows_dim(const AppendArgs &a, bool read, cudaStream_t s) {
+    if (a.pool.dim == 64) return rows_dt<KT, 64>(a, read, s);
+    if (a.pool.dim == 128) return rows_dt<KT, 128>(a, read, s);
+    return rows_dt<KT, 256>(a, read, s);
+}
+
+cudaError_t rows_kind(const AppendArgs &a, bool read, cudaStream_t s) {
+    if (a.pool.type == QPACK_KV_I8) return rows_dim<QPACK_KV_I8>(a, read, s);
+    if (a.pool.type == QPACK_KV_F16) return rows_dim<QPACK_KV_F16>(a, read, s);
+    return rows_dim<QPACK_KV_BF16>(a, read, s);
+}
+
+// ------------------------------------------------------------------------------------------------------------
+// Page operators
+// ------------------------------------------------------------------------------------------------------------
+constexpr int PLAN_THREADS = 1024;
+
+// Exclusive prefix sum of one value a thread over the block; *total gets the sum. Every thread calls it.
+__device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[w] = x;
+    __syncthreads();
+    if (w == 0) {
+        int y = lane < nw ? warp_sums[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y += z;
+        }
+        if (lane < nw) warp_sums[lane] = y;
+    }
+    __syncthreads();
+    const int before = w ? warp_sums[w - 1] : 0;
+    *total = warp_sums[nw - 1];
+    __syncthreads();                                       // warp_sums may be written again
+    return before + x - v;
+}
+
+// Work of the copy kernel: rows [0, rows) of page src to page dst, in every layer.
+struct CopyItem { int src, dst, rows; };
+
+// Workspace of the page operators: the number of items, the items, and compaction's new page numbers.
+struct PageWs {
+    int *count;        // [4]
+    CopyItem *items;   // [cap]
+    int *map;          // [pages]
+};
+__host__ __device__ inline int64_t copy_cap(int64_t pages) { return pages / 2 + 4096; }
+__host__ __device__ inline PageWs page_ws(void *ws, int64_t pages) {
+    PageWs w;
+    w.count = static_cast<int *>(ws);
+    w.items = reinterpret_cast<CopyItem *>(w.count + 4);
+    w.map = reinterpret_cast<int *>(w.items + copy_cap(pages));
+    return w;
+}
+
+// One block: the pages that the requests need, in order, are the lowest-numbered free ones. The offsets of the requests
+// (how many pages those before need) stay in shared memory; the free pages are ranked chunk by chunk and each finds its
+// request by a binary search over the offsets.
+__global__ void __launch_bounds__(PLAN_THREADS) kv_reserve_kernel(qpack_kv_tables_t t, int page_tokens, const int *seqs,
+                                                                  const int *add, int n, int64_t pages) {
+    __shared__ int sums[32];
+    __shared__ int off[4097], who[4096];                   // pages needed before request i, its row of the table
+    auto first_col = [&](int seq) {                        // the column of its first new page (lens is raised last)
+        const int64_t old = t.lens[seq] < 0 ? 0 : t.lens[seq];
+        return (old + page_tokens - 1) / page_tokens;
+    };
+    int carry = 0, tot;
+    for (int i0 = 0; i0 < n; i0 += blockDim.x) {
+        const int i = i0 + threadIdx.x;
+        int need = 0, s = -1;
+        if (i < n) {
+            s = seqs[i];
+            if (s >= 0 && s < t.seqs && add[i] >= 0) {
+                const int64_t neu = int64_t(t.lens[s] < 0 ? 0 : t.lens[s]) + add[i];
+                const int64_t last = (neu + page_tokens - 1) / page_tokens;
+                if (last > t.max_pages || neu > 0x7FFFFFFF)
+                    s = -2;                                // its row cannot hold them
+                else
+                    need = int(last - first_col(s));
+            } else {
+                s = s < 0 ? -1 : -3;
+            }
+        }
+        const int before = carry + block_scan(need, sums, &tot);
+        if (i < n) {
+            off[i] = before;
+            who[i] = s;
+            if (s == -2) atomicOr(&g_fault_paged, FAULT_NO_PAGES);
+            if (s == -3) atomicOr(&g_fault_paged, FAULT_PAGE);
+        }
+        carry += tot;
+    }
+    if (threadIdx.x == 0) off[n] = carry;
+    __syncthreads();
+    const int want = carry;
+    int found = 0;
+    for (int64_t p0 = 0; p0 < pages && found < want; p0 += blockDim.x) {
+        const int64_t p = p0 + threadIdx.x;
+        const int is_free = p < pages && t.refs[p] == 0;
+        const int rank = found + block_scan(is_free, sums, &tot);
+        if (is_free && rank < want) {
+            int lo = 0, hi = n;                            // off[lo] <= rank < off[lo + 1]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (off[mid] <= rank) lo = mid; else hi = mid;
+            }
+            // requests that need nothing share their offset with the next one: the last of them owns the rank
+            t.tables[int64_t(who[lo]) * t.stride + first_col(who[lo]) + (rank - off[lo])] = int(p);
+            t.refs[p] = 1;
+        }
+        found += tot;
+    }
+    if (found > want) found = want;
+    __syncthreads();
+    // Requests up to the last that the free pages cover stand; a request that they cover in part gives its pages back.
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int s = who[i];
+        if (s < 0) continue;
+        const int need = off[i + 1] - off[i];
+        if (off[i + 1] <= found || need == 0) {
+            t.lens[s] = (t.lens[s] < 0 ? 0 : t.lens[s]) + add[i];
+        } else {
+            atomicOr(&g_fault_paged, FAULT_NO_PAGES);
+            for (int j = off[i]; j < found && j < off[i + 1]; ++j) {
+                int *e = t.tables + int64_t(s) * t.stride + first_col(s) + (j - off[i]);
+                t.refs[*e] = 0;
+                *e = -1;
+            }
+        }
+    }
+}
+
+// One block a child. Its place among the children that need a page is a count over the parents before it, its page the
+// free one of that rank. Tables, lengths and counts of live pages are written here; the fresh page's own count is
+// written by the copy that follows, since other blocks still read it as free here.
+__global__ void __launch_bounds__(256) kv_fork_kernel(qpack_kv_tables_t t, int page_tokens, const int *src,
+                                                      const int *dst, int n, int64_t pages, PageWs w) {
+    __shared__ int sums[32];
+    __shared__ int s_fresh;
+    const int i = blockIdx.x;
+    const int s = src[i], d = dst[i];
+    auto len_of = [&](int q) {
+        if (q < 0 || q >= t.seqs) return 0;
+        const int64_t l = t.lens[q], top = int64_t(t.max_pages) * page_tokens;
+        return int(l < 0 ? 0 : (l > top ? top : l));
+    };
+    int before = 0, tot;
+    int mine = 0;
+    for (int j = threadIdx.x; j < i; j += blockDim.x) mine += (len_of(src[j]) & (page_tokens - 1)) != 0;
+    block_scan(mine, sums, &before);
+    if (threadIdx.x == 0) s_fresh = -1;
+    __syncthreads();
+    const int len = len_of(s), full = len / page_tokens, rows = len & (page_tokens - 1);
+    if (rows) {
+        int found = 0;
+        for (int64_t p0 = 0; p0 < pages && found <= before; p0 += blockDim.x) {
+            const int64_t p = p0 + threadIdx.x;
+            const int is_free = p < pages && t.refs[p] == 0;
+            const int rank = found + block_scan(is_free, sums, &tot);
+            if (is_free && rank == before) s_fresh = int(p);
+            found += tot;
+        }
+        __syncthreads();
+    }
+    const bool ok_seq = s >= 0 && s < t.seqs && d >= 0 && d < t.seqs;
+    const int fresh = s_fresh;
+    const bool grant = ok_seq && t.lens[d] == 0 && (rows == 0 || fresh >= 0);
+    const int last = ok_seq && rows ? t.tables[int64_t(s) * t.stride + full] : -1;
+    const bool copy = grant && rows && last >= 0 && last < pages;
+    __syncthreads();                                       // every thread has read lens[d]
+    if (threadIdx.x == 0) {
+        if (!grant) atomicOr(&g_fault_paged, ok_seq ? FAULT_NO_PAGES : FAULT_PAGE);
+        if (grant && rows && !copy) atomicOr(&g_fault_paged, FAULT_PAGE);
+        w.items[i] = {copy ? last : -1, grant && rows ? fresh : -1, rows};
+        if (i == 0) w.count[0] = n;
+        if (grant) {
+            t.lens[d] = len;
+            if (rows) t.tables[int64_t(d) * t.stride + full] = fresh;
+        }
+    }
+    if (!grant) return;
+    for (int c = threadIdx.x; c < full; c += blockDim.x) {
+        const int p = t.tables[int64_t(s) * t.stride + c];
+        t.tables[int64_t(d) * t.stride + c] = p;
+        if (p >= 0 && p < pages) atomicAdd(t.refs + p, 1);
+        else atomicOr(&g_fault_paged, FAULT_PAGE);
+    }
+}
+
+__global__ void __launch_bounds__(256) kv_free_kernel(qpack_kv_tables_t t, const int *seqs) {
+    const int s = seqs[blockIdx.x];
+    if (s < 0) return;
+    if (s >= t.seqs) {
+        if (threadIdx.x == 0) atomicOr(&g_fault_paged, FAULT_PAGE);
+        return;
+    }
+    for (int c = threadIdx.x; c < t.max_pages; c += blockDim.x) {
+        // exchanged, so that a sequence listed twice gives its pages back once
+        const int p = atomicExch(t.tables + int64_t(s) * t.stride + c, -1);
+        if (p < 0) continue;
+        if (p < t.pages) atomicSub(t.refs + p, 1);
+        else atomicOr(&g_fault_paged, FAULT_PAGE);
+    }
+    if (threadIdx.x == 0) t.lens[s] = 0;
+}
+
+// One block: counts the live pages, ranks the holes below and the movers above that number, and writes the moves, the
+// new numbers and the new reference counts.
+__global__ void __launch_bounds__(PLAN_THREADS) kv_compact_plan_kernel(qpack_kv_tables_t t, int page_tokens,
+                                                                       int64_t pages, int *refs_out, int *moved, PageWs w) {
+    __shared__ int sums[32];
+    int tot, nlive = 0;
+    for (int64_t p0 = 0; p0 < pages; p0 += blockDim.x) {
+        const int64_t p = p0 + threadIdx.x;
+        block_scan(p < pages && t.refs[p] > 0, sums, &tot);
+        nlive += tot;
+    }
+    int holes = 0, movers = 0;
+    for (int64_t p0 = 0; p0 < pages; p0 += blockDim.x) {
+        const int64_t p = p0 + threadIdx.x;
+        const bool in = p < pages;
+        const int r = in ? t.refs[p] : 0;
+        const int hole = in && r <= 0 && p < nlive, mover = r > 0 && p >= nlive;
+        const int hr = holes + block_scan(hole, sums, &tot);
+        holes += tot;
+        const int mr = movers + block_scan(mover, sums, &tot);
+        movers += tot;
+        if (hole) w.items[hr].dst = int(p);
+        if (mover) w.items[mr].src = int(p);
+        if (in) {
+            w.map[p] = int(p);
+            if (!hole && !mover) refs_out[p] = p < nlive ? r : 0;
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < movers; i += blockDim.x) {
+        const int a = w.items[i].src, b = w.items[i].dst;
+        w.items[i].rows = page_tokens;
+        w.map[a] = b;
+        const int r = t.refs[a];
+        refs_out[a] = 0;
+        refs_out[b] = r;
+    }
+    if (threadIdx.x == 0) {
+        w.count[0] = movers;
+        if (moved) *moved = movers;
+    }
+}
+
+// Copies the items' rows: a warp takes one head's rows of keys or values of one layer at a time, 16 bytes a lane with
+// eight loads in flight, then the rows' scales. `refs`: fork's fresh pages get their count. `tables`: compaction's
+// entries get their new numbers.
+__global__ void __launch_bounds__(256) kv_copy_kernel(qpack_kv_pool_t pool, PageWs w, const int *src_list,
+                                                      const int *dst_list, int64_t n_list, int *refs, qpack_kv_tables_t t,
+                                                      int *tables_out) {
+    const int lane = threadIdx.x & 31;
+    const int64_t warp = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int64_t warps = int64_t(gridDim.x) * (blockDim.x >> 5);
+    const int64_t n = src_list ? n_list : w.count[0];
+    const int64_t slabs = n * pool.layers * 2 * pool.heads;
+    const int es = pool.type == QPACK_KV_I8 ? 1 : 2;
+    for (int64_t j = warp; j < slabs; j += warps) {
+        const int head = int(j % pool.heads);
+        int64_t q = j / pool.heads;
+        const bool is_v = q & 1;
+        q >>= 1;
+        const int64_t layer = q % pool.layers, item = q / pool.layers;
+        CopyItem it;
+        if (src_list) it = {src_list[item], dst_list[item], pool.page_tokens};
+        else it = w.items[item];
+        if (it.src < 0 || it.dst < 0 || it.src >= pool.pages || it.dst >= pool.pages) {
+            if (src_list && lane == 0) atomicOr(&g_fault_paged, FAULT_PAGE);
+            continue;
+        }
+        char *base = static_cast<char *>(is_v ? pool.v : pool.k);
+        const int64_t in = layer * pool.layer_stride + int64_t(head) * pool.page_tokens * pool.dim;
+        const uint4 *a = reinterpret_cast<const uint4 *>(base + (in + it.src * pool.page_stride) * es);
+        uint4 *b = reinterpret_cast<uint4 *>(base + (in + it.dst * pool.page_stride) * es);
+        const int vec = it.rows * pool.dim * es / 16;
+        int x = lane;
+        for (; x + 7 * 32 < vec; x += 8 * 32) {
+            uint4 r[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) r[u] = __ldcs(a + x + 32 * u);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) __stcs(b + x + 32 * u, r[u]);
+        }
+        for (; x < vec; x += 32) __stcs(b + x, __ldcs(a + x));
+        if (es == 1) {
+            uint16_t *sb = is_v ? pool.v_scales : pool.k_scales;
+            const int64_t si = layer * pool.scale_layer_stride + int64_t(head) * pool.page_tokens * (pool.dim / 32);
+            // dim / 32 fp16 a row: whole 4-byte words
+            const uint32_t *sa = reinterpret_cast<const uint32_t *>(sb + si + it.src * pool.scale_page_stride);
+            uint32_t *sd = reinterpret_cast<uint32_t *>(sb + si + it.dst * pool.scale_page_stride);
+            for (int y = lane; y < it.rows * (pool.dim / 64); y += 32) sd[y] = sa[y];
+        }
+    }
+    const int64_t tid = int64_t(blockIdx.x) * blockDim.x + threadIdx.x, threads = int64_t(gridDim.x) * blockDim.x;
+    if (refs)
+        for (int64_t i = tid; i < n; i += threads)
+            if (w.items[i].dst >= 0) refs[w.items[i].dst] = 1;
+    if (tables_out)
+        for (int64_t i = tid; i < int64_t(t.seqs) * t.max_pages; i += threads) {
+            const int64_t at = i / t.max_pages * t.stride + i % t.max_pages;
+            const int p = t.tables[at];
+            if (p >= t.pages) atomicOr(&g_fault_paged, FAULT_PAGE);
+            tables_out[at] = p >= 0 && p < t.pages ? w.map[p] : p;
+        }
+}
+
+cudaError_t run_copy(const qpack_kv_pool_t &p, const PageWs &w, const int *src, const int *dst, int64_t n, int64_t most,
+                     int *refs, const qpack_kv_tables_t &t, int *tables_out, cudaStream_t s) {
+    const int64_t warps = most * p.layers * 2 * p.heads, cap = int64_t(num_sms()) * 8;
+    int64_t grid = (warps + 7) / 8;
+    grid = grid < 1 ? 1 : (grid < cap ? grid : cap);
+    kv_copy_kernel<<<int(grid), 256, 0, s>>>(p, w, src, dst, n, refs, t, tables_out);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t s) { return rows_kind(a, false, s); }
+cudaError_t launch_kv_read(const AppendArgs &a, cudaStream_t s) { return rows_kind(a, true, s); }
+
+int64_t kv_page_workspace(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t) {
+    return 16 + int64_t(sizeof(CopyItem)) * copy_cap(p.pages) + 4 * p.pages;
+}
+
+cudaError_t launch_kv_reserve(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t, const int32_t *seqs,
+                              const int32_t *add, int n, cudaStream_t s) {
+    kv_reserve_kernel<<<1, PLAN_THREADS, 0, s>>>(t, p.page_tokens, seqs, add, n, t.pages);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_fork(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t, const int32_t *src, const int32_t *dst,
+                           int n, void *ws, cudaStream_t s) {
+    const PageWs w = page_ws(ws, p.pages);
+    kv_fork_kernel<<<n, 256, 0, s>>>(t, p.page_tokens, src, dst, n, t.pages, w);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return run_copy(p, w, nullptr, nullptr, 0, n, t.refs, t, nullptr, s);
+}
+
+cudaError_t launch_kv_free(const qpack_kv_tables_t &t, const int32_t *seqs, int n, cudaStream_t s) {
+    kv_free_kernel<<<n, 256, 0, s>>>(t, seqs);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_compact(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t, int32_t *tables_out,
+                              int32_t *refs_out, int32_t *moved, void *ws, cudaStream_t s) {
+    const PageWs w = page_ws(ws, p.pages);
+    kv_compact_plan_kernel<<<1, PLAN_THREADS, 0, s>>>(t, p.page_tokens, t.pages, refs_out, moved, w);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return run_copy(p, w, nullptr, nullptr, 0, t.pages / 2 + 1, nullptr, t, tables_out, s);
+}
+
+cudaError_t launch_kv_copy_pages(const qpack_kv_pool_t &p, const int32_t *src, const int32_t *dst, int64_t n,
+                                 cudaStream_t s) {
+    return run_copy(p, PageWs{}, src, dst, n, n, nullptr, qpack_kv_tables_t{}, nullptr, s);
+}
+
+cudaError_t fetch_fault_paged(int32_t *flags) {
+    int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_fault_paged, sizeof(int));
+    if (e != cudaSuccess) return e;
+    *flags |= v;
+    const int zero = 0;
+    return cudaMemcpyToSymbol(g_fault_paged, &zero, sizeof(int));
+}
+
+}  // namespace qpack

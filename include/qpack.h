@@ -189,6 +189,129 @@ int qpack_kv_quantize(const uint16_t *v, int64_t n, int8_t *codes, uint16_t *sca
  *  codes 8-byte aligned, scales 2-byte aligned, out [n] fp16 16-byte aligned; n a multiple of 32. */
 int qpack_kv_dequant(const int8_t *codes, const uint16_t *scales, int64_t n, uint16_t *out, qpack_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------------------------------
+ * Paged KV cache: the cache of many sequences in pages, the operators that write, read and attend to it, and the page
+ * operators that share, release, extend and compact it.
+ *
+ * A pool holds `layers` x `pages` pages of `page_tokens` tokens: per layer and page, keys and values
+ * [heads][page_tokens][dim] without gaps, in 8 bits (QPACK_KV_I8: int8 codes and one fp16 scale per 32 elements, the
+ * rule of qpack_kv_quantize; scales [heads][page_tokens][dim / 32]) or in 16 bits (fp16, bf16; scales NULL). Element
+ * (layer, page, head, slot, i) of k and v is at layer * layer_stride + page * page_stride
+ * + (head * page_tokens + slot) * dim + i, its scale at layer * scale_layer_stride + page * scale_page_stride
+ * + (head * page_tokens + slot) * (dim / 32) + i / 32 (offsets are 64-bit). An 8-bit element stands for
+ * v' = fp16_rn(scale * code), as qpack_kv_dequant gives it.
+ *  heads        key/value heads;  dim  64, 128 or 256;  page_tokens  a power of two, 1 to 1024
+ *  k, v         16-byte aligned, layer_stride and page_stride multiples of 16 elements
+ *  k_scales, v_scales  16-byte aligned, their strides multiples of dim / 32 elements
+ *
+ * Sequences are rows of a page table on the device: token t of sequence s is in page
+ * tables[s * stride + t / page_tokens], slot t % page_tokens. lens[s] counts its tokens, refs[p] the sequences that
+ * hold page p (0: free). Entries that hold no page are -1. Append, read and attend need no refs (may be NULL).
+ *
+ * Device data that is out of range (a page number outside the pool, a position outside the table, a length longer than
+ * the table or negative, a sequence number outside the table) never reaches memory outside the buffers: the access is
+ * left out and QPACK_FAULT_PAGE is set in the fault word (qpack_fetch_fault_flags). */
+typedef enum { QPACK_KV_I8 = 0, QPACK_KV_F16 = 1, QPACK_KV_BF16 = 2 } qpack_kv_type;
+
+typedef struct {
+    void *k, *v;
+    uint16_t *k_scales, *v_scales;
+    int64_t layer_stride, page_stride;
+    int64_t scale_layer_stride, scale_page_stride;
+    int64_t pages;          /* at most 2^31 - 1 */
+    int32_t layers, heads, page_tokens, dim;
+    int32_t type;           /* qpack_kv_type */
+    int32_t reserved;       /* 0 */
+} qpack_kv_pool_t;
+
+typedef struct {
+    int32_t *tables;        /* [seqs, stride], the first max_pages entries of each row used */
+    int32_t *lens;          /* [seqs] */
+    int32_t *refs;          /* [pages], or NULL where the call does not use it */
+    int64_t stride;
+    int64_t pages;          /* entries of refs */
+    int32_t seqs, max_pages;
+} qpack_kv_tables_t;
+
+#define QPACK_FAULT_PAGE 32     /* device data out of range: a page, position, length or sequence number */
+#define QPACK_FAULT_NO_PAGES 64 /* a request of qpack_kv_reserve / qpack_kv_fork was refused: no free page, or its
+                                   row of the table is full (fork: the child is not empty) */
+
+/* Append n tokens to a layer of the cache: token i goes to position pos[i] of sequence seqs[i].
+ *  k, v       [n, ld] rows of heads * dim elements of dtype dt (QPACK_F32, F16 or BF16; a product's fp32 output goes in
+ *             as it is), 16-byte aligned, ldk and ldv >= heads * dim and multiples of 8
+ *  seqs       [n] int32, or NULL: token i belongs to sequence i
+ *  pos        [n] int32, or NULL: the sequence's last token, lens[seq] - 1. A negative position skips the token.
+ *             lens is not changed (qpack_kv_reserve extends a sequence). No two tokens may name the same place.
+ *  rope       NULL, or [rope_rows, dim] fp32, 16-byte aligned: row p holds cos (dim / 2) and sin (dim / 2) of position
+ *             p, and keys are rotated before they are stored: (x_i, x_{i + dim/2}) ->
+ *             (x_i c_i - x_{i + dim/2} s_i, x_{i + dim/2} c_i + x_i s_i), every operation rounded to fp32.
+ * 8-bit pools: per 32 elements d = fp16_rn(max|x| / 127) (at most 65504), q = clamp(rint(x / d), -127, 127), 0 where d is
+ * 0, in fp32 with IEEE division; 16-bit pools: rounded to nearest even. Non-finite inputs give unspecified codes. */
+int qpack_kv_append(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_t *t, const int32_t *seqs,
+                    const int32_t *pos, int64_t n, const void *k, const void *v, int dt, int64_t ldk, int64_t ldv,
+                    const float *rope, int64_t rope_rows, qpack_stream_t stream);
+
+/* The inverse: rows of the cache, token i from position pos[i] of sequence seqs[i] (NULL as above), as dt (QPACK_F32,
+ * F16 or BF16) into k, v [n, ld] (16-byte aligned, ld >= heads * dim and a multiple of 8). Either of k and v may be NULL.
+ * Tokens with a negative position, or out of range, are written as zero. */
+int qpack_kv_read(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_t *t, const int32_t *seqs,
+                  const int32_t *pos, int64_t n, void *k, void *v, int dt, int64_t ldk, int64_t ldv,
+                  qpack_stream_t stream);
+
+/* Attention of one new token a sequence over its cache (grouped queries: query heads h * q_heads / heads ... share
+ * key/value head h). Row b takes sequence s = seqs[b] (NULL: b), L = lens[s] and, with window > 0, its last `window`
+ * tokens only (0: all): lo = max(0, L - window).
+ *   x_t = scale * <q~_b, k'_t>, lo <= t < L;  out_b = sum_t e^{x_t - m} v'_t / sum_t e^{x_t - m};  lse_b = ln sum_t e^{x_t}
+ * Sums, softmax statistics and accumulators are fp32; queries and probabilities enter the tensor cores as two 16-bit
+ * terms each (22 bits for 8-bit and fp16 pools, 16 for bf16 pools). An empty range gives out = 0 and lse = -inf.
+ *  q     [B, ldq] of dtype qdt, q_heads * dim elements a row, 16-byte aligned, ldq a multiple of 8; q_heads a multiple of
+ *        the pool's heads;  rope  as in qpack_kv_append, applied to q at position L - 1 (NULL: q as it is)
+ *  out   [B, ldo] of dtype odt, 16-byte aligned, ldo >= q_heads * dim and a multiple of 8
+ *  lse   [B, q_heads] fp32, or NULL
+ *  ws    workspace of at least the bytes that qpack_kv_attend_workspace gives for B (or a larger B) on this device,
+ *        16-byte aligned, zeroed once before its first use. Each call leaves it ready for the next; calls that may
+ *        run at the same time need a workspace each.
+ *  B     at most 4096. Results do not depend on the order in which blocks run. */
+int qpack_kv_attend(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_t *t, const int32_t *seqs, int B,
+                    const void *q, int qdt, int64_t ldq, int q_heads, float scale, int64_t window, const float *rope,
+                    int64_t rope_rows, void *out, int odt, int64_t ldo, float *lse, void *ws, int64_t ws_bytes,
+                    qpack_stream_t stream);
+int qpack_kv_attend_workspace(const qpack_kv_pool_t *pool, int B, int q_heads, int64_t *bytes);
+
+/* Page operators. All work on the device alone and are deterministic: new pages are the lowest-numbered free ones, in the
+ * order of the requests. n <= 4096 sequences a call, each listed once.
+ *
+ * reserve: extend sequence seqs[i] by add[i] >= 0 tokens. Request i needs the pages between its old and new length, and
+ * is granted (pages entered in the table, refs 1, lens raised) when the pages that it and all requests before it need
+ * are free and its row holds them; otherwise it is left as it was and QPACK_FAULT_NO_PAGES is set. A negative seqs[i]
+ * is skipped. */
+int qpack_kv_reserve(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, const int32_t *seqs, const int32_t *add,
+                     int64_t n, qpack_stream_t stream);
+
+/* fork: make the empty sequence dst[i] a copy of src[i] (one src may be forked many times; no dst may be a src). Full pages
+ * are shared (refs + 1); a last page that is not full is copied into a fresh page, over all layers, the filled tokens
+ * only. Refused as in reserve. ws: qpack_kv_page_workspace bytes, 16-byte aligned, no initial value needed. */
+int qpack_kv_fork(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, const int32_t *src, const int32_t *dst,
+                  int64_t n, void *ws, int64_t ws_bytes, qpack_stream_t stream);
+
+/* free: take one reference from every page of sequence seqs[i], clear its row (-1) and its length. A negative seqs[i] is
+ * skipped. */
+int qpack_kv_free(const qpack_kv_tables_t *t, const int32_t *seqs, int64_t n, qpack_stream_t stream);
+
+/* compact: move live pages (refs > 0) so that they are the lowest-numbered ones. With n live pages, the i-th live page
+ * numbered n or more moves to the i-th free page below n, over all layers; every table entry and reference count
+ * follows. The results go to tables_out (rows of `stride`) and refs_out, which may be t->tables and t->refs.
+ *  moved  device int32, or NULL: the number of pages moved */
+int qpack_kv_compact(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, int32_t *tables_out, int32_t *refs_out,
+                     int32_t *moved, void *ws, int64_t ws_bytes, qpack_stream_t stream);
+
+/* Copy the contents of page src[i] to page dst[i] over all layers, n pages (device int32 arrays). No dst may be listed
+ * twice or be a src. */
+int qpack_kv_copy_pages(const qpack_kv_pool_t *pool, const int32_t *src, const int32_t *dst, int64_t n,
+                        qpack_stream_t stream);
+int qpack_kv_page_workspace(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, int64_t *bytes);
+
 /* Human-readable name of a qpack_status value. Never NULL. */
 const char *qpack_status_string(int status);
 
