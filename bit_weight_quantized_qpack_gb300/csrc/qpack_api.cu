@@ -162,7 +162,8 @@ int check_pool(const qpack_kv_pool_t *p, bool data = true) {
     if (p->pages > 1 && p->page_stride < page) return QPACK_ERR_SHAPE;
     if (i8 && p->pages > 1 && p->scale_page_stride < page / 32) return QPACK_ERR_SHAPE;
     if (!data) return QPACK_OK;
-    if (p->pages > 0 && p->layers > 0 && (!p->k || !p->v || (i8 && (!p->k_scales || !p->v_scales)))) return QPACK_ERR_ARG;
+    if (p->pages < 1) return QPACK_ERR_SHAPE;
+    if (p->layers > 0 && (!p->k || !p->v || (i8 && (!p->k_scales || !p->v_scales)))) return QPACK_ERR_ARG;
     if (!aligned(p->k, 16) || !aligned(p->v, 16) || p->page_stride % 16 || p->layer_stride % 16) return QPACK_ERR_ALIGN;
     if (i8 && (!aligned(p->k_scales, 16) || !aligned(p->v_scales, 16) || p->scale_page_stride % (p->dim / 32) ||
                p->scale_layer_stride % (p->dim / 32)))
@@ -417,7 +418,7 @@ int qpack_kv_read(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_
 int qpack_kv_attend_workspace(const qpack_kv_pool_t *pool, int B, int q_heads, int64_t *bytes) {
     if (!bytes || B < 0 || q_heads < 1) return QPACK_ERR_ARG;
     if (int rc = check_pool(pool, false)) return rc;
-    if (B > 4096 || q_heads % pool->heads) return QPACK_ERR_SHAPE;
+    if (B > 4096 || q_heads > 65536 || q_heads % pool->heads) return QPACK_ERR_SHAPE;
     *bytes = kv_attend_workspace(*pool, B, q_heads);
     return QPACK_OK;
 }
@@ -430,7 +431,7 @@ int qpack_kv_attend(const qpack_kv_pool_t *pool, int layer, const qpack_kv_table
     if ((rc = check_pool(pool)) || (rc = check_tables(t, false))) return rc;
     if (layer < 0 || layer >= pool->layers || B < 0 || q_heads < 1 || window < 0) return QPACK_ERR_ARG;
     if (qdt < QPACK_F32 || qdt > QPACK_BF16 || odt < QPACK_F32 || odt > QPACK_BF16) return QPACK_ERR_ARG;
-    if (q_heads % pool->heads || B > 4096) return QPACK_ERR_SHAPE;
+    if (q_heads % pool->heads || q_heads > 65536 || B > 4096) return QPACK_ERR_SHAPE;
     if (B == 0) return QPACK_OK;
     const int64_t width = int64_t(q_heads) * pool->dim;
     if ((rc = check_rows(q, ldq, width)) || (rc = check_rows(out, ldo, width)) || (rc = check_rope(rope, rope_rows)))

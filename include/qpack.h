@@ -218,7 +218,7 @@ typedef struct {
     uint16_t *k_scales, *v_scales;
     int64_t layer_stride, page_stride;
     int64_t scale_layer_stride, scale_page_stride;
-    int64_t pages;          /* at most 2^31 - 1 */
+    int64_t pages;          /* 1 to 2^31 - 1 */
     int32_t layers, heads, page_tokens, dim;
     int32_t type;           /* qpack_kv_type */
     int32_t reserved;       /* 0 */
@@ -266,12 +266,12 @@ int qpack_kv_read(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_
  * Sums, softmax statistics and accumulators are fp32; queries and probabilities enter the tensor cores as two 16-bit
  * terms each (22 bits for 8-bit and fp16 pools, 16 for bf16 pools). An empty range gives out = 0 and lse = -inf.
  *  q     [B, ldq] of dtype qdt, q_heads * dim elements a row, 16-byte aligned, ldq a multiple of 8; q_heads a multiple of
- *        the pool's heads;  rope  as in qpack_kv_append, applied to q at position L - 1 (NULL: q as it is)
+ *        the pool's heads, at most 65536;  rope  as in qpack_kv_append, applied to q at position L - 1 (NULL: q as it is)
  *  out   [B, ldo] of dtype odt, 16-byte aligned, ldo >= q_heads * dim and a multiple of 8
  *  lse   [B, q_heads] fp32, or NULL
- *  ws    workspace of at least the bytes that qpack_kv_attend_workspace gives for B (or a larger B) on this device,
- *        16-byte aligned, zeroed once before its first use. Each call leaves it ready for the next; calls that may
- *        run at the same time need a workspace each.
+ *  ws    workspace of at least the bytes that qpack_kv_attend_workspace gives on this device, 16-byte aligned,
+ *        zeroed once before its first use. Each call leaves it ready for the next, of any shape that it is large
+ *        enough for; calls that may run at the same time need a workspace each.
  *  B     at most 4096. Results do not depend on the order in which blocks run. */
 int qpack_kv_attend(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_t *t, const int32_t *seqs, int B,
                     const void *q, int qdt, int64_t ldq, int q_heads, float scale, int64_t window, const float *rope,
