@@ -441,7 +441,8 @@ int qpack_kv_attend(const qpack_kv_pool_t *pool, int layer, const qpack_kv_table
     if (ws_bytes < kv_attend_workspace(*pool, B, q_heads)) return QPACK_ERR_SHAPE;
     AttendArgs a = {*pool, *t, seqs, q, ldq, rope, rope_rows, out, ldo, lse, ws, window, scale, layer, B, q_heads, qdt,
                     odt};
-    return cuda_status(launch_kv_attend(a, reinterpret_cast<cudaStream_t>(stream)));
+    const cudaError_t e = launch_kv_attend(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaErrorNotSupported ? QPACK_ERR_UNSUPPORTED : cuda_status(e);
 }
 
 int qpack_kv_page_workspace(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, int64_t *bytes) {

@@ -29,7 +29,7 @@
 // element. ldmatrix moves pairs of bytes as 16-bit elements: for keys the four bytes of a thread are four consecutive
 // d (the queries' fragments use the same order of d), for values two d of two tokens.
 //
-// Work is cut by tiles of 16 tokens, not by rows: lengths are known on the device only and may be anything, so each
+// Work is cut by tiles of 16 or 32 tokens, not by rows: lengths are known on the device only and may be anything, so each
 // block adds up the rows' tiles and takes an equal share of all of them (consecutive tiles, through as many segments
 // (row, key/value head, group of query heads) as it covers), and each of its warps an equal share of the block's. A
 // warp owns a ring of cp.async stages and never waits for another warp until its share is done. A segment inside one
@@ -47,23 +47,26 @@
 namespace qpack {
 namespace attend {
 
-constexpr int TOK = 16;                     // tokens a tile
 constexpr int MAX_ROWS = 1024;              // rows a launch
 constexpr int MAX_SEGS = 65536;             // segments a launch: counters at the front of the workspace
 constexpr float P_BIAS = 12.0f;             // probabilities are held as 2^(x - m + 12)
 
-// Shape of an instance: NT groups of eight query heads, W warps, a ring of STAGES tiles each. Registers decide W
-// (accumulators D NT / 4 and query fragments D NT / 4 a thread), shared memory the stages.
+// Shape of an instance: NT groups of eight query heads, tiles of TOK tokens, W warps, a ring of STAGES tiles each.
+// Accumulators and query fragments take D NT / 4 registers a thread each, so they decide W; shared memory decides TOK
+// and the stages.
 template <int KT, int D, int NT> struct Cfg {
     static constexpr int ES = KT == QPACK_KV_I8 ? 1 : 2;
     static constexpr int RB = D * ES;                           // bytes of a token's row
     static constexpr int SB = KT == QPACK_KV_I8 ? D / 16 : 0;   // bytes of its scales
+    static constexpr int TOK = RB >= 256 ? 16 : 32;
     static constexpr int TILE = 2 * TOK * (RB + SB);            // keys, values, their scales
-    static constexpr int W = (D == 256 && KT != QPACK_KV_I8) ? 4 : (D * NT >= 256 || RB >= 256) ? 8 : 16;
-    static constexpr int STAGES = 212000 / (W * TILE) > 6 ? 6 : 212000 / (W * TILE);
-    static constexpr int FR = D * 8 * NT;                       // accumulators of a segment
-    static constexpr int PF = FR + 2 * 8 * NT;                  // floats of a partial: accumulators, maxima, sums
+    static constexpr int W = RB == 512 ? 6 : D * NT >= 256 ? 8 : 12;
+    static constexpr int STAGES = 214000 / (W * TILE) > 4 ? 4 : 214000 / (W * TILE);
+    static constexpr int NH = 8 * NT;
+    static constexpr int PS = D + 4;                            // floats of a head in a partial, padded for the banks
+    static constexpr int PF = NH * PS + 2 * NH;                 // floats of a partial: accumulators, maxima, sums
     static_assert(STAGES >= 2 && PF * 4 <= STAGES * TILE, "a warp's ring holds a partial");
+    static_assert(2 * W <= 32, "a lane a piece");
 };
 
 struct Params {
@@ -77,6 +80,9 @@ struct Params {
 
 static __device__ int g_fault_attend = 0;       // one a translation unit: one a cache type
 
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
@@ -118,6 +124,24 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+template <int V> struct Int { static constexpr int value = V; };
+
+// N bytes (a multiple of 4, aligned to at most 16 of them) of shared memory as words.
+template <int N> __device__ __forceinline__ void load_words(const unsigned char *p, uint32_t *w) {
+    if (N % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) {
+            const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
+    } else if (N == 8) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+}
+
 // Two fp32 as a packed pair of 16-bit terms, x in the low half, and the pair of what they leave.
 template <int KT> __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
     if (KT == QPACK_KV_BF16) {
@@ -142,138 +166,143 @@ __device__ __forceinline__ uint32_t dequant2(uint32_t w, uint32_t sel, uint32_t 
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-template <int DT> __device__ __forceinline__ void load2(const void *p, int64_t i, float *x) {
+// Four or two consecutive elements of a row of queries.
+template <int DT, int N> __device__ __forceinline__ void load_q(const void *p, int64_t i, float *x) {
     if (DT == DT_F32) {
-        const float2 v = *reinterpret_cast<const float2 *>(static_cast<const float *>(p) + i);
-        x[0] = v.x;
-        x[1] = v.y;
-    } else {
-        const uint32_t v = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + i);
-        if (DT == DT_F16) {
-            x[0] = h2f_bits(uint16_t(v & 0xFFFFu));
-            x[1] = h2f_bits(uint16_t(v >> 16));
+        const float *q = static_cast<const float *>(p) + i;
+        if (N == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(q);
+            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
         } else {
-            x[0] = __uint_as_float(v << 16);
-            x[1] = __uint_as_float(v & 0xFFFF0000u);
+            const float2 v = *reinterpret_cast<const float2 *>(q);
+            x[0] = v.x, x[1] = v.y;
+        }
+    } else {
+        const uint16_t *q = static_cast<const uint16_t *>(p) + i;
+        uint32_t v[2] = {0, 0};
+        if (N == 4) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(q);
+            v[0] = u.x, v[1] = u.y;
+        } else {
+            v[0] = *reinterpret_cast<const uint32_t *>(q);
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const uint32_t h = e & 1 ? v[e / 2] >> 16 : v[e / 2] & 0xFFFFu;
+            x[e] = DT == DT_F16 ? h2f_bits(uint16_t(h)) : __uint_as_float(h << 16);
         }
     }
 }
-__device__ __forceinline__ void load2(const void *p, int dt, int64_t i, float *x) {
-    if (dt == DT_F32) load2<DT_F32>(p, i, x);
-    else if (dt == DT_F16) load2<DT_F16>(p, i, x);
-    else load2<DT_BF16>(p, i, x);
-}
-__device__ __forceinline__ void store1(void *p, int dt, int64_t i, float x) {
-    if (dt == DT_F32) static_cast<float *>(p)[i] = x;
-    else if (dt == DT_F16) static_cast<uint16_t *>(p)[i] = f2h_bits(x);
-    else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
+
+// N = 1, 2 or 4 consecutive outputs, rounded once.
+template <int N> __device__ __forceinline__ void store_out(void *p, int dt, int64_t i, const float *x) {
+    if (dt == DT_F32) {
+        float *o = static_cast<float *>(p) + i;
+        if (N == 4) *reinterpret_cast<float4 *>(o) = make_float4(x[0], x[1], x[2], x[3]);
+        else if (N == 2) *reinterpret_cast<float2 *>(o) = make_float2(x[0], x[1]);
+        else *o = x[0];
+        return;
+    }
+    uint16_t h[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) h[e] = dt == DT_F16 ? f2h_bits(x[e]) : __bfloat16_as_ushort(__float2bfloat16_rn(x[e]));
+    uint16_t *o = static_cast<uint16_t *>(p) + i;
+    if (N == 4) *reinterpret_cast<uint2 *>(o) = make_uint2(h[0] | uint32_t(h[1 % N]) << 16, h[2 % N] | uint32_t(h[3 % N]) << 16);
+    else if (N == 2) *reinterpret_cast<uint32_t *>(o) = h[0] | uint32_t(h[1 % N]) << 16;
+    else *o = h[0];
 }
 
-// A row's tokens [lo, len), its tiles from the multiple of 16 below lo.
+// A row's tokens [lo, len), its tiles from the multiple of TOK below lo.
 struct Row {
     const int *table;
     unsigned lo, len, base;
-    int tiles;
+    unsigned tiles;
 };
 
-__device__ __forceinline__ Row row_of(const Params &p, int b, int *fault) {
+template <int TOK> __device__ __forceinline__ Row row_of(const Params &p, int b, int *fault) {
     Row r;
     const AttendArgs &a = p.a;
     const int seq = a.seqs ? __ldg(a.seqs + p.row0 + b) : p.row0 + b;
     int64_t len = 0;
-    bool bad = seq < 0 || seq >= a.t.seqs;
-    if (!bad) {
+    const bool known = seq >= 0 && seq < a.t.seqs;
+    bool bad = !known;
+    if (known) {
         len = __ldg(a.t.lens + seq);
-        int64_t top = int64_t(a.t.max_pages) * a.pool.page_tokens;
-        top = top < 0x7FFFFFFF ? top : 0x7FFFFFFF;
+        const int64_t cap = int64_t(a.t.max_pages) * a.pool.page_tokens, top = cap < 0x7FFFFFFF ? cap : 0x7FFFFFFF;
         bad = len < 0 || len > top;
         len = len < 0 ? 0 : (len > top ? top : len);
     }
     if (bad && fault) atomicOr(fault, FAULT_PAGE);
-    r.table = a.t.tables + (seq < 0 || seq >= a.t.seqs ? 0 : int64_t(seq) * a.t.stride);
+    r.table = a.t.tables + (known ? int64_t(seq) * a.t.stride : 0);
     r.len = unsigned(len);
     r.lo = a.window > 0 && len > a.window ? unsigned(len - a.window) : 0u;
     r.base = r.lo / TOK * TOK;
-    r.tiles = int((r.len - r.base + TOK - 1) / TOK);
+    r.tiles = (r.len - r.base + TOK - 1) / TOK;
     return r;
 }
 
-// Where a tile lies: row, segment of the row (key/value head x group of query heads), tile of the segment.
-struct Cursor {
-    int b, hc, ti;
-    Row row;
-};
-
-__device__ __forceinline__ void seek(const Params &p, const int64_t *cum, int64_t tile, Cursor &c) {
-    const int HC = p.a.pool.heads * p.C;
-    int lo = 0, hi = p.B;                                  // cum[lo] HC <= tile < cum[hi] HC
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cum[mid] * HC <= tile) lo = mid; else hi = mid;
-    }
-    c.b = lo;
-    c.row = row_of(p, lo, nullptr);
-    const int64_t rem = tile - cum[lo] * HC;
-    c.hc = int(rem / c.row.tiles);
-    c.ti = int(rem - int64_t(c.hc) * c.row.tiles);
-}
-
-// The next tile; there is one.
-__device__ __forceinline__ void step(const Params &p, const int64_t *cum, Cursor &c) {
-    if (++c.ti < c.row.tiles) return;
-    c.ti = 0;
-    if (++c.hc < p.a.pool.heads * p.C) return;
-    c.hc = 0;
-    int b = c.b + 1;
-    while (cum[b + 1] == cum[b]) ++b;
-    c.b = b;
-    c.row = row_of(p, b, nullptr);
-}
-
-// The share of block i of all tiles: equal pieces of `size` tiles, or (aligned) pieces of `size` tiles of each segment,
-// `per` blocks a segment.
+// The share of block i of all tiles, numbered row by row and segment by segment: equal pieces of `size` tiles, or
+// (per > 0) pieces of `size` tiles of each segment, `per` blocks a segment. The host keeps all numbers below 2^31.
 struct Plan {
-    int64_t total, size;
-    int per;                                               // 0: pieces run through the segments
+    unsigned total, size;
+    int per, HC;                                           // HC: segments a row
 };
-
-__device__ __forceinline__ int64_t seg_start(const Params &p, const int64_t *cum, int b, int hc) {
-    return cum[b] * p.a.pool.heads * p.C + hc * (cum[b + 1] - cum[b]);
+__device__ __forceinline__ unsigned seg_start(const Plan &pl, const unsigned *cum, int b, int hc) {
+    return cum[b] * pl.HC + hc * (cum[b + 1] - cum[b]);
 }
-
-// The blocks that share segment (b, hc), and whether block i reached it in the middle.
-__device__ __forceinline__ void sharers(const Params &p, const Plan &pl, const int64_t *cum, int b, int hc, int &first,
-                                        int &count) {
-    const int64_t s0 = seg_start(p, cum, b, hc), n = cum[b + 1] - cum[b];
+__device__ __forceinline__ unsigned block_edge(const Plan &pl, const unsigned *cum, int B, int i, int end) {
+    if (!pl.per) return min(unsigned(i + end) * pl.size, pl.total);
+    const int seg = i / pl.per;
+    if (seg >= B * pl.HC) return pl.total;
+    const int b = seg / pl.HC;
+    const unsigned n = cum[b + 1] - cum[b];
+    return seg_start(pl, cum, b, seg - b * pl.HC) + min(unsigned(i - seg * pl.per + end) * pl.size, n);
+}
+// The blocks that share a segment: the first holds it in its second slot of the workspace, the others, which begin inside
+// it, in their first.
+__device__ __forceinline__ void sharers(const Plan &pl, const unsigned *cum, int seg, int &first, int &count) {
+    const int b = seg / pl.HC;
+    const unsigned s0 = seg_start(pl, cum, b, seg - b * pl.HC), n = cum[b + 1] - cum[b];
     if (pl.per) {
-        first = (b * p.a.pool.heads * p.C + hc) * pl.per;
+        first = seg * pl.per;
         count = int((n + pl.size - 1) / pl.size);
     } else {
         first = int(s0 / pl.size);
         count = int((s0 + n - 1) / pl.size) - first + 1;
     }
 }
-__device__ __forceinline__ int64_t block_start(const Params &p, const Plan &pl, const int64_t *cum, int i) {
-    if (!pl.per) return i * pl.size < pl.total ? i * pl.size : pl.total;
-    const int HC = p.a.pool.heads * p.C, seg = i / pl.per;
-    if (seg >= p.B * HC) return pl.total;
-    const int64_t n = cum[seg / HC + 1] - cum[seg / HC], at = (i % pl.per) * pl.size;
-    return seg_start(p, cum, seg / HC, seg % HC) + (at < n ? at : n);
-}
-__device__ __forceinline__ int64_t block_end(const Params &p, const Plan &pl, const int64_t *cum, int i) {
-    if (!pl.per) return block_start(p, pl, cum, i + 1);
-    const int HC = p.a.pool.heads * p.C, seg = i / pl.per;
-    if (seg >= p.B * HC) return pl.total;
-    const int64_t n = cum[seg / HC + 1] - cum[seg / HC], at = (i % pl.per + 1) * pl.size;
-    return seg_start(p, cum, seg / HC, seg % HC) + (at < n ? at : n);
-}
 
-// Partials are kept in fragment order: element e = ((chunk * NT + group) * 4 + register) * 32 + lane.
-template <int KT, int NT> __device__ __forceinline__ void element(int e, int &d, int &head) {
-    const int lane = e & 31, r = (e >> 5) & 3, n = (e >> 7) % NT, c = (e >> 7) / NT;
-    const int g = lane >> 2, j = lane & 3;
-    head = 8 * n + 2 * j + (r & 1);
-    d = KT == QPACK_KV_I8 ? 16 * c + 2 * g + (r >> 1) : 16 * c + 8 * (r >> 1) + g;
+// Where a tile lies: row, segment of the row, its key/value head and group of query heads, tile of the segment.
+struct Cursor {
+    int b, hc, h, q;
+    unsigned ti;
+    Row row;
+};
+template <int TOK> __device__ __forceinline__ void seek(const Params &p, const Plan &pl, const unsigned *cum, unsigned tile, Cursor &c) {
+    int lo = 0, hi = p.B;                                  // cum[lo] HC <= tile < cum[hi] HC
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cum[mid] * pl.HC <= tile) lo = mid; else hi = mid;
+    }
+    c.b = lo;
+    c.row = row_of<TOK>(p, lo, nullptr);
+    const unsigned rem = tile - cum[lo] * pl.HC;
+    c.hc = int(rem / c.row.tiles);
+    c.ti = rem - c.hc * c.row.tiles;
+    c.h = c.hc / p.C;
+    c.q = c.hc - c.h * p.C;
+}
+// The next segment; there is one.
+template <int TOK> __device__ __forceinline__ void next_segment(const Params &p, const Plan &pl, const unsigned *cum, Cursor &c) {
+    c.ti = 0;
+    ++c.hc;
+    if (++c.q == p.C) c.q = 0, ++c.h;
+    if (c.hc < pl.HC) return;
+    c.hc = c.h = c.q = 0;
+    int b = c.b + 1;
+    while (cum[b + 1] == cum[b]) ++b;
+    c.b = b;
+    c.row = row_of<TOK>(p, b, nullptr);
 }
 
 // 1 / sum, or 0 where no token counted (a sum of NaN stays one).
@@ -283,55 +312,52 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -INFINITY : (m - P_BIAS) * 0.6931471805599453f + logf(l);
 }
 
-// Joins partials (part(i), i < n) and hands every element to `sink(e, head, value, base, sum)`, idx of `stride` threads.
-template <int FR, int NH, class Part, class Head, class Sink>
-__device__ __forceinline__ void join(int n, Part part, Head head_of, Sink sink, int idx, int stride) {
-    for (int e = idx; e < FR; e += stride) {
-        const int head = head_of(e);
-        float m = -INFINITY;
-        for (int i = 0; i < n; ++i) m = fmaxf(m, part(i)[FR + head]);
-        const float base = finite_base(m);
-        float o = 0.0f, l = 0.0f;
-        for (int i = 0; i < n; ++i) {
-            const float *q = part(i);
-            const float f = ex2(q[FR + head] - base);
-            o = fmaf(q[e], f, o);
-            l = fmaf(q[FR + NH + head], f, l);
-        }
-        sink(e, head, o, m, l);
+// Four accumulators (head, d .. d + 3) of n joined partials, with the partials' factors 2^(m_i - m) (factor(i, head)).
+template <int PS, class Part, class Factor>
+__device__ __forceinline__ float4 join4(int n, int head, int d, Part part, Factor factor) {
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const float4 x = *reinterpret_cast<const float4 *>(part(i) + head * PS + d);
+        const float f = factor(i, head);
+        o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y), o.z = fmaf(x.z, f, o.z), o.w = fmaf(x.w, f, o.w);
     }
+    return o;
 }
 
 template <int KT, int D, int NT>
 __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const __grid_constant__ Params p) {
     using F = Cfg<KT, D, NT>;
-    constexpr int W = F::W, STAGES = F::STAGES, TILE = F::TILE, RB = F::RB, SB = F::SB, FR = F::FR, PF = F::PF;
-    constexpr int CPR = RB / 16, CH = D / 16, NH = 8 * NT;
+    constexpr int W = F::W, STAGES = F::STAGES, TILE = F::TILE, RB = F::RB, SB = F::SB, PS = F::PS, PF = F::PF;
+    constexpr int TOK = F::TOK, CPR = RB / 16, CH = D / 16, NH = F::NH, TT = TOK / 8, THREADS = W * 32;
     constexpr bool I8 = KT == QPACK_KV_I8;
     extern __shared__ __align__(128) unsigned char smem[];
-    int64_t *cum = reinterpret_cast<int64_t *>(smem + W * STAGES * TILE);    // tiles before row b, a segment's worth
-    __shared__ int piece_seg[2 * W], piece_far[2 * W], s_max, s_last[2];
+    unsigned *cum = reinterpret_cast<unsigned *>(smem + W * STAGES * TILE);  // tiles before row b, a segment's worth
+    __shared__ int piece_seg[2 * W], piece_far[2 * W], s_last[2];
+    __shared__ unsigned s_max;
+    __shared__ const float *s_part[2 * W];
+    __shared__ float s_fac[2 * W][NH], s_inv[2 * W][NH];   // by piece: its factor, and (first of a run) the run's 1 / sum
     const AttendArgs &a = p.a;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
-    const int H = a.pool.heads, HC = H * p.C, T = a.pool.page_tokens, shift = 31 - __clz(T);
+    const int T = a.pool.page_tokens, shift = 31 - __clz(T);
 
     pdl_launch_dependents();
     pdl_wait();                                            // inputs, cache and workspace may be the previous grid's
 
     // -- the rows' tiles, and this block's share of them ------------------------------------------------------
-    for (int b = tid; b < p.B; b += W * 32) cum[b + 1] = row_of(p, b, blockIdx.x == 0 ? &g_fault_attend : nullptr).tiles;
+    for (int b = tid; b < p.B; b += THREADS)
+        cum[b + 1] = row_of<TOK>(p, b, blockIdx.x == 0 ? &g_fault_attend : nullptr).tiles;
     if (tid < 2 * W) piece_seg[tid] = -1;
     __syncthreads();
     if (w == 0) {
-        int64_t carry = 0;
-        int most = 0;
+        unsigned carry = 0, most = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const int b = b0 + lane;
-            int64_t x = b < p.B ? cum[b + 1] : 0;
-            most = max(most, int(x));
+            unsigned x = b < p.B ? cum[b + 1] : 0;
+            most = max(most, x);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+                const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += y;
             }
             x += carry;
@@ -339,118 +365,139 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
             carry = __shfl_sync(0xffffffffu, x, 31);
         }
         most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 0) {
-            cum[0] = 0;
-            s_max = most;
-        }
+        if (lane == 0) cum[0] = 0, s_max = most;
     }
     __syncthreads();
     Plan pl;
-    const int grid = gridDim.x, nseg = p.B * HC;
-    pl.total = cum[p.B] * HC;
-    pl.size = max((pl.total + grid - 1) / grid, int64_t(W));            // at least a tile a warp
+    const unsigned grid = gridDim.x;
+    pl.HC = a.pool.heads * p.C;
+    pl.total = cum[p.B] * pl.HC;
+    pl.size = max((pl.total + grid - 1) / grid, unsigned(W));           // at least a tile a warp
     pl.per = 0;
+    const unsigned nseg = p.B * pl.HC;
     if (nseg <= grid) {
         // Few segments: boundaries on theirs save the joins of the pieces, where the shares stay nearly equal.
-        const int k = grid / nseg;
-        const int64_t size = max(int64_t((s_max + k - 1) / k), int64_t(W));
+        const unsigned k = grid / nseg, size = max((s_max + k - 1) / k, unsigned(W));
         if (size <= pl.size + pl.size / 8) {
             pl.size = size;
-            pl.per = int((s_max + size - 1) / size);
-            if (pl.per < 1) pl.per = 1;
+            pl.per = max(int((s_max + size - 1) / size), 1);
         }
     }
     for (int b = blockIdx.x; b < p.B; b += grid) {
         if (cum[b + 1] != cum[b]) continue;                // an empty row
-        for (int i = tid; i < a.q_heads * D; i += W * 32) store1(a.out, a.odt, int64_t(p.row0 + b) * a.ldo + i, 0.0f);
+        const float zero = 0.0f;
+        for (int i = tid; i < a.q_heads * D; i += THREADS) store_out<1>(a.out, a.odt, int64_t(p.row0 + b) * a.ldo + i, &zero);
         if (a.lse)
-            for (int i = tid; i < a.q_heads; i += W * 32) a.lse[int64_t(p.row0 + b) * a.q_heads + i] = -INFINITY;
+            for (int i = tid; i < a.q_heads; i += THREADS) a.lse[int64_t(p.row0 + b) * a.q_heads + i] = -INFINITY;
     }
-    const int64_t start = block_start(p, pl, cum, blockIdx.x), end = block_end(p, pl, cum, blockIdx.x);
+    const unsigned start = block_edge(pl, cum, p.B, blockIdx.x, 0), end = block_edge(pl, cum, p.B, blockIdx.x, 1);
     if (start >= end) return;
-
-    // Results of a segment's element, and its log-sum-exp.
-    auto put = [&](int b, int hc, int head, int d, float x) {
-        const int in = hc % p.C * NH + head;
-        if (in < p.G) store1(a.out, a.odt, int64_t(p.row0 + b) * a.ldo + int64_t(hc / p.C * p.G + in) * D + d, x);
-    };
-    auto put_lse = [&](int b, int hc, int head, float x) {
-        const int in = hc % p.C * NH + head;
-        if (a.lse && in < p.G) a.lse[int64_t(p.row0 + b) * a.q_heads + hc / p.C * p.G + in] = x;
-    };
 
     // -- this warp's share -------------------------------------------------------------------------------------
     unsigned char *ring = smem + w * STAGES * TILE;
-    const int share = int((end - start + W - 1) / W);
-    const int64_t w0 = start + int64_t(w) * share;
-    const int nt = int(end - w0 < share ? end - w0 : share);
+    const int share = int((end - start + W - 1) / W), w0 = int(start) + w * share;
+    const int nt = min(int(end) - w0, share);
     if (nt > 0) {
         const uint32_t ring32 = smem_u32(ring);
         Cursor ci, cc;
-        seek(p, cum, w0, ci);
+        seek<TOK>(p, pl, cum, unsigned(w0), ci);
         cc = ci;
+
+        // The page of the tile, or of lane's token of it where pages are smaller than a tile; loaded a tile ahead of its
+        // use.
+        const bool large = T >= TOK;
+        auto page_of = [&](const Cursor &c) {
+            const unsigned t = c.row.base + c.ti * TOK + (large ? 0 : lane % TOK);
+            return large || (t >= c.row.lo && t < c.row.len) ? __ldg(c.row.table + (t >> shift)) : -1;
+        };
+        int entry = page_of(ci);
+        // Starts the copies of the cursor's tile into a stage: chunk i * 32 + lane of the tile goes to its row, at its
+        // place in the row xor the row's number, so that ldmatrix's eight rows meet different banks. Rows outside
+        // [lo, len) and of pages outside the pool are filled with zeros.
+        constexpr bool SWZ = RB % 128 == 0;
+        const int r0 = lane / CPR;
+        const uint32_t sw0 = r0 * RB + (((lane % CPR) ^ (SWZ ? r0 & 7 : (r0 >> 1) & 3)) << 4);
         const unsigned char *kbase = static_cast<const unsigned char *>(a.pool.k) + a.layer * a.pool.layer_stride * F::ES;
         const unsigned char *vbase = static_cast<const unsigned char *>(a.pool.v) + a.layer * a.pool.layer_stride * F::ES;
         const uint16_t *ksbase = I8 ? a.pool.k_scales + a.layer * a.pool.scale_layer_stride : nullptr;
         const uint16_t *vsbase = I8 ? a.pool.v_scales + a.layer * a.pool.scale_layer_stride : nullptr;
-
-        // The page of lane's token of the tile (tokens lane % 16), loaded a tile ahead of its use.
-        auto page_of = [&](const Cursor &c) {
-            const unsigned t = c.row.base + c.ti * TOK + (lane & 15);
-            return t >= c.row.lo && t < c.row.len ? __ldg(c.row.table + (t >> shift)) : -1;
-        };
-        int entry = page_of(ci);
-        // Starts the copies of the cursor's tile into a stage. Rows outside [lo, len) and of pages outside the pool are
-        // filled with zeros.
-        auto issue = [&](int stage) {
-            const uint32_t dst = ring32 + stage * TILE;
-            const unsigned t0 = ci.row.base + ci.ti * TOK, mine = t0 + (lane & 15);
-            const bool in = mine >= ci.row.lo && mine < ci.row.len;
-            const bool ok = in && entry >= 0 && entry < a.pool.pages;
-            if (in && !ok && lane < 16) atomicOr(&g_fault_attend, FAULT_PAGE);
-            const int page = ok ? entry : 0, h = ci.hc / p.C;
-            // element offset of the token's row
-            const int64_t row = int64_t(page) * a.pool.page_stride + (int64_t(h) * T + (mine & (T - 1))) * D;
-            const unsigned okmask = __ballot_sync(0xffffffffu, ok);
+        auto issue = [&](uint32_t dst) {
+            const unsigned t0 = ci.row.base + ci.ti * TOK;
+            if (large && t0 >= ci.row.lo && ci.row.len - t0 >= TOK && unsigned(entry) < unsigned(a.pool.pages)) {
+                // a whole tile of one page: consecutive rows
+                const unsigned row = unsigned(ci.h * T) + (t0 & (T - 1));
+                const int64_t at = (int64_t(entry) * a.pool.page_stride + row * unsigned(D)) * F::ES + lane * 16;
+                const unsigned char *ks = kbase + at, *vs = vbase + at;
 #pragma unroll
-            for (int i = 0; i < CPR / 2; ++i) {
-                const int idx = i * 32 + lane, r = idx / CPR, c = idx % CPR;
-                const int64_t off = __shfl_sync(0xffffffffu, row, r) * F::ES + c * 16;
-                const bool live = (okmask >> r) & 1;
-                const uint32_t sw = r * RB + ((c ^ (RB % 128 == 0 ? r & 7 : (r >> 1) & 3)) << 4);
-                cp16(dst + sw, kbase + off, live);
-                cp16(dst + TOK * RB + sw, vbase + off, live);
-            }
-            if (I8) {
-                const int64_t srow = int64_t(page) * a.pool.scale_page_stride + (int64_t(h) * T + (mine & (T - 1))) * (D / 32);
-                cp_small<SB ? SB : 16>(dst + 2 * TOK * RB + lane * SB, (lane < 16 ? ksbase : vsbase) + srow, ok);
+                for (int i = 0; i < TOK * CPR / 32; ++i) {
+                    const uint32_t to = dst + i * 512 + (sw0 ^ (SWZ ? ((i * 32 / CPR) & 7) << 4 : 0));
+                    cp16(to, ks + i * 512);
+                    cp16(to + TOK * RB, vs + i * 512);
+                }
+                if (I8) {
+                    const int64_t sat = int64_t(entry) * a.pool.scale_page_stride + (row + lane % TOK) * unsigned(D / 32);
+                    const uint32_t to = dst + 2 * TOK * RB + lane * SB;
+                    if (TOK == 32) {
+                        cp_small<SB ? SB : 16>(to, ksbase + sat, true);
+                        cp_small<SB ? SB : 16>(to + TOK * SB, vsbase + sat, true);
+                    } else {
+                        cp_small<SB ? SB : 16>(to, (lane < 16 ? ksbase : vsbase) + sat, true);
+                    }
+                }
+            } else {
+                const unsigned mine = t0 + lane % TOK;
+                const bool in = mine >= ci.row.lo && mine < ci.row.len;
+                const bool ok = in && unsigned(entry) < unsigned(a.pool.pages);
+                if (in && !ok) atomicOr(&g_fault_attend, FAULT_PAGE);
+                const unsigned okmask = __ballot_sync(0xffffffffu, ok);
+                const int page = ok ? entry : 0;
+                const unsigned slot = unsigned(ci.h * T) + (mine & (T - 1));
+                const int64_t row = int64_t(page) * a.pool.page_stride + slot * unsigned(D);
+#pragma unroll 4
+                for (int i = 0; i < TOK * CPR / 32; ++i) {
+                    const int idx = i * 32 + lane, r = idx / CPR, c = idx % CPR;
+                    const int64_t off = __shfl_sync(0xffffffffu, row, r) * F::ES + c * 16;
+                    const bool live = (okmask >> r) & 1;
+                    const uint32_t to = dst + i * 512 + (sw0 ^ (SWZ ? ((i * 32 / CPR) & 7) << 4 : 0));
+                    cp16(to, kbase + off, live);
+                    cp16(to + TOK * RB, vbase + off, live);
+                }
+                if (I8) {
+                    const int64_t sat = int64_t(page) * a.pool.scale_page_stride + slot * unsigned(D / 32);
+                    const uint32_t to = dst + 2 * TOK * RB + lane * SB;
+                    if (TOK == 32) {
+                        cp_small<SB ? SB : 16>(to, ksbase + sat, ok);
+                        cp_small<SB ? SB : 16>(to + TOK * SB, vsbase + sat, ok);
+                    } else {
+                        cp_small<SB ? SB : 16>(to, (lane < 16 ? ksbase : vsbase) + sat, ok);
+                    }
+                }
             }
         };
-#pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s) {
-            if (s < nt) {
-                issue(s);
-                if (s + 1 < nt) {
-                    step(p, cum, ci);
+        int left = nt;                                     // tiles to issue
+        auto advance = [&](int slot) {
+            if (left > 0) {
+                issue(ring32 + slot * TILE);
+                if (--left) {
+                    if (++ci.ti == ci.row.tiles) next_segment<TOK>(p, pl, cum, ci);
                     entry = page_of(ci);
                 }
             }
             cp_commit();
-        }
+        };
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s) advance(s);
 
-        // ldmatrix: lane addresses row lr of the tile, chunk (even) + lane / 16
-        const int lr = (lane & 7) + (lane & 8), lx = ((lane >> 4) ^ (RB % 128 == 0 ? lr & 7 : (lr >> 1) & 3)) << 4;
-        const uint32_t lrow = lr * RB;
-        uint32_t qf[CH][4 * NT];
-        float qs[NT], m[NT], l[NT], acc[CH][NT][4];
-        int begun = 0;                                     // the tile of the share with which this segment began
-        bool whole = false;
-        for (int i = 0; i < nt; ++i) {
-            if (i == 0 || cc.ti == 0) {
-                // -- a segment begins: its queries, rotated, scaled and split -----------------------------------
-                begun = i;
-                whole = cc.ti == 0;
-                const int h = cc.hc / p.C, first = cc.hc % p.C * NH;
+        // ldmatrix: lane addresses row lr of 16 tokens, chunk (even) + lane / 16
+        const int lr = (lane & 7) + (lane & 8), lx = ((lane >> 4) ^ (SWZ ? lr & 7 : (lr >> 1) & 3)) << 4;
+        int slot = 0;
+        for (int done = 0; done < nt;) {
+            // -- a segment begins: its queries, rotated, scaled and split ---------------------------------------
+            const bool whole = cc.ti == 0;
+            const int count = min(int(cc.row.tiles - cc.ti), nt - done);
+            uint32_t qf[CH][4 * NT];
+            float qs[NT], m[NT], l[NT], acc[CH][NT][4];
+            {
                 const int64_t pos = int64_t(cc.row.len) - 1;
                 const bool turn = a.rope && pos < a.rope_rows;
                 if (a.rope && !turn) atomicOr(&g_fault_attend, FAULT_PAGE);
@@ -458,31 +505,48 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                 for (int n = 0; n < NT; ++n) {
                     m[n] = -INFINITY;
                     l[n] = 0.0f;
-                    const int head = first + 8 * n + g;
-                    float x[CH][4];
-                    const int64_t at = int64_t(p.row0 + cc.b) * a.ldq + int64_t(h * p.G + head) * D;
+                    const int head = cc.q * NH + 8 * n + g;
+                    const int64_t at = int64_t(p.row0 + cc.b) * a.ldq + int64_t(cc.h * p.G + head) * D;
                     // a thread's four elements of chunk c: 16 c + 4 j .. + 3, or 16 c + 2 j, + 1 and 8 further
                     constexpr int gap = I8 ? 2 : 8;
                     const int d0 = I8 ? 4 * j : 2 * j;
+                    float x[CH][4];
+                    auto fetch = [&](auto tag) {
+                        constexpr int DT = decltype(tag)::value;
 #pragma unroll
-                    for (int c = 0; c < CH; ++c) {
-                        x[c][0] = x[c][1] = x[c][2] = x[c][3] = 0.0f;
-                        if (head < p.G) {
-                            load2(a.q, a.qdt, at + 16 * c + d0, x[c]);
-                            load2(a.q, a.qdt, at + 16 * c + d0 + gap, x[c] + 2);
+                        for (int c = 0; c < CH; ++c) {
+                            if (I8) {
+                                load_q<DT, 4>(a.q, at + 16 * c + d0, x[c]);
+                            } else {
+                                load_q<DT, 2>(a.q, at + 16 * c + d0, x[c]);
+                                load_q<DT, 2>(a.q, at + 16 * c + d0 + gap, x[c] + 2);
+                            }
                         }
+                    };
+                    if (head >= p.G) {
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) x[c][0] = x[c][1] = x[c][2] = x[c][3] = 0.0f;
+                    } else if (a.qdt == DT_F32) {
+                        fetch(Int<DT_F32>());
+                    } else if (a.qdt == DT_F16) {
+                        fetch(Int<DT_F16>());
+                    } else {
+                        fetch(Int<DT_BF16>());
                     }
                     if (turn) {
-                        const float *row = a.rope + pos * D;
+                        const float *row = a.rope + pos * D + d0;
 #pragma unroll
                         for (int c = 0; c < CH / 2; ++c)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int d = 16 * c + d0 + (e >> 1) * gap + (e & 1);
-                                const float co = __ldg(row + d), si = __ldg(row + D / 2 + d);
-                                const float u = x[c][e], v = x[c + CH / 2][e];
-                                x[c][e] = __fsub_rn(__fmul_rn(u, co), __fmul_rn(v, si));
-                                x[c + CH / 2][e] = __fadd_rn(__fmul_rn(v, co), __fmul_rn(u, si));
+                            for (int e = 0; e < 4; e += 2) {
+                                const int d = 16 * c + (e >> 1) * gap;
+                                const float2 co = __ldg(reinterpret_cast<const float2 *>(row + d));
+                                const float2 si = __ldg(reinterpret_cast<const float2 *>(row + D / 2 + d));
+                                const float u0 = x[c][e], v0 = x[c + CH / 2][e], u1 = x[c][e + 1], v1 = x[c + CH / 2][e + 1];
+                                x[c][e] = __fsub_rn(__fmul_rn(u0, co.x), __fmul_rn(v0, si.x));
+                                x[c][e + 1] = __fsub_rn(__fmul_rn(u1, co.y), __fmul_rn(v1, si.y));
+                                x[c + CH / 2][e] = __fadd_rn(__fmul_rn(v0, co.x), __fmul_rn(u0, si.x));
+                                x[c + CH / 2][e + 1] = __fadd_rn(__fmul_rn(v1, co.y), __fmul_rn(u1, si.y));
                             }
                     }
                     float big = 0.0f;
@@ -492,311 +556,365 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                         for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(x[c][e]));
                     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
                     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                    // 2^(13 - exponent of the maximum), within fp32's normal range; 1 for zero, inf and NaN
+                    // 2^(13 - exponent of the maximum), within fp32's normal range; 1 for zero, inf and NaN. The scale's
+                    // sign goes with it, so that the largest score is the largest sum.
                     const int ex = __float_as_int(big) >> 23;
                     const int up = big == 0.0f || ex == 255 ? 127 : min(254, 267 - ex);
-                    const float f = __int_as_float(up << 23), back = __int_as_float(max(254 - up, 1) << 23);
-                    qs[n] = a.scale * 1.4426950408889634f * back * (up == 254 ? 0.5f : 1.0f);
+                    const float f = __int_as_float((up << 23) | (__float_as_int(a.scale) & 0x80000000));
+                    const float back = __int_as_float(max(254 - up, 1) << 23);
+                    qs[n] = fabsf(a.scale) * 1.4426950408889634f * back * (up == 254 ? 0.5f : 1.0f);
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
                         uint32_t h0, l0, h1, l1;
                         split2<KT>(x[c][0] * f, x[c][1] * f, h0, l0);
                         split2<KT>(x[c][2] * f, x[c][3] * f, h1, l1);
                         if (NT == 1) {
-                            qf[c][0] = h0;
-                            qf[c][1] = l0;
-                            qf[c][2] = h1;
-                            qf[c][3] = l1;
+                            qf[c][0] = h0, qf[c][1] = l0, qf[c][2] = h1, qf[c][3] = l1;
                         } else {
-                            qf[c][n] = h0;
-                            qf[c][2 + n] = h1;
-                            qf[c][4 * (NT - 1) + n] = l0;
-                            qf[c][4 * (NT - 1) + 2 + n] = l1;
+                            qf[c][n] = h0, qf[c][2 + n] = h1;
+                            qf[c][4 * (NT - 1) + n] = l0, qf[c][4 * (NT - 1) + 2 + n] = l1;
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[c][n][r] = 0.0f;
+                    }
+                }
+            }
+            unsigned t0 = cc.row.base + cc.ti * TOK;
+            for (int k = 0; k < count; ++k, t0 += TOK) {
+                cp_wait<STAGES - 2>();
+                __syncwarp();                              // the tile is there, and the stage before it is read
+                advance(slot == 0 ? STAGES - 1 : slot - 1);
+                const uint32_t st = ring32 + slot * TILE + lr * RB;
+                const unsigned char *sk = ring + slot * TILE + 2 * TOK * RB, *sv = sk + TOK * SB;
+                slot = slot + 1 == STAGES ? 0 : slot + 1;
+
+                // -- scores ---------------------------------------------------------------------------------
+                float sc[TT][4];
+#pragma unroll
+                for (int t = 0; t < TT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.0f;
+#pragma unroll
+                for (int u = 0; u < TOK / 16; ++u) {
+                    if (I8) {
+                        uint32_t sw[2][SB ? SB / 4 : 1];
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) load_words<SB ? SB : 4>(sk + (g + 8 * t + 16 * u) * SB, sw[t]);
+#pragma unroll
+                        for (int c = 0; c < CH; c += 2) {
+                            uint32_t r[4];
+                            ldsm4((st + u * 16 * RB) + ((c * 16) ^ lx), r);
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                const uint32_t s = __byte_perm(sw[t][c / 4], 0u, (c / 2) & 1 ? 0x3232u : 0x1010u);
+#pragma unroll
+                                for (int v = 0; v < 2; ++v) {
+                                    const uint32_t word = r[2 * v + t] ^ 0x80808080u;
+                                    const uint32_t b0 = dequant2(word, 0x4140u, s), b1 = dequant2(word, 0x4342u, s);
+                                    const uint32_t *q = qf[c + v];
+                                    mma<KT>(sc[2 * u + t], q[0], q[1], q[2], q[3], b0, b1);
+                                    if (NT == 2) mma<KT>(sc[2 * u + t], q[4 * NT - 4], q[4 * NT - 3], q[4 * NT - 2], q[4 * NT - 1], b0, b1);
+                                }
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            uint32_t r[4];
+                            ldsm4((st + u * 16 * RB) + ((c * 32) ^ lx), r);
+                            const uint32_t *q = qf[c];
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                mma<KT>(sc[2 * u + t], q[0], q[1], q[2], q[3], r[t], r[2 + t]);
+                                if (NT == 2) mma<KT>(sc[2 * u + t], q[4 * NT - 4], q[4 * NT - 3], q[4 * NT - 2], q[4 * NT - 1], r[t], r[2 + t]);
+                            }
                         }
                     }
+                }
+
+                // -- softmax --------------------------------------------------------------------------------
+                // s[n][2 t + e]: head g of group n, token 8 t + 2 j + e, before the factor qs > 0
+                float s[NT][2 * TT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2 * TT; ++e)
+                        s[n][e] = NT == 1 ? sc[e >> 1][e & 1] + sc[e >> 1][2 + (e & 1)] : sc[e >> 1][2 * n + (e & 1)];
+                if (t0 < cc.row.lo || cc.row.len - t0 < TOK) {
+#pragma unroll
+                    for (int e = 0; e < 2 * TT; ++e) {
+                        const unsigned t = t0 + 8 * (e >> 1) + 2 * j + (e & 1);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            if (t < cc.row.lo || t >= cc.row.len) s[n][e] = -INFINITY;
+                    }
+                }
+                bool up = false;
+                float mt[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float x = s[n][0];
+#pragma unroll
+                    for (int e = 1; e < 2 * TT; ++e) x = fmaxf(x, s[n][e]);
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                    mt[n] = fmaxf(x * qs[n], m[n]);
+                    up |= mt[n] > m[n];
+                }
+                if (__any_sync(0xffffffffu, up)) {         // rare after the first tiles
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const float f = ex2(m[n] - finite_base(mt[n]));
+                        m[n] = mt[n];
+                        l[n] *= f;
+                        const float f0 = __shfl_sync(0xffffffffu, f, 8 * j), f1 = __shfl_sync(0xffffffffu, f, 8 * j + 4);
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            acc[c][n][0] *= f0;
+                            acc[c][n][1] *= f1;
+                            acc[c][n][2] *= f0;
+                            acc[c][n][3] *= f1;
+                        }
+                    }
+                }
+                uint32_t ph[NT][TT], plo[NT][TT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float base = P_BIAS - finite_base(m[n]);
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 2 * TT; ++e) {
+                        s[n][e] = ex2(fmaf(s[n][e], qs[n], base));
+                        sum += s[n][e];
+                    }
+                    l[n] += sum;
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) split2<KT>(s[n][2 * t], s[n][2 * t + 1], ph[n][t], plo[n][t]);
+                }
+
+                // -- values ---------------------------------------------------------------------------------
+#pragma unroll
+                for (int u = 0; u < TOK / 16; ++u) {
+                    if (I8) {
+                        // scales of tokens 2j and 2j + 1, and of 2j + 8 and 2j + 9: rows next to each other
+                        uint32_t va[2][SB ? SB / 2 : 1];
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) load_words<SB ? 2 * SB : 4>(sv + (2 * j + 8 * t + 16 * u) * SB, va[t]);
+#pragma unroll
+                        for (int c = 0; c < CH; c += 2) {
+                            uint32_t r[4];
+                            ldsm4_t((st + (TOK + u * 16) * RB) + ((c * 16) ^ lx), r);
+                            const uint32_t sel = (c / 2) & 1 ? 0x7632u : 0x5410u;
+                            const uint32_t s0 = __byte_perm(va[0][c / 4], va[0][(SB ? SB / 4 : 0) + c / 4], sel);
+                            const uint32_t s1 = __byte_perm(va[1][c / 4], va[1][(SB ? SB / 4 : 0) + c / 4], sel);
+#pragma unroll
+                            for (int v = 0; v < 2; ++v) {
+                                const uint32_t x0 = r[2 * v] ^ 0x80808080u, x1 = r[2 * v + 1] ^ 0x80808080u;
+                                const uint32_t a0 = dequant2(x0, 0x4240u, s0), a1 = dequant2(x0, 0x4341u, s0);
+                                const uint32_t a2 = dequant2(x1, 0x4240u, s1), a3 = dequant2(x1, 0x4341u, s1);
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    mma<KT>(acc[c + v][n], a0, a1, a2, a3, ph[n][2 * u], ph[n][2 * u + 1]);
+                                    mma<KT>(acc[c + v][n], a0, a1, a2, a3, plo[n][2 * u], plo[n][2 * u + 1]);
+                                }
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            uint32_t r[4];
+                            ldsm4_t((st + (TOK + u * 16) * RB) + ((c * 32) ^ lx), r);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                mma<KT>(acc[c][n], r[0], r[2], r[1], r[3], ph[n][2 * u], ph[n][2 * u + 1]);
+                                mma<KT>(acc[c][n], r[0], r[2], r[1], r[3], plo[n][2 * u], plo[n][2 * u + 1]);
+                            }
+                        }
+                    }
+                }
+            }
+
+            // -- the segment's end, or the share's --------------------------------------------------------------
+            const bool ended = cc.ti + count == cc.row.tiles, last = done + count == nt;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
+                l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
+            }
+            // a thread's elements: heads 8 n + 2 j + (r & 1), d = 16 c + 2 g + (r >> 1) or 16 c + g + 8 (r >> 1)
+            constexpr int gd = I8 ? 2 : 1, rd = I8 ? 1 : 8;
+            if (ended && whole) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float inv = inverse(l[n]);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float f = __shfl_sync(0xffffffffu, inv, 8 * j + 4 * r);
+                        const int head = cc.q * NH + 8 * n + 2 * j + r;
+                        if (head < p.G) {
+                            const int64_t at = int64_t(p.row0 + cc.b) * a.ldo + int64_t(cc.h * p.G + head) * D + gd * g;
+#pragma unroll
+                            for (int c = 0; c < CH; ++c) {
+                                const float o[2] = {acc[c][n][r] * f, acc[c][n][2 + r] * f};
+                                if (I8) {
+                                    store_out<2>(a.out, a.odt, at + 16 * c, o);
+                                } else {
+                                    store_out<1>(a.out, a.odt, at + 16 * c, o);
+                                    store_out<1>(a.out, a.odt, at + 16 * c + 8, o + 1);
+                                }
+                            }
+                        }
+                    }
+                    const int head = cc.q * NH + 8 * n + g;
+                    if (a.lse && j == 0 && head < p.G)
+                        a.lse[int64_t(p.row0 + cc.b) * a.q_heads + cc.h * p.G + head] = lse_of(m[n], l[n]);
+                }
+            } else {
+                // The first of two pieces waits in global memory (the ring is in use), the last one in the ring.
+                if (last) {
+                    cp_wait<0>();
+                    __syncwarp();
+                }
+                float *dst = last ? reinterpret_cast<float *>(ring) : p.warp_parts + (int64_t(blockIdx.x) * W + w) * PF;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
 #pragma unroll
                     for (int c = 0; c < CH; ++c)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[c][n][r] = 0.0f;
+                        for (int r = 0; r < 4; ++r)
+                            dst[(8 * n + 2 * j + (r & 1)) * PS + 16 * c + gd * g + rd * (r >> 1)] = acc[c][n][r];
+                    if (j == 0) {
+                        dst[NH * PS + 8 * n + g] = m[n];
+                        dst[NH * PS + NH + 8 * n + g] = l[n];
+                    }
+                }
+                if (lane == 0) {
+                    const int at = 2 * w + (done == 0 ? 0 : 1);
+                    piece_seg[at] = cc.b * pl.HC + cc.hc;
+                    piece_far[at] = last ? 0 : 1;
                 }
             }
-            cp_wait<STAGES - 2>();
-            __syncwarp();                                  // the tile is there, and the stage before it is read
-            if (i + STAGES - 1 < nt) {
-                issue((i + STAGES - 1) % STAGES);
-                if (i + STAGES < nt) {
-                    step(p, cum, ci);
-                    entry = page_of(ci);
-                }
-            }
-            cp_commit();
-            const uint32_t st = ring32 + (i % STAGES) * TILE;
-
-            // -- scores -------------------------------------------------------------------------------------
-            float sc[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-            uint32_t sw[2][SB ? SB / 4 : 1];
-            if (I8) {
-#pragma unroll
-                for (int q = 0; q < SB / 4; ++q)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        sw[t][q] = *reinterpret_cast<const uint32_t *>(ring + (i % STAGES) * TILE + 2 * TOK * RB + (g + 8 * t) * SB + 4 * q);
-#pragma unroll
-                for (int c = 0; c < CH; c += 2) {
-                    uint32_t r[4];
-                    ldsm4(st + lrow + ((c * 16) ^ lx), r);
-                    const uint32_t sel = (c / 2) & 1 ? 0x3232u : 0x1010u;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const uint32_t s = __byte_perm(sw[t][c / 4], 0u, sel);
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const uint32_t word = r[2 * u + t] ^ 0x80808080u;
-                            const uint32_t b0 = dequant2(word, 0x4140u, s), b1 = dequant2(word, 0x4342u, s);
-                            mma<KT>(sc[t], qf[c + u][0], qf[c + u][1], qf[c + u][2], qf[c + u][3], b0, b1);
-                            if (NT == 2) mma<KT>(sc[t], qf[c + u][4 * NT - 4], qf[c + u][4 * NT - 3], qf[c + u][4 * NT - 2], qf[c + u][4 * NT - 1], b0, b1);
-                        }
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    uint32_t r[4];
-                    ldsm4(st + lrow + ((c * 32) ^ lx), r);
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        mma<KT>(sc[t], qf[c][0], qf[c][1], qf[c][2], qf[c][3], r[t], r[2 + t]);
-                        if (NT == 2) mma<KT>(sc[t], qf[c][4 * NT - 4], qf[c][4 * NT - 3], qf[c][4 * NT - 2], qf[c][4 * NT - 1], r[t], r[2 + t]);
-                    }
-                }
-            }
-
-            // -- softmax ------------------------------------------------------------------------------------
-            const unsigned t0 = cc.row.base + cc.ti * TOK;
-            const bool edge = t0 < cc.row.lo || cc.row.len - t0 < TOK;
-            uint32_t ph[NT][2], plo[NT][2];
-            float x[NT][4];
-            bool up = false;
-            float mt[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float s = NT == 1 ? sc[e >> 1][e & 1] + sc[e >> 1][2 + (e & 1)] : sc[e >> 1][2 * n + (e & 1)];
-                    x[n][e] = s * qs[n];
-                    if (edge) {
-                        const unsigned t = t0 + 8 * (e >> 1) + 2 * j + (e & 1);
-                        if (t < cc.row.lo || t >= cc.row.len) x[n][e] = -INFINITY;
-                    }
-                }
-                mt[n] = fmaxf(fmaxf(x[n][0], x[n][1]), fmaxf(x[n][2], x[n][3]));
-                mt[n] = fmaxf(mt[n], __shfl_xor_sync(0xffffffffu, mt[n], 1));
-                mt[n] = fmaxf(mt[n], __shfl_xor_sync(0xffffffffu, mt[n], 2));
-                mt[n] = fmaxf(mt[n], m[n]);
-                up |= mt[n] > m[n];
-            }
-            if (__any_sync(0xffffffffu, up)) {             // rare after the first tiles
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float f = ex2(m[n] - finite_base(mt[n]));
-                    m[n] = mt[n];
-                    l[n] *= f;
-                    const float f0 = __shfl_sync(0xffffffffu, f, 8 * j), f1 = __shfl_sync(0xffffffffu, f, 8 * j + 4);
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) {
-                        acc[c][n][0] *= f0;
-                        acc[c][n][1] *= f1;
-                        acc[c][n][2] *= f0;
-                        acc[c][n][3] *= f1;
-                    }
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float base = finite_base(m[n]) - P_BIAS;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[n][e] = ex2(x[n][e] - base);
-                l[n] += (x[n][0] + x[n][1]) + (x[n][2] + x[n][3]);
-                split2<KT>(x[n][0], x[n][1], ph[n][0], plo[n][0]);
-                split2<KT>(x[n][2], x[n][3], ph[n][1], plo[n][1]);
-            }
-
-            // -- values -------------------------------------------------------------------------------------
-            if (I8) {
-                // scales of tokens 2j, 2j + 1 (and 8 further): pairs of the groups
-                uint32_t va[2][2][SB ? SB / 4 : 1];
-#pragma unroll
-                for (int q = 0; q < SB / 4; ++q)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
-                            va[t][u][q] = *reinterpret_cast<const uint32_t *>(ring + (i % STAGES) * TILE + TOK * (2 * RB + SB) +
-                                                                              (2 * j + 8 * t + u) * SB + 4 * q);
-#pragma unroll
-                for (int c = 0; c < CH; c += 2) {
-                    uint32_t r[4];
-                    ldsm4_t(st + TOK * RB + lrow + ((c * 16) ^ lx), r);
-                    const uint32_t sel = (c / 2) & 1 ? 0x7632u : 0x5410u;
-                    const uint32_t s0 = __byte_perm(va[0][0][c / 4], va[0][1][c / 4], sel);
-                    const uint32_t s1 = __byte_perm(va[1][0][c / 4], va[1][1][c / 4], sel);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t x0 = r[2 * u] ^ 0x80808080u, x1 = r[2 * u + 1] ^ 0x80808080u;
-                        const uint32_t a0 = dequant2(x0, 0x4240u, s0), a1 = dequant2(x0, 0x4341u, s0);
-                        const uint32_t a2 = dequant2(x1, 0x4240u, s1), a3 = dequant2(x1, 0x4341u, s1);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma<KT>(acc[c + u][n], a0, a1, a2, a3, ph[n][0], ph[n][1]);
-                            mma<KT>(acc[c + u][n], a0, a1, a2, a3, plo[n][0], plo[n][1]);
-                        }
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    uint32_t r[4];
-                    ldsm4_t(st + TOK * RB + lrow + ((c * 32) ^ lx), r);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma<KT>(acc[c][n], r[0], r[2], r[1], r[3], ph[n][0], ph[n][1]);
-                        mma<KT>(acc[c][n], r[0], r[2], r[1], r[3], plo[n][0], plo[n][1]);
-                    }
-                }
-            }
-
-            // -- the segment's end, or the share's ----------------------------------------------------------
-            const bool done = cc.ti + 1 == cc.row.tiles, last = i + 1 == nt;
-            if (done || last) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
-                    l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
-                }
-                if (done && whole) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float inv = inverse(l[n]);
-                        const float f0 = __shfl_sync(0xffffffffu, inv, 8 * j), f1 = __shfl_sync(0xffffffffu, inv, 8 * j + 4);
-#pragma unroll
-                        for (int c = 0; c < CH; ++c)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                int d, head;
-                                element<KT, NT>(((c * NT + n) * 4 + r) * 32 + lane, d, head);
-                                put(cc.b, cc.hc, head, d, acc[c][n][r] * (r & 1 ? f1 : f0));
-                            }
-                        if (j == 0) put_lse(cc.b, cc.hc, 8 * n + g, lse_of(m[n], l[n]));
-                    }
-                } else {
-                    // The first of two pieces waits in global memory (the ring is in use), the last one in the ring.
-                    if (last) {
-                        cp_wait<0>();
-                        __syncwarp();
-                    }
-                    float *dst = last ? reinterpret_cast<float *>(ring) : p.warp_parts + (int64_t(blockIdx.x) * W + w) * PF;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                        for (int c = 0; c < CH; ++c)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) dst[((c * NT + n) * 4 + r) * 32 + lane] = acc[c][n][r];
-                        if (j == 0) {
-                            dst[FR + 8 * n + g] = m[n];
-                            dst[FR + NH + 8 * n + g] = l[n];
-                        }
-                    }
-                    if (lane == 0) {
-                        const int at = 2 * w + (begun == 0 ? 0 : 1);
-                        piece_seg[at] = cc.b * HC + cc.hc;
-                        piece_far[at] = last ? 0 : 1;
-                    }
-                }
-            }
-            if (!last) step(p, cum, cc);
+            done += count;
+            if (!last) next_segment<TOK>(p, pl, cum, cc);
         }
         cp_wait<0>();
     }
     __syncthreads();
 
     // -- joins ------------------------------------------------------------------------------------------------
-    // Pieces in the order of their tiles; runs of one segment are found by ballots, each warp for itself.
-    const int seg = lane < 2 * W ? piece_seg[lane] : -1;
+    // Pieces in the order of their tiles, runs of one segment among them; every warp finds the runs for itself, a piece
+    // a lane.
+    int seg = lane < 2 * W ? piece_seg[lane] : -1;
     const unsigned valid = __ballot_sync(0xffffffffu, seg >= 0);
-    const unsigned below = valid & ((1u << lane) - 1u);
-    const int prev = __shfl_sync(0xffffffffu, seg, below ? 31 - __clz(below) : 0);
-    const unsigned starts = __ballot_sync(0xffffffffu, seg >= 0 && (!below || prev != seg));
-    const bool together = __popc(starts) <= 2;             // all threads on each run, or a warp a run
-    auto head_of = [](int e) {
-        int d, head;
-        element<KT, NT>(e, d, head);
-        return head;
+    const int pieces = __popc(valid);
+    if (!pieces) return;
+    const int nth = lane < pieces ? __fns(valid, 0, lane + 1) : 0;
+    const float *mine = piece_far[nth] ? p.warp_parts + (int64_t(blockIdx.x) * W + (nth >> 1)) * PF
+                                       : reinterpret_cast<const float *>(smem + (nth >> 1) * STAGES * TILE);
+    seg = __shfl_sync(0xffffffffu, seg, nth);
+    if (w == 0 && lane < pieces) s_part[lane] = mine;
+    const int prev = __shfl_up_sync(0xffffffffu, seg, 1);
+    const unsigned starts = __ballot_sync(0xffffffffu, lane < pieces && (lane == 0 || prev != seg));
+    __syncthreads();
+    auto run_end = [&](int p0) {
+        const unsigned later = starts & ~((2u << p0) - 1u);
+        return later ? __ffs(later) - 1 : pieces;
     };
-    int cross[2] = {-1, -1}, ncross = 0, run = 0;
-    for (unsigned mask = starts; mask; mask &= mask - 1, ++run) {
+    // A run that lies inside the block's share is finished here; others (at most two, the first and the last) go to the
+    // workspace.
+    int cross[2] = {-1, -1}, ncross = 0;
+    unsigned outer = 0;                                    // runs (by their first piece) that go to the workspace
+    for (unsigned mask = starts; mask; mask &= mask - 1) {
         const int p0 = __ffs(mask) - 1;
-        const unsigned rest = mask & (mask - 1);
-        const unsigned members = valid & ~((1u << p0) - 1u) & (rest ? (1u << (__ffs(rest) - 1)) - 1u : 0xffffffffu);
-        const int s = __shfl_sync(0xffffffffu, seg, p0), b = s / HC, hc = s % HC;
-        const int64_t s0 = seg_start(p, cum, b, hc), s1 = s0 + cum[b + 1] - cum[b];
-        const bool inside = s0 >= start && s1 <= end;
-        if (inside && !together && run % W != w) continue;
-        const int idx = inside && !together ? lane : tid, stride = inside && !together ? 32 : W * 32;
-        const int n = __popc(members);
-        auto part = [&](int i) -> const float * {
-            const int at = __fns(members, 0, i + 1);
-            return piece_far[at] ? p.warp_parts + (int64_t(blockIdx.x) * W + (at >> 1)) * PF
-                                 : reinterpret_cast<const float *>(smem + (at >> 1) * STAGES * TILE);
-        };
-        if (inside) {
-            join<FR, NH>(n, part, head_of, [&](int e, int head, float o, float mm, float ll) {
-                int d, hd;
-                element<KT, NT>(e, d, hd);
-                put(b, hc, head, d, o * inverse(ll));
-                if (d == 0) put_lse(b, hc, head, lse_of(mm, ll));
-            }, idx, stride);
-        } else {
-            float *dst = p.block_parts + (int64_t(blockIdx.x) * 2 + (s0 < start ? 0 : 1)) * PF;
-            join<FR, NH>(n, part, head_of, [&](int e, int head, float o, float mm, float ll) {
-                int d, hd;
-                element<KT, NT>(e, d, hd);
-                dst[e] = o;
-                if (d == 0) {
-                    dst[FR + head] = mm;
-                    dst[FR + NH + head] = ll;
-                }
-            }, idx, stride);
+        if (p0 && run_end(p0) != pieces) continue;         // neither the first nor the last
+        const int s = __shfl_sync(0xffffffffu, seg, p0), b = s / pl.HC;
+        const unsigned s0 = seg_start(pl, cum, b, s - b * pl.HC);
+        if (s0 < start || s0 + cum[b + 1] - cum[b] > end) {
+            outer |= 1u << p0;
             cross[ncross++] = s;
         }
+    }
+    auto slot_of = [&](int s) {                            // this block's slot for a segment that leaves it
+        const int b = s / pl.HC;
+        return p.block_parts + (int64_t(blockIdx.x) * 2 + (seg_start(pl, cum, b, s - b * pl.HC) < start ? 0 : 1)) * PF;
+    };
+    auto put_lse = [&](int s, int head, float x) {
+        const int b = s / pl.HC, hc = s - b * pl.HC, h = hc / p.C, in = (hc - h * p.C) * NH + head;
+        if (a.lse && in < p.G) a.lse[int64_t(p.row0 + b) * a.q_heads + h * p.G + in] = x;
+    };
+    auto put4 = [&](int s, int head, int d, float4 o, float f) {
+        const int b = s / pl.HC, hc = s - b * pl.HC, h = hc / p.C, in = (hc - h * p.C) * NH + head;
+        const float x[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
+        if (in < p.G) store_out<4>(a.out, a.odt, int64_t(p.row0 + b) * a.ldo + int64_t(h * p.G + in) * D + d, x);
+    };
+    for (int i = tid; i < pieces * NH; i += THREADS) {
+        const int at = i / NH, head = i % NH;
+        const int p0 = 31 - __clz(starts & ((2u << at) - 1u)), p1 = run_end(p0);
+        float mm = -INFINITY, ll = 0.0f;
+        for (int k = p0; k < p1; ++k) mm = fmaxf(mm, s_part[k][NH * PS + head]);
+        const float base = finite_base(mm);
+        s_fac[at][head] = ex2(s_part[at][NH * PS + head] - base);
+        if (at != p0) continue;
+        for (int k = p0; k < p1; ++k)
+            ll = fmaf(s_part[k][NH * PS + NH + head], ex2(s_part[k][NH * PS + head] - base), ll);
+        s_inv[at][head] = inverse(ll);
+        const int s = piece_seg[__fns(valid, 0, at + 1)];
+        if ((outer >> p0) & 1) {
+            float *dst = slot_of(s);
+            dst[NH * PS + head] = mm;
+            dst[NH * PS + NH + head] = ll;
+        } else {
+            put_lse(s, head, lse_of(mm, ll));
+        }
+    }
+    __syncthreads();
+    constexpr int VEC = NH * D / 4;                        // four accumulators a thread
+    const int runs = __popc(starts);
+    for (int i = tid; i < (runs * VEC + 31) / 32 * 32; i += THREADS) {      // whole warps: VEC is a multiple of 32
+        const int p0 = __fns(starts, 0, i / VEC + 1), e = i % VEC, head = e / (D / 4), d = e % (D / 4) * 4;
+        const int s = __shfl_sync(0xffffffffu, seg, p0), n = run_end(p0) - p0;
+        const float4 o = join4<PS>(n, head, d, [&](int k) { return s_part[p0 + k]; }, [&](int k, int hd) { return s_fac[p0 + k][hd]; });
+        if ((outer >> p0) & 1) *reinterpret_cast<float4 *>(slot_of(s) + head * PS + d) = o;
+        else put4(s, head, d, o, s_inv[p0][head]);
     }
     if (!ncross) return;
     __threadfence();
     __syncthreads();
     if (tid < ncross) {
-        const int s = cross[tid];
+        const int s = tid ? cross[1] : cross[0];
         int first, count;
-        sharers(p, pl, cum, s / HC, s % HC, first, count);
+        sharers(pl, cum, s, first, count);
         const int before = atomicAdd(p.counters + s, 1);
         s_last[tid] = before == count - 1;
         if (before == count - 1) p.counters[s] = 0;        // ready for the next call
     }
     __syncthreads();
+    float *fac = reinterpret_cast<float *>(smem);          // [count][NH] factors, then 1 / sum: the rings are free
     for (int c = 0; c < ncross; ++c) {
         if (!s_last[c]) continue;
         __threadfence();
-        const int s = cross[c], b = s / HC, hc = s % HC;
+        const int s = c ? cross[1] : cross[0];
         int first, count;
-        sharers(p, pl, cum, b, hc, first, count);
-        const int64_t s0 = seg_start(p, cum, b, hc);
-        auto part = [&](int i) -> const float * {
-            return p.block_parts + (int64_t(first + i) * 2 + (s0 < block_start(p, pl, cum, first + i) ? 0 : 1)) * PF;
-        };
-        join<FR, NH>(count, part, head_of, [&](int e, int head, float o, float mm, float ll) {
-            int d, hd;
-            element<KT, NT>(e, d, hd);
-            put(b, hc, head, d, o * inverse(ll));
-            if (d == 0) put_lse(b, hc, head, lse_of(mm, ll));
-        }, tid, W * 32);
+        sharers(pl, cum, s, first, count);
+        auto part = [&](int i) -> const float * { return p.block_parts + (int64_t(first + i) * 2 + (i == 0 ? 1 : 0)) * PF; };
+        if (tid < NH) {
+            float mm = -INFINITY, ll = 0.0f;
+#pragma unroll 8
+            for (int i = 0; i < count; ++i) mm = fmaxf(mm, part(i)[NH * PS + tid]);
+            const float base = finite_base(mm);
+#pragma unroll 8
+            for (int i = 0; i < count; ++i) {
+                const float f = ex2(part(i)[NH * PS + tid] - base);
+                fac[i * NH + tid] = f;
+                ll = fmaf(part(i)[NH * PS + NH + tid], f, ll);
+            }
+            fac[count * NH + tid] = inverse(ll);
+            put_lse(s, tid, lse_of(mm, ll));
+        }
+        __syncthreads();
+        for (int e = tid; e < VEC; e += THREADS) {
+            const int head = e / (D / 4), d = e % (D / 4) * 4;
+            put4(s, head, d, join4<PS>(count, head, d, part, [&](int k, int hd) { return fac[k * NH + hd]; }), fac[count * NH + head]);
+        }
+        __syncthreads();
     }
 }
 
@@ -815,8 +933,8 @@ template <int KT, int D, int NT> cudaError_t run(const AttendArgs &a, cudaStream
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    constexpr int smem = F::W * F::STAGES * F::TILE + (MAX_ROWS + 1) * 8;
-    static_assert(smem <= 227 * 1024 - 1024, "shared memory");
+    constexpr int smem = F::W * F::STAGES * F::TILE + (MAX_ROWS + 1) * 4;
+    static_assert(smem <= 227 * 1024 - 8192, "shared memory");
     if (!opted[dev]) {
         e = cudaFuncSetAttribute(attend_kernel<KT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
@@ -831,14 +949,19 @@ template <int KT, int D, int NT> cudaError_t run(const AttendArgs &a, cudaStream
     p.counters = static_cast<int *>(a.ws);
     p.block_parts = reinterpret_cast<float *>(p.counters + MAX_SEGS);
     p.warp_parts = p.block_parts + int64_t(grid) * 2 * F::PF;
-    const int rows = MAX_SEGS / HC < MAX_ROWS ? MAX_SEGS / HC : MAX_ROWS;
+    // Rows a launch: bounded by the kernel's tables, and tile numbers stay below 2^31 whatever the lengths are.
+    const int64_t most = (int64_t(a.t.max_pages) * a.pool.page_tokens + F::TOK - 1) / F::TOK + 1;
+    const int64_t fit = 0x7FFFFFFF / (most * HC);
+    if (fit < 1) return cudaErrorNotSupported;
+    int rows = MAX_SEGS / HC < MAX_ROWS ? MAX_SEGS / HC : MAX_ROWS;
+    if (fit < rows) rows = int(fit);
     for (int r = 0; r < a.B; r += rows) {
         p.row0 = r;
         p.B = a.B - r < rows ? a.B - r : rows;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(grid);
         cfg.blockDim = dim3(F::W * 32);
-        cfg.dynamicSmemBytes = F::W * F::STAGES * F::TILE + (p.B + 1) * 8;
+        cfg.dynamicSmemBytes = F::W * F::STAGES * F::TILE + (p.B + 1) * 4;
         cfg.stream = s;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
