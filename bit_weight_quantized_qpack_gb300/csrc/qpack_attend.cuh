@@ -166,31 +166,40 @@ __device__ __forceinline__ uint32_t dequant2(uint32_t w, uint32_t sel, uint32_t 
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// Four or two consecutive elements of a row of queries.
-template <int DT, int N> __device__ __forceinline__ void load_q(const void *p, int64_t i, float *x) {
-    if (DT == DT_F32) {
-        const float *q = static_cast<const float *>(p) + i;
-        if (N == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(q);
+// A thread's four elements of a 16-element chunk of queries, as loaded: i .. i + 3 (GAP 2) or i, i + 1 and GAP further.
+// fp32 takes four words, the 16-bit types the first two. Loading and converting are apart, so that the loads' latency
+// passes under the start of the cache's copies.
+template <int GAP> __device__ __forceinline__ void load_q(const void *p, int dt, int64_t i, uint32_t *x) {
+    if (dt == DT_F32) {
+        const uint32_t *q = static_cast<const uint32_t *>(p) + i;
+        if (GAP == 2) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(q);
             x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
         } else {
-            const float2 v = *reinterpret_cast<const float2 *>(q);
-            x[0] = v.x, x[1] = v.y;
+            const uint2 v = *reinterpret_cast<const uint2 *>(q), u = *reinterpret_cast<const uint2 *>(q + GAP);
+            x[0] = v.x, x[1] = v.y, x[2] = u.x, x[3] = u.y;
         }
     } else {
         const uint16_t *q = static_cast<const uint16_t *>(p) + i;
-        uint32_t v[2] = {0, 0};
-        if (N == 4) {
-            const uint2 u = *reinterpret_cast<const uint2 *>(q);
-            v[0] = u.x, v[1] = u.y;
+        if (GAP == 2) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(q);
+            x[0] = v.x, x[1] = v.y;
         } else {
-            v[0] = *reinterpret_cast<const uint32_t *>(q);
+            x[0] = *reinterpret_cast<const uint32_t *>(q);
+            x[1] = *reinterpret_cast<const uint32_t *>(q + GAP);
         }
+    }
+}
+__device__ __forceinline__ void convert_q(int dt, uint32_t *w, float *x) {
+    if (dt == DT_F32) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const uint32_t h = e & 1 ? v[e / 2] >> 16 : v[e / 2] & 0xFFFFu;
-            x[e] = DT == DT_F16 ? h2f_bits(uint16_t(h)) : __uint_as_float(h << 16);
-        }
+        for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(w[e]);
+    } else if (dt == DT_F16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = h2f_bits(uint16_t(e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
     }
 }
 
@@ -312,18 +321,24 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -INFINITY : (m - P_BIAS) * 0.6931471805599453f + logf(l);
 }
 
-// Four accumulators (head, d .. d + 3) of n joined partials, with the partials' factors 2^(m_i - m) (factor(i, head)).
-template <int PS, class Part, class Factor>
-__device__ __forceinline__ float4 join4(int n, int head, int d, Part part, Factor factor) {
+// A triple of one head and four of its accumulators, joined one by one.
+struct Triple {
+    float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float4 x = *reinterpret_cast<const float4 *>(part(i) + head * PS + d);
-        const float f = factor(i, head);
-        o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y), o.z = fmaf(x.z, f, o.z), o.w = fmaf(x.w, f, o.w);
+    __device__ __forceinline__ void add(float mi, float li, float4 x) {
+        const float top = fmaxf(m, mi), base = finite_base(top), f = ex2(m - base), h = ex2(mi - base);
+        m = top;
+        l = fmaf(li, h, l * f);
+        o.x = fmaf(x.x, h, o.x * f), o.y = fmaf(x.y, h, o.y * f), o.z = fmaf(x.z, h, o.z * f), o.w = fmaf(x.w, h, o.w * f);
     }
-    return o;
-}
+};
+
+// A piece of a segment that a warp leaves to the join: where its results go. The piece itself is in the warp's ring, or
+// (far) in the workspace where the warp went on to another segment.
+struct Piece {
+    int64_t out, lse;           // element of the first head's results
+    int seg, heads, far;        // segment; heads there are; seg < 0: no piece
+};
 
 template <int KT, int D, int NT>
 __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const __grid_constant__ Params p) {
@@ -333,10 +348,10 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     constexpr bool I8 = KT == QPACK_KV_I8;
     extern __shared__ __align__(128) unsigned char smem[];
     unsigned *cum = reinterpret_cast<unsigned *>(smem + W * STAGES * TILE);  // tiles before row b, a segment's worth
-    __shared__ int piece_seg[2 * W], piece_far[2 * W], s_last[2];
+    __shared__ Piece s_piece[2 * W];
+    __shared__ float s_m[2 * W][NH], s_l[2 * W][NH];       // a piece's maxima and sums
+    __shared__ int s_run[2 * W], s_last[2];
     __shared__ unsigned s_max;
-    __shared__ const float *s_part[2 * W];
-    __shared__ float s_fac[2 * W][NH], s_inv[2 * W][NH];   // by piece: its factor, and (first of a run) the run's 1 / sum
     const AttendArgs &a = p.a;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
     const int T = a.pool.page_tokens, shift = 31 - __clz(T);
@@ -347,7 +362,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     // -- the rows' tiles, and this block's share of them ------------------------------------------------------
     for (int b = tid; b < p.B; b += THREADS)
         cum[b + 1] = row_of<TOK>(p, b, blockIdx.x == 0 ? &g_fault_attend : nullptr).tiles;
-    if (tid < 2 * W) piece_seg[tid] = -1;
+    if (tid < 2 * W) s_piece[tid].seg = -1;
     __syncthreads();
     if (w == 0) {
         unsigned carry = 0, most = 0;
@@ -485,11 +500,11 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
             }
             cp_commit();
         };
-#pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s) advance(s);
 
         // ldmatrix: lane addresses row lr of 16 tokens, chunk (even) + lane / 16
         const int lr = (lane & 7) + (lane & 8), lx = ((lane >> 4) ^ (SWZ ? lr & 7 : (lr >> 1) & 3)) << 4;
+        constexpr int gap = I8 ? 2 : 8;                    // a thread's elements of a chunk: d0, + 1, + gap, + gap + 1
+        const int d0 = I8 ? 4 * j : 2 * j;
         int slot = 0;
         for (int done = 0; done < nt;) {
             // -- a segment begins: its queries, rotated, scaled and split ---------------------------------------
@@ -498,6 +513,21 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
             uint32_t qf[CH][4 * NT];
             float qs[NT], m[NT], l[NT], acc[CH][NT][4];
             {
+                uint32_t raw[NT][CH][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int head = cc.q * NH + 8 * n + g;
+                    const int64_t at = int64_t(p.row0 + cc.b) * a.ldq + int64_t(cc.h * p.G + head) * D + d0;
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) {
+                        raw[n][c][0] = raw[n][c][1] = raw[n][c][2] = raw[n][c][3] = 0u;
+                        if (head < p.G) load_q<gap>(a.q, a.qdt, at + 16 * c, raw[n][c]);
+                    }
+                }
+                if (done == 0) {
+#pragma unroll
+                    for (int st = 0; st < STAGES - 1; ++st) advance(st);
+                }
                 const int64_t pos = int64_t(cc.row.len) - 1;
                 const bool turn = a.rope && pos < a.rope_rows;
                 if (a.rope && !turn) atomicOr(&g_fault_attend, FAULT_PAGE);
@@ -505,34 +535,9 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                 for (int n = 0; n < NT; ++n) {
                     m[n] = -INFINITY;
                     l[n] = 0.0f;
-                    const int head = cc.q * NH + 8 * n + g;
-                    const int64_t at = int64_t(p.row0 + cc.b) * a.ldq + int64_t(cc.h * p.G + head) * D;
-                    // a thread's four elements of chunk c: 16 c + 4 j .. + 3, or 16 c + 2 j, + 1 and 8 further
-                    constexpr int gap = I8 ? 2 : 8;
-                    const int d0 = I8 ? 4 * j : 2 * j;
                     float x[CH][4];
-                    auto fetch = [&](auto tag) {
-                        constexpr int DT = decltype(tag)::value;
 #pragma unroll
-                        for (int c = 0; c < CH; ++c) {
-                            if (I8) {
-                                load_q<DT, 4>(a.q, at + 16 * c + d0, x[c]);
-                            } else {
-                                load_q<DT, 2>(a.q, at + 16 * c + d0, x[c]);
-                                load_q<DT, 2>(a.q, at + 16 * c + d0 + gap, x[c] + 2);
-                            }
-                        }
-                    };
-                    if (head >= p.G) {
-#pragma unroll
-                        for (int c = 0; c < CH; ++c) x[c][0] = x[c][1] = x[c][2] = x[c][3] = 0.0f;
-                    } else if (a.qdt == DT_F32) {
-                        fetch(Int<DT_F32>());
-                    } else if (a.qdt == DT_F16) {
-                        fetch(Int<DT_F16>());
-                    } else {
-                        fetch(Int<DT_BF16>());
-                    }
+                    for (int c = 0; c < CH; ++c) convert_q(a.qdt, raw[n][c], x[c]);
                     if (turn) {
                         const float *row = a.rope + pos * D + d0;
 #pragma unroll
@@ -773,6 +778,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                     cp_wait<0>();
                     __syncwarp();
                 }
+                const int at = 2 * w + (done == 0 ? 0 : 1);
                 float *dst = last ? reinterpret_cast<float *>(ring) : p.warp_parts + (int64_t(blockIdx.x) * W + w) * PF;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -781,15 +787,12 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             dst[(8 * n + 2 * j + (r & 1)) * PS + 16 * c + gd * g + rd * (r >> 1)] = acc[c][n][r];
-                    if (j == 0) {
-                        dst[NH * PS + 8 * n + g] = m[n];
-                        dst[NH * PS + NH + 8 * n + g] = l[n];
-                    }
+                    if (j == 0) s_m[at][8 * n + g] = m[n], s_l[at][8 * n + g] = l[n];
                 }
                 if (lane == 0) {
-                    const int at = 2 * w + (done == 0 ? 0 : 1);
-                    piece_seg[at] = cc.b * pl.HC + cc.hc;
-                    piece_far[at] = last ? 0 : 1;
+                    const int head = cc.h * p.G + cc.q * NH;
+                    s_piece[at] = {int64_t(p.row0 + cc.b) * a.ldo + int64_t(head) * D, int64_t(p.row0 + cc.b) * a.q_heads + head,
+                                   cc.b * pl.HC + cc.hc, min(NH, p.G - cc.q * NH), last ? 0 : 1};
                 }
             }
             done += count;
@@ -800,121 +803,87 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     __syncthreads();
 
     // -- joins ------------------------------------------------------------------------------------------------
-    // Pieces in the order of their tiles, runs of one segment among them; every warp finds the runs for itself, a piece
-    // a lane.
-    int seg = lane < 2 * W ? piece_seg[lane] : -1;
-    const unsigned valid = __ballot_sync(0xffffffffu, seg >= 0);
-    const int pieces = __popc(valid);
-    if (!pieces) return;
-    const int nth = lane < pieces ? __fns(valid, 0, lane + 1) : 0;
-    const float *mine = piece_far[nth] ? p.warp_parts + (int64_t(blockIdx.x) * W + (nth >> 1)) * PF
-                                       : reinterpret_cast<const float *>(smem + (nth >> 1) * STAGES * TILE);
-    seg = __shfl_sync(0xffffffffu, seg, nth);
-    if (w == 0 && lane < pieces) s_part[lane] = mine;
-    const int prev = __shfl_up_sync(0xffffffffu, seg, 1);
-    const unsigned starts = __ballot_sync(0xffffffffu, lane < pieces && (lane == 0 || prev != seg));
-    __syncthreads();
-    auto run_end = [&](int p0) {
-        const unsigned later = starts & ~((2u << p0) - 1u);
-        return later ? __ffs(later) - 1 : pieces;
-    };
-    // A run that lies inside the block's share is finished here; others (at most two, the first and the last) go to the
-    // workspace.
-    int cross[2] = {-1, -1}, ncross = 0;
-    unsigned outer = 0;                                    // runs (by their first piece) that go to the workspace
-    for (unsigned mask = starts; mask; mask &= mask - 1) {
-        const int p0 = __ffs(mask) - 1;
-        if (p0 && run_end(p0) != pieces) continue;         // neither the first nor the last
-        const int s = __shfl_sync(0xffffffffu, seg, p0), b = s / pl.HC;
-        const unsigned s0 = seg_start(pl, cum, b, s - b * pl.HC);
-        if (s0 < start || s0 + cum[b + 1] - cum[b] > end) {
-            outer |= 1u << p0;
-            cross[ncross++] = s;
-        }
+    // Pieces in the order of their tiles, one a lane, runs of one segment among them; every warp finds the runs for
+    // itself. A run that leaves the block's share (at most two do, the first and the last) goes to the workspace, the
+    // others are finished. Of a run's pieces only the last can be far.
+    const int seg = lane < 2 * W ? s_piece[lane].seg : -1;
+    const unsigned valid = __ballot_sync(0xffffffffu, seg >= 0), below = valid & ((1u << lane) - 1u);
+    if (!valid) return;
+    const int prev = __shfl_sync(0xffffffffu, seg, below ? 31 - __clz(below) : 0);
+    const bool begins = seg >= 0 && (!below || prev != seg);
+    const unsigned starts = __ballot_sync(0xffffffffu, begins);
+    const unsigned far = __ballot_sync(0xffffffffu, seg >= 0 && s_piece[lane < 2 * W ? lane : 0].far);
+    bool before_me = false, outside = false;               // the segment begins before this block's share; leaves it
+    if (begins) {
+        const int b = seg / pl.HC;
+        const unsigned s0 = seg_start(pl, cum, b, seg - b * pl.HC);
+        before_me = s0 < start;
+        outside = before_me || s0 + cum[b + 1] - cum[b] > end;
     }
-    auto slot_of = [&](int s) {                            // this block's slot for a segment that leaves it
-        const int b = s / pl.HC;
-        return p.block_parts + (int64_t(blockIdx.x) * 2 + (seg_start(pl, cum, b, s - b * pl.HC) < start ? 0 : 1)) * PF;
-    };
-    auto put_lse = [&](int s, int head, float x) {
-        const int b = s / pl.HC, hc = s - b * pl.HC, h = hc / p.C, in = (hc - h * p.C) * NH + head;
-        if (a.lse && in < p.G) a.lse[int64_t(p.row0 + b) * a.q_heads + h * p.G + in] = x;
-    };
-    auto put4 = [&](int s, int head, int d, float4 o, float f) {
-        const int b = s / pl.HC, hc = s - b * pl.HC, h = hc / p.C, in = (hc - h * p.C) * NH + head;
-        const float x[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
-        if (in < p.G) store_out<4>(a.out, a.odt, int64_t(p.row0 + b) * a.ldo + int64_t(h * p.G + in) * D + d, x);
-    };
-    for (int i = tid; i < pieces * NH; i += THREADS) {
-        const int at = i / NH, head = i % NH;
-        const int p0 = 31 - __clz(starts & ((2u << at) - 1u)), p1 = run_end(p0);
-        float mm = -INFINITY, ll = 0.0f;
-        for (int k = p0; k < p1; ++k) mm = fmaxf(mm, s_part[k][NH * PS + head]);
-        const float base = finite_base(mm);
-        s_fac[at][head] = ex2(s_part[at][NH * PS + head] - base);
-        if (at != p0) continue;
-        for (int k = p0; k < p1; ++k)
-            ll = fmaf(s_part[k][NH * PS + NH + head], ex2(s_part[k][NH * PS + head] - base), ll);
-        s_inv[at][head] = inverse(ll);
-        const int s = piece_seg[__fns(valid, 0, at + 1)];
-        if ((outer >> p0) & 1) {
-            float *dst = slot_of(s);
-            dst[NH * PS + head] = mm;
-            dst[NH * PS + NH + head] = ll;
-        } else {
-            put_lse(s, head, lse_of(mm, ll));
-        }
-    }
+    const unsigned outer = __ballot_sync(0xffffffffu, outside), early = __ballot_sync(0xffffffffu, before_me);
+    if (w == 0 && begins) s_run[__popc(starts & ((1u << lane) - 1u))] = lane;
     __syncthreads();
     constexpr int VEC = NH * D / 4;                        // four accumulators a thread
-    const int runs = __popc(starts);
-    for (int i = tid; i < (runs * VEC + 31) / 32 * 32; i += THREADS) {      // whole warps: VEC is a multiple of 32
-        const int p0 = __fns(starts, 0, i / VEC + 1), e = i % VEC, head = e / (D / 4), d = e % (D / 4) * 4;
-        const int s = __shfl_sync(0xffffffffu, seg, p0), n = run_end(p0) - p0;
-        const float4 o = join4<PS>(n, head, d, [&](int k) { return s_part[p0 + k]; }, [&](int k, int hd) { return s_fac[p0 + k][hd]; });
-        if ((outer >> p0) & 1) *reinterpret_cast<float4 *>(slot_of(s) + head * PS + d) = o;
-        else put4(s, head, d, o, s_inv[p0][head]);
+    auto finish = [&](const Piece &pc, int head, int d, const Triple &t) {
+        if (head >= pc.heads) return;
+        const float f = inverse(t.l);
+        const float x[4] = {t.o.x * f, t.o.y * f, t.o.z * f, t.o.w * f};
+        store_out<4>(a.out, a.odt, pc.out + head * D + d, x);
+        if (a.lse && d == 0) a.lse[pc.lse + head] = lse_of(t.m, t.l);
+    };
+    for (int i = tid; i < __popc(starts) * VEC; i += THREADS) {
+        const int p0 = s_run[i / VEC], e = i % VEC, head = e / (D / 4), d = e % (D / 4) * 4;
+        const unsigned later = starts & ~((2u << p0) - 1u);
+        const unsigned members = valid & ~((1u << p0) - 1u) & (later ? (later & -later) - 1u : 0xffffffffu);
+        const int tail = 31 - __clz(members), away = (far >> tail) & 1, n = __popc(members) - away;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (away) o = *reinterpret_cast<const float4 *>(p.warp_parts + (int64_t(blockIdx.x) * W + (tail >> 1)) * PF + head * PS + d);
+        Triple t;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {                      // the run's first piece, then one of each of the next warps
+            const int at = k ? ((p0 >> 1) + k) * 2 : p0;
+            t.add(s_m[at][head], s_l[at][head],
+                  *reinterpret_cast<const float4 *>(smem + (at >> 1) * STAGES * TILE + (head * PS + d) * 4));
+        }
+        if (away) t.add(s_m[tail][head], s_l[tail][head], o);
+        if ((outer >> p0) & 1) {
+            float *dst = p.block_parts + (int64_t(blockIdx.x) * 2 + ((early >> p0) & 1 ? 0 : 1)) * PF;
+            *reinterpret_cast<float4 *>(dst + head * PS + d) = t.o;
+            if (d == 0) dst[NH * PS + head] = t.m, dst[NH * PS + NH + head] = t.l;
+        } else {
+            finish(s_piece[p0], head, d, t);
+        }
     }
+    const int ncross = __popc(outer);
     if (!ncross) return;
-    __threadfence();
     __syncthreads();
     if (tid < ncross) {
-        const int s = tid ? cross[1] : cross[0];
+        const int s = s_piece[tid ? 31 - __clz(outer) : __ffs(outer) - 1].seg;
         int first, count;
         sharers(pl, cum, s, first, count);
+        __threadfence();                                   // the block's partials, before its arrival
         const int before = atomicAdd(p.counters + s, 1);
-        s_last[tid] = before == count - 1;
         if (before == count - 1) p.counters[s] = 0;        // ready for the next call
+        __threadfence();                                   // the others' arrivals, before their partials are read
+        s_last[tid] = before == count - 1;
     }
     __syncthreads();
-    float *fac = reinterpret_cast<float *>(smem);          // [count][NH] factors, then 1 / sum: the rings are free
     for (int c = 0; c < ncross; ++c) {
         if (!s_last[c]) continue;
-        __threadfence();
-        const int s = c ? cross[1] : cross[0];
+        const Piece &pc = s_piece[c ? 31 - __clz(outer) : __ffs(outer) - 1];
         int first, count;
-        sharers(pl, cum, s, first, count);
-        auto part = [&](int i) -> const float * { return p.block_parts + (int64_t(first + i) * 2 + (i == 0 ? 1 : 0)) * PF; };
-        if (tid < NH) {
-            float mm = -INFINITY, ll = 0.0f;
-#pragma unroll 8
-            for (int i = 0; i < count; ++i) mm = fmaxf(mm, part(i)[NH * PS + tid]);
-            const float base = finite_base(mm);
-#pragma unroll 8
-            for (int i = 0; i < count; ++i) {
-                const float f = ex2(part(i)[NH * PS + tid] - base);
-                fac[i * NH + tid] = f;
-                ll = fmaf(part(i)[NH * PS + NH + tid], f, ll);
-            }
-            fac[count * NH + tid] = inverse(ll);
-            put_lse(s, tid, lse_of(mm, ll));
-        }
-        __syncthreads();
+        sharers(pl, cum, pc.seg, first, count);
         for (int e = tid; e < VEC; e += THREADS) {
             const int head = e / (D / 4), d = e % (D / 4) * 4;
-            put4(s, head, d, join4<PS>(count, head, d, part, [&](int k, int hd) { return fac[k * NH + hd]; }), fac[count * NH + head]);
+            Triple t;
+#pragma unroll 8
+            for (int i = 0; i < count; ++i) {
+                const float *part = p.block_parts + (int64_t(first + i) * 2 + (i == 0 ? 1 : 0)) * PF;
+                t.add(__ldcg(part + NH * PS + head), __ldcg(part + NH * PS + NH + head),
+                      __ldcg(reinterpret_cast<const float4 *>(part + head * PS + d)));
+            }
+            finish(pc, head, d, t);
         }
-        __syncthreads();
     }
 }
 
