@@ -250,28 +250,33 @@ template <int TOK> __device__ __forceinline__ Row row_of(const Params &p, int b,
     return r;
 }
 
-// The share of block i of all tiles, numbered row by row and segment by segment: equal pieces of `size` tiles, or
-// (per > 0) pieces of `size` tiles of each segment, `per` blocks a segment. The host keeps all numbers below 2^31.
+// Shares are cut by work: a segment counts its tiles and SETUP more, the time that its queries and results take a warp
+// (shares by tiles alone left blocks with many short segments 1.6 times as long as the others). Positions ("units") run
+// row by row and segment by segment, a segment's SETUP units first. The share of block i: equal pieces of `size` units,
+// or (per > 0) pieces of `size` tiles of each segment, `per` blocks a segment. The host keeps all numbers below 2^31.
+constexpr unsigned SETUP = 1;
 struct Plan {
     unsigned total, size;
     int per, HC;                                           // HC: segments a row
 };
+// Units of a segment of row b (0: an empty row), and where the segment's begin.
+__device__ __forceinline__ unsigned seg_units(const unsigned *cum, int b) { return cum[b + 1] - cum[b]; }
 __device__ __forceinline__ unsigned seg_start(const Plan &pl, const unsigned *cum, int b, int hc) {
-    return cum[b] * pl.HC + hc * (cum[b + 1] - cum[b]);
+    return cum[b] * pl.HC + hc * seg_units(cum, b);
 }
 __device__ __forceinline__ unsigned block_edge(const Plan &pl, const unsigned *cum, int B, int i, int end) {
     if (!pl.per) return min(unsigned(i + end) * pl.size, pl.total);
     const int seg = i / pl.per;
     if (seg >= B * pl.HC) return pl.total;
-    const int b = seg / pl.HC;
-    const unsigned n = cum[b + 1] - cum[b];
-    return seg_start(pl, cum, b, seg - b * pl.HC) + min(unsigned(i - seg * pl.per + end) * pl.size, n);
+    const int b = seg / pl.HC, part = i - seg * pl.per + end;
+    const unsigned s0 = seg_start(pl, cum, b, seg - b * pl.HC);
+    return part ? min(s0 + SETUP + part * pl.size, s0 + seg_units(cum, b)) : s0;
 }
 // The blocks that share a segment: the first holds it in its second slot of the workspace, the others, which begin inside
 // it, in their first.
 __device__ __forceinline__ void sharers(const Plan &pl, const unsigned *cum, int seg, int &first, int &count) {
     const int b = seg / pl.HC;
-    const unsigned s0 = seg_start(pl, cum, b, seg - b * pl.HC), n = cum[b + 1] - cum[b];
+    const unsigned s0 = seg_start(pl, cum, b, seg - b * pl.HC) + SETUP, n = seg_units(cum, b) - SETUP;    // its tiles
     if (pl.per) {
         first = seg * pl.per;
         count = int((n + pl.size - 1) / pl.size);
@@ -287,17 +292,19 @@ struct Cursor {
     unsigned ti;
     Row row;
 };
-template <int TOK> __device__ __forceinline__ void seek(const Params &p, const Plan &pl, const unsigned *cum, unsigned tile, Cursor &c) {
-    int lo = 0, hi = p.B;                                  // cum[lo] HC <= tile < cum[hi] HC
+// The first tile at or behind a unit that is not behind the last one.
+template <int TOK> __device__ __forceinline__ void seek(const Params &p, const Plan &pl, const unsigned *cum, unsigned unit, Cursor &c) {
+    int lo = 0, hi = p.B;                                  // cum[lo] HC <= unit < cum[hi] HC
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (cum[mid] * pl.HC <= tile) lo = mid; else hi = mid;
+        if (cum[mid] * pl.HC <= unit) lo = mid; else hi = mid;
     }
     c.b = lo;
     c.row = row_of<TOK>(p, lo, nullptr);
-    const unsigned rem = tile - cum[lo] * pl.HC;
-    c.hc = int(rem / c.row.tiles);
-    c.ti = rem - c.hc * c.row.tiles;
+    const unsigned rem = unit - cum[lo] * pl.HC, n = c.row.tiles + SETUP;
+    c.hc = int(rem / n);
+    const unsigned at = rem - c.hc * n;
+    c.ti = at > SETUP ? at - SETUP : 0;
     c.h = c.hc / p.C;
     c.q = c.hc - c.h * p.C;
 }
@@ -347,7 +354,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     constexpr int TOK = F::TOK, CPR = RB / 16, CH = D / 16, NH = F::NH, TT = TOK / 8, THREADS = W * 32;
     constexpr bool I8 = KT == QPACK_KV_I8;
     extern __shared__ __align__(128) unsigned char smem[];
-    unsigned *cum = reinterpret_cast<unsigned *>(smem + W * STAGES * TILE);  // tiles before row b, a segment's worth
+    unsigned *cum = reinterpret_cast<unsigned *>(smem + W * STAGES * TILE);  // units before row b, a segment's worth
     __shared__ Piece s_piece[2 * W];
     __shared__ float s_m[2 * W][NH], s_l[2 * W][NH];       // a piece's maxima and sums
     __shared__ int s_run[2 * W], s_last[2];
@@ -360,8 +367,10 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     pdl_wait();                                            // inputs, cache and workspace may be the previous grid's
 
     // -- the rows' tiles, and this block's share of them ------------------------------------------------------
-    for (int b = tid; b < p.B; b += THREADS)
-        cum[b + 1] = row_of<TOK>(p, b, blockIdx.x == 0 ? &g_fault_attend : nullptr).tiles;
+    for (int b = tid; b < p.B; b += THREADS) {
+        const unsigned tiles = row_of<TOK>(p, b, blockIdx.x == 0 ? &g_fault_attend : nullptr).tiles;
+        cum[b + 1] = tiles ? tiles + SETUP : 0;
+    }
     if (tid < 2 * W) s_piece[tid].seg = -1;
     __syncthreads();
     if (w == 0) {
@@ -387,15 +396,15 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     const unsigned grid = gridDim.x;
     pl.HC = a.pool.heads * p.C;
     pl.total = cum[p.B] * pl.HC;
-    pl.size = max((pl.total + grid - 1) / grid, unsigned(W));           // at least a tile a warp
+    pl.size = max((pl.total + grid - 1) / grid, unsigned(W));           // at least a unit a warp
     pl.per = 0;
-    const unsigned nseg = p.B * pl.HC;
+    const unsigned nseg = p.B * pl.HC, longest = s_max ? s_max - SETUP : 0;
     if (nseg <= grid) {
         // Few segments: boundaries on theirs save the joins of the pieces, where the shares stay nearly equal.
-        const unsigned k = grid / nseg, size = max((s_max + k - 1) / k, unsigned(W));
+        const unsigned k = grid / nseg, size = max((longest + k - 1) / k, unsigned(W));
         if (size <= pl.size + pl.size / 8) {
             pl.size = size;
-            pl.per = max(int((s_max + size - 1) / size), 1);
+            pl.per = max(int((longest + size - 1) / size), 1);
         }
     }
     for (int b = blockIdx.x; b < p.B; b += grid) {
@@ -410,13 +419,28 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
 
     // -- this warp's share -------------------------------------------------------------------------------------
     unsigned char *ring = smem + w * STAGES * TILE;
-    const int share = int((end - start + W - 1) / W), w0 = int(start) + w * share;
-    const int nt = min(int(end) - w0, share);
+    const unsigned share = (end - start + W - 1) / W, w0 = min(start + w * share, end), w1 = min(w0 + share, end);
+    Cursor ci;
+    int nt = 0;                                            // its tiles
+    if (w0 < w1) {
+        seek<TOK>(p, pl, cum, w0, ci);
+        // segments whose tiles the units [w0, w1) reach, from the first one's row on
+        unsigned u = seg_start(pl, cum, ci.b, ci.hc) + SETUP;
+        int b = ci.b, hc = ci.hc;
+        for (;;) {
+            const unsigned n = seg_units(cum, b) - SETUP, from = max(u, w0), to = min(u + n, w1);
+            if (to > from) nt += to - from;
+            if (u + n >= w1) break;
+            u += n + SETUP;                                // the next segment's tiles; there is one, since w1 is behind it
+            if (++hc == pl.HC) {
+                hc = 0;
+                do ++b; while (seg_units(cum, b) == 0);
+            }
+        }
+    }
     if (nt > 0) {
         const uint32_t ring32 = smem_u32(ring);
-        Cursor ci, cc;
-        seek<TOK>(p, pl, cum, unsigned(w0), ci);
-        cc = ci;
+        Cursor cc = ci;
 
         // The page of the tile, or of lane's token of it where pages are smaller than a tile; loaded a tile ahead of its
         // use.
@@ -817,8 +841,8 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     if (begins) {
         const int b = seg / pl.HC;
         const unsigned s0 = seg_start(pl, cum, b, seg - b * pl.HC);
-        before_me = s0 < start;
-        outside = before_me || s0 + cum[b + 1] - cum[b] > end;
+        before_me = s0 + SETUP < start;
+        outside = before_me || s0 + seg_units(cum, b) > end;
     }
     const unsigned outer = __ballot_sync(0xffffffffu, outside), early = __ballot_sync(0xffffffffu, before_me);
     if (w == 0 && begins) s_run[__popc(starts & ((1u << lane) - 1u))] = lane;
@@ -839,11 +863,17 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (away) o = *reinterpret_cast<const float4 *>(p.warp_parts + (int64_t(blockIdx.x) * W + (tail >> 1)) * PF + head * PS + d);
         Triple t;
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {                      // the run's first piece, then one of each of the next warps
-            const int at = k ? ((p0 >> 1) + k) * 2 : p0;
-            t.add(s_m[at][head], s_l[at][head],
-                  *reinterpret_cast<const float4 *>(smem + (at >> 1) * STAGES * TILE + (head * PS + d) * 4));
+        for (int k0 = 0; k0 < n; k0 += 4) {                // the run's first piece, then one of each of the next warps
+            float4 x[4];
+            int at[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                at[k] = k0 + k ? ((p0 >> 1) + min(k0 + k, n - 1)) * 2 : p0;
+                x[k] = *reinterpret_cast<const float4 *>(smem + (at[k] >> 1) * STAGES * TILE + (head * PS + d) * 4);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k0 + k < n) t.add(s_m[at[k]][head], s_l[at[k]][head], x[k]);
         }
         if (away) t.add(s_m[tail][head], s_l[tail][head], o);
         if ((outer >> p0) & 1) {
@@ -861,10 +891,10 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
         const int s = s_piece[tid ? 31 - __clz(outer) : __ffs(outer) - 1].seg;
         int first, count;
         sharers(pl, cum, s, first, count);
-        __threadfence();                                   // the block's partials, before its arrival
-        const int before = atomicAdd(p.counters + s, 1);
+        // releases the block's partials, and acquires those of the blocks that arrived before
+        int before;
+        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.counters + s) : "memory");
         if (before == count - 1) p.counters[s] = 0;        // ready for the next call
-        __threadfence();                                   // the others' arrivals, before their partials are read
         s_last[tid] = before == count - 1;
     }
     __syncthreads();
@@ -876,11 +906,21 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
         for (int e = tid; e < VEC; e += THREADS) {
             const int head = e / (D / 4), d = e % (D / 4) * 4;
             Triple t;
-#pragma unroll 8
-            for (int i = 0; i < count; ++i) {
-                const float *part = p.block_parts + (int64_t(first + i) * 2 + (i == 0 ? 1 : 0)) * PF;
-                t.add(__ldcg(part + NH * PS + head), __ldcg(part + NH * PS + NH + head),
-                      __ldcg(reinterpret_cast<const float4 *>(part + head * PS + d)));
+            constexpr int LOADS = 10;                      // in flight together
+            for (int i0 = 0; i0 < count; i0 += LOADS) {
+                float mi[LOADS], li[LOADS];
+                float4 x[LOADS];
+#pragma unroll
+                for (int i = 0; i < LOADS; ++i) {
+                    if (i0 + i >= count) continue;
+                    const float *part = p.block_parts + (int64_t(first + i0 + i) * 2 + (i0 + i == 0 ? 1 : 0)) * PF;
+                    mi[i] = __ldcg(part + NH * PS + head);
+                    li[i] = __ldcg(part + NH * PS + NH + head);
+                    x[i] = __ldcg(reinterpret_cast<const float4 *>(part + head * PS + d));
+                }
+#pragma unroll
+                for (int i = 0; i < LOADS; ++i)
+                    if (i0 + i < count) t.add(mi[i], li[i], x[i]);
             }
             finish(pc, head, d, t);
         }
@@ -919,7 +959,7 @@ template <int KT, int D, int NT> cudaError_t run(const AttendArgs &a, cudaStream
     p.block_parts = reinterpret_cast<float *>(p.counters + MAX_SEGS);
     p.warp_parts = p.block_parts + int64_t(grid) * 2 * F::PF;
     // Rows a launch: bounded by the kernel's tables, and tile numbers stay below 2^31 whatever the lengths are.
-    const int64_t most = (int64_t(a.t.max_pages) * a.pool.page_tokens + F::TOK - 1) / F::TOK + 1;
+    const int64_t most = (int64_t(a.t.max_pages) * a.pool.page_tokens + F::TOK - 1) / F::TOK + 1 + SETUP;
     const int64_t fit = 0x7FFFFFFF / (most * HC);
     if (fit < 1) return cudaErrorNotSupported;
     int rows = MAX_SEGS / HC < MAX_ROWS ? MAX_SEGS / HC : MAX_ROWS;
