@@ -297,6 +297,22 @@ def qpack_kv_dequant(codes, scales, out=None, stream=None):
     return out
 
 
+# A decode step makes these calls for every layer, a few microseconds of kernel each, so their marshalling is kept
+# short: pointers and streams as plain integers.
+def _addr(t):
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise QpackError("qpack kernels take CUDA tensors")
+    return t.data_ptr()
+
+
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
 class KVPool:
     """A paged KV cache: keys and values [layers, pages, heads, page_tokens, dim], int8 codes with fp16 scales
     [layers, pages, heads, page_tokens, dim / 32], or fp16 / bf16 without scales. The layer and page strides are free (a
@@ -336,9 +352,9 @@ class KVPool:
 
         ls, ps = strides(k)
         sls, sps = strides(k_scales) if kind == KV_I8 else (0, 0)
-        self._c = _Pool(_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales), ls, ps, sls, sps, pages, layers, heads,
+        self._c = _Pool(_addr(k), _addr(v), _addr(k_scales), _addr(v_scales), ls, ps, sls, sps, pages, layers, heads,
                         page_tokens, dim, kind, 0)
-        self._ref = ctypes.byref(self._c)
+        self._ref = ctypes.addressof(self._c)
 
 
 def alloc_kv_pool(kind, layers, pages, heads, page_tokens, dim, device="cuda") -> KVPool:
@@ -365,9 +381,9 @@ class KVTables:
             _need(refs, torch.int32, "refs", numel=0)
         self.tables, self.lens, self.refs = tables, lens, refs
         stride = tables.stride(0) if tables.shape[0] > 1 else tables.shape[1]
-        self._c = _Tables(_ptr(tables), _ptr(lens), _ptr(refs), stride, 0 if refs is None else refs.numel(),
+        self._c = _Tables(_addr(tables), _addr(lens), _addr(refs), stride, 0 if refs is None else refs.numel(),
                           tables.shape[0], tables.shape[1])
-        self._ref = ctypes.byref(self._c)
+        self._ref = ctypes.addressof(self._c)
 
 
 def alloc_kv_tables(seqs, max_pages, pages, device="cuda") -> KVTables:
@@ -396,7 +412,7 @@ def _need_rows(t, what, heads, dim):
 
 
 def _need_i32(t, what, n):
-    if t is not None:
+    if t is not None and (t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous()):
         _need(t, torch.int32, what, numel=n)
 
 
@@ -422,36 +438,41 @@ def qpack_kv_append(pool, layer, tables, k, v, seqs=None, pos=None, rope=None, s
     _need_i32(seqs, "seqs", n)
     _need_i32(pos, "pos", n)
     rows = _need_rope(rope, pool.dim)
-    rc = lib().qpack_kv_append(pool._ref, layer, tables._ref, _ptr(seqs), _ptr(pos), n, _ptr(k), _ptr(v), dt, ldk, ldv,
-                               _ptr(rope), rows, _stream(stream))
-    _check(rc, "qpack_kv_append")
+    rc = (_lib or lib()).qpack_kv_append(pool._ref, layer, tables._ref, _addr(seqs), _addr(pos), n, _addr(k), _addr(v), dt, ldk, ldv,
+          _addr(rope), rows, _raw_stream(stream))
+    if rc:
+        _check(rc, "qpack_kv_append")
 
 
 def qpack_kv_read(pool, layer, tables, seqs=None, pos=None, k_out=None, v_out=None, n=None, stream=None):
     """Rows of the cache: token i from position pos[i] of sequence seqs[i] (as in qpack_kv_append). Returns (k, v),
     [n, heads, dim], float16 (bfloat16 for a bfloat16 pool) unless given."""
-    given = next((t for t in (seqs, pos, k_out, v_out) if t is not None), None)
     if n is None:
+        given = seqs if seqs is not None else pos if pos is not None else k_out if k_out is not None else v_out
         if given is None:
             raise QpackError("n: needed where neither seqs, pos nor an output is given")
         n = given.shape[0]
     if k_out is None and v_out is None:
         dt = torch.bfloat16 if pool.k.dtype == torch.bfloat16 else torch.float16
         k_out, v_out = (torch.empty((n, pool.heads, pool.dim), dtype=dt, device=pool.k.device) for _ in range(2))
-    ld = {}
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is not None:
-            ld[name] = _need_rows(t, name, pool.heads, pool.dim)
-            if t.shape[0] < n:
-                raise QpackError(f"{name}: expected at least {n} rows, got {t.shape[0]}")
-    if len({c for c, _ in ld.values()}) != 1:
-        raise QpackError("k_out, v_out: expected the same type")
+    dk = dv = None
+    ldk = ldv = 0
+    if k_out is not None:
+        dk, ldk = _need_rows(k_out, "k_out", pool.heads, pool.dim)
+        if k_out.shape[0] < n:
+            raise QpackError(f"k_out: expected at least {n} rows, got {k_out.shape[0]}")
+    if v_out is not None:
+        dv, ldv = _need_rows(v_out, "v_out", pool.heads, pool.dim)
+        if v_out.shape[0] < n:
+            raise QpackError(f"v_out: expected at least {n} rows, got {v_out.shape[0]}")
+        if dk is not None and dk != dv:
+            raise QpackError("k_out, v_out: expected the same type")
     _need_i32(seqs, "seqs", n)
     _need_i32(pos, "pos", n)
-    dt = next(iter(ld.values()))[0]
-    rc = lib().qpack_kv_read(pool._ref, layer, tables._ref, _ptr(seqs), _ptr(pos), n, _ptr(k_out), _ptr(v_out), dt,
-                             ld.get("k_out", (0, 0))[1], ld.get("v_out", (0, 0))[1], _stream(stream))
-    _check(rc, "qpack_kv_read")
+    rc = (_lib or lib()).qpack_kv_read(pool._ref, layer, tables._ref, _addr(seqs), _addr(pos), n, _addr(k_out), _addr(v_out),
+          dv if dk is None else dk, ldk, ldv, _raw_stream(stream))
+    if rc:
+        _check(rc, "qpack_kv_read")
     return k_out, v_out
 
 
@@ -461,21 +482,25 @@ class KVWorkspace:
 
     def __init__(self, bytes, device):
         self.buffer = torch.zeros(bytes, dtype=torch.uint8, device=device)
-        self._p = _ptr(self.buffer)
+        self._p = _addr(self.buffer)
         self.bytes = bytes
 
 
 def alloc_kv_workspace(pool, batch, q_heads) -> KVWorkspace:
     """For qpack_kv_attend with up to `batch` rows."""
     n = ctypes.c_int64(0)
-    _check(lib().qpack_kv_attend_workspace(pool._ref, batch, q_heads, ctypes.byref(n)), "qpack_kv_attend_workspace")
+    rc = (_lib or lib()).qpack_kv_attend_workspace(pool._ref, batch, q_heads, ctypes.byref(n))
+    if rc:
+        _check(rc, "qpack_kv_attend_workspace")
     return KVWorkspace(n.value, pool.k.device)
 
 
 def alloc_kv_page_workspace(pool, tables) -> KVWorkspace:
     """For qpack_kv_fork and qpack_kv_compact."""
     n = ctypes.c_int64(0)
-    _check(lib().qpack_kv_page_workspace(pool._ref, tables._ref, ctypes.byref(n)), "qpack_kv_page_workspace")
+    rc = (_lib or lib()).qpack_kv_page_workspace(pool._ref, tables._ref, ctypes.byref(n))
+    if rc:
+        _check(rc, "qpack_kv_page_workspace")
     return KVWorkspace(n.value, pool.k.device)
 
 
@@ -503,10 +528,11 @@ def qpack_kv_attend(pool, layer, tables, q, seqs=None, scale=None, window=0, rop
     if workspace is None:
         workspace = alloc_kv_workspace(pool, B, q_heads)
     rows = _need_rope(rope, D)
-    rc = lib().qpack_kv_attend(pool._ref, layer, tables._ref, _ptr(seqs), B, _ptr(q), qdt, ldq, q_heads,
-                               D ** -0.5 if scale is None else scale, window, _ptr(rope), rows, _ptr(out), odt, ldo,
-                               _ptr(lse), workspace._p, workspace.bytes, _stream(stream))
-    _check(rc, "qpack_kv_attend")
+    rc = (_lib or lib()).qpack_kv_attend(pool._ref, layer, tables._ref, _addr(seqs), B, _addr(q), qdt, ldq, q_heads,
+          D ** -0.5 if scale is None else scale, window, _addr(rope), rows, _addr(out), odt, ldo, _addr(lse), workspace._p,
+          workspace.bytes, _raw_stream(stream))
+    if rc:
+        _check(rc, "qpack_kv_attend")
     return out
 
 
@@ -522,7 +548,9 @@ def qpack_kv_reserve(pool, tables, seqs, add, stream=None):
     n = seqs.numel()
     _need_i32(seqs, "seqs", n)
     _need_i32(add, "add", n)
-    _check(lib().qpack_kv_reserve(pool._ref, tables._ref, _ptr(seqs), _ptr(add), n, _stream(stream)), "qpack_kv_reserve")
+    rc = (_lib or lib()).qpack_kv_reserve(pool._ref, tables._ref, _addr(seqs), _addr(add), n, _raw_stream(stream))
+    if rc:
+        _check(rc, "qpack_kv_reserve")
 
 
 def qpack_kv_fork(pool, tables, src, dst, workspace=None, stream=None):
@@ -532,8 +560,10 @@ def qpack_kv_fork(pool, tables, src, dst, workspace=None, stream=None):
     _need_i32(src, "src", n)
     _need_i32(dst, "dst", n)
     workspace = alloc_kv_page_workspace(pool, tables) if workspace is None else workspace
-    _check(lib().qpack_kv_fork(pool._ref, tables._ref, _ptr(src), _ptr(dst), n, workspace._p, workspace.bytes,
-                               _stream(stream)), "qpack_kv_fork")
+    rc = (_lib or lib()).qpack_kv_fork(pool._ref, tables._ref, _addr(src), _addr(dst), n, workspace._p, workspace.bytes,
+          _raw_stream(stream))
+    if rc:
+        _check(rc, "qpack_kv_fork")
 
 
 def qpack_kv_free(tables, seqs, stream=None):
@@ -541,7 +571,9 @@ def qpack_kv_free(tables, seqs, stream=None):
     _need_refs(tables)
     n = seqs.numel()
     _need_i32(seqs, "seqs", n)
-    _check(lib().qpack_kv_free(tables._ref, _ptr(seqs), n, _stream(stream)), "qpack_kv_free")
+    rc = (_lib or lib()).qpack_kv_free(tables._ref, _addr(seqs), n, _raw_stream(stream))
+    if rc:
+        _check(rc, "qpack_kv_free")
 
 
 def qpack_kv_compact(pool, tables, tables_out=None, refs_out=None, moved=None, workspace=None, stream=None):
@@ -556,8 +588,10 @@ def qpack_kv_compact(pool, tables, tables_out=None, refs_out=None, moved=None, w
     _need(refs_out, torch.int32, "refs_out", numel=tables.refs.numel())
     _need_i32(moved, "moved", 1)
     workspace = alloc_kv_page_workspace(pool, tables) if workspace is None else workspace
-    _check(lib().qpack_kv_compact(pool._ref, tables._ref, _ptr(tables_out), _ptr(refs_out), _ptr(moved), workspace._p,
-                                  workspace.bytes, _stream(stream)), "qpack_kv_compact")
+    rc = (_lib or lib()).qpack_kv_compact(pool._ref, tables._ref, _addr(tables_out), _addr(refs_out), _addr(moved), workspace._p,
+          workspace.bytes, _raw_stream(stream))
+    if rc:
+        _check(rc, "qpack_kv_compact")
     return tables_out, refs_out
 
 
@@ -566,7 +600,9 @@ def qpack_kv_copy_pages(pool, src, dst, stream=None):
     n = src.numel()
     _need_i32(src, "src", n)
     _need_i32(dst, "dst", n)
-    _check(lib().qpack_kv_copy_pages(pool._ref, _ptr(src), _ptr(dst), n, _stream(stream)), "qpack_kv_copy_pages")
+    rc = (_lib or lib()).qpack_kv_copy_pages(pool._ref, _addr(src), _addr(dst), n, _raw_stream(stream))
+    if rc:
+        _check(rc, "qpack_kv_copy_pages")
 
 
 def qpack_fetch_fault_flags() -> int:
