@@ -157,15 +157,6 @@ template <int KT> __device__ __forceinline__ void split2(float x, float y, uint3
     }
 }
 
-// Bytes of w (codes + 128) chosen by `sel` as fp16 codes times their scales: (1024 + u) - 1152 is exact, one rounding.
-__device__ __forceinline__ uint32_t dequant2(uint32_t w, uint32_t sel, uint32_t scale) {
-    const uint32_t u = __byte_perm(w, 0x64646464u, sel);
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));
-    const __half2 c = __hsub2(*reinterpret_cast<const __half2 *>(&u), off);
-    const __half2 v = __hmul2(c, *reinterpret_cast<const __half2 *>(&scale));
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-
 // A thread's four elements of a 16-element chunk of queries, as loaded: i .. i + 3 (GAP 2) or i, i + 1 and GAP further.
 // fp32 takes four words, the 16-bit types the first two. Loading and converting are apart, so that the loads' latency
 // passes under the start of the cache's copies.

@@ -20,117 +20,6 @@ __device__ int g_fault_paged = 0;
 // ------------------------------------------------------------------------------------------------------------
 // Append and read back
 // ------------------------------------------------------------------------------------------------------------
-constexpr int ROW_THREADS = 256;
-
-template <int DT> struct Elem { using type = uint16_t; };
-template <> struct Elem<DT_F32> { using type = float; };
-
-// Where token i of the call lives: its sequence and position, and the element offset of its page's first head.
-struct Place {
-    int64_t page;      // -1: nowhere (a skipped token, or one out of range)
-    int pos, slot;
-};
-
-__device__ __forceinline__ Place place_of(const AppendArgs &a, int64_t i) {
-    Place p = {-1, -1, 0};
-    const int64_t seq = a.seqs ? int64_t(__ldg(a.seqs + i)) : i;
-    if (seq < 0 || seq >= a.t.seqs) {
-        atomicOr(&g_fault_paged, FAULT_PAGE);
-        return p;
-    }
-    p.pos = a.pos ? __ldg(a.pos + i) : __ldg(a.t.lens + seq) - 1;
-    if (p.pos < 0) return p;
-    const int shift = 31 - __clz(a.pool.page_tokens);
-    const int col = p.pos >> shift;
-    p.slot = p.pos & (a.pool.page_tokens - 1);
-    const int page = col < a.t.max_pages ? __ldg(a.t.tables + seq * a.t.stride + col) : -1;
-    if (page < 0 || page >= a.pool.pages) {
-        atomicOr(&g_fault_paged, FAULT_PAGE);
-        return p;
-    }
-    p.page = page;
-    return p;
-}
-
-// Eight consecutive elements a lane, so a row of D takes D / 8 lanes: 32 / (D / 8) rows a warp. The rotation's partner
-// (i +- D/2) is D/16 lanes away, and the four lanes of a 32-element group reduce its maximum with two shuffles.
-template <int KT, int D, int DT>
-__global__ void __launch_bounds__(ROW_THREADS) kv_append_kernel(AppendArgs a, int64_t rows) {
-    constexpr int LPR = D / 8, RPW = 32 / LPR;
-    const int lane = threadIdx.x & 31, sub = lane % LPR;
-    const int64_t warps = int64_t(gridDim.x) * (ROW_THREADS / 32);
-    const int H = a.pool.heads;
-    for (int64_t r0 = (int64_t(blockIdx.x) * (ROW_THREADS / 32) + (threadIdx.x >> 5)) * RPW; r0 < rows; r0 += warps * RPW) {
-        const int64_t r = r0 + lane / LPR;
-        const bool live = r < rows;
-        const int64_t tok = live ? r / (2 * H) : 0;
-        const int kh = live ? int(r - tok * 2 * H) : 0;
-        const bool is_v = kh >= H;
-        const int head = is_v ? kh - H : kh;
-        Place pl = {-1, -1, 0};
-        if (live) pl = place_of(a, tok);
-        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (pl.page >= 0) load8<DT>(is_v ? a.v : a.k, tok * (is_v ? a.ldv : a.ldk) + int64_t(head) * D + sub * 8, x);
-        if (a.rope) {                                      // uniform: the shuffles are the warp's
-            const bool turn = pl.page >= 0 && !is_v;
-            const bool in = turn && pl.pos < a.rope_rows;
-            if (turn && !in) atomicOr(&g_fault_paged, FAULT_PAGE);
-            const bool lower = sub < LPR / 2;
-            float c[8] = {1, 1, 1, 1, 1, 1, 1, 1}, s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (in) {
-                const int64_t row = int64_t(pl.pos) * D + (sub % (LPR / 2)) * 8;
-                load8<DT_F32>(a.rope, row, c);
-                load8<DT_F32>(a.rope, row + D / 2, s);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float y = __shfl_xor_sync(0xffffffffu, x[e], LPR / 2);
-                // lower half: x c - y s; upper half: x c + y s; each operation rounded
-                const float ys = __fmul_rn(y, s[e]);
-                if (in) x[e] = lower ? __fsub_rn(__fmul_rn(x[e], c[e]), ys) : __fadd_rn(__fmul_rn(x[e], c[e]), ys);
-            }
-        }
-        const int64_t in_page = (int64_t(head) * a.pool.page_tokens + pl.slot) * D + sub * 8;
-        if (KT == QPACK_KV_I8) {
-            float m = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            const uint16_t d16 = f2h_bits(fminf(__fdiv_rn(m, 127.0f), 65504.0f));
-            const float d = h2f_bits(d16);
-            uint8_t cb[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (d > 0.0f) rint_codes<8>(x, d, __frcp_rn(d), 0, -127, 127, 0, cb);
-            uint32_t w[2] = {0u, 0u};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e >> 2] |= uint32_t(cb[e]) << (8 * (e & 3));
-            if (pl.page >= 0) {
-                int8_t *base = static_cast<int8_t *>(is_v ? a.pool.v : a.pool.k);
-                const int64_t at = a.layer * a.pool.layer_stride + pl.page * a.pool.page_stride + in_page;
-                *reinterpret_cast<uint2 *>(base + at) = make_uint2(w[0], w[1]);
-                if ((sub & 3) == 0) {
-                    uint16_t *sc = is_v ? a.pool.v_scales : a.pool.k_scales;
-                    sc[a.layer * a.pool.scale_layer_stride + pl.page * a.pool.scale_page_stride + in_page / 32] = d16;
-                }
-            }
-        } else if (pl.page >= 0) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (KT == QPACK_KV_F16) {
-                    w[e] = uint32_t(f2h_bits(x[2 * e])) | (uint32_t(f2h_bits(x[2 * e + 1])) << 16);
-                } else {
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
-                    w[e] = *reinterpret_cast<const uint32_t *>(&b);
-                }
-            }
-            uint16_t *base = static_cast<uint16_t *>(is_v ? a.pool.v : a.pool.k);
-            const int64_t at = a.layer * a.pool.layer_stride + pl.page * a.pool.page_stride + in_page;
-            *reinterpret_cast<uint4 *>(base + at) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-    }
-}
-
 template <int DT> __device__ __forceinline__ void store8(void *p, int64_t idx, const float *x) {
     if (DT == DT_F32) {
         float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p) + idx);
@@ -151,55 +40,213 @@ template <int DT> __device__ __forceinline__ void store8(void *p, int64_t idx, c
     }
 }
 
-// Rows of the cache as they stand for: code x scale rounded to fp16 (the definition of the 8-bit cache), then to DT.
-template <int KT, int D, int DT>
-__global__ void __launch_bounds__(ROW_THREADS) kv_read_kernel(AppendArgs a, int64_t rows) {
-    constexpr int LPR = D / 8, RPW = 32 / LPR;
-    const int lane = threadIdx.x & 31, sub = lane % LPR;
-    const int64_t warps = int64_t(gridDim.x) * (ROW_THREADS / 32);
-    const int H = a.pool.heads;
-    for (int64_t r0 = (int64_t(blockIdx.x) * (ROW_THREADS / 32) + (threadIdx.x >> 5)) * RPW; r0 < rows; r0 += warps * RPW) {
-        const int64_t r = r0 + lane / LPR;
-        if (r >= rows) continue;
-        const int64_t tok = r / (2 * H);
-        const int kh = int(r - tok * 2 * H);
-        const bool is_v = kh >= H;
-        const int head = is_v ? kh - H : kh;
-        void *out = is_v ? a.v : a.k;
-        if (!out) continue;
-        const Place pl = place_of(a, tok);
-        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (pl.page >= 0) {
-            const int64_t in_page = (int64_t(head) * a.pool.page_tokens + pl.slot) * D + sub * 8;
-            const int64_t at = a.layer * a.pool.layer_stride + pl.page * a.pool.page_stride + in_page;
-            const void *base = is_v ? a.pool.v : a.pool.k;
-            if (KT == QPACK_KV_I8) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const int8_t *>(base) + at);
-                const uint16_t *sc = is_v ? a.pool.v_scales : a.pool.k_scales;
-                const float d = h2f_bits(
-                    sc[a.layer * a.pool.scale_layer_stride + pl.page * a.pool.scale_page_stride + in_page / 32]);
-                const uint32_t ww[2] = {w.x, w.y};
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    x[e] = h2f_bits(f2h_bits(d * float(int8_t(uint8_t(ww[e >> 2] >> (8 * (e & 3)))))));
-            } else {
-                load8<KT == QPACK_KV_F16 ? DT_F16 : DT_BF16>(base, at, x);
-            }
+// A warp takes one token's keys or its values, U x RPW heads of them: eight consecutive elements a lane, so a row of D
+// takes D / 8 lanes, RPW = 256 / D rows a pass. The token's place (sequence and position, then the page: two dependent
+// loads) is found once for all of them, while the U rows' loads are in flight; with a row a warp the chain of loads was
+// the time (28 us instead of 13 for 8191 tokens of 8 heads).
+constexpr int ROW_WARPS = 4, ROW_U = 4;
+
+struct Place {
+    int page, pos, slot;   // page -1: nowhere (a skipped token, or one out of range)
+};
+
+__device__ __forceinline__ Place place_of(const AppendArgs &a, int64_t i, bool report) {
+    Place p = {-1, -1, 0};
+    const int64_t seq = a.seqs ? int64_t(__ldg(a.seqs + i)) : i;
+    bool bad = seq < 0 || seq >= a.t.seqs;
+    if (!bad) {
+        p.pos = a.pos ? __ldg(a.pos + i) : __ldg(a.t.lens + seq) - 1;
+        if (p.pos >= 0) {
+            const int shift = 31 - __clz(a.pool.page_tokens), col = p.pos >> shift;
+            p.slot = p.pos & (a.pool.page_tokens - 1);
+            p.page = col < a.t.max_pages ? __ldg(a.t.tables + seq * a.t.stride + col) : -1;
+            bad = p.page < 0 || p.page >= a.pool.pages;
+            if (bad) p.page = -1;
         }
-        store8<DT>(out, tok * (is_v ? a.ldv : a.ldk) + int64_t(head) * D + sub * 8, x);
+    }
+    if (bad && report) atomicOr(&g_fault_paged, FAULT_PAGE);
+    return p;
+}
+
+// The warp's item: token, keys or values, first head of the lane's row.
+struct Item {
+    unsigned tok;
+    bool is_v, live;
+    int head;
+};
+template <int D, int U> __device__ __forceinline__ Item item_of(unsigned items, unsigned half) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR;
+    const unsigned item = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
+    Item t;
+    t.live = item < items;
+    t.tok = item / (2 * half);
+    const unsigned rest = item - t.tok * 2 * half;
+    t.is_v = rest >= half;
+    t.head = int((t.is_v ? rest - half : rest) * (U * RPW) + (threadIdx.x & 31) / LPR);
+    return t;
+}
+
+// The rotation's partner (i +- D/2) is D/16 lanes away, and the four lanes of a 32-element group reduce its maximum
+// with two shuffles.
+template <int KT, int D, int DT>
+__global__ void __launch_bounds__(ROW_WARPS * 32) kv_append_kernel(AppendArgs a, int64_t first, unsigned items, unsigned half) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR, U = ROW_U;
+    const int lane = threadIdx.x & 31, sub = lane % LPR, H = a.pool.heads;
+    pdl_launch_dependents();
+    const Item t = item_of<D, U>(items, half);
+    pdl_wait();
+    if (!t.live) return;                                   // whole warps
+    const int64_t tok = first + t.tok;
+    const int64_t row = tok * (t.is_v ? a.ldv : a.ldk) + sub * 8;
+    float x[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[u][e] = 0.0f;
+        if (t.head + u * RPW < H) load8<DT>(t.is_v ? a.v : a.k, row + int64_t(t.head + u * RPW) * D, x[u]);
+    }
+    const Place pl = place_of(a, tok, lane == 0);
+    if (pl.page < 0) return;
+    if (a.rope && !t.is_v) {
+        const bool in = pl.pos < a.rope_rows;
+        if (!in && lane == 0) atomicOr(&g_fault_paged, FAULT_PAGE);
+        const bool lower = sub < LPR / 2;
+        float c[8] = {1, 1, 1, 1, 1, 1, 1, 1}, s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (in) {
+            const int64_t at = int64_t(pl.pos) * D + (sub % (LPR / 2)) * 8;
+            load8<DT_F32>(a.rope, at, c);
+            load8<DT_F32>(a.rope, at + D / 2, s);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float y = __shfl_xor_sync(0xffffffffu, x[u][e], LPR / 2);
+                // lower half: x c - y s; upper half: x c + y s; each operation rounded
+                const float xc = __fmul_rn(x[u][e], c[e]), ys = __fmul_rn(y, s[e]);
+                if (in) x[u][e] = lower ? __fsub_rn(xc, ys) : __fadd_rn(xc, ys);
+            }
+    }
+    const int64_t page = a.layer * a.pool.layer_stride + pl.page * a.pool.page_stride;
+    const int64_t spage = a.layer * a.pool.scale_layer_stride + pl.page * a.pool.scale_page_stride;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int head = t.head + u * RPW;
+        const unsigned in_page = (unsigned(head) * a.pool.page_tokens + pl.slot) * unsigned(D) + sub * 8;
+        if (KT == QPACK_KV_I8) {
+            float m = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[u][e]));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const uint16_t d16 = f2h_bits(fminf(__fdiv_rn(m, 127.0f), 65504.0f));
+            const float d = h2f_bits(d16);
+            uint8_t cb[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (d > 0.0f) rint_codes<8>(x[u], d, __frcp_rn(d), 0, -127, 127, 0, cb);
+            uint32_t w[2] = {0u, 0u};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e >> 2] |= uint32_t(cb[e]) << (8 * (e & 3));
+            if (head < H) {
+                *reinterpret_cast<uint2 *>(static_cast<int8_t *>(t.is_v ? a.pool.v : a.pool.k) + page + in_page) = make_uint2(w[0], w[1]);
+                if ((sub & 3) == 0) (t.is_v ? a.pool.v_scales : a.pool.k_scales)[spage + in_page / 32] = d16;
+            }
+        } else if (head < H) {
+            store8<KT == QPACK_KV_F16 ? DT_F16 : DT_BF16>(t.is_v ? a.pool.v : a.pool.k, page + in_page, x[u]);
+        }
     }
 }
 
+// Rows of the cache as they stand for: code x scale rounded to fp16 (the definition of the 8-bit cache), then to DT.
+template <int KT, int D, int DT>
+__global__ void __launch_bounds__(ROW_WARPS * 32) kv_read_kernel(AppendArgs a, int64_t first, unsigned items, unsigned half) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR, U = ROW_U;
+    const int lane = threadIdx.x & 31, sub = lane % LPR, H = a.pool.heads;
+    pdl_launch_dependents();
+    const Item t = item_of<D, U>(items, half);
+    pdl_wait();
+    void *out = t.is_v ? a.v : a.k;
+    if (!t.live || !out) return;
+    const int64_t tok = first + t.tok;
+    const Place pl = place_of(a, tok, lane == 0);
+    const int64_t page = a.layer * a.pool.layer_stride + pl.page * a.pool.page_stride;
+    const int64_t spage = a.layer * a.pool.scale_layer_stride + pl.page * a.pool.scale_page_stride;
+    const void *base = t.is_v ? a.pool.v : a.pool.k;
+    constexpr int WORDS = KT == QPACK_KV_I8 ? 2 : 4;
+    uint32_t w[U][WORDS];
+    uint32_t sc[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int e = 0; e < WORDS; ++e) w[u][e] = 0u;
+        sc[u] = 0u;
+        if (pl.page < 0 || t.head + u * RPW >= H) continue;
+        const unsigned in_page = (unsigned(t.head + u * RPW) * a.pool.page_tokens + pl.slot) * unsigned(D) + sub * 8;
+        if (KT == QPACK_KV_I8) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const int8_t *>(base) + page + in_page);
+            w[u][0] = v.x, w[u][1] = v.y;
+            sc[u] = (t.is_v ? a.pool.v_scales : a.pool.k_scales)[spage + in_page / 32];
+        } else {
+            const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + page + in_page);
+            w[u][0] = v.x, w[u][1] = v.y, w[u][WORDS - 2] = v.z, w[u][WORDS - 1] = v.w;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (t.head + u * RPW >= H) continue;
+        uint32_t h[4];                                     // eight 16-bit values
+        if (KT == QPACK_KV_I8) {
+            const uint32_t s = sc[u] | sc[u] << 16;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t c = w[u][e] ^ 0x80808080u;
+                h[2 * e] = dequant2(c, 0x4140u, s), h[2 * e + 1] = dequant2(c, 0x4342u, s);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = w[u][e % WORDS];
+        }
+        const int64_t at = tok * (t.is_v ? a.ldv : a.ldk) + int64_t(t.head + u * RPW) * D + sub * 8;
+        constexpr int HT = KT == QPACK_KV_BF16 ? DT_BF16 : DT_F16;
+        if (DT == HT) {
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) = make_uint4(h[0], h[1], h[2], h[3]);
+        } else {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[2 * e] = HT == DT_F16 ? h2f_bits(uint16_t(h[e] & 0xFFFFu)) : __uint_as_float(h[e] << 16);
+                x[2 * e + 1] = HT == DT_F16 ? h2f_bits(uint16_t(h[e] >> 16)) : __uint_as_float(h[e] & 0xFFFF0000u);
+            }
+            store8<DT>(out, at, x);
+        }
+    }
+}
+
+// Launches a kernel that waits for the previous grid itself: its blocks are set up while that one ends.
+template <class... A> cudaError_t launch_dependent(void (*kernel)(A...), int64_t grid, int threads, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int KT, int D, int DT> cudaError_t run_rows(const AppendArgs &a, bool read, cudaStream_t s) {
-    const int64_t rows = a.n * 2 * a.pool.heads;
-    constexpr int per_block = (ROW_THREADS / 32) * (32 / (D / 8));
-    const int64_t need = (rows + per_block - 1) / per_block, cap = int64_t(num_sms()) * 8;
-    const int grid = int(need < cap ? need : cap);
-    if (read)
-        kv_read_kernel<KT, D, DT><<<grid, ROW_THREADS, 0, s>>>(a, rows);
-    else
-        kv_append_kernel<KT, D, DT><<<grid, ROW_THREADS, 0, s>>>(a, rows);
-    return cudaGetLastError();
+    constexpr int heads = ROW_U * (256 / D);               // a warp's
+    const unsigned half = (a.pool.heads + heads - 1) / heads;
+    const int64_t most = (int64_t(1) << 30) / (2 * half);  // tokens a launch: item numbers stay below 2^31
+    for (int64_t i = 0; i < a.n; i += most) {
+        const int64_t n = a.n - i < most ? a.n - i : most;
+        const unsigned items = unsigned(n * 2 * half);
+        const cudaError_t e = launch_dependent(read ? kv_read_kernel<KT, D, DT> : kv_append_kernel<KT, D, DT>,
+                                               (items + ROW_WARPS - 1) / ROW_WARPS, ROW_WARPS * 32, s, a, i, items, half);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 template <int KT, int D> cudaError_t rows_dt(const AppendArgs &a, bool read, cudaStream_t s) {
