@@ -40,183 +40,246 @@ template <int DT> __device__ __forceinline__ void store8(void *p, int64_t idx, c
     }
 }
 
-// A warp takes one token's keys or its values, U x RPW heads of them: eight consecutive elements a lane, so a row of D
+// A warp takes one token, U x RPW heads of its keys and of its values: eight consecutive elements a lane, so a row of D
 // takes D / 8 lanes, RPW = 256 / D rows a pass. The token's place (sequence and position, then the page: two dependent
-// loads) is found once for all of them, while the U rows' loads are in flight; with a row a warp the chain of loads was
-// the time (28 us instead of 13 for 8191 tokens of 8 heads).
+// loads) is found once for all of them, while appended rows are in flight; with a row a warp that chain of loads was
+// the time.
 constexpr int ROW_WARPS = 4, ROW_U = 4;
 
 struct Place {
     int page, pos, slot;   // page -1: nowhere (a skipped token, or one out of range)
 };
 
-__device__ __forceinline__ Place place_of(const AppendArgs &a, int64_t i, bool report) {
-    Place p = {-1, -1, 0};
+// First the sequence and the position, loaded together where both are given.
+__device__ __forceinline__ int64_t spot_of(const AppendArgs &a, int64_t i, Place &p) {
+    p = {-1, -1, 0};
     const int64_t seq = a.seqs ? int64_t(__ldg(a.seqs + i)) : i;
-    bool bad = seq < 0 || seq >= a.t.seqs;
-    if (!bad) {
-        p.pos = a.pos ? __ldg(a.pos + i) : __ldg(a.t.lens + seq) - 1;
-        if (p.pos >= 0) {
-            const int shift = 31 - __clz(a.pool.page_tokens), col = p.pos >> shift;
-            p.slot = p.pos & (a.pool.page_tokens - 1);
-            p.page = col < a.t.max_pages ? __ldg(a.t.tables + seq * a.t.stride + col) : -1;
-            bad = p.page < 0 || p.page >= a.pool.pages;
-            if (bad) p.page = -1;
-        }
+    if (a.pos) p.pos = __ldg(a.pos + i);
+    if (seq < 0 || seq >= a.t.seqs) {
+        p.pos = -1;
+        return -1;
+    }
+    if (!a.pos) p.pos = __ldg(a.t.lens + seq) - 1;
+    p.slot = p.pos & (a.pool.page_tokens - 1);
+    return seq;
+}
+__device__ __forceinline__ void page_of(const AppendArgs &a, int64_t seq, Place &p, bool report) {
+    bool bad = seq < 0;
+    if (p.pos >= 0) {
+        const int col = p.pos >> (31 - __clz(a.pool.page_tokens));
+        p.page = col < a.t.max_pages ? __ldg(a.t.tables + seq * a.t.stride + col) : -1;
+        bad = p.page < 0 || p.page >= a.pool.pages;
+        if (bad) p.page = -1;
     }
     if (bad && report) atomicOr(&g_fault_paged, FAULT_PAGE);
-    return p;
 }
 
-// The warp's item: token, keys or values, first head of the lane's row.
-struct Item {
-    unsigned tok;
-    bool is_v, live;
-    int head;
-};
-template <int D, int U> __device__ __forceinline__ Item item_of(unsigned items, unsigned half) {
-    constexpr int LPR = D / 8, RPW = 32 / LPR;
-    const unsigned item = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
-    Item t;
-    t.live = item < items;
-    t.tok = item / (2 * half);
-    const unsigned rest = item - t.tok * 2 * half;
-    t.is_v = rest >= half;
-    t.head = int((t.is_v ? rest - half : rest) * (U * RPW) + (threadIdx.x & 31) / LPR);
-    return t;
+// Eight consecutive elements as loaded, and as fp32.
+template <int DT> struct Raw { uint32_t w[DT == DT_F32 ? 8 : 4]; };
+template <int DT> __device__ __forceinline__ void load_raw(const void *p, int64_t idx, Raw<DT> &r) {
+    const uint4 *q = DT == DT_F32 ? reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + idx)
+                                  : reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + idx);
+#pragma unroll
+    for (int i = 0; i < (DT == DT_F32 ? 2 : 1); ++i) {
+        const uint4 v = __ldg(q + i);
+        r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+    }
+}
+template <int DT> __device__ __forceinline__ void convert(const Raw<DT> &r, float *x) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if (DT == DT_F32) x[e] = __uint_as_float(r.w[e % (DT == DT_F32 ? 8 : 4)]);
+        else if (DT == DT_F16) x[e] = h2f_bits(uint16_t(e & 1 ? r.w[e / 2] >> 16 : r.w[e / 2] & 0xFFFFu));
+        else x[e] = __uint_as_float(e & 1 ? r.w[e / 2] & 0xFFFF0000u : r.w[e / 2] << 16);
+    }
 }
 
 // The rotation's partner (i +- D/2) is D/16 lanes away, and the four lanes of a 32-element group reduce its maximum
 // with two shuffles.
 template <int KT, int D, int DT>
-__global__ void __launch_bounds__(ROW_WARPS * 32) kv_append_kernel(AppendArgs a, int64_t first, unsigned items, unsigned half) {
+__global__ void __launch_bounds__(ROW_WARPS * 32, 4) kv_append_kernel(AppendArgs a, int64_t first, unsigned items, unsigned groups) {
     constexpr int LPR = D / 8, RPW = 32 / LPR, U = ROW_U;
     const int lane = threadIdx.x & 31, sub = lane % LPR, H = a.pool.heads;
     pdl_launch_dependents();
-    const Item t = item_of<D, U>(items, half);
+    const unsigned item = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5), tok_in = groups == 1 ? item : item / groups;
+    const int head0 = int(item - tok_in * groups) * (U * RPW) + lane / LPR;
     pdl_wait();
-    if (!t.live) return;                                   // whole warps
-    const int64_t tok = first + t.tok;
-    const int64_t row = tok * (t.is_v ? a.ldv : a.ldk) + sub * 8;
-    float x[U][8];
+    if (item >= items) return;                             // whole warps
+    const int64_t tok = first + tok_in;
+    Raw<DT> raw[2][U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[u][e] = 0.0f;
-        if (t.head + u * RPW < H) load8<DT>(t.is_v ? a.v : a.k, row + int64_t(t.head + u * RPW) * D, x[u]);
-    }
-    const Place pl = place_of(a, tok, lane == 0);
-    if (pl.page < 0) return;
-    if (a.rope && !t.is_v) {
-        const bool in = pl.pos < a.rope_rows;
-        if (!in && lane == 0) atomicOr(&g_fault_paged, FAULT_PAGE);
-        const bool lower = sub < LPR / 2;
-        float c[8] = {1, 1, 1, 1, 1, 1, 1, 1}, s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (in) {
-            const int64_t at = int64_t(pl.pos) * D + (sub % (LPR / 2)) * 8;
-            load8<DT_F32>(a.rope, at, c);
-            load8<DT_F32>(a.rope, at + D / 2, s);
-        }
+    for (int v = 0; v < 2; ++v) {
+        const int64_t row = tok * (v ? a.ldv : a.ldk) + sub * 8;
 #pragma unroll
         for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float y = __shfl_xor_sync(0xffffffffu, x[u][e], LPR / 2);
-                // lower half: x c - y s; upper half: x c + y s; each operation rounded
-                const float xc = __fmul_rn(x[u][e], c[e]), ys = __fmul_rn(y, s[e]);
-                if (in) x[u][e] = lower ? __fsub_rn(xc, ys) : __fadd_rn(xc, ys);
-            }
+            if (head0 + u * RPW < H) load_raw<DT>(v ? a.v : a.k, row + (head0 + u * RPW) * D, raw[v][u]);
+            else raw[v][u] = Raw<DT>{};
     }
+    Place pl;
+    const int64_t seq = spot_of(a, tok, pl);
+    float c[8] = {1, 1, 1, 1, 1, 1, 1, 1}, s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (a.rope && pl.pos >= 0 && pl.pos < a.rope_rows) {
+        const int64_t at = int64_t(pl.pos) * D + (sub % (LPR / 2)) * 8;
+        load8<DT_F32>(a.rope, at, c);
+        load8<DT_F32>(a.rope, at + D / 2, s);
+    }
+    page_of(a, seq, pl, lane == 0);
+    if (pl.page < 0) return;
     const int64_t page = a.layer * a.pool.layer_stride + pl.page * a.pool.page_stride;
     const int64_t spage = a.layer * a.pool.scale_layer_stride + pl.page * a.pool.scale_page_stride;
+    const unsigned in_page = (unsigned(head0) * a.pool.page_tokens + pl.slot) * unsigned(D) + sub * 8;
+    const unsigned pass = unsigned(RPW) * a.pool.page_tokens * unsigned(D);            // to the next row of the lane
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int head = t.head + u * RPW;
-        const unsigned in_page = (unsigned(head) * a.pool.page_tokens + pl.slot) * unsigned(D) + sub * 8;
-        if (KT == QPACK_KV_I8) {
-            float m = 0.0f;
+    for (int v = 0; v < 2; ++v) {
+        float x[U][8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[u][e]));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            const uint16_t d16 = f2h_bits(fminf(__fdiv_rn(m, 127.0f), 65504.0f));
-            const float d = h2f_bits(d16);
-            uint8_t cb[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (d > 0.0f) rint_codes<8>(x[u], d, __frcp_rn(d), 0, -127, 127, 0, cb);
-            uint32_t w[2] = {0u, 0u};
+        for (int u = 0; u < U; ++u) convert<DT>(raw[v][u], x[u]);
+        if (a.rope && v == 0) {
+            if (pl.pos >= a.rope_rows && lane == 0) atomicOr(&g_fault_paged, FAULT_PAGE);
+            // lower half: x c - y s; upper half: x c + y s; each operation rounded
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e >> 2] |= uint32_t(cb[e]) << (8 * (e & 3));
-            if (head < H) {
-                *reinterpret_cast<uint2 *>(static_cast<int8_t *>(t.is_v ? a.pool.v : a.pool.k) + page + in_page) = make_uint2(w[0], w[1]);
-                if ((sub & 3) == 0) (t.is_v ? a.pool.v_scales : a.pool.k_scales)[spage + in_page / 32] = d16;
-            }
-        } else if (head < H) {
-            store8<KT == QPACK_KV_F16 ? DT_F16 : DT_BF16>(t.is_v ? a.pool.v : a.pool.k, page + in_page, x[u]);
+            for (int e = 0; e < 8; ++e) s[e] = sub < LPR / 2 ? -s[e] : s[e];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float y = __shfl_xor_sync(0xffffffffu, x[u][e], LPR / 2);
+                    x[u][e] = __fadd_rn(__fmul_rn(x[u][e], c[e]), __fmul_rn(y, s[e]));
+                }
         }
+        if (KT != QPACK_KV_I8) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (head0 + u * RPW < H)
+                    store8<KT == QPACK_KV_F16 ? DT_F16 : DT_BF16>(v ? a.pool.v : a.pool.k, page + in_page + u * pass, x[u]);
+            continue;
+        }
+        // The scales: the four lanes of a group hold the maxima of U = 4 rows alike, so lane k of them does row k's two
+        // divisions for all.
+        static_assert(U == 4, "a lane a row");
+        float m[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            m[u] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m[u] = fmaxf(m[u], fabsf(x[u][e]));
+            m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], 1));
+            m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], 2));
+        }
+        const int k = lane & 3;
+        const float mine = k & 2 ? (k & 1 ? m[3] : m[2]) : (k & 1 ? m[1] : m[0]);
+        const uint16_t d16 = f2h_bits(fminf(__fdiv_rn(mine, 127.0f), 65504.0f));
+        const float d = h2f_bits(d16), rs = d > 0.0f ? __frcp_rn(d) : 0.0f;     // a scale of 0 gives codes of 0
+        // A scale that fp16 holds as a normal number is off by at most 2^-11 of max / 127, so no quotient is beyond
+        // 127.07 and none needs the clamp; the others take the written definition below.
+        const bool tiny = d < 0x1p-14f && d > 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int from = (lane & ~3) + u;
+            const float r = __shfl_sync(0xffffffffu, rs, from);
+            bool plain = __shfl_sync(0xffffffffu, tiny, from);
+            // q = rint(x r) read from the low byte of x r + 1.5 2^23. x r is within 2^-24 |x / d| of x / d, and the
+            // rounded quotient too, together less than 2^-16: where x r is nearer than 1/2 - 2^-15 to q, q is the
+            // quotient's rint.
+            float y[8], off = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                y[e] = __fmaf_rn(x[u][e], r, 12582912.0f);
+                off = fmaxf(off, fabsf(__fmaf_rn(x[u][e], r, 12582912.0f - y[e])));
+            }
+            uint32_t w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t lo = __byte_perm(__float_as_uint(y[4 * e]), __float_as_uint(y[4 * e + 1]), 0x0040u);
+                const uint32_t hi = __byte_perm(__float_as_uint(y[4 * e + 2]), __float_as_uint(y[4 * e + 3]), 0x0040u);
+                w[e] = __byte_perm(lo, hi, 0x5410u);
+            }
+            plain |= !(off <= 0.5f - 0x1p-15f);
+            if (__any_sync(0xffffffffu, plain)) {          // rare
+                const float du = h2f_bits(uint16_t(__shfl_sync(0xffffffffu, int(d16), from)));
+                if (plain && du > 0.0f) {
+                    uint8_t cb[8];
+                    rint_codes<8>(x[u], du, r, 0, -127, 127, 0, cb);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        w[e] = cb[4 * e] | uint32_t(cb[4 * e + 1]) << 8 | uint32_t(cb[4 * e + 2]) << 16 | uint32_t(cb[4 * e + 3]) << 24;
+                }
+            }
+            if (head0 + u * RPW < H)
+                *reinterpret_cast<uint2 *>(static_cast<int8_t *>(v ? a.pool.v : a.pool.k) + page + in_page + u * pass) = make_uint2(w[0], w[1]);
+        }
+        if (head0 + k * RPW < H) (v ? a.pool.v_scales : a.pool.k_scales)[spage + (in_page + k * pass) / 32] = d16;
     }
 }
 
 // Rows of the cache as they stand for: code x scale rounded to fp16 (the definition of the 8-bit cache), then to DT.
 template <int KT, int D, int DT>
-__global__ void __launch_bounds__(ROW_WARPS * 32) kv_read_kernel(AppendArgs a, int64_t first, unsigned items, unsigned half) {
+__global__ void __launch_bounds__(ROW_WARPS * 32, 8) kv_read_kernel(AppendArgs a, int64_t first, unsigned items, unsigned groups) {
     constexpr int LPR = D / 8, RPW = 32 / LPR, U = ROW_U;
     const int lane = threadIdx.x & 31, sub = lane % LPR, H = a.pool.heads;
     pdl_launch_dependents();
-    const Item t = item_of<D, U>(items, half);
+    const unsigned item = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5), tok_in = groups == 1 ? item : item / groups;
+    const int head0 = int(item - tok_in * groups) * (U * RPW) + lane / LPR;
     pdl_wait();
-    void *out = t.is_v ? a.v : a.k;
-    if (!t.live || !out) return;
-    const int64_t tok = first + t.tok;
-    const Place pl = place_of(a, tok, lane == 0);
+    if (item >= items) return;                             // whole warps
+    const int64_t tok = first + tok_in;
+    Place pl;
+    const int64_t seq = spot_of(a, tok, pl);
+    page_of(a, seq, pl, lane == 0);
     const int64_t page = a.layer * a.pool.layer_stride + pl.page * a.pool.page_stride;
     const int64_t spage = a.layer * a.pool.scale_layer_stride + pl.page * a.pool.scale_page_stride;
-    const void *base = t.is_v ? a.pool.v : a.pool.k;
+    const unsigned in_page = (unsigned(head0) * a.pool.page_tokens + pl.slot) * unsigned(D) + sub * 8;
+    const unsigned pass = unsigned(RPW) * a.pool.page_tokens * unsigned(D);
     constexpr int WORDS = KT == QPACK_KV_I8 ? 2 : 4;
-    uint32_t w[U][WORDS];
-    uint32_t sc[U];
+    uint32_t w[2][U][WORDS], sc[2][U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int v = 0; v < 2; ++v)
 #pragma unroll
-        for (int e = 0; e < WORDS; ++e) w[u][e] = 0u;
-        sc[u] = 0u;
-        if (pl.page < 0 || t.head + u * RPW >= H) continue;
-        const unsigned in_page = (unsigned(t.head + u * RPW) * a.pool.page_tokens + pl.slot) * unsigned(D) + sub * 8;
-        if (KT == QPACK_KV_I8) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const int8_t *>(base) + page + in_page);
-            w[u][0] = v.x, w[u][1] = v.y;
-            sc[u] = (t.is_v ? a.pool.v_scales : a.pool.k_scales)[spage + in_page / 32];
-        } else {
-            const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + page + in_page);
-            w[u][0] = v.x, w[u][1] = v.y, w[u][WORDS - 2] = v.z, w[u][WORDS - 1] = v.w;
-        }
-    }
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (t.head + u * RPW >= H) continue;
-        uint32_t h[4];                                     // eight 16-bit values
-        if (KT == QPACK_KV_I8) {
-            const uint32_t s = sc[u] | sc[u] << 16;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t c = w[u][e] ^ 0x80808080u;
-                h[2 * e] = dequant2(c, 0x4140u, s), h[2 * e + 1] = dequant2(c, 0x4342u, s);
+            for (int e = 0; e < WORDS; ++e) w[v][u][e] = 0u;
+            sc[v][u] = 0u;
+            if (pl.page < 0 || head0 + u * RPW >= H || !(v ? a.v : a.k)) continue;
+            const void *base = v ? a.pool.v : a.pool.k;
+            if (KT == QPACK_KV_I8) {
+                const uint2 q = *reinterpret_cast<const uint2 *>(static_cast<const int8_t *>(base) + page + in_page + u * pass);
+                w[v][u][0] = q.x, w[v][u][1] = q.y;
+                sc[v][u] = (v ? a.pool.v_scales : a.pool.k_scales)[spage + (in_page + u * pass) / 32];
+            } else {
+                const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + page + in_page + u * pass);
+                w[v][u][0] = q.x, w[v][u][1] = q.y, w[v][u][WORDS - 2] = q.z, w[v][u][WORDS - 1] = q.w;
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = w[u][e % WORDS];
         }
-        const int64_t at = tok * (t.is_v ? a.ldv : a.ldk) + int64_t(t.head + u * RPW) * D + sub * 8;
-        constexpr int HT = KT == QPACK_KV_BF16 ? DT_BF16 : DT_F16;
-        if (DT == HT) {
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) = make_uint4(h[0], h[1], h[2], h[3]);
-        } else {
-            float x[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[2 * e] = HT == DT_F16 ? h2f_bits(uint16_t(h[e] & 0xFFFFu)) : __uint_as_float(h[e] << 16);
-                x[2 * e + 1] = HT == DT_F16 ? h2f_bits(uint16_t(h[e] >> 16)) : __uint_as_float(h[e] & 0xFFFF0000u);
+    for (int v = 0; v < 2; ++v) {
+        void *out = v ? a.v : a.k;
+        if (!out) continue;
+        const int64_t row = tok * (v ? a.ldv : a.ldk) + sub * 8;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (head0 + u * RPW >= H) continue;
+            uint32_t h[4];                                 // eight 16-bit values
+            if (KT == QPACK_KV_I8) {
+                const uint32_t s = sc[v][u] | sc[v][u] << 16;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t c = w[v][u][e] ^ 0x80808080u;
+                    h[2 * e] = dequant2(c, 0x4140u, s), h[2 * e + 1] = dequant2(c, 0x4342u, s);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[e] = w[v][u][e % WORDS];
             }
-            store8<DT>(out, at, x);
+            const int64_t at = row + (head0 + u * RPW) * D;
+            constexpr int HT = KT == QPACK_KV_BF16 ? DT_BF16 : DT_F16;
+            if (DT == HT) {
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) = make_uint4(h[0], h[1], h[2], h[3]);
+            } else {
+                Raw<HT> r = {h[0], h[1], h[2], h[3]};
+                float x[8];
+                convert<HT>(r, x);
+                store8<DT>(out, at, x);
+            }
         }
     }
 }
@@ -237,13 +300,13 @@ template <class... A> cudaError_t launch_dependent(void (*kernel)(A...), int64_t
 
 template <int KT, int D, int DT> cudaError_t run_rows(const AppendArgs &a, bool read, cudaStream_t s) {
     constexpr int heads = ROW_U * (256 / D);               // a warp's
-    const unsigned half = (a.pool.heads + heads - 1) / heads;
-    const int64_t most = (int64_t(1) << 30) / (2 * half);  // tokens a launch: item numbers stay below 2^31
+    const unsigned groups = (a.pool.heads + heads - 1) / heads;
+    const int64_t most = (int64_t(1) << 30) / groups;      // tokens a launch: item numbers stay below 2^31
     for (int64_t i = 0; i < a.n; i += most) {
         const int64_t n = a.n - i < most ? a.n - i : most;
-        const unsigned items = unsigned(n * 2 * half);
+        const unsigned items = unsigned(n * groups);
         const cudaError_t e = launch_dependent(read ? kv_read_kernel<KT, D, DT> : kv_append_kernel<KT, D, DT>,
-                                               (items + ROW_WARPS - 1) / ROW_WARPS, ROW_WARPS * 32, s, a, i, items, half);
+                                               (items + ROW_WARPS - 1) / ROW_WARPS, ROW_WARPS * 32, s, a, i, items, groups);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
