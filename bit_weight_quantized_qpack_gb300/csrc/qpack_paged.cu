@@ -362,6 +362,20 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
     return before + x - v;
 }
 
+// Reference counts are ranked in chunks of SCAN a thread, so that a few thousand pages are one pass of the block (a page
+// a thread took seven passes of three barriers each, 3 us, at 1600 pages). Bit i of the result: page p + i passes `test`.
+constexpr int SCAN = 8;
+template <class Test> __device__ __forceinline__ unsigned pages_where(const int *refs, int64_t p, int64_t pages, Test test) {
+    unsigned m = 0;
+    int r[SCAN];
+#pragma unroll
+    for (int i = 0; i < SCAN; ++i) r[i] = p + i < pages ? refs[p + i] : 0;
+#pragma unroll
+    for (int i = 0; i < SCAN; ++i)
+        if (p + i < pages && test(r[i], p + i)) m |= 1u << i;
+    return m;
+}
+
 // Work of the copy kernel: rows [0, rows) of page src to page dst, in every layer.
 struct CopyItem { int src, dst, rows; };
 
@@ -392,6 +406,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_reserve_kernel(qpack_kv_table
         return (old + page_tokens - 1) / page_tokens;
     };
     int carry = 0, tot;
+    pdl_launch_dependents();
+    pdl_wait();
     for (int i0 = 0; i0 < n; i0 += blockDim.x) {
         const int i = i0 + threadIdx.x;
         int need = 0, s = -1;
@@ -421,19 +437,20 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_reserve_kernel(qpack_kv_table
     __syncthreads();
     const int want = carry;
     int found = 0;
-    for (int64_t p0 = 0; p0 < pages && found < want; p0 += blockDim.x) {
-        const int64_t p = p0 + threadIdx.x;
-        const int is_free = p < pages && t.refs[p] == 0;
-        const int rank = found + block_scan(is_free, sums, &tot);
-        if (is_free && rank < want) {
+    for (int64_t p0 = 0; p0 < pages && found < want; p0 += blockDim.x * SCAN) {
+        const int64_t p = p0 + threadIdx.x * SCAN;
+        unsigned m = pages_where(t.refs, p, pages, [](int r, int64_t) { return r == 0; });
+        int rank = found + block_scan(__popc(m), sums, &tot);
+        for (; m && rank < want; m &= m - 1, ++rank) {
             int lo = 0, hi = n;                            // off[lo] <= rank < off[lo + 1]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
                 if (off[mid] <= rank) lo = mid; else hi = mid;
             }
             // requests that need nothing share their offset with the next one: the last of them owns the rank
-            t.tables[int64_t(who[lo]) * t.stride + first_col(who[lo]) + (rank - off[lo])] = int(p);
-            t.refs[p] = 1;
+            const int page = int(p) + __ffs(m) - 1;
+            t.tables[int64_t(who[lo]) * t.stride + first_col(who[lo]) + (rank - off[lo])] = page;
+            t.refs[page] = 1;
         }
         found += tot;
     }
@@ -464,6 +481,8 @@ __global__ void __launch_bounds__(256) kv_fork_kernel(qpack_kv_tables_t t, int p
                                                       const int *dst, int n, int64_t pages, PageWs w) {
     __shared__ int sums[32];
     __shared__ int s_fresh;
+    pdl_launch_dependents();
+    pdl_wait();
     const int i = blockIdx.x;
     const int s = src[i], d = dst[i];
     auto len_of = [&](int q) {
@@ -480,11 +499,14 @@ __global__ void __launch_bounds__(256) kv_fork_kernel(qpack_kv_tables_t t, int p
     const int len = len_of(s), full = len / page_tokens, rows = len & (page_tokens - 1);
     if (rows) {
         int found = 0;
-        for (int64_t p0 = 0; p0 < pages && found <= before; p0 += blockDim.x) {
-            const int64_t p = p0 + threadIdx.x;
-            const int is_free = p < pages && t.refs[p] == 0;
-            const int rank = found + block_scan(is_free, sums, &tot);
-            if (is_free && rank == before) s_fresh = int(p);
+        for (int64_t p0 = 0; p0 < pages && found <= before; p0 += blockDim.x * SCAN) {
+            const int64_t p = p0 + threadIdx.x * SCAN;
+            unsigned m = pages_where(t.refs, p, pages, [](int r, int64_t) { return r == 0; });
+            const int rank = found + block_scan(__popc(m), sums, &tot);
+            if (rank <= before && before < rank + __popc(m)) {
+                for (int k = rank; k < before; ++k) m &= m - 1;
+                s_fresh = int(p) + __ffs(m) - 1;
+            }
             found += tot;
         }
         __syncthreads();
@@ -515,6 +537,8 @@ __global__ void __launch_bounds__(256) kv_fork_kernel(qpack_kv_tables_t t, int p
 }
 
 __global__ void __launch_bounds__(256) kv_free_kernel(qpack_kv_tables_t t, const int *seqs) {
+    pdl_launch_dependents();
+    pdl_wait();
     const int s = seqs[blockIdx.x];
     if (s < 0) return;
     if (s >= t.seqs) {
@@ -537,26 +561,30 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_compact_plan_kernel(qpack_kv_
                                                                        int64_t pages, int *refs_out, int *moved, PageWs w) {
     __shared__ int sums[32];
     int tot, nlive = 0;
-    for (int64_t p0 = 0; p0 < pages; p0 += blockDim.x) {
-        const int64_t p = p0 + threadIdx.x;
-        block_scan(p < pages && t.refs[p] > 0, sums, &tot);
+    pdl_launch_dependents();
+    pdl_wait();
+    for (int64_t p0 = 0; p0 < pages; p0 += blockDim.x * SCAN) {
+        const unsigned m = pages_where(t.refs, p0 + threadIdx.x * SCAN, pages, [](int r, int64_t) { return r > 0; });
+        block_scan(__popc(m), sums, &tot);
         nlive += tot;
     }
     int holes = 0, movers = 0;
-    for (int64_t p0 = 0; p0 < pages; p0 += blockDim.x) {
-        const int64_t p = p0 + threadIdx.x;
-        const bool in = p < pages;
-        const int r = in ? t.refs[p] : 0;
-        const int hole = in && r <= 0 && p < nlive, mover = r > 0 && p >= nlive;
-        const int hr = holes + block_scan(hole, sums, &tot);
-        holes += tot;
-        const int mr = movers + block_scan(mover, sums, &tot);
-        movers += tot;
-        if (hole) w.items[hr].dst = int(p);
-        if (mover) w.items[mr].src = int(p);
-        if (in) {
-            w.map[p] = int(p);
-            if (!hole && !mover) refs_out[p] = p < nlive ? r : 0;
+    for (int64_t p0 = 0; p0 < pages; p0 += blockDim.x * SCAN) {
+        const int64_t p = p0 + threadIdx.x * SCAN;
+        const unsigned hole = pages_where(t.refs, p, pages, [&](int r, int64_t q) { return r <= 0 && q < nlive; });
+        const unsigned mover = pages_where(t.refs, p, pages, [&](int r, int64_t q) { return r > 0 && q >= nlive; });
+        // both ranks in one scan: at most 2^13 of each a chunk, carried in whole numbers
+        const int both = block_scan(__popc(hole) | __popc(mover) << 16, sums, &tot);
+        int hr = holes + (both & 0xFFFF), mr = movers + (both >> 16);
+        holes += tot & 0xFFFF;
+        movers += tot >> 16;
+        for (unsigned m = hole; m; m &= m - 1) w.items[hr++].dst = int(p) + __ffs(m) - 1;
+        for (unsigned m = mover; m; m &= m - 1) w.items[mr++].src = int(p) + __ffs(m) - 1;
+#pragma unroll
+        for (int i = 0; i < SCAN; ++i) {
+            if (p + i >= pages) break;
+            w.map[p + i] = int(p + i);
+            if (!((hole | mover) >> i & 1)) refs_out[p + i] = p + i < nlive ? t.refs[p + i] : 0;
         }
     }
     __syncthreads();
@@ -583,6 +611,8 @@ __global__ void __launch_bounds__(256) kv_copy_kernel(qpack_kv_pool_t pool, Page
     const int lane = threadIdx.x & 31;
     const int64_t warp = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int64_t warps = int64_t(gridDim.x) * (blockDim.x >> 5);
+    pdl_launch_dependents();
+    pdl_wait();
     const int64_t n = src_list ? n_list : w.count[0];
     const int64_t slabs = n * pool.layers * 2 * pool.heads;
     const int es = pool.type == QPACK_KV_I8 ? 1 : 2;
@@ -640,8 +670,7 @@ cudaError_t run_copy(const qpack_kv_pool_t &p, const PageWs &w, const int *src, 
     const int64_t warps = most * p.layers * 2 * p.heads, cap = int64_t(num_sms()) * 8;
     int64_t grid = (warps + 7) / 8;
     grid = grid < 1 ? 1 : (grid < cap ? grid : cap);
-    kv_copy_kernel<<<int(grid), 256, 0, s>>>(p, w, src, dst, n, refs, t, tables_out);
-    return cudaGetLastError();
+    return launch_dependent(kv_copy_kernel, grid, 256, s, p, w, src, dst, n, refs, t, tables_out);
 }
 
 }  // namespace
@@ -655,29 +684,26 @@ int64_t kv_page_workspace(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t) 
 
 cudaError_t launch_kv_reserve(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t, const int32_t *seqs,
                               const int32_t *add, int n, cudaStream_t s) {
-    kv_reserve_kernel<<<1, PLAN_THREADS, 0, s>>>(t, p.page_tokens, seqs, add, n, t.pages);
-    return cudaGetLastError();
+    return launch_dependent(kv_reserve_kernel, 1, PLAN_THREADS, s, t, int(p.page_tokens), seqs, add, n, t.pages);
 }
 
 cudaError_t launch_kv_fork(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t, const int32_t *src, const int32_t *dst,
                            int n, void *ws, cudaStream_t s) {
     const PageWs w = page_ws(ws, p.pages);
-    kv_fork_kernel<<<n, 256, 0, s>>>(t, p.page_tokens, src, dst, n, t.pages, w);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_dependent(kv_fork_kernel, n, 256, s, t, int(p.page_tokens), src, dst, n, t.pages, w);
     if (e != cudaSuccess) return e;
     return run_copy(p, w, nullptr, nullptr, 0, n, t.refs, t, nullptr, s);
 }
 
 cudaError_t launch_kv_free(const qpack_kv_tables_t &t, const int32_t *seqs, int n, cudaStream_t s) {
-    kv_free_kernel<<<n, 256, 0, s>>>(t, seqs);
-    return cudaGetLastError();
+    return launch_dependent(kv_free_kernel, n, 256, s, t, seqs);
 }
 
 cudaError_t launch_kv_compact(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t, int32_t *tables_out,
                               int32_t *refs_out, int32_t *moved, void *ws, cudaStream_t s) {
     const PageWs w = page_ws(ws, p.pages);
-    kv_compact_plan_kernel<<<1, PLAN_THREADS, 0, s>>>(t, p.page_tokens, t.pages, refs_out, moved, w);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_dependent(kv_compact_plan_kernel, 1, PLAN_THREADS, s, t, int(p.page_tokens), t.pages,
+                                           refs_out, moved, w);
     if (e != cudaSuccess) return e;
     return run_copy(p, w, nullptr, nullptr, 0, t.pages / 2 + 1, nullptr, t, tables_out, s);
 }
