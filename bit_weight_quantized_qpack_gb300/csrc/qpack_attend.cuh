@@ -60,7 +60,7 @@ template <int KT, int D, int NT> struct Cfg {
     static constexpr int SB = KT == QPACK_KV_I8 ? D / 16 : 0;   // bytes of its scales
     static constexpr int TOK = RB >= 256 ? 16 : 32;
     static constexpr int TILE = 2 * TOK * (RB + SB);            // keys, values, their scales
-    static constexpr int W = RB == 512 ? 6 : D * NT >= 256 ? 8 : 12;
+    static constexpr int W = RB == 512 ? 6 : D * NT >= 256 || (KT == QPACK_KV_I8 && D == 128) ? 8 : 12;
     static constexpr int STAGES = 214000 / (W * TILE) > 4 ? 4 : 214000 / (W * TILE);
     static constexpr int NH = 8 * NT;
     static constexpr int PS = D + 4;                            // floats of a head in a partial, padded for the banks
@@ -73,6 +73,7 @@ struct Params {
     AttendArgs a;
     int B, C, G;                // rows of this launch, groups of query heads, query heads a key/value head
     int row0;                   // first row of this launch
+    int per_seg;                // blocks a segment where there are as many blocks as segments or more, else 0
     int *counters;              // [MAX_SEGS], zero between calls
     float *block_parts;         // [grid][2][PF]
     float *warp_parts;          // [grid][W][PF]
@@ -250,30 +251,46 @@ struct Plan {
     unsigned total, size;
     int per, HC;                                           // HC: segments a row
 };
+// a / b, b > 0. The set-up of a block is a chain of these; by an approximate quotient, put right in integers, each
+// takes half as long as the general division.
+__device__ __forceinline__ unsigned quot(unsigned a, unsigned b) {
+    const float r = __fdividef(1.0f, float(b));
+    unsigned q = unsigned(float(a) * r);
+    q += int(float(int(a - q * b)) * r);                   // off by at most 2^9 before, by one after
+    int rest = int(a - q * b);
+    if (rest < 0) --q, rest += b;
+    if (rest >= int(b)) ++q;
+    return q;
+}
 // Units of a segment of row b (0: an empty row), and where the segment's begin.
 __device__ __forceinline__ unsigned seg_units(const unsigned *cum, int b) { return cum[b + 1] - cum[b]; }
 __device__ __forceinline__ unsigned seg_start(const Plan &pl, const unsigned *cum, int b, int hc) {
     return cum[b] * pl.HC + hc * seg_units(cum, b);
 }
-__device__ __forceinline__ unsigned block_edge(const Plan &pl, const unsigned *cum, int B, int i, int end) {
-    if (!pl.per) return min(unsigned(i + end) * pl.size, pl.total);
-    const int seg = i / pl.per;
-    if (seg >= B * pl.HC) return pl.total;
-    const int b = seg / pl.HC, part = i - seg * pl.per + end;
-    const unsigned s0 = seg_start(pl, cum, b, seg - b * pl.HC);
-    return part ? min(s0 + SETUP + part * pl.size, s0 + seg_units(cum, b)) : s0;
+__device__ __forceinline__ void block_share(const Plan &pl, const unsigned *cum, int B, int i, unsigned &start, unsigned &end) {
+    if (!pl.per) {
+        start = min(unsigned(i) * pl.size, pl.total), end = min(start + pl.size, pl.total);
+        return;
+    }
+    const int seg = quot(i, pl.per);
+    start = end = pl.total;
+    if (seg >= B * pl.HC) return;
+    const int b = quot(seg, pl.HC), part = i - seg * pl.per;
+    const unsigned s0 = seg_start(pl, cum, b, seg - b * pl.HC), s1 = s0 + seg_units(cum, b);
+    start = part ? min(s0 + SETUP + part * pl.size, s1) : s0;
+    end = min(s0 + SETUP + (part + 1) * pl.size, s1);
 }
 // The blocks that share a segment: the first holds it in its second slot of the workspace, the others, which begin inside
 // it, in their first.
 __device__ __forceinline__ void sharers(const Plan &pl, const unsigned *cum, int seg, int &first, int &count) {
-    const int b = seg / pl.HC;
+    const int b = quot(seg, pl.HC);
     const unsigned s0 = seg_start(pl, cum, b, seg - b * pl.HC) + SETUP, n = seg_units(cum, b) - SETUP;    // its tiles
     if (pl.per) {
         first = seg * pl.per;
-        count = int((n + pl.size - 1) / pl.size);
+        count = int(quot(n + pl.size - 1, pl.size));
     } else {
-        first = int(s0 / pl.size);
-        count = int((s0 + n - 1) / pl.size) - first + 1;
+        first = int(quot(s0, pl.size));
+        count = int(quot(s0 + n - 1, pl.size)) - first + 1;
     }
 }
 
@@ -293,10 +310,10 @@ template <int TOK> __device__ __forceinline__ void seek(const Params &p, const P
     c.b = lo;
     c.row = row_of<TOK>(p, lo, nullptr);
     const unsigned rem = unit - cum[lo] * pl.HC, n = c.row.tiles + SETUP;
-    c.hc = int(rem / n);
+    c.hc = int(quot(rem, n));
     const unsigned at = rem - c.hc * n;
     c.ti = at > SETUP ? at - SETUP : 0;
-    c.h = c.hc / p.C;
+    c.h = p.C == 1 ? c.hc : int(quot(c.hc, p.C));
     c.q = c.hc - c.h * p.C;
 }
 // The next segment; there is one.
@@ -319,15 +336,24 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -INFINITY : (m - P_BIAS) * 0.6931471805599453f + logf(l);
 }
 
-// A triple of one head and four of its accumulators, joined one by one.
+// A triple of one head and four of its accumulators, joined with n <= N others.
 struct Triple {
     float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    __device__ __forceinline__ void add(float mi, float li, float4 x) {
-        const float top = fmaxf(m, mi), base = finite_base(top), f = ex2(m - base), h = ex2(mi - base);
+    template <int N> __device__ __forceinline__ void add(const float (&mi)[N], const float (&li)[N], const float4 (&x)[N], int n) {
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < N; ++i) top = i < n ? fmaxf(top, mi[i]) : top;
+        const float base = finite_base(top), f = ex2(m - base);
         m = top;
-        l = fmaf(li, h, l * f);
-        o.x = fmaf(x.x, h, o.x * f), o.y = fmaf(x.y, h, o.y * f), o.z = fmaf(x.z, h, o.z * f), o.w = fmaf(x.w, h, o.w * f);
+        l *= f, o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (i >= n) continue;
+            const float h = ex2(mi[i] - base);
+            l = fmaf(li[i], h, l);
+            o.x = fmaf(x[i].x, h, o.x), o.y = fmaf(x[i].y, h, o.y), o.z = fmaf(x[i].z, h, o.z), o.w = fmaf(x[i].w, h, o.w);
+        }
     }
 };
 
@@ -387,15 +413,14 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     const unsigned grid = gridDim.x;
     pl.HC = a.pool.heads * p.C;
     pl.total = cum[p.B] * pl.HC;
-    pl.size = max((pl.total + grid - 1) / grid, unsigned(W));           // at least a unit a warp
+    pl.size = max(quot(pl.total + grid - 1, grid), unsigned(W));        // at least a unit a warp
     pl.per = 0;
-    const unsigned nseg = p.B * pl.HC, longest = s_max ? s_max - SETUP : 0;
-    if (nseg <= grid) {
+    if (p.per_seg) {
         // Few segments: boundaries on theirs save the joins of the pieces, where the shares stay nearly equal.
-        const unsigned k = grid / nseg, size = max((longest + k - 1) / k, unsigned(W));
+        const unsigned longest = s_max ? s_max - SETUP : 0, k = p.per_seg, size = max(quot(longest + k - 1, k), unsigned(W));
         if (size <= pl.size + pl.size / 8) {
             pl.size = size;
-            pl.per = max(int((longest + size - 1) / size), 1);
+            pl.per = max(int(quot(longest + size - 1, size)), 1);
         }
     }
     for (int b = blockIdx.x; b < p.B; b += grid) {
@@ -405,7 +430,8 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
         if (a.lse)
             for (int i = tid; i < a.q_heads; i += THREADS) a.lse[int64_t(p.row0 + b) * a.q_heads + i] = -INFINITY;
     }
-    const unsigned start = block_edge(pl, cum, p.B, blockIdx.x, 0), end = block_edge(pl, cum, p.B, blockIdx.x, 1);
+    unsigned start, end;
+    block_share(pl, cum, p.B, blockIdx.x, start, end);
     if (start >= end) return;
 
     // -- this warp's share -------------------------------------------------------------------------------------
@@ -830,7 +856,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     const unsigned far = __ballot_sync(0xffffffffu, seg >= 0 && s_piece[lane < 2 * W ? lane : 0].far);
     bool before_me = false, outside = false;               // the segment begins before this block's share; leaves it
     if (begins) {
-        const int b = seg / pl.HC;
+        const int b = quot(seg, pl.HC);
         const unsigned s0 = seg_start(pl, cum, b, seg - b * pl.HC);
         before_me = s0 + SETUP < start;
         outside = before_me || s0 + seg_units(cum, b) > end;
@@ -855,18 +881,21 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
         if (away) o = *reinterpret_cast<const float4 *>(p.warp_parts + (int64_t(blockIdx.x) * W + (tail >> 1)) * PF + head * PS + d);
         Triple t;
         for (int k0 = 0; k0 < n; k0 += 4) {                // the run's first piece, then one of each of the next warps
+            float mi[4], li[4];
             float4 x[4];
-            int at[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                at[k] = k0 + k ? ((p0 >> 1) + min(k0 + k, n - 1)) * 2 : p0;
-                x[k] = *reinterpret_cast<const float4 *>(smem + (at[k] >> 1) * STAGES * TILE + (head * PS + d) * 4);
+                const int at = k0 + k ? ((p0 >> 1) + min(k0 + k, n - 1)) * 2 : p0;
+                mi[k] = s_m[at][head], li[k] = s_l[at][head];
+                x[k] = *reinterpret_cast<const float4 *>(smem + (at >> 1) * STAGES * TILE + (head * PS + d) * 4);
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (k0 + k < n) t.add(s_m[at[k]][head], s_l[at[k]][head], x[k]);
+            t.add(mi, li, x, n - k0);
         }
-        if (away) t.add(s_m[tail][head], s_l[tail][head], o);
+        if (away) {
+            const float mi[1] = {s_m[tail][head]}, li[1] = {s_l[tail][head]};
+            const float4 x[1] = {o};
+            t.add(mi, li, x, 1);
+        }
         if ((outer >> p0) & 1) {
             float *dst = p.block_parts + (int64_t(blockIdx.x) * 2 + ((early >> p0) & 1 ? 0 : 1)) * PF;
             *reinterpret_cast<float4 *>(dst + head * PS + d) = t.o;
@@ -897,7 +926,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
         for (int e = tid; e < VEC; e += THREADS) {
             const int head = e / (D / 4), d = e % (D / 4) * 4;
             Triple t;
-            constexpr int LOADS = 10;                      // in flight together
+            constexpr int LOADS = 20;                      // in flight together: one round for a segment over 20 blocks
             for (int i0 = 0; i0 < count; i0 += LOADS) {
                 float mi[LOADS], li[LOADS];
                 float4 x[LOADS];
@@ -909,9 +938,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                     li[i] = __ldcg(part + NH * PS + NH + head);
                     x[i] = __ldcg(reinterpret_cast<const float4 *>(part + head * PS + d));
                 }
-#pragma unroll
-                for (int i = 0; i < LOADS; ++i)
-                    if (i0 + i < count) t.add(mi[i], li[i], x[i]);
+                t.add(mi, li, x, count - i0);
             }
             finish(pc, head, d, t);
         }
@@ -951,13 +978,14 @@ template <int KT, int D, int NT> cudaError_t run(const AttendArgs &a, cudaStream
     p.warp_parts = p.block_parts + int64_t(grid) * 2 * F::PF;
     // Rows a launch: bounded by the kernel's tables, and tile numbers stay below 2^31 whatever the lengths are.
     const int64_t most = (int64_t(a.t.max_pages) * a.pool.page_tokens + F::TOK - 1) / F::TOK + 1 + SETUP;
-    const int64_t fit = 0x7FFFFFFF / (most * HC);
+    const int64_t fit = 0x7FFF0000 / (most * HC);
     if (fit < 1) return cudaErrorNotSupported;
     int rows = MAX_SEGS / HC < MAX_ROWS ? MAX_SEGS / HC : MAX_ROWS;
     if (fit < rows) rows = int(fit);
     for (int r = 0; r < a.B; r += rows) {
         p.row0 = r;
         p.B = a.B - r < rows ? a.B - r : rows;
+        p.per_seg = grid / (p.B * HC);
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(grid);
         cfg.blockDim = dim3(F::W * 32);
