@@ -565,13 +565,27 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                         if (head < p.G) load_q<gap>(a.q, a.qdt, at + 16 * c, raw[n][c]);
                     }
                 }
+                const int64_t pos = int64_t(cc.row.len) - 1;
+                const bool turn = a.rope && pos < a.rope_rows;
+                float2 co[CH / 2][2], si[CH / 2][2];
+                if (turn) {
+                    const float *row = a.rope + pos * D + d0;
+#pragma unroll
+                    for (int c = 0; c < CH / 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            co[c][e] = __ldg(reinterpret_cast<const float2 *>(row + 16 * c + e * gap));
+                            si[c][e] = __ldg(reinterpret_cast<const float2 *>(row + D / 2 + 16 * c + e * gap));
+                        }
+                } else if (a.rope) {
+                    atomicOr(&g_fault_attend, FAULT_PAGE);
+                }
+                // The cache's copies are started behind these loads: before them, they held them up (by 2 us, of which
+                // one was lost to the copies behind).
                 if (done == 0) {
 #pragma unroll
                     for (int st = 0; st < STAGES - 1; ++st) advance(st);
                 }
-                const int64_t pos = int64_t(cc.row.len) - 1;
-                const bool turn = a.rope && pos < a.rope_rows;
-                if (a.rope && !turn) atomicOr(&g_fault_attend, FAULT_PAGE);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     m[n] = -INFINITY;
@@ -580,19 +594,14 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
 #pragma unroll
                     for (int c = 0; c < CH; ++c) convert_q(a.qdt, raw[n][c], x[c]);
                     if (turn) {
-                        const float *row = a.rope + pos * D + d0;
 #pragma unroll
                         for (int c = 0; c < CH / 2; ++c)
 #pragma unroll
-                            for (int e = 0; e < 4; e += 2) {
-                                const int d = 16 * c + (e >> 1) * gap;
-                                const float2 co = __ldg(reinterpret_cast<const float2 *>(row + d));
-                                const float2 si = __ldg(reinterpret_cast<const float2 *>(row + D / 2 + d));
-                                const float u0 = x[c][e], v0 = x[c + CH / 2][e], u1 = x[c][e + 1], v1 = x[c + CH / 2][e + 1];
-                                x[c][e] = __fsub_rn(__fmul_rn(u0, co.x), __fmul_rn(v0, si.x));
-                                x[c][e + 1] = __fsub_rn(__fmul_rn(u1, co.y), __fmul_rn(v1, si.y));
-                                x[c + CH / 2][e] = __fadd_rn(__fmul_rn(v0, co.x), __fmul_rn(u0, si.x));
-                                x[c + CH / 2][e + 1] = __fadd_rn(__fmul_rn(v1, co.y), __fmul_rn(u1, si.y));
+                            for (int e = 0; e < 4; ++e) {
+                                const float cs = e & 1 ? co[c][e >> 1].y : co[c][e >> 1].x, sn = e & 1 ? si[c][e >> 1].y : si[c][e >> 1].x;
+                                const float u = x[c][e], v = x[c + CH / 2][e];
+                                x[c][e] = __fsub_rn(__fmul_rn(u, cs), __fmul_rn(v, sn));
+                                x[c + CH / 2][e] = __fadd_rn(__fmul_rn(v, cs), __fmul_rn(u, sn));
                             }
                     }
                     float big = 0.0f;
