@@ -24,7 +24,7 @@ int64_t kv_attend_workspace(const qpack_kv_pool_t &pool, int, int q_heads) {
     if (pool.type == QPACK_KV_I8) parts = attend::workspace<QPACK_KV_I8>(pool, q_heads, grid);
     else if (pool.type == QPACK_KV_F16) parts = attend::workspace<QPACK_KV_F16>(pool, q_heads, grid);
     else parts = attend::workspace<QPACK_KV_BF16>(pool, q_heads, grid);
-    return int64_t(attend::MAX_SEGS) * 4 + parts;
+    return int64_t(attend::MAX_COUNTERS) * 4 + parts;
 }
 
 cudaError_t launch_kv_attend(const AttendArgs &a, cudaStream_t s) {

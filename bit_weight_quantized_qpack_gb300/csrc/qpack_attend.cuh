@@ -48,7 +48,7 @@ namespace qpack {
 namespace attend {
 
 constexpr int MAX_ROWS = 1024;              // rows a launch
-constexpr int MAX_SEGS = 65536;             // segments a launch: counters at the front of the workspace
+constexpr int MAX_COUNTERS = 1 << 18;       // of a launch: the front of the workspace
 constexpr float P_BIAS = 12.0f;             // probabilities are held as 2^(x - m + 12)
 
 // Shape of an instance: NT groups of eight query heads, tiles of TOK tokens, W warps, a ring of STAGES tiles each.
@@ -64,7 +64,9 @@ template <int KT, int D, int NT> struct Cfg {
     static constexpr int STAGES = 214000 / (W * TILE) > 4 ? 4 : 214000 / (W * TILE);
     static constexpr int NH = 8 * NT;
     static constexpr int PS = D + 4;                            // floats of a head in a partial, padded for the banks
-    static constexpr int PF = NH * PS + 2 * NH;                 // floats of a partial: accumulators, maxima, sums
+    static constexpr int PF = NH * PS;                          // floats of a piece's accumulators
+    static constexpr int VEC = NH * D / 4;                      // threads of a join, four accumulators each
+    static constexpr int SLICES = VEC / 32;                     // warps of a join, each on its own
     static_assert(STAGES >= 2 && PF * 4 <= STAGES * TILE, "a warp's ring holds a partial");
     static_assert(2 * W <= 32, "a lane a piece");
 };
@@ -74,8 +76,9 @@ struct Params {
     int B, C, G;                // rows of this launch, groups of query heads, query heads a key/value head
     int row0;                   // first row of this launch
     int per_seg;                // blocks a segment where there are as many blocks as segments or more, else 0
-    int *counters;              // [MAX_SEGS], zero between calls
-    float *block_parts;         // [grid][2][PF]
+    int *counters;              // [segments][SLICES], zero between calls
+    float4 *block_parts;        // [grid][2][VEC]: accumulators of a piece that leaves its block
+    float2 *block_sums;         // [grid][2][VEC]: maximum and sum, once a thread
     float *warp_parts;          // [grid][W][PF]
 };
 
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     unsigned *cum = reinterpret_cast<unsigned *>(smem + W * STAGES * TILE);  // units before row b, a segment's worth
     __shared__ Piece s_piece[2 * W];
     __shared__ float s_m[2 * W][NH], s_l[2 * W][NH];       // a piece's maxima and sums
-    __shared__ int s_run[2 * W], s_last[2];
+    __shared__ int s_run[2 * W];
     __shared__ unsigned s_max;
     const AttendArgs &a = p.a;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
@@ -384,18 +387,22 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     pdl_wait();                                            // inputs, cache and workspace may be the previous grid's
 
     // -- the rows' tiles, and this block's share of them ------------------------------------------------------
-    for (int b = tid; b < p.B; b += THREADS) {
-        const unsigned tiles = row_of<TOK>(p, b, blockIdx.x == 0 ? &g_fault_attend : nullptr).tiles;
-        cum[b + 1] = tiles ? tiles + SETUP : 0;
+    // Up to 32 rows are added up by every warp for itself (all write the same sums): no barrier before the copies.
+    if (lane < 2) s_piece[2 * w + lane].seg = -1;
+    const bool few = p.B <= 32;
+    int *fault = blockIdx.x == 0 && (w == 0 || !few) ? &g_fault_attend : nullptr;
+    if (!few) {
+        for (int b = tid; b < p.B; b += THREADS) cum[b + 1] = row_of<TOK>(p, b, fault).tiles;
+        __syncthreads();
     }
-    if (tid < 2 * W) s_piece[tid].seg = -1;
-    __syncthreads();
-    if (w == 0) {
-        unsigned carry = 0, most = 0;
+    unsigned longest = 0;                                  // tiles of the longest row
+    if (few || w == 0) {
+        unsigned carry = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const int b = b0 + lane;
-            unsigned x = b < p.B ? cum[b + 1] : 0;
-            most = max(most, x);
+            unsigned x = b >= p.B ? 0u : few ? row_of<TOK>(p, b, fault).tiles : cum[b + 1];
+            longest = max(longest, x);
+            x = x ? x + SETUP : 0u;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
@@ -405,10 +412,14 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
             if (b < p.B) cum[b + 1] = x;
             carry = __shfl_sync(0xffffffffu, x, 31);
         }
-        most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 0) cum[0] = 0, s_max = most;
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (lane == 0) cum[0] = 0, s_max = longest;
+        __syncwarp();
     }
-    __syncthreads();
+    if (!few) {
+        __syncthreads();
+        longest = s_max;
+    }
     Plan pl;
     const unsigned grid = gridDim.x;
     pl.HC = a.pool.heads * p.C;
@@ -417,7 +428,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     pl.per = 0;
     if (p.per_seg) {
         // Few segments: boundaries on theirs save the joins of the pieces, where the shares stay nearly equal.
-        const unsigned longest = s_max ? s_max - SETUP : 0, k = p.per_seg, size = max(quot(longest + k - 1, k), unsigned(W));
+        const unsigned k = p.per_seg, size = max(quot(longest + k - 1, k), unsigned(W));
         if (size <= pl.size + pl.size / 8) {
             pl.size = size;
             pl.per = max(int(quot(longest + size - 1, size)), 1);
@@ -567,8 +578,10 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                 }
                 const int64_t pos = int64_t(cc.row.len) - 1;
                 const bool turn = a.rope && pos < a.rope_rows;
+                if (a.rope && !turn) atomicOr(&g_fault_attend, FAULT_PAGE);
                 float2 co[CH / 2][2], si[CH / 2][2];
-                if (turn) {
+                auto fetch_rotation = [&] {
+                    if (!turn) return;
                     const float *row = a.rope + pos * D + d0;
 #pragma unroll
                     for (int c = 0; c < CH / 2; ++c)
@@ -577,15 +590,16 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                             co[c][e] = __ldg(reinterpret_cast<const float2 *>(row + 16 * c + e * gap));
                             si[c][e] = __ldg(reinterpret_cast<const float2 *>(row + D / 2 + 16 * c + e * gap));
                         }
-                } else if (a.rope) {
-                    atomicOr(&g_fault_attend, FAULT_PAGE);
-                }
+                };
                 // The cache's copies are started behind these loads: before them, they held them up (by 2 us, of which
-                // one was lost to the copies behind).
+                // one was lost to the copies behind). Where the registers do not hold both, the rotation comes later.
+                constexpr bool both = D * NT <= 128;
+                if (both) fetch_rotation();
                 if (done == 0) {
 #pragma unroll
                     for (int st = 0; st < STAGES - 1; ++st) advance(st);
                 }
+                if (!both) fetch_rotation();
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     m[n] = -INFINITY;
@@ -854,8 +868,8 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
 
     // -- joins ------------------------------------------------------------------------------------------------
     // Pieces in the order of their tiles, one a lane, runs of one segment among them; every warp finds the runs for
-    // itself. A run that leaves the block's share (at most two do, the first and the last) goes to the workspace, the
-    // others are finished. Of a run's pieces only the last can be far.
+    // itself. A run that leaves the block's share (the first and the last may) goes to the workspace, the others are
+    // finished. Of a run's pieces only the last can be far.
     const int seg = lane < 2 * W ? s_piece[lane].seg : -1;
     const unsigned valid = __ballot_sync(0xffffffffu, seg >= 0), below = valid & ((1u << lane) - 1u);
     if (!valid) return;
@@ -873,7 +887,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     const unsigned outer = __ballot_sync(0xffffffffu, outside), early = __ballot_sync(0xffffffffu, before_me);
     if (w == 0 && begins) s_run[__popc(starts & ((1u << lane) - 1u))] = lane;
     __syncthreads();
-    constexpr int VEC = NH * D / 4;                        // four accumulators a thread
+    constexpr int VEC = F::VEC;
     auto finish = [&](const Piece &pc, int head, int d, const Triple &t) {
         if (head >= pc.heads) return;
         const float f = inverse(t.l);
@@ -881,7 +895,9 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
         store_out<4>(a.out, a.odt, pc.out + head * D + d, x);
         if (a.lse && d == 0) a.lse[pc.lse + head] = lse_of(t.m, t.l);
     };
-    for (int i = tid; i < __popc(starts) * VEC; i += THREADS) {
+    const int todo = __popc(starts) * VEC;
+    int left_base = 0, left_n = 0;                         // lane k: where the warp's k-th part that leaves the block is
+    for (int i = tid; i < todo; i += THREADS) {
         const int p0 = s_run[i / VEC], e = i % VEC, head = e / (D / 4), d = e % (D / 4) * 4;
         const unsigned later = starts & ~((2u << p0) - 1u);
         const unsigned members = valid & ~((1u << p0) - 1u) & (later ? (later & -later) - 1u : 0xffffffffu);
@@ -905,52 +921,54 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
             const float4 x[1] = {o};
             t.add(mi, li, x, 1);
         }
-        if ((outer >> p0) & 1) {
-            float *dst = p.block_parts + (int64_t(blockIdx.x) * 2 + ((early >> p0) & 1 ? 0 : 1)) * PF;
-            *reinterpret_cast<float4 *>(dst + head * PS + d) = t.o;
-            if (d == 0) dst[NH * PS + head] = t.m, dst[NH * PS + NH + head] = t.l;
-        } else {
+        if (!((outer >> p0) & 1)) {
             finish(s_piece[p0], head, d, t);
+            continue;
         }
+        // A part for the workspace. A segment's first block has it in its second slot, the others, which begin inside the
+        // segment, in their first.
+        const int64_t mine = (int64_t(blockIdx.x) * 2 + ((early >> p0) & 1 ? 0 : 1)) * VEC + e;
+        p.block_parts[mine] = t.o;
+        p.block_sums[mine] = make_float2(t.m, t.l);
+        if (lane == left_n) left_base = i - lane;
+        ++left_n;
     }
-    const int ncross = __popc(outer);
-    if (!ncross) return;
-    __syncthreads();
-    if (tid < ncross) {
-        const int s = s_piece[tid ? 31 - __clz(outer) : __ffs(outer) - 1].seg;
-        int first, count;
+    if (!left_n) return;
+    // The segments' other blocks: each of the join's warps is on its own with its 32 x 4 accumulators of a segment. The
+    // last of the blocks' warps to arrive joins them all, in the order of the blocks.
+    __syncwarp();
+    int first = 0, count = 0;
+    bool am_last = false;
+    if (lane < left_n) {
+        const int s = s_piece[s_run[left_base / VEC]].seg;
         sharers(pl, cum, s, first, count);
-        // releases the block's partials, and acquires those of the blocks that arrived before
-        int before;
-        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.counters + s) : "memory");
-        if (before == count - 1) p.counters[s] = 0;        // ready for the next call
-        s_last[tid] = before == count - 1;
+        int *counter = p.counters + int64_t(s) * F::SLICES + left_base % VEC / 32, before;
+        // releases the warp's part, acquires those that came before
+        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+        am_last = before == count - 1;
+        if (am_last) *counter = 0;                         // ready for the next call
     }
-    __syncthreads();
-    for (int c = 0; c < ncross; ++c) {
-        if (!s_last[c]) continue;
-        const Piece &pc = s_piece[c ? 31 - __clz(outer) : __ffs(outer) - 1];
-        int first, count;
-        sharers(pl, cum, pc.seg, first, count);
-        for (int e = tid; e < VEC; e += THREADS) {
-            const int head = e / (D / 4), d = e % (D / 4) * 4;
-            Triple t;
-            constexpr int LOADS = 20;                      // in flight together: one round for a segment over 20 blocks
-            for (int i0 = 0; i0 < count; i0 += LOADS) {
-                float mi[LOADS], li[LOADS];
-                float4 x[LOADS];
+    __syncwarp();
+    for (unsigned mask = __ballot_sync(0xffffffffu, am_last); mask; mask &= mask - 1) {
+        const int from = __ffs(mask) - 1, i = __shfl_sync(0xffffffffu, left_base, from) + lane;
+        const int f0 = __shfl_sync(0xffffffffu, first, from), n = __shfl_sync(0xffffffffu, count, from);
+        const int e = i % VEC, head = e / (D / 4), d = e % (D / 4) * 4;
+        Triple t;
+        constexpr int LOADS = 20;                          // in flight together: one round for a segment over 20 blocks
+        for (int i0 = 0; i0 < n; i0 += LOADS) {
+            float mi[LOADS], li[LOADS];
+            float4 x[LOADS];
 #pragma unroll
-                for (int i = 0; i < LOADS; ++i) {
-                    if (i0 + i >= count) continue;
-                    const float *part = p.block_parts + (int64_t(first + i0 + i) * 2 + (i0 + i == 0 ? 1 : 0)) * PF;
-                    mi[i] = __ldcg(part + NH * PS + head);
-                    li[i] = __ldcg(part + NH * PS + NH + head);
-                    x[i] = __ldcg(reinterpret_cast<const float4 *>(part + head * PS + d));
-                }
-                t.add(mi, li, x, count - i0);
+            for (int k = 0; k < LOADS; ++k) {
+                if (i0 + k >= n) continue;
+                const int64_t at = (int64_t(f0 + i0 + k) * 2 + (i0 + k == 0 ? 1 : 0)) * VEC + e;
+                const float2 ml = __ldcg(p.block_sums + at);
+                mi[k] = ml.x, li[k] = ml.y;
+                x[k] = __ldcg(p.block_parts + at);
             }
-            finish(pc, head, d, t);
+            t.add(mi, li, x, n - i0);
         }
+        finish(s_piece[s_run[i / VEC]], head, d, t);
     }
 }
 
@@ -959,7 +977,7 @@ inline int groups(const qpack_kv_pool_t &pool, int q_heads) { return q_heads / p
 
 template <int KT, int D, int NT> int64_t part_bytes(int grid) {
     using F = Cfg<KT, D, NT>;
-    return int64_t(grid) * (2 + F::W) * F::PF * 4;
+    return int64_t(grid) * (2 * F::VEC * 24 + F::W * F::PF * 4);
 }
 
 template <int KT, int D, int NT> cudaError_t run(const AttendArgs &a, cudaStream_t s) {
@@ -983,13 +1001,14 @@ template <int KT, int D, int NT> cudaError_t run(const AttendArgs &a, cudaStream
     p.C = (p.G + 8 * NT - 1) / (8 * NT);
     const int HC = a.pool.heads * p.C;
     p.counters = static_cast<int *>(a.ws);
-    p.block_parts = reinterpret_cast<float *>(p.counters + MAX_SEGS);
-    p.warp_parts = p.block_parts + int64_t(grid) * 2 * F::PF;
+    p.block_parts = reinterpret_cast<float4 *>(p.counters + MAX_COUNTERS);
+    p.block_sums = reinterpret_cast<float2 *>(p.block_parts + int64_t(grid) * 2 * F::VEC);
+    p.warp_parts = reinterpret_cast<float *>(p.block_sums + int64_t(grid) * 2 * F::VEC);
     // Rows a launch: bounded by the kernel's tables, and tile numbers stay below 2^31 whatever the lengths are.
     const int64_t most = (int64_t(a.t.max_pages) * a.pool.page_tokens + F::TOK - 1) / F::TOK + 1 + SETUP;
     const int64_t fit = 0x7FFF0000 / (most * HC);
     if (fit < 1) return cudaErrorNotSupported;
-    int rows = MAX_SEGS / HC < MAX_ROWS ? MAX_SEGS / HC : MAX_ROWS;
+    int rows = MAX_COUNTERS / (HC * F::SLICES) < MAX_ROWS ? MAX_COUNTERS / (HC * F::SLICES) : MAX_ROWS;
     if (fit < rows) rows = int(fit);
     for (int r = 0; r < a.B; r += rows) {
         p.row0 = r;
