@@ -954,20 +954,26 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
         const int f0 = __shfl_sync(0xffffffffu, first, from), n = __shfl_sync(0xffffffffu, count, from);
         const int e = i % VEC, head = e / (D / 4), d = e % (D / 4) * 4;
         Triple t;
-        constexpr int LOADS = 20;                          // in flight together: one round for a segment over 20 blocks
-        for (int i0 = 0; i0 < n; i0 += LOADS) {
-            float mi[LOADS], li[LOADS];
-            float4 x[LOADS];
+        // Loads in flight together: few segments over many blocks have up to ten in a round; the usual two or three parts
+        // are not kept waiting by the longer code (1 to 3 us, mostly of fetching instructions).
+        auto gather = [&](auto loads) {
+            constexpr int L = decltype(loads)::value;
+            for (int i0 = 0; i0 < n; i0 += L) {
+                float mi[L], li[L];
+                float4 x[L];
 #pragma unroll
-            for (int k = 0; k < LOADS; ++k) {
-                if (i0 + k >= n) continue;
-                const int64_t at = (int64_t(f0 + i0 + k) * 2 + (i0 + k == 0 ? 1 : 0)) * VEC + e;
-                const float2 ml = __ldcg(p.block_sums + at);
-                mi[k] = ml.x, li[k] = ml.y;
-                x[k] = __ldcg(p.block_parts + at);
+                for (int k = 0; k < L; ++k) {
+                    if (i0 + k >= n) continue;
+                    const int64_t at = (int64_t(f0 + i0 + k) * 2 + (i0 + k == 0 ? 1 : 0)) * VEC + e;
+                    const float2 ml = __ldcg(p.block_sums + at);
+                    mi[k] = ml.x, li[k] = ml.y;
+                    x[k] = __ldcg(p.block_parts + at);
+                }
+                t.add(mi, li, x, n - i0);
             }
-            t.add(mi, li, x, n - i0);
-        }
+        };
+        if (n <= 4) gather(Int<4>());
+        else gather(Int<7>());
         finish(s_piece[s_run[i / VEC]], head, d, t);
     }
 }
