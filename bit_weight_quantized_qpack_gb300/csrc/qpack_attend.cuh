@@ -658,45 +658,47 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                 slot = slot + 1 == STAGES ? 0 : slot + 1;
 
                 // -- scores ---------------------------------------------------------------------------------
-                float sc[TT][4];
+                // The accumulators of the tile's eights of tokens (and with NT = 2 of leading terms and remainders) take
+                // turns, so that no product waits for the one before it.
+                float sc[TT][4], sl[NT == 2 ? TT : 1][4];
 #pragma unroll
-                for (int t = 0; t < TT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.0f;
+                for (int t = 0; t < TT; ++t) {
+                    sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.0f;
+                    if (NT == 2) sl[t % (NT == 2 ? TT : 1)][0] = sl[t % (NT == 2 ? TT : 1)][1] = sl[t % (NT == 2 ? TT : 1)][2] = sl[t % (NT == 2 ? TT : 1)][3] = 0.0f;
+                }
+                uint32_t sw[TT][SB ? SB / 4 : 1];
+                if (I8) {
 #pragma unroll
-                for (int u = 0; u < TOK / 16; ++u) {
-                    if (I8) {
-                        uint32_t sw[2][SB ? SB / 4 : 1];
+                    for (int t = 0; t < TT; ++t) load_words<SB ? SB : 4>(sk + (g + 8 * t) * SB, sw[t]);
+                }
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) load_words<SB ? SB : 4>(sk + (g + 8 * t + 16 * u) * SB, sw[t]);
+                for (int c = 0; c < CH; c += I8 ? 2 : 1) {
 #pragma unroll
-                        for (int c = 0; c < CH; c += 2) {
-                            uint32_t r[4];
-                            ldsm4((st + u * 16 * RB) + ((c * 16) ^ lx), r);
+                    for (int u = 0; u < TOK / 16; ++u) {
+                        uint32_t r[4];
+                        ldsm4((st + u * 16 * RB) + ((c * 16 * F::ES) ^ lx), r);
+#pragma unroll
+                        for (int v = 0; v < (I8 ? 2 : 1); ++v) {
+                            const uint32_t *q = qf[c + v];
 #pragma unroll
                             for (int t = 0; t < 2; ++t) {
-                                const uint32_t s = __byte_perm(sw[t][c / 4], 0u, (c / 2) & 1 ? 0x3232u : 0x1010u);
-#pragma unroll
-                                for (int v = 0; v < 2; ++v) {
+                                uint32_t b0 = r[t], b1 = r[2 + t];
+                                if (I8) {
+                                    const uint32_t s = __byte_perm(sw[2 * u + t][c / 4], 0u, (c / 2) & 1 ? 0x3232u : 0x1010u);
                                     const uint32_t word = r[2 * v + t] ^ 0x80808080u;
-                                    const uint32_t b0 = dequant2(word, 0x4140u, s), b1 = dequant2(word, 0x4342u, s);
-                                    const uint32_t *q = qf[c + v];
-                                    mma<KT>(sc[2 * u + t], q[0], q[1], q[2], q[3], b0, b1);
-                                    if (NT == 2) mma<KT>(sc[2 * u + t], q[4 * NT - 4], q[4 * NT - 3], q[4 * NT - 2], q[4 * NT - 1], b0, b1);
+                                    b0 = dequant2(word, 0x4140u, s), b1 = dequant2(word, 0x4342u, s);
                                 }
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < CH; ++c) {
-                            uint32_t r[4];
-                            ldsm4((st + u * 16 * RB) + ((c * 32) ^ lx), r);
-                            const uint32_t *q = qf[c];
-#pragma unroll
-                            for (int t = 0; t < 2; ++t) {
-                                mma<KT>(sc[2 * u + t], q[0], q[1], q[2], q[3], r[t], r[2 + t]);
-                                if (NT == 2) mma<KT>(sc[2 * u + t], q[4 * NT - 4], q[4 * NT - 3], q[4 * NT - 2], q[4 * NT - 1], r[t], r[2 + t]);
+                                mma<KT>(sc[2 * u + t], q[0], q[1], q[2], q[3], b0, b1);
+                                if (NT == 2) mma<KT>(sl[(2 * u + t) % (NT == 2 ? TT : 1)], q[4 * NT - 4], q[4 * NT - 3], q[4 * NT - 2], q[4 * NT - 1], b0, b1);
                             }
                         }
                     }
+                }
+                if (NT == 2) {
+#pragma unroll
+                    for (int t = 0; t < TT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[t][e] += sl[t % (NT == 2 ? TT : 1)][e];
                 }
 
                 // -- softmax --------------------------------------------------------------------------------
