@@ -632,6 +632,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                     const float f = __int_as_float((up << 23) | (__float_as_int(a.scale) & 0x80000000));
                     const float back = __int_as_float(max(254 - up, 1) << 23);
                     qs[n] = fabsf(a.scale) * 1.4426950408889634f * back * (up == 254 ? 0.5f : 1.0f);
+                    if (qs[n] == 0.0f) qs[n] = 0x1p-126f;   // a masked token's -inf stays one where the scale is 0
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
                         uint32_t h0, l0, h1, l1;

@@ -216,6 +216,14 @@ def test_attend_query_magnitudes(qpg, qscale):
     attend_case(qpg, "i8", 2, 4, 128, 16, [50, 1], qscale=qscale, scale=min(1.0, 5.0 / qscale) if qscale > 60 else None, seed=4)
 
 
+def test_attend_scale_zero(qpg):
+    """A scale of 0 (or one that vanishes beside the queries) gives the mean of the values, masked tokens left out."""
+    for kind in ("i8", "f16", "bf16"):
+        attend_case(qpg, kind, 2, 4, 128, 16, [1, 5, 16, 77, 0], scale=0.0, seed=11)
+        attend_case(qpg, kind, 2, 4, 64, 16, [1, 5, 16, 77, 0], scale=0.0, window=3, poison=True, seed=12)
+    attend_case(qpg, "i8", 2, 9, 128, 16, [33, 2], scale=1e-38, qscale=1e-30, seed=13)
+
+
 def test_attend_strided_rows(qpg):
     """q and out as slices of wider rows (a fused projection's output), 2-D and 3-D."""
     lens, H, G, D, T = [30, 75, 2], 2, 4, 64, 16
