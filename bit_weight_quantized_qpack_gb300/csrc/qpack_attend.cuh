@@ -60,7 +60,7 @@ template <int KT, int D, int NT> struct Cfg {
     static constexpr int SB = KT == QPACK_KV_I8 ? D / 16 : 0;   // bytes of its scales
     static constexpr int TOK = RB >= 256 ? 16 : 32;
     static constexpr int TILE = 2 * TOK * (RB + SB);            // keys, values, their scales
-    static constexpr int W = RB == 512 ? 6 : 8;
+    static constexpr int W = RB == 512 ? 6 : D * NT >= 256 || (KT == QPACK_KV_I8 && D == 128) ? 8 : 12;
     static constexpr int STAGES = 214000 / (W * TILE) > 4 ? 4 : 214000 / (W * TILE);
     static constexpr int NH = 8 * NT;
     static constexpr int PS = D + 4;                            // floats of a head in a partial, padded for the banks
