@@ -363,17 +363,24 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
 }
 
 // Reference counts are ranked in chunks of SCAN a thread, so that a few thousand pages are one pass of the block (a page
-// a thread took seven passes of three barriers each, 3 us, at 1600 pages). Bit i of the result: page p + i passes `test`.
+// a thread took seven passes of three barriers each, 3 us, at 1600 pages).
 constexpr int SCAN = 8;
-template <class Test> __device__ __forceinline__ unsigned pages_where(const int *refs, int64_t p, int64_t pages, Test test) {
-    unsigned m = 0;
-    int r[SCAN];
+__device__ __forceinline__ void load_refs(const int *refs, int64_t p, int64_t pages, int (&r)[SCAN]) {
 #pragma unroll
     for (int i = 0; i < SCAN; ++i) r[i] = p + i < pages ? refs[p + i] : 0;
+}
+// Bit i: page p + i exists and passes `test` of its count and number.
+template <class Test> __device__ __forceinline__ unsigned pages_where(const int (&r)[SCAN], int64_t p, int64_t pages, Test test) {
+    unsigned m = 0;
 #pragma unroll
     for (int i = 0; i < SCAN; ++i)
         if (p + i < pages && test(r[i], p + i)) m |= 1u << i;
     return m;
+}
+__device__ __forceinline__ unsigned free_pages(const int *refs, int64_t p, int64_t pages) {
+    int r[SCAN];
+    load_refs(refs, p, pages, r);
+    return pages_where(r, p, pages, [](int n, int64_t) { return n == 0; });
 }
 
 // Work of the copy kernel: rows [0, rows) of page src to page dst, in every layer.
@@ -439,7 +446,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_reserve_kernel(qpack_kv_table
     int found = 0;
     for (int64_t p0 = 0; p0 < pages && found < want; p0 += blockDim.x * SCAN) {
         const int64_t p = p0 + threadIdx.x * SCAN;
-        unsigned m = pages_where(t.refs, p, pages, [](int r, int64_t) { return r == 0; });
+        unsigned m = free_pages(t.refs, p, pages);
         int rank = found + block_scan(__popc(m), sums, &tot);
         for (; m && rank < want; m &= m - 1, ++rank) {
             int lo = 0, hi = n;                            // off[lo] <= rank < off[lo + 1]
@@ -501,7 +508,7 @@ __global__ void __launch_bounds__(256) kv_fork_kernel(qpack_kv_tables_t t, int p
         int found = 0;
         for (int64_t p0 = 0; p0 < pages && found <= before; p0 += blockDim.x * SCAN) {
             const int64_t p = p0 + threadIdx.x * SCAN;
-            unsigned m = pages_where(t.refs, p, pages, [](int r, int64_t) { return r == 0; });
+            unsigned m = free_pages(t.refs, p, pages);
             const int rank = found + block_scan(__popc(m), sums, &tot);
             if (rank <= before && before < rank + __popc(m)) {
                 for (int k = rank; k < before; ++k) m &= m - 1;
@@ -563,38 +570,46 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_compact_plan_kernel(qpack_kv_
     int tot, nlive = 0;
     pdl_launch_dependents();
     pdl_wait();
-    for (int64_t p0 = 0; p0 < pages; p0 += blockDim.x * SCAN) {
-        const unsigned m = pages_where(t.refs, p0 + threadIdx.x * SCAN, pages, [](int r, int64_t) { return r > 0; });
-        block_scan(__popc(m), sums, &tot);
+    const int64_t chunk = blockDim.x * SCAN;
+    int r[SCAN];
+    for (int64_t p0 = 0; p0 < pages; p0 += chunk) {
+        const int64_t p = p0 + threadIdx.x * SCAN;
+        load_refs(t.refs, p, pages, r);
+        block_scan(__popc(pages_where(r, p, pages, [](int n, int64_t) { return n > 0; })), sums, &tot);
         nlive += tot;
     }
     int holes = 0, movers = 0;
-    for (int64_t p0 = 0; p0 < pages; p0 += blockDim.x * SCAN) {
+    for (int64_t p0 = 0; p0 < pages; p0 += chunk) {
         const int64_t p = p0 + threadIdx.x * SCAN;
-        const unsigned hole = pages_where(t.refs, p, pages, [&](int r, int64_t q) { return r <= 0 && q < nlive; });
-        const unsigned mover = pages_where(t.refs, p, pages, [&](int r, int64_t q) { return r > 0 && q >= nlive; });
-        // both ranks in one scan: at most 2^13 of each a chunk, carried in whole numbers
+        if (pages > chunk) load_refs(t.refs, p, pages, r); // else they are there
+        const unsigned hole = pages_where(r, p, pages, [&](int n, int64_t q) { return n <= 0 && q < nlive; });
+        const unsigned mover = pages_where(r, p, pages, [&](int n, int64_t q) { return n > 0 && q >= nlive; });
+        // both ranks in one scan: at most 2^13 of each a chunk
         const int both = block_scan(__popc(hole) | __popc(mover) << 16, sums, &tot);
         int hr = holes + (both & 0xFFFF), mr = movers + (both >> 16);
         holes += tot & 0xFFFF;
         movers += tot >> 16;
-        for (unsigned m = hole; m; m &= m - 1) w.items[hr++].dst = int(p) + __ffs(m) - 1;
-        for (unsigned m = mover; m; m &= m - 1) w.items[mr++].src = int(p) + __ffs(m) - 1;
 #pragma unroll
         for (int i = 0; i < SCAN; ++i) {
             if (p + i >= pages) break;
             w.map[p + i] = int(p + i);
-            if (!((hole | mover) >> i & 1)) refs_out[p + i] = p + i < nlive ? t.refs[p + i] : 0;
+            if (hole >> i & 1) {
+                w.items[hr++].dst = int(p + i);            // its count comes from the page that moves here
+            } else if (mover >> i & 1) {
+                w.items[mr].src = int(p + i);
+                w.items[mr++].rows = r[i];                 // the count, until the lists are matched
+                refs_out[p + i] = 0;
+            } else {
+                refs_out[p + i] = p + i < nlive ? r[i] : 0;
+            }
         }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < movers; i += blockDim.x) {
-        const int a = w.items[i].src, b = w.items[i].dst;
+        const CopyItem it = w.items[i];
         w.items[i].rows = page_tokens;
-        w.map[a] = b;
-        const int r = t.refs[a];
-        refs_out[a] = 0;
-        refs_out[b] = r;
+        w.map[it.src] = it.dst;
+        refs_out[it.dst] = it.rows;
     }
     if (threadIdx.x == 0) {
         w.count[0] = movers;
