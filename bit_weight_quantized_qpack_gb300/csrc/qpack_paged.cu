@@ -97,7 +97,7 @@ template <int DT> __device__ __forceinline__ void convert(const Raw<DT> &r, floa
 // The rotation's partner (i +- D/2) is D/16 lanes away, and the four lanes of a 32-element group reduce its maximum
 // with two shuffles.
 template <int KT, int D, int DT>
-__global__ void __launch_bounds__(ROW_WARPS * 32, KT == QPACK_KV_I8 || DT == DT_F32 ? 5 : 8) kv_append_kernel(AppendArgs a, int64_t first, unsigned items, unsigned groups) {
+__global__ void __launch_bounds__(ROW_WARPS * 32, KT == QPACK_KV_I8 || DT == DT_F32 ? 5 : 7) kv_append_kernel(AppendArgs a, int64_t first, unsigned items, unsigned groups) {
     constexpr int LPR = D / 8, RPW = 32 / LPR, U = ROW_U;
     const int lane = threadIdx.x & 31, sub = lane % LPR, H = a.pool.heads;
     pdl_launch_dependents();

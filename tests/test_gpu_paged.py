@@ -542,6 +542,39 @@ def test_page_operators_random_walk(qpg, kind, layers, H, T, D, P, S, MP, pad):
         same_state(qpg, pool, tables, sim)
 
 
+def test_page_operators_many_pages(qpg):
+    """More pages than one pass of the planning blocks ranks, and free pages that lie behind the first pass."""
+    P, S, MP, T = 20011, 40, 900, 1
+    pool = make_pool(qpg, "i8", 1, P, 1, T, 64, 1)
+    tables = qpg.alloc_kv_tables(S, MP, P)
+    ws = qpg.alloc_kv_page_workspace(pool, tables)
+    sim = ref.Pages(S, MP, P, T, token_view(pool))
+    i32 = lambda a: torch.tensor(list(a), dtype=torch.int32, device="cuda")  # noqa: E731
+    rng = np.random.default_rng(3)
+    for step in range(4):
+        seqs, add = list(range(S)), rng.integers(0, 400, S).tolist()
+        qpg.qpack_kv_reserve(pool, tables, i32(seqs), i32(add))
+        sim.reserve(seqs, add)
+        same_state(qpg, pool, tables, sim)
+        gone = rng.permutation(S)[:S // 3].tolist()
+        qpg.qpack_kv_free(tables, i32(gone))
+        sim.free(gone)
+        parents = [s for s in range(S) if s not in gone]
+        src, dst = [parents[i % 5] for i in range(len(gone))], gone
+        qpg.qpack_kv_fork(pool, tables, i32(src), i32(dst), workspace=ws)
+        sim.fork(src, dst)
+        same_state(qpg, pool, tables, sim)
+    qpg.qpack_kv_free(tables, i32(range(0, S, 2)))
+    sim.free(range(0, S, 2))
+    moved = torch.zeros(1, dtype=torch.int32, device="cuda")
+    qpg.qpack_kv_compact(pool, tables, moved=moved, workspace=ws)
+    assert sim.compact() == int(moved) > 0
+    same_state(qpg, pool, tables, sim)
+    qpg.qpack_kv_reserve(pool, tables, i32([0]), i32([MP]))  # and from behind the live pages
+    sim.reserve([0], [MP])
+    same_state(qpg, pool, tables, sim)
+
+
 def test_compact_out_of_place(qpg):
     pool = make_pool(qpg, "f16", 2, 30, 2, 8, 64, 1)
     refs = torch.zeros(30, dtype=torch.int32, device="cuda")
