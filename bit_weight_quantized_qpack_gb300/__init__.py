@@ -21,6 +21,7 @@ F32, F16, BF16 = 0, 1, 2
 FLAG_RANGE = 1
 FAULT_NONFINITE_X = 16
 FAULT_PAGE, FAULT_NO_PAGES = 32, 64
+KV_ATTEND_ZEROED = 1 << 20
 KV_I8, KV_F16, KV_BF16 = 0, 1, 2
 # (sub-blocks per super-block, asymmetric) for the super-block formats
 _SB = {Q2S: (16, True), Q3S: (16, False), Q5S: (8, True), Q6S: (16, False)}
@@ -477,11 +478,13 @@ def qpack_kv_read(pool, layer, tables, seqs=None, pos=None, k_out=None, v_out=No
 
 
 class KVWorkspace:
-    """Scratch memory of a call, laid out once. Attention's is zeroed here and left ready by every call; calls that may
-    run at the same time need one each."""
+    """Scratch memory of a call, laid out once, its first `zeroed` bytes zeroed: attention counts in them, and every
+    call leaves them as it found them. Calls that may run at the same time need a workspace each."""
 
-    def __init__(self, bytes, device):
-        self.buffer = torch.zeros(bytes, dtype=torch.uint8, device=device)
+    def __init__(self, bytes, device, zeroed=0):
+        self.buffer = torch.empty(bytes, dtype=torch.uint8, device=device)
+        if zeroed:
+            self.buffer[:zeroed].zero_()
         self._p = _addr(self.buffer)
         self.bytes = bytes
 
@@ -492,7 +495,7 @@ def alloc_kv_workspace(pool, batch, q_heads) -> KVWorkspace:
     rc = (_lib or lib()).qpack_kv_attend_workspace(pool._ref, batch, q_heads, ctypes.byref(n))
     if rc:
         _check(rc, "qpack_kv_attend_workspace")
-    return KVWorkspace(n.value, pool.k.device)
+    return KVWorkspace(n.value, pool.k.device, KV_ATTEND_ZEROED)
 
 
 def alloc_kv_page_workspace(pool, tables) -> KVWorkspace:

@@ -48,7 +48,7 @@ namespace qpack {
 namespace attend {
 
 constexpr int MAX_ROWS = 1024;              // rows a launch
-constexpr int MAX_COUNTERS = 1 << 18;       // of a launch: the front of the workspace
+constexpr int MAX_COUNTERS = QPACK_KV_ATTEND_ZEROED / 4;    // of a launch: the front of the workspace
 constexpr float P_BIAS = 12.0f;             // probabilities are held as 2^(x - m + 12)
 
 // Shape of an instance: NT groups of eight query heads, tiles of TOK tokens, W warps, a ring of STAGES tiles each.
@@ -211,7 +211,8 @@ template <int N> __device__ __forceinline__ void store_out(void *p, int dt, int6
 #pragma unroll
     for (int e = 0; e < N; ++e) h[e] = dt == DT_F16 ? f2h_bits(x[e]) : __bfloat16_as_ushort(__float2bfloat16_rn(x[e]));
     uint16_t *o = static_cast<uint16_t *>(p) + i;
-    if (N == 4) *reinterpret_cast<uint2 *>(o) = make_uint2(h[0] | uint32_t(h[1 % N]) << 16, h[2 % N] | uint32_t(h[3 % N]) << 16);
+    if (N == 4)
+        *reinterpret_cast<uint2 *>(o) = make_uint2(h[0] | uint32_t(h[1 % N]) << 16, h[2 % N] | uint32_t(h[3 % N]) << 16);
     else if (N == 2) *reinterpret_cast<uint32_t *>(o) = h[0] | uint32_t(h[1 % N]) << 16;
     else *o = h[0];
 }
@@ -270,7 +271,8 @@ __device__ __forceinline__ unsigned seg_units(const unsigned *cum, int b) { retu
 __device__ __forceinline__ unsigned seg_start(const Plan &pl, const unsigned *cum, int b, int hc) {
     return cum[b] * pl.HC + hc * seg_units(cum, b);
 }
-__device__ __forceinline__ void block_share(const Plan &pl, const unsigned *cum, int B, int i, unsigned &start, unsigned &end) {
+__device__ __forceinline__ void block_share(const Plan &pl, const unsigned *cum, int B, int i, unsigned &start,
+                                            unsigned &end) {
     if (!pl.per) {
         start = min(unsigned(i) * pl.size, pl.total), end = min(start + pl.size, pl.total);
         return;
@@ -304,7 +306,8 @@ struct Cursor {
     Row row;
 };
 // The first tile at or behind a unit that is not behind the last one.
-template <int TOK> __device__ __forceinline__ void seek(const Params &p, const Plan &pl, const unsigned *cum, unsigned unit, Cursor &c) {
+template <int TOK>
+__device__ __forceinline__ void seek(const Params &p, const Plan &pl, const unsigned *cum, unsigned unit, Cursor &c) {
     int lo = 0, hi = p.B;                                  // cum[lo] HC <= unit < cum[hi] HC
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -320,7 +323,8 @@ template <int TOK> __device__ __forceinline__ void seek(const Params &p, const P
     c.q = c.hc - c.h * p.C;
 }
 // The next segment; there is one.
-template <int TOK> __device__ __forceinline__ void next_segment(const Params &p, const Plan &pl, const unsigned *cum, Cursor &c) {
+template <int TOK>
+__device__ __forceinline__ void next_segment(const Params &p, const Plan &pl, const unsigned *cum, Cursor &c) {
     c.ti = 0;
     ++c.hc;
     if (++c.q == p.C) c.q = 0, ++c.h;
@@ -343,7 +347,8 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 struct Triple {
     float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    template <int N> __device__ __forceinline__ void add(const float (&mi)[N], const float (&li)[N], const float4 (&x)[N], int n) {
+    template <int N>
+    __device__ __forceinline__ void add(const float (&mi)[N], const float (&li)[N], const float4 (&x)[N], int n) {
         float top = m;
 #pragma unroll
         for (int i = 0; i < N; ++i) top = i < n ? fmaxf(top, mi[i]) : top;
@@ -355,7 +360,8 @@ struct Triple {
             if (i >= n) continue;
             const float h = ex2(mi[i] - base);
             l = fmaf(li[i], h, l);
-            o.x = fmaf(x[i].x, h, o.x), o.y = fmaf(x[i].y, h, o.y), o.z = fmaf(x[i].z, h, o.z), o.w = fmaf(x[i].w, h, o.w);
+            o.x = fmaf(x[i].x, h, o.x), o.y = fmaf(x[i].y, h, o.y);
+            o.z = fmaf(x[i].z, h, o.z), o.w = fmaf(x[i].w, h, o.w);
         }
     }
 };
@@ -437,7 +443,8 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     for (int b = blockIdx.x; b < p.B; b += grid) {
         if (cum[b + 1] != cum[b]) continue;                // an empty row
         const float zero = 0.0f;
-        for (int i = tid; i < a.q_heads * D; i += THREADS) store_out<1>(a.out, a.odt, int64_t(p.row0 + b) * a.ldo + i, &zero);
+        for (int i = tid; i < a.q_heads * D; i += THREADS)
+            store_out<1>(a.out, a.odt, int64_t(p.row0 + b) * a.ldo + i, &zero);
         if (a.lse)
             for (int i = tid; i < a.q_heads; i += THREADS) a.lse[int64_t(p.row0 + b) * a.q_heads + i] = -INFINITY;
     }
@@ -612,7 +619,8 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                         for (int c = 0; c < CH / 2; ++c)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const float cs = e & 1 ? co[c][e >> 1].y : co[c][e >> 1].x, sn = e & 1 ? si[c][e >> 1].y : si[c][e >> 1].x;
+                                const float cs = e & 1 ? co[c][e >> 1].y : co[c][e >> 1].x;
+                                const float sn = e & 1 ? si[c][e >> 1].y : si[c][e >> 1].x;
                                 const float u = x[c][e], v = x[c + CH / 2][e];
                                 x[c][e] = __fsub_rn(__fmul_rn(u, cs), __fmul_rn(v, sn));
                                 x[c + CH / 2][e] = __fadd_rn(__fmul_rn(v, cs), __fmul_rn(u, sn));
@@ -638,12 +646,10 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                         uint32_t h0, l0, h1, l1;
                         split2<KT>(x[c][0] * f, x[c][1] * f, h0, l0);
                         split2<KT>(x[c][2] * f, x[c][3] * f, h1, l1);
-                        if (NT == 1) {
+                        if constexpr (NT == 1)
                             qf[c][0] = h0, qf[c][1] = l0, qf[c][2] = h1, qf[c][3] = l1;
-                        } else {
-                            qf[c][n] = h0, qf[c][2 + n] = h1;
-                            qf[c][4 * (NT - 1) + n] = l0, qf[c][4 * (NT - 1) + 2 + n] = l1;
-                        }
+                        else
+                            qf[c][n] = h0, qf[c][2 + n] = h1, qf[c][4 + n] = l0, qf[c][6 + n] = l1;
 #pragma unroll
                         for (int r = 0; r < 4; ++r) acc[c][n][r] = 0.0f;
                     }
@@ -661,12 +667,11 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                 // -- scores ---------------------------------------------------------------------------------
                 // The accumulators of the tile's eights of tokens (and with NT = 2 of leading terms and remainders) take
                 // turns, so that no product waits for the one before it.
-                float sc[TT][4], sl[NT == 2 ? TT : 1][4];
+                float sc[TT][4], sl[TT][4];
 #pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.0f;
-                    if (NT == 2) sl[t % (NT == 2 ? TT : 1)][0] = sl[t % (NT == 2 ? TT : 1)][1] = sl[t % (NT == 2 ? TT : 1)][2] = sl[t % (NT == 2 ? TT : 1)][3] = 0.0f;
-                }
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[t][e] = sl[t][e] = 0.0f;
                 uint32_t sw[TT][SB ? SB / 4 : 1];
                 if (I8) {
 #pragma unroll
@@ -684,22 +689,23 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
 #pragma unroll
                             for (int t = 0; t < 2; ++t) {
                                 uint32_t b0 = r[t], b1 = r[2 + t];
-                                if (I8) {
-                                    const uint32_t s = __byte_perm(sw[2 * u + t][c / 4], 0u, (c / 2) & 1 ? 0x3232u : 0x1010u);
+                                if constexpr (I8) {
+                                    const uint32_t odd = (c / 2) & 1 ? 0x3232u : 0x1010u;
+                                    const uint32_t s = __byte_perm(sw[2 * u + t][c / 4], 0u, odd);
                                     const uint32_t word = r[2 * v + t] ^ 0x80808080u;
                                     b0 = dequant2(word, 0x4140u, s), b1 = dequant2(word, 0x4342u, s);
                                 }
                                 mma<KT>(sc[2 * u + t], q[0], q[1], q[2], q[3], b0, b1);
-                                if (NT == 2) mma<KT>(sl[(2 * u + t) % (NT == 2 ? TT : 1)], q[4 * NT - 4], q[4 * NT - 3], q[4 * NT - 2], q[4 * NT - 1], b0, b1);
+                                if constexpr (NT == 2) mma<KT>(sl[2 * u + t], q[4], q[5], q[6], q[7], b0, b1);
                             }
                         }
                     }
                 }
-                if (NT == 2) {
+                if constexpr (NT == 2) {
 #pragma unroll
                     for (int t = 0; t < TT; ++t)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[t][e] += sl[t % (NT == 2 ? TT : 1)][e];
+                        for (int e = 0; e < 4; ++e) sc[t][e] += sl[t][e];
                 }
 
                 // -- softmax --------------------------------------------------------------------------------
@@ -858,8 +864,9 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                 }
                 if (lane == 0) {
                     const int head = cc.h * p.G + cc.q * NH;
-                    s_piece[at] = {int64_t(p.row0 + cc.b) * a.ldo + int64_t(head) * D, int64_t(p.row0 + cc.b) * a.q_heads + head,
-                                   cc.b * pl.HC + cc.hc, min(NH, p.G - cc.q * NH), last ? 0 : 1};
+                    s_piece[at] = {int64_t(p.row0 + cc.b) * a.ldo + int64_t(head) * D,
+                                   int64_t(p.row0 + cc.b) * a.q_heads + head, cc.b * pl.HC + cc.hc,
+                                   min(NH, p.G - cc.q * NH), last ? 0 : 1};
                 }
             }
             done += count;
@@ -906,7 +913,10 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
         const unsigned members = valid & ~((1u << p0) - 1u) & (later ? (later & -later) - 1u : 0xffffffffu);
         const int tail = 31 - __clz(members), away = (far >> tail) & 1, n = __popc(members) - away;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (away) o = *reinterpret_cast<const float4 *>(p.warp_parts + (int64_t(blockIdx.x) * W + (tail >> 1)) * PF + head * PS + d);
+        if (away) {
+            const float *far_part = p.warp_parts + (int64_t(blockIdx.x) * W + (tail >> 1)) * PF;
+            o = *reinterpret_cast<const float4 *>(far_part + head * PS + d);
+        }
         Triple t;
         for (int k0 = 0; k0 < n; k0 += 4) {                // the run's first piece, then one of each of the next warps
             float mi[4], li[4];
@@ -1044,30 +1054,30 @@ template <int KT> cudaError_t launch(const AttendArgs &a, cudaStream_t s);
 template <int KT> int64_t workspace(const qpack_kv_pool_t &pool, int q_heads, int grid);
 template <int KT> cudaError_t fetch_fault(int32_t *flags);
 
-#define QPACK_ATTEND_TYPE(KT)                                                                                            \
-    namespace qpack {                                                                                                    \
-    namespace attend {                                                                                                   \
-    template <> cudaError_t launch<KT>(const AttendArgs &a, cudaStream_t s) {                                            \
-        const int nt = groups(a.pool, a.q_heads);                                                                        \
-        if (a.pool.dim == 64) return nt == 2 ? run<KT, 64, 2>(a, s) : run<KT, 64, 1>(a, s);                              \
-        if (a.pool.dim == 128) return nt == 2 ? run<KT, 128, 2>(a, s) : run<KT, 128, 1>(a, s);                           \
-        return run<KT, 256, 1>(a, s);                                                                                    \
-    }                                                                                                                    \
-    template <> int64_t workspace<KT>(const qpack_kv_pool_t &pool, int q_heads, int grid) {                              \
-        const int nt = groups(pool, q_heads);                                                                            \
-        if (pool.dim == 64) return nt == 2 ? part_bytes<KT, 64, 2>(grid) : part_bytes<KT, 64, 1>(grid);                  \
-        if (pool.dim == 128) return nt == 2 ? part_bytes<KT, 128, 2>(grid) : part_bytes<KT, 128, 1>(grid);               \
-        return part_bytes<KT, 256, 1>(grid);                                                                             \
-    }                                                                                                                    \
-    template <> cudaError_t fetch_fault<KT>(int32_t * flags) {                                                           \
-        int v = 0;                                                                                                       \
-        const cudaError_t e = cudaMemcpyFromSymbol(&v, g_fault_attend, sizeof(int));                                     \
-        if (e != cudaSuccess) return e;                                                                                  \
-        *flags |= v;                                                                                                     \
-        const int zero = 0;                                                                                              \
-        return cudaMemcpyToSymbol(g_fault_attend, &zero, sizeof(int));                                                   \
-    }                                                                                                                    \
-    }                                                                                                                    \
+#define QPACK_ATTEND_TYPE(KT)                                                                                         \
+    namespace qpack {                                                                                                 \
+    namespace attend {                                                                                                \
+    template <> cudaError_t launch<KT>(const AttendArgs &a, cudaStream_t s) {                                         \
+        const int nt = groups(a.pool, a.q_heads);                                                                     \
+        if (a.pool.dim == 64) return nt == 2 ? run<KT, 64, 2>(a, s) : run<KT, 64, 1>(a, s);                           \
+        if (a.pool.dim == 128) return nt == 2 ? run<KT, 128, 2>(a, s) : run<KT, 128, 1>(a, s);                        \
+        return run<KT, 256, 1>(a, s);                                                                                 \
+    }                                                                                                                 \
+    template <> int64_t workspace<KT>(const qpack_kv_pool_t &pool, int q_heads, int grid) {                           \
+        const int nt = groups(pool, q_heads);                                                                         \
+        if (pool.dim == 64) return nt == 2 ? part_bytes<KT, 64, 2>(grid) : part_bytes<KT, 64, 1>(grid);               \
+        if (pool.dim == 128) return nt == 2 ? part_bytes<KT, 128, 2>(grid) : part_bytes<KT, 128, 1>(grid);            \
+        return part_bytes<KT, 256, 1>(grid);                                                                          \
+    }                                                                                                                 \
+    template <> cudaError_t fetch_fault<KT>(int32_t * flags) {                                                        \
+        int v = 0;                                                                                                    \
+        const cudaError_t e = cudaMemcpyFromSymbol(&v, g_fault_attend, sizeof(int));                                  \
+        if (e != cudaSuccess) return e;                                                                               \
+        *flags |= v;                                                                                                  \
+        const int zero = 0;                                                                                           \
+        return cudaMemcpyToSymbol(g_fault_attend, &zero, sizeof(int));                                                \
+    }                                                                                                                 \
+    }                                                                                                                 \
     }
 
 }  // namespace attend

@@ -270,9 +270,10 @@ int qpack_kv_read(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_
  *  out   [B, ldo] of dtype odt, 16-byte aligned, ldo >= q_heads * dim and a multiple of 8
  *  lse   [B, q_heads] fp32, or NULL
  *  ws    workspace of at least the bytes that qpack_kv_attend_workspace gives on this device, 16-byte aligned,
- *        zeroed once before its first use. Each call leaves it ready for the next, of any shape that it is large
+ *        its first QPACK_KV_ATTEND_ZEROED bytes zeroed once before its first use. Each call leaves it ready for the next, of any shape that it is large
  *        enough for; calls that may run at the same time need a workspace each.
  *  B     at most 4096. Results do not depend on the order in which blocks run. */
+#define QPACK_KV_ATTEND_ZEROED (1 << 20)
 int qpack_kv_attend(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_t *t, const int32_t *seqs, int B,
                     const void *q, int qdt, int64_t ldq, int q_heads, float scale, int64_t window, const float *rope,
                     int64_t rope_rows, void *out, int odt, int64_t ldo, float *lse, void *ws, int64_t ws_bytes,
