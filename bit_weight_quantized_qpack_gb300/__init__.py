@@ -439,8 +439,8 @@ def qpack_kv_append(pool, layer, tables, k, v, seqs=None, pos=None, rope=None, s
     _need_i32(seqs, "seqs", n)
     _need_i32(pos, "pos", n)
     rows = _need_rope(rope, pool.dim)
-    rc = (_lib or lib()).qpack_kv_append(pool._ref, layer, tables._ref, _addr(seqs), _addr(pos), n, _addr(k), _addr(v), dt, ldk, ldv,
-          _addr(rope), rows, _raw_stream(stream))
+    rc = (_lib or lib()).qpack_kv_append(pool._ref, layer, tables._ref, _addr(seqs), _addr(pos), n, _addr(k), _addr(v),
+                                         dt, ldk, ldv, _addr(rope), rows, _raw_stream(stream))
     if rc:
         _check(rc, "qpack_kv_append")
 
@@ -470,8 +470,8 @@ def qpack_kv_read(pool, layer, tables, seqs=None, pos=None, k_out=None, v_out=No
             raise QpackError("k_out, v_out: expected the same type")
     _need_i32(seqs, "seqs", n)
     _need_i32(pos, "pos", n)
-    rc = (_lib or lib()).qpack_kv_read(pool._ref, layer, tables._ref, _addr(seqs), _addr(pos), n, _addr(k_out), _addr(v_out),
-          dv if dk is None else dk, ldk, ldv, _raw_stream(stream))
+    rc = (_lib or lib()).qpack_kv_read(pool._ref, layer, tables._ref, _addr(seqs), _addr(pos), n, _addr(k_out),
+                                       _addr(v_out), dv if dk is None else dk, ldk, ldv, _raw_stream(stream))
     if rc:
         _check(rc, "qpack_kv_read")
     return k_out, v_out
@@ -509,8 +509,8 @@ def alloc_kv_page_workspace(pool, tables) -> KVWorkspace:
 
 def qpack_kv_attend(pool, layer, tables, q, seqs=None, scale=None, window=0, rope=None, out=None, lse=None,
                     workspace=None, stream=None):
-    """Attention of one new token a row: q [B, q_heads, dim] or [B, q_heads * dim] (float32, float16 or bfloat16) over the
-    cache of sequence seqs[b] (default b), its last `window` tokens where that is not 0. scale defaults to dim ** -0.5.
+    """Attention of one new token a row: q [B, q_heads, dim] or [B, q_heads * dim] (float32, float16 or bfloat16) over
+    the cache of sequence seqs[b] (default b), its last `window` tokens where that is not 0. scale defaults to dim ** -0.5.
     Returns out, of q's shape, float16 unless given (float32 and bfloat16 too); lse, a float32 [B, q_heads] tensor if
     wanted, gets the log-sum-exp. A kept workspace (alloc_kv_workspace) saves its allocation."""
     D = pool.dim
@@ -532,8 +532,8 @@ def qpack_kv_attend(pool, layer, tables, q, seqs=None, scale=None, window=0, rop
         workspace = alloc_kv_workspace(pool, B, q_heads)
     rows = _need_rope(rope, D)
     rc = (_lib or lib()).qpack_kv_attend(pool._ref, layer, tables._ref, _addr(seqs), B, _addr(q), qdt, ldq, q_heads,
-          D ** -0.5 if scale is None else scale, window, _addr(rope), rows, _addr(out), odt, ldo, _addr(lse), workspace._p,
-          workspace.bytes, _raw_stream(stream))
+                                         D ** -0.5 if scale is None else scale, window, _addr(rope), rows, _addr(out),
+                                         odt, ldo, _addr(lse), workspace._p, workspace.bytes, _raw_stream(stream))
     if rc:
         _check(rc, "qpack_kv_attend")
     return out
@@ -563,8 +563,8 @@ def qpack_kv_fork(pool, tables, src, dst, workspace=None, stream=None):
     _need_i32(src, "src", n)
     _need_i32(dst, "dst", n)
     workspace = alloc_kv_page_workspace(pool, tables) if workspace is None else workspace
-    rc = (_lib or lib()).qpack_kv_fork(pool._ref, tables._ref, _addr(src), _addr(dst), n, workspace._p, workspace.bytes,
-          _raw_stream(stream))
+    rc = (_lib or lib()).qpack_kv_fork(pool._ref, tables._ref, _addr(src), _addr(dst), n, workspace._p,
+                                       workspace.bytes, _raw_stream(stream))
     if rc:
         _check(rc, "qpack_kv_fork")
 
@@ -591,8 +591,8 @@ def qpack_kv_compact(pool, tables, tables_out=None, refs_out=None, moved=None, w
     _need(refs_out, torch.int32, "refs_out", numel=tables.refs.numel())
     _need_i32(moved, "moved", 1)
     workspace = alloc_kv_page_workspace(pool, tables) if workspace is None else workspace
-    rc = (_lib or lib()).qpack_kv_compact(pool._ref, tables._ref, _addr(tables_out), _addr(refs_out), _addr(moved), workspace._p,
-          workspace.bytes, _raw_stream(stream))
+    rc = (_lib or lib()).qpack_kv_compact(pool._ref, tables._ref, _addr(tables_out), _addr(refs_out), _addr(moved),
+                                          workspace._p, workspace.bytes, _raw_stream(stream))
     if rc:
         _check(rc, "qpack_kv_compact")
     return tables_out, refs_out

@@ -5,13 +5,20 @@
 // scale log2 e, m' = max(m, x_t), l' = l 2^(m - m') + 2^(x_t - m'), o' = o 2^(m - m') + 2^(x_t - m') v'_t; out = o / l.
 // Triples (m, l, o) over parts of a sequence join by the same rule, in any grouping; here always in a fixed order.
 //
-// What bounds it. Every cached byte is read once: 2 (D + D/16) bytes a token and key/value head in 8 bits, 12.2 clocks
-// of an SM's share of the copy rate at D = 128. The two products take 4 D flops a token and query head, too much for
-// the CUDA cores with eight heads a key head (2048 FMAs against 1560 issue slots in those 12.2 clocks) and 1% of the
-// tensor cores' rate. A query block has 1 to 16 rows where tcgen05.mma has at least 64, and its accumulators would
-// have to come back from TMEM for every tile's softmax, so the products run on the warp-level mma.sync (m16n8k16):
-// its fragments are registers, the softmax needs no exchange but two shuffles, and 32 instructions per 16 tokens fit
-// the budget.
+// What bounds it. Every cached byte is read once: 2 (D + D/16) bytes a token and key/value head in 8 bits, at D = 128
+// 12.6 clocks of an SM's share of the copy rate (6787 GB/s over 152 SMs at 2.07 GHz). The two products take 4 D flops a
+// token and query head, too much for the CUDA cores with eight heads a key head (2048 FMAs against 1610 issue slots in
+// those 12.6 clocks). A query block has 1 to 16 rows where tcgen05.mma has at least 64, and its accumulators would have
+// to come back from TMEM for every tile's softmax, so the products run on the warp-level mma.sync (m16n8k16): its
+// fragments are registers, the softmax needs no exchange but two shuffles, and 32 instructions per 16 tokens keep the
+// tensor pipe 30% busy. Unpacking the 8-bit cache is the largest part of the instructions (14 of some 23 a token and
+// warp), and they are issued on half of the cycles.
+//
+// Measured: 64 sequences of 4096 to 8192 tokens, 64 query heads over 8, 8 bits: 138.8 us = 6190 GB/s, 91% of the copy
+// rate; one sequence of 131071 tokens, 32 over 8: 52.6 us = 80%. What is left there is some 10 us a call, whatever its
+// size: 2 us until the first copies start (lengths, then pages: dependent loads), 2 to 4 us by which the slowest SM ends
+// after the middle one, 3 us for the joins of blocks, the launch. A row of 97 tokens takes 7 us. Sixteen query heads a
+// key head are bound by the instructions instead (62% of the copy rate).
 //
 //   S = Q K^T:     A = queries (16 rows), B = 16 tokens x D. With up to eight query heads rows 0-7 hold the queries'
 //                  leading 16-bit terms and rows 8-15 the remainders of the same heads, so one instruction takes both
@@ -29,13 +36,13 @@
 // element. ldmatrix moves pairs of bytes as 16-bit elements: for keys the four bytes of a thread are four consecutive
 // d (the queries' fragments use the same order of d), for values two d of two tokens.
 //
-// Work is cut by tiles of 16 or 32 tokens, not by rows: lengths are known on the device only and may be anything, so each
-// block adds up the rows' tiles and takes an equal share of all of them (consecutive tiles, through as many segments
-// (row, key/value head, group of query heads) as it covers), and each of its warps an equal share of the block's. A
-// warp owns a ring of cp.async stages and never waits for another warp until its share is done. A segment inside one
-// warp's share is finished by that warp; one inside a block's share is joined in shared memory; one that spans blocks
-// goes through the workspace, and the last block to arrive joins it. Where the segments are few and equally long, block
-// boundaries are put on theirs.
+// Work is cut by tiles of 16 or 32 tokens, not by rows: lengths are known on the device only and may be anything, so
+// each block adds up the rows' tiles and takes an equal share of all of them (consecutive tiles, through as many
+// segments (row, key/value head, group of query heads) as it covers), and each of its warps an equal share of the
+// block's. A warp owns a ring of cp.async stages and never waits for another warp until its share is done. A segment
+// inside one warp's share is finished by that warp; one inside a block's share is joined in shared memory; one that
+// spans blocks goes through the workspace, and the last block's warps to arrive join it. Where the segments are few and
+// equally long, block boundaries are put on theirs.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -52,8 +59,11 @@ constexpr int MAX_COUNTERS = QPACK_KV_ATTEND_ZEROED / 4;    // of a launch: the 
 constexpr float P_BIAS = 12.0f;             // probabilities are held as 2^(x - m + 12)
 
 // Shape of an instance: NT groups of eight query heads, tiles of TOK tokens, W warps, a ring of STAGES tiles each.
-// Accumulators and query fragments take D NT / 4 registers a thread each, so they decide W; shared memory decides TOK
-// and the stages.
+// Accumulators and query fragments take D NT / 4 registers a thread each, so they bound W; shared memory bounds TOK and
+// the stages. Measured (one block an SM throughout; us for one sequence of 131071 tokens / 64 of 4096 to 8192, 8 bits,
+// D = 128): 8 warps x 32 tokens 54.9 / 141.3, 12 x 32 57.0 / 141.0, 10 x 32 59.5 / 151, 12 x 16 59.7 / 146, 16 x 16
+// 60.9 / 147; two blocks of 4 warps an SM 57.9 / 140.7 where one of 8 had come to 52.3 / 136.8. At D = 64 and in 16 bits
+// at 128 twelve warps are up to 10% faster than eight on long caches (62 against 68 us) and 2% slower on short ones.
 template <int KT, int D, int NT> struct Cfg {
     static constexpr int ES = KT == QPACK_KV_I8 ? 1 : 2;
     static constexpr int RB = D * ES;                           // bytes of a token's row
@@ -98,7 +108,9 @@ template <int N> __device__ __forceinline__ void cp_small(uint32_t dst, const vo
                      "r"(ok ? N : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t *r) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -111,7 +123,8 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t *r) {
 
 // c += a b, m16n8k16, fp16 or bf16 operands.
 template <int KT>
-__device__ __forceinline__ void mma(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
     if (KT == QPACK_KV_BF16)
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                      "{%0, %1, %2, %3};"
@@ -992,7 +1005,11 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
 }
 
 // -- host -------------------------------------------------------------------------------------------------------
-inline int groups(const qpack_kv_pool_t &pool, int q_heads) { return q_heads / pool.heads > 8 && pool.dim <= 128 ? 2 : 1; }
+// Groups of eight query heads a block takes together: two where a key head has more than eight and the registers hold
+// both (at 256 they do not: the cache is then read once a group).
+inline int groups(const qpack_kv_pool_t &pool, int q_heads) {
+    return q_heads / pool.heads > 8 && pool.dim <= 128 ? 2 : 1;
+}
 
 template <int KT, int D, int NT> int64_t part_bytes(int grid) {
     using F = Cfg<KT, D, NT>;

@@ -246,15 +246,15 @@ typedef struct {
  *  rope       NULL, or [rope_rows, dim] fp32, 16-byte aligned: row p holds cos (dim / 2) and sin (dim / 2) of position
  *             p, and keys are rotated before they are stored: (x_i, x_{i + dim/2}) ->
  *             (x_i c_i - x_{i + dim/2} s_i, x_{i + dim/2} c_i + x_i s_i), every operation rounded to fp32.
- * 8-bit pools: per 32 elements d = fp16_rn(max|x| / 127) (at most 65504), q = clamp(rint(x / d), -127, 127), 0 where d is
- * 0, in fp32 with IEEE division; 16-bit pools: rounded to nearest even. Non-finite inputs give unspecified codes. */
+ * 8-bit pools: per 32 elements d = fp16_rn(max|x| / 127) (at most 65504), q = clamp(rint(x / d), -127, 127), 0 where d
+ * is 0, in fp32 with IEEE division; 16-bit pools: rounded to nearest even. Non-finite inputs give unspecified codes. */
 int qpack_kv_append(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_t *t, const int32_t *seqs,
                     const int32_t *pos, int64_t n, const void *k, const void *v, int dt, int64_t ldk, int64_t ldv,
                     const float *rope, int64_t rope_rows, qpack_stream_t stream);
 
 /* The inverse: rows of the cache, token i from position pos[i] of sequence seqs[i] (NULL as above), as dt (QPACK_F32,
- * F16 or BF16) into k, v [n, ld] (16-byte aligned, ld >= heads * dim and a multiple of 8). Either of k and v may be NULL.
- * Tokens with a negative position, or out of range, are written as zero. */
+ * F16 or BF16) into k, v [n, ld] (16-byte aligned, ld >= heads * dim and a multiple of 8). Either of k and v may be
+ * NULL. Tokens with a negative position, or out of range, are written as zero. */
 int qpack_kv_read(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_t *t, const int32_t *seqs,
                   const int32_t *pos, int64_t n, void *k, void *v, int dt, int64_t ldk, int64_t ldv,
                   qpack_stream_t stream);
@@ -262,16 +262,18 @@ int qpack_kv_read(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_
 /* Attention of one new token a sequence over its cache (grouped queries: query heads h * q_heads / heads ... share
  * key/value head h). Row b takes sequence s = seqs[b] (NULL: b), L = lens[s] and, with window > 0, its last `window`
  * tokens only (0: all): lo = max(0, L - window).
- *   x_t = scale * <q~_b, k'_t>, lo <= t < L;  out_b = sum_t e^{x_t - m} v'_t / sum_t e^{x_t - m};  lse_b = ln sum_t e^{x_t}
+ *   x_t = scale * <q~_b, k'_t>, lo <= t < L
+ *   out_b = sum_t e^{x_t - m} v'_t / sum_t e^{x_t - m},  lse_b = ln sum_t e^{x_t}
  * Sums, softmax statistics and accumulators are fp32; queries and probabilities enter the tensor cores as two 16-bit
  * terms each (22 bits for 8-bit and fp16 pools, 16 for bf16 pools). An empty range gives out = 0 and lse = -inf.
- *  q     [B, ldq] of dtype qdt, q_heads * dim elements a row, 16-byte aligned, ldq a multiple of 8; q_heads a multiple of
- *        the pool's heads, at most 65536;  rope  as in qpack_kv_append, applied to q at position L - 1 (NULL: q as it is)
+ *  q     [B, ldq] of dtype qdt, q_heads * dim elements a row, 16-byte aligned, ldq a multiple of 8; q_heads a multiple
+ *        of the pool's heads, at most 65536
+ *  rope  as in qpack_kv_append, applied to q at position L - 1 (NULL: q as it is)
  *  out   [B, ldo] of dtype odt, 16-byte aligned, ldo >= q_heads * dim and a multiple of 8
  *  lse   [B, q_heads] fp32, or NULL
- *  ws    workspace of at least the bytes that qpack_kv_attend_workspace gives on this device, 16-byte aligned,
- *        its first QPACK_KV_ATTEND_ZEROED bytes zeroed once before its first use. Each call leaves it ready for the next, of any shape that it is large
- *        enough for; calls that may run at the same time need a workspace each.
+ *  ws    workspace of at least the bytes that qpack_kv_attend_workspace gives on this device, 16-byte aligned, its
+ *        first QPACK_KV_ATTEND_ZEROED bytes zeroed once before its first use. Each call leaves it ready for the next, of
+ *        any shape that it is large enough for; calls that may run at the same time need a workspace each.
  *  B     at most 4096. Results do not depend on the order in which blocks run. */
 #define QPACK_KV_ATTEND_ZEROED (1 << 20)
 int qpack_kv_attend(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_t *t, const int32_t *seqs, int B,
@@ -280,8 +282,8 @@ int qpack_kv_attend(const qpack_kv_pool_t *pool, int layer, const qpack_kv_table
                     qpack_stream_t stream);
 int qpack_kv_attend_workspace(const qpack_kv_pool_t *pool, int B, int q_heads, int64_t *bytes);
 
-/* Page operators. All work on the device alone and are deterministic: new pages are the lowest-numbered free ones, in the
- * order of the requests. n <= 4096 sequences a call, each listed once.
+/* Page operators. All work on the device alone and are deterministic: new pages are the lowest-numbered free ones, in
+ * the order of the requests. n <= 4096 sequences a call, each listed once.
  *
  * reserve: extend sequence seqs[i] by add[i] >= 0 tokens. Request i needs the pages between its old and new length, and
  * is granted (pages entered in the table, refs 1, lens raised) when the pages that it and all requests before it need
@@ -290,9 +292,9 @@ int qpack_kv_attend_workspace(const qpack_kv_pool_t *pool, int B, int q_heads, i
 int qpack_kv_reserve(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, const int32_t *seqs, const int32_t *add,
                      int64_t n, qpack_stream_t stream);
 
-/* fork: make the empty sequence dst[i] a copy of src[i] (one src may be forked many times; no dst may be a src). Full pages
- * are shared (refs + 1); a last page that is not full is copied into a fresh page, over all layers, the filled tokens
- * only. Refused as in reserve. ws: qpack_kv_page_workspace bytes, 16-byte aligned, no initial value needed. */
+/* fork: make the empty sequence dst[i] a copy of src[i] (one src may be forked many times; no dst may be a src). Full
+ * pages are shared (refs + 1); a last page that is not full is copied into a fresh page, over all layers, the filled
+ * tokens only. Refused as in reserve. ws: qpack_kv_page_workspace bytes, 16-byte aligned, no initial value needed. */
 int qpack_kv_fork(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, const int32_t *src, const int32_t *dst,
                   int64_t n, void *ws, int64_t ws_bytes, qpack_stream_t stream);
 
