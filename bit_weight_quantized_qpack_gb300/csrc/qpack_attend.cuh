@@ -50,6 +50,7 @@
 
 #include "qpack_dev.cuh"
 #include "qpack_launch.h"
+#include "qpack_paged.cuh"
 
 namespace qpack {
 namespace attend {

@@ -16,10 +16,8 @@ enum : int { FMT_Q4G32 = 0, FMT_Q2S = 1, FMT_Q3S = 2, FMT_Q5S = 3, FMT_Q6S = 4, 
 enum : int { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2 };
 
 // Bits OR-ed into a per-translation-unit device fault word when a bounded wait gives up, or when a decode product met
-// an inf or nan activation (its outputs are then nan; the public value is QPACK_FAULT_NONFINITE_X). The paged cache's
-// operators record page numbers, positions and lengths out of range, and requests refused for want of pages.
-enum : int { FAULT_WAIT_FULL = 1, FAULT_WAIT_EMPTY = 2, FAULT_WAIT_MMA = 4, FAULT_WAIT_TMEM = 8, FAULT_NONFINITE_X = 16,
-             FAULT_PAGE = 32, FAULT_NO_PAGES = 64 };
+// an inf or nan activation (its outputs are then nan; the public value is QPACK_FAULT_NONFINITE_X).
+enum : int { FAULT_WAIT_FULL = 1, FAULT_WAIT_EMPTY = 2, FAULT_WAIT_MMA = 4, FAULT_WAIT_TMEM = 8, FAULT_NONFINITE_X = 16 };
 
 template <int F> struct Fmt;
 // INT4 symmetric group 32: 16 code bytes per group, fp32 scale in a separate array.
@@ -227,17 +225,6 @@ __device__ __forceinline__ uint32_t lop3_sel(uint32_t a, uint32_t b, uint32_t c)
     uint32_t d;
     asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
-}
-
-// 8-bit cache elements: bytes of w (codes + 128, that is the code word xor 0x80808080) chosen by `sel` (second and fourth
-// selector 4), times a pair of fp16 scales: the byte under the exponent of 1024 is 1024 + u, less 1152 the code
-// (exact), and the product rounds once, so the pair is fp16_rn(scale * code).
-__device__ __forceinline__ uint32_t dequant2(uint32_t w, uint32_t sel, uint32_t scale) {
-    const uint32_t u = __byte_perm(w, 0x64646464u, sel);
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));
-    const __half2 c = __hsub2(*reinterpret_cast<const __half2 *>(&u), off);
-    const __half2 v = __hmul2(c, *reinterpret_cast<const __half2 *>(&scale));
-    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 }  // namespace qpack

@@ -14,6 +14,7 @@
 
 #include "qpack_dev.cuh"
 #include "qpack_launch.h"
+#include "qpack_paged.cuh"
 #include "qpack_quot.cuh"
 
 namespace qpack {
