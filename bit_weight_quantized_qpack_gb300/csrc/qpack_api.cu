@@ -505,7 +505,8 @@ const char *qpack_status_string(int status) {
     switch (status) {
         case QPACK_OK: return "QPACK_OK";
         case QPACK_ERR_ARG: return "QPACK_ERR_ARG: null pointer, bad enum or negative size";
-        case QPACK_ERR_SHAPE: return "QPACK_ERR_SHAPE: K not a multiple of the group / super-block, or M out of range";
+        case QPACK_ERR_SHAPE: return "QPACK_ERR_SHAPE: K not a multiple of the group / super-block, M out of range, or a cache, table or "
+                                      "workspace size out of range";
         case QPACK_ERR_ALIGN: return "QPACK_ERR_ALIGN: pointer or leading dimension misaligned";
         case QPACK_ERR_RANGE: return "QPACK_ERR_RANGE: value out of the format's range";
         case QPACK_ERR_CUDA: return "QPACK_ERR_CUDA: a CUDA call or kernel launch failed";
@@ -533,6 +534,6 @@ int qpack_set_option(int option, int value) {
     return QPACK_ERR_ARG;
 }
 
-int qpack_version(void) { return 1 * 10000 + 0 * 100 + 0; }
+int qpack_version(void) { return 1 * 10000 + 1 * 100 + 0; }
 
 }  // extern "C"

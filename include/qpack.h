@@ -245,7 +245,8 @@ typedef struct {
  *             lens is not changed (qpack_kv_reserve extends a sequence). No two tokens may name the same place.
  *  rope       NULL, or [rope_rows, dim] fp32, 16-byte aligned: row p holds cos (dim / 2) and sin (dim / 2) of position
  *             p, and keys are rotated before they are stored: (x_i, x_{i + dim/2}) ->
- *             (x_i c_i - x_{i + dim/2} s_i, x_{i + dim/2} c_i + x_i s_i), every operation rounded to fp32.
+ *             (x_i c_i - x_{i + dim/2} s_i, x_{i + dim/2} c_i + x_i s_i), every operation rounded to fp32. Keys of
+ *             positions behind the table are stored as they are, and QPACK_FAULT_PAGE is set.
  * 8-bit pools: per 32 elements d = fp16_rn(max|x| / 127) (at most 65504), q = clamp(rint(x / d), -127, 127), 0 where d
  * is 0, in fp32 with IEEE division; 16-bit pools: rounded to nearest even. Non-finite inputs give unspecified codes. */
 int qpack_kv_append(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_t *t, const int32_t *seqs,
@@ -274,7 +275,8 @@ int qpack_kv_read(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_
  *  ws    workspace of at least the bytes that qpack_kv_attend_workspace gives on this device, 16-byte aligned, its
  *        first QPACK_KV_ATTEND_ZEROED bytes zeroed once before its first use. Each call leaves it ready for the next, of
  *        any shape that it is large enough for; calls that may run at the same time need a workspace each.
- *  B     at most 4096. Results do not depend on the order in which blocks run. */
+ *  B     at most 4096. Results do not depend on the order in which blocks run.
+ * QPACK_ERR_UNSUPPORTED: one row of the table could hold more than 2^31 tiles over all heads. */
 #define QPACK_KV_ATTEND_ZEROED (1 << 20)
 int qpack_kv_attend(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_t *t, const int32_t *seqs, int B,
                     const void *q, int qdt, int64_t ldq, int q_heads, float scale, int64_t window, const float *rope,

@@ -224,6 +224,35 @@ def test_attend_scale_zero(qpg):
     attend_case(qpg, "i8", 2, 9, 128, 16, [33, 2], scale=1e-38, qscale=1e-30, seed=13)
 
 
+@pytest.mark.parametrize("H,G,B", [(1, 2, 2300), (40, 1, 700)])
+def test_attend_many_rows(qpg, H, G, B):
+    """More rows than one launch takes (by their number, and by rows times heads), some empty, chosen in any order."""
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(0, 70, 300)]
+    attend_case(qpg, "i8", H, G, 64, 16, lens, seqs=[int(x) for x in rng.integers(0, 300, B)], seed=B)
+
+
+def test_rotation_table_too_short(qpg):
+    """Positions behind the rotation table are left unrotated and reported; the others are not touched by it."""
+    lens, D = [10, 40], 64
+    pool = make_pool(qpg, "f16", 1, 5, 1, 16, D, 1)
+    tab, tables = make_tables(qpg, lens, 16, 5, 2)
+    rope = torch.from_numpy(rope_table(20, D)).cuda()
+    q = torch.randn((2, 4, D), device="cuda")
+    full = torch.cat([rope, torch.cat([torch.ones((20, D // 2)), torch.zeros((20, D // 2))], 1).cuda()])
+    want = qpg.qpack_kv_attend(pool, 0, tables, q, rope=full)
+    assert qpg.qpack_fetch_fault_flags() == 0
+    assert torch.equal(qpg.qpack_kv_attend(pool, 0, tables, q, rope=rope), want)
+    assert qpg.qpack_fetch_fault_flags() == qpg.FAULT_PAGE
+    x = torch.randn((2, 1, D), device="cuda")
+    qpg.qpack_kv_append(pool, 0, tables, x, x, rope=rope)
+    assert qpg.qpack_fetch_fault_flags() == qpg.FAULT_PAGE
+    k, _ = qpg.qpack_kv_read(pool, 0, tables, n=2)
+    x32 = x.cpu().numpy()
+    assert np.array_equal(f64(k)[0], ref.rotate32(x32[:1], rope_table(20, D)[9:10])[0].astype(np.float16).astype(np.float64))
+    assert np.array_equal(f64(k)[1], x32[1].astype(np.float16).astype(np.float64))
+
+
 def test_attend_strided_rows(qpg):
     """q and out as slices of wider rows (a fused projection's output), 2-D and 3-D."""
     lens, H, G, D, T = [30, 75, 2], 2, 4, 64, 16
