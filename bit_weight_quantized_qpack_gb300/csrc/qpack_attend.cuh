@@ -27,8 +27,9 @@
 //   O^T = V^T P^T: A = values transposed by ldmatrix, B = probabilities: S's accumulator layout is B's operand layout
 //                  as it stands. Probabilities go in as two terms as well.
 //
-// Both terms carry 22 bits together (16 where the cache is bfloat16): scores and sums then differ from fp32 arithmetic
-// by less than the output's rounding, where a single fp16 term would add errors of that size. Queries are scaled by a
+// Both terms carry 22 bits together: scores and sums then differ from fp32 arithmetic by less than the output's
+// rounding, where a single fp16 term would add errors of that size. Where the cache is bfloat16 they carry 16: enough
+// for probabilities, while queries get a third term. Queries are scaled by a
 // power of two to a maximum in [2^13, 2^14) and probabilities by 2^12, so neither term meets fp16's range.
 //
 // 8-bit elements become fp16(scale * code), exactly the cache's definition: a byte permute puts code + 128 under the
@@ -63,16 +64,21 @@ constexpr float P_BIAS = 12.0f;             // probabilities are held as 2^(x - 
 // Accumulators and query fragments take D NT / 4 registers a thread each, so they bound W; shared memory bounds TOK and
 // the stages. Measured (one block an SM throughout; us for one sequence of 131071 tokens / 64 of 4096 to 8192, 8 bits,
 // D = 128): 8 warps x 32 tokens 54.9 / 141.3, 12 x 32 57.0 / 141.0, 10 x 32 59.5 / 151, 12 x 16 59.7 / 146, 16 x 16
-// 60.9 / 147; two blocks of 4 warps an SM 57.9 / 140.7 where one of 8 had come to 52.3 / 136.8. At D = 64 and in 16 bits
-// at 128 twelve warps are up to 10% faster than eight on long caches (62 against 68 us) and 2% slower on short ones.
+// 60.9 / 147; two blocks of 4 warps an SM 57.9 / 140.7 where one of 8 had come to 52.3 / 136.8. At D = 64 and in fp16 at
+// 128 twelve warps are up to 10% faster than eight on long caches (62 against 68 us) and 2% slower on short ones; in
+// bfloat16 at 128 their registers spill over the third terms (27.5 against 25.6 us).
 template <int KT, int D, int NT> struct Cfg {
     static constexpr int ES = KT == QPACK_KV_I8 ? 1 : 2;
     static constexpr int RB = D * ES;                           // bytes of a token's row
     static constexpr int SB = KT == QPACK_KV_I8 ? D / 16 : 0;   // bytes of its scales
     static constexpr int TOK = RB >= 256 ? 16 : 32;
     static constexpr int TILE = 2 * TOK * (RB + SB);            // keys, values, their scales
-    static constexpr int W = RB == 512 ? 6 : D * NT >= 256 || (KT == QPACK_KV_I8 && D == 128) ? 8 : 12;
-    static constexpr int STAGES = 214000 / (W * TILE) > 4 ? 4 : 214000 / (W * TILE);
+    static constexpr int W = RB == 512 ? 6 : D * NT >= 256 || (KT != QPACK_KV_F16 && D == 128) ? 8 : 12;
+    // Two bfloat16 terms hold 16 bits: what an fp32 or rotated query has beyond waits in shared memory for a third product.
+    static constexpr bool THREE = KT == QPACK_KV_BF16;
+    static constexpr int Q3 = THREE ? D / 16 * 2 * NT * 128 : 0;    // bytes a warp
+    static constexpr int ROOM = (222000 - W * Q3) / (W * TILE);
+    static constexpr int STAGES = ROOM > 4 ? 4 : ROOM;
     static constexpr int NH = 8 * NT;
     static constexpr int PS = D + 4;                            // floats of a head in a partial, padded for the banks
     static constexpr int PF = NH * PS;                          // floats of a piece's accumulators
@@ -173,6 +179,14 @@ template <int KT> __device__ __forceinline__ void split2(float x, float y, uint3
         hi = *reinterpret_cast<const uint32_t *>(&h);
         lo = *reinterpret_cast<const uint32_t *>(&l);
     }
+}
+
+// What two bfloat16 terms leave of a pair, rounded to a third (exact for fp32 inputs: 24 bits in three terms of 8).
+__device__ __forceinline__ uint32_t third_term(float x, float y, uint32_t hi, uint32_t lo) {
+    const float a = x - __uint_as_float(hi << 16) - __uint_as_float(lo << 16);
+    const float b = y - __uint_as_float(hi & 0xFFFF0000u) - __uint_as_float(lo & 0xFFFF0000u);
+    const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&t);
 }
 
 // A thread's four elements of a 16-element chunk of queries, as loaded: i .. i + 3 (GAP 2) or i, i + 1 and GAP further.
@@ -394,7 +408,8 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     constexpr int TOK = F::TOK, CPR = RB / 16, CH = D / 16, NH = F::NH, TT = TOK / 8, THREADS = W * 32;
     constexpr bool I8 = KT == QPACK_KV_I8;
     extern __shared__ __align__(128) unsigned char smem[];
-    unsigned *cum = reinterpret_cast<unsigned *>(smem + W * STAGES * TILE);  // units before row b, a segment's worth
+    // behind the rings: third terms, and the units before row b (of one segment a row)
+    unsigned *cum = reinterpret_cast<unsigned *>(smem + W * (STAGES * TILE + F::Q3));
     __shared__ Piece s_piece[2 * W];
     __shared__ float s_m[2 * W][NH], s_l[2 * W][NH];       // a piece's maxima and sums
     __shared__ int s_run[2 * W];
@@ -584,6 +599,9 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
             const bool whole = cc.ti == 0;
             const int count = min(int(cc.row.tiles - cc.ti), nt - done);
             uint32_t qf[CH][4 * NT];
+            constexpr bool THREE = F::THREE;
+            uint32_t *q3 = reinterpret_cast<uint32_t *>(smem + W * STAGES * TILE + w * F::Q3) + lane;
+            bool third = false;                            // whether any query of the segment has a third term
             float qs[NT], m[NT], l[NT], acc[CH][NT][4];
             {
                 uint32_t raw[NT][CH][4];
@@ -664,10 +682,18 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                             qf[c][0] = h0, qf[c][1] = l0, qf[c][2] = h1, qf[c][3] = l1;
                         else
                             qf[c][n] = h0, qf[c][2 + n] = h1, qf[c][4 + n] = l0, qf[c][6 + n] = l1;
+                        if constexpr (THREE) {
+                            const uint32_t t0 = third_term(x[c][0] * f, x[c][1] * f, h0, l0);
+                            const uint32_t t1 = third_term(x[c][2] * f, x[c][3] * f, h1, l1);
+                            q3[(c * 2 * NT + n) * 32] = t0;
+                            q3[(c * 2 * NT + NT + n) * 32] = t1;
+                            third |= ((t0 | t1) & 0x7FFF7FFFu) != 0;
+                        }
 #pragma unroll
                         for (int r = 0; r < 4; ++r) acc[c][n][r] = 0.0f;
                     }
                 }
+                if (THREE) third = __any_sync(0xffffffffu, third);
             }
             unsigned t0 = cc.row.base + cc.ti * TOK;
             for (int k = 0; k < count; ++k, t0 += TOK) {
@@ -715,7 +741,21 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                         }
                     }
                 }
-                if constexpr (NT == 2) {
+                if (THREE && third) {
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+#pragma unroll
+                        for (int u = 0; u < TOK / 16; ++u) {
+                            uint32_t r[4];
+                            ldsm4((st + u * 16 * RB) + ((c * 16 * F::ES) ^ lx), r);
+                            const uint32_t *q = q3 + c * 2 * NT * 32;      // a lane reads what it wrote
+                            const uint32_t a0 = q[0], a2 = q[NT * 32];
+                            const uint32_t a1 = NT == 2 ? q[32] : 0u, a3 = NT == 2 ? q[(2 * NT - 1) * 32] : 0u;
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) mma<KT>(sl[2 * u + t], a0, a1, a2, a3, r[t], r[2 + t]);
+                        }
+                }
+                if (NT == 2 || THREE) {
 #pragma unroll
                     for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -1024,8 +1064,8 @@ template <int KT, int D, int NT> cudaError_t run(const AttendArgs &a, cudaStream
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    constexpr int smem = F::W * F::STAGES * F::TILE + (MAX_ROWS + 1) * 4;
-    static_assert(smem <= 227 * 1024 - 8192, "shared memory");
+    constexpr int smem = F::W * (F::STAGES * F::TILE + F::Q3) + (MAX_ROWS + 1) * 4;
+    static_assert(smem <= 227 * 1024 - 5120, "shared memory");
     if (!opted[dev]) {
         e = cudaFuncSetAttribute(attend_kernel<KT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
@@ -1054,7 +1094,7 @@ template <int KT, int D, int NT> cudaError_t run(const AttendArgs &a, cudaStream
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(grid);
         cfg.blockDim = dim3(F::W * 32);
-        cfg.dynamicSmemBytes = F::W * F::STAGES * F::TILE + (p.B + 1) * 4;
+        cfg.dynamicSmemBytes = F::W * (F::STAGES * F::TILE + F::Q3) + (p.B + 1) * 4;
         cfg.stream = s;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

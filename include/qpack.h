@@ -266,7 +266,8 @@ int qpack_kv_read(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_
  *   x_t = scale * <q~_b, k'_t>, lo <= t < L
  *   out_b = sum_t e^{x_t - m} v'_t / sum_t e^{x_t - m},  lse_b = ln sum_t e^{x_t}
  * Sums, softmax statistics and accumulators are fp32; queries and probabilities enter the tensor cores as two 16-bit
- * terms each (22 bits for 8-bit and fp16 pools, 16 for bf16 pools). An empty range gives out = 0 and lse = -inf.
+ * terms each (22 bits) where the pool is 8-bit or fp16, as three (24) and two (16) where it is bf16. An empty range
+ * gives out = 0 and lse = -inf.
  *  q     [B, ldq] of dtype qdt, q_heads * dim elements a row, 16-byte aligned, ldq a multiple of 8; q_heads a multiple
  *        of the pool's heads, at most 65536
  *  rope  as in qpack_kv_append, applied to q at position L - 1 (NULL: q as it is)
