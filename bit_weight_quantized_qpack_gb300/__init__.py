@@ -347,9 +347,8 @@ class KVPool:
         self.layers, self.pages, self.heads, self.page_tokens, self.dim = layers, pages, heads, page_tokens, dim
 
         def strides(t):                                         # of an extent of one they mean nothing
-            page = t[0, 0].numel() if t.numel() else 0
-            ps = t.stride(1) if t.shape[1] > 1 else page
-            return (t.stride(0) if t.shape[0] > 1 else 0), ps
+            st = t.stride()
+            return (st[0] if layers > 1 else 0), (st[1] if pages > 1 else heads * page_tokens * t.shape[4])
 
         ls, ps = strides(k)
         sls, sps = strides(k_scales) if kind == KV_I8 else (0, 0)
