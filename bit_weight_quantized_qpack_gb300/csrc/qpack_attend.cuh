@@ -544,14 +544,32 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                 const int page = ok ? entry : 0;
                 const unsigned slot = unsigned(ci.h * T) + (mine & (T - 1));
                 const int64_t row = int64_t(page) * a.pool.page_stride + slot * unsigned(D);
+                constexpr int HALF = TOK * CPR / 64;       // copies of half a tile
+                if (TOK == 32 && T == 16 && okmask == 0xffffffffu) {
+                    // a whole tile of two pages, the most common of the small ones: two runs of rows (48 rows of up to
+                    // 8192 tokens 108.6 us instead of 113.9; with pages of 64 107.9)
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        const int64_t at = __shfl_sync(0xffffffffu, row, 16 * v) * F::ES + lane * 16;
+                        const unsigned char *ks = kbase + at, *vs = vbase + at;
+#pragma unroll
+                        for (int i = 0; i < HALF; ++i) {
+                            const int n = v * HALF + i;
+                            const uint32_t to = dst + n * 512 + (sw0 ^ (SWZ ? ((n * 32 / CPR) & 7) << 4 : 0));
+                            cp16(to, ks + i * 512);
+                            cp16(to + TOK * RB, vs + i * 512);
+                        }
+                    }
+                } else {
 #pragma unroll 4
-                for (int i = 0; i < TOK * CPR / 32; ++i) {
-                    const int idx = i * 32 + lane, r = idx / CPR, c = idx % CPR;
-                    const int64_t off = __shfl_sync(0xffffffffu, row, r) * F::ES + c * 16;
-                    const bool live = (okmask >> r) & 1;
-                    const uint32_t to = dst + i * 512 + (sw0 ^ (SWZ ? ((i * 32 / CPR) & 7) << 4 : 0));
-                    cp16(to, kbase + off, live);
-                    cp16(to + TOK * RB, vbase + off, live);
+                    for (int i = 0; i < TOK * CPR / 32; ++i) {
+                        const int idx = i * 32 + lane, r = idx / CPR, c = idx % CPR;
+                        const int64_t off = __shfl_sync(0xffffffffu, row, r) * F::ES + c * 16;
+                        const bool live = (okmask >> r) & 1;
+                        const uint32_t to = dst + i * 512 + (sw0 ^ (SWZ ? ((i * 32 / CPR) & 7) << 4 : 0));
+                        cp16(to, kbase + off, live);
+                        cp16(to + TOK * RB, vbase + off, live);
+                    }
                 }
                 if (I8) {
                     const int64_t sat = int64_t(page) * a.pool.scale_page_stride + slot * unsigned(D / 32);
