@@ -14,11 +14,11 @@
 // tensor pipe 30% busy. Unpacking the 8-bit cache is the largest part of the instructions (14 of some 23 a token and
 // warp), and they are issued on half of the cycles.
 //
-// Measured: 64 sequences of 4096 to 8192 tokens, 64 query heads over 8, 8 bits: 138.8 us = 6190 GB/s, 91% of the copy
-// rate; one sequence of 131071 tokens, 32 over 8: 52.6 us = 80%. What is left there is some 10 us a call, whatever its
+// Measured: 64 sequences of 4096 to 8192 tokens, 64 query heads over 8, 8 bits: 139 us = 6180 GB/s, 91% of the copy
+// rate; one sequence of 131071 tokens, 32 over 8: 53.7 us = 78%. What is left there is some 10 us a call, whatever its
 // size: 2 us until the first copies start (lengths, then pages: dependent loads), 2 to 4 us by which the slowest SM ends
 // after the middle one, 3 us for the joins of blocks, the launch. A row of 97 tokens takes 7 us. Sixteen query heads a
-// key head are bound by the instructions instead (62% of the copy rate).
+// key head are bound by the instructions instead (63% of the copy rate).
 //
 //   S = Q K^T:     A = queries (16 rows), B = 16 tokens x D. With up to eight query heads rows 0-7 hold the queries'
 //                  leading 16-bit terms and rows 8-15 the remainders of the same heads, so one instruction takes both
