@@ -308,10 +308,13 @@ def _addr(t):
     return t.data_ptr()
 
 
+# of a torch without CUDA neither exists, and no call gets as far as asking for its stream
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(stream):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _current_stream(_current_device()) if stream is None else stream.cuda_stream
 
 
 class KVPool:
@@ -397,18 +400,20 @@ _DTYPE_CODE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 
 
 def _need_rows(t, what, heads, dim):
-    """Token rows: [n, heads * dim] or [n, heads, dim], a row contiguous. Returns (dtype code, row stride)."""
+    """Token rows: [n, heads * dim] or [n, heads, dim], a row contiguous. Returns (dtype code, row stride, n)."""
     code = _DTYPE_CODE.get(t.dtype)
     if code is None:
         raise QpackError(f"{what}: expected float32, float16 or bfloat16, got {t.dtype}")
-    shape, st, nd = t.shape, t.stride(), t.dim()
-    if nd == 2:
-        ok = shape[1] == heads * dim and st[1] == 1
+    shape, st = t.shape, t.stride()
+    if len(shape) == 3:
+        n, h, d = shape
+        ok = h == heads and d == dim and st[2] == 1 and (st[1] == dim or heads == 1)
     else:
-        ok = nd == 3 and shape[1] == heads and shape[2] == dim and st[2] == 1 and (heads == 1 or st[1] == dim)
+        ok = len(shape) == 2 and shape[1] == heads * dim and st[1] == 1
+        n = shape[0] if ok else 0
     if not ok:
         raise QpackError(f"{what}: expected rows of {heads} x {dim}, got {tuple(shape)} with strides {tuple(st)}")
-    return code, (st[0] if shape[0] > 1 else heads * dim)
+    return code, (st[0] if n > 1 else heads * dim), n
 
 
 def _need_i32(t, what, n):
@@ -420,20 +425,19 @@ def _need_rope(rope, dim):
     """Rows of the rotation table."""
     if rope is None:
         return 0
-    if rope.dtype != torch.float32 or rope.dim() != 2 or rope.shape[1] != dim or not rope.is_contiguous():
-        raise QpackError(f"rope: expected a contiguous float32 [positions, {dim}] table, got {rope.dtype} "
-                         f"{tuple(rope.shape)}")
-    return rope.shape[0]
+    shape = rope.shape
+    if rope.dtype is not torch.float32 or len(shape) != 2 or shape[1] != dim or not rope.is_contiguous():
+        raise QpackError(f"rope: expected a contiguous float32 [positions, {dim}] table, got {rope.dtype} {tuple(shape)}")
+    return shape[0]
 
 
 def qpack_kv_append(pool, layer, tables, k, v, seqs=None, pos=None, rope=None, stream=None):
     """Write new tokens' keys and values (rows [n, heads, dim], float32, float16 or bfloat16) into a layer of the cache:
     token i at position pos[i] of sequence seqs[i] (default: the last token of sequence i). Keys are rotated first
     where `rope` (float32 [positions, dim]: cos | sin) is given; int8 pools quantize by qpack_kv_quantize's rule."""
-    dt, ldk = _need_rows(k, "k", pool.heads, pool.dim)
-    dtv, ldv = _need_rows(v, "v", pool.heads, pool.dim)
-    n = k.shape[0]
-    if dtv != dt or v.shape[0] != n:
+    dt, ldk, n = _need_rows(k, "k", pool.heads, pool.dim)
+    dtv, ldv, nv = _need_rows(v, "v", pool.heads, pool.dim)
+    if dtv != dt or nv != n:
         raise QpackError("k, v: expected the same type and number of rows")
     _need_i32(seqs, "seqs", n)
     _need_i32(pos, "pos", n)
@@ -458,13 +462,13 @@ def qpack_kv_read(pool, layer, tables, seqs=None, pos=None, k_out=None, v_out=No
     dk = dv = None
     ldk = ldv = 0
     if k_out is not None:
-        dk, ldk = _need_rows(k_out, "k_out", pool.heads, pool.dim)
-        if k_out.shape[0] < n:
-            raise QpackError(f"k_out: expected at least {n} rows, got {k_out.shape[0]}")
+        dk, ldk, rows = _need_rows(k_out, "k_out", pool.heads, pool.dim)
+        if rows < n:
+            raise QpackError(f"k_out: expected at least {n} rows, got {rows}")
     if v_out is not None:
-        dv, ldv = _need_rows(v_out, "v_out", pool.heads, pool.dim)
-        if v_out.shape[0] < n:
-            raise QpackError(f"v_out: expected at least {n} rows, got {v_out.shape[0]}")
+        dv, ldv, rows = _need_rows(v_out, "v_out", pool.heads, pool.dim)
+        if rows < n:
+            raise QpackError(f"v_out: expected at least {n} rows, got {rows}")
         if dk is not None and dk != dv:
             raise QpackError("k_out, v_out: expected the same type")
     _need_i32(seqs, "seqs", n)
@@ -512,16 +516,14 @@ def qpack_kv_attend(pool, layer, tables, q, seqs=None, scale=None, window=0, rop
     the cache of sequence seqs[b] (default b), its last `window` tokens where that is not 0. scale defaults to dim ** -0.5.
     Returns out, of q's shape, float16 unless given (float32 and bfloat16 too); lse, a float32 [B, q_heads] tensor if
     wanted, gets the log-sum-exp. A kept workspace (alloc_kv_workspace) saves its allocation."""
-    D = pool.dim
-    B = q.shape[0]
-    width = q.shape[1] * (D if q.dim() == 3 else 1)
-    q_heads = width // D
-    qdt, ldq = _need_rows(q, "q", q_heads, D)
+    D, shape = pool.dim, q.shape
+    q_heads = shape[1] if len(shape) == 3 else shape[-1] // D
+    qdt, ldq, B = _need_rows(q, "q", q_heads, D)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
-    odt, ldo = _need_rows(out, "out", q_heads, D)
-    if out.shape[0] < B:
-        raise QpackError(f"out: expected at least {B} rows, got {out.shape[0]}")
+        out = torch.empty(shape, dtype=torch.float16, device=q.device)
+    odt, ldo, rows = _need_rows(out, "out", q_heads, D)
+    if rows < B:
+        raise QpackError(f"out: expected at least {B} rows, got {rows}")
     _need_i32(seqs, "seqs", B)
     if seqs is None and tables.tables.shape[0] < B:
         raise QpackError(f"q: {B} rows, but the table has {tables.tables.shape[0]} sequences")
