@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     unsigned *cum = reinterpret_cast<unsigned *>(smem + W * (STAGES * TILE + F::Q3));
     __shared__ Piece s_piece[2 * W];
     __shared__ float s_m[2 * W][NH], s_l[2 * W][NH];       // a piece's maxima and sums
-    __shared__ int s_run[2 * W];
+    __shared__ int s_runs[W][2 * W];                       // a warp's list of runs, by their first pieces
     __shared__ unsigned s_max;
     const AttendArgs &a = p.a;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
@@ -956,8 +956,9 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
         outside = before_me || s0 + seg_units(cum, b) > end;
     }
     const unsigned outer = __ballot_sync(0xffffffffu, outside), early = __ballot_sync(0xffffffffu, before_me);
-    if (w == 0 && begins) s_run[__popc(starts & ((1u << lane) - 1u))] = lane;
-    __syncthreads();
+    int *s_run = s_runs[w];
+    if (begins) s_run[__popc(starts & ((1u << lane) - 1u))] = lane;
+    __syncwarp();
     constexpr int VEC = F::VEC;
     auto finish = [&](const Piece &pc, int head, int d, const Triple &t) {
         if (head >= pc.heads) return;
