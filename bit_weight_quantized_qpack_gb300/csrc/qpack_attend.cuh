@@ -415,7 +415,8 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     pdl_wait();                                            // inputs, cache and workspace may be the previous grid's
 
     // -- the rows' tiles, and this block's share of them ------------------------------------------------------
-    // Up to 32 rows are added up by every warp for itself (all write the same sums): no barrier before the copies.
+    // Up to 32 rows are added up by every warp for itself (all write the same sums): no barrier before the copies (one
+    // row of 2000 tokens 9.3 us instead of 9.9; more rows would be a longer loop in every warp).
     if (lane < 2) s_piece[2 * w + lane].seg = -1;
     const bool few = p.B <= 32;
     int *fault = blockIdx.x == 0 && (w == 0 || !few) ? &g_fault_attend : nullptr;
@@ -1055,7 +1056,8 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
 
 // -- host -------------------------------------------------------------------------------------------------------
 // Groups of eight query heads a block takes together: two where a key head has more than eight and the registers hold
-// both (at 256 they do not: the cache is then read once a group).
+// both (at 256 they do not: the cache is then read once a group). 48 rows of up to 8192 tokens with 16 heads a key head,
+// two groups together against one after the other: 148 / 189 us at 128 in 8 bits, 88 / 112 at 64, 109 / 173 in bfloat16.
 inline int groups(const qpack_kv_pool_t &pool, int q_heads) {
     return q_heads / pool.heads > 8 && pool.dim <= 128 ? 2 : 1;
 }

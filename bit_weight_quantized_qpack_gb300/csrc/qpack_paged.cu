@@ -100,7 +100,8 @@ template <int DT> __device__ __forceinline__ void convert(const Raw<DT> &r, floa
 }
 
 // The rotation's partner (i +- D/2) is D/16 lanes away, and the four lanes of a 32-element group reduce its maximum
-// with two shuffles.
+// with two shuffles. Blocks an SM, 8191 tokens of 8 heads in fp16 into 8 bits: 4 18.1 us, 5 15.4, 6 17.1, 8 17.3
+// (registers spill); in bfloat16 throughout: 4 16.3, 5 13.6, 7 12.8.
 template <int KT, int D, int DT>
 __global__ void __launch_bounds__(ROW_WARPS * 32, KT == QPACK_KV_I8 || DT == DT_F32 ? 5 : 7) kv_append_kernel(AppendArgs a, int64_t first, unsigned items, unsigned groups) {
     constexpr int LPR = D / 8, RPW = 32 / LPR, U = ROW_U;
