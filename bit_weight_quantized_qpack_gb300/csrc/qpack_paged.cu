@@ -2,9 +2,9 @@
 // bits, scatter into pages), reading rows back, and the page operators (reserve, fork, free, compact, copy).
 //
 // Append and read are streams: every element is read and written once, so HBM bounds them at length and the launch at
-// a decode step's few tokens. 8191 tokens of 8 heads of 128 in fp16: append into 8 bits 15.4 us (49% of the copy rate),
-// read back 11.4 us (67%); at 100000 tokens 67% and 89%. Append is held up by its own chain in each warp (loads, scales,
-// codes) with 20 warps an SM; fewer registers spill, and half the instructions of the codes' test changed nothing.
+// a decode step's few tokens. 8191 tokens of 8 heads of 128 in fp16: append into 8 bits 14.6 us (52% of the copy rate),
+// read back 11.4 us (67%); at 100000 tokens 74% and 89%. Append is held up by its own chain in each warp (loads, scales,
+// codes) with 24 warps an SM; fewer registers spill.
 // The page operators move the pages that they have to (HBM bound: 598 MB of pages compacted in 194 us, 91% of the copy
 // rate) after a plan on the tables alone (a few us of dependent loads). All of it is deterministic: pages are ranked by
 // number and requests by place, never by arrival.
@@ -100,10 +100,10 @@ template <int DT> __device__ __forceinline__ void convert(const Raw<DT> &r, floa
 }
 
 // The rotation's partner (i +- D/2) is D/16 lanes away, and the four lanes of a 32-element group reduce its maximum
-// with two shuffles. Blocks an SM, 8191 tokens of 8 heads in fp16 into 8 bits: 4 18.1 us, 5 15.4, 6 17.1, 8 17.3
-// (registers spill); in bfloat16 throughout: 4 16.3, 5 13.6, 7 12.8.
+// with two shuffles. Blocks an SM, 8191 tokens of 8 heads in fp16 into 8 bits: 4 17.9 us, 5 16.2, 6 14.6, 7 15.8
+// (registers spill); from fp32: 4 18.4, 5 18.7, 6 24.4; in bfloat16 throughout: 4 16.3, 5 13.6, 7 12.8.
 template <int KT, int D, int DT>
-__global__ void __launch_bounds__(ROW_WARPS * 32, KT == QPACK_KV_I8 || DT == DT_F32 ? 5 : 7) kv_append_kernel(AppendArgs a, int64_t first, unsigned items, unsigned groups) {
+__global__ void __launch_bounds__(ROW_WARPS * 32, DT == DT_F32 ? 5 : KT == QPACK_KV_I8 ? 6 : 7) kv_append_kernel(AppendArgs a, int64_t first, unsigned items, unsigned groups) {
     constexpr int LPR = D / 8, RPW = 32 / LPR, U = ROW_U;
     const int lane = threadIdx.x & 31, sub = lane % LPR, H = a.pool.heads;
     pdl_launch_dependents();
@@ -177,13 +177,13 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, KT == QPACK_KV_I8 || DT == DT_
         const uint16_t d16 = f2h_bits(fminf(__fdiv_rn(mine, 127.0f), 65504.0f));
         const float d = h2f_bits(d16), rs = d > 0.0f ? __frcp_rn(d) : 0.0f;     // a scale of 0 gives codes of 0
         // A scale that fp16 holds as a normal number is off by at most 2^-11 of max / 127, so no quotient is beyond
-        // 127.07 and none needs the clamp; the others take the written definition below.
-        const bool tiny = d < 0x1p-14f && d > 0.0f;
+        // 127.07 and none needs the clamp; the others take the written definition below (their reciprocal goes negative).
+        const float give = d < 0x1p-14f ? -rs : rs;
+        uint32_t w[U][2];
+        bool plain[U], any = false;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int from = (lane & ~3) + u;
-            const float r = __shfl_sync(0xffffffffu, rs, from);
-            bool plain = __shfl_sync(0xffffffffu, tiny, from);
+            const float r0 = __shfl_sync(0xffffffffu, give, (lane & ~3) + u), r = fabsf(r0);
             // q = rint(x r) read from the low byte of x r + 1.5 2^23. x r is within 2^-24 |x / d| of x / d, and the
             // rounded quotient too, together less than 2^-16: where x r is nearer than 1/2 - 2^-15 to q, q is the
             // quotient's rint.
@@ -193,27 +193,32 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, KT == QPACK_KV_I8 || DT == DT_
                 y[e] = __fmaf_rn(x[u][e], r, 12582912.0f);
                 off = fmaxf(off, fabsf(__fmaf_rn(x[u][e], r, 12582912.0f - y[e])));
             }
-            uint32_t w[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const uint32_t lo = __byte_perm(__float_as_uint(y[4 * e]), __float_as_uint(y[4 * e + 1]), 0x0040u);
                 const uint32_t hi = __byte_perm(__float_as_uint(y[4 * e + 2]), __float_as_uint(y[4 * e + 3]), 0x0040u);
-                w[e] = __byte_perm(lo, hi, 0x5410u);
+                w[u][e] = __byte_perm(lo, hi, 0x5410u);
             }
-            plain |= !(off <= 0.5f - 0x1p-15f);
-            if (__any_sync(0xffffffffu, plain)) {          // rare
-                const float du = h2f_bits(uint16_t(__shfl_sync(0xffffffffu, int(d16), from)));
-                if (plain && du > 0.0f) {
-                    uint8_t cb[8];
-                    rint_codes<8>(x[u], du, r, 0, -127, 127, 0, cb);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        w[e] = cb[4 * e] | uint32_t(cb[4 * e + 1]) << 8 | uint32_t(cb[4 * e + 2]) << 16 | uint32_t(cb[4 * e + 3]) << 24;
-                }
-            }
-            if (head0 + u * RPW < H)
-                *reinterpret_cast<uint2 *>(static_cast<int8_t *>(v ? a.pool.v : a.pool.k) + page + in_page + u * pass) = make_uint2(w[0], w[1]);
+            plain[u] = !(off <= 0.5f - 0x1p-15f) || r0 < 0.0f;
+            any |= plain[u];
         }
+        if (__any_sync(0xffffffffu, any)) {                // rare
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float du = h2f_bits(uint16_t(__shfl_sync(0xffffffffu, int(d16), (lane & ~3) + u)));
+                if (!plain[u] || !(du > 0.0f)) continue;
+                uint8_t cb[8];
+                rint_codes<8>(x[u], du, __frcp_rn(du), 0, -127, 127, 0, cb);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    w[u][e] = cb[4 * e] | uint32_t(cb[4 * e + 1]) << 8 | uint32_t(cb[4 * e + 2]) << 16 |
+                              uint32_t(cb[4 * e + 3]) << 24;
+            }
+        }
+        int8_t *base = static_cast<int8_t *>(v ? a.pool.v : a.pool.k) + page + in_page;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (head0 + u * RPW < H) *reinterpret_cast<uint2 *>(base + u * pass) = make_uint2(w[u][0], w[u][1]);
         if (head0 + k * RPW < H) (v ? a.pool.v_scales : a.pool.k_scales)[spage + (in_page + k * pass) / 32] = d16;
     }
 }
