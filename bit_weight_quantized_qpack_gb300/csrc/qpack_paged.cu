@@ -2,10 +2,10 @@
 // bits, scatter into pages), reading rows back, and the page operators (reserve, fork, free, compact, copy).
 //
 // Append and read are streams: every element is read and written once, so HBM bounds them at length and the launch at
-// a decode step's few tokens. 8191 tokens of 8 heads of 128 in fp16: append into 8 bits 14.6 us (52% of the copy rate),
+// a decode step's few tokens. 8191 tokens of 8 heads of 128 in fp16: append into 8 bits 14.5 us (52% of the copy rate),
 // read back 11.4 us (67%); at 100000 tokens 74% and 89%. Append is held up by its own chain in each warp (loads, scales,
 // codes) with 24 warps an SM; fewer registers spill.
-// The page operators move the pages that they have to (HBM bound: 598 MB of pages compacted in 194 us, 91% of the copy
+// The page operators move the pages that they have to (HBM bound: 598 MB of pages compacted in 195 us, 91% of the copy
 // rate) after a plan on the tables alone (a few us of dependent loads). All of it is deterministic: pages are ranked by
 // number and requests by place, never by arrival.
 #include <cuda_bf16.h>
@@ -642,12 +642,14 @@ __global__ void __launch_bounds__(256) kv_copy_kernel(qpack_kv_pool_t pool, Page
     const int64_t n = src_list ? n_list : w.count[0];
     const int64_t slabs = n * pool.layers * 2 * pool.heads;
     const int es = pool.type == QPACK_KV_I8 ? 1 : 2;
+    const bool narrow = slabs < (int64_t(1) << 31);        // 32-bit divisions do (64 children: 28.0 us, not 28.4)
     for (int64_t j = warp; j < slabs; j += warps) {
-        const int head = int(j % pool.heads);
-        int64_t q = j / pool.heads;
-        const bool is_v = q & 1;
-        q >>= 1;
-        const int64_t layer = q % pool.layers, item = q / pool.layers;
+        const int64_t pair = narrow ? int64_t(unsigned(j) / unsigned(pool.heads)) : j / pool.heads;
+        const int64_t page = pair >> 1;                    // (item, layer)
+        const int64_t item = narrow ? int64_t(unsigned(page) / unsigned(pool.layers)) : page / pool.layers;
+        const int64_t layer = page - item * pool.layers;
+        const int head = int(j - pair * pool.heads);
+        const bool is_v = pair & 1;
         CopyItem it;
         if (src_list) it = {src_list[item], dst_list[item], pool.page_tokens};
         else it = w.items[item];
