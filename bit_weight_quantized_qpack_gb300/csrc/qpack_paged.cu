@@ -5,7 +5,7 @@
 // a decode step's few tokens. 8191 tokens of 8 heads of 128 in fp16: append into 8 bits 14.5 us (52% of the copy rate),
 // read back 11.4 us (67%); at 100000 tokens 74% and 89%. Append is held up by its own chain in each warp (loads, scales,
 // codes) with 24 warps an SM; fewer registers spill.
-// The page operators move the pages that they have to (HBM bound: 598 MB of pages compacted in 195 us, 91% of the copy
+// The page operators move the pages that they have to (HBM bound: 598 MB of pages compacted in 197 us, 90% of the copy
 // rate) after a plan on the tables alone (a few us of dependent loads). All of it is deterministic: pages are ranked by
 // number and requests by place, never by arrival.
 #include <cuda_bf16.h>
