@@ -176,9 +176,10 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, DT == DT_F32 ? 5 : KT == QPACK
         const float mine = k & 2 ? (k & 1 ? m[3] : m[2]) : (k & 1 ? m[1] : m[0]);
         const uint16_t d16 = f2h_bits(fminf(__fdiv_rn(mine, 127.0f), 65504.0f));
         const float d = h2f_bits(d16), rs = d > 0.0f ? __frcp_rn(d) : 0.0f;     // a scale of 0 gives codes of 0
-        // A scale that fp16 holds as a normal number is off by at most 2^-11 of max / 127, so no quotient is beyond
-        // 127.07 and none needs the clamp; the others take the written definition below (their reciprocal goes negative).
-        const float give = d < 0x1p-14f ? -rs : rs;
+        // A scale that fp16 holds as a normal number below its largest is off by at most 2^-11 of max / 127, so no quotient
+        // is beyond 127.07 and none needs the clamp. The others, subnormal or cut to 65504, take the written definition
+        // below (their reciprocal goes negative).
+        const float give = d < 0x1p-14f || d >= 65504.0f ? -rs : rs;
         uint32_t w[U][2];
         bool plain[U], any = false;
 #pragma unroll

@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_paged import DT, cache_rows, f64, make_pool, make_tables, pages_for
+from oracle import paged as ref
+from test_gpu_paged import DT, cache_rows, f64, make_pool, make_tables, pages_for, rope_table
 
 pytestmark = pytest.mark.gpu
 
@@ -60,4 +61,35 @@ def test_attend_very_large_scores(qpg, kind, G, top):
             # a few roundings of the sums, each of at most n terms
             assert np.all(np.abs(f64(out[s]) - want) <= (np.abs(v).mean(0) * (n / 8 + 64) * 2.0 ** -23)), (mode, n)
             assert np.allclose(f64(lse[s]), f64(q[s, :, 5]), rtol=2.0 ** -21, atol=0)
+    assert qpg.qpack_fetch_fault_flags() == 0
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# append
+# ---------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("xdt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rope", [False, True])
+def test_append_saturated_scales(qpg, xdt, D, rope):
+    """Groups whose scale ends at fp16's largest number: codes are clamped as the rule says, bit for bit."""
+    tops = [8.2e6, 8.319e6, 8.33e6, 8.36e6, 9e6, 1e7, 256 * 65504.0, 257.4 * 65504, 1e9, 2.0 ** 22 * 65504, 2.0 ** 23 * 65504,
+            1e12, 1e20, 1e30]
+    H, T, n = 3, 16, len(tops)
+    rng = np.random.default_rng(D)
+    x = rng.uniform(-1, 1, (2, n, H, D)) * np.exp(rng.uniform(-4, 0, (2, n, H, D)))
+    x[..., ::32], x[..., 1::32] = 1.0, -1.0                 # every group reaches its magnitude, with both signs
+    x = torch.from_numpy(x * np.array(tops)[:, None, None]).float().to(DT[xdt]).cuda()
+    pool = make_pool(qpg, "i8", 1, 3, H, T, D, 1)
+    tab, tables = make_tables(qpg, [n], T, 3, 2)
+    seqs, pos = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.arange(n, dtype=torch.int32, device="cuda")
+    table = rope_table(n, D, 3)
+    qpg.qpack_kv_append(pool, 0, tables, x[0], x[1], seqs=seqs, pos=pos, rope=torch.from_numpy(table).cuda() if rope else None)
+    page = int(tab[0, 0])
+    for c, s, a in ((pool.k, pool.k_scales, x[0]), (pool.v, pool.v_scales, x[1])):
+        a = a.float().cpu().numpy()
+        if rope and c is pool.k:
+            a = ref.rotate32(a, table)
+        codes, scales = ref.quantize32(a)
+        assert np.array_equal(s[0, page, :, :n].transpose(0, 1).cpu().numpy().view(np.uint16), scales.view(np.uint16))
+        assert np.array_equal(c[0, page, :, :n].transpose(0, 1).cpu().numpy(), codes)
     assert qpg.qpack_fetch_fault_flags() == 0
