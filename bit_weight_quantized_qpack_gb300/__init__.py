@@ -8,6 +8,7 @@ when the CUDA library is not built or no GPU is present.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -317,6 +318,24 @@ def _raw_stream(stream):
     return _current_stream(_current_device()) if stream is None else stream.cuda_stream
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Where a call allocates what the caller did not give: in the order of the stream that it runs on, so that zeroing comes
+    before the kernels, and memory that is given back is not handed out again before they end."""
+    return _HERE if stream is None else torch.cuda.stream(stream)
+
+
+def _out(stream, shape, dtype, device):
+    """An output of a call on `stream`, to be read on the current stream too."""
+    with _on(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 class KVPool:
     """A paged KV cache: keys and values [layers, pages, heads, page_tokens, dim], int8 codes with fp16 scales
     [layers, pages, heads, page_tokens, dim / 32], or fp16 / bf16 without scales. The layer and page strides are free (a
@@ -458,7 +477,7 @@ def qpack_kv_read(pool, layer, tables, seqs=None, pos=None, k_out=None, v_out=No
         n = given.shape[0]
     if k_out is None and v_out is None:
         dt = torch.bfloat16 if pool.k.dtype == torch.bfloat16 else torch.float16
-        k_out, v_out = (torch.empty((n, pool.heads, pool.dim), dtype=dt, device=pool.k.device) for _ in range(2))
+        k_out, v_out = (_out(stream, (n, pool.heads, pool.dim), dt, pool.k.device) for _ in range(2))
     dk = dv = None
     ldk = ldv = 0
     if k_out is not None:
@@ -482,7 +501,9 @@ def qpack_kv_read(pool, layer, tables, seqs=None, pos=None, k_out=None, v_out=No
 
 class KVWorkspace:
     """Scratch memory of a call, laid out once, its first `zeroed` bytes zeroed: attention counts in them, and every
-    call leaves them as it found them. Calls that may run at the same time need a workspace each."""
+    call leaves them as it found them. Calls that may run at the same time need a workspace each. It is allocated and zeroed
+    on the current stream: a call on another one has to be ordered behind that, and the workspace has to outlive the call
+    there (as with any tensor that torch allocates)."""
 
     def __init__(self, bytes, device, zeroed=0):
         self.buffer = torch.empty(bytes, dtype=torch.uint8, device=device)
@@ -520,7 +541,7 @@ def qpack_kv_attend(pool, layer, tables, q, seqs=None, scale=None, window=0, rop
     q_heads = shape[1] if len(shape) == 3 else shape[-1] // D
     qdt, ldq, B = _need_rows(q, "q", q_heads, D)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float16, device=q.device)
+        out = _out(stream, shape, torch.float16, q.device)
     odt, ldo, rows = _need_rows(out, "out", q_heads, D)
     if rows < B:
         raise QpackError(f"out: expected at least {B} rows, got {rows}")
@@ -530,7 +551,8 @@ def qpack_kv_attend(pool, layer, tables, q, seqs=None, scale=None, window=0, rop
     if lse is not None:
         _need(lse, torch.float32, "lse", numel=B * q_heads)
     if workspace is None:
-        workspace = alloc_kv_workspace(pool, B, q_heads)
+        with _on(stream):
+            workspace = alloc_kv_workspace(pool, B, q_heads)
     rows = _need_rope(rope, D)
     rc = (_lib or lib()).qpack_kv_attend(pool._ref, layer, tables._ref, _addr(seqs), B, _addr(q), qdt, ldq, q_heads,
                                          D ** -0.5 if scale is None else scale, window, _addr(rope), rows, _addr(out),
@@ -563,7 +585,9 @@ def qpack_kv_fork(pool, tables, src, dst, workspace=None, stream=None):
     n = src.numel()
     _need_i32(src, "src", n)
     _need_i32(dst, "dst", n)
-    workspace = alloc_kv_page_workspace(pool, tables) if workspace is None else workspace
+    if workspace is None:
+        with _on(stream):
+            workspace = alloc_kv_page_workspace(pool, tables)
     rc = (_lib or lib()).qpack_kv_fork(pool._ref, tables._ref, _addr(src), _addr(dst), n, workspace._p,
                                        workspace.bytes, _raw_stream(stream))
     if rc:
@@ -591,7 +615,9 @@ def qpack_kv_compact(pool, tables, tables_out=None, refs_out=None, moved=None, w
         raise QpackError("tables_out: expected the tables' type, shape and strides")
     _need(refs_out, torch.int32, "refs_out", numel=tables.refs.numel())
     _need_i32(moved, "moved", 1)
-    workspace = alloc_kv_page_workspace(pool, tables) if workspace is None else workspace
+    if workspace is None:
+        with _on(stream):
+            workspace = alloc_kv_page_workspace(pool, tables)
     rc = (_lib or lib()).qpack_kv_compact(pool._ref, tables._ref, _addr(tables_out), _addr(refs_out), _addr(moved),
                                           workspace._p, workspace.bytes, _raw_stream(stream))
     if rc:

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from oracle import paged as ref
-from test_gpu_paged import DT, cache_rows, f64, make_pool, make_tables, pages_for, rope_table
+from test_gpu_paged import DT, cache_rows, f64, make_pool, make_tables, pages_for, rope_table, same_state, token_view
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +93,86 @@ def test_append_saturated_scales(qpg, xdt, D, rope):
         assert np.array_equal(s[0, page, :, :n].transpose(0, 1).cpu().numpy().view(np.uint16), scales.view(np.uint16))
         assert np.array_equal(c[0, page, :, :n].transpose(0, 1).cpu().numpy(), codes)
     assert qpg.qpack_fetch_fault_flags() == 0
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# another stream
+# ---------------------------------------------------------------------------------------------------------------
+def soil(bytes):
+    """Leaves non-zero bytes in what the allocator hands out next on this stream."""
+    for n in {bytes, max(bytes // 2, 512)}:
+        torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda")
+
+
+def busy():
+    """Keeps the current stream busy for some milliseconds."""
+    torch.cuda._sleep(20_000_000)
+
+
+def test_attend_other_stream_default_workspace(qpg):
+    """A call on a stream of the caller's choice, without workspace or output: what it allocates is zeroed, used and
+    released in that stream's order, while the current stream is busy and allocates the same sizes."""
+    lens = [7777, 10, 3000]
+    pages = pages_for(lens, 16)
+    pool = make_pool(qpg, "i8", 1, pages, 2, 16, 128, 1)
+    _, tables = make_tables(qpg, lens, 16, pages, 2)
+    q = torch.randn((3, 8, 128), device="cuda")
+    want = qpg.qpack_kv_attend(pool, 0, tables, q)
+    size = qpg.alloc_kv_workspace(pool, 3, 8).bytes
+    s = torch.cuda.Stream()
+    soil(size)
+    torch.cuda.synchronize()
+    for _ in range(4):
+        busy()
+        out = qpg.qpack_kv_attend(pool, 0, tables, q, stream=s)
+        soil(size)                                          # behind the current stream's work, over what the call gave back
+        s.synchronize()
+        assert torch.equal(out, want)
+    torch.cuda.synchronize()
+    assert qpg.qpack_fetch_fault_flags() == 0
+
+
+def test_read_other_stream_default_outputs(qpg):
+    lens = [500]
+    pool = make_pool(qpg, "i8", 1, 40, 2, 16, 128, 1)
+    _, tables = make_tables(qpg, lens, 16, 40, 2)
+    seqs, pos = torch.zeros(500, dtype=torch.int32, device="cuda"), torch.arange(500, dtype=torch.int32, device="cuda")
+    want = qpg.qpack_kv_read(pool, 0, tables, seqs, pos)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.full_like(want[0], 3.0)                           # its memory is free again, the fill still to come
+    busy()
+    torch.full_like(want[0], 3.0)
+    got = qpg.qpack_kv_read(pool, 0, tables, seqs, pos, stream=s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_page_operators_other_stream_default_workspace(qpg):
+    """Fork and compact on another stream without a workspace: their list of copies is not overwritten by what the current
+    stream allocates next."""
+    s = torch.cuda.Stream()
+    for kind in ("i8", "f16"):
+        pool = make_pool(qpg, kind, 4, 600, 2, 16, 128, 1)
+        tables = qpg.alloc_kv_tables(60, 20, 600)
+        sim = ref.Pages(60, 20, 600, 16, token_view(pool))
+        ids = torch.arange(60, dtype=torch.int32, device="cuda")
+        seqs, add = list(range(8)), [37, 300, 5, 16, 129, 200, 1, 90]
+        qpg.qpack_kv_reserve(pool, tables, ids[:8], torch.tensor(add, dtype=torch.int32, device="cuda"))
+        sim.reserve(seqs, add)
+        src, dst = [i % 8 for i in range(48)], list(range(8, 56))
+        t_src, t_dst, t_gone = ids[:8].repeat(6), ids[8:56], ids[0:40:3].contiguous()
+        size = qpg.alloc_kv_page_workspace(pool, tables).bytes
+        torch.cuda.synchronize()
+        busy()
+        qpg.qpack_kv_fork(pool, tables, t_src, t_dst, stream=s)
+        soil(size)
+        qpg.qpack_kv_free(tables, t_gone, stream=s)
+        qpg.qpack_kv_compact(pool, tables, stream=s)
+        soil(size)
+        sim.fork(src, dst)
+        sim.free(range(0, 40, 3))
+        assert sim.compact() > 0
+        s.synchronize()
+        same_state(qpg, pool, tables, sim)
