@@ -29,9 +29,10 @@
 //                  as it stands. Probabilities go in as two terms as well.
 //
 // Both terms carry 22 bits together: scores and sums then differ from fp32 arithmetic by less than the output's
-// rounding, where a single fp16 term would add errors of that size. Where the cache is bfloat16 they carry 16: enough
-// for probabilities, while queries get a third term. Queries are scaled by a
-// power of two to a maximum in [2^13, 2^14) and probabilities by 2^12, so neither term meets fp16's range.
+// rounding, where a single fp16 term would add errors of that size. Queries are scaled by a power of two to a maximum in
+// [2^13, 2^14) and probabilities by 2^12, so neither term meets fp16's range. Where the cache is bfloat16 two terms carry
+// 16 bits: enough for probabilities, while queries get a third term. These have fp32's range and stay as they are: scaled,
+// the sums would pass it before the fp32 form's do.
 //
 // 8-bit elements become fp16(scale * code), exactly the cache's definition: a byte permute puts code + 128 under the
 // exponent of 1024, one packed subtraction takes 1152 off (exact), one packed product rounds once: 1.75 instructions an
@@ -59,7 +60,6 @@ namespace attend {
 
 constexpr int MAX_ROWS = 1024;              // rows a launch
 constexpr int MAX_COUNTERS = QPACK_KV_ATTEND_ZEROED / 4;    // of a launch: the front of the workspace
-constexpr float P_BIAS = 12.0f;             // probabilities are held as 2^(x - m + 12)
 
 // Shape of an instance: NT groups of eight query heads, tiles of TOK tokens, W warps, a ring of STAGES tiles each.
 // Accumulators and query fragments take D NT / 4 registers a thread each, so they bound W; shared memory bounds TOK and
@@ -87,6 +87,8 @@ template <int KT, int D, int NT> struct Cfg {
     static constexpr int SLICES = VEC / 32;                     // warps of a join, each on its own
     static_assert(STAGES >= 2 && PF * 4 <= STAGES * TILE, "a warp's ring holds a partial");
     static_assert(2 * W <= 32, "a lane a piece");
+    // Probabilities are held as 2^(x - m + P_BIAS), and queries are brought to a like height (the head of this file says why).
+    static constexpr float P_BIAS = KT == QPACK_KV_BF16 ? 0.0f : 12.0f;
 };
 
 struct Params {
@@ -361,8 +363,8 @@ __device__ __forceinline__ void next_segment(const Params &p, const Plan &pl, co
 // 1 / sum, or 0 where no token counted (a sum of NaN stays one).
 __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 __device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.0f : m; }
-__device__ __forceinline__ float lse_of(float m, float l) {
-    return l == 0.0f ? -INFINITY : (m - P_BIAS) * 0.6931471805599453f + logf(l);
+__device__ __forceinline__ float lse_of(float m, float l, float bias) {
+    return l == 0.0f ? -INFINITY : (m - bias) * 0.6931471805599453f + logf(l);
 }
 
 // A triple of one head and four of its accumulators, joined with n <= N others.
@@ -674,10 +676,10 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                         for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(x[c][e]));
                     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
                     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                    // 2^(13 - exponent of the maximum), within fp32's normal range; 1 for zero, inf and NaN. The scale's
-                    // sign goes with it, so that the largest score is the largest sum.
+                    // 2^(13 - exponent of the maximum), within fp32's normal range; 1 for zero, inf and NaN, and for bfloat16
+                    // terms. The scale's sign goes with it, so that the largest score is the largest sum.
                     const int ex = __float_as_int(big) >> 23;
-                    const int up = big == 0.0f || ex == 255 ? 127 : min(254, 267 - ex);
+                    const int up = KT == QPACK_KV_BF16 || big == 0.0f || ex == 255 ? 127 : min(254, 267 - ex);
                     const float f = __int_as_float((up << 23) | (__float_as_int(a.scale) & 0x80000000));
                     const float back = __int_as_float(max(254 - up, 1) << 23);
                     qs[n] = fabsf(a.scale) * 1.4426950408889634f * back * (up == 254 ? 0.5f : 1.0f);
@@ -826,7 +828,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                     float sum = 0.0f;
 #pragma unroll
                     for (int e = 0; e < 2 * TT; ++e) {
-                        s[n][e] = ex2(fmaf(s[n][e] - top, qs[n], P_BIAS));
+                        s[n][e] = ex2(fmaf(s[n][e] - top, qs[n], F::P_BIAS));
                         sum += s[n][e];
                     }
                     l[n] += sum;
@@ -909,7 +911,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                     }
                     const int head = cc.q * NH + 8 * n + g;
                     if (a.lse && j == 0 && head < p.G)
-                        a.lse[int64_t(p.row0 + cc.b) * a.q_heads + cc.h * p.G + head] = lse_of(mx[n], l[n]);
+                        a.lse[int64_t(p.row0 + cc.b) * a.q_heads + cc.h * p.G + head] = lse_of(mx[n], l[n], F::P_BIAS);
                 }
             } else {
                 // The first of two pieces waits in global memory (the ring is in use), the last one in the ring.
@@ -970,7 +972,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
         const float f = inverse(t.l);
         const float x[4] = {t.o.x * f, t.o.y * f, t.o.z * f, t.o.w * f};
         store_out<4>(a.out, a.odt, pc.out + head * D + d, x);
-        if (a.lse && d == 0) a.lse[pc.lse + head] = lse_of(t.m, t.l);
+        if (a.lse && d == 0) a.lse[pc.lse + head] = lse_of(t.m, t.l, F::P_BIAS);
     };
     const int todo = __popc(starts) * VEC;
     int left_base = 0, left_n = 0;                         // lane k: where the warp's k-th part that leaves the block is

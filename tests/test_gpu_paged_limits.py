@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from oracle import paged as ref
-from test_gpu_paged import DT, cache_rows, f64, make_pool, make_tables, pages_for, rope_table, same_state, token_view
+from test_gpu_paged import DT, cache_rows, check_attend, f64, make_pool, make_tables, pages_for, rope_table, same_state, token_view
 
 pytestmark = pytest.mark.gpu
 
@@ -62,6 +62,27 @@ def test_attend_very_large_scores(qpg, kind, G, top):
             assert np.all(np.abs(f64(out[s]) - want) <= (np.abs(v).mean(0) * (n / 8 + 64) * 2.0 ** -23)), (mode, n)
             assert np.allclose(f64(lse[s]), f64(q[s, :, 5]), rtol=2.0 ** -21, atol=0)
     assert qpg.qpack_fetch_fault_flags() == 0
+
+
+@pytest.mark.parametrize("what", ["values", "keys", "small keys"])
+@pytest.mark.parametrize("D,G", [(64, 3), (64, 16), (128, 4), (128, 11), (256, 2)])
+def test_attend_bf16_magnitudes(qpg, what, D, G):
+    """A bf16 cache has fp32's range: values of 2^116, keys of 2^112 beside queries of 2^-112 and the other way round give
+    what they give in fp32."""
+    T, H, lens = 16, 2, [1, 33, 700, 5000]
+    pages = pages_for(lens, T)
+    pool = make_pool(qpg, "bf16", 1, pages, H, T, D, 11)
+    tab, tables = make_tables(qpg, lens, T, pages, 12)
+    q = torch.randn((len(lens), H * G, D), device="cuda")
+    if what == "values":
+        pool.v.mul_(2.0 ** 116)
+    else:
+        pool.k.mul_(2.0 ** (112 if what == "keys" else -105))
+        q.mul_(2.0 ** (-112 if what == "keys" else 105))
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    qpg.qpack_kv_attend(pool, 0, tables, q, out=out, lse=lse)
+    assert qpg.qpack_fetch_fault_flags() == 0
+    check_attend(out, lse, "f32", "bf16", f64(q), pool, 0, tab, lens, range(len(lens)), D ** -0.5, 0, None)
 
 
 # ---------------------------------------------------------------------------------------------------------------
