@@ -268,6 +268,10 @@ int qpack_kv_read(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_
  * Sums, softmax statistics and accumulators are fp32; queries and probabilities enter the tensor cores as two 16-bit
  * terms each (22 bits) where the pool is 8-bit or fp16, as three (24) and two (16) where it is bf16. An empty range
  * gives out = 0 and lse = -inf.
+ * The formula is for finite keys and values (a value above 65504 in an fp16 pool, or a scale times a code, is infinite).
+ * A key that is not may make the heads of its key/value head NaN in its row, even where the formula gives it no weight; a
+ * value that is not makes its element of their outputs infinite or NaN. Nothing else changes. Slots that hold no token
+ * of the range may hold anything. A query that is not finite makes its own head NaN.
  *  q     [B, ldq] of dtype qdt, q_heads * dim elements a row, 16-byte aligned, ldq a multiple of 8; q_heads a multiple
  *        of the pool's heads, at most 65536
  *  rope  as in qpack_kv_append, applied to q at position L - 1 (NULL: q as it is)

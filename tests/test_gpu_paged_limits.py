@@ -85,6 +85,46 @@ def test_attend_bf16_magnitudes(qpg, what, D, G):
     check_attend(out, lse, "f32", "bf16", f64(q), pool, 0, tab, lens, range(len(lens)), D ** -0.5, 0, None)
 
 
+@pytest.mark.parametrize("kind", ["i8", "f16", "bf16"])
+@pytest.mark.parametrize("D,G,window,rope", [(64, 3, 0, False), (128, 8, 0, True), (128, 11, 300, False), (256, 4, 0, False), (64, 16, 0, True)])
+def test_attend_infinite_elements_stay_where_they_are(qpg, kind, D, G, window, rope):
+    """A key that is not finite (fp16(scale * code) among them) reaches the heads of its key/value head in its row, a value
+    that is not finite its own element of these; all else keeps its bits."""
+    T, H, lens = 16, 4, [1, 2, 40, 700, 9000, 33]
+    pages = pages_for(lens, T)
+    pool = make_pool(qpg, kind, 2, pages, H, T, D, 21)
+    tab, tables = make_tables(qpg, lens, T, pages, 22)
+    q = torch.randn((len(lens), H * G, D), device="cuda")
+    call = dict(window=window, rope=torch.from_numpy(rope_table(max(lens), D, 1)).cuda() if rope else None)
+    outs, lses = ([torch.empty(s, device="cuda") for _ in range(2)] for s in (q.shape, q.shape[:2]))
+    qpg.qpack_kv_attend(pool, 1, tables, q, out=outs[0], lse=lses[0], **call)
+    rng = np.random.default_rng(D + G)
+    same, odd = torch.ones(q.shape, dtype=torch.bool), torch.zeros(q.shape, dtype=torch.bool)
+    same_lse = torch.ones(q.shape[:2], dtype=torch.bool)
+    for s, n in enumerate(lens[:-1]):                       # key/value head 0: a key, 1: a value, 2: both, 3: neither
+        for h, what in ((0, "k"), (1, "v"), (2, "kv")):
+            for x in what:
+                t, d, sign = int(rng.integers(max(0, n - 300), n)), int(rng.integers(0, D)), rng.choice([-1.0, 1.0])
+                at, heads = (1, int(tab[s, t // T]), h, t % T), slice(h * G, (h + 1) * G)
+                codes, scales = (pool.k, pool.k_scales) if x == "k" else (pool.v, pool.v_scales)
+                if kind == "i8":
+                    codes[at][d // 32 * 32:d // 32 * 32 + 32] = 0
+                    codes[at][d], scales[at][d // 32] = int(127 * sign), 65504.0
+                    if x == "v":                            # the group's other values changed too
+                        same[s, heads, d // 32 * 32:d // 32 * 32 + 32] = False
+                else:
+                    codes[at][d] = float(rng.choice(["inf", "nan"])) * sign
+                if x == "v":
+                    same[s, heads, d], odd[s, heads, d] = False, True
+                else:
+                    same[s, heads], same_lse[s, heads] = False, False
+    for _ in range(2):                                      # the workspace is as it was
+        qpg.qpack_kv_attend(pool, 1, tables, q, out=outs[1], lse=lses[1], **call)
+    assert qpg.qpack_fetch_fault_flags() == 0
+    assert torch.equal(outs[0].cpu()[same], outs[1].cpu()[same]) and torch.equal(lses[0].cpu()[same_lse], lses[1].cpu()[same_lse])
+    assert not torch.isfinite(outs[1].cpu()[odd]).any() and torch.isfinite(outs[0]).all()
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # append
 # ---------------------------------------------------------------------------------------------------------------
