@@ -257,12 +257,12 @@ struct Row {
 template <int TOK> __device__ __forceinline__ Row row_of(const Params &p, int b, int *fault) {
     Row r;
     const AttendArgs &a = p.a;
-    const int seq = a.seqs ? __ldg(a.seqs + p.row0 + b) : p.row0 + b;
+    const int seq = a.seqs ? a.seqs[p.row0 + b] : p.row0 + b;
     int64_t len = 0;
     const bool known = seq >= 0 && seq < a.t.seqs;
     bool bad = !known;
     if (known) {
-        len = __ldg(a.t.lens + seq);
+        len = a.t.lens[seq];
         const int64_t cap = int64_t(a.t.max_pages) * a.pool.page_tokens, top = cap < 0x7FFFFFFF ? cap : 0x7FFFFFFF;
         bad = len < 0 || len > top;
         len = len < 0 ? 0 : (len > top ? top : len);
@@ -415,7 +415,9 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
     const int T = a.pool.page_tokens, shift = 31 - __clz(T);
 
     pdl_launch_dependents();
-    pdl_wait();                                            // inputs, cache and workspace may be the previous grid's
+    // Inputs, cache and workspace may be the previous grid's, lengths and tables among them: none of what is loaded below is
+    // read-only for as long as this grid lives, and all of it is read by plain loads.
+    pdl_wait();
 
     // -- the rows' tiles, and this block's share of them ------------------------------------------------------
     // Up to 32 rows are added up by every warp for itself (all write the same sums): no barrier before the copies (one
@@ -504,7 +506,7 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
         const bool large = T >= TOK;
         auto page_of = [&](const Cursor &c) {
             const unsigned t = c.row.base + c.ti * TOK + (large ? 0 : lane % TOK);
-            return large || (t >= c.row.lo && t < c.row.len) ? __ldg(c.row.table + (t >> shift)) : -1;
+            return large || (t >= c.row.lo && t < c.row.len) ? c.row.table[t >> shift] : -1;
         };
         int entry = page_of(ci);
         // Starts the copies of the cursor's tile into a stage: chunk i * 32 + lane of the tile goes to its row, at its
@@ -637,8 +639,8 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                     for (int c = 0; c < CH / 2; ++c)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            co[c][e] = __ldg(reinterpret_cast<const float2 *>(row + 16 * c + e * gap));
-                            si[c][e] = __ldg(reinterpret_cast<const float2 *>(row + D / 2 + 16 * c + e * gap));
+                            co[c][e] = *reinterpret_cast<const float2 *>(row + 16 * c + e * gap);
+                            si[c][e] = *reinterpret_cast<const float2 *>(row + D / 2 + 16 * c + e * gap);
                         }
                 };
                 // The cache's copies are started behind these loads: before them, they held them up (by 2 us, of which

@@ -58,13 +58,13 @@ struct Place {
 // First the sequence and the position, loaded together where both are given.
 __device__ __forceinline__ int64_t spot_of(const AppendArgs &a, int64_t i, Place &p) {
     p = {-1, -1, 0};
-    const int64_t seq = a.seqs ? int64_t(__ldg(a.seqs + i)) : i;
-    if (a.pos) p.pos = __ldg(a.pos + i);
+    const int64_t seq = a.seqs ? int64_t(a.seqs[i]) : i;
+    if (a.pos) p.pos = a.pos[i];
     if (seq < 0 || seq >= a.t.seqs) {
         p.pos = -1;
         return -1;
     }
-    if (!a.pos) p.pos = __ldg(a.t.lens + seq) - 1;
+    if (!a.pos) p.pos = a.t.lens[seq] - 1;
     p.slot = p.pos & (a.pool.page_tokens - 1);
     return seq;
 }
@@ -72,21 +72,22 @@ __device__ __forceinline__ void page_of(const AppendArgs &a, int64_t seq, Place 
     bool bad = seq < 0;
     if (p.pos >= 0) {
         const int col = p.pos >> (31 - __clz(a.pool.page_tokens));
-        p.page = col < a.t.max_pages ? __ldg(a.t.tables + seq * a.t.stride + col) : -1;
+        p.page = col < a.t.max_pages ? a.t.tables[seq * a.t.stride + col] : -1;
         bad = p.page < 0 || p.page >= a.pool.pages;
         if (bad) p.page = -1;
     }
     if (bad && report) atomicOr(&g_fault_paged, FAULT_PAGE);
 }
 
-// Eight consecutive elements as loaded, and as fp32.
+// Eight consecutive elements as loaded, and as fp32. Plain loads, as of all that the previous grid may have written: these
+// kernels begin while it runs.
 template <int DT> struct Raw { uint32_t w[DT == DT_F32 ? 8 : 4]; };
 template <int DT> __device__ __forceinline__ void load_raw(const void *p, int64_t idx, Raw<DT> &r) {
     const uint4 *q = DT == DT_F32 ? reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + idx)
                                   : reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + idx);
 #pragma unroll
     for (int i = 0; i < (DT == DT_F32 ? 2 : 1); ++i) {
-        const uint4 v = __ldg(q + i);
+        const uint4 v = q[i];
         r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
     }
 }
@@ -126,8 +127,13 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, DT == DT_F32 ? 5 : KT == QPACK
     float c[8] = {1, 1, 1, 1, 1, 1, 1, 1}, s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (a.rope && pl.pos >= 0 && pl.pos < a.rope_rows) {
         const int64_t at = int64_t(pl.pos) * D + (sub % (LPR / 2)) * 8;
-        load8<DT_F32>(a.rope, at, c);
-        load8<DT_F32>(a.rope, at + D / 2, s);
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(a.rope + at + e);
+            const float4 y = *reinterpret_cast<const float4 *>(a.rope + at + D / 2 + e);
+            c[e] = x.x, c[e + 1] = x.y, c[e + 2] = x.z, c[e + 3] = x.w;
+            s[e] = y.x, s[e + 1] = y.y, s[e + 2] = y.z, s[e + 3] = y.w;
+        }
     }
     page_of(a, seq, pl, lane == 0);
     if (pl.page < 0) return;
