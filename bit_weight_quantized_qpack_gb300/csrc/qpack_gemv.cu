@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(G1_THREADS, 1)
             for (int t = 0; t < 4; ++t) raw[cc][t] = make_uint4(0u, 0u, 0u, 0u);
             if (u < U) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t) raw[cc][t] = __ldg(xg + 4 * u + t);
+                for (int t = 0; t < 4; ++t) raw[cc][t] = xg[4 * u + t];
             }
         }
         bool bad = false;
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(G1_THREADS, 1)
                     } else {
                         const uint4 *xrow = xg + (int64_t(m) * a.ldx) / 8 + 4 * u;
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) raw[d][t] = __ldg(xrow + t);
+                        for (int t = 0; t < 4; ++t) raw[d][t] = xrow[t];
                     }
                 }
             }

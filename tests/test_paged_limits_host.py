@@ -3,11 +3,12 @@ import os
 
 
 def test_no_read_only_loads_in_dependent_kernels():
-    """The paged cache's kernels are launched while the grid before them runs and wait for it themselves. What it writes
-    (lengths, tables, queries, new rows) is not read-only during their life, so none of them uses read-only loads."""
+    """The decode product and the paged cache's kernels are launched while the grid before them runs and wait for it
+    themselves. What it writes (activations, lengths, tables, queries, new rows) is not read-only during their life, so none
+    of them uses read-only loads."""
     import re
     csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_weight_quantized_qpack_gb300", "csrc")
-    for name in ("qpack_attend.cuh", "qpack_paged.cu", "qpack_paged.cuh"):
+    for name in ("qpack_attend.cuh", "qpack_paged.cu", "qpack_paged.cuh", "qpack_gemv.cu"):
         with open(os.path.join(csrc, name), encoding="utf-8") as f:
             text = f.read()
         assert not re.search(r"__ldg|ld\.global\.nc|\bload8<", text), name
