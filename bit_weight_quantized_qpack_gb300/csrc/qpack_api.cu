@@ -518,11 +518,7 @@ const char *qpack_status_string(int status) {
 int qpack_fetch_fault_flags(int32_t *flags) {
     if (!flags) return QPACK_ERR_ARG;
     *flags = 0;
-    cudaError_t e = fetch_fault_gemv(flags);
-    if (e == cudaSuccess) e = fetch_fault_prefill(flags);
-    if (e == cudaSuccess) e = fetch_fault_paged(flags);
-    if (e == cudaSuccess) e = fetch_fault_attend(flags);
-    return cuda_status(e);
+    return cuda_status(fetch_faults(flags));
 }
 
 int qpack_set_option(int option, int value) {

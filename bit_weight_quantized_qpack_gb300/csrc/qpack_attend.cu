@@ -13,9 +13,9 @@ template <> cudaError_t launch<QPACK_KV_BF16>(const AttendArgs &, cudaStream_t);
 template <> int64_t workspace<QPACK_KV_I8>(const qpack_kv_pool_t &, int, int);
 template <> int64_t workspace<QPACK_KV_F16>(const qpack_kv_pool_t &, int, int);
 template <> int64_t workspace<QPACK_KV_BF16>(const qpack_kv_pool_t &, int, int);
-template <> cudaError_t fetch_fault<QPACK_KV_I8>(int32_t *);
-template <> cudaError_t fetch_fault<QPACK_KV_F16>(int32_t *);
-template <> cudaError_t fetch_fault<QPACK_KV_BF16>(int32_t *);
+template <> cudaError_t fault_word<QPACK_KV_I8>(int **);
+template <> cudaError_t fault_word<QPACK_KV_F16>(int **);
+template <> cudaError_t fault_word<QPACK_KV_BF16>(int **);
 }  // namespace attend
 
 int64_t kv_attend_workspace(const qpack_kv_pool_t &pool, int, int q_heads) {
@@ -33,10 +33,10 @@ cudaError_t launch_kv_attend(const AttendArgs &a, cudaStream_t s) {
     return attend::launch<QPACK_KV_BF16>(a, s);
 }
 
-cudaError_t fetch_fault_attend(int32_t *flags) {
-    cudaError_t e = attend::fetch_fault<QPACK_KV_I8>(flags);
-    if (e == cudaSuccess) e = attend::fetch_fault<QPACK_KV_F16>(flags);
-    if (e == cudaSuccess) e = attend::fetch_fault<QPACK_KV_BF16>(flags);
+cudaError_t fault_words_attend(int **words) {
+    cudaError_t e = attend::fault_word<QPACK_KV_I8>(words);
+    if (e == cudaSuccess) e = attend::fault_word<QPACK_KV_F16>(words + 1);
+    if (e == cudaSuccess) e = attend::fault_word<QPACK_KV_BF16>(words + 2);
     return e;
 }
 

@@ -1127,7 +1127,7 @@ template <int KT, int D, int NT> cudaError_t run(const AttendArgs &a, cudaStream
 // What each cache type's translation unit defines.
 template <int KT> cudaError_t launch(const AttendArgs &a, cudaStream_t s);
 template <int KT> int64_t workspace(const qpack_kv_pool_t &pool, int q_heads, int grid);
-template <int KT> cudaError_t fetch_fault(int32_t *flags);
+template <int KT> cudaError_t fault_word(int **word);
 
 #define QPACK_ATTEND_TYPE(KT)                                                                                         \
     namespace qpack {                                                                                                 \
@@ -1144,13 +1144,8 @@ template <int KT> cudaError_t fetch_fault(int32_t *flags);
         if (pool.dim == 128) return nt == 2 ? part_bytes<KT, 128, 2>(grid) : part_bytes<KT, 128, 1>(grid);            \
         return part_bytes<KT, 256, 1>(grid);                                                                          \
     }                                                                                                                 \
-    template <> cudaError_t fetch_fault<KT>(int32_t * flags) {                                                        \
-        int v = 0;                                                                                                    \
-        const cudaError_t e = cudaMemcpyFromSymbol(&v, g_fault_attend, sizeof(int));                                  \
-        if (e != cudaSuccess) return e;                                                                               \
-        *flags |= v;                                                                                                  \
-        const int zero = 0;                                                                                           \
-        return cudaMemcpyToSymbol(g_fault_attend, &zero, sizeof(int));                                                \
+    template <> cudaError_t fault_word<KT>(int **word) {                                                              \
+        return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_fault_attend);                                 \
     }                                                                                                                 \
     }                                                                                                                 \
     }

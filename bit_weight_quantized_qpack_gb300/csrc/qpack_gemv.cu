@@ -991,13 +991,6 @@ cudaError_t launch_gemv(int fmt, const GemvArgs &a, cudaStream_t s) {
     }
 }
 
-cudaError_t fetch_fault_gemv(int32_t *flags) {
-    int v = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_fault_gemv, sizeof(int));
-    if (e != cudaSuccess) return e;
-    *flags |= v;
-    const int zero = 0;
-    return cudaMemcpyToSymbol(g_fault_gemv, &zero, sizeof(int));
-}
+cudaError_t fault_word_gemv(int **word) { return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_fault_gemv); }
 
 }  // namespace qpack

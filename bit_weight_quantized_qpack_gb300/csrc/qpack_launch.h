@@ -72,8 +72,9 @@ cudaError_t launch_prefill(int fmt, const PrefillArgs &a, cudaStream_t s);
 // 8-bit KV cache (qpack_kv.cu); n a positive multiple of 32, pointers checked by the caller.
 cudaError_t launch_kv_quantize(const uint16_t *v, int64_t n, int8_t *q, uint16_t *scales, cudaStream_t s);
 cudaError_t launch_kv_dequant(const int8_t *q, const uint16_t *scales, int64_t n, uint16_t *out, cudaStream_t s);
-cudaError_t fetch_fault_gemv(int32_t *flags);
-cudaError_t fetch_fault_prefill(int32_t *flags);
+// Addresses of the translation units' fault words on the current device.
+cudaError_t fault_word_gemv(int **word);
+cudaError_t fault_word_prefill(int **word);
 
 // Paged KV cache (qpack_paged.cu, qpack_attend.cu). The pool and the tables as the C ABI has them, checked.
 struct AppendArgs {
@@ -119,8 +120,9 @@ cudaError_t launch_kv_compact(const qpack_kv_pool_t &p, const qpack_kv_tables_t 
 cudaError_t launch_kv_copy_pages(const qpack_kv_pool_t &p, const int32_t *src, const int32_t *dst, int64_t n,
                                  cudaStream_t s);
 int64_t kv_page_workspace(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t);
-cudaError_t fetch_fault_paged(int32_t *flags);
-cudaError_t fetch_fault_attend(int32_t *flags);
+cudaError_t fault_word_paged(int **word);
+cudaError_t fault_words_attend(int **words);    // one a cache type
+cudaError_t fetch_faults(int32_t *flags);
 
 int num_sms();
 int weight_prefetch_enabled();   // per-device option QPACK_OPT_WEIGHT_PREFETCH

@@ -748,13 +748,6 @@ cudaError_t launch_kv_copy_pages(const qpack_kv_pool_t &p, const int32_t *src, c
     return run_copy(p, PageWs{}, src, dst, n, n, nullptr, qpack_kv_tables_t{}, nullptr, s);
 }
 
-cudaError_t fetch_fault_paged(int32_t *flags) {
-    int v = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_fault_paged, sizeof(int));
-    if (e != cudaSuccess) return e;
-    *flags |= v;
-    const int zero = 0;
-    return cudaMemcpyToSymbol(g_fault_paged, &zero, sizeof(int));
-}
+cudaError_t fault_word_paged(int **word) { return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_fault_paged); }
 
 }  // namespace qpack

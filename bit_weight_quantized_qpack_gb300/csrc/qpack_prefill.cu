@@ -977,13 +977,6 @@ cudaError_t launch_prefill(int fmt, const PrefillArgs &a, cudaStream_t s) {
     }
 }
 
-cudaError_t fetch_fault_prefill(int32_t *flags) {
-    int v = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_fault_prefill, sizeof(int));
-    if (e != cudaSuccess) return e;
-    *flags |= v;
-    const int zero = 0;
-    return cudaMemcpyToSymbol(g_fault_prefill, &zero, sizeof(int));
-}
+cudaError_t fault_word_prefill(int **word) { return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_fault_prefill); }
 
 }  // namespace qpack

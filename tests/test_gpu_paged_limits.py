@@ -237,3 +237,23 @@ def test_page_operators_other_stream_default_workspace(qpg):
         assert sim.compact() > 0
         s.synchronize()
         same_state(qpg, pool, tables, sim)
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# fault word
+# ---------------------------------------------------------------------------------------------------------------
+def test_faults_are_fetched_once(qpg):
+    """Every kernel's reports reach the fault word and are gone once they are fetched."""
+    for kind in ("i8", "f16", "bf16"):
+        pool = make_pool(qpg, kind, 1, 5, 1, 16, 64, 1)
+        tab, tables = make_tables(qpg, [20], 16, 5, 2)
+        q, bad = torch.randn((1, 2, 64), device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+        qpg.qpack_kv_attend(pool, 0, tables, q, seqs=bad)
+        assert [qpg.qpack_fetch_fault_flags() for _ in range(2)] == [qpg.FAULT_PAGE, 0]
+        qpg.qpack_kv_attend(pool, 0, tables, q, seqs=bad)
+        tables.refs = torch.ones(5, dtype=torch.int32, device="cuda")
+        full = qpg.KVTables(tables.tables, tables.lens, tables.refs)
+        qpg.qpack_kv_reserve(pool, full, 0 * bad, 16 * bad)
+        assert [qpg.qpack_fetch_fault_flags() for _ in range(2)] == [qpg.FAULT_PAGE | qpg.FAULT_NO_PAGES, 0]
+        qpg.qpack_kv_attend(pool, 0, tables, q)
+        assert qpg.qpack_fetch_fault_flags() == 0
