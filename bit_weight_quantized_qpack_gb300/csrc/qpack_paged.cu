@@ -354,27 +354,27 @@ cudaError_t rows_kind(const AppendArgs &a, bool read, cudaStream_t s) {
 constexpr int PLAN_THREADS = 1024;
 
 // Exclusive prefix sum of one value a thread over the block; *total gets the sum. Every thread calls it.
-__device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
+template <class V> __device__ __forceinline__ V block_scan(V v, V *warp_sums, V *total) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    int x = v;
+    V x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        const V y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     if (lane == 31) warp_sums[w] = x;
     __syncthreads();
     if (w == 0) {
-        int y = lane < nw ? warp_sums[lane] : 0;
+        V y = lane < nw ? warp_sums[lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int z = __shfl_up_sync(0xffffffffu, y, o);
+            const V z = __shfl_up_sync(0xffffffffu, y, o);
             if (lane >= o) y += z;
         }
         if (lane < nw) warp_sums[lane] = y;
     }
     __syncthreads();
-    const int before = w ? warp_sums[w - 1] : 0;
+    const V before = w ? warp_sums[w - 1] : 0;
     *total = warp_sums[nw - 1];
     __syncthreads();                                       // warp_sums may be written again
     return before + x - v;
@@ -420,52 +420,59 @@ __host__ __device__ inline PageWs page_ws(void *ws, int64_t pages) {
 }
 
 // One block: the pages that the requests need, in order, are the lowest-numbered free ones. The offsets of the requests
-// (how many pages those before need) stay in shared memory; the free pages are ranked chunk by chunk and each finds its
-// request by a binary search over the offsets.
+// (how many pages those before need) stay in shared memory, cut to one more than there are pages: what is behind is
+// refused alike, and 4096 requests of 2^31 pages fit. The free pages are ranked chunk by chunk and each finds its request by
+// a binary search over the offsets.
 __global__ void __launch_bounds__(PLAN_THREADS) kv_reserve_kernel(qpack_kv_tables_t t, int page_tokens, const int *seqs,
                                                                   const int *add, int n, int64_t pages) {
-    __shared__ int sums[32];
-    __shared__ int off[4097], who[4096];                   // pages needed before request i, its row of the table
+    __shared__ long long needs[32];
+    __shared__ int sums[32], who[4096];                    // a request's row of the table
+    __shared__ unsigned off[4097];                         // pages needed before request i
     auto first_col = [&](int seq) {                        // the column of its first new page (lens is raised last)
         const int64_t old = t.lens[seq] < 0 ? 0 : t.lens[seq];
         return (old + page_tokens - 1) / page_tokens;
     };
-    int carry = 0, tot;
+    auto behind = [&](int seq, int i) {                    // and the one behind its last
+        return (int64_t(t.lens[seq] < 0 ? 0 : t.lens[seq]) + add[i] + page_tokens - 1) / page_tokens;
+    };
+    const long long top = pages + 1;
+    long long want = 0, all;
+    int tot;
     pdl_launch_dependents();
     pdl_wait();
     for (int i0 = 0; i0 < n; i0 += blockDim.x) {
         const int i = i0 + threadIdx.x;
-        int need = 0, s = -1;
+        long long need = 0;
+        int s = -1;
         if (i < n) {
             s = seqs[i];
             if (s >= 0 && s < t.seqs && add[i] >= 0) {
-                const int64_t neu = int64_t(t.lens[s] < 0 ? 0 : t.lens[s]) + add[i];
-                const int64_t last = (neu + page_tokens - 1) / page_tokens;
+                const int64_t neu = int64_t(t.lens[s] < 0 ? 0 : t.lens[s]) + add[i], last = behind(s, i);
                 if (last > t.max_pages || neu > 0x7FFFFFFF)
                     s = -2;                                // its row cannot hold them
                 else
-                    need = int(last - first_col(s));
+                    need = last - first_col(s);
             } else {
                 s = s < 0 ? -1 : -3;
             }
         }
-        const int before = carry + block_scan(need, sums, &tot);
+        const long long before = want + block_scan(need, needs, &all);
         if (i < n) {
-            off[i] = before;
+            off[i] = unsigned(min(before, top));
             who[i] = s;
             if (s == -2) atomicOr(&g_fault_paged, FAULT_NO_PAGES);
             if (s == -3) atomicOr(&g_fault_paged, FAULT_PAGE);
         }
-        carry += tot;
+        want += all;
     }
-    if (threadIdx.x == 0) off[n] = carry;
+    want = min(want, top);
+    if (threadIdx.x == 0) off[n] = unsigned(want);
     __syncthreads();
-    const int want = carry;
-    int found = 0;
+    int64_t found = 0;
     for (int64_t p0 = 0; p0 < pages && found < want; p0 += blockDim.x * SCAN) {
         const int64_t p = p0 + threadIdx.x * SCAN;
         unsigned m = free_pages(t.refs, p, pages);
-        int rank = found + block_scan(__popc(m), sums, &tot);
+        int64_t rank = found + block_scan(__popc(m), sums, &tot);
         for (; m && rank < want; m &= m - 1, ++rank) {
             int lo = 0, hi = n;                            // off[lo] <= rank < off[lo + 1]
             while (hi - lo > 1) {
@@ -485,12 +492,11 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_reserve_kernel(qpack_kv_table
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const int s = who[i];
         if (s < 0) continue;
-        const int need = off[i + 1] - off[i];
-        if (off[i + 1] <= found || need == 0) {
+        if (off[i + 1] <= found || behind(s, i) == first_col(s)) {
             t.lens[s] = (t.lens[s] < 0 ? 0 : t.lens[s]) + add[i];
         } else {
             atomicOr(&g_fault_paged, FAULT_NO_PAGES);
-            for (int j = off[i]; j < found && j < off[i + 1]; ++j) {
+            for (int64_t j = off[i]; j < found && j < off[i + 1]; ++j) {
                 int *e = t.tables + int64_t(s) * t.stride + first_col(s) + (j - off[i]);
                 t.refs[*e] = 0;
                 *e = -1;

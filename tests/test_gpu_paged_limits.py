@@ -257,3 +257,34 @@ def test_faults_are_fetched_once(qpg):
         assert [qpg.qpack_fetch_fault_flags() for _ in range(2)] == [qpg.FAULT_PAGE | qpg.FAULT_NO_PAGES, 0]
         qpg.qpack_kv_attend(pool, 0, tables, q)
         assert qpg.qpack_fetch_fault_flags() == 0
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# page operators
+# ---------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("pages", [8, 5000])
+def test_reserve_more_pages_than_32_bits_count(qpg, pages):
+    """Requests whose pages together pass 2^31 (and 2^32): refused, each without a trace; those before them and those that
+    need no page stand."""
+    MP = 1 << 30
+    pool = make_pool(qpg, "i8", 1, pages, 1, 1, 64, 1)
+    tab = torch.empty((6, MP), dtype=torch.int32, device="cuda")
+    tab[:, :pages + 8] = -1
+    lens = torch.tensor([0, 0, 0, 2, 0, 0], dtype=torch.int32, device="cuda")
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    tab[3, :2], refs[:2] = torch.tensor([1, 0], dtype=torch.int32, device="cuda"), 1
+    tables = qpg.KVTables(tab, lens, refs)
+    seqs = torch.tensor([4, 0, 1, 3, 2, 5], dtype=torch.int32, device="cuda")
+    for second in (MP, MP - 5):                             # the sum of the large ones: 2^31, or some less; then past 2^32
+        add = torch.tensor([3, MP, second, 0, 7, MP], dtype=torch.int32, device="cuda")
+        qpg.qpack_kv_reserve(pool, tables, seqs, add)
+        assert qpg.qpack_fetch_fault_flags() == qpg.FAULT_NO_PAGES
+        assert lens.tolist() == [0, 0, 0, 2, 3, 0] and refs.tolist() == [1] * 5 + [0] * (pages - 5)
+        assert tab[4, :4].tolist() == [2, 3, 4, -1] and tab[3, :3].tolist() == [1, 0, -1]
+        assert (tab[[0, 1, 2, 5], :pages + 8] == -1).all()
+        qpg.qpack_kv_free(qpg.KVTables(tab[:, :pages], lens, refs), torch.tensor([4], dtype=torch.int32, device="cuda"))
+        assert qpg.qpack_fetch_fault_flags() == 0
+    big = 4096                                              # as many requests as a call takes, all of one row
+    qpg.qpack_kv_reserve(pool, tables, torch.full((big,), -1, dtype=torch.int32, device="cuda"),
+                         torch.full((big,), MP, dtype=torch.int32, device="cuda"))
+    assert qpg.qpack_fetch_fault_flags() == 0 and lens.tolist() == [0, 0, 0, 2, 0, 0]
