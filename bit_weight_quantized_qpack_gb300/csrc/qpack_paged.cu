@@ -488,21 +488,22 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_reserve_kernel(qpack_kv_table
     }
     if (found > want) found = want;
     __syncthreads();
-    // Requests up to the last that the free pages cover stand; a request that they cover in part gives its pages back.
+    // Requests up to the last that the free pages cover stand; one that they cover in part gives its pages back, before any
+    // length is raised: a sequence listed twice, which no call may do, then still finds the places that it wrote to.
+    auto stands = [&](int i) { return off[i + 1] <= found || behind(who[i], i) == first_col(who[i]); };
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const int s = who[i];
-        if (s < 0) continue;
-        if (off[i + 1] <= found || behind(s, i) == first_col(s)) {
-            t.lens[s] = (t.lens[s] < 0 ? 0 : t.lens[s]) + add[i];
-        } else {
-            atomicOr(&g_fault_paged, FAULT_NO_PAGES);
-            for (int64_t j = off[i]; j < found && j < off[i + 1]; ++j) {
-                int *e = t.tables + int64_t(s) * t.stride + first_col(s) + (j - off[i]);
-                t.refs[*e] = 0;
-                *e = -1;
-            }
+        if (s < 0 || stands(i)) continue;
+        atomicOr(&g_fault_paged, FAULT_NO_PAGES);
+        for (int64_t j = off[i]; j < found && j < off[i + 1]; ++j) {
+            int *e = t.tables + int64_t(s) * t.stride + first_col(s) + (j - off[i]);
+            t.refs[*e] = 0;
+            *e = -1;
         }
     }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+        if (who[i] >= 0 && stands(i)) t.lens[who[i]] = (t.lens[who[i]] < 0 ? 0 : t.lens[who[i]]) + add[i];
 }
 
 // One block a child. Its place among the children that need a page is a count over the parents before it, its page the

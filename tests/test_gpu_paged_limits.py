@@ -288,3 +288,22 @@ def test_reserve_more_pages_than_32_bits_count(qpg, pages):
     qpg.qpack_kv_reserve(pool, tables, torch.full((big,), -1, dtype=torch.int32, device="cuda"),
                          torch.full((big,), MP, dtype=torch.int32, device="cuda"))
     assert qpg.qpack_fetch_fault_flags() == 0 and lens.tolist() == [0, 0, 0, 2, 0, 0]
+
+
+def test_reserve_listed_twice_stays_in_its_row(qpg):
+    """A sequence listed twice, against the rules, with pages for one request and part of the other: nothing outside its row,
+    the reference counts and the lengths is touched."""
+    pages, MP, n = 3000, 2000, 600
+    pool = make_pool(qpg, "i8", 1, pages, 1, 1, 64, 1)
+    for add in ([1200, 1990], [1, 2000] * (n // 2), [5] * n + [1999]):
+        tab = torch.full((5, MP), -7, dtype=torch.int32, device="cuda")
+        tab[2] = -1
+        lens, refs = torch.zeros(5, dtype=torch.int32, device="cuda"), torch.zeros(pages + 64, dtype=torch.int32, device="cuda")
+        refs[pages:] = -9
+        tables = qpg.KVTables(tab, lens, refs[:pages])
+        qpg.qpack_kv_reserve(pool, tables, torch.full((len(add),), 2, dtype=torch.int32, device="cuda"),
+                             torch.tensor(add, dtype=torch.int32, device="cuda"))
+        assert qpg.qpack_fetch_fault_flags() == qpg.FAULT_NO_PAGES
+        assert (tab[[0, 1, 3, 4]] == -7).all() and (refs[pages:] == -9).all()
+        assert lens[[0, 1, 3, 4]].tolist() == [0] * 4 and set(refs[:pages].unique().tolist()) <= {0, 1}
+        assert ((tab[2] >= -1) & (tab[2] < pages)).all()
