@@ -429,13 +429,13 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_reserve_kernel(qpack_kv_table
     __shared__ int sums[32], who[4096];                    // a request's row of the table
     __shared__ unsigned off[4097];                         // pages needed before request i
     auto first_col = [&](int seq) {                        // the column of its first new page (lens is raised last)
-        const int64_t old = t.lens[seq] < 0 ? 0 : t.lens[seq];
-        return (old + page_tokens - 1) / page_tokens;
+        return (int64_t(t.lens[seq]) + page_tokens - 1) / page_tokens;
     };
     auto behind = [&](int seq, int i) {                    // and the one behind its last
-        return (int64_t(t.lens[seq] < 0 ? 0 : t.lens[seq]) + add[i] + page_tokens - 1) / page_tokens;
+        return (int64_t(t.lens[seq]) + add[i] + page_tokens - 1) / page_tokens;
     };
     const long long top = pages + 1;
+    const int64_t longest = int64_t(t.max_pages) * page_tokens;
     long long want = 0, all;
     int tot;
     pdl_launch_dependents();
@@ -446,8 +446,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_reserve_kernel(qpack_kv_table
         int s = -1;
         if (i < n) {
             s = seqs[i];
-            if (s >= 0 && s < t.seqs && add[i] >= 0) {
-                const int64_t neu = int64_t(t.lens[s] < 0 ? 0 : t.lens[s]) + add[i], last = behind(s, i);
+            if (s >= 0 && s < t.seqs && add[i] >= 0 && t.lens[s] >= 0 && t.lens[s] <= longest) {
+                const int64_t neu = int64_t(t.lens[s]) + add[i], last = behind(s, i);
                 if (last > t.max_pages || neu > 0x7FFFFFFF)
                     s = -2;                                // its row cannot hold them
                 else
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_reserve_kernel(qpack_kv_table
     }
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += blockDim.x)
-        if (who[i] >= 0 && stands(i)) t.lens[who[i]] = (t.lens[who[i]] < 0 ? 0 : t.lens[who[i]]) + add[i];
+        if (who[i] >= 0 && stands(i)) t.lens[who[i]] += add[i];
 }
 
 // One block a child. Its place among the children that need a page is a count over the parents before it, its page the
@@ -517,11 +517,10 @@ __global__ void __launch_bounds__(256) kv_fork_kernel(qpack_kv_tables_t t, int p
     pdl_wait();
     const int i = blockIdx.x;
     const int s = src[i], d = dst[i];
-    auto len_of = [&](int q) {
-        if (q < 0 || q >= t.seqs) return 0;
-        const int64_t l = t.lens[q], top = int64_t(t.max_pages) * page_tokens;
-        return int(l < 0 ? 0 : (l > top ? top : l));
+    auto known = [&](int q) {                              // a sequence, with a length that its row can hold
+        return q >= 0 && q < t.seqs && t.lens[q] >= 0 && t.lens[q] <= int64_t(t.max_pages) * page_tokens;
     };
+    auto len_of = [&](int q) { return known(q) ? t.lens[q] : 0; };
     int before = 0, tot;
     int mine = 0;
     for (int j = threadIdx.x; j < i; j += blockDim.x) mine += (len_of(src[j]) & (page_tokens - 1)) != 0;
@@ -543,7 +542,7 @@ __global__ void __launch_bounds__(256) kv_fork_kernel(qpack_kv_tables_t t, int p
         }
         __syncthreads();
     }
-    const bool ok_seq = s >= 0 && s < t.seqs && d >= 0 && d < t.seqs;
+    const bool ok_seq = known(s) && d >= 0 && d < t.seqs;
     const int fresh = s_fresh;
     const bool grant = ok_seq && t.lens[d] == 0 && (rows == 0 || fresh >= 0);
     const int last = ok_seq && rows ? t.tables[int64_t(s) * t.stride + full] : -1;

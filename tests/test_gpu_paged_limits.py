@@ -307,3 +307,27 @@ def test_reserve_listed_twice_stays_in_its_row(qpg):
         assert (tab[[0, 1, 3, 4]] == -7).all() and (refs[pages:] == -9).all()
         assert lens[[0, 1, 3, 4]].tolist() == [0] * 4 and set(refs[:pages].unique().tolist()) <= {0, 1}
         assert ((tab[2] >= -1) & (tab[2] < pages)).all()
+
+
+def test_page_operators_lengths_out_of_range(qpg):
+    """Lengths that are negative or longer than the row: reported, and the request is left out; the others of the call stand."""
+    T, MP, pages = 16, 4, 40
+    pool = make_pool(qpg, "i8", 2, pages, 1, T, 64, 1)
+    for bad in (-1, -2 ** 31, MP * T + 1, 2 ** 31 - 1):
+        tables = qpg.alloc_kv_tables(6, MP, pages)
+        i = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+        qpg.qpack_kv_reserve(pool, tables, i(0, 1), i(20, 64))
+        tables.lens[2] = bad
+        before = tables.tables.clone()
+        qpg.qpack_kv_reserve(pool, tables, i(2, 0), i(5, 20))
+        assert qpg.qpack_fetch_fault_flags() == qpg.FAULT_PAGE
+        assert tables.lens.tolist() == [40, 64, bad, 0, 0, 0] and tables.tables[0].tolist() == [0, 1, 6, -1]
+        assert torch.equal(tables.tables[1:], before[1:]) and int(tables.refs.sum()) == 7
+        held = [t.clone() for t in (tables.tables, tables.refs)]
+        qpg.qpack_kv_fork(pool, tables, i(2, 2), i(3, 4))
+        assert qpg.qpack_fetch_fault_flags() == qpg.FAULT_PAGE and tables.lens.tolist() == [40, 64, bad, 0, 0, 0]
+        assert torch.equal(held[0], tables.tables) and torch.equal(held[1], tables.refs)
+        qpg.qpack_kv_fork(pool, tables, i(2, 0, 1), i(3, 4, 5))
+        assert qpg.qpack_fetch_fault_flags() == qpg.FAULT_PAGE
+        assert tables.lens.tolist() == [40, 64, bad, 0, 40, 64] and tables.tables[4].tolist() == [0, 1, 7, -1]
+        assert tables.tables[5].tolist() == tables.tables[1].tolist()
