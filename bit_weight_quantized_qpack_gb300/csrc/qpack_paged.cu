@@ -60,6 +60,7 @@ __device__ __forceinline__ int64_t spot_of(const AppendArgs &a, int64_t i, Place
     p = {-1, -1, 0};
     const int64_t seq = a.seqs ? int64_t(a.seqs[i]) : i;
     if (a.pos) p.pos = a.pos[i];
+    if (a.pos && p.pos < 0) return 0;                      // skipped, whatever its sequence
     if (seq < 0 || seq >= a.t.seqs) {
         p.pos = -1;
         return -1;

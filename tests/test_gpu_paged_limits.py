@@ -156,6 +156,24 @@ def test_append_saturated_scales(qpg, xdt, D, rope):
     assert qpg.qpack_fetch_fault_flags() == 0
 
 
+def test_skipped_tokens_of_no_sequence(qpg):
+    """A negative position skips a token whatever its sequence number (padding is often -1 in both): nothing is written, nothing
+    reported, and reading gives zeros."""
+    pool = make_pool(qpg, "i8", 1, 5, 2, 16, 64, 1)
+    tab, tables = make_tables(qpg, [20], 16, 5, 2)
+    i = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    x, seqs, pos = torch.randn((4, 2, 64), device="cuda"), i(-1, 0, 7, -2 ** 31), i(-1, 3, -5, -2 ** 31)
+    before = pool.k.clone()
+    qpg.qpack_kv_append(pool, 0, tables, x, x, seqs=seqs, pos=pos)
+    k, v = qpg.qpack_kv_read(pool, 0, tables, seqs, pos)
+    assert qpg.qpack_fetch_fault_flags() == 0
+    want = ref.values(*ref.quantize32(x[1:2].cpu().numpy()))[0]
+    for got in (k, v):
+        assert np.array_equal(f64(got[1]), want) and not got[[0, 2, 3]].any()
+    before[0, int(tab[0, 0]), :, 3] = pool.k[0, int(tab[0, 0]), :, 3]
+    assert torch.equal(before, pool.k)
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # another stream
 # ---------------------------------------------------------------------------------------------------------------
