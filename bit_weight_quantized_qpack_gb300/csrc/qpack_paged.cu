@@ -60,7 +60,10 @@ __device__ __forceinline__ int64_t spot_of(const AppendArgs &a, int64_t i, Place
     p = {-1, -1, 0};
     const int64_t seq = a.seqs ? int64_t(a.seqs[i]) : i;
     if (a.pos) p.pos = a.pos[i];
-    if (a.pos && p.pos < 0) return 0;                      // skipped, whatever its sequence
+    if (a.pos && p.pos < 0) {                              // skipped, whatever its sequence
+        p.pos = -1;
+        return 0;
+    }
     if (seq < 0 || seq >= a.t.seqs) {
         p.pos = -1;
         return -1;
@@ -70,7 +73,7 @@ __device__ __forceinline__ int64_t spot_of(const AppendArgs &a, int64_t i, Place
     return seq;
 }
 __device__ __forceinline__ void page_of(const AppendArgs &a, int64_t seq, Place &p, bool report) {
-    bool bad = seq < 0;
+    bool bad = seq < 0 || p.pos < -1;                      // a length below 0
     if (p.pos >= 0) {
         const int col = p.pos >> (31 - __clz(a.pool.page_tokens));
         p.page = col < a.t.max_pages ? a.t.tables[seq * a.t.stride + col] : -1;

@@ -174,6 +174,23 @@ def test_skipped_tokens_of_no_sequence(qpg):
     assert torch.equal(before, pool.k)
 
 
+def test_default_position_of_a_negative_length(qpg):
+    """A token at the last position of a sequence whose length is negative: left out and reported; of an empty one: skipped."""
+    pool = make_pool(qpg, "i8", 1, 5, 2, 16, 64, 1)
+    tab, tables = make_tables(qpg, [20, 3], 16, 5, 2)
+    x, before = torch.randn((2, 2, 64), device="cuda"), pool.k.clone()
+    before[0, int(tab[1, 0]), :, 2] = 0
+    for bad, flags in ((0, 0), (-1, 32), (-5, 32), (-2 ** 31, 32)):
+        tables.lens[0] = bad
+        qpg.qpack_kv_append(pool, 0, tables, x, x)
+        assert qpg.qpack_fetch_fault_flags() == flags, bad
+        k, v = qpg.qpack_kv_read(pool, 0, tables, n=2)
+        assert qpg.qpack_fetch_fault_flags() == flags and not k[0].any() and not v[0].any() and k[1].any()
+        after = pool.k.clone()
+        after[0, int(tab[1, 0]), :, 2] = 0
+        assert torch.equal(after, before)
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # another stream
 # ---------------------------------------------------------------------------------------------------------------
