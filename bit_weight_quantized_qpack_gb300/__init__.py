@@ -381,7 +381,9 @@ class KVPool:
 
 def alloc_kv_pool(kind, layers, pages, heads, page_tokens, dim, device="cuda") -> KVPool:
     """An empty pool of the kind KV_I8, KV_F16 or KV_BF16."""
-    dt = {KV_I8: torch.int8, KV_F16: torch.float16, KV_BF16: torch.bfloat16}[kind]
+    dt = {KV_I8: torch.int8, KV_F16: torch.float16, KV_BF16: torch.bfloat16}.get(kind)
+    if dt is None:
+        raise QpackError(f"kind: expected KV_I8, KV_F16 or KV_BF16, got {kind!r}")
     shape = (layers, pages, heads, page_tokens, dim)
     k, v = (torch.zeros(shape, dtype=dt, device=device) for _ in range(2))
     if kind != KV_I8:

@@ -12,3 +12,12 @@ def test_no_read_only_loads_in_dependent_kernels():
         with open(os.path.join(csrc, name), encoding="utf-8") as f:
             text = f.read()
         assert not re.search(r"__ldg|ld\.global\.nc|\bload8<", text), name
+
+
+def test_unknown_pool_kind():
+    import pytest
+
+    import bit_weight_quantized_qpack_gb300 as qp
+    for kind in (3, -1, "i8", None):
+        with pytest.raises(qp.QpackError, match="kind: expected KV_I8"):
+            qp.alloc_kv_pool(kind, 1, 4, 2, 16, 64, device="cpu")
