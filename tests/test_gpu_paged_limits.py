@@ -125,6 +125,34 @@ def test_attend_infinite_elements_stay_where_they_are(qpg, kind, D, G, window, r
     assert not torch.isfinite(outs[1].cpu()[odd]).any() and torch.isfinite(outs[0]).all()
 
 
+@pytest.mark.parametrize("kind", ["i8", "f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [1, 8, 11, 16])
+def test_attend_scores_keep_the_querys_bits(qpg, kind, D, G):
+    """One token whose key is 1 at a single place, every place in turn: the log-sum-exp is that element of the query, to the
+    22 bits of two fp16 terms or the 24 of three bfloat16 ones and the roundings of a product by log2 e and one by ln 2 in
+    fp32. Two bfloat16 terms (16 bits) would be off by 2^-18 of it on average."""
+    pool = make_pool(qpg, kind, 1, D, 1, 1, D, 1)
+    pool.k.zero_()
+    pool.k[0, torch.arange(D), 0, 0, torch.arange(D)] = 1
+    if kind == "i8":
+        pool.k_scales.fill_(1.0)
+    tables = qpg.KVTables(torch.arange(D, dtype=torch.int32, device="cuda").view(D, 1), torch.ones(D, dtype=torch.int32, device="cuda"))
+    g = torch.Generator(device="cuda")
+    g.manual_seed(D + G)
+    q = torch.empty((D, G, D), device="cuda").uniform_(64, 128, generator=g)
+    lse = torch.empty((D, G), device="cuda")
+    for scale in (1.0, -1.0):
+        qpg.qpack_kv_attend(pool, 0, tables, q, scale=scale, lse=lse)
+        want = scale * f64(q)[np.arange(D), :, np.arange(D)]
+        tol = 128 * 2.0 ** -22 + 128 * 3 * 2.0 ** -24 + 2.0 ** -19      # a term's last bit, three roundings, the logarithm's
+        assert np.all(np.abs(f64(lse) - want) <= tol)
+    terms = ref.bf16(want.astype(np.float32))
+    two = terms + ref.bf16((want - terms).astype(np.float32))
+    assert np.mean(np.abs(two - want) > tol) > 0.5         # what the third term is for
+    assert qpg.qpack_fetch_fault_flags() == 0
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # append
 # ---------------------------------------------------------------------------------------------------------------
