@@ -31,8 +31,9 @@
 // Both terms carry 22 bits together: scores and sums then differ from fp32 arithmetic by less than the output's
 // rounding, where a single fp16 term would add errors of that size. Queries are scaled by a power of two to a maximum in
 // [2^13, 2^14) and probabilities by 2^12, so neither term meets fp16's range. Where the cache is bfloat16 two terms carry
-// 16 bits: enough for probabilities, while queries get a third term. These have fp32's range and stay as they are: scaled,
-// the sums would pass it before the fp32 form's do.
+// 16 bits: queries get a third term, and so do probabilities where the output is fp32 (2% of the time); a 16-bit output
+// does not show their 2^-17. bfloat16 terms have fp32's range and stay as they are: scaled, the sums would pass it before
+// the fp32 form's do.
 //
 // 8-bit elements become fp16(scale * code), exactly the cache's definition: a byte permute puts code + 128 under the
 // exponent of 1024, one packed subtraction takes 1152 off (exact), one packed product rounds once: 1.75 instructions an
@@ -839,6 +840,25 @@ __global__ void __launch_bounds__(Cfg<KT, D, NT>::W * 32, 1) attend_kernel(const
                 }
 
                 // -- values ---------------------------------------------------------------------------------
+                if (THREE && a.odt == DT_F32) {
+                    // what two bfloat16 terms leave of the probabilities, where the output keeps more than their 16 bits
+#pragma unroll
+                    for (int u = 0; u < TOK / 16; ++u) {
+                        uint32_t pt[NT][2];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int t = 0; t < 2; ++t)
+                                pt[n][t] = third_term(s[n][4 * u + 2 * t], s[n][4 * u + 2 * t + 1], ph[n][2 * u + t], plo[n][2 * u + t]);
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            uint32_t r[4];
+                            ldsm4_t((st + (TOK + u * 16) * RB) + ((c * 16 * F::ES) ^ lx), r);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) mma<KT>(acc[c][n], r[0], r[2], r[1], r[3], pt[n][0], pt[n][1]);
+                        }
+                    }
+                }
 #pragma unroll
                 for (int u = 0; u < TOK / 16; ++u) {
                     if (I8) {

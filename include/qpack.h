@@ -266,8 +266,8 @@ int qpack_kv_read(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_
  *   x_t = scale * <q~_b, k'_t>, lo <= t < L
  *   out_b = sum_t e^{x_t - m} v'_t / sum_t e^{x_t - m},  lse_b = ln sum_t e^{x_t}
  * Sums, softmax statistics and accumulators are fp32; queries and probabilities enter the tensor cores as two 16-bit
- * terms each (22 bits) where the pool is 8-bit or fp16, as three (24) and two (16) where it is bf16. An empty range
- * gives out = 0 and lse = -inf.
+ * terms each (22 bits) where the pool is 8-bit or fp16; where it is bf16, queries as three (24), probabilities as three where
+ * the output is fp32, else as two (16). An empty range gives out = 0 and lse = -inf.
  * The formula is for finite keys and values (a value above 65504 in an fp16 pool, or a scale times a code, is infinite).
  * A key that is not may make the heads of its key/value head NaN in its row, even where the formula gives it no weight; a
  * value that is not makes its element of their outputs infinite or NaN. Nothing else changes. Slots that hold no token

@@ -153,6 +153,41 @@ def test_attend_scores_keep_the_querys_bits(qpg, kind, D, G):
     assert qpg.qpack_fetch_fault_flags() == 0
 
 
+@pytest.mark.parametrize("kind", ["i8", "f16", "bf16"])
+@pytest.mark.parametrize("D,G", [(64, 1), (64, 16), (128, 8), (128, 11), (256, 4)])
+def test_attend_fp32_outputs_keep_the_weights_bits(qpg, kind, D, G):
+    """Each token's value is 1 at a place of its own, so an fp32 output shows the weights: to the exponential's and the
+    division's roundings and to the terms' 22 bits or more, over bf16 caches too (two bfloat16 terms would leave 16)."""
+    n, T = 60, 16
+    pool = make_pool(qpg, kind, 1, 6, 1, T, D, 1)
+    tab, tables = make_tables(qpg, [n], T, 6, 2)
+    page, slot = torch.from_numpy(tab[0])[torch.arange(n) // T].long(), torch.arange(n) % T
+    for c in (pool.k, pool.v):
+        c.zero_()
+    if kind == "i8":
+        pool.k_scales.fill_(2.0 ** -7), pool.v_scales.fill_(1.0)
+    g = torch.Generator()
+    g.manual_seed(D + G)
+    key = torch.randint(-127, 128, (n,), generator=g)
+    pool.k[0, page, 0, slot, 7] = (key.float() * (1 if kind == "i8" else 2.0 ** -7)).to(pool.k.dtype).cuda()
+    pool.v[0, page, 0, slot, torch.arange(n)] = 1
+    q = torch.zeros((1, G, D), device="cuda")
+    q[0, :, 7] = torch.linspace(0.3, 1.5, G)
+    out = torch.empty_like(q)
+    qpg.qpack_kv_attend(pool, 0, tables, q, scale=1.0, out=out)
+    x = f64(q)[0, :, 7, None] * (key.numpy() * 2.0 ** -7)
+    e = np.exp(x - x.max(1, keepdims=True))
+    want = e / e.sum(1, keepdims=True)
+    # scores of at most 1.5: a term's last bit and four roundings, at log2 e; the exponential's 2^-22, the terms' 2^-22, sum and
+    # division
+    tol = want * (1.5 * 1.443 * (2.0 ** -22 + 4 * 2.0 ** -24) + 2.0 ** -22 + 2.0 ** -22 + 12 * 2.0 ** -24)
+    assert np.all(np.abs(f64(out)[0, :, :n] - want) <= tol)
+    two = ref.bf16(e.astype(np.float32))
+    two = two + ref.bf16((e - two).astype(np.float32)).astype(np.float64)
+    assert np.mean(np.abs(two / e.sum(1, keepdims=True) - want) > tol) > 0.1       # what the third term is for
+    assert not out[0, :, n:].any() and qpg.qpack_fetch_fault_flags() == 0
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # append
 # ---------------------------------------------------------------------------------------------------------------
