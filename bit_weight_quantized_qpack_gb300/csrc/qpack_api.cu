@@ -419,7 +419,7 @@ int qpack_kv_attend_workspace(const qpack_kv_pool_t *pool, int B, int q_heads, i
     if (!bytes || B < 0 || q_heads < 1) return QPACK_ERR_ARG;
     if (int rc = check_pool(pool, false)) return rc;
     if (B > 4096 || q_heads > 65536 || q_heads % pool->heads) return QPACK_ERR_SHAPE;
-    *bytes = kv_attend_workspace(*pool, B, q_heads);
+    *bytes = kv_attend_workspace(*pool, q_heads);
     return QPACK_OK;
 }
 
@@ -438,7 +438,7 @@ int qpack_kv_attend(const qpack_kv_pool_t *pool, int layer, const qpack_kv_table
         return rc;
     if (!aligned(seqs, 4) || !aligned(lse, 4) || !aligned(ws, 16)) return QPACK_ERR_ALIGN;
     if (!ws) return QPACK_ERR_ARG;
-    if (ws_bytes < kv_attend_workspace(*pool, B, q_heads)) return QPACK_ERR_SHAPE;
+    if (ws_bytes < kv_attend_workspace(*pool, q_heads)) return QPACK_ERR_SHAPE;
     AttendArgs a = {*pool, *t, seqs, q, ldq, rope, rope_rows, out, ldo, lse, ws, window, scale, layer, B, q_heads, qdt,
                     odt};
     const cudaError_t e = launch_kv_attend(a, reinterpret_cast<cudaStream_t>(stream));
@@ -449,7 +449,7 @@ int qpack_kv_page_workspace(const qpack_kv_pool_t *pool, const qpack_kv_tables_t
     if (!bytes) return QPACK_ERR_ARG;
     int rc;
     if ((rc = check_pool(pool, false)) || (rc = check_tables(t, false))) return rc;
-    *bytes = kv_page_workspace(*pool, *t);
+    *bytes = kv_page_workspace(*pool);
     return QPACK_OK;
 }
 
@@ -468,7 +468,7 @@ int qpack_kv_fork(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, const
     if (n == 0) return QPACK_OK;
     if (!src || !dst || !ws) return QPACK_ERR_ARG;
     if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(ws, 16)) return QPACK_ERR_ALIGN;
-    if (ws_bytes < kv_page_workspace(*pool, *t)) return QPACK_ERR_SHAPE;
+    if (ws_bytes < kv_page_workspace(*pool)) return QPACK_ERR_SHAPE;
     return cuda_status(launch_kv_fork(*pool, *t, src, dst, int(n), ws, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -487,7 +487,7 @@ int qpack_kv_compact(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, in
     if (int rc = check_page_op(pool, t, 0)) return rc;
     if (!ws || (t->pages > 0 && !refs_out) || (t->seqs > 0 && t->max_pages > 0 && !tables_out)) return QPACK_ERR_ARG;
     if (!aligned(tables_out, 4) || !aligned(refs_out, 4) || !aligned(moved, 4) || !aligned(ws, 16)) return QPACK_ERR_ALIGN;
-    if (ws_bytes < kv_page_workspace(*pool, *t)) return QPACK_ERR_SHAPE;
+    if (ws_bytes < kv_page_workspace(*pool)) return QPACK_ERR_SHAPE;
     return cuda_status(launch_kv_compact(*pool, *t, tables_out, refs_out, moved, ws, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -18,7 +18,7 @@ template <> cudaError_t fault_word<QPACK_KV_F16>(int **);
 template <> cudaError_t fault_word<QPACK_KV_BF16>(int **);
 }  // namespace attend
 
-int64_t kv_attend_workspace(const qpack_kv_pool_t &pool, int, int q_heads) {
+int64_t kv_attend_workspace(const qpack_kv_pool_t &pool, int q_heads) {
     const int grid = num_sms();
     int64_t parts;
     if (pool.type == QPACK_KV_I8) parts = attend::workspace<QPACK_KV_I8>(pool, q_heads, grid);

@@ -108,7 +108,7 @@ struct AttendArgs {
     int layer, B, q_heads, qdt, odt;
 };
 cudaError_t launch_kv_attend(const AttendArgs &a, cudaStream_t s);
-int64_t kv_attend_workspace(const qpack_kv_pool_t &pool, int B, int q_heads);
+int64_t kv_attend_workspace(const qpack_kv_pool_t &pool, int q_heads);
 
 cudaError_t launch_kv_reserve(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t, const int32_t *seqs,
                               const int32_t *add, int n, cudaStream_t s);
@@ -119,7 +119,7 @@ cudaError_t launch_kv_compact(const qpack_kv_pool_t &p, const qpack_kv_tables_t 
                               int32_t *refs_out, int32_t *moved, void *ws, cudaStream_t s);
 cudaError_t launch_kv_copy_pages(const qpack_kv_pool_t &p, const int32_t *src, const int32_t *dst, int64_t n,
                                  cudaStream_t s);
-int64_t kv_page_workspace(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t);
+int64_t kv_page_workspace(const qpack_kv_pool_t &p);
 cudaError_t fault_word_paged(int **word);
 cudaError_t fault_words_attend(int **words);    // one a cache type
 cudaError_t fetch_faults(int32_t *flags);

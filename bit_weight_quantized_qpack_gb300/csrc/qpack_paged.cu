@@ -723,7 +723,7 @@ cudaError_t run_copy(const qpack_kv_pool_t &p, const PageWs &w, const int *src, 
 cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t s) { return rows_kind(a, false, s); }
 cudaError_t launch_kv_read(const AppendArgs &a, cudaStream_t s) { return rows_kind(a, true, s); }
 
-int64_t kv_page_workspace(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t) {
+int64_t kv_page_workspace(const qpack_kv_pool_t &p) {
     return 16 + int64_t(sizeof(CopyItem)) * copy_cap(p.pages) + 4 * p.pages;
 }
 

@@ -301,7 +301,8 @@ int qpack_kv_reserve(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, co
 
 /* fork: make the empty sequence dst[i] a copy of src[i] (one src may be forked many times; no dst may be a src). Full
  * pages are shared (refs + 1); a last page that is not full is copied into a fresh page, over all layers, the filled
- * tokens only. Refused as in reserve. ws: qpack_kv_page_workspace bytes, 16-byte aligned, no initial value needed. */
+ * tokens only. Refused as in reserve, and where dst[i] is not empty; the page that a refused request of a known sequence would
+ * have got is passed over. ws: qpack_kv_page_workspace bytes, 16-byte aligned, no initial value needed. */
 int qpack_kv_fork(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, const int32_t *src, const int32_t *dst,
                   int64_t n, void *ws, int64_t ws_bytes, qpack_stream_t stream);
 

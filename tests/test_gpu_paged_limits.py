@@ -254,6 +254,31 @@ def test_default_position_of_a_negative_length(qpg):
         assert torch.equal(after, before)
 
 
+def test_append_and_attend_at_saturation(qpg):
+    """A token whose largest value the 8-bit cache holds as infinite (fp16(65504 * 127)): read back as the rule has it, and
+    attention sees it in that element alone, or in its head where it is a key."""
+    H, D, T = 2, 128, 16
+    pool = make_pool(qpg, "i8", 1, 3, H, T, D, 1)
+    _, tables = make_tables(qpg, [3], T, 3, 2)
+    k = torch.randn((3, H, D), device="cuda")
+    v = torch.randn((3, H, D), device="cuda")
+    v[1, 0, 40], k[2, 1, 7] = 9e6, -1e7
+    seqs, pos = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.arange(3, dtype=torch.int32, device="cuda")
+    qpg.qpack_kv_append(pool, 0, tables, k, v, seqs=seqs, pos=pos)
+    kr, vr = qpg.qpack_kv_read(pool, 0, tables, seqs, pos)
+    for got, x in ((kr, k), (vr, v)):
+        assert np.array_equal(f64(got), ref.values(*ref.quantize32(x.cpu().numpy())))
+    assert f64(vr)[1, 0, 40] == np.inf and f64(kr)[2, 1, 7] == -np.inf
+    q = torch.randn((1, 2 * H, D), device="cuda")
+    out = qpg.qpack_kv_attend(pool, 0, tables, q, out=torch.empty_like(q))
+    fine = f64(vr)[:, 0].copy()
+    fine[1, 40] = 0
+    want, _ = ref.attend(f64(q[0, :2]), f64(kr)[:, :1], fine[:, None], D ** -0.5)
+    rest = np.arange(D) != 40
+    assert np.allclose(f64(out)[0, :2, rest], want[:, rest].T, rtol=0, atol=2.0 ** -18 * np.abs(fine).max())
+    assert not np.isfinite(f64(out)[0, :2, 40]).any() and qpg.qpack_fetch_fault_flags() == 0
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # another stream
 # ---------------------------------------------------------------------------------------------------------------
