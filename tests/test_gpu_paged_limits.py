@@ -454,3 +454,24 @@ def test_page_operators_lengths_out_of_range(qpg):
         assert qpg.qpack_fetch_fault_flags() == qpg.FAULT_PAGE
         assert tables.lens.tolist() == [40, 64, bad, 0, 40, 64] and tables.tables[4].tolist() == [0, 1, 7, -1]
         assert tables.tables[5].tolist() == tables.tables[1].tolist()
+
+
+def test_fork_refused_among_others(qpg):
+    """Children that are not empty, parents that do not exist and pages that run out, in the middle of a call: the others get
+    the pages of their places in it."""
+    T, pages = 16, 24
+    pool = make_pool(qpg, "i8", 2, pages, 2, T, 64, 1)
+    tables, sim = qpg.alloc_kv_tables(16, 6, pages), ref.Pages(16, 6, pages, T, token_view(pool))
+    i = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    for op, a, b in (("reserve", [0, 1, 2, 3], [20, 32, 5, 90]), ("fork", [0, 2, 1, 0, 2], [4, 3, 5, 6, 7]), ("free", [6, 1], None),
+                     ("fork", [0, 0, 2, 5, 2, 0, 0, 2], [8, 4, 9, 10, 2, 11, 12, 13]), ("reserve", [9, 10, 8], [1, 40, 12])):
+        if op == "free":
+            qpg.qpack_kv_free(tables, i(a))
+            sim.free(a)
+            continue
+        if op == "reserve":
+            qpg.qpack_kv_reserve(pool, tables, i(a), i(b))
+        else:
+            qpg.qpack_kv_fork(pool, tables, i(a), i(b))
+        getattr(sim, op)(a, b)
+        same_state(qpg, pool, tables, sim)
