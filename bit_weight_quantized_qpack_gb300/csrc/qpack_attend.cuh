@@ -16,10 +16,11 @@
 // warp), and they are issued on half of the cycles.
 //
 // Measured: 64 sequences of 4096 to 8192 tokens, 64 query heads over 8, 8 bits: 139 us = 6180 GB/s, 91% of the copy
-// rate; one sequence of 131071 tokens, 32 over 8: 53.7 us = 78%. What is left there is some 10 us a call, whatever its
-// size: 2 us until the first copies start (lengths, then pages: dependent loads), 2 to 4 us by which the slowest SM ends
-// after the middle one, 3 us for the joins of blocks, the launch. A row of 97 tokens takes 7 us. Sixteen query heads a
-// key head are bound by the instructions instead (63% of the copy rate).
+// rate; one sequence of 131071 tokens, 32 over 8: 53.4 us = 79%. What is left there is some 10 us a call, whatever its
+// size: 2 us until the first copies start (lengths, then pages: dependent loads; queries are in registers after 4 us, in
+// the last block after 8), 2 to 4 us by which the slowest SM ends after the middle one, 3 us for the joins of blocks, the
+// launch. A row of 97 tokens takes 7 us. Sixteen query heads a key head are bound by the instructions instead (62% of the
+// copy rate).
 //
 //   S = Q K^T:     A = queries (16 rows), B = 16 tokens x D. With up to eight query heads rows 0-7 hold the queries'
 //                  leading 16-bit terms and rows 8-15 the remainders of the same heads, so one instruction takes both
@@ -67,8 +68,10 @@ constexpr int MAX_COUNTERS = QPACK_KV_ATTEND_ZEROED / 4;    // of a launch: the 
 // the stages. Measured (one block an SM throughout; us for one sequence of 131071 tokens / 64 of 4096 to 8192, 8 bits,
 // D = 128): 8 warps x 32 tokens 54.9 / 141.3, 12 x 32 57.0 / 141.0, 10 x 32 59.5 / 151, 12 x 16 59.7 / 146, 16 x 16
 // 60.9 / 147; two blocks of 4 warps an SM 57.9 / 140.7 where one of 8 had come to 52.3 / 136.8. At D = 64 and in fp16 at
-// 128 twelve warps are up to 10% faster than eight on long caches (62 against 68 us) and 2% slower on short ones; in
-// bfloat16 at 128 their registers spill over the third terms (27.5 against 25.6 us).
+// 128 twelve warps are up to 10% faster than eight on long caches (62 against 68 us) and 2% slower on short ones, although
+// 20 bytes a thread spill in fp16; in bfloat16 at 128 their registers spill over the third terms (27.5 against 25.6 us).
+// What else spills: 12 to 136 bytes where two groups of heads are held together (most in 8 bits at 128) or rows have 256
+// elements. The other five instances of 64 and 128 elements with one group do not.
 template <int KT, int D, int NT> struct Cfg {
     static constexpr int ES = KT == QPACK_KV_I8 ? 1 : 2;
     static constexpr int RB = D * ES;                           // bytes of a token's row

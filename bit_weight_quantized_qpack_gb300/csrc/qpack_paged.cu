@@ -2,10 +2,10 @@
 // bits, scatter into pages), reading rows back, and the page operators (reserve, fork, free, compact, copy).
 //
 // Append and read are streams: every element is read and written once, so HBM bounds them at length and the launch at
-// a decode step's few tokens. 8191 tokens of 8 heads of 128 in fp16: append into 8 bits 14.5 us (52% of the copy rate),
-// read back 11.4 us (67%); at 100000 tokens 74% and 89%. Append is held up by its own chain in each warp (loads, scales,
-// codes) with 24 warps an SM; fewer registers spill.
-// The page operators move the pages that they have to (HBM bound: 598 MB of pages compacted in 197 us, 90% of the copy
+// a decode step's few tokens. 8191 tokens of 8 heads of 128 in fp16: append into 8 bits 14.6 us (52% of the copy rate),
+// read back 11.4 us (66%); at 100000 tokens 74% and 89%. Append is held up by its own chain in each warp (loads, scales,
+// codes) with 24 warps an SM (below, at the kernel, what more and fewer cost).
+// The page operators move the pages that they have to (HBM bound: 598 MB of pages compacted in 195 us, 91% of the copy
 // rate) after a plan on the tables alone (a few us of dependent loads). All of it is deterministic: pages are ranked by
 // number and requests by place, never by arrival.
 #include <cuda_bf16.h>
@@ -105,10 +105,17 @@ template <int DT> __device__ __forceinline__ void convert(const Raw<DT> &r, floa
 }
 
 // The rotation's partner (i +- D/2) is D/16 lanes away, and the four lanes of a 32-element group reduce its maximum
-// with two shuffles. Blocks an SM, 8191 tokens of 8 heads in fp16 into 8 bits: 4 17.9 us, 5 16.2, 6 14.6, 7 15.8
-// (registers spill); from fp32: 4 18.4, 5 18.7, 6 24.4; in bfloat16 throughout: 4 16.3, 5 13.6, 7 12.8.
+// with two shuffles.
+// Blocks an SM (us; 100000 tokens of 8 heads of 128; bytes that spill at 4, 5, 6, 7, 8 in brackets):
+//   fp32 into 8 bits    4 171, 5 167, 6 222, 7 265, 8 244 (0, 0, 248, 456, 472)     into bf16  186, 178, 211, 222, 223
+//   fp16 into 8 bits    4 165, 5 144, 6 124, 7 130, 8 137 (0, 0, 24, 68, 176)       into bf16  154, 129, 124, 124, 129
+//   bf16 into 8 bits    4 165, 5 144, 6 133, 7 137, 8 143 (0, 0, 28, 112, 196)      into bf16  165, 137, 129, 125, 125
+// 8191 tokens, and widths of 64 and 256, fall in the same order but for fp32 into 8 bits, where 4 takes 18.2 us and 5 18.5,
+// and bf16 into 8 bits at 256, where 5 and 7 are 5% faster than 6. So 5 from fp32, and from 16 bits 6 into 8 bits, whose few
+// spilled bytes cost less than a block fewer, 7 into 16 bits, which do not spill.
 template <int KT, int D, int DT>
-__global__ void __launch_bounds__(ROW_WARPS * 32, DT == DT_F32 ? 5 : KT == QPACK_KV_I8 ? 6 : 7) kv_append_kernel(AppendArgs a, int64_t first, unsigned items, unsigned groups) {
+__global__ void __launch_bounds__(ROW_WARPS * 32, DT == DT_F32 ? 5 : KT == QPACK_KV_I8 ? 6 : 7)
+    kv_append_kernel(AppendArgs a, int64_t first, unsigned items, unsigned groups) {
     constexpr int LPR = D / 8, RPW = 32 / LPR, U = ROW_U;
     const int lane = threadIdx.x & 31, sub = lane % LPR, H = a.pool.heads;
     pdl_launch_dependents();
@@ -645,9 +652,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_compact_plan_kernel(qpack_kv_
     }
 }
 
-// Copies the items' rows: 6.2 TB/s over a 32-layer cache. A warp takes one head's rows of keys or values of one layer at a time, 16 bytes a lane with
-// eight loads in flight, then the rows' scales. `refs`: fork's fresh pages get their count. `tables`: compaction's
-// entries get their new numbers.
+// Copies the items' rows: 6.2 TB/s over a 32-layer cache. A warp takes one head's rows of keys or values of one layer at a
+// time, 16 bytes a lane with eight loads in flight, then the rows' scales. `refs`: fork's fresh pages get their count.
+// `tables`: compaction's entries get their new numbers.
 __global__ void __launch_bounds__(256) kv_copy_kernel(qpack_kv_pool_t pool, PageWs w, const int *src_list,
                                                       const int *dst_list, int64_t n_list, int *refs, qpack_kv_tables_t t,
                                                       int *tables_out) {
@@ -659,7 +666,7 @@ __global__ void __launch_bounds__(256) kv_copy_kernel(qpack_kv_pool_t pool, Page
     const int64_t n = src_list ? n_list : w.count[0];
     const int64_t slabs = n * pool.layers * 2 * pool.heads;
     const int es = pool.type == QPACK_KV_I8 ? 1 : 2;
-    const bool narrow = slabs < (int64_t(1) << 31);        // 32-bit divisions do (64 children: 28.0 us, not 28.4)
+    const bool narrow = slabs < (int64_t(1) << 31);        // 32-bit divisions do (64 children: 0.4 us less of 28)
     for (int64_t j = warp; j < slabs; j += warps) {
         const int64_t pair = narrow ? int64_t(unsigned(j) / unsigned(pool.heads)) : j / pool.heads;
         const int64_t page = pair >> 1;                    // (item, layer)
