@@ -323,8 +323,11 @@ _HERE = contextlib.nullcontext()
 
 def _on(stream):
     """Where a call allocates what the caller did not give: in the order of the stream that it runs on, so that zeroing comes
-    before the kernels, and memory that is given back is not handed out again before they end."""
-    return _HERE if stream is None else torch.cuda.stream(stream)
+    before the kernels, and memory that is given back is not handed out again before they end. `stream` is a torch stream, or
+    anything with a `cuda_stream` handle, as for the launch."""
+    if stream is None:
+        return _HERE
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream))
 
 
 def _out(stream, shape, dtype, device):

@@ -312,6 +312,12 @@ def test_attend_other_stream_default_workspace(qpg):
         soil(size)                                          # behind the current stream's work, over what the call gave back
         s.synchronize()
         assert torch.equal(out, want)
+
+    class Handle:                                           # a stream of another library: its handle is all that a launch takes
+        cuda_stream = s.cuda_stream
+    out = qpg.qpack_kv_attend(pool, 0, tables, q, stream=Handle())
+    s.synchronize()
+    assert torch.equal(out, want)
     torch.cuda.synchronize()
     assert qpg.qpack_fetch_fault_flags() == 0
 
