@@ -29,8 +29,11 @@ cudaError_t fetch_faults(int32_t *flags) {
     if (e == cudaSuccess) e = fault_word_paged(&w.at[2]);
     if (e == cudaSuccess) e = fault_words_attend(&w.at[3]);
     if (e != cudaSuccess) return e;
-    collect_kernel<<<1, 32>>>(w);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(32);
+    // its own status: an earlier error of the caller's is neither reported here nor cleared
+    if ((e = cudaLaunchKernelEx(&cfg, collect_kernel, w)) != cudaSuccess) return e;
     return cudaMemcpyFromSymbol(flags, g_fault, sizeof(int));
 }
 

@@ -481,3 +481,16 @@ def test_fork_refused_among_others(qpg):
             qpg.qpack_kv_fork(pool, tables, i(a), i(b))
         getattr(sim, op)(a, b)
         same_state(qpg, pool, tables, sim)
+
+
+def test_fetch_keeps_an_earlier_error(qpg):
+    """An error that another library's call left behind is not the fetch's: it succeeds, and the error is still there."""
+    import ctypes
+    rt = ctypes.CDLL("libcudart.so.13")
+    assert rt.cudaGetLastError() == 0
+    assert rt.cudaGetDeviceProperties(None, 0) != 0         # invalid argument, on the host
+    try:
+        assert qpg.qpack_fetch_fault_flags() == 0
+        assert rt.cudaPeekAtLastError() != 0
+    finally:
+        rt.cudaGetLastError()
