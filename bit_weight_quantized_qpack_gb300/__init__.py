@@ -91,6 +91,7 @@ def lib():
                 "qpack_kv_compact": ([P, P, P, P, P, P, I64, P], I),
                 "qpack_kv_copy_pages": ([P, P, P, I64, P], I),
                 "qpack_kv_page_workspace": ([P, P, ctypes.POINTER(I64)], I),
+                "qpack_qk_norm_rope": ([P, P, I64, I, I, I, ctypes.c_float, P, I64, I, I, P, P, P, P], I),
                 "qpack_status_string": ([I], ctypes.c_char_p),
                 "qpack_fetch_fault_flags": ([ctypes.POINTER(ctypes.c_int32)], I),
                 "qpack_version": ([], I),
@@ -638,6 +639,73 @@ def qpack_kv_copy_pages(pool, src, dst, stream=None):
     rc = (_lib or lib()).qpack_kv_copy_pages(pool._ref, _addr(src), _addr(dst), n, _raw_stream(stream))
     if rc:
         _check(rc, "qpack_kv_copy_pages")
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("ldo", ctypes.c_int64), ("heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+def _here(stream, *tensors):
+    """All of them on the device that the call runs on: the current one, or the stream's."""
+    dev = _current_device() if stream is None or not isinstance(stream, torch.cuda.Stream) else stream.device_index
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise QpackError(f"a tensor is on {t.device}, the call runs on device {dev}")
+
+
+def _side(x, out, weight, what, like, stream):
+    """Heads [n, heads, dim] of one side and where they go."""
+    if x.dim() != 3:
+        raise QpackError(f"{what}: expected [n, heads, dim], got {tuple(x.shape)}")
+    n, heads, dim = x.shape
+    dt, ldx, _ = _need_rows(x, what, heads, dim)
+    if like is not None and like != (n, dim, x.dtype):
+        raise QpackError(f"{what}: expected q's rows, dim and type, got {n}, {dim} and {x.dtype}")
+    if out is None:
+        out = _out(stream, x.shape, x.dtype, x.device)
+    odt, ldo, rows = _need_rows(out, what + "_out", heads, dim)
+    if rows < n:
+        raise QpackError(f"{what}_out: expected at least {n} rows, got {rows}")
+    if weight is not None:
+        _need(weight, torch.float32, what + "_weight", numel=dim)
+        if weight.numel() != dim:
+            raise QpackError(f"{what}_weight: expected {dim} elements, got {weight.numel()}")
+    return out, dt, odt, _Heads(_addr(x), _addr(out), _addr(weight), ldx, ldo, heads, 0)
+
+
+def qpack_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, eps=1e-6, rope=None, interleaved=False, tables=None,
+                       seqs=None, pos=None, q_out=None, k_out=None, stream=None):
+    """Norm and rotation of query and key heads [n, heads, dim] in one pass: x / sqrt(mean(x^2) + eps) * weight where a
+    weight (float32 [dim]) is given, then the rotation of the first rope.shape[1] elements by row `position` of `rope`
+    (float32 [positions, cos | sin]): pairs half of them apart, or neighbours (interleaved). Token i's position is pos[i], or
+    the last one of sequence seqs[i] (default i) of `tables`; negative positions leave their rows as they were. Returns
+    (q_out, k_out), of the inputs' type unless given (an input itself will do); k may be None."""
+    if rope is not None:
+        turn = rope.shape[1] if rope.dim() == 2 else -1
+        rows = _need_rope(rope, turn)
+        if pos is None and tables is None:
+            raise QpackError("pos: needed for the rotation where no tables are given")
+    else:
+        turn = rows = 0
+    q_out, dt, odt, cq = _side(q, q_out, q_weight, "q", None, stream)
+    ck, n = None, q.shape[0]
+    if k is not None:
+        k_out, _, odk, ck = _side(k, k_out, k_weight, "k", (n, q.shape[2], q.dtype), stream)
+        if odk != odt:
+            raise QpackError("q_out, k_out: expected the same type")
+    _need_i32(pos, "pos", n)
+    if pos is None:
+        _need_i32(seqs, "seqs", n)
+        if tables is not None and seqs is None and tables.tables.shape[0] < n:
+            raise QpackError(f"q: {n} rows, but the table has {tables.tables.shape[0]} sequences")
+    _here(stream, q, k, q_out, k_out, q_weight, k_weight, rope, seqs, pos)
+    rc = (_lib or lib()).qpack_qk_norm_rope(
+        ctypes.addressof(cq), None if ck is None else ctypes.addressof(ck), n, q.shape[2], dt, odt, eps, _addr(rope), rows,
+        turn, bool(interleaved), None if tables is None else tables._ref, _addr(seqs), _addr(pos), _raw_stream(stream))
+    if rc:
+        _check(rc, "qpack_qk_norm_rope")
+    return q_out, k_out
 
 
 def qpack_fetch_fault_flags() -> int:

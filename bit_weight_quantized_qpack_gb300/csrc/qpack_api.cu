@@ -501,6 +501,42 @@ int qpack_kv_copy_pages(const qpack_kv_pool_t *pool, const int32_t *src, const i
     return cuda_status(launch_kv_copy_pages(*pool, src, dst, n, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int qpack_qk_norm_rope(const qpack_heads_t *q, const qpack_heads_t *k, int64_t n, int dim, int dt, int odt, float eps,
+                       const float *rope, int64_t rope_rows, int rope_dim, int interleaved, const qpack_kv_tables_t *t,
+                       const int32_t *seqs, const int32_t *pos, qpack_stream_t stream) {
+    int rc;
+    if (n < 0 || dt < QPACK_F32 || dt > QPACK_BF16 || odt < QPACK_F32 || odt > QPACK_BF16) return QPACK_ERR_ARG;
+    if (!(eps >= 0.0f && eps <= 3.402823466e38f) || (interleaved != 0 && interleaved != 1)) return QPACK_ERR_ARG;
+    if (dim < 8 || dim > 256 || dim % 8) return QPACK_ERR_SHAPE;
+    if (rope ? rope_dim < 8 || rope_dim > dim || rope_dim % 8 : rope_dim != 0) return QPACK_ERR_SHAPE;
+    if (t && (rc = check_tables(t, false))) return rc;
+    if ((rc = check_rope(rope, rope_rows))) return rc;
+    if (n > 0 && rope && !pos && !t) return QPACK_ERR_ARG;
+    if (!aligned(seqs, 4) || !aligned(pos, 4)) return QPACK_ERR_ALIGN;
+    HeadsArgs a = {};
+    const qpack_heads_t *side[2] = {q, k};
+    int64_t heads = 0;
+    for (int i = 0; i < 2; ++i) {
+        const qpack_heads_t *h = side[i];
+        if (!h || h->heads == 0) continue;
+        if (h->heads < 0 || h->reserved) return QPACK_ERR_ARG;
+        if (h->heads > 65536) return QPACK_ERR_SHAPE;
+        if (n == 0) continue;
+        const int64_t width = int64_t(h->heads) * dim;
+        if ((rc = check_rows(h->x, h->ldx, width)) || (rc = check_rows(h->out, h->ldo, width))) return rc;
+        if (h->x == h->out && (dt != odt || h->ldx != h->ldo)) return QPACK_ERR_ARG;
+        if (!aligned(h->weight, 16)) return QPACK_ERR_ALIGN;
+        a.side[i] = {h->x, h->out, h->weight, h->ldx, h->ldo, h->heads};
+        heads += h->heads;
+    }
+    if (n == 0 || heads == 0) return QPACK_OK;
+    if (t) a.t = *t;
+    a.has_tables = t != nullptr;
+    a.seqs = seqs, a.pos = pos, a.rope = rope, a.n = n, a.rope_rows = rope_rows;
+    a.eps = eps, a.dim = dim, a.turn = rope_dim, a.dt = dt, a.odt = odt, a.near_pairs = interleaved != 0;
+    return cuda_status(launch_heads(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 const char *qpack_status_string(int status) {
     switch (status) {
         case QPACK_OK: return "QPACK_OK";

@@ -122,6 +122,28 @@ cudaError_t launch_kv_copy_pages(const qpack_kv_pool_t &p, const int32_t *src, c
 int64_t kv_page_workspace(const qpack_kv_pool_t &p);
 cudaError_t fault_word_paged(int **word);
 cudaError_t fault_words_attend(int **words);    // one a cache type
+
+// Norm and rotation of query and key heads (qpack_heads.cu).
+struct HeadsSide {
+    const void *x;
+    void *out;
+    const float *weight;         // null: no norm
+    int64_t ldx, ldo;
+    int heads;                   // 0: none
+};
+struct HeadsArgs {
+    HeadsSide side[2];           // queries, keys
+    qpack_kv_tables_t t;
+    const int32_t *seqs, *pos;
+    const float *rope;           // null: no rotation
+    int64_t n, rope_rows;
+    float eps;
+    int dim, turn, dt, odt;
+    bool near_pairs, has_tables;
+};
+cudaError_t launch_heads(const HeadsArgs &a, cudaStream_t s);
+cudaError_t fault_word_heads(int **word);
+
 cudaError_t fetch_faults(int32_t *flags);
 
 int num_sms();

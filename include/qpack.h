@@ -323,6 +323,41 @@ int qpack_kv_copy_pages(const qpack_kv_pool_t *pool, const int32_t *src, const i
                         qpack_stream_t stream);
 int qpack_kv_page_workspace(const qpack_kv_pool_t *pool, const qpack_kv_tables_t *t, int64_t *bytes);
 
+/* ---------------------------------------------------------------------------------------------------------------
+ * What a decode step does to query and key heads between their product and the cache: the root-mean-square norm of each
+ * head and the position rotation, in one pass over queries and keys.
+ *   y = x / sqrt(mean(x^2) + eps) * weight      (weight NULL: y = x)
+ *   (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s)  for the pairs of the first rope_dim elements, the rest stays y
+ * in fp32, products and sums rounded each by itself (without a weight rotated keys are those that qpack_kv_append would
+ * store), the result rounded once to odt. Heads that are rotated here go to qpack_kv_append and the attention calls without
+ * their `rope`.
+ *  q, k        either may be NULL, or have 0 heads
+ *    x, out    [n, ldx] and [n, ldo]: rows of heads * dim elements of dtype dt and odt (QPACK_F32, F16 or BF16), 16-byte
+ *              aligned, ldx and ldo >= heads * dim and multiples of 8. out may be x where dt is odt and ldx is ldo; otherwise
+ *              the outputs overlap nothing.
+ *    weight    [dim] fp32, 16-byte aligned, or NULL
+ *  dim         elements of a head, a multiple of 8, 8 to 256
+ *  eps         >= 0, finite (used with a weight only)
+ *  rope        NULL (no rotation), or [rope_rows, rope_dim] fp32, 16-byte aligned: row p holds cos (rope_dim / 2) and sin
+ *              (rope_dim / 2) of position p (whatever scaling a long context asks for is in the table)
+ *  rope_dim    a multiple of 8, at most dim (0 without rope)
+ *  interleaved 0: pairs (i, i + rope_dim / 2); 1: pairs (2i, 2i + 1)
+ *  t, seqs, pos  token i's position: pos[i] (int32), or where pos is NULL the last one of sequence seqs[i] (NULL: i) of t,
+ *              lens - 1. t and pos may both be NULL where rope is. A token whose position is negative is skipped: its
+ *              rows of out are left as they were. A sequence or length out of range skips the token, and a position behind
+ *              the table leaves its heads without rotation; both set QPACK_FAULT_PAGE. */
+typedef struct {
+    const void *x;
+    void *out;
+    const float *weight;
+    int64_t ldx, ldo;
+    int32_t heads;
+    int32_t reserved;       /* 0 */
+} qpack_heads_t;
+int qpack_qk_norm_rope(const qpack_heads_t *q, const qpack_heads_t *k, int64_t n, int dim, int dt, int odt, float eps,
+                       const float *rope, int64_t rope_rows, int rope_dim, int interleaved, const qpack_kv_tables_t *t,
+                       const int32_t *seqs, const int32_t *pos, qpack_stream_t stream);
+
 /* Human-readable name of a qpack_status value. Never NULL. */
 const char *qpack_status_string(int status);
 

@@ -1,0 +1,94 @@
+"""Host-side checks of the operators around the cache (norm and rotation of heads): the restatement that the GPU tests
+compare with against independent pins, and the refusals of the C ABI and of the binding, which come before any launch."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import decode as ref
+from oracle import paged
+
+OK, ARG, SHAPE, ALIGN = 0, -1, -2, -3
+P = 4096            # an address that is never followed: refusals come first
+
+
+@pytest.fixture(scope="module")
+def qp():
+    from bit_weight_quantized_qpack_gb300 import _build
+    _build.build()
+    import bit_weight_quantized_qpack_gb300 as qp
+    qp.lib()
+    return qp
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# norm and rotation of heads
+# ---------------------------------------------------------------------------------------------------------------
+def test_norm_restatement():
+    """A normed head has a mean square of one, whatever its size; weights scale its elements; torch agrees."""
+    rng = np.random.default_rng(0)
+    x = rng.normal(size=(5, 3, 40)) * np.exp(rng.uniform(-5, 5, (5, 3, 1)))
+    y, _ = ref.norm_rope(x, np.ones(40))
+    assert np.allclose((y * y).mean(-1), 1) and np.allclose(ref.norm_rope(7 * x, np.ones(40))[0], y)
+    w = rng.normal(size=40)
+    want = torch.nn.functional.rms_norm(torch.from_numpy(x), (40,), torch.from_numpy(w), 1e-3)
+    assert np.allclose(ref.norm_rope(x, w, 1e-3)[0], want, rtol=1e-12)
+
+
+def test_rotation_restatement():
+    """The half layout is the cache's rotation; neighbours are the half layout of permuted elements; the rest stays."""
+    rng = np.random.default_rng(1)
+    x, a = rng.normal(size=(4, 2, 48)), rng.uniform(-3, 3, (4, 16))
+    rows = np.concatenate([np.cos(a), np.sin(a)], 1)
+    y, size = ref.norm_rope(x, rows=rows)
+    assert np.allclose(y[..., :32], paged.rotate64(x[..., :32], rows)) and np.array_equal(y[..., 32:], x[..., 32:])
+    assert np.all(np.abs(y) <= size * (1 + 1e-15))
+    perm = np.concatenate([np.arange(0, 32, 2), np.arange(1, 32, 2)])
+    near, _ = ref.norm_rope(x, rows=rows, interleaved=True)
+    assert np.allclose(near[..., perm], ref.norm_rope(x[..., perm], rows=rows)[0])
+
+
+def heads(qp, x=P, out=2 * P, weight=0, ldx=256, ldo=256, n=2, reserved=0):
+    return qp._Heads(x or None, out or None, weight or None, ldx, ldo, n, reserved)
+
+
+def call_heads(qp, q=None, k=None, n=4, dim=128, dt=0, odt=0, eps=1e-6, rope=P, rows=10, turn=128, near=0, t=None, seqs=0,
+               pos=P):
+    q = heads(qp) if q is None else q
+    return qp.lib().qpack_qk_norm_rope(ctypes.byref(q), None if k is None else ctypes.byref(k), n, dim, dt, odt, eps,
+                                       rope or None, rows, turn, near, t, seqs or None, pos or None, None)
+
+
+def test_heads_refusals(qp):
+    c = lambda **kw: call_heads(qp, **kw)  # noqa: E731
+    h = lambda **kw: heads(qp, **kw)  # noqa: E731
+    assert c(n=0) == OK and c(q=h(n=0)) == OK and qp.lib().qpack_qk_norm_rope(
+        None, None, 5, 128, 0, 0, 1e-6, None, 0, 0, 0, None, None, None, None) == OK
+    for bad in (dict(n=-1), dict(dt=3), dict(odt=-1), dict(eps=-1e-9), dict(eps=float("nan")), dict(eps=float("inf")),
+                dict(near=2), dict(pos=0), dict(rows=-1), dict(q=h(x=0)), dict(q=h(out=0)), dict(q=h(n=-1)),
+                dict(q=h(reserved=1)), dict(k=h(n=-2)), dict(q=h(out=P), odt=1), dict(q=h(out=P, ldo=264))):
+        assert c(**bad) == ARG, bad
+    for bad in (dict(dim=4), dict(dim=264), dict(dim=100), dict(turn=136), dict(turn=4), dict(turn=0), dict(turn=60),
+                dict(rope=0), dict(q=h(ldx=248)), dict(q=h(ldo=128)), dict(k=h(n=3)), dict(q=h(n=65537))):
+        assert c(**bad) == SHAPE, bad
+    for bad in (dict(q=h(x=P + 8)), dict(q=h(out=P + 4)), dict(q=h(weight=P + 4)), dict(q=h(ldx=260)), dict(rope=P + 8),
+                dict(pos=P + 2), dict(seqs=P + 1)):
+        assert c(**bad) == ALIGN, bad
+    t = qp._Tables(P, None, None, 4, 0, 2, 4)
+    assert c(t=ctypes.byref(t)) == ARG                     # sequences without lengths
+
+
+def test_heads_binding_refusals(qp):
+    x = torch.zeros(4, 2, 64)
+    pos = torch.zeros(4, dtype=torch.int32)
+    rope = torch.zeros(10, 64)
+    bad = [dict(q=x.view(4, 128)), dict(q=x.double()), dict(q=x.transpose(1, 2)), dict(q=x[:, :, ::2]),
+           dict(q=x, k=x[:3]), dict(q=x, k=x.half()), dict(q=x, k=torch.zeros(4, 2, 32)), dict(q=x, q_weight=torch.zeros(32)),
+           dict(q=x, q_weight=torch.zeros(128)), dict(q=x, q_weight=torch.zeros(64).half()), dict(q=x, rope=rope),
+           dict(q=x, rope=rope.half(), pos=pos), dict(q=x, rope=rope[0], pos=pos), dict(q=x, rope=rope[:, ::2], pos=pos),
+           dict(q=x, rope=rope, pos=pos.long()), dict(q=x, rope=rope, pos=pos[:3]), dict(q=x, q_out=x[:2]),
+           dict(q=x, q_out=x.double()), dict(q=x, rope=rope, pos=pos)]      # the last: not on a GPU
+    for kw in bad:
+        with pytest.raises(qp.QpackError):
+            qp.qpack_qk_norm_rope(**kw)
