@@ -92,6 +92,7 @@ def lib():
                 "qpack_kv_copy_pages": ([P, P, P, I64, P], I),
                 "qpack_kv_page_workspace": ([P, P, ctypes.POINTER(I64)], I),
                 "qpack_qk_norm_rope": ([P, P, I64, I, I, I, ctypes.c_float, P, I64, I, I, P, P, P, P], I),
+                "qpack_sample": ([P, I, I64, I64, I64, P, P, P, P, P, P, P, P], I),
                 "qpack_status_string": ([I], ctypes.c_char_p),
                 "qpack_fetch_fault_flags": ([ctypes.POINTER(ctypes.c_int32)], I),
                 "qpack_version": ([], I),
@@ -648,10 +649,12 @@ class _Heads(ctypes.Structure):
 
 def _here(stream, *tensors):
     """All of them on the device that the call runs on: the current one, or the stream's."""
-    dev = _current_device() if stream is None or not isinstance(stream, torch.cuda.Stream) else stream.device_index
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise QpackError(f"a tensor is on {t.device}, the call runs on device {dev}")
+    on = {t.get_device() for t in tensors if t is not None}
+    if -1 in on:
+        raise QpackError("qpack kernels take CUDA tensors")
+    dev = stream.device_index if isinstance(stream, torch.cuda.Stream) else _current_device()
+    if on != {dev}:
+        raise QpackError(f"tensors on devices {sorted(on)}, the call runs on {dev}")
 
 
 def _side(x, out, weight, what, like, stream):
@@ -706,6 +709,43 @@ def qpack_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, eps=1e-6, rope=N
     if rc:
         _check(rc, "qpack_qk_norm_rope")
     return q_out, k_out
+
+
+def _need_each(t, dtype, what, n):
+    """A number a row."""
+    if t is not None and (t.dtype is not dtype or t.numel() < n or not t.is_contiguous()):
+        _need(t, dtype, what, numel=n)
+
+
+def qpack_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None, stream=None):
+    """The next token of each row of logits [B, V] (float32, float16 or bfloat16; -inf masks a token) by the random numbers
+    u (float32 [B], in [0, 1)). temperature, top_p, min_p (float32 [B]) and top_k (int32 [B]) may each be left out; a
+    temperature of 0 takes the largest logit, top_k 0, top_p 1 and min_p 0 switch a row's filter off. Returns tokens, int32 [B]
+    (-1 for a row that is masked altogether); probs, a float32 [B] tensor if wanted, gets the token's share among those kept."""
+    code = _DTYPE_CODE.get(logits.dtype)
+    if code is None:
+        raise QpackError(f"logits: expected float32, float16 or bfloat16, got {logits.dtype}")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise QpackError(f"logits: expected a row-major matrix, got {tuple(logits.shape)} with strides {tuple(logits.stride())}")
+    B, V = logits.shape
+    if u is None:
+        raise QpackError("u: a random number for each row is needed")
+    _need_each(u, torch.float32, "u", B)
+    _need_each(temperature, torch.float32, "temperature", B)
+    _need_each(top_k, torch.int32, "top_k", B)
+    _need_each(top_p, torch.float32, "top_p", B)
+    _need_each(min_p, torch.float32, "min_p", B)
+    if tokens is None:
+        tokens = _out(stream, (B,), torch.int32, logits.device)
+    _need_each(tokens, torch.int32, "tokens", B)
+    _need_each(probs, torch.float32, "probs", B)
+    _here(stream, logits, u, temperature, top_k, top_p, min_p, tokens, probs)
+    rc = (_lib or lib()).qpack_sample(_addr(logits), code, logits.stride(0), V, B, _addr(temperature), _addr(top_k),
+                                      _addr(top_p), _addr(min_p), _addr(u), _addr(tokens), _addr(probs),
+                                      _raw_stream(stream))
+    if rc:
+        _check(rc, "qpack_sample")
+    return tokens
 
 
 def qpack_fetch_fault_flags() -> int:

@@ -537,6 +537,20 @@ int qpack_qk_norm_rope(const qpack_heads_t *q, const qpack_heads_t *k, int64_t n
     return cuda_status(launch_heads(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int qpack_sample(const void *logits, int dt, int64_t ld, int64_t V, int64_t B, const float *temperature,
+                 const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *tokens,
+                 float *probs, qpack_stream_t stream) {
+    if (B < 0 || V < 0 || dt < QPACK_F32 || dt > QPACK_BF16) return QPACK_ERR_ARG;
+    if (V < 1 || V > (1 << 20) || B > 0x7FFFFFFF || (B > 1 && ld < V)) return QPACK_ERR_SHAPE;
+    if (B == 0) return QPACK_OK;
+    if (!logits || !u || !tokens) return QPACK_ERR_ARG;
+    if (!aligned(logits, dt == QPACK_F32 ? 4 : 2) || !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) ||
+        !aligned(min_p, 4) || !aligned(u, 4) || !aligned(tokens, 4) || !aligned(probs, 4))
+        return QPACK_ERR_ALIGN;
+    SampleArgs a = {logits, ld, B, V, temperature, top_k, top_p, min_p, u, tokens, probs, dt, 0};
+    return cuda_status(launch_sample(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 const char *qpack_status_string(int status) {
     switch (status) {
         case QPACK_OK: return "QPACK_OK";

@@ -144,6 +144,21 @@ struct HeadsArgs {
 cudaError_t launch_heads(const HeadsArgs &a, cudaStream_t s);
 cudaError_t fault_word_heads(int **word);
 
+// The draw of tokens from logits (qpack_sample.cu).
+struct SampleArgs {
+    const void *logits;
+    int64_t ld, rows, vocab;
+    const float *temperature;    // null: 1
+    const int32_t *top_k;        // these null: no filter
+    const float *top_p, *min_p;
+    const float *u;
+    int32_t *tokens;
+    float *probs;                // or null
+    int dt, places;              // places: binary places of a weight, set by the launcher
+};
+cudaError_t launch_sample(SampleArgs a, cudaStream_t s);
+cudaError_t fault_word_sample(int **word);
+
 cudaError_t fetch_faults(int32_t *flags);
 
 int num_sms();

@@ -358,6 +358,28 @@ int qpack_qk_norm_rope(const qpack_heads_t *q, const qpack_heads_t *k, int64_t n
                        const float *rope, int64_t rope_rows, int rope_dim, int interleaved, const qpack_kv_tables_t *t,
                        const int32_t *seqs, const int32_t *pos, qpack_stream_t stream);
 
+/* The next token of each row from its logits x_0 .. x_{V-1}, by a given random number. With m = max x and
+ * w_i = e^{(x_i - m) / T}:
+ *   order   tokens by falling logit, the lowest index first among equals
+ *   top_k   k of them are kept (k <= 0, or as many as there are: all)
+ *   top_p   of these, the shortest run from the top whose weights reach top_p of the sum of these (at least one; >= 1: all)
+ *   min_p   of these, the ones with w_i >= min_p (<= 0: all; >= 1: those of the maximum)
+ *   token   the lowest index whose sum of kept weights up to and including it passes u times their total
+ * Weights and sums are exact to some 2^-43 of the largest weight, and do not depend on the order in which blocks run.
+ * A logit of -inf masks its token: it is not counted and never drawn. A row without any other gives token -1 and
+ * probability 0. A temperature below 2^-64 (0, negative or NaN too) gives the lowest index of the maximum and probability 1;
+ * one above 2^64 counts as 2^64. A NaN among the filters' numbers switches the filter off. u outside [0, 1) counts as the
+ * nearest number inside, NaN as 0. A logit of NaN or +inf gives token -1 and probability NaN for its row, and sets
+ * QPACK_FAULT_NONFINITE_X.
+ *  logits       [B, ld] of dtype dt (QPACK_F32, F16 or BF16), aligned to its elements, ld >= V; V at most 2^20
+ *  temperature, top_k, top_p, min_p  [B] fp32 (top_k int32), or NULL: 1, and no filter
+ *  u            [B] fp32
+ *  tokens       [B] int32;  probs  [B] fp32, or NULL: the token's weight over the total of those kept
+ * No output overlaps an input. */
+int qpack_sample(const void *logits, int dt, int64_t ld, int64_t V, int64_t B, const float *temperature,
+                 const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *tokens,
+                 float *probs, qpack_stream_t stream);
+
 /* Human-readable name of a qpack_status value. Never NULL. */
 const char *qpack_status_string(int status);
 

@@ -1,4 +1,4 @@
-"""Host-side checks of the operators around the cache (norm and rotation of heads): the restatement that the GPU tests
+"""Host-side checks of the operators around the cache (norm and rotation of heads, the draw of tokens): the restatement that the GPU tests
 compare with against independent pins, and the refusals of the C ABI and of the binding, which come before any launch."""
 import ctypes
 
@@ -92,3 +92,69 @@ def test_heads_binding_refusals(qp):
     for kw in bad:
         with pytest.raises(qp.QpackError):
             qp.qpack_qk_norm_rope(**kw)
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# the draw of tokens
+# ---------------------------------------------------------------------------------------------------------------
+def test_sample_restatement_by_hand():
+    """A row whose weights are powers of two: 4 2 1 1 over their sum 8, at tokens 2, 0, 1 and 3."""
+    x = np.log(np.array([2.0, 1.0, 4.0, 1.0]))
+    at = lambda u, **kw: ref.sample(x, u, **kw)[0]  # noqa: E731
+    assert [at(u) for u in (0.0, 0.24, 0.26, 0.37, 0.38, 0.87, 0.88)] == [0, 0, 1, 1, 2, 2, 3]
+    assert ref.sample(x, 0.5)[1] == pytest.approx(0.5)
+    assert list(ref.sample(x, 0.5, top_k=3)[2]) == [0, 1, 2]           # of equals the lowest index
+    assert list(ref.sample(x, 0.5, top_p=0.49)[2]) == [2] and list(ref.sample(x, 0.5, top_p=0.51)[2]) == [0, 2]
+    assert list(ref.sample(x, 0.5, top_k=2, top_p=0.7)[2]) == [0, 2]   # p of the two's sum: 4 / 6 < 0.7
+    assert list(ref.sample(x, 0.5, top_k=2, top_p=0.66)[2]) == [2]
+    assert list(ref.sample(x, 0.5, min_p=0.3)[2]) == [0, 2] and list(ref.sample(x, 0.5, min_p=1.0)[2]) == [2]
+    assert ref.sample(x, 0.99, temperature=0.0)[:2] == (2, 1.0)
+    assert ref.sample(x, 0.5, temperature=0.5)[1] == pytest.approx(16 / 22)
+    x[2] = -np.inf
+    assert [at(u) for u in (0.49, 0.51, 0.76)] == [0, 1, 3] and at(0.9, top_k=1) == 0
+    assert ref.sample(np.full(3, -np.inf), 0.5)[:2] == (-1, 0.0)
+
+
+def test_sample_restatement_against_sorting():
+    """The filters as they are usually written, on sorted probabilities."""
+    rng = np.random.default_rng(3)
+    for _ in range(50):
+        x = rng.normal(size=200) * 2
+        t, k, p, m = rng.uniform(0.3, 2), int(rng.integers(1, 150)), rng.uniform(0.1, 0.99), rng.uniform(0, 0.2)
+        q = torch.from_numpy(x / t).softmax(0)
+        v, i = q.sort(descending=True)
+        v, i = v[:k] / v[:k].sum(), i[:k]
+        keep = (v.cumsum(0) - v) < p
+        v, i = v[keep], i[keep]
+        keep = v >= m * v[0]
+        want = sorted(i[keep].tolist())
+        assert list(ref.sample(x, rng.random(), t, k, p, m)[2]) == want
+
+
+def call_sample(qp, logits=P, dt=0, ld=100, V=100, B=3, t=0, k=0, p=0, m=0, u=P, tokens=P, probs=0):
+    return qp.lib().qpack_sample(logits or None, dt, ld, V, B, t or None, k or None, p or None, m or None, u or None,
+                                 tokens or None, probs or None, None)
+
+
+def test_sample_refusals(qp):
+    c = lambda **kw: call_sample(qp, **kw)  # noqa: E731
+    assert c(B=0) == OK and c(B=0, logits=0, u=0, tokens=0) == OK
+    for bad in (dict(B=-1), dict(V=-1), dict(dt=3), dict(dt=-1), dict(logits=0), dict(u=0), dict(tokens=0)):
+        assert c(**bad) == ARG, bad
+    for bad in (dict(V=0), dict(V=2 ** 20 + 1, ld=2 ** 21), dict(ld=99), dict(B=2 ** 31)):
+        assert c(**bad) == SHAPE, bad
+    for bad in (dict(logits=P + 2), dict(logits=P + 1, dt=1), dict(u=P + 2), dict(tokens=P + 1), dict(probs=P + 2), dict(t=P + 1),
+                dict(k=P + 2), dict(p=P + 3), dict(m=P + 2)):
+        assert c(**bad) == ALIGN, bad
+
+
+def test_sample_binding_refusals(qp):
+    x, u, i = torch.zeros(4, 10), torch.zeros(4), torch.zeros(4, dtype=torch.int32)
+    bad = [dict(logits=x[0], u=u), dict(logits=x.double(), u=u), dict(logits=x.t(), u=u), dict(logits=x[:, ::2], u=u),
+           dict(logits=x, u=None), dict(logits=x, u=u[:3]), dict(logits=x, u=u.double()), dict(logits=x, u=u, temperature=u[:2]),
+           dict(logits=x, u=u, top_k=i.long()), dict(logits=x, u=u, top_k=u), dict(logits=x, u=u, top_p=u.half()),
+           dict(logits=x, u=u, min_p=torch.zeros(8)[::2]), dict(logits=x, u=u, tokens=i[:3]), dict(logits=x, u=u, tokens=u),
+           dict(logits=x, u=u, probs=i), dict(logits=x, u=u)]              # the last: not on a GPU
+    for kw in bad:
+        with pytest.raises(qp.QpackError):
+            qp.qpack_sample(**kw)
