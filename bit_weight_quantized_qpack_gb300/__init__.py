@@ -85,6 +85,9 @@ def lib():
                 "qpack_kv_attend": ([P, I, P, P, I, P, I, I64, I, ctypes.c_float, I64, P, I64, P, I, I64, P, P, I64, P],
                                     I),
                 "qpack_kv_attend_workspace": ([P, I, I, ctypes.POINTER(I64)], I),
+                "qpack_kv_attend_shared": ([P, I, P, P, I, P, P, I, P, I, I64, I, ctypes.c_float, P, I64, P, I, I64, P, P, I64, P],
+                                           I),
+                "qpack_kv_shared_workspace": ([P, I, I, ctypes.POINTER(I64)], I),
                 "qpack_kv_reserve": ([P, P, P, P, I64, P], I),
                 "qpack_kv_fork": ([P, P, P, P, I64, P, I64, P], I),
                 "qpack_kv_free": ([P, P, I64, P], I),
@@ -566,6 +569,53 @@ def qpack_kv_attend(pool, layer, tables, q, seqs=None, scale=None, window=0, rop
                                          odt, ldo, _addr(lse), workspace._p, workspace.bytes, _raw_stream(stream))
     if rc:
         _check(rc, "qpack_kv_attend")
+    return out
+
+
+def alloc_kv_shared_workspace(pool, batch, q_heads) -> KVWorkspace:
+    """For qpack_kv_attend_shared with up to `batch` rows (and for qpack_kv_attend)."""
+    n = ctypes.c_int64(0)
+    rc = (_lib or lib()).qpack_kv_shared_workspace(pool._ref, batch, q_heads, ctypes.byref(n))
+    if rc:
+        _check(rc, "qpack_kv_shared_workspace")
+    return KVWorkspace(n.value, pool.k.device, KV_ATTEND_ZEROED)
+
+
+def qpack_kv_attend_shared(pool, layer, tables, q, first, prefix, seqs=None, scale=None, rope=None, out=None, lse=None,
+                           workspace=None, stream=None):
+    """qpack_kv_attend for rows in groups that share a prefix: rows first[g] .. first[g + 1] - 1 (int32 [groups + 1]) have
+    the first prefix[g] tokens (int32 [groups]) in common, which are read once, from the pages of the group's first row; the
+    rest of a row's tokens are its own. The other arguments and the result are qpack_kv_attend's. A kept workspace
+    (alloc_kv_shared_workspace) saves its allocation."""
+    D, shape = pool.dim, q.shape
+    q_heads = shape[1] if len(shape) == 3 else shape[-1] // D
+    qdt, ldq, B = _need_rows(q, "q", q_heads, D)
+    groups = prefix.numel()
+    _need_i32(prefix, "prefix", groups)
+    if first.numel() != groups + 1:
+        raise QpackError(f"first: expected {groups + 1} rows for {groups} prefixes, got {first.numel()}")
+    _need_i32(first, "first", groups + 1)
+    if out is None:
+        out = _out(stream, shape, torch.float16, q.device)
+    odt, ldo, rows = _need_rows(out, "out", q_heads, D)
+    if rows < B:
+        raise QpackError(f"out: expected at least {B} rows, got {rows}")
+    _need_i32(seqs, "seqs", B)
+    if seqs is None and tables.tables.shape[0] < B:
+        raise QpackError(f"q: {B} rows, but the table has {tables.tables.shape[0]} sequences")
+    if lse is not None:
+        _need(lse, torch.float32, "lse", numel=B * q_heads)
+    rows = _need_rope(rope, D)
+    _here(stream, pool.k, tables.lens, q, first, prefix, out, lse, seqs, rope)
+    if workspace is None:
+        with _on(stream):
+            workspace = alloc_kv_shared_workspace(pool, B, q_heads)
+    rc = (_lib or lib()).qpack_kv_attend_shared(pool._ref, layer, tables._ref, _addr(seqs), B, _addr(first), _addr(prefix),
+                                                groups, _addr(q), qdt, ldq, q_heads, D ** -0.5 if scale is None else scale,
+                                                _addr(rope), rows, _addr(out), odt, ldo, _addr(lse), workspace._p,
+                                                workspace.bytes, _raw_stream(stream))
+    if rc:
+        _check(rc, "qpack_kv_attend_shared")
     return out
 
 

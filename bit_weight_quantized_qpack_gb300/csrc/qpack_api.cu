@@ -440,8 +440,40 @@ int qpack_kv_attend(const qpack_kv_pool_t *pool, int layer, const qpack_kv_table
     if (!ws) return QPACK_ERR_ARG;
     if (ws_bytes < kv_attend_workspace(*pool, q_heads)) return QPACK_ERR_SHAPE;
     AttendArgs a = {*pool, *t, seqs, q, ldq, rope, rope_rows, out, ldo, lse, ws, window, scale, layer, B, q_heads, qdt,
-                    odt};
+                    odt, nullptr};
     const cudaError_t e = launch_kv_attend(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaErrorNotSupported ? QPACK_ERR_UNSUPPORTED : cuda_status(e);
+}
+
+int qpack_kv_shared_workspace(const qpack_kv_pool_t *pool, int B, int q_heads, int64_t *bytes) {
+    if (!bytes || B < 0 || q_heads < 1) return QPACK_ERR_ARG;
+    if (int rc = check_pool(pool, false)) return rc;
+    if (B > 4096 || q_heads > 65536 || q_heads % pool->heads) return QPACK_ERR_SHAPE;
+    *bytes = kv_shared_workspace(*pool, B, q_heads);
+    return QPACK_OK;
+}
+
+int qpack_kv_attend_shared(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_t *t, const int32_t *seqs, int B,
+                           const int32_t *first, const int32_t *prefix, int groups, const void *q, int qdt, int64_t ldq,
+                           int q_heads, float scale, const float *rope, int64_t rope_rows, void *out, int odt, int64_t ldo,
+                           float *lse, void *ws, int64_t ws_bytes, qpack_stream_t stream) {
+    int rc;
+    if ((rc = check_pool(pool)) || (rc = check_tables(t, false))) return rc;
+    if (layer < 0 || layer >= pool->layers || B < 0 || q_heads < 1 || groups < 0) return QPACK_ERR_ARG;
+    if (qdt < QPACK_F32 || qdt > QPACK_BF16 || odt < QPACK_F32 || odt > QPACK_BF16) return QPACK_ERR_ARG;
+    if (q_heads % pool->heads || q_heads > 65536 || B > 4096 || groups > 1024) return QPACK_ERR_SHAPE;
+    if (B == 0) return QPACK_OK;
+    const int64_t width = int64_t(q_heads) * pool->dim;
+    if ((rc = check_rows(q, ldq, width)) || (rc = check_rows(out, ldo, width)) || (rc = check_rope(rope, rope_rows)))
+        return rc;
+    if (groups > 0 && (!first || !prefix)) return QPACK_ERR_ARG;
+    if (!aligned(seqs, 4) || !aligned(lse, 4) || !aligned(ws, 16) || !aligned(first, 4) || !aligned(prefix, 4))
+        return QPACK_ERR_ALIGN;
+    if (!ws) return QPACK_ERR_ARG;
+    if (ws_bytes < kv_shared_workspace(*pool, B, q_heads)) return QPACK_ERR_SHAPE;
+    SharedArgs a = {*pool, *t, seqs, first, prefix, q, ldq, rope, rope_rows, out, ldo, lse, ws, scale, layer, B, groups, q_heads,
+                    qdt, odt, 0, 0};
+    const cudaError_t e = launch_kv_attend_shared(a, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaErrorNotSupported ? QPACK_ERR_UNSUPPORTED : cuda_status(e);
 }
 

@@ -275,8 +275,9 @@ template <int TOK> __device__ __forceinline__ Row row_of(const Params &p, int b,
     r.table = a.t.tables + (known ? int64_t(seq) * a.t.stride : 0);
     r.len = unsigned(len);
     r.lo = a.window > 0 && len > a.window ? unsigned(len - a.window) : 0u;
+    if (a.from) r.lo = min(unsigned(a.from[p.row0 + b]), r.len);       // a window is not given with it
     r.base = r.lo / TOK * TOK;
-    r.tiles = (r.len - r.base + TOK - 1) / TOK;
+    r.tiles = r.lo < r.len ? (r.len - r.base + TOK - 1) / TOK : 0u;
     return r;
 }
 

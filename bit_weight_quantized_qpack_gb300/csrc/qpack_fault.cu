@@ -7,7 +7,7 @@
 namespace qpack {
 namespace {
 
-constexpr int WORDS = 8;
+constexpr int WORDS = 11;
 struct Words {
     int *at[WORDS];
 };
@@ -30,6 +30,7 @@ cudaError_t fetch_faults(int32_t *flags) {
     if (e == cudaSuccess) e = fault_words_attend(&w.at[3]);
     if (e == cudaSuccess) e = fault_word_heads(&w.at[6]);
     if (e == cudaSuccess) e = fault_word_sample(&w.at[7]);
+    if (e == cudaSuccess) e = fault_words_shared(&w.at[8]);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1);

@@ -106,9 +106,32 @@ struct AttendArgs {
     int64_t window;
     float scale;
     int layer, B, q_heads, qdt, odt;
+    const int *from;             // null, or each row's first token (on the device)
 };
 cudaError_t launch_kv_attend(const AttendArgs &a, cudaStream_t s);
 int64_t kv_attend_workspace(const qpack_kv_pool_t &pool, int q_heads);
+
+// Attention where groups of rows share a prefix (qpack_shared.cu).
+struct SharedArgs {
+    qpack_kv_pool_t pool;
+    qpack_kv_tables_t t;
+    const int32_t *seqs;
+    const int32_t *first, *prefix;   // [groups + 1], [groups]
+    const void *q;
+    int64_t ldq;
+    const float *rope;
+    int64_t rope_rows;
+    void *out;
+    int64_t ldo;
+    float *lse;
+    void *ws;
+    float scale;
+    int layer, B, groups, q_heads, qdt, odt;
+    int q_terms, p_terms;        // 16-bit terms of queries and probabilities, set by the launcher
+};
+cudaError_t launch_kv_attend_shared(const SharedArgs &a, cudaStream_t s);
+int64_t kv_shared_workspace(const qpack_kv_pool_t &pool, int64_t B, int q_heads);
+cudaError_t fault_words_shared(int **words);    // one a cache type
 
 cudaError_t launch_kv_reserve(const qpack_kv_pool_t &p, const qpack_kv_tables_t &t, const int32_t *seqs,
                               const int32_t *add, int n, cudaStream_t s);

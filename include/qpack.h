@@ -289,6 +289,28 @@ int qpack_kv_attend(const qpack_kv_pool_t *pool, int layer, const qpack_kv_table
                     qpack_stream_t stream);
 int qpack_kv_attend_workspace(const qpack_kv_pool_t *pool, int B, int q_heads, int64_t *bytes);
 
+/* Attention of one new token a row, as qpack_kv_attend without a window, for batches in which groups of rows share a prefix
+ * (samples forked from one prompt): a prefix is read once a group.
+ * Rows first[g] .. first[g + 1] - 1 are group g; they share the first prefix[g] tokens, which are read from the pages of the
+ * group's first row. Of a row's sequence (seqs as above, L = lens) the tokens t < min(L, prefix[g]) are those, and the tokens
+ * prefix[g] <= t < L are its own. Rows of no group have no prefix. With sequences that share their prefixes by
+ * qpack_kv_fork (full pages are the same, a last page that is not full is a copy) the result is qpack_kv_attend's.
+ *  first   [groups + 1] int32, rising from 0 or more to at most B (equal neighbours: a group without rows); anything else sets
+ *          QPACK_FAULT_PAGE, and all rows go without a prefix. May be NULL where groups is 0.
+ *  prefix  [groups] int32, 0 to the length of the group's first row; others are cut to that and set QPACK_FAULT_PAGE
+ *  groups  at most 1024
+ * Scores, maxima, sums and accumulators are fp32. Over the prefix, queries enter the tensor cores as two 16-bit terms (22 bits
+ * where the pool is 8-bit or fp16, 16 where it is bf16; one term where that holds them whole), probabilities as one (11 bits)
+ * where the pool is 8-bit or fp16 and the output has 16 bits, else as two. Own tokens are attended to as by qpack_kv_attend.
+ * The other arguments, limits and errors are qpack_kv_attend's.
+ *  ws      at least qpack_kv_shared_workspace bytes for this B or more, 16-byte aligned, the first QPACK_KV_ATTEND_ZEROED of
+ *          them zeroed once; as qpack_kv_attend's otherwise, and good for its calls too. */
+int qpack_kv_attend_shared(const qpack_kv_pool_t *pool, int layer, const qpack_kv_tables_t *t, const int32_t *seqs, int B,
+                           const int32_t *first, const int32_t *prefix, int groups, const void *q, int qdt, int64_t ldq,
+                           int q_heads, float scale, const float *rope, int64_t rope_rows, void *out, int odt, int64_t ldo,
+                           float *lse, void *ws, int64_t ws_bytes, qpack_stream_t stream);
+int qpack_kv_shared_workspace(const qpack_kv_pool_t *pool, int B, int q_heads, int64_t *bytes);
+
 /* Page operators. All work on the device alone and are deterministic: new pages are the lowest-numbered free ones, in
  * the order of the requests. n <= 4096 sequences a call, each listed once.
  *

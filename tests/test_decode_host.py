@@ -158,3 +158,56 @@ def test_sample_binding_refusals(qp):
     for kw in bad:
         with pytest.raises(qp.QpackError):
             qp.qpack_sample(**kw)
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# attention over shared prefixes
+# ---------------------------------------------------------------------------------------------------------------
+def call_shared(qp, layer=0, seqs=0, B=4, first=P, prefix=P, groups=2, q=P, qdt=0, ldq=1024, q_heads=8, scale=0.1, rope=0, rows=0,
+                out=P, odt=1, ldo=1024, lse=0, ws=P, ws_bytes=None, type=1, dim=128, heads=2, tables=P, seq=8):
+    pool = qp._Pool(P, P, None, None, 1 << 20, 1 << 14, 0, 0, 64, 1, heads, 16, dim, type, 0)
+    t = qp._Tables(tables or None, P, None, 8, 0, seq, 8)
+    if ws_bytes is None:
+        n = ctypes.c_int64(0)
+        good = qp._Pool(P, P, None, None, 1 << 20, 1 << 14, 0, 0, 64, 1, 2, 16, 128, 1, 0)
+        assert qp.lib().qpack_kv_shared_workspace(ctypes.byref(good), 4, 8, ctypes.byref(n)) == OK
+        ws_bytes = n.value
+    return qp.lib().qpack_kv_attend_shared(
+        ctypes.byref(pool), layer, ctypes.byref(t), seqs or None, B, first or None, prefix or None, groups, q or None, qdt, ldq,
+        q_heads, scale, rope or None, rows, out or None, odt, ldo, lse or None, ws or None, ws_bytes, None)
+
+
+def test_shared_refusals(qp):
+    c = lambda **kw: call_shared(qp, **kw)  # noqa: E731
+    assert c(B=0) == OK and c(B=0, q=0, out=0, ws=0, first=0, prefix=0) == OK
+    for bad in (dict(layer=1), dict(layer=-1), dict(B=-1), dict(groups=-1), dict(q_heads=0), dict(qdt=3), dict(odt=-1), dict(q=0),
+                dict(out=0), dict(ws=0), dict(first=0), dict(prefix=0), dict(rows=-1), dict(tables=0), dict(type=3)):
+        assert c(**bad) == ARG, bad
+    for bad in (dict(q_heads=7), dict(B=4097), dict(groups=1025), dict(ldq=1016), dict(ldo=512), dict(ws_bytes=1 << 20),
+                dict(dim=96), dict(q_heads=65536 + 2)):
+        assert c(**bad) == SHAPE, bad
+    for bad in (dict(q=P + 8), dict(out=P + 8), dict(ldq=1028), dict(ldo=1028), dict(first=P + 2), dict(prefix=P + 1),
+                dict(seqs=P + 2), dict(lse=P + 2), dict(ws=P + 8), dict(rope=P + 4)):
+        assert c(**bad) == ALIGN, bad
+    pool = qp._Pool(P, P, None, None, 1 << 20, 1 << 14, 0, 0, 64, 1, 2, 16, 128, 1, 0)
+    size = lambda B, h: qp.lib().qpack_kv_shared_workspace(ctypes.byref(pool), B, h, ctypes.byref(n)) or n.value  # noqa: E731
+    n = ctypes.c_int64(0)
+    assert size(-1, 8) == ARG and size(4, 0) == ARG and size(4, 7) == SHAPE and size(4097, 8) == SHAPE
+    assert size(0, 8) > 1 << 20 and size(64, 8) > size(8, 8)
+    assert qp.lib().qpack_kv_shared_workspace(ctypes.byref(pool), 4, 8, None) == ARG
+
+
+def test_shared_binding_refusals(qp):
+    pool = object.__new__(qp.KVPool)
+    pool.heads, pool.dim, pool.k = 2, 64, torch.zeros(1)
+    tab = object.__new__(qp.KVTables)
+    tab.tables, tab.lens = torch.zeros(4, 3, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
+    q, f, p = torch.zeros(4, 6, 64), torch.tensor([0, 2, 4], dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    ok = dict(q=q, first=f, prefix=p)
+    bad = [dict(q=q.double()), dict(q=q[:, :, :32]), dict(first=f.long()), dict(first=f[:2]), dict(prefix=p.float()),
+           dict(prefix=torch.zeros(4, dtype=torch.int32)[::2]), dict(q=torch.zeros(5, 6, 64)), dict(out=torch.zeros(3, 6, 64)),
+           dict(out=torch.zeros(4, 6, 64).double()), dict(lse=torch.zeros(5)), dict(lse=torch.zeros(24).half()),
+           dict(seqs=f.long()), dict(seqs=f[:3]), dict(rope=torch.zeros(4, 32)), dict()]      # the last: not on a GPU
+    for kw in bad:
+        with pytest.raises(qp.QpackError):
+            qp.qpack_kv_attend_shared(pool, 0, tab, **{**ok, **kw})
