@@ -461,7 +461,7 @@ int qpack_kv_attend_shared(const qpack_kv_pool_t *pool, int layer, const qpack_k
     if ((rc = check_pool(pool)) || (rc = check_tables(t, false))) return rc;
     if (layer < 0 || layer >= pool->layers || B < 0 || q_heads < 1 || groups < 0) return QPACK_ERR_ARG;
     if (qdt < QPACK_F32 || qdt > QPACK_BF16 || odt < QPACK_F32 || odt > QPACK_BF16) return QPACK_ERR_ARG;
-    if (q_heads % pool->heads || q_heads > 65536 || B > 4096 || groups > 1024) return QPACK_ERR_SHAPE;
+    if (q_heads % pool->heads || q_heads > 65536 || B > 4096 || groups > 512) return QPACK_ERR_SHAPE;
     if (B == 0) return QPACK_OK;
     const int64_t width = int64_t(q_heads) * pool->dim;
     if ((rc = check_rows(q, ldq, width)) || (rc = check_rows(out, ldo, width)) || (rc = check_rope(rope, rope_rows)))

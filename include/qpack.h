@@ -298,7 +298,7 @@ int qpack_kv_attend_workspace(const qpack_kv_pool_t *pool, int B, int q_heads, i
  *  first   [groups + 1] int32, rising from 0 or more to at most B (equal neighbours: a group without rows); anything else sets
  *          QPACK_FAULT_PAGE, and all rows go without a prefix. May be NULL where groups is 0.
  *  prefix  [groups] int32, 0 to the length of the group's first row; others are cut to that and set QPACK_FAULT_PAGE
- *  groups  at most 1024
+ *  groups  at most 512
  * Scores, maxima, sums and accumulators are fp32. Over the prefix, queries enter the tensor cores as two 16-bit terms (22 bits
  * where the pool is 8-bit or fp16, 16 where it is bf16; one term where that holds them whole), probabilities as one (11 bits)
  * where the pool is 8-bit or fp16 and the output has 16 bits, else as two. Own tokens are attended to as by qpack_kv_attend.

@@ -183,7 +183,7 @@ def test_shared_refusals(qp):
     for bad in (dict(layer=1), dict(layer=-1), dict(B=-1), dict(groups=-1), dict(q_heads=0), dict(qdt=3), dict(odt=-1), dict(q=0),
                 dict(out=0), dict(ws=0), dict(first=0), dict(prefix=0), dict(rows=-1), dict(tables=0), dict(type=3)):
         assert c(**bad) == ARG, bad
-    for bad in (dict(q_heads=7), dict(B=4097), dict(groups=1025), dict(ldq=1016), dict(ldo=512), dict(ws_bytes=1 << 20),
+    for bad in (dict(q_heads=7), dict(B=4097), dict(groups=513), dict(ldq=1016), dict(ldo=512), dict(ws_bytes=1 << 20),
                 dict(dim=96), dict(q_heads=65536 + 2)):
         assert c(**bad) == SHAPE, bad
     for bad in (dict(q=P + 8), dict(out=P + 8), dict(ldq=1028), dict(ldo=1028), dict(first=P + 2), dict(prefix=P + 1),
