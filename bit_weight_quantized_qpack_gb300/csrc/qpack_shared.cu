@@ -18,7 +18,7 @@ namespace {
 
 // The parts of the workspace behind the attention's own; bytes of all of it.
 int64_t lay_out(const qpack_kv_pool_t &pool, int64_t B, int q_heads, unsigned char *ws, Work &w) {
-    const int64_t n = B * q_heads, slots = int64_t(num_sms()) * 2 * (pool.dim <= 128 ? 2 * ROWS : ROWS);   // queries of a block
+    const int64_t n = B * q_heads, slots = int64_t(num_sms()) * 2 * (2 * ROWS);
     int64_t at = round_up(kv_attend_workspace(pool, q_heads), 16);
     auto part = [&](int64_t bytes) {
         unsigned char *p = ws ? ws + at : nullptr;

@@ -24,7 +24,7 @@ constexpr int THREADS = (MMA_WARP + 1) * 32, LOAD_THREADS = LOADERS * 32;
 
 // Where results go between the launches of a call. Written by the prefix kernel's first block: the plan of the call.
 struct Plan {
-    int size, total, blocks, ok;            // units of a block, of the call; blocks of the prefix kernel
+    int size, item;                         // units of a block; queries that a block takes together
     int cum[MAX_GROUPS + 1];                // units before group g
     int length[MAX_GROUPS];                 // its prefix, as used
     int from[MAX_BATCH];                    // a row's first token behind its prefix
@@ -35,8 +35,8 @@ struct Work {
     float *own_out, *own_lse;               // [B, q_heads, D], [B, q_heads]: attention over what rows have of their own
     float *direct;                          // [B, q_heads, D] accumulators of prefixes that one block took
     float2 *direct_ml;                      // [B, q_heads] their maxima (base 2) and sums
-    float *piece;                           // [blocks][2][queries of an item][D] of prefixes that several took
-    float2 *piece_ml;                       // [blocks][2][queries of an item]
+    float *piece;                           // [blocks][2][2 ROWS][D] of prefixes that several took
+    float2 *piece_ml;                       // [blocks][2][2 ROWS]
 };
 struct Params {
     SharedArgs a;
@@ -47,9 +47,8 @@ struct Params {
 // Shape of an instance.
 template <int KT, int D> struct Cfg {
     static constexpr bool BF = KT == QPACK_KV_BF16, I8 = KT == QPACK_KV_I8;
-    static constexpr bool DUAL = D <= 128;                 // two accumulators fit the tensor memory beside two tiles' scores
+    static constexpr bool TWO = D <= 128;                  // two accumulators fit the tensor memory beside two tiles' scores
     static constexpr int TOK = D == 256 ? 64 : 128;        // tokens of a tile
-    static constexpr int ITEM = DUAL ? 2 * ROWS : ROWS;    // queries that a block takes together
     static constexpr int BLOCKS = D / 64;                  // 128-byte columns of an operand
     static constexpr int QB = ROWS * 128, KB = TOK * 128;  // bytes of a column of queries, of a tile
     static constexpr int Q_BYTES = BLOCKS * QB, TILE_BYTES = BLOCKS * KB;
@@ -58,18 +57,22 @@ template <int KT, int D> struct Cfg {
     static constexpr int O_COL = 0, O_STEP = D, S_COL = 256, S_STEP = TOK;
     // Probabilities are held as 2^(x - m + BIAS), at most 2^(BIAS + GROW): m is a maximum that lags behind by up to GROW.
     static constexpr float BIAS = BF ? 0.0f : 7.0f, GROW = 8.0f;
-    // Shared memory: the queries' terms, a ring of tiles (keys or values of TOK tokens each), tables and barriers.
-    static constexpr int QUERIES = ITEM / ROWS * Q_BYTES;  // bytes of a term of the item's queries
-    static constexpr int REST = (MAX_GROUPS + 1) * 4 + 256;
-    static constexpr int ring(int terms) {
-        const int n = (227 * 1024 - REST - terms * QUERIES) / TILE_BYTES;
+    // Shared memory: the queries (one or two operands), 8-bit codes on their way (RAWS places), a ring of tiles of 16-bit keys or
+    // values, the plan and the barriers. The results of a segment are put together over the first three.
+    static constexpr int SMEM = 227 * 1024, REST = (MAX_GROUPS + 1) * 4 + (TWO ? 2 : 1) * ROWS * 4 + 256;
+    static constexpr int RAWS = !I8 ? 0 : D == 256 ? 2 : 4, RAW_BYTES = TOK * D, RAW_ALL = RAWS * RAW_BYTES;
+    static constexpr int ring(int operands) {
+        const int n = (SMEM - REST - operands * Q_BYTES - RAW_ALL) / TILE_BYTES;
         return n < 8 ? n : 8;
     }
-    static constexpr int smem(int terms) { return terms * QUERIES + ring(terms) * TILE_BYTES + REST; }
-    static_assert(ring(2) >= 3 && (!DUAL || 3 * TILE_BYTES >= ROWS * D * 4) && TILE_BYTES >= 3 * ITEM * 4, "the ring holds what is exchanged in it");
+    static constexpr int PS = D + 4;                       // floats of a row of results, padded for the banks
+    static_assert(ring(2) >= (I8 ? 2 : 3), "tiles");
+    static_assert((TWO ? 2 : 1) * ROWS * PS * 4 <= SMEM - REST, "results");
 };
 
 static __device__ int g_fault_shared = 0;
+
+template <bool V> struct Bool { static constexpr bool value = V; };
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -144,19 +147,6 @@ __device__ __forceinline__ int row_len(const SharedArgs &a, int seq) {
     const int64_t len = a.t.lens[seq];
     return int(len < 0 ? 0 : len > cap ? cap : len);
 }
-// Whether group g's rows are where rows can be.
-__device__ __forceinline__ bool group_ok(const SharedArgs &a, int g) {
-    const int lo = a.first[g], hi = a.first[g + 1];
-    return lo >= 0 && lo <= hi && hi <= a.B;
-}
-// The prefix that a group shares: as given, at most what its first row holds.
-__device__ __forceinline__ int group_prefix(const SharedArgs &a, int g, bool &bad) {
-    if (a.first[g] == a.first[g + 1]) return 0;
-    const int given = a.prefix[g], len = row_len(a, row_seq(a, a.first[g]));
-    bad = given < 0 || given > len;
-    return min(max(given, 0), len);
-}
-
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
@@ -186,7 +176,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 // A block's place in the call: a group, its key/value head and block of queries, the tiles of it that are this block's.
 struct Segment {
-    int g, h, mb, row0, rows, length, tile0, tile1, tiles, page_row;
+    int g, length, row0, rows, page_row;    // the group: its prefix, its rows, the sequence whose pages are read
+    int blocks, tiles;                      // blocks of queries, tiles of a block
+    int h, mb, tile0, nt;
 };
 
 // A place in the ring: slot, and the parity of the passes over it.
@@ -194,66 +186,47 @@ struct Slot {
     int at, phase;
     __device__ __forceinline__ void forward(int n, int ring) {
         at += n;
-        if (at >= ring) at -= ring, phase ^= 1;
+        while (at >= ring) at -= ring, phase ^= 1;
     }
 };
 
-// NP = 1, 2 or 4 consecutive elements of a query as loaded, and as fp32.
-template <int NP> struct Elems { uint32_t w[NP]; };
-template <int NP> __device__ __forceinline__ void load_elems(const void *p, int dt, int64_t i, Elems<NP> &r) {
+// N consecutive elements of a query as fp32, N a multiple of 4.
+template <int N> __device__ __forceinline__ void load_q(const void *p, int dt, int64_t i, float *x) {
     if (dt == DT_F32) {
-        const uint32_t *q = static_cast<const uint32_t *>(p) + i;
-        if (NP == 1) r.w[0] = q[0];
-        else if (NP == 2) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(q);
-            r.w[0] = v.x, r.w[NP > 1 ? 1 : 0] = v.y;
-        } else {
-            const uint4 v = *reinterpret_cast<const uint4 *>(q);
-            r.w[0] = v.x, r.w[NP > 1 ? 1 : 0] = v.y, r.w[NP > 2 ? 2 : 0] = v.z, r.w[NP > 3 ? 3 : 0] = v.w;
-        }
-    } else {
-        const uint16_t *q = static_cast<const uint16_t *>(p) + i;
-        if (NP == 1) r.w[0] = q[0];
-        else if (NP == 2) r.w[0] = *reinterpret_cast<const uint32_t *>(q);
-        else {
-            const uint2 v = *reinterpret_cast<const uint2 *>(q);
-            r.w[0] = v.x, r.w[NP > 1 ? 1 : 0] = v.y;
-        }
-    }
-}
-template <int NP> __device__ __forceinline__ void widen(const Elems<NP> &r, int dt, float *x) {
 #pragma unroll
-    for (int e = 0; e < NP; ++e) {
-        const uint32_t h = e & 1 ? r.w[e / 2] >> 16 : r.w[e / 2] & 0xFFFFu;
-        x[e] = dt == DT_F32 ? __uint_as_float(r.w[e]) : dt == DT_F16 ? h2f_bits(uint16_t(h)) : __uint_as_float(h << 16);
+        for (int e = 0; e < N; e += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + e);
+            x[e] = v.x, x[e + 1] = v.y, x[e + 2] = v.z, x[e + 3] = v.w;
+        }
+        return;
     }
-}
-// NP elements of 16 bits each into shared memory.
-template <int NP> __device__ __forceinline__ void put(uint8_t *p, const uint32_t *w) {
-    if (NP == 1) *reinterpret_cast<uint16_t *>(p) = uint16_t(w[0]);
-    else if (NP == 2) *reinterpret_cast<uint32_t *>(p) = w[0];
-    else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[NP > 2 ? 1 : 0]);
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i + e);
+        const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t h = k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu;
+            x[e + k] = dt == DT_F16 ? h2f_bits(uint16_t(h)) : __uint_as_float(h << 16);
+        }
+    }
 }
 
 template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_kernel(const __grid_constant__ Params p) {
     using F = Cfg<KT, D>;
-    constexpr int TOK = F::TOK, ITEM = F::ITEM;
-    constexpr bool BF = F::BF, I8 = F::I8, DUAL = F::DUAL;
+    constexpr int TOK = F::TOK, PS = F::PS;
+    constexpr bool BF = F::BF, I8 = F::I8, TWO = F::TWO;
     extern __shared__ __align__(1024) uint8_t sm[];
     const SharedArgs &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int R = F::ring(a.q_terms);
     const uint32_t base = smem_u32(sm);
-    uint8_t *const ring = sm + a.q_terms * F::QUERIES;
-    const uint32_t ring32 = smem_u32(ring);
-    int *const cum = reinterpret_cast<int *>(ring + R * F::TILE_BYTES);
-    uint64_t *const full = reinterpret_cast<uint64_t *>(cum + MAX_GROUPS + 2), *const empty = full + 8;
+    int *const cum = reinterpret_cast<int *>(sm + F::SMEM - F::REST);
+    float *const x_scale = reinterpret_cast<float *>(cum + MAX_GROUPS + 1);
+    uint64_t *const full = reinterpret_cast<uint64_t *>(sm + F::SMEM - 248), *const empty = full + 8;
     uint64_t *const s_full = empty + 8, *const p_full = s_full + 2, *const pv_done = p_full + 2, *const o_done = pv_done + 1;
     uint32_t *const s_tmem = reinterpret_cast<uint32_t *>(o_done + 1);
     volatile int *const s_ok = reinterpret_cast<volatile int *>(s_tmem + 1), *const s_dead = s_ok + 1;
-    // what is exchanged in the ring while it is empty
-    int *const x_len = reinterpret_cast<int *>(ring), *const x_lim = x_len + ITEM;
-    float *const x_scale = reinterpret_cast<float *>(x_lim + ITEM);
+    int *const s_group = reinterpret_cast<int *>(s_tmem + 3);      // the first segment's: number, prefix, row, rows, sequence
 
     if (base & 1023) {                                     // operands are laid out from a multiple of 1024 bytes on
         if (tid == 0) atomicOr(&g_fault_shared, FAULT_WAIT_TMEM);
@@ -270,53 +243,62 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
         tmem_alloc(s_tmem, 512);
         tmem_relinquish();
     }
+    pdl_launch_dependents();
+    pdl_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    pdl_launch_dependents();
-    pdl_wait();
 
-    // -- the plan ------------------------------------------------------------------------------------------
-    for (int g = tid; g < a.groups; g += THREADS) {
-        bool bad = false;
-        int units = 0;
-        if (!group_ok(a, g)) {
+    // -- the plan: a thread a group ---------------------------------------------------------------------------
+    static_assert(MAX_GROUPS <= THREADS, "a thread a group");
+    int length = 0, row0 = 0, rows = 0, page_row = -1;
+    if (tid < a.groups) {
+        row0 = a.first[tid], rows = a.first[tid + 1] - row0;
+        const int given = a.prefix[tid];
+        if (row0 < 0 || rows < 0 || row0 + int64_t(rows) > a.B) {
             *s_ok = 0;
-        } else {
-            const int n = group_prefix(a, g, bad), rows = a.first[g + 1] - a.first[g];
-            units = (n + TOK - 1) / TOK * ((rows * p.G + ITEM - 1) / ITEM) * a.pool.heads;
-            if (blockIdx.x == 0) p.w.plan->length[g] = n;
+        } else if (rows > 0) {
+            page_row = row_seq(a, row0);
+            const int len = row_len(a, page_row);
+            length = min(max(given, 0), len);
+            if ((given < 0 || given > len) && blockIdx.x == 0) atomicOr(&g_fault_shared, FAULT_PAGE);
         }
-        if (bad && blockIdx.x == 0) atomicOr(&g_fault_shared, FAULT_PAGE);
-        cum[g + 1] = units;
     }
-    __syncthreads();
+    const int tiles = (length + TOK - 1) / TOK, queries = rows * p.G;
+    // Two blocks of queries at a time share a tile's conversion and its way from L2, where queries are one term each (with two
+    // the products take longer than either) and every block gets enough tiles to pay for twice the queries and results.
+    const int most = TWO && a.q_terms == 1 ? __syncthreads_or(queries > ROWS && int64_t(tiles) * ((queries + 2 * ROWS - 1) / (2 * ROWS)) *
+                                                              a.pool.heads >= 6 * int64_t(gridDim.x)) : (__syncthreads(), 0);
+    const int item = most ? 2 * ROWS : ROWS;
     const bool ok = *s_ok;
-    if (warp == 0) {
-        int carry = 0;
-        for (int g0 = 0; g0 < a.groups; g0 += 32) {
-            int x = g0 + lane < a.groups && ok ? cum[g0 + lane + 1] : 0;
+    const int units = ok ? tiles * ((queries + item - 1) / item) * a.pool.heads : 0;
+    {                                                      // inclusive sums over the groups
+        int x = units;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
-            }
-            x += carry;
-            if (g0 + lane < a.groups) cum[g0 + lane + 1] = x;
-            carry = __shfl_sync(0xffffffffu, x, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
         }
-        if (lane == 0) cum[0] = 0;
+        if (lane == 31) x_scale[warp] = __int_as_float(x);
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) x += __float_as_int(x_scale[w]);
+        if (tid < a.groups) cum[tid + 1] = x;
+        if (tid == 0) cum[0] = 0;
     }
     __syncthreads();
     const int total = cum[a.groups], size = max(1, (total + int(gridDim.x) - 1) / int(gridDim.x));
-    if (blockIdx.x == 0) {
+    const int unit0 = min(int(blockIdx.x) * size, total), unit1 = min(unit0 + size, total);
+    if (tid < a.groups && cum[tid] <= unit0 && unit0 < cum[tid + 1])
+        s_group[0] = tid, s_group[1] = length, s_group[2] = row0, s_group[3] = rows, s_group[4] = page_row;
+    if (blockIdx.x == gridDim.x - 1) {                     // the block with the least to do
         Plan &pl = *p.w.plan;
         if (tid == 0) {
-            pl.size = size, pl.total = total, pl.blocks = gridDim.x, pl.ok = ok;
+            pl.size = size, pl.item = item;
             if (!ok) atomicOr(&g_fault_shared, FAULT_PAGE);
         }
-        for (int g = tid; g <= a.groups; g += THREADS) pl.cum[g] = cum[g];
+        if (tid < a.groups) pl.cum[tid] = cum[tid], pl.length[tid] = length;
+        __syncthreads();
         for (int b = tid; b < a.B; b += THREADS) {
             int g = -1, from = 0;
             if (ok && a.groups > 0 && b >= a.first[0] && b < a.first[a.groups]) {
@@ -325,130 +307,114 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     const int mid = (lo + hi) >> 1;
                     if (a.first[mid] <= b) lo = mid; else hi = mid;
                 }
-                g = lo;
-                bool bad;
-                from = group_prefix(a, g, bad);
+                g = lo, from = pl.length[lo];
             }
             pl.group[b] = g, pl.from[b] = from;
         }
     }
+    __syncthreads();
+    if (unit0 >= unit1) {
+        if (warp == MMA_WARP) tmem_dealloc(tmem, 512);
+        return;
+    }
 
     // -- this block's units --------------------------------------------------------------------------------
-    const int unit1 = min((int(blockIdx.x) + 1) * size, total);
+    Segment sg;
+    sg.g = s_group[0], sg.length = s_group[1], sg.row0 = s_group[2], sg.rows = s_group[3], sg.page_row = s_group[4];
+    const int operands = a.q_terms * (item / ROWS), R = F::ring(operands);
+    uint8_t *const raw = sm + operands * F::Q_BYTES;
+    uint8_t *const ring = raw + F::RAW_ALL;
+    const uint32_t ring32 = smem_u32(ring);
     const int shift = 31 - __clz(a.pool.page_tokens);
     Slot load = {0, 0}, keys = {0, 0}, values = {0, 0};    // of the loaders; of the products
     int s_phase = 0, s_phase1 = 0, p_phase = 0, p_phase1 = 0, pv_phase = 0, o_phase = 0;
     bool dead = false;
-    for (int unit = min(int(blockIdx.x) * size, total); unit < unit1;) {
-        Segment sg;
+    for (int unit = unit0;;) {
+        sg.blocks = (sg.rows * p.G + item - 1) / item, sg.tiles = (sg.length + TOK - 1) / TOK;
         {
-            int lo = 0, hi = a.groups;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (cum[mid] <= unit) lo = mid; else hi = mid;
-            }
-            bool bad;
-            sg.g = lo;
-            sg.length = group_prefix(a, lo, bad), sg.row0 = a.first[lo], sg.rows = a.first[lo + 1] - sg.row0;
-            sg.tiles = (sg.length + TOK - 1) / TOK;
-            const int item = (unit - cum[lo]) / sg.tiles, blocks = (sg.rows * p.G + ITEM - 1) / ITEM;
-            sg.tile0 = unit - cum[lo] - item * sg.tiles;
-            sg.h = item / blocks, sg.mb = item - sg.h * blocks;
-            sg.tile1 = min(sg.tiles, sg.tile0 + unit1 - unit);
-            sg.page_row = row_seq(a, sg.row0);
+            const int at = unit - cum[sg.g], i = at / sg.tiles;
+            sg.tile0 = at - i * sg.tiles, sg.h = i / sg.blocks, sg.mb = i - sg.h * sg.blocks;
+            sg.nt = min(sg.tiles - sg.tile0, unit1 - unit);
         }
-        const int live = min(ITEM, sg.rows * p.G - sg.mb * ITEM);   // queries there are
+        const int live = min(item, sg.rows * p.G - sg.mb * item);   // queries there are
         const bool dual = live > ROWS;                     // two blocks of queries, each with its softmax group; else one, whose
                                                            // tiles the groups take in turn (where there are two accumulators)
-        const int nt = sg.tile1 - sg.tile0, jobs = dual ? 2 * nt : nt;
-
-        // -- queries, rotated, scaled and split: a warp a query ---------------------------------------------------
-        for (int r = tid; r < ITEM; r += THREADS) {
-            int len = 0;
-            if (r < live) len = row_len(a, row_seq(a, sg.row0 + (sg.mb * ITEM + r) / p.G));
-            x_len[r] = len, x_lim[r] = r < live ? min(len, sg.length) : sg.length;    // rows past the last as if they saw all
-        }
-        __syncthreads();
-        if (warp < MMA_WARP) {
-            constexpr int NP = D / 64, U = D == 256 ? 2 : 4;
-            const int top = dual ? ITEM : ROWS;
-            for (int r0 = warp; r0 < top; r0 += MMA_WARP * U) {
-                Elems<NP> raw[U][2];
-                float2 turn[U][NP];                        // cos, sin
+        const int nt = sg.nt, jobs = dual ? 2 * nt : nt;
+        int lim = sg.length;                               // tokens that this thread's query sees (softmax groups)
+        float f = 0.0f, m = -INFINITY, l = 0.0f;           // its scale, running maximum and sum
+        if (warp < 2 * SOFT || warp == MMA_WARP) {
+            // -- queries, rotated, scaled and split: eight lanes a query
+            constexpr int N = D / 16;                      // a lane's elements i and as many i + D / 2
+            const int sub = lane & 7, top = dual ? 2 * ROWS : ROWS;
+            if (warp < 2 * SOFT) {
+#pragma unroll 1
+                for (int r = warp * 4 + (lane >> 3); r < top; r += 2 * SOFT * 4) {
+                    float x[2][N];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int r = r0 + u * MMA_WARP;
+                    for (int e = 0; e < N; ++e) x[0][e] = x[1][e] = 0.0f;
+                    if (r < live) {
+                        const int rr = sg.mb * item + r, b = rr / p.G, head = sg.h * p.G + rr - b * p.G;
+                        const int64_t at = int64_t(sg.row0 + b) * a.ldq + int64_t(head) * D + sub * N;
+                        load_q<N>(a.q, a.qdt, at, x[0]);
+                        load_q<N>(a.q, a.qdt, at + D / 2, x[1]);
+                        if (a.rope) {
+                            const int pos = row_len(a, row_seq(a, sg.row0 + b)) - 1;
+                            if (pos >= a.rope_rows) {
+                                if (sub == 0) atomicOr(&g_fault_shared, FAULT_PAGE);
+                            } else if (pos >= 0) {
+                                const float *t = a.rope + int64_t(pos) * D + sub * N;
 #pragma unroll
-                    for (int e = 0; e < NP; ++e) raw[u][0].w[e] = raw[u][1].w[e] = 0u, turn[u][e] = make_float2(1.0f, 0.0f);
-                    if (r >= live) continue;
-                    const int rr = sg.mb * ITEM + r, b = rr / p.G, head = sg.h * p.G + rr - b * p.G, len = x_len[r];
-                    const int64_t at = int64_t(sg.row0 + b) * a.ldq + int64_t(head) * D + lane * NP;
-                    load_elems<NP>(a.q, a.qdt, at, raw[u][0]);
-                    load_elems<NP>(a.q, a.qdt, at + D / 2, raw[u][1]);
-                    if (a.rope && len > 0) {
-                        if (len - 1 < a.rope_rows) {
-                            const float *t = a.rope + int64_t(len - 1) * D + lane * NP;
+                                for (int e = 0; e < N; e += 4) {
+                                    const float4 c4 = *reinterpret_cast<const float4 *>(t + e);
+                                    const float4 s4 = *reinterpret_cast<const float4 *>(t + D / 2 + e);
+                                    const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-                            for (int e = 0; e < NP; ++e) turn[u][e] = make_float2(t[e], t[D / 2 + e]);
-                        } else if (lane == 0) {
-                            atomicOr(&g_fault_shared, FAULT_PAGE);
+                                    for (int k = 0; k < 4; ++k) {
+                                        const float i = x[0][e + k], j = x[1][e + k];
+                                        x[0][e + k] = __fsub_rn(__fmul_rn(i, c[k]), __fmul_rn(j, s[k]));
+                                        x[1][e + k] = __fadd_rn(__fmul_rn(j, c[k]), __fmul_rn(i, s[k]));
+                                    }
+                                }
+                            }
                         }
                     }
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int r = r0 + u * MMA_WARP;
-                    if (r >= top) break;
-                    float x[2][NP];
-                    widen<NP>(raw[u][0], a.qdt, x[0]);
-                    widen<NP>(raw[u][1], a.qdt, x[1]);
                     float big = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < NP; ++e) {
-                        const float i = x[0][e], j = x[1][e], c = turn[u][e].x, s = turn[u][e].y;
-                        if (a.rope) {
-                            x[0][e] = __fsub_rn(__fmul_rn(i, c), __fmul_rn(j, s));
-                            x[1][e] = __fadd_rn(__fmul_rn(j, c), __fmul_rn(i, s));
-                        }
-                        big = fmaxf(big, fmaxf(fabsf(x[0][e]), fabsf(x[1][e])));
-                    }
+                    for (int e = 0; e < N; ++e) big = fmaxf(big, fmaxf(fabsf(x[0][e]), fabsf(x[1][e])));
 #pragma unroll
-                    for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                    for (int o = 4; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
                     // a power of two that brings the maximum to [2^13, 2^14), within fp32's normal range; 1 for zero, inf and NaN,
                     // and for bfloat16 terms. The scale's sign goes with it, so that the largest score is the largest sum.
                     const int ex = __float_as_int(big) >> 23;
                     const int up = BF || big == 0.0f || ex == 255 ? 127 : min(254, 267 - ex);
-                    const float f = __int_as_float((up << 23) | (__float_as_int(a.scale) & 0x80000000));
+                    const float g = __int_as_float((up << 23) | (__float_as_int(a.scale) & 0x80000000));
                     const float back = __int_as_float(max(254 - up, 1) << 23);
-                    float factor = fabsf(a.scale) * 1.4426950408889634f * back * (up == 254 ? 0.5f : 1.0f);
-                    if (factor == 0.0f) factor = 0x1p-126f;
-                    if (lane == 0) x_scale[r] = factor;
+                    const float factor = fabsf(a.scale) * 1.4426950408889634f * back * (up == 254 ? 0.5f : 1.0f);
+                    if (sub == 0) x_scale[r] = factor == 0.0f ? 0x1p-126f : factor;
+                    const int block = r / ROWS, row = r % ROWS;
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        uint32_t h[(NP + 1) / 2], l[(NP + 1) / 2];
+                    for (int s = 0; s < 2; ++s)
 #pragma unroll
-                        for (int e = 0; e < NP; e += 2) {
-                            const float y = x[s][e] * f, z = NP > 1 ? x[s][NP > 1 ? e + 1 : e] * f : 0.0f;
-                            h[e / 2] = pack2<BF>(y, z);
-                            l[e / 2] = rest2<BF>(y, z, h[e / 2]);
+                        for (int e = 0; e < N; e += 4) {
+                            const int d = s * (D / 2) + sub * N + e;
+                            uint8_t *to = sm + block * F::Q_BYTES + (d / 64) * F::QB + sw128_off(row, (d % 64) / 8) + (d % 8) * 2;
+                            const float y[4] = {x[s][e] * g, x[s][e + 1] * g, x[s][e + 2] * g, x[s][e + 3] * g};
+                            const uint2 h = make_uint2(pack2<BF>(y[0], y[1]), pack2<BF>(y[2], y[3]));
+                            *reinterpret_cast<uint2 *>(to) = h;
+                            if (a.q_terms == 2)            // one block of queries then
+                                *reinterpret_cast<uint2 *>(to + F::Q_BYTES) =
+                                    make_uint2(rest2<BF>(y[0], y[1], h.x), rest2<BF>(y[2], y[3], h.y));
                         }
-                        const int d = s * (D / 2) + lane * NP;
-                        uint8_t *to = sm + (r / ROWS) * F::Q_BYTES + (d / 64) * F::QB + sw128_off(r % ROWS, (d % 64) / 8) + (d % 8) * 2;
-                        put<NP>(to, h);
-                        if (a.q_terms == 2) put<NP>(to + F::QUERIES, l);
-                    }
                 }
+                fence_proxy_async_smem();
             }
-            fence_proxy_async_smem();
+            named_bar_sync(1, (2 * SOFT + 1) * 32);
+            if (warp < 2 * SOFT) {
+                const int r = dual ? tid : tid % ROWS;
+                f = x_scale[r];
+                if (r < live) lim = min(lim, row_len(a, row_seq(a, sg.row0 + (sg.mb * item + r) / p.G)));
+            }
         }
-        __syncthreads();
-        const int my_row = tid % ROWS + (dual && tid >= ROWS ? ROWS : 0);      // of the softmax groups
-        int lim = 0;
-        float f = 0.0f;
-        if (warp < 2 * SOFT) lim = x_lim[my_row], f = x_scale[my_row];
-        __syncthreads();                                   // the ring is free
-
-        float m = -INFINITY, l = 0.0f;                     // of this thread's query
         if (warp == MMA_WARP) {
             // ------------------------------------ products ------------------------------------
             if (lane == 0) {
@@ -462,7 +428,7 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
                             umma_f16(tmem + F::S_COL + (j & 1) * F::S_STEP,
-                                     sw128_kmajor_desc(base + term * F::QUERIES + mb * F::Q_BYTES + (k / 4) * F::QB + (k % 4) * 32),
+                                     sw128_kmajor_desc(base + (term + mb) * F::Q_BYTES + (k / 4) * F::QB + (k % 4) * 32),
                                      sw128_kmajor_desc(kt + (k / 4) * F::KB + (k % 4) * 32), kIdesc<BF, TOK, false>, term || k);
                     umma_commit(&s_full[j & 1]);
                     if (!dual || mb == 1) {
@@ -484,8 +450,8 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     if (dead) break;
                     tc_fence_after();
                     const uint32_t vt = ring32 + values.at * F::TILE_BYTES;
-                    const uint32_t o = tmem + F::O_COL + (DUAL ? (j & 1) * F::O_STEP : 0);
-                    const bool more = DUAL ? j > 1 : j > 0;    // the accumulators hold something
+                    const uint32_t o = tmem + F::O_COL + (TWO ? (j & 1) * F::O_STEP : 0);
+                    const bool more = TWO ? j > 1 : j > 0; // the accumulators hold something
                     for (int term = 0; term < a.p_terms; ++term)
 #pragma unroll
                         for (int k = 0; k < TOK / 16; ++k)
@@ -496,12 +462,12 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                         // the last values come right behind their predecessor where tiles are taken in turn
                         values.forward(!dual && t == nt - 2 ? 1 : 2, R);
                     }
-                    if (!DUAL) umma_commit(pv_done);
+                    if (!TWO) umma_commit(pv_done);
                     if (j + 2 < jobs) scores(j + 2);
                 }
                 umma_commit(o_done);
                 keys = begin;                              // to the next segment's first place
-                for (int n = 0; n < 2 * nt; n += 2) keys.forward(2, R);
+                keys.phase ^= 2 * nt / R & 1, keys.forward(2 * nt % R, R);
                 if (dead) *s_dead = 1;
             }
             __syncwarp();
@@ -512,101 +478,114 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
             // a segment's tiles in the order of the products: keys of the next tile before values of this one where tiles are
             // taken in turn, keys and values of a tile else
             const int steps = 2 * nt;
-            auto place = [&](int n, int &tile) -> bool {   // whether the n-th are values
-                if (dual) {
-                    tile = n >> 1;
-                    return n & 1;
+            auto place = [&](int n, int &t0) -> bool {     // whether the n-th are values; the tile's first token
+                int tile;
+                bool v;
+                if (dual) tile = n >> 1, v = n & 1;
+                else if (n == 0 || n == steps - 1) tile = n == 0 ? 0 : nt - 1, v = n != 0;
+                else tile = n & 1 ? (n + 1) >> 1 : (n >> 1) - 1, v = !(n & 1);
+                t0 = (sg.tile0 + tile) * TOK;
+                return v;
+            };
+            // a thread's rows: STEP apart, C bytes of each
+            constexpr int CPR = I8 ? D / 16 : D / 8, NC = TOK * CPR / LOAD_THREADS, STEP = LOAD_THREADS / CPR;
+            const int row = t / CPR, c = t % CPR;
+            // pages of its rows of the n-th tile, -1 where there is none
+            auto pages = [&](int n, int (&pg)[NC]) {
+                int t0;
+                const bool v = place(n, t0);
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    const int at = t0 + row + i * STEP;
+                    pg[i] = n < steps && at < sg.length ? table[at >> shift] : -1;
                 }
-                if (n == 0 || (n == steps - 1)) {
-                    tile = n == 0 ? 0 : nt - 1;
-                    return n != 0;
-                }
-                tile = n & 1 ? (n + 1) >> 1 : (n >> 1) - 1;
-                return !(n & 1);
+                if (c == 0 && !v && n < steps)
+#pragma unroll
+                    for (int i = 0; i < NC; ++i)
+                        if (t0 + row + i * STEP < sg.length && unsigned(pg[i]) >= unsigned(a.pool.pages)) atomicOr(&g_fault_shared, FAULT_PAGE);
             };
-            // page of a tile's row, -1 where there is none
-            auto page_of = [&](int tile, int r, bool report) -> int {
-                const int at = (sg.tile0 + tile) * TOK + r;
-                if (at >= sg.length) return -1;
-                const int page = table[at >> shift];
-                if (unsigned(page) < unsigned(a.pool.pages)) return page;
-                if (report) atomicOr(&g_fault_shared, FAULT_PAGE);
-                return -1;
-            };
-            auto slot_of = [&](int tile, int r) -> unsigned {
-                return unsigned(sg.h * a.pool.page_tokens) + (unsigned((sg.tile0 + tile) * TOK + r) & (a.pool.page_tokens - 1));
-            };
+            const unsigned slots = sg.h * a.pool.page_tokens, within = a.pool.page_tokens - 1;
             auto wait_empty = [&] { dead = dead || !mbar_wait_bounded(&empty[load.at], load.phase ^ 1); };
             if constexpr (I8) {
-                // 16 codes a thread and row: loaded a place of the ring ahead, their pages two
-                constexpr int CPR = D / 16, NC = TOK * CPR / LOAD_THREADS, STEP = LOAD_THREADS / CPR;
-                const int row = t / CPR, c = t % CPR;
-                struct Raw {
-                    uint4 code[NC];
-                    uint32_t scale[NC];
-                };
-                auto pages = [&](int n, int (&pg)[NC]) {
-                    int tile;
-                    const bool v = place(min(n, steps - 1), tile);
+                // Codes come asynchronously into places of this thread's own, RAWS tiles ahead; their scales (whose lines are asked
+                // into L2 with the codes) come into registers a tile ahead.
+                uint32_t *const codes = reinterpret_cast<uint32_t *>(raw) + t * 4;
+                const uint32_t codes32 = smem_u32(codes);
+                auto fetch = [&](int n, const int (&pg)[NC]) {
+                    if (n < steps) {
+                        int t0;
+                        const bool v = place(n, t0);
+                        const int8_t *from = static_cast<const int8_t *>(v ? a.pool.v : a.pool.k) + a.layer * a.pool.layer_stride + c * 16;
+                        const uint16_t *scales = (v ? a.pool.v_scales : a.pool.k_scales) + a.layer * a.pool.scale_layer_stride;
 #pragma unroll
-                    for (int i = 0; i < NC; ++i) pg[i] = n < steps ? page_of(tile, row + i * STEP, c == 0 && !v) : -1;
+                        for (int i = 0; i < NC; ++i) {
+                            const bool there = unsigned(pg[i]) < unsigned(a.pool.pages);
+                            const unsigned s = slots + (unsigned(t0 + row + i * STEP) & within);
+                            const int64_t page = there ? pg[i] : 0;
+                            cp16(codes32 + (n % F::RAWS) * F::RAW_BYTES + i * (LOAD_THREADS * 16), from + page * a.pool.page_stride + s * unsigned(D), there);
+                            if (there && c == 0)
+                                asm volatile("prefetch.global.L2 [%0];" ::"l"(scales + page * a.pool.scale_page_stride + s * unsigned(D / 32)));
+                        }
+                    }
+                    cp_commit();
                 };
-                auto fetch = [&](int n, const int (&pg)[NC], Raw &raw) {
-                    int tile;
-                    const bool v = place(min(n, steps - 1), tile);
-                    const int8_t *codes = static_cast<const int8_t *>(v ? a.pool.v : a.pool.k) + a.layer * a.pool.layer_stride + c * 16;
+                auto fetch_scales = [&](int n, uint32_t (&sc)[NC]) {
+                    if (n >= steps) return;
+                    int t0;
+                    const bool v = place(n, t0);
                     const uint16_t *scales = (v ? a.pool.v_scales : a.pool.k_scales) + a.layer * a.pool.scale_layer_stride + c / 2;
 #pragma unroll
                     for (int i = 0; i < NC; ++i) {
-                        raw.code[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-                        raw.scale[i] = 0;                  // a row without a page: zeros
-                        if (pg[i] < 0) continue;
-                        const unsigned s = slot_of(tile, row + i * STEP);
-                        raw.code[i] = *reinterpret_cast<const uint4 *>(codes + pg[i] * a.pool.page_stride + s * unsigned(D));
-                        raw.scale[i] = scales[pg[i] * a.pool.scale_page_stride + s * unsigned(D / 32)];
+                        const int at = t0 + row + i * STEP;
+                        const int pg = at < sg.length ? table[at >> shift] : -1;
+                        sc[i] = 0;                         // a row without a page: zeros
+                        if (unsigned(pg) < unsigned(a.pool.pages))
+                            sc[i] = scales[pg * a.pool.scale_page_stride + (slots + (unsigned(at) & within)) * unsigned(D / 32)];
                     }
                 };
-                auto convert = [&](const Raw &raw) {
-                    wait_empty();
-                    if (!dead) {
-                        uint8_t *to = ring + load.at * F::TILE_BYTES + (c / 4) * F::KB;
-#pragma unroll
-                        for (int i = 0; i < NC; ++i) {
-                            const uint32_t s = raw.scale[i] | raw.scale[i] << 16;
-                            const uint32_t w[4] = {raw.code[i].x ^ 0x80808080u, raw.code[i].y ^ 0x80808080u,
-                                                   raw.code[i].z ^ 0x80808080u, raw.code[i].w ^ 0x80808080u};
-                            uint4 lo = make_uint4(dequant2(w[0], 0x4140u, s), dequant2(w[0], 0x4342u, s),
-                                                  dequant2(w[1], 0x4140u, s), dequant2(w[1], 0x4342u, s));
-                            uint4 hi = make_uint4(dequant2(w[2], 0x4140u, s), dequant2(w[2], 0x4342u, s),
-                                                  dequant2(w[3], 0x4140u, s), dequant2(w[3], 0x4342u, s));
-                            const int r = row + i * STEP, flip = c / 4 & 1;    // odd columns the other half first: other banks
-                            *reinterpret_cast<uint4 *>(to + sw128_off(r, (c % 4) * 2 + flip)) = flip ? hi : lo;
-                            *reinterpret_cast<uint4 *>(to + sw128_off(r, (c % 4) * 2 + 1 - flip)) = flip ? lo : hi;
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&full[load.at]);
-                    }
-                    load.forward(1, R);
-                };
-                Raw x, y;
                 int pg[NC];
+                uint32_t sc[NC], next[NC];
                 pages(0, pg);
-                fetch(0, pg, x);
-                pages(1, pg);
 #pragma unroll 1
-                for (int n = 0; n < steps; n += 2) {       // an even number of places
-                    fetch(n + 1, pg, y);
-                    pages(n + 2, pg);
-                    convert(x);
-                    fetch(n + 2, pg, x);
-                    pages(n + 3, pg);
-                    convert(y);
+                for (int n = 0; n < F::RAWS; ++n) {
+                    fetch(n, pg);
+                    pages(n + 1, pg);
                 }
+                fetch_scales(0, next);
+#pragma unroll 1
+                for (int n = 0; n < steps; ++n) {
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) sc[i] = next[i] | next[i] << 16;
+                    fetch_scales(n + 1, next);
+                    cp_wait<F::RAWS - 1>();
+                    uint4 code[NC];
+#pragma unroll
+                    for (int i = 0; i < NC; ++i)
+                        code[i] = *reinterpret_cast<const uint4 *>(codes + ((n % F::RAWS) * F::RAW_BYTES + i * (LOAD_THREADS * 16)) / 4);
+                    wait_empty();
+                    if (dead) break;
+                    uint8_t *to = ring + load.at * F::TILE_BYTES + (c / 4) * F::KB;
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) {
+                        const uint32_t w[4] = {code[i].x ^ 0x80808080u, code[i].y ^ 0x80808080u, code[i].z ^ 0x80808080u, code[i].w ^ 0x80808080u};
+                        const uint4 lo = make_uint4(dequant2(w[0], 0x4140u, sc[i]), dequant2(w[0], 0x4342u, sc[i]),
+                                                    dequant2(w[1], 0x4140u, sc[i]), dequant2(w[1], 0x4342u, sc[i]));
+                        const uint4 hi = make_uint4(dequant2(w[2], 0x4140u, sc[i]), dequant2(w[2], 0x4342u, sc[i]),
+                                                    dequant2(w[3], 0x4140u, sc[i]), dequant2(w[3], 0x4342u, sc[i]));
+                        const int r = row + i * STEP, flip = c / 4 & 1;        // odd columns the other half first: other banks
+                        *reinterpret_cast<uint4 *>(to + sw128_off(r, (c % 4) * 2 + flip)) = flip ? hi : lo;
+                        *reinterpret_cast<uint4 *>(to + sw128_off(r, (c % 4) * 2 + 1 - flip)) = flip ? lo : hi;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[load.at]);
+                    load.forward(1, R);
+                    fetch(n + F::RAWS, pg);
+                    pages(n + F::RAWS + 1, pg);
+                }
+                cp_wait<0>();
             } else {
                 // 16 bytes a thread and row, asynchronously; a place is handed over when `lag` more are under way
-                constexpr int CPR = D / 8, NC = TOK * CPR / LOAD_THREADS, STEP = LOAD_THREADS / CPR;
-                const int row = t / CPR, c = t % CPR;
                 const int lag = min(R - 2, 3);
                 Slot done = load;
                 auto hand_over = [&] {
@@ -615,22 +594,25 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     if (lane == 0) mbar_arrive(&full[done.at]);
                     done.forward(1, R);
                 };
-                for (int n = 0; n < steps && !dead; ++n) {
-                    int tile;
-                    const bool v = place(n, tile);
-                    const uint16_t *src = static_cast<const uint16_t *>(v ? a.pool.v : a.pool.k) + a.layer * a.pool.layer_stride + c * 8;
-                    int pg[NC];
-#pragma unroll
-                    for (int i = 0; i < NC; ++i) pg[i] = page_of(tile, row + i * STEP, c == 0 && !v);
+                int pg[NC];
+                pages(0, pg);
+#pragma unroll 1
+                for (int n = 0; n < steps; ++n) {
+                    int t0;
+                    const bool v = place(n, t0);
+                    const uint16_t *from = static_cast<const uint16_t *>(v ? a.pool.v : a.pool.k) + a.layer * a.pool.layer_stride + c * 8;
                     wait_empty();
                     if (dead) break;
                     const uint32_t to = ring32 + load.at * F::TILE_BYTES + (c / 8) * F::KB;
 #pragma unroll
                     for (int i = 0; i < NC; ++i) {
                         const int r = row + i * STEP;
-                        cp16(to + sw128_off(r, c % 8), src + max(pg[i], 0) * a.pool.page_stride + slot_of(tile, r) * unsigned(D), pg[i] >= 0);
+                        const bool there = unsigned(pg[i]) < unsigned(a.pool.pages);
+                        cp16(to + sw128_off(r, c % 8), from + int64_t(there ? pg[i] : 0) * a.pool.page_stride +
+                                                           (slots + (unsigned(t0 + r) & within)) * unsigned(D), there);
                     }
                     cp_commit();
+                    pages(n + 1, pg);
                     load.forward(1, R);
                     if (n >= lag) {
                         if (lag == 1) cp_wait<1>();
@@ -643,44 +625,52 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                 if (!dead)
                     for (int n = max(0, steps - lag); n < steps; ++n) hand_over();
             }
-            if (dead) *s_dead = 1;
         } else {
             // ------------------------------------- softmax -------------------------------------
             const int wg = warp / SOFT;
             const uint32_t lanes = tmem + (uint32_t(32 * (warp % SOFT)) << 16);
-            const uint32_t o = lanes + F::O_COL + (DUAL ? wg * F::O_STEP : 0);
+            const uint32_t o = lanes + F::O_COL + (TWO ? wg * F::O_STEP : 0);
             bool any = false;                              // the accumulators hold something
             const bool idle = (dual ? wg * ROWS : 0) + 32 * (warp % SOFT) >= live;     // no queries in this warp's lanes
-            for (int j = DUAL ? wg : wg * jobs; j < jobs; j += DUAL ? 2 : 1) {
-                const int t0 = (sg.tile0 + (dual ? j >> 1 : j)) * TOK, left = lim - t0;
+            for (int j = TWO ? wg : wg * jobs; j < jobs; j += TWO ? 2 : 1) {
+                const int left = lim - (sg.tile0 + (dual ? j >> 1 : j)) * TOK;
                 const uint32_t sc = lanes + F::S_COL + (j & 1) * F::S_STEP;
                 // (a group that has its own score buffer keeps its phase in s_phase)
-                const int phase = DUAL || !(j & 1) ? s_phase : s_phase1;
+                const int phase = TWO || !(j & 1) ? s_phase : s_phase1;
                 const bool seen = !dead && mbar_wait_bounded(&s_full[j & 1], phase);
-                if (DUAL || !(j & 1)) s_phase ^= 1; else s_phase1 ^= 1;
+                if (TWO || !(j & 1)) s_phase ^= 1; else s_phase1 ^= 1;
                 if (!__all_sync(0xffffffffu, seen)) {
                     dead = true;
                     break;
                 }
                 tc_fence_after();
+                if (!TWO) pv_phase ^= 1;
                 if (idle) {
-                    if (!DUAL) pv_phase ^= 1;
                     if (lane == 0) mbar_arrive(&p_full[j & 1]);
                     continue;
                 }
                 const bool all = __all_sync(0xffffffffu, left >= TOK);
                 float top = -INFINITY;
 #pragma unroll 1
-                for (int c = 0; c < TOK; c += 32) {
-                    uint32_t x[32];
+                for (int c = 0; c < TOK; c += 64) {
+                    uint32_t x[32], y[32];
                     tmem_ld32(sc + c, x);
+                    tmem_ld32(sc + c + 32, y);
                     tmem_ld_wait();
                     if (all) {
+                        float t1 = -INFINITY;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(top, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+                        for (int i = 0; i < 32; ++i) {
+                            top = fmaxf(top, __uint_as_float(x[i]));
+                            t1 = fmaxf(t1, __uint_as_float(y[i]));
+                        }
+                        top = fmaxf(top, t1);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) top = c + i < left ? fmaxf(top, __uint_as_float(x[i])) : top;
+                        for (int i = 0; i < 32; ++i) {
+                            top = c + i < left ? fmaxf(top, __uint_as_float(x[i])) : top;
+                            top = c + 32 + i < left ? fmaxf(top, __uint_as_float(y[i])) : top;
+                        }
                     }
                 }
                 // the maximum lags; where it has to follow, what has been added up follows too
@@ -690,8 +680,8 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     m = move ? top : m;
                     if (any) {
                         l *= shrink;
-                        if (!DUAL) {                       // the previous tile's product may still be adding
-                            const bool there = mbar_wait_bounded(pv_done, pv_phase ^ 1);
+                        if (!TWO) {                        // the previous tile's product may still be adding
+                            const bool there = mbar_wait_bounded(pv_done, pv_phase);
                             if (!__all_sync(0xffffffffu, there)) {
                                 dead = true;
                                 break;
@@ -710,14 +700,11 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     }
                 }
                 any = true;
-                if (!DUAL) pv_phase ^= 1;
                 const float from = m == -INFINITY ? 0.0f : m;
-                float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll 1
-                for (int c = 0; c < TOK; c += 32) {
-                    uint32_t x[32], h[16], g[16];
-                    tmem_ld32(sc + c, x);
-                    tmem_ld_wait();
+                float2 sum = make_float2(0.0f, 0.0f), sum1 = sum;
+                auto weigh = [&](int c, const uint32_t (&x)[32], auto second) {
+                    constexpr bool SECOND = decltype(second)::value;
+                    uint32_t h[16], g[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float2 e = fma2(sub2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), from), f, F::BIAS);
@@ -726,20 +713,40 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                             e.x = c + 2 * i < left ? e.x : 0.0f;
                             e.y = c + 2 * i + 1 < left ? e.y : 0.0f;
                         }
-                        sum = add2(sum, e);
+                        if (i & 1) sum1 = add2(sum1, e); else sum = add2(sum, e);
                         h[i] = pack2<BF>(e.x, e.y);
-                        if (BF || a.p_terms == 2) g[i] = rest2<BF>(e.x, e.y, h[i]);
+                        if (SECOND) g[i] = rest2<BF>(e.x, e.y, h[i]);
                     }
                     tmem_st16(sc + c, h);
-                    if (BF || a.p_terms == 2) tmem_st16(sc + c + 16, g);
+                    if (SECOND) tmem_st16(sc + c + 16, g);
+                };
+                if (BF || a.p_terms == 2) {
+#pragma unroll 1
+                    for (int c = 0; c < TOK; c += 32) {
+                        uint32_t x[32];
+                        tmem_ld32(sc + c, x);
+                        tmem_ld_wait();
+                        weigh(c, x, Bool<true>());
+                    }
+                } else {                                   // a chunk's loads under the one before
+                    uint32_t x[32], y[32];
+                    tmem_ld32(sc, x);
+#pragma unroll 1
+                    for (int c = 0; c < TOK; c += 64) {
+                        tmem_ld_wait();
+                        tmem_ld32(sc + c + 32, y);
+                        weigh(c, x, Bool<false>());
+                        tmem_ld_wait();
+                        if (c + 64 < TOK) tmem_ld32(sc + c + 64, x);
+                        weigh(c + 32, y, Bool<false>());
+                    }
                 }
-                l += sum.x + sum.y;
+                l += sum.x + sum.y + (sum1.x + sum1.y);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[j & 1]);
             }
-            // ---- the segment's results
             if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_bounded(o_done, o_phase));
             tc_fence_after();
         }
@@ -747,62 +754,73 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
         if (dead) *s_dead = 1;
         __syncthreads();
         if (*s_dead) break;
+
+        // -- the segment's results: rows of shared memory, then as whole rows to the workspace ----------------------
+        float *const rows_out = reinterpret_cast<float *>(sm);
+        const bool whole = sg.tile0 == 0 && nt == sg.tiles;
         if (warp < 2 * SOFT) {
-            const int wg = warp / SOFT, row = tid % ROWS;
-            const uint32_t o = tmem + (uint32_t(32 * (warp % SOFT)) << 16) + F::O_COL;
-            // one block of queries in two accumulators: each group hands half of its columns to the other through the ring
-            const bool merge = DUAL && !dual && jobs > 1;
-            float *const swap = reinterpret_cast<float *>(ring);               // [D][ROWS]
-            float mine = 1.0f, other = 0.0f;
+            const int wg = warp / SOFT, row = tid % ROWS, r = dual ? tid : row;
+            const uint32_t o = tmem + (uint32_t(32 * (warp % SOFT)) << 16) + F::O_COL + (TWO ? wg * F::O_STEP : 0);
+            // one block of queries in two accumulators: each group puts down half of the columns, then adds the other half
+            const bool merge = TWO && !dual && jobs > 1;
+            float mine = 1.0f;
             if (merge) {
-                // maxima and sums first, then accumulators
-                float2 *ml = reinterpret_cast<float2 *>(ring);
+                float2 *ml = reinterpret_cast<float2 *>(sm);
                 ml[wg * ROWS + row] = make_float2(m, l);
-                named_bar_sync(1, 2 * SOFT * 32);
+                named_bar_sync(2, 2 * SOFT * 32);
                 const float2 him = ml[(wg ^ 1) * ROWS + row];
                 const float both = fmaxf(m, him.x), at = both == -INFINITY ? 0.0f : both;
-                mine = m == -INFINITY ? 0.0f : ex2((m - at) * f), other = him.x == -INFINITY ? 0.0f : ex2((him.x - at) * f);
-                m = both, l = l * mine + him.y * other;
-                named_bar_sync(1, 2 * SOFT * 32);
-                const int theirs = wg ? 0 : D / 2;
-                for (int c = 0; c < D / 2; c += 32) {
-                    uint32_t x[32];
-                    tmem_ld32(o + (wg ? F::O_STEP : 0) + theirs + c, x);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) swap[(theirs + c + i) * ROWS + row] = __uint_as_float(x[i]);
-                }
-                named_bar_sync(1, 2 * SOFT * 32);
+                mine = m == -INFINITY ? 0.0f : ex2((m - at) * f);
+                l = l * mine + (him.x == -INFINITY ? 0.0f : him.y * ex2((him.x - at) * f));
+                m = both;
+                named_bar_sync(2, 2 * SOFT * 32);
             }
-            const bool whole = sg.tile0 == 0 && sg.tile1 == sg.tiles;
-            const int r = dual ? my_row : row;
-            const int rr = sg.mb * ITEM + r, b = rr / p.G, head = sg.h * p.G + rr - b * p.G;
-            const int64_t at = whole ? int64_t(sg.row0 + b) * a.q_heads + head : (int64_t(blockIdx.x) * 2 + (sg.tile0 == 0)) * ITEM + r;
-            float *out = (whole ? p.w.direct : p.w.piece) + at * D;
-            // columns that this thread writes: all of its own accumulators, or its half of both; the first group's alone else
-            const bool writes = dual || merge || wg == 0;
-            const int c0 = merge && wg ? D / 2 : 0, c1 = merge && !wg ? D / 2 : D;
-            if (writes)
-                for (int c = c0; c < c1; c += 32) {
-                    uint32_t x[32];
-                    tmem_ld32(o + (wg && DUAL ? F::O_STEP : 0) + c, x);
-                    tmem_ld_wait();
-                    if (merge)
+            if (dual || merge || wg == 0)
+                for (int half = 0; half < (merge ? 2 : 1); ++half) {
+                    const int c0 = merge ? (wg ^ half) * (D / 2) : 0, c1 = merge ? c0 + D / 2 : D;
+#pragma unroll 1
+                    for (int c = c0; c < c1; c += 32) {
+                        uint32_t x[32];
+                        tmem_ld32(o + c, x);
+                        tmem_ld_wait();
+                        float4 *to = reinterpret_cast<float4 *>(rows_out + r * PS + c);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            x[i] = __float_as_uint(fmaf(swap[(c + i) * ROWS + row], other, __uint_as_float(x[i]) * mine));
-                    if (r < live)
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<uint4 *>(out + c + i) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                        for (int i = 0; i < 8; ++i) {
+                            float4 v = make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]), __uint_as_float(x[4 * i + 2]),
+                                                   __uint_as_float(x[4 * i + 3]));
+                            if (merge) {
+                                const float4 w = half ? to[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                v = make_float4(fmaf(v.x, mine, w.x), fmaf(v.y, mine, w.y), fmaf(v.z, mine, w.z), fmaf(v.w, mine, w.w));
+                            }
+                            to[i] = v;
+                        }
+                    }
+                    if (merge && half == 0) named_bar_sync(2, 2 * SOFT * 32);
                 }
             // the maximum as a power of two, the probabilities' height taken off
-            if (r < live && (dual || wg == 0))
+            if (r < live && (dual || wg == 0)) {
+                const int rr = sg.mb * item + r, b = rr / p.G, head = sg.h * p.G + rr - b * p.G;
+                const int64_t at = whole ? int64_t(sg.row0 + b) * a.q_heads + head : (int64_t(blockIdx.x) * 2 + (sg.tile0 == 0)) * (2 * ROWS) + r;
                 (whole ? p.w.direct_ml : p.w.piece_ml)[at] = make_float2(m == -INFINITY ? -INFINITY : m * f - F::BIAS, l);
+            }
             tc_fence_before();
         }
         __syncthreads();
+#pragma unroll 1
+        for (int i = tid; i < live * (D / 4); i += THREADS) {
+            const int r = i / (D / 4), c = i % (D / 4) * 4, rr = sg.mb * item + r, b = rr / p.G, head = sg.h * p.G + rr - b * p.G;
+            const int64_t at = whole ? int64_t(sg.row0 + b) * a.q_heads + head : (int64_t(blockIdx.x) * 2 + (sg.tile0 == 0)) * (2 * ROWS) + r;
+            *reinterpret_cast<float4 *>((whole ? p.w.direct : p.w.piece) + at * D + c) = *reinterpret_cast<const float4 *>(rows_out + r * PS + c);
+        }
         unit += nt;
+        if (unit >= unit1) break;
+        if (unit == cum[sg.g + 1]) {                       // the next group that has units
+            do ++sg.g; while (cum[sg.g + 1] == unit);
+            sg.row0 = a.first[sg.g], sg.rows = a.first[sg.g + 1] - sg.row0;
+            sg.page_row = row_seq(a, sg.row0);
+            sg.length = min(max(a.prefix[sg.g], 0), row_len(a, sg.page_row));
+        }
+        __syncthreads();
     }
     if (*s_dead && tid == 0) atomicOr(&g_fault_shared, FAULT_WAIT_MMA);
     __syncthreads();
@@ -816,7 +834,7 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
 }
 
 // The parts of a row's query head joined: prefix pieces in the order of their blocks, then what the row has of its own.
-template <int D> __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Params p, int tok, int item) {
+template <int D> __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Params p, int tok) {
     constexpr int N = D / 32;                              // elements a lane
     const SharedArgs &a = p.a;
     const int lane = threadIdx.x & 31;
@@ -839,7 +857,7 @@ template <int D> __global__ void __launch_bounds__(128) join_kernel(const __grid
     };
     const int g = pl.group[b];
     if (g >= 0 && pl.length[g] > 0) {
-        const int row0 = a.first[g], rows = a.first[g + 1] - row0, tiles = (pl.length[g] + tok - 1) / tok;
+        const int item = pl.item, row0 = a.first[g], rows = a.first[g + 1] - row0, tiles = (pl.length[g] + tok - 1) / tok;
         const int rr = (b - row0) * p.G + head - h * p.G, mb = rr / item, blocks = (rows * p.G + item - 1) / item;
         const int u0 = pl.cum[g] + (h * blocks + mb) * tiles;
         const int f0 = u0 / pl.size, f1 = (u0 + tiles - 1) / pl.size;
@@ -848,7 +866,7 @@ template <int D> __global__ void __launch_bounds__(128) join_kernel(const __grid
             add(p.w.direct + i * D, ml.x, ml.y);
         } else {
             for (int j = f0; j <= f1; ++j) {
-                const int64_t at = (int64_t(j) * 2 + (j == f0)) * item + rr % item;
+                const int64_t at = (int64_t(j) * 2 + (j == f0)) * (2 * ROWS) + rr % item;
                 const float2 ml = p.w.piece_ml[at];
                 add(p.w.piece + at * D, ml.x, ml.y);
             }
@@ -877,8 +895,7 @@ template <int KT, int D> cudaError_t run(const Params &p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!opted[dev]) {
-        const int most = F::smem(1) > F::smem(2) ? F::smem(1) : F::smem(2);
-        e = cudaFuncSetAttribute(prefix_kernel<KT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        e = cudaFuncSetAttribute(prefix_kernel<KT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
         if (e != cudaSuccess) return e;
         opted[dev] = 1;
     }
@@ -888,7 +905,7 @@ template <int KT, int D> cudaError_t run(const Params &p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(num_sms());
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = F::smem(p.a.q_terms);        // above half of an SM's: one block an SM, which takes all of the tensor memory
+    cfg.dynamicSmemBytes = F::SMEM;                        // above half of an SM's: one block an SM, which takes all of the tensor memory
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -904,7 +921,7 @@ template <int KT, int D> cudaError_t run(const Params &p, cudaStream_t s) {
     cfg.gridDim = dim3(unsigned((int64_t(a.B) * a.q_heads + 3) / 4));
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, F::TOK, F::ITEM);
+    return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, F::TOK);
 }
 
 // What each cache type's translation unit defines.
