@@ -60,7 +60,7 @@ template <int KT, int D> struct Cfg {
     // Shared memory: the queries (one or two operands), 8-bit codes on their way (RAWS places), a ring of tiles of 16-bit keys or
     // values, the plan and the barriers. The results of a segment are put together over the first three.
     static constexpr int SMEM = 227 * 1024, REST = (MAX_GROUPS + 1) * 4 + (TWO ? 2 : 1) * ROWS * 4 + 256;
-    static constexpr int RAWS = !I8 ? 0 : D == 256 ? 2 : 4, RAW_BYTES = TOK * D, RAW_ALL = RAWS * RAW_BYTES;
+    static constexpr int RAWS = !I8 ? 0 : D == 256 ? 2 : D == 128 ? 3 : 4, RAW_BYTES = TOK * D, RAW_ALL = RAWS * RAW_BYTES;
     static constexpr int ring(int operands) {
         const int n = (SMEM - REST - operands * Q_BYTES - RAW_ALL) / TILE_BYTES;
         return n < 8 ? n : 8;
@@ -71,8 +71,6 @@ template <int KT, int D> struct Cfg {
 };
 
 static __device__ int g_fault_shared = 0;
-
-template <bool V> struct Bool { static constexpr bool value = V; };
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -103,6 +101,20 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
           "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
           "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
           "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -186,7 +198,7 @@ struct Slot {
     int at, phase;
     __device__ __forceinline__ void forward(int n, int ring) {
         at += n;
-        while (at >= ring) at -= ring, phase ^= 1;
+        if (at >= ring) at -= ring, phase ^= 1;
     }
 };
 
@@ -343,38 +355,46 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
         int lim = sg.length;                               // tokens that this thread's query sees (softmax groups)
         float f = 0.0f, m = -INFINITY, l = 0.0f;           // its scale, running maximum and sum
         if (warp < 2 * SOFT || warp == MMA_WARP) {
-            // -- queries, rotated, scaled and split: eight lanes a query
+            // -- queries, rotated, scaled and split: eight lanes a query. Whose they are and where they lie is found by a lane a
+            // query first, so that the loads of a pass depend on nothing.
             constexpr int N = D / 16;                      // a lane's elements i and as many i + D / 2
-            const int sub = lane & 7, top = dual ? 2 * ROWS : ROWS;
+            const int sub = lane & 7, top = (live + 31) / 32 * 32;         // rows behind the last stay as they are, if not of its warp
             if (warp < 2 * SOFT) {
+                int my_pos = -1;
+                int64_t my_at = 0;
+                if (const int r = warp * 4 + (lane & 3) + (lane >> 2) * 32; r < live) {
+                    const int rr = sg.mb * item + r, b = rr / p.G, head = sg.h * p.G + rr - b * p.G;
+                    my_at = int64_t(sg.row0 + b) * a.ldq + int64_t(head) * D;
+                    if (a.rope) my_pos = row_len(a, row_seq(a, sg.row0 + b)) - 1;
+                    if (my_pos >= a.rope_rows) {
+                        if (a.rope) atomicOr(&g_fault_shared, FAULT_PAGE);
+                        my_pos = -1;
+                    }
+                }
 #pragma unroll 1
-                for (int r = warp * 4 + (lane >> 3); r < top; r += 2 * SOFT * 4) {
+                for (int it = 0; it * 32 < top; ++it) {
+                    const int r = it * 32 + warp * 4 + (lane >> 3);
+                    const int pos = __shfl_sync(0xffffffffu, my_pos, it * 4 + (lane >> 3));
+                    const int64_t at = __shfl_sync(0xffffffffu, my_at, it * 4 + (lane >> 3)) + sub * N;
                     float x[2][N];
 #pragma unroll
                     for (int e = 0; e < N; ++e) x[0][e] = x[1][e] = 0.0f;
                     if (r < live) {
-                        const int rr = sg.mb * item + r, b = rr / p.G, head = sg.h * p.G + rr - b * p.G;
-                        const int64_t at = int64_t(sg.row0 + b) * a.ldq + int64_t(head) * D + sub * N;
                         load_q<N>(a.q, a.qdt, at, x[0]);
                         load_q<N>(a.q, a.qdt, at + D / 2, x[1]);
-                        if (a.rope) {
-                            const int pos = row_len(a, row_seq(a, sg.row0 + b)) - 1;
-                            if (pos >= a.rope_rows) {
-                                if (sub == 0) atomicOr(&g_fault_shared, FAULT_PAGE);
-                            } else if (pos >= 0) {
-                                const float *t = a.rope + int64_t(pos) * D + sub * N;
+                    }
+                    if (pos >= 0) {
+                        const float *t = a.rope + int64_t(pos) * D + sub * N;
 #pragma unroll
-                                for (int e = 0; e < N; e += 4) {
-                                    const float4 c4 = *reinterpret_cast<const float4 *>(t + e);
-                                    const float4 s4 = *reinterpret_cast<const float4 *>(t + D / 2 + e);
-                                    const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+                        for (int e = 0; e < N; e += 4) {
+                            const float4 c4 = *reinterpret_cast<const float4 *>(t + e);
+                            const float4 s4 = *reinterpret_cast<const float4 *>(t + D / 2 + e);
+                            const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-                                    for (int k = 0; k < 4; ++k) {
-                                        const float i = x[0][e + k], j = x[1][e + k];
-                                        x[0][e + k] = __fsub_rn(__fmul_rn(i, c[k]), __fmul_rn(j, s[k]));
-                                        x[1][e + k] = __fadd_rn(__fmul_rn(j, c[k]), __fmul_rn(i, s[k]));
-                                    }
-                                }
+                            for (int k = 0; k < 4; ++k) {
+                                const float i = x[0][e + k], j = x[1][e + k];
+                                x[0][e + k] = __fsub_rn(__fmul_rn(i, c[k]), __fmul_rn(j, s[k]));
+                                x[1][e + k] = __fadd_rn(__fmul_rn(j, c[k]), __fmul_rn(i, s[k]));
                             }
                         }
                     }
@@ -423,13 +443,17 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     if (!dual || mb == 0) dead = dead || !mbar_wait_bounded(&full[keys.at], keys.phase);
                     if (dead) return;
                     tc_fence_after();
-                    const uint32_t kt = ring32 + keys.at * F::TILE_BYTES;
-                    for (int term = 0; term < a.q_terms; ++term)
+                    // descriptors by adding to the address field of the first: one thread issues all products, and building each
+                    // anew took it as long as the products take (118 clocks apiece)
+                    const uint64_t kd = sw128_kmajor_desc(ring32 + keys.at * F::TILE_BYTES);
+                    const uint32_t to = tmem + F::S_COL + (j & 1) * F::S_STEP;
+                    for (int term = 0; term < a.q_terms; ++term) {
+                        const uint64_t qd = sw128_kmajor_desc(base + (term + mb) * F::Q_BYTES);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            umma_f16(tmem + F::S_COL + (j & 1) * F::S_STEP,
-                                     sw128_kmajor_desc(base + (term + mb) * F::Q_BYTES + (k / 4) * F::QB + (k % 4) * 32),
-                                     sw128_kmajor_desc(kt + (k / 4) * F::KB + (k % 4) * 32), kIdesc<BF, TOK, false>, term || k);
+                            umma_f16(to, qd + ((k / 4) * F::QB + (k % 4) * 32) / 16, kd + ((k / 4) * F::KB + (k % 4) * 32) / 16,
+                                     kIdesc<BF, TOK, false>, term || k);
+                    }
                     umma_commit(&s_full[j & 1]);
                     if (!dual || mb == 1) {
                         umma_commit(&empty[keys.at]);
@@ -449,14 +473,14 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     if (j & 1) p_phase1 ^= 1; else p_phase ^= 1;
                     if (dead) break;
                     tc_fence_after();
-                    const uint32_t vt = ring32 + values.at * F::TILE_BYTES;
-                    const uint32_t o = tmem + F::O_COL + (TWO ? (j & 1) * F::O_STEP : 0);
+                    const uint64_t vd = sw128_mnmajor_desc(ring32 + values.at * F::TILE_BYTES, F::KB);
+                    const uint32_t o = tmem + F::O_COL + (TWO ? (j & 1) * F::O_STEP : 0), w = tmem + F::S_COL + (j & 1) * F::S_STEP;
                     const bool more = TWO ? j > 1 : j > 0; // the accumulators hold something
                     for (int term = 0; term < a.p_terms; ++term)
 #pragma unroll
                         for (int k = 0; k < TOK / 16; ++k)
-                            umma_f16_ts(o, tmem + F::S_COL + (j & 1) * F::S_STEP + (k / 2) * 32 + term * 16 + (k % 2) * 8,
-                                        sw128_mnmajor_desc(vt + k * 2048, F::KB), kIdesc<BF, D, true>, more || term || k);
+                            umma_f16_ts(o, w + (k / 2) * 32 + term * 16 + (k % 2) * 8, vd + k * (2048 / 16), kIdesc<BF, D, true>,
+                                        more || term || k);
                     if (!dual || mb == 1) {
                         umma_commit(&empty[values.at]);
                         // the last values come right behind their predecessor where tiles are taken in turn
@@ -487,143 +511,142 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                 t0 = (sg.tile0 + tile) * TOK;
                 return v;
             };
-            // a thread's rows: STEP apart, C bytes of each
+            // A thread has 16 bytes of NC rows of a tile, STEP rows apart; a warp has WR rows. Where a row lies is found by one lane
+            // (lane j: the warp's j-th row) and handed to the others by shuffles: by every lane for itself it was most of the
+            // loaders' instructions.
             constexpr int CPR = I8 ? D / 16 : D / 8, NC = TOK * CPR / LOAD_THREADS, STEP = LOAD_THREADS / CPR;
-            const int row = t / CPR, c = t % CPR;
-            // pages of its rows of the n-th tile, -1 where there is none
-            auto pages = [&](int n, int (&pg)[NC]) {
+            constexpr int SUB = 32 / CPR, WR = SUB * NC;
+            static_assert(WR <= 32, "a lane a row");
+            const int c = t % CPR, row = t / CPR;
+            const unsigned slots = sg.h * a.pool.page_tokens, within = a.pool.page_tokens - 1;
+            // the page that holds the warp's row j in the n-th tile: -1 none
+            auto row_of = [&](int j) { return (t >> 5) * SUB + j % SUB + j / SUB * STEP; };
+            auto page_of = [&](int n, int j) -> int {
+                if (n >= steps || j >= WR) return -1;
                 int t0;
                 const bool v = place(n, t0);
+                const int at = t0 + row_of(j);
+                if (at >= sg.length) return -1;
+                const int page = table[at >> shift];
+                if (unsigned(page) < unsigned(a.pool.pages)) return page;
+                if (!v) atomicOr(&g_fault_shared, FAULT_PAGE);
+                return -1;
+            };
+            auto slot_of = [&](int t0, int j) -> unsigned { return slots + (unsigned(t0 + row_of(j)) & within); };
+            auto wait_empty = [&] { dead = dead || !mbar_wait_bounded(&empty[load.at], load.phase ^ 1); };
+            auto arrive = [&](const Slot &at) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[at.at]);
+            };
+            // starts the copies of the n-th tile's rows, `page` this lane's row's, to dst + i * step (XOR-ed in by `to`)
+            auto copy = [&](int n, int page, auto to) {
+                int t0;
+                const bool v = place(n, t0);
+                const char *from = static_cast<const char *>(v ? a.pool.v : a.pool.k) + a.layer * a.pool.layer_stride * (I8 ? 1 : 2) + c * 16;
+                const int64_t mine = page < 0 ? -1 : (page * a.pool.page_stride + int64_t(slot_of(t0, lane)) * D) * (I8 ? 1 : 2);
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
-                    const int at = t0 + row + i * STEP;
-                    pg[i] = n < steps && at < sg.length ? table[at >> shift] : -1;
+                    const int64_t off = __shfl_sync(0xffffffffu, mine, i * SUB + lane / CPR);
+                    cp16(to(i), from + (off < 0 ? 0 : off), off >= 0);
                 }
-                if (c == 0 && !v && n < steps)
-#pragma unroll
-                    for (int i = 0; i < NC; ++i)
-                        if (t0 + row + i * STEP < sg.length && unsigned(pg[i]) >= unsigned(a.pool.pages)) atomicOr(&g_fault_shared, FAULT_PAGE);
             };
-            const unsigned slots = sg.h * a.pool.page_tokens, within = a.pool.page_tokens - 1;
-            auto wait_empty = [&] { dead = dead || !mbar_wait_bounded(&empty[load.at], load.phase ^ 1); };
             if constexpr (I8) {
                 // Codes come asynchronously into places of this thread's own, RAWS tiles ahead; their scales (whose lines are asked
-                // into L2 with the codes) come into registers a tile ahead.
-                uint32_t *const codes = reinterpret_cast<uint32_t *>(raw) + t * 4;
-                const uint32_t codes32 = smem_u32(codes);
-                auto fetch = [&](int n, const int (&pg)[NC]) {
+                // into L2 with the codes) into registers a tile ahead: lane j has pair j % WPR of the warp's row j / WPR.
+                constexpr int WPR = D / 64;
+                const uint32_t codes32 = smem_u32(raw) + t * 16;
+                const uint8_t *const codes = raw + t * 16;
+                int in = 0, out = 0;                       // places of the codes
+                auto fetch = [&](int n, int page) {
                     if (n < steps) {
+                        copy(n, page, [&](int i) { return codes32 + in * F::RAW_BYTES + i * (LOAD_THREADS * 16); });
                         int t0;
                         const bool v = place(n, t0);
-                        const int8_t *from = static_cast<const int8_t *>(v ? a.pool.v : a.pool.k) + a.layer * a.pool.layer_stride + c * 16;
-                        const uint16_t *scales = (v ? a.pool.v_scales : a.pool.k_scales) + a.layer * a.pool.scale_layer_stride;
-#pragma unroll
-                        for (int i = 0; i < NC; ++i) {
-                            const bool there = unsigned(pg[i]) < unsigned(a.pool.pages);
-                            const unsigned s = slots + (unsigned(t0 + row + i * STEP) & within);
-                            const int64_t page = there ? pg[i] : 0;
-                            cp16(codes32 + (n % F::RAWS) * F::RAW_BYTES + i * (LOAD_THREADS * 16), from + page * a.pool.page_stride + s * unsigned(D), there);
-                            if (there && c == 0)
-                                asm volatile("prefetch.global.L2 [%0];" ::"l"(scales + page * a.pool.scale_page_stride + s * unsigned(D / 32)));
-                        }
+                        if (page >= 0)
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"((v ? a.pool.v_scales : a.pool.k_scales) + a.layer * a.pool.scale_layer_stride +
+                                                                         page * a.pool.scale_page_stride + int64_t(slot_of(t0, lane)) * (D / 32)));
                     }
                     cp_commit();
+                    in = in + 1 == F::RAWS ? 0 : in + 1;
                 };
-                auto fetch_scales = [&](int n, uint32_t (&sc)[NC]) {
-                    if (n >= steps) return;
+                auto scale_pair = [&](int n) -> uint32_t {
+                    const int j = lane / WPR, page = page_of(n, j);
+                    if (page < 0) return 0;                // a row without a page: zeros
                     int t0;
                     const bool v = place(n, t0);
-                    const uint16_t *scales = (v ? a.pool.v_scales : a.pool.k_scales) + a.layer * a.pool.scale_layer_stride + c / 2;
-#pragma unroll
-                    for (int i = 0; i < NC; ++i) {
-                        const int at = t0 + row + i * STEP;
-                        const int pg = at < sg.length ? table[at >> shift] : -1;
-                        sc[i] = 0;                         // a row without a page: zeros
-                        if (unsigned(pg) < unsigned(a.pool.pages))
-                            sc[i] = scales[pg * a.pool.scale_page_stride + (slots + (unsigned(at) & within)) * unsigned(D / 32)];
-                    }
+                    return *reinterpret_cast<const uint32_t *>((v ? a.pool.v_scales : a.pool.k_scales) + a.layer * a.pool.scale_layer_stride +
+                                                               page * a.pool.scale_page_stride + int64_t(slot_of(t0, j)) * (D / 32) + lane % WPR * 2);
                 };
-                int pg[NC];
-                uint32_t sc[NC], next[NC];
-                pages(0, pg);
+                int page = page_of(0, lane);
 #pragma unroll 1
                 for (int n = 0; n < F::RAWS; ++n) {
-                    fetch(n, pg);
-                    pages(n + 1, pg);
+                    fetch(n, page);
+                    page = page_of(n + 1, lane);
                 }
-                fetch_scales(0, next);
+                uint32_t next = scale_pair(0);
+                const int flip = c / 4 & 1;                // odd columns the other half first: other banks
+                uint32_t to_off[NC];
+#pragma unroll
+                for (int i = 0; i < NC; ++i) to_off[i] = (c / 4) * F::KB + sw128_off(row + i * STEP, (c % 4) * 2 + flip);
 #pragma unroll 1
                 for (int n = 0; n < steps; ++n) {
-#pragma unroll
-                    for (int i = 0; i < NC; ++i) sc[i] = next[i] | next[i] << 16;
-                    fetch_scales(n + 1, next);
+                    const uint32_t pair = next;
+                    next = scale_pair(n + 1);
                     cp_wait<F::RAWS - 1>();
-                    uint4 code[NC];
-#pragma unroll
-                    for (int i = 0; i < NC; ++i)
-                        code[i] = *reinterpret_cast<const uint4 *>(codes + ((n % F::RAWS) * F::RAW_BYTES + i * (LOAD_THREADS * 16)) / 4);
                     wait_empty();
                     if (dead) break;
-                    uint8_t *to = ring + load.at * F::TILE_BYTES + (c / 4) * F::KB;
+                    uint8_t *to = ring + load.at * F::TILE_BYTES;
 #pragma unroll
                     for (int i = 0; i < NC; ++i) {
-                        const uint32_t w[4] = {code[i].x ^ 0x80808080u, code[i].y ^ 0x80808080u, code[i].z ^ 0x80808080u, code[i].w ^ 0x80808080u};
-                        const uint4 lo = make_uint4(dequant2(w[0], 0x4140u, sc[i]), dequant2(w[0], 0x4342u, sc[i]),
-                                                    dequant2(w[1], 0x4140u, sc[i]), dequant2(w[1], 0x4342u, sc[i]));
-                        const uint4 hi = make_uint4(dequant2(w[2], 0x4140u, sc[i]), dequant2(w[2], 0x4342u, sc[i]),
-                                                    dequant2(w[3], 0x4140u, sc[i]), dequant2(w[3], 0x4342u, sc[i]));
-                        const int r = row + i * STEP, flip = c / 4 & 1;        // odd columns the other half first: other banks
-                        *reinterpret_cast<uint4 *>(to + sw128_off(r, (c % 4) * 2 + flip)) = flip ? hi : lo;
-                        *reinterpret_cast<uint4 *>(to + sw128_off(r, (c % 4) * 2 + 1 - flip)) = flip ? lo : hi;
+                        const uint4 code = *reinterpret_cast<const uint4 *>(codes + out * F::RAW_BYTES + i * (LOAD_THREADS * 16));
+                        const uint32_t two = __shfl_sync(0xffffffffu, pair, (i * SUB + lane / CPR) * WPR + c / 4);
+                        const uint32_t s = __byte_perm(two, two, c & 2 ? 0x3232u : 0x1010u);
+                        const uint32_t w[4] = {(flip ? code.z : code.x) ^ 0x80808080u, (flip ? code.w : code.y) ^ 0x80808080u,
+                                               (flip ? code.x : code.z) ^ 0x80808080u, (flip ? code.y : code.w) ^ 0x80808080u};
+                        *reinterpret_cast<uint4 *>(to + to_off[i]) = make_uint4(
+                            dequant2(w[0], 0x4140u, s), dequant2(w[0], 0x4342u, s), dequant2(w[1], 0x4140u, s), dequant2(w[1], 0x4342u, s));
+                        *reinterpret_cast<uint4 *>(to + (to_off[i] ^ 16)) = make_uint4(
+                            dequant2(w[2], 0x4140u, s), dequant2(w[2], 0x4342u, s), dequant2(w[3], 0x4140u, s), dequant2(w[3], 0x4342u, s));
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[load.at]);
+                    arrive(load);
                     load.forward(1, R);
-                    fetch(n + F::RAWS, pg);
-                    pages(n + F::RAWS + 1, pg);
+                    out = out + 1 == F::RAWS ? 0 : out + 1;
+                    fetch(n + F::RAWS, page);
+                    page = page_of(n + F::RAWS + 1, lane);
                 }
                 cp_wait<0>();
             } else {
-                // 16 bytes a thread and row, asynchronously; a place is handed over when `lag` more are under way
+                // a place is handed over when `lag` more are under way
                 const int lag = min(R - 2, 3);
                 Slot done = load;
-                auto hand_over = [&] {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[done.at]);
-                    done.forward(1, R);
-                };
-                int pg[NC];
-                pages(0, pg);
+                int page = page_of(0, lane);
+                uint32_t to_off[NC];
+#pragma unroll
+                for (int i = 0; i < NC; ++i) to_off[i] = (c / 8) * F::KB + sw128_off(row + i * STEP, c % 8);
 #pragma unroll 1
                 for (int n = 0; n < steps; ++n) {
-                    int t0;
-                    const bool v = place(n, t0);
-                    const uint16_t *from = static_cast<const uint16_t *>(v ? a.pool.v : a.pool.k) + a.layer * a.pool.layer_stride + c * 8;
                     wait_empty();
                     if (dead) break;
-                    const uint32_t to = ring32 + load.at * F::TILE_BYTES + (c / 8) * F::KB;
-#pragma unroll
-                    for (int i = 0; i < NC; ++i) {
-                        const int r = row + i * STEP;
-                        const bool there = unsigned(pg[i]) < unsigned(a.pool.pages);
-                        cp16(to + sw128_off(r, c % 8), from + int64_t(there ? pg[i] : 0) * a.pool.page_stride +
-                                                           (slots + (unsigned(t0 + r) & within)) * unsigned(D), there);
-                    }
+                    const uint32_t to = ring32 + load.at * F::TILE_BYTES;
+                    copy(n, page, [&](int i) { return to + to_off[i]; });
                     cp_commit();
-                    pages(n + 1, pg);
+                    page = page_of(n + 1, lane);
                     load.forward(1, R);
                     if (n >= lag) {
                         if (lag == 1) cp_wait<1>();
                         else if (lag == 2) cp_wait<2>();
                         else cp_wait<3>();
-                        hand_over();
+                        arrive(done);
+                        done.forward(1, R);
                     }
                 }
                 cp_wait<0>();
                 if (!dead)
-                    for (int n = max(0, steps - lag); n < steps; ++n) hand_over();
+                    for (int n = max(0, steps - lag); n < steps; ++n) {
+                        arrive(done);
+                        done.forward(1, R);
+                    }
             }
         } else {
             // ------------------------------------- softmax -------------------------------------
@@ -702,43 +725,50 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                 any = true;
                 const float from = m == -INFINITY ? 0.0f : m;
                 float2 sum = make_float2(0.0f, 0.0f), sum1 = sum;
-                auto weigh = [&](int c, const uint32_t (&x)[32], auto second) {
-                    constexpr bool SECOND = decltype(second)::value;
-                    uint32_t h[16], g[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float2 e = fma2(sub2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), from), f, F::BIAS);
-                        e = make_float2(ex2(e.x), ex2(e.y));
-                        if (!all) {
-                            e.x = c + 2 * i < left ? e.x : 0.0f;
-                            e.y = c + 2 * i + 1 < left ? e.y : 0.0f;
-                        }
-                        if (i & 1) sum1 = add2(sum1, e); else sum = add2(sum, e);
-                        h[i] = pack2<BF>(e.x, e.y);
-                        if (SECOND) g[i] = rest2<BF>(e.x, e.y, h[i]);
-                    }
-                    tmem_st16(sc + c, h);
-                    if (SECOND) tmem_st16(sc + c + 16, g);
+                // two scores' weights, the second of them that of token c + 1 of the tile
+                auto weigh = [&](int c, uint32_t u, uint32_t v) -> float2 {
+                    float2 e = fma2(sub2(make_float2(__uint_as_float(u), __uint_as_float(v)), from), f, F::BIAS);
+                    e = make_float2(ex2(e.x), ex2(e.y));
+                    if (!all) e = make_float2(c < left ? e.x : 0.0f, c + 1 < left ? e.y : 0.0f);
+                    return e;
                 };
                 if (BF || a.p_terms == 2) {
 #pragma unroll 1
                     for (int c = 0; c < TOK; c += 32) {
-                        uint32_t x[32];
+                        uint32_t x[32], h[16], g[16];
                         tmem_ld32(sc + c, x);
                         tmem_ld_wait();
-                        weigh(c, x, Bool<true>());
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 e = weigh(c + 2 * i, x[2 * i], x[2 * i + 1]);
+                            if (i & 1) sum1 = add2(sum1, e); else sum = add2(sum, e);
+                            h[i] = pack2<BF>(e.x, e.y);
+                            g[i] = rest2<BF>(e.x, e.y, h[i]);
+                        }
+                        tmem_st16(sc + c, h);
+                        tmem_st16(sc + c + 16, g);
                     }
-                } else {                                   // a chunk's loads under the one before
-                    uint32_t x[32], y[32];
-                    tmem_ld32(sc, x);
+                } else {                                   // 16 scores' loads under the weights of the 16 before
+                    uint32_t x[16], y[16];
+                    auto half = [&](int c, const uint32_t (&z)[16]) {
+                        uint32_t h[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 e = weigh(c + 2 * i, z[2 * i], z[2 * i + 1]);
+                            if (i & 1) sum1 = add2(sum1, e); else sum = add2(sum, e);
+                            h[i] = pack2<BF>(e.x, e.y);
+                        }
+                        tmem_st8(sc + c / 32 * 32 + c % 32 / 2, h);
+                    };
+                    tmem_ld16(sc, x);
 #pragma unroll 1
-                    for (int c = 0; c < TOK; c += 64) {
+                    for (int c = 0; c < TOK; c += 32) {
                         tmem_ld_wait();
-                        tmem_ld32(sc + c + 32, y);
-                        weigh(c, x, Bool<false>());
+                        tmem_ld16(sc + c + 16, y);
+                        half(c, x);
                         tmem_ld_wait();
-                        if (c + 64 < TOK) tmem_ld32(sc + c + 64, x);
-                        weigh(c + 32, y, Bool<false>());
+                        if (c + 32 < TOK) tmem_ld16(sc + c + 32, x);
+                        half(c + 16, y);
                     }
                 }
                 l += sum.x + sum.y + (sum1.x + sum1.y);
@@ -833,47 +863,68 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
     }
 }
 
-// The parts of a row's query head joined: prefix pieces in the order of their blocks, then what the row has of its own.
+// The parts of a row's query head joined: prefix pieces in the order of their blocks, then what the row has of its own. A warp
+// a query head. The pieces' maxima and sums come a lane a piece, so that their accumulators, weighted at once, depend on no
+// other's.
 template <int D> __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Params p, int tok) {
     constexpr int N = D / 32;                              // elements a lane
     const SharedArgs &a = p.a;
     const int lane = threadIdx.x & 31;
     const int64_t i = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
     pdl_launch_dependents();
-    pdl_wait();
     if (i >= int64_t(a.B) * a.q_heads) return;
     const int b = int(i / a.q_heads), head = int(i - int64_t(b) * a.q_heads), h = head / p.G;
+    pdl_wait();
     const Plan &pl = *p.w.plan;
     float o[N], m = -INFINITY, l = 0.0f;
 #pragma unroll
     for (int e = 0; e < N; ++e) o[e] = 0.0f;
-    auto add = [&](const float *x, float mi, float li) {
-        if (!(li != 0.0f)) return;
-        const float top = fmaxf(m, mi), f = m == -INFINITY ? 0.0f : ex2(m - top), g = ex2(mi - top);
-        m = top;
-        l = fmaf(li, g, l * f);
+    // joins up to 32 parts: a lane's maximum and sum (none: 0), and where lane j's accumulators lie
+    auto join = [&](float mi, float li, const float *from, int64_t step, int n) {
+        if (!(li != 0.0f)) mi = -INFINITY;                 // (a sum of NaN counts)
+        float top = mi;
 #pragma unroll
-        for (int e = 0; e < N; ++e) o[e] = fmaf(x[lane * N + e], g, o[e] * f);
+        for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        top = fmaxf(top, m);
+        const float old = m == -INFINITY ? 0.0f : ex2(m - top), w = li != 0.0f ? ex2(mi - top) : 0.0f;
+        float sum = w != 0.0f ? li * w : 0.0f;
+#pragma unroll
+        for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        m = top, l = fmaf(l, old, sum);
+#pragma unroll
+        for (int e = 0; e < N; ++e) o[e] *= old;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+            const float wj = __shfl_sync(0xffffffffu, w, j);
+            if (wj == 0.0f) continue;                      // may hold anything
+            const float *x = from + j * step + lane * N;
+#pragma unroll
+            for (int e = 0; e < N; ++e) o[e] = fmaf(x[e], wj, o[e]);
+        }
     };
     const int g = pl.group[b];
     if (g >= 0 && pl.length[g] > 0) {
-        const int item = pl.item, row0 = a.first[g], rows = a.first[g + 1] - row0, tiles = (pl.length[g] + tok - 1) / tok;
+        const int item = pl.item, size = pl.size, row0 = a.first[g], rows = a.first[g + 1] - row0, tiles = (pl.length[g] + tok - 1) / tok;
         const int rr = (b - row0) * p.G + head - h * p.G, mb = rr / item, blocks = (rows * p.G + item - 1) / item;
         const int u0 = pl.cum[g] + (h * blocks + mb) * tiles;
-        const int f0 = u0 / pl.size, f1 = (u0 + tiles - 1) / pl.size;
-        if (f0 == f1) {
-            const float2 ml = p.w.direct_ml[i];
-            add(p.w.direct + i * D, ml.x, ml.y);
+        const int f0 = u0 / size, n = (u0 + tiles - 1) / size - f0 + 1;
+        if (n == 1) {
+            const float2 ml = lane == 0 ? p.w.direct_ml[i] : make_float2(-INFINITY, 0.0f);
+            join(ml.x, ml.y, p.w.direct + i * D, 0, 1);
         } else {
-            for (int j = f0; j <= f1; ++j) {
-                const int64_t at = (int64_t(j) * 2 + (j == f0)) * (2 * ROWS) + rr % item;
-                const float2 ml = p.w.piece_ml[at];
-                add(p.w.piece + at * D, ml.x, ml.y);
+            // the first block's piece is in its second place, the others' in their first
+            const int64_t first = int64_t(f0) * 2 * (2 * ROWS) + rr % item;
+            float2 ml = lane == 0 ? p.w.piece_ml[first + 2 * ROWS] : make_float2(-INFINITY, 0.0f);
+            join(ml.x, ml.y, p.w.piece + (first + 2 * ROWS) * D, 0, 1);
+            for (int j0 = 1; j0 < n; j0 += 32) {
+                const int64_t at = first + int64_t(j0) * (4 * ROWS);
+                ml = j0 + lane < n ? p.w.piece_ml[at + lane * (4 * ROWS)] : make_float2(-INFINITY, 0.0f);
+                join(ml.x, ml.y, p.w.piece + at * D, int64_t(4 * ROWS) * D, min(32, n - j0));
             }
         }
     }
     const float own = p.w.own_lse[i];
-    if (own != -INFINITY) add(p.w.own_out + i * D, own * 1.4426950408889634f, 1.0f);
+    join(lane == 0 ? own * 1.4426950408889634f : -INFINITY, lane == 0 && own != -INFINITY ? 1.0f : 0.0f, p.w.own_out + i * D, 0, 1);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int64_t at = int64_t(b) * a.ldo + int64_t(head) * D + lane * N;
 #pragma unroll
