@@ -49,6 +49,9 @@ template <int KT, int D> struct Cfg {
     static constexpr bool BF = KT == QPACK_KV_BF16, I8 = KT == QPACK_KV_I8;
     static constexpr bool TWO = D <= 128;                  // two accumulators fit the tensor memory beside two tiles' scores
     static constexpr int TOK = D == 256 ? 64 : 128;        // tokens of a tile
+    // Loaders take a tile together, or, where they convert it, in two teams that take them in turn: with one, the waits and
+    // latencies of a tile had nothing to pass under.
+    static constexpr int TEAMS = I8 ? 2 : 1, TEAM = LOAD_THREADS / TEAMS;
     static constexpr int BLOCKS = D / 64;                  // 128-byte columns of an operand
     static constexpr int QB = ROWS * 128, KB = TOK * 128;  // bytes of a column of queries, of a tile
     static constexpr int Q_BYTES = BLOCKS * QB, TILE_BYTES = BLOCKS * KB;
@@ -57,10 +60,10 @@ template <int KT, int D> struct Cfg {
     static constexpr int O_COL = 0, O_STEP = D, S_COL = 256, S_STEP = TOK;
     // Probabilities are held as 2^(x - m + BIAS), at most 2^(BIAS + GROW): m is a maximum that lags behind by up to GROW.
     static constexpr float BIAS = BF ? 0.0f : 7.0f, GROW = 8.0f;
-    // Shared memory: the queries (one or two operands), 8-bit codes on their way (RAWS places), a ring of tiles of 16-bit keys or
+    // Shared memory: the queries (one or two operands), 8-bit codes on their way (a tile a team), a ring of tiles of 16-bit keys or
     // values, the plan and the barriers. The results of a segment are put together over the first three.
     static constexpr int SMEM = 227 * 1024, REST = (MAX_GROUPS + 1) * 4 + (TWO ? 2 : 1) * ROWS * 4 + 256;
-    static constexpr int RAWS = !I8 ? 0 : D == 256 ? 2 : D == 128 ? 3 : 4, RAW_BYTES = TOK * D, RAW_ALL = RAWS * RAW_BYTES;
+    static constexpr int RAW_BYTES = TOK * D, RAW_ALL = I8 ? TEAMS * RAW_BYTES : 0;
     static constexpr int ring(int operands) {
         const int n = (SMEM - REST - operands * Q_BYTES - RAW_ALL) / TILE_BYTES;
         return n < 8 ? n : 8;
@@ -77,13 +80,37 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// A (128 x 16, in TMEM) times B.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// The products are issued by one lane of a warp that runs through their code as a whole: all they are given is the same for
+// the warp then, and lies where the instruction wants it (one lane alone in a branch took 135 clocks a product).
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void umma_ss(uint32_t one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+// A (128 x 16, in TMEM) times B.
+__device__ __forceinline__ void umma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t one, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(one)
         : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -230,7 +257,7 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
     constexpr bool BF = F::BF, I8 = F::I8, TWO = F::TWO;
     extern __shared__ __align__(1024) uint8_t sm[];
     const SharedArgs &a = p.a;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = smem_u32(sm);
     int *const cum = reinterpret_cast<int *>(sm + F::SMEM - F::REST);
     float *const x_scale = reinterpret_cast<float *>(cum + MAX_GROUPS + 1);
@@ -245,7 +272,7 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < 8; ++i) mbar_init(&full[i], LOADERS), mbar_init(&empty[i], 1);
+        for (int i = 0; i < 8; ++i) mbar_init(&full[i], LOADERS / F::TEAMS), mbar_init(&empty[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], SOFT);
         mbar_init(pv_done, 1), mbar_init(o_done, 1);
         fence_mbar_init();
@@ -338,7 +365,7 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
     uint8_t *const ring = raw + F::RAW_ALL;
     const uint32_t ring32 = smem_u32(ring);
     const int shift = 31 - __clz(a.pool.page_tokens);
-    Slot load = {0, 0}, keys = {0, 0}, values = {0, 0};    // of the loaders; of the products
+    Slot load = {I8 && warp >= 2 * SOFT + LOADERS / 2 ? 1 : 0, 0}, keys = {0, 0}, values = {0, 0};    // of the loaders; of the products
     int s_phase = 0, s_phase1 = 0, p_phase = 0, p_phase1 = 0, pv_phase = 0, o_phase = 0;
     bool dead = false;
     for (int unit = unit0;;) {
@@ -437,7 +464,8 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
         }
         if (warp == MMA_WARP) {
             // ------------------------------------ products ------------------------------------
-            if (lane == 0) {
+            const uint32_t one = elect_one();
+            {
                 auto scores = [&](int j) {
                     const int mb = dual ? j & 1 : 0;
                     if (!dual || mb == 0) dead = dead || !mbar_wait_bounded(&full[keys.at], keys.phase);
@@ -451,12 +479,12 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                         const uint64_t qd = sw128_kmajor_desc(base + (term + mb) * F::Q_BYTES);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            umma_f16(to, qd + ((k / 4) * F::QB + (k % 4) * 32) / 16, kd + ((k / 4) * F::KB + (k % 4) * 32) / 16,
+                            umma_ss(one, to, qd + ((k / 4) * F::QB + (k % 4) * 32) / 16, kd + ((k / 4) * F::KB + (k % 4) * 32) / 16,
                                      kIdesc<BF, TOK, false>, term || k);
                     }
-                    umma_commit(&s_full[j & 1]);
+                    commit(one, &s_full[j & 1]);
                     if (!dual || mb == 1) {
-                        umma_commit(&empty[keys.at]);
+                        commit(one, &empty[keys.at]);
                         keys.forward(!dual && j == 0 && nt > 1 ? 1 : 2, R);
                     }
                 };
@@ -479,25 +507,23 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     for (int term = 0; term < a.p_terms; ++term)
 #pragma unroll
                         for (int k = 0; k < TOK / 16; ++k)
-                            umma_f16_ts(o, w + (k / 2) * 32 + term * 16 + (k % 2) * 8, vd + k * (2048 / 16), kIdesc<BF, D, true>,
+                            umma_ts(one, o, w + (k / 2) * 32 + term * 16 + (k % 2) * 8, vd + k * (2048 / 16), kIdesc<BF, D, true>,
                                         more || term || k);
                     if (!dual || mb == 1) {
-                        umma_commit(&empty[values.at]);
+                        commit(one, &empty[values.at]);
                         // the last values come right behind their predecessor where tiles are taken in turn
                         values.forward(!dual && t == nt - 2 ? 1 : 2, R);
                     }
-                    if (!TWO) umma_commit(pv_done);
+                    if (!TWO) commit(one, pv_done);
                     if (j + 2 < jobs) scores(j + 2);
                 }
-                umma_commit(o_done);
+                commit(one, o_done);
                 keys = begin;                              // to the next segment's first place
                 keys.phase ^= 2 * nt / R & 1, keys.forward(2 * nt % R, R);
-                if (dead) *s_dead = 1;
             }
-            __syncwarp();
         } else if (warp >= 2 * SOFT) {
             // ------------------------------------- loaders -------------------------------------
-            const int t = tid - 2 * SOFT * 32;
+            const int team = (warp - 2 * SOFT) / (LOADERS / F::TEAMS), t = tid - 2 * SOFT * 32 - team * F::TEAM;
             const int *table = a.t.tables + int64_t(sg.page_row) * a.t.stride;
             // a segment's tiles in the order of the products: keys of the next tile before values of this one where tiles are
             // taken in turn, keys and values of a tile else
@@ -514,9 +540,9 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
             // A thread has 16 bytes of NC rows of a tile, STEP rows apart; a warp has WR rows. Where a row lies is found by one lane
             // (lane j: the warp's j-th row) and handed to the others by shuffles: by every lane for itself it was most of the
             // loaders' instructions.
-            constexpr int CPR = I8 ? D / 16 : D / 8, NC = TOK * CPR / LOAD_THREADS, STEP = LOAD_THREADS / CPR;
+            constexpr int CPR = I8 ? D / 16 : D / 8, NC = TOK * CPR / F::TEAM, STEP = F::TEAM / CPR;
             constexpr int SUB = 32 / CPR, WR = SUB * NC;
-            static_assert(WR <= 32, "a lane a row");
+            static_assert(WR <= 32 && STEP % 8 == 0, "a lane a row; a thread's rows lie alike in the swizzle");
             const int c = t % CPR, row = t / CPR;
             const unsigned slots = sg.h * a.pool.page_tokens, within = a.pool.page_tokens - 1;
             // the page that holds the warp's row j in the n-th tile: -1 none
@@ -539,8 +565,8 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[at.at]);
             };
-            // starts the copies of the n-th tile's rows, `page` this lane's row's, to dst + i * step (XOR-ed in by `to`)
-            auto copy = [&](int n, int page, auto to) {
+            // starts the copies of the n-th tile's rows, `page` this lane's row's, to `to` and on in steps
+            auto copy = [&](int n, int page, uint32_t to, int step) {
                 int t0;
                 const bool v = place(n, t0);
                 const char *from = static_cast<const char *>(v ? a.pool.v : a.pool.k) + a.layer * a.pool.layer_stride * (I8 ? 1 : 2) + c * 16;
@@ -548,72 +574,72 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
                     const int64_t off = __shfl_sync(0xffffffffu, mine, i * SUB + lane / CPR);
-                    cp16(to(i), from + (off < 0 ? 0 : off), off >= 0);
+                    cp16(to + i * step, from + (off < 0 ? 0 : off), off >= 0);
                 }
             };
             if constexpr (I8) {
-                // Codes come asynchronously into places of this thread's own, RAWS tiles ahead; their scales (whose lines are asked
-                // into L2 with the codes) into registers a tile ahead: lane j has pair j % WPR of the warp's row j / WPR.
-                constexpr int WPR = D / 64;
-                const uint32_t codes32 = smem_u32(raw) + t * 16;
-                const uint8_t *const codes = raw + t * 16;
-                int in = 0, out = 0;                       // places of the codes
+                // A tile's codes come asynchronously into places of this thread's own, while it converts the tile before from its
+                // registers; a row's scales come to the lane that found the row.
+                constexpr int WPR = D / 64;                // pairs of scales a row
+                const uint8_t *const codes = raw + team * F::RAW_BYTES + t * 16;
+                const uint32_t codes32 = smem_u32(codes);
+                uint32_t next[WPR];
                 auto fetch = [&](int n, int page) {
-                    if (n < steps) {
-                        copy(n, page, [&](int i) { return codes32 + in * F::RAW_BYTES + i * (LOAD_THREADS * 16); });
-                        int t0;
-                        const bool v = place(n, t0);
-                        if (page >= 0)
-                            asm volatile("prefetch.global.L2 [%0];" ::"l"((v ? a.pool.v_scales : a.pool.k_scales) + a.layer * a.pool.scale_layer_stride +
-                                                                         page * a.pool.scale_page_stride + int64_t(slot_of(t0, lane)) * (D / 32)));
-                    }
+                    if (n >= steps) return;
+                    copy(n, page, codes32, F::TEAM * 16);
                     cp_commit();
-                    in = in + 1 == F::RAWS ? 0 : in + 1;
-                };
-                auto scale_pair = [&](int n) -> uint32_t {
-                    const int j = lane / WPR, page = page_of(n, j);
-                    if (page < 0) return 0;                // a row without a page: zeros
                     int t0;
                     const bool v = place(n, t0);
-                    return *reinterpret_cast<const uint32_t *>((v ? a.pool.v_scales : a.pool.k_scales) + a.layer * a.pool.scale_layer_stride +
-                                                               page * a.pool.scale_page_stride + int64_t(slot_of(t0, j)) * (D / 32) + lane % WPR * 2);
-                };
-                int page = page_of(0, lane);
-#pragma unroll 1
-                for (int n = 0; n < F::RAWS; ++n) {
-                    fetch(n, page);
-                    page = page_of(n + 1, lane);
-                }
-                uint32_t next = scale_pair(0);
-                const int flip = c / 4 & 1;                // odd columns the other half first: other banks
-                uint32_t to_off[NC];
+                    const uint16_t *from = (v ? a.pool.v_scales : a.pool.k_scales) + a.layer * a.pool.scale_layer_stride;
 #pragma unroll
-                for (int i = 0; i < NC; ++i) to_off[i] = (c / 4) * F::KB + sw128_off(row + i * STEP, (c % 4) * 2 + flip);
+                    for (int e = 0; e < WPR; ++e) next[e] = 0; // a row without a page: zeros
+                    if (page < 0) return;
+                    from += page * a.pool.scale_page_stride + int64_t(slot_of(t0, lane)) * (D / 32);
+                    if constexpr (WPR == 1) next[0] = *reinterpret_cast<const uint32_t *>(from);
+                    else if constexpr (WPR == 2) {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(from);
+                        next[0] = x.x, next[1] = x.y;
+                    } else {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(from);
+                        next[0] = x.x, next[1] = x.y, next[2] = x.z, next[3] = x.w;
+                    }
+                };
+                fetch(team, page_of(team, lane));
+                int page = page_of(team + F::TEAMS, lane);
+                const int flip = c / 4 & 1;                // odd columns the other half first: other banks
+                const uint32_t off = (c / 4) * F::KB + sw128_off(row, (c % 4) * 2 + flip);
 #pragma unroll 1
-                for (int n = 0; n < steps; ++n) {
-                    const uint32_t pair = next;
-                    next = scale_pair(n + 1);
-                    cp_wait<F::RAWS - 1>();
+                for (int n = team; n < steps; n += F::TEAMS) {
+                    cp_wait<0>();
+                    uint4 code[NC];
+                    uint32_t pair[WPR];
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) code[i] = *reinterpret_cast<const uint4 *>(codes + i * (F::TEAM * 16));
+#pragma unroll
+                    for (int e = 0; e < WPR; ++e) pair[e] = next[e];
+                    fetch(n + F::TEAMS, page);
+                    page = page_of(n + 2 * F::TEAMS, lane);
                     wait_empty();
                     if (dead) break;
                     uint8_t *to = ring + load.at * F::TILE_BYTES;
 #pragma unroll
                     for (int i = 0; i < NC; ++i) {
-                        const uint4 code = *reinterpret_cast<const uint4 *>(codes + out * F::RAW_BYTES + i * (LOAD_THREADS * 16));
-                        const uint32_t two = __shfl_sync(0xffffffffu, pair, (i * SUB + lane / CPR) * WPR + c / 4);
+                        uint32_t two = __shfl_sync(0xffffffffu, pair[0], i * SUB + lane / CPR);
+#pragma unroll
+                        for (int e = 1; e < WPR; ++e) {
+                            const uint32_t x = __shfl_sync(0xffffffffu, pair[e], i * SUB + lane / CPR);
+                            two = c / 4 == e ? x : two;
+                        }
                         const uint32_t s = __byte_perm(two, two, c & 2 ? 0x3232u : 0x1010u);
-                        const uint32_t w[4] = {(flip ? code.z : code.x) ^ 0x80808080u, (flip ? code.w : code.y) ^ 0x80808080u,
-                                               (flip ? code.x : code.z) ^ 0x80808080u, (flip ? code.y : code.w) ^ 0x80808080u};
-                        *reinterpret_cast<uint4 *>(to + to_off[i]) = make_uint4(
+                        const uint32_t w[4] = {(flip ? code[i].z : code[i].x) ^ 0x80808080u, (flip ? code[i].w : code[i].y) ^ 0x80808080u,
+                                               (flip ? code[i].x : code[i].z) ^ 0x80808080u, (flip ? code[i].y : code[i].w) ^ 0x80808080u};
+                        *reinterpret_cast<uint4 *>(to + off + i * (STEP * 128)) = make_uint4(
                             dequant2(w[0], 0x4140u, s), dequant2(w[0], 0x4342u, s), dequant2(w[1], 0x4140u, s), dequant2(w[1], 0x4342u, s));
-                        *reinterpret_cast<uint4 *>(to + (to_off[i] ^ 16)) = make_uint4(
+                        *reinterpret_cast<uint4 *>(to + (off ^ 16) + i * (STEP * 128)) = make_uint4(
                             dequant2(w[2], 0x4140u, s), dequant2(w[2], 0x4342u, s), dequant2(w[3], 0x4140u, s), dequant2(w[3], 0x4342u, s));
                     }
                     arrive(load);
-                    load.forward(1, R);
-                    out = out + 1 == F::RAWS ? 0 : out + 1;
-                    fetch(n + F::RAWS, page);
-                    page = page_of(n + F::RAWS + 1, lane);
+                    load.forward(F::TEAMS, R);
                 }
                 cp_wait<0>();
             } else {
@@ -621,15 +647,12 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                 const int lag = min(R - 2, 3);
                 Slot done = load;
                 int page = page_of(0, lane);
-                uint32_t to_off[NC];
-#pragma unroll
-                for (int i = 0; i < NC; ++i) to_off[i] = (c / 8) * F::KB + sw128_off(row + i * STEP, c % 8);
+                const uint32_t off = (c / 8) * F::KB + sw128_off(row, c % 8);
 #pragma unroll 1
                 for (int n = 0; n < steps; ++n) {
                     wait_empty();
                     if (dead) break;
-                    const uint32_t to = ring32 + load.at * F::TILE_BYTES;
-                    copy(n, page, [&](int i) { return to + to_off[i]; });
+                    copy(n, page, ring32 + load.at * F::TILE_BYTES + off, STEP * 128);
                     cp_commit();
                     page = page_of(n + 1, lane);
                     load.forward(1, R);
