@@ -87,23 +87,30 @@ __device__ __forceinline__ uint32_t elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void umma_ss(uint32_t one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// Descriptors are given by their low words: between operands and steps only the address field there changes, and one addition
+// a descriptor is what the issuing warp can do beside a product. High word: 1024 bytes between groups of rows, version 1,
+// 128-byte swizzle.
+constexpr uint32_t DESC_HI = 1024 >> 4 | 1u << 14 | 2u << 29;
+__device__ __forceinline__ void umma_ss(uint32_t one, uint32_t d_tmem, uint32_t adesc, uint32_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        "mov.b64 a, {%1, %6};\n\t"
+        "mov.b64 b, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(adesc), "r"(bdesc), "r"(idesc), "r"(accumulate), "r"(one), "n"(DESC_HI)
         : "memory");
 }
 // A (128 x 16, in TMEM) times B.
-__device__ __forceinline__ void umma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void umma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint32_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        "mov.b64 b, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "r"(bdesc), "r"(idesc), "r"(accumulate), "r"(one), "n"(DESC_HI)
         : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t one, uint64_t *bar) {
@@ -146,17 +153,11 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Descriptor of an operand whose rows run along the product's sum (tokens) and lie 128 bytes apart, 64 elements of the
-// other index (d) a row, 128-byte swizzle: groups of eight rows 1024 bytes apart, columns of 64 elements `column` bytes apart.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t column) {
-    uint64_t d = 0;
-    d |= uint64_t((smem_addr >> 4) & 0x3FFFu);
-    d |= uint64_t(column >> 4) << 16;
-    d |= uint64_t(1024 >> 4) << 32;
-    d |= uint64_t(1) << 46;
-    d |= uint64_t(2) << 61;
-    return d;
-}
+// Low words of operand descriptors with 128-byte swizzle, groups of eight rows of 128 bytes 1024 bytes apart: rows of 64
+// elements of the product's sum (queries, keys); rows that run along the sum themselves (values by tokens), whose columns of 64
+// elements lie `column` bytes apart.
+__device__ __forceinline__ uint32_t desc_k(uint32_t smem_addr) { return (smem_addr >> 4 & 0x3FFFu) | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t smem_addr, uint32_t column) { return (smem_addr >> 4 & 0x3FFFu) | column >> 4 << 16; }
 // Instruction descriptors, kind::f16: fp32 sums, M = 128, N, B's layout.
 template <bool BF, int N, bool MN> constexpr uint32_t kIdesc =
     (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (MN ? 1u << 16 : 0u) | (uint32_t(N >> 3) << 17) | (uint32_t(ROWS >> 4) << 24);
@@ -204,6 +205,11 @@ __device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
     asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %5};\n\t"
         "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
         : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -471,12 +477,10 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     if (!dual || mb == 0) dead = dead || !mbar_wait_bounded(&full[keys.at], keys.phase);
                     if (dead) return;
                     tc_fence_after();
-                    // descriptors by adding to the address field of the first: one thread issues all products, and building each
-                    // anew took it as long as the products take (118 clocks apiece)
-                    const uint64_t kd = sw128_kmajor_desc(ring32 + keys.at * F::TILE_BYTES);
+                    const uint32_t kd = desc_k(ring32 + keys.at * F::TILE_BYTES);
                     const uint32_t to = tmem + F::S_COL + (j & 1) * F::S_STEP;
                     for (int term = 0; term < a.q_terms; ++term) {
-                        const uint64_t qd = sw128_kmajor_desc(base + (term + mb) * F::Q_BYTES);
+                        const uint32_t qd = desc_k(base + (term + mb) * F::Q_BYTES);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
                             umma_ss(one, to, qd + ((k / 4) * F::QB + (k % 4) * 32) / 16, kd + ((k / 4) * F::KB + (k % 4) * 32) / 16,
@@ -501,7 +505,7 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     if (j & 1) p_phase1 ^= 1; else p_phase ^= 1;
                     if (dead) break;
                     tc_fence_after();
-                    const uint64_t vd = sw128_mnmajor_desc(ring32 + values.at * F::TILE_BYTES, F::KB);
+                    const uint32_t vd = desc_mn(ring32 + values.at * F::TILE_BYTES, F::KB);
                     const uint32_t o = tmem + F::O_COL + (TWO ? (j & 1) * F::O_STEP : 0), w = tmem + F::S_COL + (j & 1) * F::S_STEP;
                     const bool more = TWO ? j > 1 : j > 0; // the accumulators hold something
                     for (int term = 0; term < a.p_terms; ++term)
@@ -703,21 +707,19 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     tmem_ld32(sc + c, x);
                     tmem_ld32(sc + c + 32, y);
                     tmem_ld_wait();
-                    if (all) {
-                        float t1 = -INFINITY;
+                    if (!all)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            top = fmaxf(top, __uint_as_float(x[i]));
-                            t1 = fmaxf(t1, __uint_as_float(y[i]));
+                            x[i] = c + i < left ? x[i] : 0xFF800000u;          // -inf
+                            y[i] = c + 32 + i < left ? y[i] : 0xFF800000u;
                         }
-                        top = fmaxf(top, t1);
-                    } else {
+                    float t1 = -INFINITY;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            top = c + i < left ? fmaxf(top, __uint_as_float(x[i])) : top;
-                            top = c + 32 + i < left ? fmaxf(top, __uint_as_float(y[i])) : top;
-                        }
+                    for (int i = 0; i < 32; i += 2) {
+                        top = max3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                        t1 = max3(t1, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
                     }
+                    top = fmaxf(top, t1);
                 }
                 // the maximum lags; where it has to follow, what has been added up follows too
                 const bool move = top > m && !((top - m) * f <= F::GROW);
