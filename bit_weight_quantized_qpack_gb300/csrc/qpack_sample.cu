@@ -27,9 +27,10 @@ namespace {
 
 __device__ int g_fault_sample = 0;
 
-constexpr int THREADS = 1024, WARPS = THREADS / 32;
-constexpr int BINS = 2048;      // two a thread
+constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int BINS = 2048, PER = BINS / THREADS;
 constexpr int CAP = 1024;       // tokens ranked among each other
+constexpr int MOST_BLOCKS = 8;  // a row's
 
 // ------------------------------------------------------------------------------------------------------------
 // Weights
@@ -59,13 +60,15 @@ struct Heat {
     int places;
 };
 // round(2^places e^{(x - top) / T}) for x <= top.
-__device__ __forceinline__ unsigned long long weight(const Heat &h, const float2 *pow2, float x) {
+template <int DT> __device__ __forceinline__ unsigned long long weight(const Heat &h, const float2 *pow2, float x) {
     // d = x - top in two floats, exactly; y = d log2(e) / T. Products and sums are written out, so that none is contracted.
-    const float d = __fsub_rn(x, h.top), v = __fsub_rn(d, x);
-    const float d_lo = __fsub_rn(__fsub_rn(x, __fsub_rn(d, v)), __fadd_rn(h.top, v));
+    const float d = __fsub_rn(x, h.top);
     const float y = __fmul_rn(d, h.hi);
     if (!(y > -48.0f)) return 0;                           // below half of a weight's last place; x = -inf
-    const float y_lo = __fadd_rn(__fmaf_rn(d, h.hi, -y), __fmaf_rn(d, h.lo, __fmul_rn(d_lo, h.hi)));
+    float tail = __fmul_rn(d, h.lo);
+    const float v = __fsub_rn(d, x);
+    tail = __fmaf_rn(__fsub_rn(__fsub_rn(x, __fsub_rn(d, v)), __fadd_rn(h.top, v)), h.hi, tail);
+    const float y_lo = __fadd_rn(__fmaf_rn(d, h.hi, -y), tail);
     // y = n + j / 256 + r
     constexpr float magic = 12582912.0f / STEPS;           // 1.5 2^23 / 256: its last place is 1 / 256
     const float shifted = __fadd_rn(y, magic);
@@ -150,23 +153,49 @@ template <int DT> struct Logits {
 };
 
 // ------------------------------------------------------------------------------------------------------------
-// The kernel: a block a row
+// The kernel: one to eight blocks a row, which read each other's shared memory
 // ------------------------------------------------------------------------------------------------------------
 struct Shared {
     float2 pow2[STEPS];
-    unsigned count[BINS];
-    unsigned w_lo[BINS], w_hi[BINS];
-    unsigned keys[CAP];
+    unsigned count[BINS], w_lo[BINS], w_hi[BINS];
+    unsigned keys[CAP];         // of this block's tokens in the interval
+    unsigned all_keys[CAP];     // of all blocks'
     unsigned long long weights[CAP];
-    unsigned long long scan64[WARPS], scan64b[WARPS];
+    unsigned long long scan64[WARPS];
     unsigned scan32[WARPS];
-    unsigned long long best;
+    // what the blocks tell each other
+    unsigned long long best, sum, kept;
+    unsigned ties, listed, lo_key, hi_key;
     int bad;
-    unsigned listed, lo_key, hi_key;
+    // what a thread tells its block
     int bin;
-    unsigned bin_count, found_key, found_ties;
-    unsigned long long before_weight, sum_weight, goal;
-    unsigned before_count;
+    unsigned found_key, found_ties;
+    unsigned long long above;
+};
+
+struct Cluster {
+    unsigned rank, size;
+    __device__ __forceinline__ Cluster() {
+        asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+        asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+    }
+    __device__ __forceinline__ void sync() const {
+        if (size == 1) __syncthreads();
+        else asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+    template <class V> __device__ __forceinline__ V read(const V *p, unsigned r) const {
+        uint32_t at;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(r));
+        if constexpr (sizeof(V) == 8) {
+            unsigned long long v;
+            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+            return v;
+        } else {
+            unsigned v;
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+            return V(v);
+        }
+    }
 };
 
 // Exclusive sums over the block; *total: the sum. Every thread calls it.
@@ -181,18 +210,14 @@ template <class V> __device__ __forceinline__ V block_sum(V v, V *space, V *tota
     __syncthreads();
     if (lane == 31) space[w] = x;
     __syncthreads();
-    if (w == 0) {
-        V y = space[lane];
+    V before = 0, all = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const V z = __shfl_up_sync(0xffffffffu, y, o);
-            if (lane >= o) y += z;
-        }
-        space[lane] = y;
+    for (int i = 0; i < WARPS; ++i) {
+        before += i < w ? space[i] : 0;
+        all += space[i];
     }
-    __syncthreads();
-    *total = space[WARPS - 1];
-    return (w ? space[w - 1] : 0) + x - v;
+    *total = all;
+    return before + x - v;
 }
 
 // How a pass of the selection tells a token's interval: by m - x, or by key. Out of range: -1.
@@ -200,138 +225,194 @@ struct Intervals {
     float top, per;             // by distance: (top - x) per, the last interval takes the rest
     unsigned lo, hi;            // by key: lo <= key <= hi
     int shift;                  // < 0: by distance
+    float floor;                // tokens below are in no interval
     __device__ __forceinline__ int of(float x) const {
-        if (x == -INFINITY) return -1;
+        if (!(x >= floor) || x == -INFINITY) return -1;
         if (shift < 0) return int(fminf((top - x) * per, float(BINS - 1)));
         const unsigned k = key_of(x);
         return k < lo || k > hi ? -1 : int((hi - k) >> shift);
     }
 };
 
-template <int DT, bool WEIGH>
-__device__ __forceinline__ void fill(Shared &s, const Logits<DT> &row, const Intervals &iv, const Heat &heat) {
-    for (int i = threadIdx.x; i < BINS; i += THREADS) s.count[i] = s.w_lo[i] = s.w_hi[i] = 0;
-    __syncthreads();
-    for (int v = threadIdx.x; v < row.vectors; v += THREADS) {
-        float x[Logits<DT>::VE];
-        row.load(v, x);
-#pragma unroll
-        for (int e = 0; e < Logits<DT>::VE; ++e) {
-            const int b = iv.of(x[e]);
-            if (b < 0) continue;
-            atomicAdd(&s.count[b], 1u);
-            if (WEIGH) {
-                const unsigned long long w = weight(heat, s.pow2, x[e]);
-                const unsigned lo = unsigned(w), old = atomicAdd(&s.w_lo[b], lo);
-                const unsigned carry = unsigned(w >> 32) + (old + lo < old);
-                if (carry) atomicAdd(&s.w_hi[b], carry);
-            }
+// What a row's passes share.
+template <int DT> struct Row {
+    static constexpr int VE = Logits<DT>::VE;
+    Shared &s;
+    const Cluster &c;
+    Logits<DT> logits;
+    int v0, v1;                 // this block's vectors
+    Heat heat;
+
+    __device__ __forceinline__ unsigned long long weigh(float x) const { return weight<DT>(heat, s.pow2, x); }
+    // f(vector, its elements) over this block's vectors, two at a time for each thread
+    template <class F> __device__ __forceinline__ void each(F f) const {
+        int v = v0 + threadIdx.x;
+        for (; v + THREADS < v1; v += 2 * THREADS) {
+            float x[VE], y[VE];
+            logits.load(v, x);
+            logits.load(v + THREADS, y);
+            f(v, x);
+            f(v + THREADS, y);
+        }
+        if (v < v1) {
+            float x[VE];
+            logits.load(v, x);
+            f(v, x);
         }
     }
-    __syncthreads();
-}
 
-// Finds the token at which the running count (or weight) from the top reaches `goal`: its key, and how many of the tokens of
-// that key are kept. before_*: what lies above the intervals of `iv`, which the histogram holds.
-template <int DT, bool WEIGH>
-__device__ __forceinline__ void select(Shared &s, const Logits<DT> &row, Intervals iv, const Heat &heat,
-                                       unsigned long long goal) {
-    const int tid = threadIdx.x;
-    unsigned long long above = 0;                          // counts or weights above the intervals
-    for (;;) {
-        // the interval that reaches the goal
-        unsigned long long mine[2], total;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            mine[i] = WEIGH ? (static_cast<unsigned long long>(s.w_hi[2 * tid + i]) << 32) + s.w_lo[2 * tid + i]
-                            : s.count[2 * tid + i];
-        unsigned long long at = above + block_sum(mine[0] + mine[1], s.scan64, &total);
-        if (tid == 0) s.listed = 0, s.lo_key = 0xFFFFFFFFu, s.hi_key = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (at < goal && goal <= at + mine[i]) s.bin = 2 * tid + i, s.bin_count = s.count[2 * tid + i], s.before_weight = at;
-            at += mine[i];
+    // Counts the intervals' tokens, or (WEIGH) adds up their weights, of which those below `least` are left out. Returns the
+    // thread's sum of all weights.
+    template <bool WEIGH> __device__ __forceinline__ unsigned long long fill(const Intervals &iv, unsigned long long least) {
+        for (int i = threadIdx.x; i < BINS; i += THREADS) {
+            if (WEIGH) s.w_lo[i] = s.w_hi[i] = 0;
+            else s.count[i] = 0;
         }
         __syncthreads();
-        const int bin = s.bin;
-        const unsigned n = s.bin_count;
-        above = s.before_weight;
-        // its tokens
-        unsigned lo = 0xFFFFFFFFu, hi = 0;
-        for (int v = tid; v < row.vectors; v += THREADS) {
-            float x[Logits<DT>::VE];
-            row.load(v, x);
+        unsigned long long sum = 0;
+        each([&](int, const float (&x)[VE]) {
 #pragma unroll
-            for (int e = 0; e < Logits<DT>::VE; ++e) {
-                if (iv.of(x[e]) != bin) continue;
-                const unsigned k = key_of(x[e]);
-                lo = min(lo, k), hi = max(hi, k);
-                if (n <= CAP) s.keys[atomicAdd(&s.listed, 1u)] = k;
-            }
-        }
-        lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
-        if ((tid & 31) == 0) atomicMin(&s.lo_key, lo), atomicMax(&s.hi_key, hi);
-        __syncthreads();
-        lo = s.lo_key, hi = s.hi_key;
-        if (lo == hi) {                                    // all alike
-            if (tid == 0) {
-                const unsigned long long w = WEIGH ? weight(heat, s.pow2, of_key(lo)) : 1;
-                s.found_key = lo, s.found_ties = unsigned((goal - above + w - 1) / w);
-            }
-            break;
-        }
-        if (n <= CAP) {
-            if (WEIGH && tid < n) s.weights[tid] = weight(heat, s.pow2, of_key(s.keys[tid]));
-            __syncthreads();
-            if (tid < n) {
-                const unsigned k = s.keys[tid];
-                unsigned long long over = above;
-                unsigned same = 0;
-                for (int i = 0; i < int(n); ++i) {
-                    const unsigned o = s.keys[i];
-                    if (o > k) over += WEIGH ? s.weights[i] : 1;
-                    same += o == k;
+            for (int e = 0; e < VE; ++e) {
+                if (!WEIGH) {
+                    const int b = iv.of(x[e]);
+                    if (b >= 0) atomicAdd(&s.count[b], 1u);
+                } else if (x[e] >= iv.floor) {
+                    const unsigned long long w = weigh(x[e]);
+                    sum += w;
+                    const int b = w >= least ? iv.of(x[e]) : -1;
+                    if (b >= 0) {
+                        const unsigned lo = unsigned(w), old = atomicAdd(&s.w_lo[b], lo);
+                        const unsigned carry = unsigned(w >> 32) + (old + lo < old);
+                        if (carry) atomicAdd(&s.w_hi[b], carry);
+                    }
                 }
-                const unsigned long long w = WEIGH ? s.weights[tid] : 1;
-                if (over < goal && goal <= over + same * w)
-                    s.found_key = k, s.found_ties = unsigned((goal - over + w - 1) / w);
             }
-            break;
-        }
-        // too many: divide the interval by keys
-        iv.lo = lo, iv.hi = hi;
-        const int bits = 32 - __clz(hi - lo);
-        iv.shift = max(0, bits - 11);
-        fill<DT, WEIGH>(s, row, iv, heat);
+        });
+        return sum;
     }
-    __syncthreads();
-}
 
-template <int DT> __global__ void __launch_bounds__(THREADS, 1) sample_kernel(SampleArgs a) {
-    extern __shared__ __align__(16) unsigned char smem[];
-    Shared &s = *reinterpret_cast<Shared *>(smem);
+    // Finds the token at which the running count (or weight) from the top reaches `goal`: its key, and how many of the tokens of
+    // that key are kept (s.found_key, s.found_ties). The intervals are filled. Every thread of all blocks calls it.
+    template <bool WEIGH> __device__ __forceinline__ void select(Intervals iv, unsigned long long goal, unsigned long long least) {
+        const int tid = threadIdx.x;
+        unsigned long long above = 0;                      // counts or weights above the intervals
+        for (;;) {
+            c.sync();
+            // the interval that reaches the goal
+            unsigned long long mine[PER], sum = 0, total;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                mine[i] = 0;
+                for (unsigned r = 0; r < c.size; ++r)
+                    mine[i] += WEIGH ? (static_cast<unsigned long long>(c.read(&s.w_hi[PER * tid + i], r)) << 32) + c.read(&s.w_lo[PER * tid + i], r)
+                                     : c.read(&s.count[PER * tid + i], r);
+                sum += mine[i];
+            }
+            unsigned long long at = above + block_sum(sum, s.scan64, &total);
+            if (tid == 0) s.listed = 0, s.lo_key = 0xFFFFFFFFu, s.hi_key = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                if (at < goal && goal <= at + mine[i]) s.bin = PER * tid + i, s.above = at;
+                at += mine[i];
+            }
+            __syncthreads();
+            const int bin = s.bin;
+            above = s.above;
+            // its tokens
+            unsigned lo = 0xFFFFFFFFu, hi = 0;
+            each([&](int, const float (&x)[VE]) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    if (iv.of(x[e]) != bin || (WEIGH && least > 1 && weigh(x[e]) < least)) continue;
+                    const unsigned k = key_of(x[e]);
+                    lo = min(lo, k), hi = max(hi, k);
+                    const unsigned n = atomicAdd(&s.listed, 1u);
+                    if (n < CAP) s.keys[n] = k;
+                }
+            });
+            lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
+            if ((tid & 31) == 0) atomicMin(&s.lo_key, lo), atomicMax(&s.hi_key, hi);
+            c.sync();
+            unsigned n = 0;
+            lo = 0xFFFFFFFFu, hi = 0;
+            for (unsigned r = 0; r < c.size; ++r) {
+                n += c.read(&s.listed, r);
+                lo = min(lo, c.read(&s.lo_key, r)), hi = max(hi, c.read(&s.hi_key, r));
+            }
+            if (lo == hi) {                                // all alike
+                if (tid == 0) {
+                    const unsigned long long w = WEIGH ? weigh(of_key(lo)) : 1;
+                    s.found_key = lo, s.found_ties = unsigned((goal - above + w - 1) / w);
+                }
+                break;
+            }
+            if (n <= CAP) {
+                unsigned first = 0;
+                for (unsigned r = 0; r < c.size; ++r) {
+                    const unsigned m = c.read(&s.listed, r);
+                    for (unsigned i = tid; i < m; i += THREADS) {
+                        const unsigned k = c.read(&s.keys[i], r);
+                        s.all_keys[first + i] = k;
+                        if (WEIGH) s.weights[first + i] = weigh(of_key(k));
+                    }
+                    first += m;
+                }
+                __syncthreads();
+                for (unsigned t = tid; t < n; t += THREADS) {
+                    const unsigned k = s.all_keys[t];
+                    unsigned long long over = above;
+                    unsigned same = 0;
+                    for (unsigned i = 0; i < n; ++i) {
+                        const unsigned o = s.all_keys[i];
+                        if (o > k) over += WEIGH ? s.weights[i] : 1;
+                        same += o == k;
+                    }
+                    const unsigned long long w = WEIGH ? s.weights[t] : 1;
+                    if (over < goal && goal <= over + same * w) s.found_key = k, s.found_ties = unsigned((goal - over + w - 1) / w);
+                }
+                break;
+            }
+            // too many: divide the interval by keys
+            iv.lo = lo, iv.hi = hi;
+            iv.shift = max(0, 32 - __clz(hi - lo) - 11);
+            fill<WEIGH>(iv, least);
+        }
+        __syncthreads();
+    }
+};
+
+template <int DT> __global__ void __launch_bounds__(THREADS, 2) sample_kernel(SampleArgs a) {
+    __shared__ Shared s;
     constexpr int VE = Logits<DT>::VE;
+    const Cluster c;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const int64_t b = blockIdx.x;
+    const int64_t b = blockIdx.x / c.size;
     if (tid < STEPS) s.pow2[tid] = make_float2(g_pow2.hi[tid], g_pow2.lo[tid]);
-    if (tid == 0) s.best = 0, s.bad = 0;
+    if (tid == 0) s.best = 0, s.bad = 0, s.sum = 0;
     pdl_launch_dependents();
     pdl_wait();
-    const Logits<DT> row(static_cast<const unsigned char *>(a.logits) + b * a.ld * Logits<DT>::ES, int(a.vocab));
+    Row<DT> row = {s, c, Logits<DT>(static_cast<const unsigned char *>(a.logits) + b * a.ld * Logits<DT>::ES, int(a.vocab)), 0, 0, {}};
+    const int share = (row.logits.vectors + int(c.size) - 1) / int(c.size);
+    row.v0 = min(int(c.rank) * share, row.logits.vectors), row.v1 = min(row.v0 + share, row.logits.vectors);
+    const float given = a.temperature ? a.temperature[b] : 1.0f, heat_t = given > 0x1p64f ? 0x1p64f : given;
+    const int k = a.top_k ? a.top_k[b] : 0;
+    const float p = a.top_p ? a.top_p[b] : 1.0f, min_p = a.min_p ? a.min_p[b] : 0.0f, u = fminf(fmaxf(a.u[b], 0.0f), 0x1.fffffep-1f);
     __syncthreads();
 
     // -- the maximum, at its lowest index --------------------------------------------------------------------
     unsigned long long best = 0;                           // key, then the index inverted
     bool bad = false;
-    for (int v = tid; v < row.vectors; v += THREADS) {
-        float x[VE];
-        row.load(v, x);
+    {
+        float top = -INFINITY;
+        int at = 0;
+        row.each([&](int v, const float (&x)[VE]) {
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            bad |= !(x[e] < INFINITY);                     // NaN or +inf
-            const unsigned long long k = static_cast<unsigned long long>(key_of(x[e])) << 32 | unsigned(~(row.index(v) + e));
-            best = x[e] > -INFINITY && k > best ? k : best;
-        }
+            for (int e = 0; e < VE; ++e) {
+                bad |= !(x[e] < INFINITY);                 // NaN or +inf
+                if (x[e] > top) top = x[e], at = row.logits.index(v) + e;      // a thread's indices rise
+            }
+        });
+        if (top > -INFINITY) best = static_cast<unsigned long long>(key_of(top)) << 32 | unsigned(~at);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
@@ -340,89 +421,102 @@ template <int DT> __global__ void __launch_bounds__(THREADS, 1) sample_kernel(Sa
         if (best) atomicMax(&s.best, best);
         if (bad) s.bad = 1;
     }
-    __syncthreads();
-    best = s.best;
-    const float given = a.temperature ? a.temperature[b] : 1.0f, heat_t = given > 0x1p64f ? 0x1p64f : given;
-    if (s.bad || best == 0 || !(heat_t >= 0x1p-64f)) {
-        if (tid == 0) {
-            if (s.bad) atomicOr(&g_fault_sample, FAULT_NONFINITE_X);
-            a.tokens[b] = s.bad || best == 0 ? -1 : int(~unsigned(best));
-            if (a.probs) a.probs[b] = s.bad ? __int_as_float(0x7FC00000) : best == 0 ? 0.0f : 1.0f;
+    c.sync();
+    best = 0, bad = false;
+    for (unsigned r = 0; r < c.size; ++r) best = max(best, c.read(&s.best, r)), bad |= c.read(&s.bad, r) != 0;
+    if (bad || best == 0 || !(heat_t >= 0x1p-64f)) {
+        if (tid == 0 && c.rank == 0) {
+            if (bad) atomicOr(&g_fault_sample, FAULT_NONFINITE_X);
+            a.tokens[b] = bad || best == 0 ? -1 : int(~unsigned(best));
+            if (a.probs) a.probs[b] = bad ? __int_as_float(0x7FC00000) : best == 0 ? 0.0f : 1.0f;
         }
+        if (c.size > 1) c.sync();                          // none leaves while another reads its memory
         return;
     }
-    Heat heat;
     {
-        const double c = 1.4426950408889634 / double(heat_t);
-        heat.hi = float(c), heat.lo = float(c - double(heat.hi));
-        heat.top = of_key(unsigned(best >> 32));
-        heat.places = a.places;
+        const double ratio = 1.4426950408889634 / double(heat_t);
+        row.heat.hi = float(ratio), row.heat.lo = float(ratio - double(row.heat.hi));
+        row.heat.top = of_key(unsigned(best >> 32));
+        row.heat.places = a.places;
     }
+    const unsigned long long one = 1ull << a.places;
 
     // -- the last token kept by top-k and top-p ---------------------------------------------------------------
-    const int k = a.top_k ? a.top_k[b] : 0;
-    const float p = a.top_p ? a.top_p[b] : 1.0f, min_p = a.min_p ? a.min_p[b] : 0.0f;
     bool cut_k = k > 0 && k < a.vocab;
     const bool cut_p = p < 1.0f;
-    unsigned last_key = 0, last_ties = 0;                  // kept: keys above, and so many of this one (0: nothing cut)
+    unsigned last_ties = 0;                                // kept: logits above the last one, and so many equal to it (0: nothing cut)
+    float last = -INFINITY;
     if (cut_k || cut_p) {
-        Intervals iv;
-        iv.top = heat.top, iv.per = BINS / fmaxf(32.0f, 32.0f * heat_t), iv.shift = -1;
-        unsigned long long sum;
-        if (cut_p) fill<DT, true>(s, row, iv, heat);
-        else fill<DT, false>(s, row, iv, heat);
+        Intervals iv = {row.heat.top, BINS / fmaxf(32.0f, 32.0f * heat_t), 0, 0, -1, -INFINITY};
         if (cut_k) {
-            unsigned total;
-            block_sum(s.count[2 * tid] + s.count[2 * tid + 1], s.scan32, &total);
+            row.template fill<false>(iv, 0);
+            unsigned total = 0, mine = 0;
+            c.sync();
+            for (int i = 0; i < PER; ++i)
+                for (unsigned r = 0; r < c.size; ++r) mine += c.read(&s.count[PER * tid + i], r);
+            block_sum(mine, s.scan32, &total);
             cut_k = unsigned(k) < total;                   // masked tokens do not count
-        }
-        if (cut_k) {
-            select<DT, false>(s, row, iv, heat, unsigned(k));
-            last_key = s.found_key, last_ties = s.found_ties;
+            if (cut_k) {
+                row.template select<false>(iv, unsigned(k), 0);
+                last = of_key(s.found_key), last_ties = s.found_ties;
+                iv.floor = last;
+            }
         }
         if (cut_p) {
-            // the sum over the k tokens
-            unsigned long long mine = 0;
-            for (int v = tid; v < row.vectors; v += THREADS) {
-                float x[VE];
-                row.load(v, x);
+            // The sum of the tokens kept so far, and their weights by intervals. Tokens whose weight is below (1 - p) / 2 of the
+            // largest over their number stay below (1 - p) / 2 of the sum all together: they are behind the last one kept, and
+            // are left out.
+            const unsigned long long least = max(1ull, part_of(fminf((1.0f - fmaxf(p, 0.0f)) * 0.5f, 0.5f), one, false) / a.vocab);
+            unsigned long long sum = row.template fill<true>(iv, least), total;
+            if (cut_k) {                                   // of the last one's equals only those kept
+                sum = 0;
+                row.each([&](int, const float (&x)[VE]) {
 #pragma unroll
-                for (int e = 0; e < VE; ++e)
-                    if (key_of(x[e]) > last_key) mine += weight(heat, s.pow2, x[e]);
+                    for (int e = 0; e < VE; ++e)
+                        if (x[e] > last) sum += row.weigh(x[e]);
+                });
             }
-            block_sum(mine, s.scan64, &sum);
-            if (cut_k) {
-                sum += last_ties * weight(heat, s.pow2, of_key(last_key));
-                fill<DT, true>(s, row, iv, heat);
-            }
-            const unsigned long long goal = max(1ull, part_of(fmaxf(p, 0.0f), sum, true));
-            select<DT, true>(s, row, iv, heat, goal);
-            last_key = s.found_key, last_ties = s.found_ties;
+            block_sum(sum, s.scan64, &total);
+            if (tid == 0) s.sum = total;
+            c.sync();
+            sum = 0;
+            for (unsigned r = 0; r < c.size; ++r) sum += c.read(&s.sum, r);
+            if (cut_k) sum += last_ties * row.weigh(last);
+            row.template select<true>(iv, max(1ull, part_of(fmaxf(p, 0.0f), sum, true)), least);
+            last = of_key(s.found_key), last_ties = s.found_ties;
         }
     }
-    const unsigned long long one = 1ull << heat.places;
     const unsigned long long least = min_p >= 1.0f ? one : min_p > 0.0f ? max(1ull, part_of(min_p, one, true)) : 1ull;
-    const unsigned long long last_weight = last_ties ? weight(heat, s.pow2, of_key(last_key)) : 0;
+    const unsigned long long last_weight = last_ties ? row.weigh(last) : 0;
     const bool ties_count = last_weight >= least;
 
-    // -- sums of kept weights by warps' shares of the row, in order of index ---------------------------------------
-    const int per = (row.vectors + WARPS - 1) / WARPS, v0 = w * per, v1 = min(v0 + per, row.vectors);
+    // -- sums of kept weights by warps' shares of the block's vectors, in order of index ------------------------------
+    const int per = (row.v1 - row.v0 + WARPS - 1) / WARPS, v0 = min(row.v0 + w * per, row.v1), v1 = min(v0 + per, row.v1);
     auto kept = [&](float x, unsigned &ties) -> unsigned long long {
-        const unsigned key = key_of(x);
-        if (last_ties && key <= last_key) {
-            ties += key == last_key;
+        if (x <= last) {                                   // (-inf where nothing is cut)
+            ties += x == last && last_ties;
             return 0;
         }
-        const unsigned long long y = weight(heat, s.pow2, x);
+        const unsigned long long y = row.weigh(x);
         return y >= least ? y : 0;
     };
     unsigned long long sum = 0;
     unsigned ties = 0;
-    for (int v = v0 + lane; v < v1; v += 32) {
-        float x[VE];
-        row.load(v, x);
+    {
+        int v = v0 + lane;
+        for (; v + 32 < v1; v += 64) {
+            float x[VE], y[VE];
+            row.logits.load(v, x);
+            row.logits.load(v + 32, y);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) sum += kept(x[e], ties);
+            for (int e = 0; e < VE; ++e) sum += kept(x[e], ties) + kept(y[e], ties);
+        }
+        if (v < v1) {
+            float x[VE];
+            row.logits.load(v, x);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) sum += kept(x[e], ties);
+        }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -430,85 +524,101 @@ template <int DT> __global__ void __launch_bounds__(THREADS, 1) sample_kernel(Sa
     __syncthreads();
     if (lane == 0) s.scan64[w] = sum, s.scan32[w] = ties;
     __syncthreads();
-    unsigned long long before = 0, total = 0;
-    unsigned ties_before = 0, all_ties = 0;
-    for (int i = 0; i < WARPS; ++i) {
-        const unsigned here = min(s.scan32[i], last_ties - min(all_ties, last_ties));
-        const unsigned long long add = s.scan64[i] + (ties_count ? here * last_weight : 0);
-        if (i < w) before += add, ties_before += s.scan32[i];
-        total += add, all_ties += s.scan32[i];
-        if (i == w) sum = add;
+    if (tid == 0) {
+        unsigned long long all = 0;
+        unsigned equal = 0;
+        for (int i = 0; i < WARPS; ++i) all += s.scan64[i], equal += s.scan32[i];
+        s.kept = all, s.ties = equal;
     }
-    const float u = fminf(fmaxf(a.u[b], 0.0f), 0x1.fffffep-1f);
-    const unsigned long long goal = part_of(u, total, false);
-    if (goal < before || goal >= before + sum) return;     // another warp's
-
-    // -- the token -----------------------------------------------------------------------------------------------
-    unsigned left = last_ties - min(ties_before, last_ties);
-    unsigned long long run = before;
-    for (int v = v0; v < v1; v += 32) {
-        float x[VE];
-        row.load(v + lane < v1 ? v + lane : row.vectors, x);
-        unsigned t = 0;
-        unsigned long long mine = 0;
-#pragma unroll
-        for (int e = 0; e < VE; ++e) mine += kept(x[e], t);
-        unsigned t_scan = t;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned y = __shfl_up_sync(0xffffffffu, t_scan, o);
-            if (lane >= o) t_scan += y;
-        }
-        unsigned may = left - min(left, t_scan - t);       // ties that this lane may keep
-        mine += ties_count ? min(t, may) * last_weight : 0;
-        unsigned long long scan = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long y = __shfl_up_sync(0xffffffffu, scan, o);
-            if (lane >= o) scan += y;
-        }
-        const unsigned long long end = run + scan;
-        if (goal >= end - mine && goal < end) {
-            unsigned long long at = end - mine;
-            for (int e = 0; e < VE; ++e) {
-                unsigned tie = 0;
-                unsigned long long y = kept(x[e], tie);
-                if (tie && may) y = ties_count ? last_weight : 0, --may;
-                if (goal < at + y) {
-                    a.tokens[b] = row.index(v + lane) + e;
-                    if (a.probs) a.probs[b] = float(double(y) / double(total));
+    c.sync();
+    // kept weights before this warp's share, and in all
+    unsigned long long before = 0, total = 0, mine = 0;
+    unsigned ties_before = 0, all_ties = 0;
+    for (unsigned r = 0; r < c.size; ++r) {
+        const unsigned here = c.read(&s.ties, r), may = last_ties - min(all_ties, last_ties);
+        const unsigned long long add = c.read(&s.kept, r) + (ties_count ? min(here, may) * last_weight : 0);
+        if (r == c.rank) {
+            before = total, ties_before = all_ties;
+            for (int i = 0; i < WARPS; ++i) {
+                const unsigned left = last_ties - min(ties_before, last_ties);
+                const unsigned long long part = s.scan64[i] + (ties_count ? min(s.scan32[i], left) * last_weight : 0);
+                if (i == w) {
+                    mine = part;
                     break;
                 }
-                at += y;
+                before += part, ties_before += s.scan32[i];
             }
         }
-        run += __shfl_sync(0xffffffffu, scan, 31);
-        left -= min(left, __shfl_sync(0xffffffffu, t_scan, 31));
-        if (goal < run) return;
+        total += add, all_ties += here;
     }
+    const unsigned long long goal = part_of(u, total, false);
+    if (goal >= before && goal < before + mine) {          // one warp's
+        unsigned left = last_ties - min(ties_before, last_ties);
+        unsigned long long run = before;
+        for (int v = v0; v < v1; v += 32) {
+            float x[VE];
+            row.logits.load(v + lane < v1 ? v + lane : row.logits.vectors, x);
+            unsigned t = 0;
+            unsigned long long here = 0;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) here += kept(x[e], t);
+            unsigned t_scan = t;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned y = __shfl_up_sync(0xffffffffu, t_scan, o);
+                if (lane >= o) t_scan += y;
+            }
+            unsigned may = left - min(left, t_scan - t);   // ties that this lane may keep
+            here += ties_count ? min(t, may) * last_weight : 0;
+            unsigned long long scan = here;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long y = __shfl_up_sync(0xffffffffu, scan, o);
+                if (lane >= o) scan += y;
+            }
+            const unsigned long long end = run + scan;
+            if (goal >= end - here && goal < end) {
+                unsigned long long at = end - here;
+                for (int e = 0; e < VE; ++e) {
+                    unsigned tie = 0;
+                    unsigned long long y = kept(x[e], tie);
+                    if (tie && may) y = ties_count ? last_weight : 0, --may;
+                    if (goal < at + y) {
+                        a.tokens[b] = row.logits.index(v + lane) + e;
+                        if (a.probs) a.probs[b] = float(double(y) / double(total));
+                        break;
+                    }
+                    at += y;
+                }
+            }
+            run += __shfl_sync(0xffffffffu, scan, 31);
+            left -= min(left, __shfl_sync(0xffffffffu, t_scan, 31));
+            if (goal < run) break;
+        }
+    }
+    if (c.size > 1) c.sync();                              // none leaves while another reads its memory
+}
+
+// Blocks a row: as many as keep the SMs busy, of 4096 tokens or more each.
+int blocks_a_row(int64_t rows, int64_t vocab) {
+    int n = 1;
+    while (n < MOST_BLOCKS && rows * n * 2 <= 2 * num_sms() && vocab >= 8192 * n) n *= 2;
+    return n;
 }
 
 template <int DT> cudaError_t run(const SampleArgs &a, cudaStream_t s) {
-    static int opted[64] = {0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!opted[dev]) {
-        e = cudaFuncSetAttribute(sample_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
-        if (e != cudaSuccess) return e;
-        opted[dev] = 1;
-    }
+    const int blocks = blocks_a_row(a.rows, a.vocab);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(a.rows));
+    cfg.gridDim = dim3(unsigned(a.rows * blocks));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(blocks), attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = blocks > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, sample_kernel<DT>, a);
 }
 
