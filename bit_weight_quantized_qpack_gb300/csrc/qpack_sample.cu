@@ -27,8 +27,7 @@ namespace {
 
 __device__ int g_fault_sample = 0;
 
-constexpr int THREADS = 512, WARPS = THREADS / 32;
-constexpr int BINS = 2048, PER = BINS / THREADS;
+constexpr int BINS = 2048;
 constexpr int CAP = 1024;       // tokens ranked among each other
 constexpr int MOST_BLOCKS = 8;  // a row's
 
@@ -60,7 +59,7 @@ struct Heat {
     int places;
 };
 // round(2^places e^{(x - top) / T}) for x <= top.
-template <int DT> __device__ __forceinline__ unsigned long long weight(const Heat &h, const float2 *pow2, float x) {
+__device__ __forceinline__ unsigned long long weight(const Heat &h, const float2 *pow2, float x) {
     // d = x - top in two floats, exactly; y = d log2(e) / T. Products and sums are written out, so that none is contracted.
     const float d = __fsub_rn(x, h.top);
     const float y = __fmul_rn(d, h.hi);
@@ -87,11 +86,14 @@ template <int DT> __device__ __forceinline__ unsigned long long weight(const Hea
     const float c = __fmul_rn(t.x, a), sum = __fadd_rn(t.x, c);
     const float low = __fadd_rn(__fmaf_rn(t.x, a, -c), __fmaf_rn(t.x, b, __fmaf_rn(t.y, a, t.y)));
     const float rest = __fadd_rn(__fsub_rn(c, __fsub_rn(sum, t.x)), low);
-    // in units of 2^-48: sum has 24 bits from 2^-1 or 2^0 on, |rest| < 2^-17
-    const long long fixed = (static_cast<long long>(__float2int_rn(sum * 0x1p30f)) << 18) + __float2int_rn(rest * 0x1p48f);
-    const int shift = 48 - h.places - n;                   // >= 2
-    if (shift >= 50) return 0;
-    return static_cast<unsigned long long>((fixed + (1ll << (shift - 1))) >> shift);
+    // (sum + rest) 2^e: sum's 24 bits (from 2^-1 or 2^0 on) are a whole number where e is 24 or more, |rest| 2^e is below 2^30;
+    // where e is less the sum of both is rounded at once
+    const int e = h.places + n;
+    const bool whole = e >= 24;
+    const float part = (whole ? 0.0f : sum) + rest;
+    const int low_part = __float2int_rn(part * __int_as_float((e + 127) << 23));
+    const unsigned high = whole ? unsigned(__float2int_rn(sum * 0x1p24f)) : 0u;
+    return static_cast<unsigned long long>(high) * (1u << (max(e, 24) - 24)) + static_cast<long long>(low_part);
 }
 
 // Logits as unsigned numbers of the same order (-0 counts as +0).
@@ -161,17 +163,24 @@ struct Shared {
     unsigned keys[CAP];         // of this block's tokens in the interval
     unsigned all_keys[CAP];     // of all blocks'
     unsigned long long weights[CAP];
-    unsigned long long scan64[WARPS];
-    unsigned scan32[WARPS];
+    unsigned long long scan64[32];
+    unsigned scan32[32];
     // what the blocks tell each other
-    unsigned long long best, sum, kept;
-    unsigned ties, listed, lo_key, hi_key;
+    unsigned long long sum, kept;
+    unsigned best, first, ties, listed, lo_key, hi_key;
     int bad;
     // what a thread tells its block
     int bin;
     unsigned found_key, found_ties;
     unsigned long long above;
 };
+
+// The largest of three; NaN where one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 struct Cluster {
     unsigned rank, size;
@@ -199,7 +208,7 @@ struct Cluster {
 };
 
 // Exclusive sums over the block; *total: the sum. Every thread calls it.
-template <class V> __device__ __forceinline__ V block_sum(V v, V *space, V *total) {
+template <int WARPS, class V> __device__ __forceinline__ V block_sum(V v, V *space, V *total) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     V x = v;
 #pragma unroll
@@ -226,6 +235,12 @@ struct Intervals {
     unsigned lo, hi;            // by key: lo <= key <= hi
     int shift;                  // < 0: by distance
     float floor;                // tokens below are in no interval
+    // Whether x is in interval `bin`, as of() has it.
+    __device__ __forceinline__ bool has(int bin, float x) const {
+        if (shift >= 0) return of(x) == bin;
+        const float at = (top - x) * per;
+        return x >= floor && x > -INFINITY && at >= float(bin) && (at < float(bin + 1) || bin == BINS - 1);
+    }
     __device__ __forceinline__ int of(float x) const {
         if (!(x >= floor) || x == -INFINITY) return -1;
         if (shift < 0) return int(fminf((top - x) * per, float(BINS - 1)));
@@ -235,15 +250,15 @@ struct Intervals {
 };
 
 // What a row's passes share.
-template <int DT> struct Row {
-    static constexpr int VE = Logits<DT>::VE;
+template <int DT, int THREADS> struct Row {
+    static constexpr int VE = Logits<DT>::VE, WARPS = THREADS / 32, PER = BINS / THREADS;
     Shared &s;
     const Cluster &c;
     Logits<DT> logits;
     int v0, v1;                 // this block's vectors
     Heat heat;
 
-    __device__ __forceinline__ unsigned long long weigh(float x) const { return weight<DT>(heat, s.pow2, x); }
+    __device__ __forceinline__ unsigned long long weigh(float x) const { return weight(heat, s.pow2, x); }
     // f(vector, its elements) over this block's vectors, two at a time for each thread
     template <class F> __device__ __forceinline__ void each(F f) const {
         int v = v0 + threadIdx.x;
@@ -308,7 +323,7 @@ template <int DT> struct Row {
                                      : c.read(&s.count[PER * tid + i], r);
                 sum += mine[i];
             }
-            unsigned long long at = above + block_sum(sum, s.scan64, &total);
+            unsigned long long at = above + block_sum<WARPS>(sum, s.scan64, &total);
             if (tid == 0) s.listed = 0, s.lo_key = 0xFFFFFFFFu, s.hi_key = 0;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
@@ -323,7 +338,7 @@ template <int DT> struct Row {
             each([&](int, const float (&x)[VE]) {
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    if (iv.of(x[e]) != bin || (WEIGH && least > 1 && weigh(x[e]) < least)) continue;
+                    if (!iv.has(bin, x[e]) || (WEIGH && least > 1 && weigh(x[e]) < least)) continue;
                     const unsigned k = key_of(x[e]);
                     lo = min(lo, k), hi = max(hi, k);
                     const unsigned n = atomicAdd(&s.listed, 1u);
@@ -381,17 +396,18 @@ template <int DT> struct Row {
     }
 };
 
-template <int DT> __global__ void __launch_bounds__(THREADS, 2) sample_kernel(SampleArgs a) {
+// THREADS: 512, two blocks an SM, where a row has one; 1024 where it has more, so that they lie on different SMs.
+template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(SampleArgs a) {
     __shared__ Shared s;
-    constexpr int VE = Logits<DT>::VE;
+    constexpr int VE = Logits<DT>::VE, WARPS = THREADS / 32, PER = BINS / THREADS;
     const Cluster c;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int64_t b = blockIdx.x / c.size;
     if (tid < STEPS) s.pow2[tid] = make_float2(g_pow2.hi[tid], g_pow2.lo[tid]);
-    if (tid == 0) s.best = 0, s.bad = 0, s.sum = 0;
+    if (tid == 0) s.best = 0, s.bad = 0, s.first = 0xFFFFFFFFu;
     pdl_launch_dependents();
     pdl_wait();
-    Row<DT> row = {s, c, Logits<DT>(static_cast<const unsigned char *>(a.logits) + b * a.ld * Logits<DT>::ES, int(a.vocab)), 0, 0, {}};
+    Row<DT, THREADS> row = {s, c, Logits<DT>(static_cast<const unsigned char *>(a.logits) + b * a.ld * Logits<DT>::ES, int(a.vocab)), 0, 0, {}};
     const int share = (row.logits.vectors + int(c.size) - 1) / int(c.size);
     row.v0 = min(int(c.rank) * share, row.logits.vectors), row.v1 = min(row.v0 + share, row.logits.vectors);
     const float given = a.temperature ? a.temperature[b] : 1.0f, heat_t = given > 0x1p64f ? 0x1p64f : given;
@@ -399,35 +415,38 @@ template <int DT> __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Sa
     const float p = a.top_p ? a.top_p[b] : 1.0f, min_p = a.min_p ? a.min_p[b] : 0.0f, u = fminf(fmaxf(a.u[b], 0.0f), 0x1.fffffep-1f);
     __syncthreads();
 
-    // -- the maximum, at its lowest index --------------------------------------------------------------------
-    unsigned long long best = 0;                           // key, then the index inverted
-    bool bad = false;
-    {
-        float top = -INFINITY;
-        int at = 0;
-        row.each([&](int v, const float (&x)[VE]) {
+    // -- the maximum ----------------------------------------------------------------------------------------------
+    float top = -INFINITY;
+    row.each([&](int, const float (&x)[VE]) {
 #pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                bad |= !(x[e] < INFINITY);                 // NaN or +inf
-                if (x[e] > top) top = x[e], at = row.logits.index(v) + e;      // a thread's indices rise
-            }
-        });
-        if (top > -INFINITY) best = static_cast<unsigned long long>(key_of(top)) << 32 | unsigned(~at);
-    }
+        for (int e = 0; e < VE; e += 2) top = max3_nan(top, x[e], x[e + 1]);
+    });
 #pragma unroll
-    for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-    bad = __any_sync(0xffffffffu, bad);
+    for (int o = 16; o; o >>= 1) top = max3_nan(top, top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) {
-        if (best) atomicMax(&s.best, best);
-        if (bad) s.bad = 1;
+        if (!(top < INFINITY)) s.bad = 1;
+        else if (top > -INFINITY) atomicMax(&s.best, key_of(top));
     }
     c.sync();
-    best = 0, bad = false;
+    unsigned best = 0;
+    bool bad = false;
     for (unsigned r = 0; r < c.size; ++r) best = max(best, c.read(&s.best, r)), bad |= c.read(&s.bad, r) != 0;
+    top = of_key(best);
     if (bad || best == 0 || !(heat_t >= 0x1p-64f)) {
+        // a token without a draw: none, or the lowest index of the maximum
+        if (!bad && best) {
+            row.each([&](int v, const float (&x)[VE]) {
+#pragma unroll
+                for (int e = VE - 1; e >= 0; --e)
+                    if (x[e] == top) atomicMin(&s.first, unsigned(row.logits.index(v) + e));
+            });
+            c.sync();
+        }
         if (tid == 0 && c.rank == 0) {
+            unsigned first = 0xFFFFFFFFu;
+            for (unsigned r = 0; r < c.size; ++r) first = min(first, c.read(&s.first, r));
             if (bad) atomicOr(&g_fault_sample, FAULT_NONFINITE_X);
-            a.tokens[b] = bad || best == 0 ? -1 : int(~unsigned(best));
+            a.tokens[b] = int(first);                      // -1 where there is none
             if (a.probs) a.probs[b] = bad ? __int_as_float(0x7FC00000) : best == 0 ? 0.0f : 1.0f;
         }
         if (c.size > 1) c.sync();                          // none leaves while another reads its memory
@@ -436,7 +455,7 @@ template <int DT> __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Sa
     {
         const double ratio = 1.4426950408889634 / double(heat_t);
         row.heat.hi = float(ratio), row.heat.lo = float(ratio - double(row.heat.hi));
-        row.heat.top = of_key(unsigned(best >> 32));
+        row.heat.top = top;
         row.heat.places = a.places;
     }
     const unsigned long long one = 1ull << a.places;
@@ -454,7 +473,7 @@ template <int DT> __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Sa
             c.sync();
             for (int i = 0; i < PER; ++i)
                 for (unsigned r = 0; r < c.size; ++r) mine += c.read(&s.count[PER * tid + i], r);
-            block_sum(mine, s.scan32, &total);
+            block_sum<WARPS>(mine, s.scan32, &total);
             cut_k = unsigned(k) < total;                   // masked tokens do not count
             if (cut_k) {
                 row.template select<false>(iv, unsigned(k), 0);
@@ -476,7 +495,7 @@ template <int DT> __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Sa
                         if (x[e] > last) sum += row.weigh(x[e]);
                 });
             }
-            block_sum(sum, s.scan64, &total);
+            block_sum<WARPS>(sum, s.scan64, &total);
             if (tid == 0) s.sum = total;
             c.sync();
             sum = 0;
@@ -502,22 +521,24 @@ template <int DT> __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Sa
     };
     unsigned long long sum = 0;
     unsigned ties = 0;
-    {
+    auto over = [&](auto one_token) {                      // two vectors at a time
         int v = v0 + lane;
         for (; v + 32 < v1; v += 64) {
             float x[VE], y[VE];
             row.logits.load(v, x);
             row.logits.load(v + 32, y);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) sum += kept(x[e], ties) + kept(y[e], ties);
+            for (int e = 0; e < VE; ++e) one_token(x[e]), one_token(y[e]);
         }
         if (v < v1) {
             float x[VE];
             row.logits.load(v, x);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) sum += kept(x[e], ties);
+            for (int e = 0; e < VE; ++e) one_token(x[e]);
         }
-    }
+    };
+    if (!last_ties && least == 1) over([&](float x) { sum += row.weigh(x); });
+    else over([&](float x) { sum += kept(x, ties); });
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     ties = __reduce_add_sync(0xffffffffu, ties);
@@ -602,12 +623,11 @@ template <int DT> __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Sa
 // Blocks a row: as many as keep the SMs busy, of 4096 tokens or more each.
 int blocks_a_row(int64_t rows, int64_t vocab) {
     int n = 1;
-    while (n < MOST_BLOCKS && rows * n * 2 <= 2 * num_sms() && vocab >= 8192 * n) n *= 2;
+    while (n < MOST_BLOCKS && rows * n * 2 <= num_sms() && vocab >= 8192 * n) n *= 2;
     return n;
 }
 
-template <int DT> cudaError_t run(const SampleArgs &a, cudaStream_t s) {
-    const int blocks = blocks_a_row(a.rows, a.vocab);
+template <int DT, int THREADS> cudaError_t run(const SampleArgs &a, int blocks, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(a.rows * blocks));
     cfg.blockDim = dim3(THREADS);
@@ -619,7 +639,11 @@ template <int DT> cudaError_t run(const SampleArgs &a, cudaStream_t s) {
     attr[1].val.clusterDim.x = unsigned(blocks), attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = blocks > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, sample_kernel<DT>, a);
+    return cudaLaunchKernelEx(&cfg, sample_kernel<DT, THREADS>, a);
+}
+template <int DT> cudaError_t run_type(const SampleArgs &a, cudaStream_t s) {
+    const int blocks = blocks_a_row(a.rows, a.vocab);
+    return blocks > 1 ? run<DT, 1024>(a, blocks, s) : run<DT, 512>(a, 1, s);
 }
 
 }  // namespace
@@ -628,7 +652,7 @@ cudaError_t launch_sample(SampleArgs a, cudaStream_t s) {
     int bits = 0;
     while ((int64_t(1) << bits) < a.vocab) ++bits;
     a.places = 62 - bits < 46 ? 62 - bits : 46;
-    return a.dt == DT_F32 ? run<DT_F32>(a, s) : a.dt == DT_F16 ? run<DT_F16>(a, s) : run<DT_BF16>(a, s);
+    return a.dt == DT_F32 ? run_type<DT_F32>(a, s) : a.dt == DT_F16 ? run_type<DT_F16>(a, s) : run_type<DT_BF16>(a, s);
 }
 
 cudaError_t fault_word_sample(int **word) {
