@@ -96,6 +96,12 @@ __device__ __forceinline__ unsigned long long weight(const Heat &h, const float2
     return static_cast<unsigned long long>(high) * (1u << (max(e, 24) - 24)) + static_cast<long long>(low_part);
 }
 
+// The same by a call, where few tokens are weighed: the kernel's code is read cold by every launch.
+__device__ __noinline__ unsigned long long weight_call(float hi, float lo, float top, int places, const float2 *pow2, float x) {
+    const Heat h = {hi, lo, top, places};
+    return weight(h, pow2, x);
+}
+
 // Logits as unsigned numbers of the same order (-0 counts as +0).
 __device__ __forceinline__ unsigned key_of(float x) {
     const unsigned u = __float_as_uint(x + 0.0f);
@@ -128,23 +134,33 @@ template <int DT> struct Logits {
         skew = int(p & 15) / ES, count = n, vectors = (skew + n + VE - 1) / VE;
     }
     __device__ __forceinline__ int index(int vec) const { return vec * VE - skew; }     // of its first element
-    __device__ __forceinline__ void load(int vec, float (&x)[VE]) const {
+    __device__ __forceinline__ bool inside(int vec) const { return vec >= (skew > 0) && vec < (skew + count) / VE; }
+    // A vector's words: loaded where all of it is the row's, -inf else; `patch` puts in what there is of the ends.
+    __device__ __forceinline__ uint4 words(int vec) const {
+        constexpr uint32_t none = DT == DT_F32 ? 0xFF800000u : DT == DT_F16 ? 0xFC00FC00u : 0xFF80FF80u;
+        uint4 v = make_uint4(none, none, none, none);
+        if (inside(vec)) v = *reinterpret_cast<const uint4 *>(base + int64_t(vec) * 16);
+        return v;
+    }
+    __device__ __forceinline__ void patch(int vec, float (&x)[VE]) const {
+        if (inside(vec) || vec >= vectors) return;
         const int i0 = index(vec);
-        if (vec < vectors && i0 >= 0 && i0 + VE <= count) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(base + int64_t(vec) * 16);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < VE; ++e) x[e] = value(w[e * ES / 4], e);
-            return;
-        }
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            x[e] = -INFINITY;
-            if (vec < vectors && i0 + e >= 0 && i0 + e < count) {
+        for (int e = 0; e < VE; ++e)
+            if (i0 + e >= 0 && i0 + e < count) {
                 const unsigned char *p = base + int64_t(vec) * 16 + e * ES;
-                x[e] = DT == DT_F32 ? *reinterpret_cast<const float *>(p) : value(*reinterpret_cast<const uint16_t *>(p), 0);
+                const float y = DT == DT_F32 ? *reinterpret_cast<const float *>(p) : value(*reinterpret_cast<const uint16_t *>(p), 0);
+#pragma unroll
+                for (int k = 0; k < VE; ++k) x[k] = k == e ? y : x[k];
             }
-        }
+    }
+    static __device__ __forceinline__ void widen(const uint4 &v, float (&x)[VE]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < VE; ++e) x[e] = value(w[e * ES / 4], e);
+    }
+    __device__ __forceinline__ void load(int vec, float (&x)[VE]) const {
+        widen(words(vec), x);
+        patch(vec, x);
     }
     // element e of the word that holds it
     static __device__ __forceinline__ float value(uint32_t w, int e) {
@@ -159,7 +175,8 @@ template <int DT> struct Logits {
 // ------------------------------------------------------------------------------------------------------------
 struct Shared {
     float2 pow2[STEPS];
-    unsigned count[BINS], w_lo[BINS], w_hi[BINS];
+    alignas(16) unsigned count[BINS];       // of the tokens in an interval,
+    alignas(16) uint2 sums[BINS];           // or their weights: low and high words
     unsigned keys[CAP];         // of this block's tokens in the interval
     unsigned all_keys[CAP];     // of all blocks'
     unsigned long long weights[CAP];
@@ -192,6 +209,13 @@ struct Cluster {
         if (size == 1) __syncthreads();
         else asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
+    __device__ __forceinline__ uint2 read2(const unsigned *p, unsigned r) const {       // aligned to 8 bytes
+        uint32_t at;
+        uint2 v;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(r));
+        asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+        return v;
+    }
     template <class V> __device__ __forceinline__ V read(const V *p, unsigned r) const {
         uint32_t at;
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(r));
@@ -219,13 +243,15 @@ template <int WARPS, class V> __device__ __forceinline__ V block_sum(V v, V *spa
     __syncthreads();
     if (lane == 31) space[w] = x;
     __syncthreads();
-    V before = 0, all = 0;
+    V y = lane < WARPS ? space[lane] : 0;                  // every warp adds up all of them
 #pragma unroll
-    for (int i = 0; i < WARPS; ++i) {
-        before += i < w ? space[i] : 0;
-        all += space[i];
+    for (int o = 1; o < WARPS; o <<= 1) {
+        const V z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
     }
-    *total = all;
+    *total = __shfl_sync(0xffffffffu, y, WARPS - 1);
+    V before = __shfl_sync(0xffffffffu, y, w ? w - 1 : 0);
+    if (w == 0) before = 0;
     return before + x - v;
 }
 
@@ -259,20 +285,22 @@ template <int DT, int THREADS> struct Row {
     Heat heat;
 
     __device__ __forceinline__ unsigned long long weigh(float x) const { return weight(heat, s.pow2, x); }
-    // f(vector, its elements) over this block's vectors, two at a time for each thread
+    __device__ __forceinline__ unsigned long long weigh_rare(float x) const { return weight_call(heat.hi, heat.lo, heat.top, heat.places, s.pow2, x); }
+    // f(vector, its elements) over this block's vectors, whose loads are under way together by 16 elements a thread: the passes
+    // behind the first read L2, and wait for it more than they compute.
+    static constexpr int FLIGHT = 16 / VE;
     template <class F> __device__ __forceinline__ void each(F f) const {
-        int v = v0 + threadIdx.x;
-        for (; v + THREADS < v1; v += 2 * THREADS) {
-            float x[VE], y[VE];
-            logits.load(v, x);
-            logits.load(v + THREADS, y);
-            f(v, x);
-            f(v + THREADS, y);
-        }
-        if (v < v1) {
-            float x[VE];
-            logits.load(v, x);
-            f(v, x);
+        for (int v = v0 + int(threadIdx.x); v < v1; v += FLIGHT * THREADS) {
+            uint4 raw[FLIGHT];
+#pragma unroll
+            for (int i = 0; i < FLIGHT; ++i) raw[i] = logits.words(v + i * THREADS < v1 ? v + i * THREADS : logits.vectors);
+#pragma unroll
+            for (int i = 0; i < FLIGHT; ++i) {
+                float x[VE];
+                Logits<DT>::widen(raw[i], x);
+                if (v + i * THREADS < v1) logits.patch(v + i * THREADS, x);
+                f(v + i * THREADS, x);
+            }
         }
     }
 
@@ -280,7 +308,7 @@ template <int DT, int THREADS> struct Row {
     // thread's sum of all weights.
     template <bool WEIGH> __device__ __forceinline__ unsigned long long fill(const Intervals &iv, unsigned long long least) {
         for (int i = threadIdx.x; i < BINS; i += THREADS) {
-            if (WEIGH) s.w_lo[i] = s.w_hi[i] = 0;
+            if (WEIGH) s.sums[i] = make_uint2(0, 0);
             else s.count[i] = 0;
         }
         __syncthreads();
@@ -294,11 +322,12 @@ template <int DT, int THREADS> struct Row {
                 } else if (x[e] >= iv.floor) {
                     const unsigned long long w = weigh(x[e]);
                     sum += w;
-                    const int b = w >= least ? iv.of(x[e]) : -1;
+                    if (w < least) continue;
+                    const int b = iv.of(x[e]);
                     if (b >= 0) {
-                        const unsigned lo = unsigned(w), old = atomicAdd(&s.w_lo[b], lo);
+                        const unsigned lo = unsigned(w), old = atomicAdd(&s.sums[b].x, lo);
                         const unsigned carry = unsigned(w >> 32) + (old + lo < old);
-                        if (carry) atomicAdd(&s.w_hi[b], carry);
+                        if (carry) atomicAdd(&s.sums[b].y, carry);
                     }
                 }
             }
@@ -306,23 +335,44 @@ template <int DT, int THREADS> struct Row {
         return sum;
     }
 
+    // The thread's intervals of all blocks: counts, or weights. All blocks' words are asked for before the first is added.
+    __device__ __forceinline__ void counts_of(unsigned long long (&n)[PER]) const {
+#pragma unroll
+        for (int i = 0; i < PER; i += 2) {
+            uint2 x[MOST_BLOCKS];
+#pragma unroll
+            for (unsigned r = 0; r < MOST_BLOCKS; ++r) x[r] = r < c.size ? c.read2(&s.count[PER * threadIdx.x + i], r) : make_uint2(0, 0);
+            n[i] = n[i + 1] = 0;
+#pragma unroll
+            for (unsigned r = 0; r < MOST_BLOCKS; ++r) n[i] += x[r].x, n[i + 1] += x[r].y;
+        }
+    }
+    __device__ __forceinline__ void weights_of(unsigned long long (&n)[PER]) const {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            uint2 x[MOST_BLOCKS];
+#pragma unroll
+            for (unsigned r = 0; r < MOST_BLOCKS; ++r) x[r] = r < c.size ? c.read2(&s.sums[PER * threadIdx.x + i].x, r) : make_uint2(0, 0);
+            n[i] = 0;
+#pragma unroll
+            for (unsigned r = 0; r < MOST_BLOCKS; ++r) n[i] += static_cast<unsigned long long>(x[r].y) << 32 | x[r].x;
+        }
+    }
+
     // Finds the token at which the running count (or weight) from the top reaches `goal`: its key, and how many of the tokens of
     // that key are kept (s.found_key, s.found_ties). The intervals are filled. Every thread of all blocks calls it.
-    template <bool WEIGH> __device__ __forceinline__ void select(Intervals iv, unsigned long long goal, unsigned long long least) {
+    // `apart`: the blocks have not met since.
+    template <bool WEIGH> __device__ __forceinline__ void select(Intervals iv, unsigned long long goal, unsigned long long least, bool apart) {
         const int tid = threadIdx.x;
         unsigned long long above = 0;                      // counts or weights above the intervals
-        for (;;) {
-            c.sync();
+        for (;; apart = true) {
+            if (apart) c.sync();
             // the interval that reaches the goal
             unsigned long long mine[PER], sum = 0, total;
+            if (WEIGH) weights_of(mine);
+            else counts_of(mine);
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                mine[i] = 0;
-                for (unsigned r = 0; r < c.size; ++r)
-                    mine[i] += WEIGH ? (static_cast<unsigned long long>(c.read(&s.w_hi[PER * tid + i], r)) << 32) + c.read(&s.w_lo[PER * tid + i], r)
-                                     : c.read(&s.count[PER * tid + i], r);
-                sum += mine[i];
-            }
+            for (int i = 0; i < PER; ++i) sum += mine[i];
             unsigned long long at = above + block_sum<WARPS>(sum, s.scan64, &total);
             if (tid == 0) s.listed = 0, s.lo_key = 0xFFFFFFFFu, s.hi_key = 0;
 #pragma unroll
@@ -338,7 +388,7 @@ template <int DT, int THREADS> struct Row {
             each([&](int, const float (&x)[VE]) {
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    if (!iv.has(bin, x[e]) || (WEIGH && least > 1 && weigh(x[e]) < least)) continue;
+                    if (!iv.has(bin, x[e]) || (WEIGH && least > 1 && weigh_rare(x[e]) < least)) continue;
                     const unsigned k = key_of(x[e]);
                     lo = min(lo, k), hi = max(hi, k);
                     const unsigned n = atomicAdd(&s.listed, 1u);
@@ -356,7 +406,7 @@ template <int DT, int THREADS> struct Row {
             }
             if (lo == hi) {                                // all alike
                 if (tid == 0) {
-                    const unsigned long long w = WEIGH ? weigh(of_key(lo)) : 1;
+                    const unsigned long long w = WEIGH ? weigh_rare(of_key(lo)) : 1;
                     s.found_key = lo, s.found_ties = unsigned((goal - above + w - 1) / w);
                 }
                 break;
@@ -368,7 +418,7 @@ template <int DT, int THREADS> struct Row {
                     for (unsigned i = tid; i < m; i += THREADS) {
                         const unsigned k = c.read(&s.keys[i], r);
                         s.all_keys[first + i] = k;
-                        if (WEIGH) s.weights[first + i] = weigh(of_key(k));
+                        if (WEIGH) s.weights[first + i] = weigh_rare(of_key(k));
                     }
                     first += m;
                 }
@@ -452,9 +502,10 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
         if (c.size > 1) c.sync();                          // none leaves while another reads its memory
         return;
     }
-    {
-        const double ratio = 1.4426950408889634 / double(heat_t);
-        row.heat.hi = float(ratio), row.heat.lo = float(ratio - double(row.heat.hi));
+    {                                                      // log2(e) / T in two floats: fp64 would take 4 us of a block's threads
+        constexpr float log2e_hi = 1.44269502162933349609375f, log2e_lo = 1.925963033500e-8f;
+        row.heat.hi = __fdiv_rn(log2e_hi, heat_t);
+        row.heat.lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-row.heat.hi, heat_t, log2e_hi), log2e_lo), heat_t);
         row.heat.top = top;
         row.heat.places = a.places;
     }
@@ -471,12 +522,14 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
             row.template fill<false>(iv, 0);
             unsigned total = 0, mine = 0;
             c.sync();
-            for (int i = 0; i < PER; ++i)
-                for (unsigned r = 0; r < c.size; ++r) mine += c.read(&s.count[PER * tid + i], r);
+            unsigned long long each_one[PER];
+            row.counts_of(each_one);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) mine += unsigned(each_one[i]);
             block_sum<WARPS>(mine, s.scan32, &total);
             cut_k = unsigned(k) < total;                   // masked tokens do not count
             if (cut_k) {
-                row.template select<false>(iv, unsigned(k), 0);
+                row.template select<false>(iv, unsigned(k), 0, false);
                 last = of_key(s.found_key), last_ties = s.found_ties;
                 iv.floor = last;
             }
@@ -492,7 +545,7 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
                 row.each([&](int, const float (&x)[VE]) {
 #pragma unroll
                     for (int e = 0; e < VE; ++e)
-                        if (x[e] > last) sum += row.weigh(x[e]);
+                        if (x[e] > last) sum += row.weigh_rare(x[e]);
                 });
             }
             block_sum<WARPS>(sum, s.scan64, &total);
@@ -500,13 +553,13 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
             c.sync();
             sum = 0;
             for (unsigned r = 0; r < c.size; ++r) sum += c.read(&s.sum, r);
-            if (cut_k) sum += last_ties * row.weigh(last);
-            row.template select<true>(iv, max(1ull, part_of(fmaxf(p, 0.0f), sum, true)), least);
+            if (cut_k) sum += last_ties * row.weigh_rare(last);
+            row.template select<true>(iv, max(1ull, part_of(fmaxf(p, 0.0f), sum, true)), least, false);
             last = of_key(s.found_key), last_ties = s.found_ties;
         }
     }
     const unsigned long long least = min_p >= 1.0f ? one : min_p > 0.0f ? max(1ull, part_of(min_p, one, true)) : 1ull;
-    const unsigned long long last_weight = last_ties ? row.weigh(last) : 0;
+    const unsigned long long last_weight = last_ties ? row.weigh_rare(last) : 0;
     const bool ties_count = last_weight >= least;
 
     // -- sums of kept weights by warps' shares of the block's vectors, in order of index ------------------------------
@@ -516,25 +569,25 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
             ties += x == last && last_ties;
             return 0;
         }
-        const unsigned long long y = row.weigh(x);
+        const unsigned long long y = row.weigh_rare(x);
         return y >= least ? y : 0;
     };
     unsigned long long sum = 0;
     unsigned ties = 0;
-    auto over = [&](auto one_token) {                      // two vectors at a time
-        int v = v0 + lane;
-        for (; v + 32 < v1; v += 64) {
-            float x[VE], y[VE];
-            row.logits.load(v, x);
-            row.logits.load(v + 32, y);
+    auto over = [&](auto one_token) {
+        constexpr int FLIGHT = Row<DT, THREADS>::FLIGHT;
+        for (int v = v0 + lane; v < v1; v += FLIGHT * 32) {
+            uint4 raw[FLIGHT];
 #pragma unroll
-            for (int e = 0; e < VE; ++e) one_token(x[e]), one_token(y[e]);
-        }
-        if (v < v1) {
-            float x[VE];
-            row.logits.load(v, x);
+            for (int i = 0; i < FLIGHT; ++i) raw[i] = row.logits.words(v + i * 32 < v1 ? v + i * 32 : row.logits.vectors);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) one_token(x[e]);
+            for (int i = 0; i < FLIGHT; ++i) {
+                float x[VE];
+                Logits<DT>::widen(raw[i], x);
+                if (v + i * 32 < v1) row.logits.patch(v + i * 32, x);
+#pragma unroll
+                for (int e = 0; e < VE; ++e) one_token(x[e]);
+            }
         }
     };
     if (!last_ties && least == 1) over([&](float x) { sum += row.weigh(x); });
