@@ -19,6 +19,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
+
 #include "qpack_dev.cuh"
 #include "qpack_launch.h"
 
@@ -147,11 +149,14 @@ template <int DT> struct Logits {
         const int i0 = index(vec);
         for (int e = 0; e < VE; ++e)
             if (i0 + e >= 0 && i0 + e < count) {
-                const unsigned char *p = base + int64_t(vec) * 16 + e * ES;
-                const float y = DT == DT_F32 ? *reinterpret_cast<const float *>(p) : value(*reinterpret_cast<const uint16_t *>(p), 0);
+                const float y = element(vec, e);
 #pragma unroll
                 for (int k = 0; k < VE; ++k) x[k] = k == e ? y : x[k];
             }
+    }
+    __device__ __forceinline__ float element(int vec, int e) const {           // one of the row's
+        const unsigned char *p = base + int64_t(vec) * 16 + e * ES;
+        return DT == DT_F32 ? *reinterpret_cast<const float *>(p) : value(*reinterpret_cast<const uint16_t *>(p), 0);
     }
     static __device__ __forceinline__ void widen(const uint4 &v, float (&x)[VE]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -261,12 +266,6 @@ struct Intervals {
     unsigned lo, hi;            // by key: lo <= key <= hi
     int shift;                  // < 0: by distance
     float floor;                // tokens below are in no interval
-    // Whether x is in interval `bin`, as of() has it.
-    __device__ __forceinline__ bool has(int bin, float x) const {
-        if (shift >= 0) return of(x) == bin;
-        const float at = (top - x) * per;
-        return x >= floor && x > -INFINITY && at >= float(bin) && (at < float(bin + 1) || bin == BINS - 1);
-    }
     __device__ __forceinline__ int of(float x) const {
         if (!(x >= floor) || x == -INFINITY) return -1;
         if (shift < 0) return int(fminf((top - x) * per, float(BINS - 1)));
@@ -286,26 +285,49 @@ template <int DT, int THREADS> struct Row {
 
     __device__ __forceinline__ unsigned long long weigh(float x) const { return weight(heat, s.pow2, x); }
     __device__ __forceinline__ unsigned long long weigh_rare(float x) const { return weight_call(heat.hi, heat.lo, heat.top, heat.places, s.pow2, x); }
-    // f(vector, its elements) over this block's vectors, whose loads are under way together by 16 elements a thread: the passes
-    // behind the first read L2, and wait for it more than they compute.
+    // 16 elements a thread and pass, whose loads are under way together: the passes behind the first read L2, and wait for it
+    // more than they compute.
     static constexpr int FLIGHT = 16 / VE;
-    template <class F> __device__ __forceinline__ void each(F f) const {
-        for (int v = v0 + int(threadIdx.x); v < v1; v += FLIGHT * THREADS) {
+    // batch(first vector, elements): from vector v on, `step` apart, to `end`
+    template <class B> __device__ __forceinline__ void batches(int v, int step, int end, B batch) const {
+        for (; v < end; v += FLIGHT * step) {
             uint4 raw[FLIGHT];
 #pragma unroll
-            for (int i = 0; i < FLIGHT; ++i) raw[i] = logits.words(v + i * THREADS < v1 ? v + i * THREADS : logits.vectors);
+            for (int i = 0; i < FLIGHT; ++i) raw[i] = logits.words(v + i * step < end ? v + i * step : logits.vectors);
+            float x[FLIGHT][VE];
 #pragma unroll
             for (int i = 0; i < FLIGHT; ++i) {
-                float x[VE];
-                Logits<DT>::widen(raw[i], x);
-                if (v + i * THREADS < v1) logits.patch(v + i * THREADS, x);
-                f(v + i * THREADS, x);
+                Logits<DT>::widen(raw[i], x[i]);
+                if (v + i * step < end) logits.patch(v + i * step, x[i]);
             }
+            batch(v, x);
+        }
+    }
+    template <class F> __device__ __forceinline__ void each(F f) const {
+        batches(v0 + int(threadIdx.x), THREADS, v1, [&](int, const float (&x)[FLIGHT][VE]) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f(x[i / VE][i % VE]);
+        });
+    }
+    // The elements of a batch that are at or above a limit, as bits.
+    static __device__ __forceinline__ unsigned reach(float limit, const float (&x)[FLIGHT][VE]) {
+        unsigned m = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m |= x[i / VE][i % VE] >= limit ? 1u << i : 0u;
+        return m;
+    }
+    // f(vector, element of it, x) of those elements, one after the other: few of many are looked at, and a branch an element
+    // cost more than all else
+    template <class F> __device__ __forceinline__ void pick(unsigned m, int v, int step, F f) const {
+        while (m) {
+            const int i = __ffs(m) - 1, vec = v + i / VE * step;
+            m &= m - 1;
+            f(vec, i % VE, logits.element(vec, i % VE));
         }
     }
 
     // Counts the intervals' tokens, or (WEIGH) adds up their weights, of which those below `least` are left out. Returns the
-    // thread's sum of all weights.
+    // thread's sum of all weights above iv.floor.
     template <bool WEIGH> __device__ __forceinline__ unsigned long long fill(const Intervals &iv, unsigned long long least) {
         for (int i = threadIdx.x; i < BINS; i += THREADS) {
             if (WEIGH) s.sums[i] = make_uint2(0, 0);
@@ -313,25 +335,33 @@ template <int DT, int THREADS> struct Row {
         }
         __syncthreads();
         unsigned long long sum = 0;
-        each([&](int, const float (&x)[VE]) {
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                if (!WEIGH) {
-                    const int b = iv.of(x[e]);
-                    if (b >= 0) atomicAdd(&s.count[b], 1u);
-                } else if (x[e] >= iv.floor) {
-                    const unsigned long long w = weigh(x[e]);
-                    sum += w;
-                    if (w < least) continue;
-                    const int b = iv.of(x[e]);
-                    if (b >= 0) {
-                        const unsigned lo = unsigned(w), old = atomicAdd(&s.sums[b].x, lo);
-                        const unsigned carry = unsigned(w >> 32) + (old + lo < old);
-                        if (carry) atomicAdd(&s.sums[b].y, carry);
-                    }
-                }
-            }
-        });
+        auto put = [&](float x, unsigned long long w) {
+            const int b = iv.of(x);
+            if (b < 0) return;
+            const unsigned lo = unsigned(w), old = atomicAdd(&s.sums[b].x, lo);
+            const unsigned carry = unsigned(w >> 32) + (old + lo < old);
+            if (carry) atomicAdd(&s.sums[b].y, carry);
+        };
+        if (!WEIGH) {
+            each([&](float x) {
+                const int b = iv.of(x);
+                if (b >= 0) atomicAdd(&s.count[b], 1u);
+            });
+        } else if (iv.floor == -INFINITY) {
+            each([&](float x) {
+                const unsigned long long w = weigh(x);
+                sum += w;
+                if (w >= least) put(x, w);
+            });
+        } else {                                           // few are left
+            batches(v0 + int(threadIdx.x), THREADS, v1, [&](int v, const float (&x)[FLIGHT][VE]) {
+                pick(reach(iv.floor, x), v, THREADS, [&](int, int, float y) {
+                    const unsigned long long w = weigh_rare(y);
+                    if (y > iv.floor) sum += w;
+                    if (w >= least) put(y, w);
+                });
+            });
+        }
         return sum;
     }
 
@@ -385,15 +415,16 @@ template <int DT, int THREADS> struct Row {
             above = s.above;
             // its tokens
             unsigned lo = 0xFFFFFFFFu, hi = 0;
-            each([&](int, const float (&x)[VE]) {
-#pragma unroll
-                for (int e = 0; e < VE; ++e) {
-                    if (!iv.has(bin, x[e]) || (WEIGH && least > 1 && weigh_rare(x[e]) < least)) continue;
-                    const unsigned k = key_of(x[e]);
+            // (a little below the interval's lower end: of() decides)
+            const float from = iv.shift >= 0 ? of_key(iv.lo) : bin == BINS - 1 ? -FLT_MAX : iv.top - float(bin + 2) / iv.per;
+            batches(v0 + tid, THREADS, v1, [&](int v, const float (&x)[FLIGHT][VE]) {
+                pick(reach(fmaxf(from, iv.floor), x), v, THREADS, [&](int, int, float y) {
+                    if (iv.of(y) != bin || (WEIGH && least > 1 && weigh_rare(y) < least)) return;
+                    const unsigned k = key_of(y);
                     lo = min(lo, k), hi = max(hi, k);
                     const unsigned n = atomicAdd(&s.listed, 1u);
                     if (n < CAP) s.keys[n] = k;
-                }
+                });
             });
             lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
             if ((tid & 31) == 0) atomicMin(&s.lo_key, lo), atomicMax(&s.hi_key, hi);
@@ -467,9 +498,9 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
 
     // -- the maximum ----------------------------------------------------------------------------------------------
     float top = -INFINITY;
-    row.each([&](int, const float (&x)[VE]) {
+    row.batches(row.v0 + tid, THREADS, row.v1, [&](int, const float (&x)[Row<DT, THREADS>::FLIGHT][VE]) {
 #pragma unroll
-        for (int e = 0; e < VE; e += 2) top = max3_nan(top, x[e], x[e + 1]);
+        for (int i = 0; i < 16; i += 2) top = max3_nan(top, x[i / VE][i % VE], x[i / VE][i % VE + 1]);
     });
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = max3_nan(top, top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -485,10 +516,8 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
     if (bad || best == 0 || !(heat_t >= 0x1p-64f)) {
         // a token without a draw: none, or the lowest index of the maximum
         if (!bad && best) {
-            row.each([&](int v, const float (&x)[VE]) {
-#pragma unroll
-                for (int e = VE - 1; e >= 0; --e)
-                    if (x[e] == top) atomicMin(&s.first, unsigned(row.logits.index(v) + e));
+            row.batches(row.v0 + tid, THREADS, row.v1, [&](int v, const float (&x)[Row<DT, THREADS>::FLIGHT][VE]) {
+                row.pick(row.reach(top, x), v, THREADS, [&](int vec, int e, float) { atomicMin(&s.first, unsigned(row.logits.index(vec) + e)); });
             });
             c.sync();
         }
@@ -540,20 +569,12 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
             // are left out.
             const unsigned long long least = max(1ull, part_of(fminf((1.0f - fmaxf(p, 0.0f)) * 0.5f, 0.5f), one, false) / a.vocab);
             unsigned long long sum = row.template fill<true>(iv, least), total;
-            if (cut_k) {                                   // of the last one's equals only those kept
-                sum = 0;
-                row.each([&](int, const float (&x)[VE]) {
-#pragma unroll
-                    for (int e = 0; e < VE; ++e)
-                        if (x[e] > last) sum += row.weigh_rare(x[e]);
-                });
-            }
             block_sum<WARPS>(sum, s.scan64, &total);
             if (tid == 0) s.sum = total;
             c.sync();
             sum = 0;
             for (unsigned r = 0; r < c.size; ++r) sum += c.read(&s.sum, r);
-            if (cut_k) sum += last_ties * row.weigh_rare(last);
+            if (cut_k) sum += last_ties * row.weigh_rare(last);    // of the last one's equals those kept
             row.template select<true>(iv, max(1ull, part_of(fmaxf(p, 0.0f), sum, true)), least, false);
             last = of_key(s.found_key), last_ties = s.found_ties;
         }
@@ -574,24 +595,21 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
     };
     unsigned long long sum = 0;
     unsigned ties = 0;
-    auto over = [&](auto one_token) {
-        constexpr int FLIGHT = Row<DT, THREADS>::FLIGHT;
-        for (int v = v0 + lane; v < v1; v += FLIGHT * 32) {
-            uint4 raw[FLIGHT];
+    const bool all = !last_ties && least == 1;
+    row.batches(v0 + lane, 32, v1, [&](int v, const float (&x)[Row<DT, THREADS>::FLIGHT][VE]) {
+        const unsigned m = all ? 0xFFFFu : row.reach(last, x);
+        if (all || __any_sync(__activemask(), __popc(m) > 4)) {        // many: all of them, without a branch each
 #pragma unroll
-            for (int i = 0; i < FLIGHT; ++i) raw[i] = row.logits.words(v + i * 32 < v1 ? v + i * 32 : row.logits.vectors);
-#pragma unroll
-            for (int i = 0; i < FLIGHT; ++i) {
-                float x[VE];
-                Logits<DT>::widen(raw[i], x);
-                if (v + i * 32 < v1) row.logits.patch(v + i * 32, x);
-#pragma unroll
-                for (int e = 0; e < VE; ++e) one_token(x[e]);
+            for (int i = 0; i < 16; ++i) {
+                const float y = x[i / VE][i % VE];
+                const unsigned long long z = row.weigh(y);
+                ties += y == last && last_ties;
+                sum += (y > last || all) && z >= least ? z : 0;
             }
+        } else {
+            row.pick(m, v, 32, [&](int, int, float y) { sum += kept(y, ties); });
         }
-    };
-    if (!last_ties && least == 1) over([&](float x) { sum += row.weigh(x); });
-    else over([&](float x) { sum += kept(x, ties); });
+    });
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     ties = __reduce_add_sync(0xffffffffu, ties);
