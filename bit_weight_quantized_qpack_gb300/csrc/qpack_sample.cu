@@ -53,7 +53,7 @@ constexpr Pow2Table make_pow2_table() {
     }
     return t;
 }
-__device__ const Pow2Table g_pow2 = make_pow2_table();
+__device__ const __align__(16) Pow2Table g_pow2 = make_pow2_table();
 
 // log2(e) / T in two fp32, the row's maximum, and the binary places of a weight.
 struct Heat {
@@ -61,11 +61,10 @@ struct Heat {
     int places;
 };
 // round(2^places e^{(x - top) / T}) for x <= top.
-__device__ __forceinline__ unsigned long long weight(const Heat &h, const float2 *pow2, float x) {
+__device__ __forceinline__ unsigned long long weight(const Heat &h, const float *pow2, float x) {
     // d = x - top in two floats, exactly; y = d log2(e) / T. Products and sums are written out, so that none is contracted.
     const float d = __fsub_rn(x, h.top);
-    const float y = __fmul_rn(d, h.hi);
-    if (!(y > -48.0f)) return 0;                           // below half of a weight's last place; x = -inf
+    const float full = __fmul_rn(d, h.hi), y = fmaxf(full, -60.0f);
     float tail = __fmul_rn(d, h.lo);
     const float v = __fsub_rn(d, x);
     tail = __fmaf_rn(__fsub_rn(__fsub_rn(x, __fsub_rn(d, v)), __fadd_rn(h.top, v)), h.hi, tail);
@@ -75,7 +74,8 @@ __device__ __forceinline__ unsigned long long weight(const Heat &h, const float2
     const float shifted = __fadd_rn(y, magic);
     const float r = __fsub_rn(y, __fsub_rn(shifted, magic));
     const int nj = __float_as_int(shifted) - __float_as_int(magic);
-    const float2 t = pow2[nj & (STEPS - 1)];
+    const float *entry = pow2 + (nj & (STEPS - 1)) * 32;
+    const float2 t = make_float2(entry[0], entry[STEPS * 32]);
     const int n = (nj + STEPS / 2) >> 8;
     // 2^(r + y_lo) - 1 = a + b: ln2 z + ln2^2 / 2 z^2 + ln2^3 / 6 z^3, |z| < 2^-8.9; the next term is below 2^-42
     constexpr float ln2_hi = 0.693147182464599609375f, ln2_lo = -1.904654299957767e-9f;
@@ -93,13 +93,14 @@ __device__ __forceinline__ unsigned long long weight(const Heat &h, const float2
     const int e = h.places + n;
     const bool whole = e >= 24;
     const float part = (whole ? 0.0f : sum) + rest;
-    const int low_part = __float2int_rn(part * __int_as_float((e + 127) << 23));
+    // (below half of a weight's last place, x = -inf too: 0, since a NaN converts to it)
+    const int low_part = __float2int_rn(part * (full > -48.0f ? __int_as_float((e + 127) << 23) : __int_as_float(0x7FC00000)));
     const unsigned high = whole ? unsigned(__float2int_rn(sum * 0x1p24f)) : 0u;
     return static_cast<unsigned long long>(high) * (1u << (max(e, 24) - 24)) + static_cast<long long>(low_part);
 }
 
 // The same by a call, where few tokens are weighed: the kernel's code is read cold by every launch.
-__device__ __noinline__ unsigned long long weight_call(float hi, float lo, float top, int places, const float2 *pow2, float x) {
+__device__ __noinline__ unsigned long long weight_call(float hi, float lo, float top, int places, const float *pow2, float x) {
     const Heat h = {hi, lo, top, places};
     return weight(h, pow2, x);
 }
@@ -179,7 +180,7 @@ template <int DT> struct Logits {
 // The kernel: one to eight blocks a row, which read each other's shared memory
 // ------------------------------------------------------------------------------------------------------------
 struct Shared {
-    float2 pow2[STEPS];
+    float pow2[2][STEPS][32];   // high and low parts, once for each lane's bank: lanes ask for entries at random
     alignas(16) unsigned count[BINS];       // of the tokens in an interval,
     alignas(16) uint2 sums[BINS];           // or their weights: low and high words
     unsigned keys[CAP];         // of this block's tokens in the interval
@@ -192,7 +193,7 @@ struct Shared {
     unsigned best, first, ties, listed, lo_key, hi_key;
     int bad;
     // what a thread tells its block
-    int bin;
+    int bin, share;
     unsigned found_key, found_ties;
     unsigned long long above;
 };
@@ -282,9 +283,10 @@ template <int DT, int THREADS> struct Row {
     Logits<DT> logits;
     int v0, v1;                 // this block's vectors
     Heat heat;
+    const float *pow2;          // the lane's table
 
-    __device__ __forceinline__ unsigned long long weigh(float x) const { return weight(heat, s.pow2, x); }
-    __device__ __forceinline__ unsigned long long weigh_rare(float x) const { return weight_call(heat.hi, heat.lo, heat.top, heat.places, s.pow2, x); }
+    __device__ __forceinline__ unsigned long long weigh(float x) const { return weight(heat, pow2, x); }
+    __device__ __forceinline__ unsigned long long weigh_rare(float x) const { return weight_call(heat.hi, heat.lo, heat.top, heat.places, pow2, x); }
     // 16 elements a thread and pass, whose loads are under way together: the passes behind the first read L2, and wait for it
     // more than they compute.
     static constexpr int FLIGHT = 16 / VE;
@@ -309,11 +311,11 @@ template <int DT, int THREADS> struct Row {
             for (int i = 0; i < 16; ++i) f(x[i / VE][i % VE]);
         });
     }
-    // The elements of a batch that are at or above a limit, as bits.
-    static __device__ __forceinline__ unsigned reach(float limit, const float (&x)[FLIGHT][VE]) {
+    // The elements of a batch that are at or above a limit, and not above another, as bits.
+    static __device__ __forceinline__ unsigned reach(float limit, const float (&x)[FLIGHT][VE], float most = INFINITY) {
         unsigned m = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m |= x[i / VE][i % VE] >= limit ? 1u << i : 0u;
+        for (int i = 0; i < 16; ++i) m |= x[i / VE][i % VE] >= limit && x[i / VE][i % VE] <= most ? 1u << i : 0u;
         return m;
     }
     // f(vector, element of it, x) of those elements, one after the other: few of many are looked at, and a branch an element
@@ -415,10 +417,11 @@ template <int DT, int THREADS> struct Row {
             above = s.above;
             // its tokens
             unsigned lo = 0xFFFFFFFFu, hi = 0;
-            // (a little below the interval's lower end: of() decides)
+            // (a little outside the interval's ends: of() decides)
             const float from = iv.shift >= 0 ? of_key(iv.lo) : bin == BINS - 1 ? -FLT_MAX : iv.top - float(bin + 2) / iv.per;
+            const float to = iv.shift >= 0 ? of_key(iv.hi) : iv.top - float(bin - 1) / iv.per;
             batches(v0 + tid, THREADS, v1, [&](int v, const float (&x)[FLIGHT][VE]) {
-                pick(reach(fmaxf(from, iv.floor), x), v, THREADS, [&](int, int, float y) {
+                pick(reach(fmaxf(from, iv.floor), x, to), v, THREADS, [&](int, int, float y) {
                     if (iv.of(y) != bin || (WEIGH && least > 1 && weigh_rare(y) < least)) return;
                     const unsigned k = key_of(y);
                     lo = min(lo, k), hi = max(hi, k);
@@ -458,6 +461,7 @@ template <int DT, int THREADS> struct Row {
                     const unsigned k = s.all_keys[t];
                     unsigned long long over = above;
                     unsigned same = 0;
+#pragma unroll 8
                     for (unsigned i = 0; i < n; ++i) {
                         const unsigned o = s.all_keys[i];
                         if (o > k) over += WEIGH ? s.weights[i] : 1;
@@ -479,16 +483,21 @@ template <int DT, int THREADS> struct Row {
 
 // THREADS: 512, two blocks an SM, where a row has one; 1024 where it has more, so that they lie on different SMs.
 template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(SampleArgs a) {
-    __shared__ Shared s;
+    extern __shared__ __align__(16) unsigned char smem[];
+    Shared &s = *reinterpret_cast<Shared *>(smem);
     constexpr int VE = Logits<DT>::VE, WARPS = THREADS / 32, PER = BINS / THREADS;
     const Cluster c;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int64_t b = blockIdx.x / c.size;
-    if (tid < STEPS) s.pow2[tid] = make_float2(g_pow2.hi[tid], g_pow2.lo[tid]);
-    if (tid == 0) s.best = 0, s.bad = 0, s.first = 0xFFFFFFFFu;
+    for (int i = w; i < 2 * STEPS / 4; i += WARPS) {       // a warp four entries: a lane a copy
+        const float4 t = reinterpret_cast<const float4 *>(&g_pow2)[i];
+        float *to = &s.pow2[0][0][0] + i * 128 + lane;
+        to[0] = t.x, to[32] = t.y, to[64] = t.z, to[96] = t.w;
+    }
+    if (tid == 0) s.best = 0, s.bad = 0, s.first = 0xFFFFFFFFu, s.share = -1;
     pdl_launch_dependents();
     pdl_wait();
-    Row<DT, THREADS> row = {s, c, Logits<DT>(static_cast<const unsigned char *>(a.logits) + b * a.ld * Logits<DT>::ES, int(a.vocab)), 0, 0, {}};
+    Row<DT, THREADS> row = {s, c, Logits<DT>(static_cast<const unsigned char *>(a.logits) + b * a.ld * Logits<DT>::ES, int(a.vocab)), 0, 0, {}, &s.pow2[0][0][lane]};
     const int share = (row.logits.vectors + int(c.size) - 1) / int(c.size);
     row.v0 = min(int(c.rank) * share, row.logits.vectors), row.v1 = min(row.v0 + share, row.logits.vectors);
     const float given = a.temperature ? a.temperature[b] : 1.0f, heat_t = given > 0x1p64f ? 0x1p64f : given;
@@ -644,47 +653,40 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
         total += add, all_ties += here;
     }
     const unsigned long long goal = part_of(u, total, false);
-    if (goal >= before && goal < before + mine) {          // one warp's
-        unsigned left = last_ties - min(ties_before, last_ties);
-        unsigned long long run = before;
-        for (int v = v0; v < v1; v += 32) {
+    if (lane == 0 && goal >= before && goal < before + mine)       // one warp's
+        s.share = w, s.above = before, s.found_ties = ties_before;
+    __syncthreads();
+    if (const int holder = s.share; holder >= 0) {         // the block looks through the warp's share together
+        unsigned left = last_ties - min(s.found_ties, last_ties);
+        unsigned long long run = s.above;
+        const int from = row.v0 + holder * per, to = min(from + per, row.v1);
+        for (int v = from; v < to; v += THREADS) {
             float x[VE];
-            row.logits.load(v + lane < v1 ? v + lane : row.logits.vectors, x);
-            unsigned t = 0;
-            unsigned long long here = 0;
+            row.logits.load(v + tid < to ? v + tid : row.logits.vectors, x);
+            unsigned t = 0, t_all;
+            unsigned long long here = 0, all_here;
 #pragma unroll
             for (int e = 0; e < VE; ++e) here += kept(x[e], t);
-            unsigned t_scan = t;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned y = __shfl_up_sync(0xffffffffu, t_scan, o);
-                if (lane >= o) t_scan += y;
-            }
-            unsigned may = left - min(left, t_scan - t);   // ties that this lane may keep
+            const unsigned t_before = block_sum<WARPS>(t, s.scan32, &t_all);
+            unsigned may = left - min(left, t_before);     // ties that this thread may keep
             here += ties_count ? min(t, may) * last_weight : 0;
-            unsigned long long scan = here;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned long long y = __shfl_up_sync(0xffffffffu, scan, o);
-                if (lane >= o) scan += y;
-            }
-            const unsigned long long end = run + scan;
-            if (goal >= end - here && goal < end) {
-                unsigned long long at = end - here;
+            const unsigned long long start = run + block_sum<WARPS>(here, s.scan64, &all_here);
+            if (goal >= start && goal < start + here) {
+                unsigned long long at = start;
                 for (int e = 0; e < VE; ++e) {
                     unsigned tie = 0;
                     unsigned long long y = kept(x[e], tie);
                     if (tie && may) y = ties_count ? last_weight : 0, --may;
                     if (goal < at + y) {
-                        a.tokens[b] = row.logits.index(v + lane) + e;
+                        a.tokens[b] = row.logits.index(v + tid) + e;
                         if (a.probs) a.probs[b] = float(double(y) / double(total));
                         break;
                     }
                     at += y;
                 }
             }
-            run += __shfl_sync(0xffffffffu, scan, 31);
-            left -= min(left, __shfl_sync(0xffffffffu, t_scan, 31));
+            run += all_here;
+            left -= min(left, t_all);
             if (goal < run) break;
         }
     }
@@ -699,9 +701,20 @@ int blocks_a_row(int64_t rows, int64_t vocab) {
 }
 
 template <int DT, int THREADS> cudaError_t run(const SampleArgs &a, int blocks, cudaStream_t s) {
+    static int opted[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!opted[dev]) {
+        e = cudaFuncSetAttribute(sample_kernel<DT, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+        if (e != cudaSuccess) return e;
+        opted[dev] = 1;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(a.rows * blocks));
     cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
