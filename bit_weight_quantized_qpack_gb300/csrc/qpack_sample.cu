@@ -222,6 +222,11 @@ struct Cluster {
         asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
         return v;
     }
+    // A word of block `lane`, or `none`: a warp asks all blocks at once (a loop over them waits for each).
+    template <class V> __device__ __forceinline__ V read_lane(const V *p, V none) const {
+        const unsigned r = threadIdx.x & 31;
+        return r < size ? read(p, r) : none;
+    }
     template <class V> __device__ __forceinline__ V read(const V *p, unsigned r) const {
         uint32_t at;
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(r));
@@ -432,12 +437,9 @@ template <int DT, int THREADS> struct Row {
             lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
             if ((tid & 31) == 0) atomicMin(&s.lo_key, lo), atomicMax(&s.hi_key, hi);
             c.sync();
-            unsigned n = 0;
-            lo = 0xFFFFFFFFu, hi = 0;
-            for (unsigned r = 0; r < c.size; ++r) {
-                n += c.read(&s.listed, r);
-                lo = min(lo, c.read(&s.lo_key, r)), hi = max(hi, c.read(&s.hi_key, r));
-            }
+            const unsigned listed = c.read_lane(&s.listed, 0u), n = __reduce_add_sync(0xffffffffu, listed);
+            lo = __reduce_min_sync(0xffffffffu, c.read_lane(&s.lo_key, 0xFFFFFFFFu));
+            hi = __reduce_max_sync(0xffffffffu, c.read_lane(&s.hi_key, 0u));
             if (lo == hi) {                                // all alike
                 if (tid == 0) {
                     const unsigned long long w = WEIGH ? weigh_rare(of_key(lo)) : 1;
@@ -448,7 +450,7 @@ template <int DT, int THREADS> struct Row {
             if (n <= CAP) {
                 unsigned first = 0;
                 for (unsigned r = 0; r < c.size; ++r) {
-                    const unsigned m = c.read(&s.listed, r);
+                    const unsigned m = __shfl_sync(0xffffffffu, listed, r);
                     for (unsigned i = tid; i < m; i += THREADS) {
                         const unsigned k = c.read(&s.keys[i], r);
                         s.all_keys[first + i] = k;
@@ -518,9 +520,8 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
         else if (top > -INFINITY) atomicMax(&s.best, key_of(top));
     }
     c.sync();
-    unsigned best = 0;
-    bool bad = false;
-    for (unsigned r = 0; r < c.size; ++r) best = max(best, c.read(&s.best, r)), bad |= c.read(&s.bad, r) != 0;
+    const unsigned best = __reduce_max_sync(0xffffffffu, c.read_lane(&s.best, 0u));
+    const bool bad = __any_sync(0xffffffffu, c.read_lane(&s.bad, 0) != 0);
     top = of_key(best);
     if (bad || best == 0 || !(heat_t >= 0x1p-64f)) {
         // a token without a draw: none, or the lowest index of the maximum
@@ -581,8 +582,10 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
             block_sum<WARPS>(sum, s.scan64, &total);
             if (tid == 0) s.sum = total;
             c.sync();
-            sum = 0;
-            for (unsigned r = 0; r < c.size; ++r) sum += c.read(&s.sum, r);
+            sum = c.read_lane(&s.sum, 0ull);
+#pragma unroll
+            for (int o = MOST_BLOCKS / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            sum = __shfl_sync(0xffffffffu, sum, 0);
             if (cut_k) sum += last_ties * row.weigh_rare(last);    // of the last one's equals those kept
             row.template select<true>(iv, max(1ull, part_of(fmaxf(p, 0.0f), sum, true)), least, false);
             last = of_key(s.found_key), last_ties = s.found_ties;
@@ -635,9 +638,11 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
     // kept weights before this warp's share, and in all
     unsigned long long before = 0, total = 0, mine = 0;
     unsigned ties_before = 0, all_ties = 0;
+    const unsigned long long sums = c.read_lane(&s.kept, 0ull);
+    const unsigned equals = c.read_lane(&s.ties, 0u);
     for (unsigned r = 0; r < c.size; ++r) {
-        const unsigned here = c.read(&s.ties, r), may = last_ties - min(all_ties, last_ties);
-        const unsigned long long add = c.read(&s.kept, r) + (ties_count ? min(here, may) * last_weight : 0);
+        const unsigned here = __shfl_sync(0xffffffffu, equals, r), may = last_ties - min(all_ties, last_ties);
+        const unsigned long long add = __shfl_sync(0xffffffffu, sums, r) + (ties_count ? min(here, may) * last_weight : 0);
         if (r == c.rank) {
             before = total, ties_before = all_ties;
             for (int i = 0; i < WARPS; ++i) {
