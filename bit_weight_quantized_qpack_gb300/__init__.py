@@ -11,6 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -606,13 +607,14 @@ def qpack_kv_attend_shared(pool, layer, tables, q, first, prefix, seqs=None, sca
     if lse is not None:
         _need(lse, torch.float32, "lse", numel=B * q_heads)
     rows = _need_rope(rope, D)
-    _here(stream, pool.k, tables.lens, q, first, prefix, out, lse, seqs, rope)
+    dev = _device(stream)
+    _at(pool.k, dev), _at(tables.lens, dev)
     if workspace is None:
         with _on(stream):
             workspace = alloc_kv_shared_workspace(pool, B, q_heads)
-    rc = (_lib or lib()).qpack_kv_attend_shared(pool._ref, layer, tables._ref, _addr(seqs), B, _addr(first), _addr(prefix),
-                                                groups, _addr(q), qdt, ldq, q_heads, D ** -0.5 if scale is None else scale,
-                                                _addr(rope), rows, _addr(out), odt, ldo, _addr(lse), workspace._p,
+    rc = (_lib or lib()).qpack_kv_attend_shared(pool._ref, layer, tables._ref, _at(seqs, dev), B, _at(first, dev), _at(prefix, dev),
+                                                groups, _at(q, dev), qdt, ldq, q_heads, D ** -0.5 if scale is None else scale,
+                                                _at(rope, dev), rows, _at(out, dev), odt, ldo, _at(lse, dev), workspace._p,
                                                 workspace.bytes, _raw_stream(stream))
     if rc:
         _check(rc, "qpack_kv_attend_shared")
@@ -697,18 +699,27 @@ class _Heads(ctypes.Structure):
                 ("ldo", ctypes.c_int64), ("heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
-def _here(stream, *tensors):
-    """All of them on the device that the call runs on: the current one, or the stream's."""
-    on = {t.get_device() for t in tensors if t is not None}
-    if -1 in on:
-        raise QpackError("qpack kernels take CUDA tensors")
-    dev = stream.device_index if isinstance(stream, torch.cuda.Stream) else _current_device()
-    if on != {dev}:
-        raise QpackError(f"tensors on devices {sorted(on)}, the call runs on {dev}")
+_heads_bytes = struct.Struct("@PPPqqii").pack               # a _Heads, in a third of the time that making one takes
 
 
-def _side(x, out, weight, what, like, stream):
-    """Heads [n, heads, dim] of one side and where they go."""
+def _device(stream):
+    """The device that a call runs on: the current one, or the stream's (-2, which no tensor is on, where CUDA is not in use)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream.device_index
+    return _current_device() if torch.cuda.is_initialized() else -2
+
+
+def _at(t, dev):
+    """The address of a tensor, which has to be on the call's device."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise QpackError("qpack kernels take CUDA tensors" if not t.is_cuda else f"a tensor is on {t.device}, the call runs on device {dev}")
+    return t.data_ptr()
+
+
+def _side(x, out, weight, what, like, stream, dev):
+    """Heads [n, heads, dim] of one side and where they go: the outputs, both types, the C structure's bytes."""
     if x.dim() != 3:
         raise QpackError(f"{what}: expected [n, heads, dim], got {tuple(x.shape)}")
     n, heads, dim = x.shape
@@ -720,11 +731,9 @@ def _side(x, out, weight, what, like, stream):
     odt, ldo, rows = _need_rows(out, what + "_out", heads, dim)
     if rows < n:
         raise QpackError(f"{what}_out: expected at least {n} rows, got {rows}")
-    if weight is not None:
-        _need(weight, torch.float32, what + "_weight", numel=dim)
-        if weight.numel() != dim:
-            raise QpackError(f"{what}_weight: expected {dim} elements, got {weight.numel()}")
-    return out, dt, odt, _Heads(_addr(x), _addr(out), _addr(weight), ldx, ldo, heads, 0)
+    if weight is not None and (weight.dtype is not torch.float32 or weight.numel() != dim or not weight.is_contiguous()):
+        raise QpackError(f"{what}_weight: expected {dim} contiguous float32 elements, got {weight.dtype} {tuple(weight.shape)}")
+    return out, dt, odt, _heads_bytes(_at(x, dev), _at(out, dev), _at(weight, dev) or 0, ldx, ldo, heads, 0)
 
 
 def qpack_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, eps=1e-6, rope=None, interleaved=False, tables=None,
@@ -734,17 +743,18 @@ def qpack_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, eps=1e-6, rope=N
     (float32 [positions, cos | sin]): pairs half of them apart, or neighbours (interleaved). Token i's position is pos[i], or
     the last one of sequence seqs[i] (default i) of `tables`; negative positions leave their rows as they were. Returns
     (q_out, k_out), of the inputs' type unless given (an input itself will do); k may be None."""
+    turn = rows = 0
     if rope is not None:
         turn = rope.shape[1] if rope.dim() == 2 else -1
         rows = _need_rope(rope, turn)
         if pos is None and tables is None:
             raise QpackError("pos: needed for the rotation where no tables are given")
-    else:
-        turn = rows = 0
-    q_out, dt, odt, cq = _side(q, q_out, q_weight, "q", None, stream)
-    ck, n = None, q.shape[0]
+    dev = _device(stream)
+    q_out, dt, odt, cq = _side(q, q_out, q_weight, "q", None, stream, dev)
+    n, _, dim = q.shape
+    ck = None
     if k is not None:
-        k_out, _, odk, ck = _side(k, k_out, k_weight, "k", (n, q.shape[2], q.dtype), stream)
+        k_out, _, odk, ck = _side(k, k_out, k_weight, "k", (n, dim, q.dtype), stream, dev)
         if odk != odt:
             raise QpackError("q_out, k_out: expected the same type")
     _need_i32(pos, "pos", n)
@@ -752,10 +762,9 @@ def qpack_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, eps=1e-6, rope=N
         _need_i32(seqs, "seqs", n)
         if tables is not None and seqs is None and tables.tables.shape[0] < n:
             raise QpackError(f"q: {n} rows, but the table has {tables.tables.shape[0]} sequences")
-    _here(stream, q, k, q_out, k_out, q_weight, k_weight, rope, seqs, pos)
-    rc = (_lib or lib()).qpack_qk_norm_rope(
-        ctypes.addressof(cq), None if ck is None else ctypes.addressof(ck), n, q.shape[2], dt, odt, eps, _addr(rope), rows,
-        turn, bool(interleaved), None if tables is None else tables._ref, _addr(seqs), _addr(pos), _raw_stream(stream))
+    rc = (_lib or lib()).qpack_qk_norm_rope(cq, ck, n, dim, dt, odt, eps, _at(rope, dev), rows, turn, 1 if interleaved else 0,
+                                            None if tables is None else tables._ref, _at(seqs, dev), _at(pos, dev),
+                                            _raw_stream(stream))
     if rc:
         _check(rc, "qpack_qk_norm_rope")
     return q_out, k_out
@@ -789,9 +798,9 @@ def qpack_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None
         tokens = _out(stream, (B,), torch.int32, logits.device)
     _need_each(tokens, torch.int32, "tokens", B)
     _need_each(probs, torch.float32, "probs", B)
-    _here(stream, logits, u, temperature, top_k, top_p, min_p, tokens, probs)
-    rc = (_lib or lib()).qpack_sample(_addr(logits), code, logits.stride(0), V, B, _addr(temperature), _addr(top_k),
-                                      _addr(top_p), _addr(min_p), _addr(u), _addr(tokens), _addr(probs),
+    dev = _device(stream)
+    rc = (_lib or lib()).qpack_sample(_at(logits, dev), code, logits.stride(0), V, B, _at(temperature, dev), _at(top_k, dev),
+                                      _at(top_p, dev), _at(min_p, dev), _at(u, dev), _at(tokens, dev), _at(probs, dev),
                                       _raw_stream(stream))
     if rc:
         _check(rc, "qpack_sample")

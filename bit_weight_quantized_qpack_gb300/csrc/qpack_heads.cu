@@ -8,9 +8,10 @@
 // What bounds it. Each element is read and written once, and one row of the table is read for all heads of a token: the
 // copy rate at length, the launch and one chain position -> table row -> store at a decode step's few tokens.
 //
-// A head takes dim / 8 lanes, in groups of 8, 16 or 32 lanes. A lane holds both elements of its pairs (lane l of a half
-// layout the elements 4l .. 4l + 3 and their partners turn / 2 further), so that the rotation needs no shuffle and a lane
-// writes what it has read: in place is fine. Behind the rotated part a lane holds eight elements in a row.
+// A lane holds two runs of RUN elements, 16 bytes each where the type and the sizes allow it: lane l of a half layout the
+// elements RUN l and on and their partners turn / 2 further, so that the rotation needs no shuffle and a lane writes what it has
+// read (in place is fine); behind the rotated part, and of neighbouring pairs, 2 RUN elements in a row. A head takes
+// dim / (2 RUN) lanes of a group of 4 to 32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -25,35 +26,45 @@ namespace {
 __device__ int g_fault_heads = 0;
 
 constexpr int WARPS = 4;        // a block
-constexpr int ROWS = 4;         // heads in flight a group of lanes
+// Heads in flight a group of lanes (us for 16 fp32 tokens / 8191 bfloat16 tokens of 40 heads of 128, runs of four: 2 2.2 / 40.5,
+// 4 2.8 / 37.6, 6 3.5 / 43.0, 8 4.3 / 44.8).
+constexpr int ROWS = 4;
 
-// Four consecutive elements. Plain loads: the previous grid may have written them, and in place they are written here.
-template <int DT> struct Four { uint32_t w[DT == DT_F32 ? 4 : 2]; };
-template <int DT> __device__ __forceinline__ void load4(const void *p, int64_t i, Four<DT> &r) {
-    if (DT == DT_F32) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i);
-        r.w[0] = v.x, r.w[1] = v.y, r.w[DT == DT_F32 ? 2 : 0] = v.z, r.w[DT == DT_F32 ? 3 : 1] = v.w;
-    } else {
-        const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+// RUN = 4 or 8 consecutive elements, aligned to 8 or 16 bytes. Plain loads: the previous grid may have written them, and in place
+// they are written here.
+template <int DT, int RUN> struct Raw { uint32_t w[DT == DT_F32 ? RUN : RUN / 2]; };
+template <int DT, int RUN> __device__ __forceinline__ void load_run(const void *p, int64_t i, Raw<DT, RUN> &r) {
+    constexpr int WORDS = DT == DT_F32 ? RUN : RUN / 2;
+    const uint32_t *q = DT == DT_F32 ? static_cast<const uint32_t *>(p) + i : reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + i);
+    if constexpr (WORDS == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(q);
         r.w[0] = v.x, r.w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int e = 0; e < WORDS; e += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(q + e);
+            r.w[e] = v.x, r.w[e + 1] = v.y, r.w[e + 2] = v.z, r.w[e + 3] = v.w;
+        }
     }
 }
-template <int DT> __device__ __forceinline__ void widen(const Four<DT> &r, float *x) {
+template <int DT, int RUN> __device__ __forceinline__ void widen(const Raw<DT, RUN> &r, float *x) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < RUN; ++e) {
         if (DT == DT_F32) x[e] = __uint_as_float(r.w[DT == DT_F32 ? e : 0]);
         else if (DT == DT_F16) x[e] = h2f_bits(uint16_t(e & 1 ? r.w[e / 2] >> 16 : r.w[e / 2] & 0xFFFFu));
         else x[e] = __uint_as_float(e & 1 ? r.w[e / 2] & 0xFFFF0000u : r.w[e / 2] << 16);
     }
 }
-template <int DT> __device__ __forceinline__ void store4(void *p, int64_t i, const float *x) {
+template <int DT, int RUN> __device__ __forceinline__ void store_run(void *p, int64_t i, const float *x) {
     if (DT == DT_F32) {
-        *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = make_float4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+        for (int e = 0; e < RUN; e += 4)
+            *reinterpret_cast<float4 *>(static_cast<float *>(p) + i + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
         return;
     }
-    uint32_t w[2];
+    uint32_t w[RUN / 2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < RUN / 2; ++e) {
         if (DT == DT_F16) {
             w[e] = uint32_t(f2h_bits(x[2 * e])) | uint32_t(f2h_bits(x[2 * e + 1])) << 16;
         } else {
@@ -61,7 +72,9 @@ template <int DT> __device__ __forceinline__ void store4(void *p, int64_t i, con
             w[e] = *reinterpret_cast<const uint32_t *>(&b);
         }
     }
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) = make_uint2(w[0], w[1]);
+    uint16_t *o = static_cast<uint16_t *>(p) + i;
+    if constexpr (RUN == 4) *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[RUN / 2 - 2], w[RUN / 2 - 1]);
 }
 
 // The token's position: -1 where it is skipped (a negative position, an empty sequence) or its sequence is out of range.
@@ -75,8 +88,8 @@ __device__ __forceinline__ int position(const HeadsArgs &a, int64_t i, bool repo
     return max(len, 0) - 1;
 }
 
-// G lanes a head: dim <= 8 G. NEAR: pairs are neighbours.
-template <int XT, int OT, int G, bool NEAR>
+// G lanes a head: dim <= 2 RUN G. NEAR: pairs are neighbours.
+template <int XT, int OT, int RUN, int G, bool NEAR>
 __global__ void __launch_bounds__(WARPS * 32) heads_kernel(HeadsArgs a, int64_t first, unsigned items, unsigned q_groups,
                                                            unsigned groups) {
     constexpr int PER = 32 / G;                            // heads a pass of the warp
@@ -91,55 +104,61 @@ __global__ void __launch_bounds__(WARPS * 32) heads_kernel(HeadsArgs a, int64_t 
     const int64_t tok = first + tok_in;
     const HeadsSide &x = a.side[side];
     const int D = a.dim, half = a.turn / 2;
-    const bool holds = l < D / 8;
-    const bool turned = a.rope && 4 * l < half;            // lane of the rotated part
-    // the lane's two runs of four elements
-    const int at0 = NEAR || !turned ? 8 * l : 4 * l, at1 = NEAR || !turned ? 8 * l + 4 : half + 4 * l;
-    Four<XT> raw[ROWS][2];
+    const bool holds = l < D / (2 * RUN);
+    const bool turned = a.rope && RUN * l < half;          // lane of the rotated part
+    // the lane's two runs
+    const int at0 = NEAR || !turned ? 2 * RUN * l : RUN * l, at1 = NEAR || !turned ? 2 * RUN * l + RUN : half + RUN * l;
+    Raw<XT, RUN> raw[ROWS][2];
 #pragma unroll
     for (int u = 0; u < ROWS; ++u) {
         const int head = head0 + u * PER;
-        raw[u][0] = raw[u][1] = Four<XT>{};
+        raw[u][0] = raw[u][1] = Raw<XT, RUN>{};
         if (holds && head < x.heads) {
-            load4<XT>(x.x, tok * x.ldx + int64_t(head) * D + at0, raw[u][0]);
-            load4<XT>(x.x, tok * x.ldx + int64_t(head) * D + at1, raw[u][1]);
+            load_run<XT, RUN>(x.x, tok * x.ldx + int64_t(head) * D + at0, raw[u][0]);
+            load_run<XT, RUN>(x.x, tok * x.ldx + int64_t(head) * D + at1, raw[u][1]);
         }
     }
     const int pos = position(a, tok, lane == 0 && group == 0);
     if (pos < 0) return;
-    float c[4] = {1, 1, 1, 1}, s[4] = {0, 0, 0, 0};
+    float c[RUN], s[RUN];
     const bool in_table = pos < a.rope_rows;
     if (turned && in_table) {
-        const float *row = a.rope + int64_t(pos) * a.turn + 4 * l;
-        const float4 cc = *reinterpret_cast<const float4 *>(row), ss = *reinterpret_cast<const float4 *>(row + half);
-        c[0] = cc.x, c[1] = cc.y, c[2] = cc.z, c[3] = cc.w;
-        s[0] = ss.x, s[1] = ss.y, s[2] = ss.z, s[3] = ss.w;
+        const float *row = a.rope + int64_t(pos) * a.turn + RUN * l;
+#pragma unroll
+        for (int e = 0; e < RUN; e += 4) {
+            const float4 cc = *reinterpret_cast<const float4 *>(row + e), ss = *reinterpret_cast<const float4 *>(row + half + e);
+            c[e] = cc.x, c[e + 1] = cc.y, c[e + 2] = cc.z, c[e + 3] = cc.w;
+            s[e] = ss.x, s[e + 1] = ss.y, s[e + 2] = ss.z, s[e + 3] = ss.w;
+        }
     }
     if (a.rope && !in_table && lane == 0 && group == 0) atomicOr(&g_fault_heads, FAULT_PAGE);
-    float w[8] = {};
-    if (x.weight && holds) {
-        const float4 lo = *reinterpret_cast<const float4 *>(x.weight + at0), hi = *reinterpret_cast<const float4 *>(x.weight + at1);
-        w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w, w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
-    }
+    float w[2 * RUN] = {};
+    if (x.weight && holds)
+#pragma unroll
+        for (int e = 0; e < RUN; e += 4) {
+            const float4 lo = *reinterpret_cast<const float4 *>(x.weight + at0 + e), hi = *reinterpret_cast<const float4 *>(x.weight + at1 + e);
+            w[e] = lo.x, w[e + 1] = lo.y, w[e + 2] = lo.z, w[e + 3] = lo.w;
+            w[RUN + e] = hi.x, w[RUN + e + 1] = hi.y, w[RUN + e + 2] = hi.z, w[RUN + e + 3] = hi.w;
+        }
 #pragma unroll
     for (int u = 0; u < ROWS; ++u) {
-        float y[8];
-        widen<XT>(raw[u][0], y);
-        widen<XT>(raw[u][1], y + 4);
+        float y[2 * RUN];
+        widen<XT, RUN>(raw[u][0], y);
+        widen<XT, RUN>(raw[u][1], y + RUN);
         if (x.weight) {                                    // the same for the whole warp
             float sum = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(y[e], y[e], sum);
+            for (int e = 0; e < 2 * RUN; ++e) sum = fmaf(y[e], y[e], sum);
 #pragma unroll
             for (int o = G / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             const float r = __frsqrt_rn(__fdiv_rn(sum, float(D)) + a.eps);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = y[e] * r * w[e];
+            for (int e = 0; e < 2 * RUN; ++e) y[e] = y[e] * r * w[e];
         }
         if (turned && in_table) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float &p = y[NEAR ? 2 * e : e], &q = y[NEAR ? 2 * e + 1 : 4 + e];
+            for (int e = 0; e < RUN; ++e) {
+                float &p = y[NEAR ? 2 * e : e], &q = y[NEAR ? 2 * e + 1 : RUN + e];
                 const float m = p;
                 p = __fsub_rn(__fmul_rn(m, c[e]), __fmul_rn(q, s[e]));
                 q = __fadd_rn(__fmul_rn(q, c[e]), __fmul_rn(m, s[e]));
@@ -147,13 +166,13 @@ __global__ void __launch_bounds__(WARPS * 32) heads_kernel(HeadsArgs a, int64_t 
         }
         const int head = head0 + u * PER;
         if (holds && head < x.heads) {
-            store4<OT>(x.out, tok * x.ldo + int64_t(head) * D + at0, y);
-            store4<OT>(x.out, tok * x.ldo + int64_t(head) * D + at1, y + 4);
+            store_run<OT, RUN>(x.out, tok * x.ldo + int64_t(head) * D + at0, y);
+            store_run<OT, RUN>(x.out, tok * x.ldo + int64_t(head) * D + at1, y + RUN);
         }
     }
 }
 
-template <int XT, int OT, int G, bool NEAR> cudaError_t run(const HeadsArgs &a, cudaStream_t s) {
+template <int XT, int OT, int RUN, int G, bool NEAR> cudaError_t run(const HeadsArgs &a, cudaStream_t s) {
     constexpr int per = ROWS * (32 / G);                   // a warp's heads
     const unsigned q_groups = (a.side[0].heads + per - 1) / per, groups = q_groups + (a.side[1].heads + per - 1) / per;
     const int64_t most = (int64_t(1) << 30) / groups;      // tokens a launch: item numbers stay below 2^31
@@ -168,16 +187,20 @@ template <int XT, int OT, int G, bool NEAR> cudaError_t run(const HeadsArgs &a, 
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, heads_kernel<XT, OT, G, NEAR>, a, i, items, q_groups, groups);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, heads_kernel<XT, OT, RUN, G, NEAR>, a, i, items, q_groups, groups);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
-template <int XT, int OT, int G> cudaError_t run_pairs(const HeadsArgs &a, cudaStream_t s) {
-    return a.near_pairs ? run<XT, OT, G, true>(a, s) : run<XT, OT, G, false>(a, s);
+template <int XT, int OT, int RUN, int G> cudaError_t run_pairs(const HeadsArgs &a, cudaStream_t s) {
+    return a.near_pairs ? run<XT, OT, RUN, G, true>(a, s) : run<XT, OT, RUN, G, false>(a, s);
 }
 template <int XT, int OT> cudaError_t run_dim(const HeadsArgs &a, cudaStream_t s) {
-    return a.dim <= 64 ? run_pairs<XT, OT, 8>(a, s) : a.dim <= 128 ? run_pairs<XT, OT, 16>(a, s) : run_pairs<XT, OT, 32>(a, s);
+    // runs of eight where they are 16 bytes on the way in, and both parts of a head are made of pairs of runs
+    if constexpr (XT != DT_F32)
+        if (a.dim % 16 == 0 && a.turn % 16 == 0)
+            return a.dim <= 64 ? run_pairs<XT, OT, 8, 4>(a, s) : a.dim <= 128 ? run_pairs<XT, OT, 8, 8>(a, s) : run_pairs<XT, OT, 8, 16>(a, s);
+    return a.dim <= 64 ? run_pairs<XT, OT, 4, 8>(a, s) : a.dim <= 128 ? run_pairs<XT, OT, 4, 16>(a, s) : run_pairs<XT, OT, 4, 32>(a, s);
 }
 template <int XT> cudaError_t run_out(const HeadsArgs &a, cudaStream_t s) {
     return a.odt == DT_F32 ? run_dim<XT, DT_F32>(a, s) : a.odt == DT_F16 ? run_dim<XT, DT_F16>(a, s) : run_dim<XT, DT_BF16>(a, s);
