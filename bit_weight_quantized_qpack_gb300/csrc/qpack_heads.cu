@@ -6,7 +6,9 @@
 // before their sum, as the cache's append has it: without a weight the rotated keys are those that append would store.
 //
 // What bounds it. Each element is read and written once, and one row of the table is read for all heads of a token: the
-// copy rate at length, the launch and one chain position -> table row -> store at a decode step's few tokens.
+// copy rate at length (8191 bfloat16 tokens of 40 heads of 128: 38 us, 67% of it; the chain position -> table row -> store in
+// the warps that fit an SM), the launch and that chain at a decode step's few tokens (2.1 us in a graph, 10.5 by a call from
+// Python, whose host time that is).
 //
 // A lane holds two runs of RUN elements, 16 bytes each where the type and the sizes allow it: lane l of a half layout the
 // elements RUN l and on and their partners turn / 2 further, so that the rotation needs no shuffle and a lane writes what it has
@@ -26,9 +28,10 @@ namespace {
 __device__ int g_fault_heads = 0;
 
 constexpr int WARPS = 4;        // a block
-// Heads in flight a group of lanes (us for 16 fp32 tokens / 8191 bfloat16 tokens of 40 heads of 128, runs of four: 2 2.2 / 40.5,
-// 4 2.8 / 37.6, 6 3.5 / 43.0, 8 4.3 / 44.8).
-constexpr int ROWS = 4;
+// Heads in flight a group of lanes. us for 16 fp32 tokens / 8191 bfloat16 tokens of 40 heads of 128 (the latter in runs of
+// eight): 1 1.8 / 44.4, 2 2.1 / 38.6, 4 2.8 / 38.2; in runs of four 2 2.2 / 40.5, 4 2.8 / 37.6, 6 3.5 / 43.0. A grid that stays
+// and asks for the next position a pass ahead took 41 us.
+constexpr int ROWS = 2;
 
 // RUN = 4 or 8 consecutive elements, aligned to 8 or 16 bytes. Plain loads: the previous grid may have written them, and in place
 // they are written here.
