@@ -1141,7 +1141,7 @@ template <int KT, int D, int NT> cudaError_t run(const AttendArgs &a, cudaStream
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = a.from ? 0 : 1;                     // (behind a kernel that fills every SM nothing is gained)
         e = cudaLaunchKernelEx(&cfg, attend_kernel<KT, D, NT>, p);
         if (e != cudaSuccess) return e;
     }

@@ -888,78 +888,102 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
     }
 }
 
-// The parts of a row's query head joined: prefix pieces in the order of their blocks, then what the row has of its own. A warp
-// a query head. The pieces' maxima and sums come a lane a piece, so that their accumulators, weighted at once, depend on no
-// other's.
-template <int D> __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Params p, int tok) {
-    constexpr int N = D / 32;                              // elements a lane
+// The parts of a row's query head joined: prefix pieces in the order of their blocks, then what the row has of its own. A block a
+// query head: every warp finds the common maximum and sum, a part a lane, and adds up every JOIN-th part's accumulators, four
+// parts' loads at a time and the first four's under way meanwhile; the warps' sums are added in shared memory. It is bound by the
+// chain plan -> maxima -> accumulators and by how many blocks pass through an SM. us at 1 / 2 / 4 / 8 warps: 64 rows of 32 heads of
+// 128, 10 parts 6.8 / 6.5 / 7.9 / 12.5; 17 rows of 16 heads of 256, 28 parts 10.4 / 7.9 / 6.1 / 6.0 (19 by a warp that took one
+// part after another).
+template <int D> constexpr int JOIN_WARPS = D == 256 ? 4 : 2;
+template <int D> __global__ void __launch_bounds__(JOIN_WARPS<D> * 32) join_kernel(const __grid_constant__ Params p, int tok) {
+    constexpr int JOIN = JOIN_WARPS<D>, N = D / 32;        // elements a lane
+    __shared__ __align__(16) float s_o[JOIN][D];
     const SharedArgs &a = p.a;
-    const int lane = threadIdx.x & 31;
-    const int64_t i = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    pdl_launch_dependents();
-    if (i >= int64_t(a.B) * a.q_heads) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t i = blockIdx.x;
     const int b = int(i / a.q_heads), head = int(i - int64_t(b) * a.q_heads), h = head / p.G;
+    pdl_launch_dependents();
     pdl_wait();
     const Plan &pl = *p.w.plan;
-    float o[N], m = -INFINITY, l = 0.0f;
-#pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = 0.0f;
-    // joins up to 32 parts: a lane's maximum and sum (none: 0), and where lane j's accumulators lie
-    auto join = [&](float mi, float li, const float *from, int64_t step, int n) {
-        if (!(li != 0.0f)) mi = -INFINITY;                 // (a sum of NaN counts)
-        float top = mi;
-#pragma unroll
-        for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-        top = fmaxf(top, m);
-        const float old = m == -INFINITY ? 0.0f : ex2(m - top), w = li != 0.0f ? ex2(mi - top) : 0.0f;
-        float sum = w != 0.0f ? li * w : 0.0f;
-#pragma unroll
-        for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-        m = top, l = fmaf(l, old, sum);
-#pragma unroll
-        for (int e = 0; e < N; ++e) o[e] *= old;
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) {
-            const float wj = __shfl_sync(0xffffffffu, w, j);
-            if (wj == 0.0f) continue;                      // may hold anything
-            const float *x = from + j * step + lane * N;
-#pragma unroll
-            for (int e = 0; e < N; ++e) o[e] = fmaf(x[e], wj, o[e]);
-        }
-    };
+    const float own = p.w.own_lse[i];
     const int g = pl.group[b];
+    // parts: n prefix pieces, of which the first block's is in its second place, the others' in their first; then the own one
+    int n = 0;
+    const float *piece = p.w.direct + i * D;
+    const float2 *ml = p.w.direct_ml + i;
+    int64_t step = 0, skip = 0;
     if (g >= 0 && pl.length[g] > 0) {
         const int item = pl.item, size = pl.size, row0 = a.first[g], rows = a.first[g + 1] - row0, tiles = (pl.length[g] + tok - 1) / tok;
         const int rr = (b - row0) * p.G + head - h * p.G, mb = rr / item, blocks = (rows * p.G + item - 1) / item;
-        const int u0 = pl.cum[g] + (h * blocks + mb) * tiles;
-        const int f0 = u0 / size, n = (u0 + tiles - 1) / size - f0 + 1;
-        if (n == 1) {
-            const float2 ml = lane == 0 ? p.w.direct_ml[i] : make_float2(-INFINITY, 0.0f);
-            join(ml.x, ml.y, p.w.direct + i * D, 0, 1);
-        } else {
-            // the first block's piece is in its second place, the others' in their first
-            const int64_t first = int64_t(f0) * 2 * (2 * ROWS) + rr % item;
-            float2 ml = lane == 0 ? p.w.piece_ml[first + 2 * ROWS] : make_float2(-INFINITY, 0.0f);
-            join(ml.x, ml.y, p.w.piece + (first + 2 * ROWS) * D, 0, 1);
-            for (int j0 = 1; j0 < n; j0 += 32) {
-                const int64_t at = first + int64_t(j0) * (4 * ROWS);
-                ml = j0 + lane < n ? p.w.piece_ml[at + lane * (4 * ROWS)] : make_float2(-INFINITY, 0.0f);
-                join(ml.x, ml.y, p.w.piece + at * D, int64_t(4 * ROWS) * D, min(32, n - j0));
-            }
+        const int u0 = pl.cum[g] + (h * blocks + mb) * tiles, f0 = u0 / size;
+        n = (u0 + tiles - 1) / size - f0 + 1;
+        if (n > 1) {
+            const int64_t first = int64_t(f0) * (4 * ROWS) + rr % item;
+            piece = p.w.piece + first * D, ml = p.w.piece_ml + first;
+            step = 4 * ROWS, skip = 2 * ROWS;
         }
     }
-    const float own = p.w.own_lse[i];
-    join(lane == 0 ? own * 1.4426950408889634f : -INFINITY, lane == 0 && own != -INFINITY ? 1.0f : 0.0f, p.w.own_out + i * D, 0, 1);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int64_t at = int64_t(b) * a.ldo + int64_t(head) * D + lane * N;
+    // a part's maximum (base 2) and sum (of zero: it has no tokens, and its accumulators may hold anything)
+    auto part = [&](int k) -> float2 {
+        if (k == n) return make_float2(own * 1.4426950408889634f, own != -INFINITY ? 1.0f : 0.0f);
+        return k < n ? ml[k * step + (k ? 0 : skip)] : make_float2(0.0f, 0.0f);
+    };
+    float2 x[4];
+    float v[4][N];
+    auto load = [&](int k0) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-        const float x = o[e] * inv;
-        if (a.odt == DT_F32) static_cast<float *>(a.out)[at + e] = x;
-        else if (a.odt == DT_F16) static_cast<uint16_t *>(a.out)[at + e] = f2h_bits(x);
-        else static_cast<uint16_t *>(a.out)[at + e] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+        for (int j = 0; j < 4; ++j) {
+            const int k = k0 + j * JOIN;
+            x[j] = part(k);
+            const float *from = (k < n ? piece + (k * step + (k ? 0 : skip)) * D : p.w.own_out + i * D) + lane * N;
+#pragma unroll
+            for (int e = 0; e < N; e += 2) {
+                const float2 y = k <= n ? *reinterpret_cast<const float2 *>(from + e) : make_float2(0.0f, 0.0f);
+                v[j][e] = y.x, v[j][e + 1] = y.y;
+            }
+        }
+    };
+    load(warp);                                            // under way while the maximum is found
+    float m = -INFINITY, l = 0.0f;
+    for (int k = lane; k <= n; k += 32) {
+        const float2 y = part(k);
+        if (y.y != 0.0f) m = fmaxf(m, y.x);
     }
-    if (a.lse && lane == 0) a.lse[i] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+#pragma unroll
+    for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    for (int k = lane; k <= n; k += 32) {
+        const float2 y = part(k);
+        if (y.y != 0.0f) l = fmaf(y.y, ex2(y.x - m), l);   // (a sum of NaN counts)
+    }
+#pragma unroll
+    for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+    float o[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = 0.0f;
+    for (int k0 = warp; k0 <= n; k0 += 4 * JOIN) {
+        if (k0 != warp) load(k0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float w = x[j].y != 0.0f ? ex2(x[j].x - m) : 0.0f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) o[e] = w != 0.0f ? fmaf(v[j][e], w, o[e]) : o[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < N; e += 2) *reinterpret_cast<float2 *>(&s_o[warp][lane * N + e]) = make_float2(o[e], o[e + 1]);
+    __syncthreads();
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    for (int d = threadIdx.x; d < D; d += JOIN * 32) {
+        float x = s_o[0][d];
+#pragma unroll
+        for (int k = 1; k < JOIN; ++k) x += s_o[k][d];
+        x *= inv;
+        const int64_t at = int64_t(b) * a.ldo + int64_t(head) * D + d;
+        if (a.odt == DT_F32) static_cast<float *>(a.out)[at] = x;
+        else if (a.odt == DT_F16) static_cast<uint16_t *>(a.out)[at] = f2h_bits(x);
+        else static_cast<uint16_t *>(a.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+    }
+    if (a.lse && threadIdx.x == 0) a.lse[i] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
 }
 
 // -- host -------------------------------------------------------------------------------------------------------
@@ -994,9 +1018,13 @@ template <int KT, int D> cudaError_t run(const Params &p, cudaStream_t s) {
     own.scale = a.scale, own.layer = a.layer, own.B = a.B, own.q_heads = a.q_heads, own.qdt = a.qdt, own.odt = DT_F32;
     own.from = p.w.plan->from;
     if ((e = launch_kv_attend(own, s)) != cudaSuccess) return e;
-    cfg.gridDim = dim3(unsigned((int64_t(a.B) * a.q_heads + 3) / 4));
-    cfg.blockDim = dim3(128);
+    // One after the other: blocks that come early, while their predecessors' still run, gather on the SMs that are done first and
+    // then wait there for one another's loads (64 samples / 32 rows of 65531 / 17 rows with heads of 256, us in a graph: both
+    // early 52.3 / 150.5 / 107, the attention alone 48.5 / 141 / 54.6, neither 46.5 / 135 / 54.5).
+    cfg.gridDim = dim3(unsigned(int64_t(a.B) * a.q_heads));
+    cfg.blockDim = dim3(JOIN_WARPS<D> * 32);
     cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 0;
     return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, F::TOK);
 }
 
