@@ -55,10 +55,10 @@ cudaError_t launch_kv_attend_shared(const SharedArgs &a, cudaStream_t s) {
     p.a.q_terms = !a.rope && a.qdt == (bf ? QPACK_BF16 : QPACK_F16) ? 1 : 2;
     p.a.p_terms = bf || a.odt == QPACK_F32 ? 2 : 1;
     shared::lay_out(a.pool, a.B, a.q_heads, static_cast<unsigned char *>(a.ws), p.w);
-    // the units of a call are counted in 31 bits
-    const int64_t tiles = (int64_t(a.t.max_pages) * a.pool.page_tokens + 63) / 64;
+    // tokens up to the end of a last tile and the units of a call are counted in 31 bits
+    const int64_t tokens = int64_t(a.t.max_pages) * a.pool.page_tokens, tiles = (tokens + 63) / 64;
     const int64_t items = (int64_t(a.B) * p.G / shared::ROWS + 1 + a.groups) * a.pool.heads;
-    if (tiles >= (int64_t(1) << 30) || items * tiles >= (int64_t(1) << 30)) return cudaErrorNotSupported;
+    if (tokens > 0x7FFFFF00 || items * tiles >= (int64_t(1) << 30)) return cudaErrorNotSupported;
     if (a.pool.type == QPACK_KV_I8) return shared::launch<QPACK_KV_I8>(p, s);
     if (a.pool.type == QPACK_KV_F16) return shared::launch<QPACK_KV_F16>(p, s);
     return shared::launch<QPACK_KV_BF16>(p, s);

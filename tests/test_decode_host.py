@@ -9,7 +9,7 @@ import torch
 from oracle import decode as ref
 from oracle import paged
 
-OK, ARG, SHAPE, ALIGN = 0, -1, -2, -3
+OK, ARG, SHAPE, ALIGN, UNSUPPORTED = 0, -1, -2, -3, -6
 P = 4096            # an address that is never followed: refusals come first
 
 
@@ -164,9 +164,10 @@ def test_sample_binding_refusals(qp):
 # attention over shared prefixes
 # ---------------------------------------------------------------------------------------------------------------
 def call_shared(qp, layer=0, seqs=0, B=4, first=P, prefix=P, groups=2, q=P, qdt=0, ldq=1024, q_heads=8, scale=0.1, rope=0, rows=0,
-                out=P, odt=1, ldo=1024, lse=0, ws=P, ws_bytes=None, type=1, dim=128, heads=2, tables=P, seq=8):
+                out=P, odt=1, ldo=1024, lse=0, ws=P, ws_bytes=None, type=1, dim=128, heads=2, tables=P, seq=8,
+                max_pages=8):
     pool = qp._Pool(P, P, None, None, 1 << 20, 1 << 14, 0, 0, 64, 1, heads, 16, dim, type, 0)
-    t = qp._Tables(tables or None, P, None, 8, 0, seq, 8)
+    t = qp._Tables(tables or None, P, None, max_pages, 0, seq, max_pages)
     if ws_bytes is None:
         n = ctypes.c_int64(0)
         good = qp._Pool(P, P, None, None, 1 << 20, 1 << 14, 0, 0, 64, 1, 2, 16, 128, 1, 0)
@@ -195,6 +196,12 @@ def test_shared_refusals(qp):
     assert size(-1, 8) == ARG and size(4, 0) == ARG and size(4, 7) == SHAPE and size(4097, 8) == SHAPE
     assert size(0, 8) > 1 << 20 and size(64, 8) > size(8, 8)
     assert qp.lib().qpack_kv_shared_workspace(ctypes.byref(pool), 4, 8, None) == ARG
+
+
+def test_shared_refuses_uncountable_lengths(qp):
+    """Tables of 2^31 tokens (16 a page) and tiles of all queries past 2^30: positions and units would pass their 31 bits."""
+    for bad in (dict(max_pages=1 << 27), dict(max_pages=1 << 28), dict(max_pages=(1 << 27) - 17, groups=512)):
+        assert call_shared(qp, **bad) == UNSUPPORTED, bad
 
 
 def test_shared_binding_refusals(qp):
