@@ -612,6 +612,6 @@ int qpack_set_option(int option, int value) {
     return QPACK_ERR_ARG;
 }
 
-int qpack_version(void) { return 1 * 10000 + 1 * 100 + 0; }
+int qpack_version(void) { return 1 * 10000 + 2 * 100 + 0; }
 
 }  // extern "C"

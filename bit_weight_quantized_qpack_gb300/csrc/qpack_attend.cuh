@@ -283,7 +283,7 @@ template <int TOK> __device__ __forceinline__ Row row_of(const Params &p, int b,
 
 // Shares are cut by work: a segment counts its tiles and SETUP more, the time that its queries and results take a warp
 // (shares by tiles alone left blocks with many short segments 1.6 times as long as the others; 90 rows of 0 to 4000
-// tokens: 1 37.4 us, 2 34.3, 3 34.2; 3072 segments of up to 40 tokens: 13.6, 13.4, 18.0). Positions ("units") run
+// tokens: 1 37.4 us, 2 34.3, 3 34.2; some 3000 segments of up to 40 tokens: 13.6, 13.4, 18.0). Positions ("units") run
 // row by row and segment by segment, a segment's SETUP units first. The share of block i: equal pieces of `size` units,
 // or (whole) segment i. The host keeps all numbers below 2^31.
 constexpr unsigned SETUP = 2;

@@ -1,5 +1,5 @@
 // qpack_fault.cu — the library's fault word: the translation units' words taken together and cleared by one small kernel, so
-// that a fetch is a launch and a copy whatever their number (16 us; a copy there and back for each of six words took 75).
+// that a fetch is a launch and a copy whatever their number (16 us; a copy there and back for each of six of them took 75).
 #include <cuda_runtime.h>
 
 #include "qpack_launch.h"

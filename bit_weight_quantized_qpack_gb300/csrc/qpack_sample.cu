@@ -15,6 +15,16 @@
 // The kept tokens are found without sorting: a histogram of counts and weights over 2048 intervals of m - x shows the interval
 // in which the k-th token or the p-th part of the sum lies, its tokens are gathered and ranked among each other; an
 // interval of too many tokens is divided again by the bits of the logits, until its tokens are few or all equal.
+//
+// What bounds it. A row is read from HBM once and from L2 some four times more (maximum, histogram, gathering, the sums of the
+// draw), 64 rows of 128256 fp32 logits 33 MB (156 MB through L2): 5 us at the copy rate, 70 us as it is. The passes are bound by the
+// weights' instructions (schedulers 57% busy) and by what stands between them: two barriers of the row's blocks a pass, sums over
+// 2048 intervals, a launch's cold instruction cache. One row of 32000 is all latency: 25 us.
+//
+// A row is split over up to 8 blocks of a cluster, which read each other's totals in shared memory, as long as all rows' blocks run
+// at once; rows enough to fill the GPU take a block of 512 threads each, two an SM (us for one row of 32000 / 64 of 128256 / 256 of
+// 32000 unfiltered / 33 of 50257 of all kinds: a block of 1024 a row 48 / 213 / 64 / 78, split 29 / 90 / 55 / 43, as it is 25 / 70 / 33 /
+// 31; as it is but with twice the blocks, of 512 threads, where a row is split 25 / 73 / 33 / 61).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -1,5 +1,33 @@
-// qpack_shared.cuh — attention of one new token a row where groups of rows share a prefix: the kernel over the prefixes,
-// instantiated per cache type in qpack_shared_i8.cu, qpack_shared_f16.cu and qpack_shared_bf16.cu.
+// qpack_shared.cuh — attention of one new token a row where groups of rows share a prefix: the kernels over the prefixes and
+// for the joins, instantiated per cache type in qpack_shared_i8.cu, qpack_shared_f16.cu and qpack_shared_bf16.cu.
+//
+// The mathematics. Row b of group g sees the tokens 0 .. L_b - 1, of which the first P_g are those of the group's first row. For
+// any split of a row's tokens into sets S with m_S = max s_t, l_S = sum e^(s_t - m_S), o_S = sum e^(s_t - m_S) v_t, the whole is
+//     out = sum_S e^(m_S - m) o_S / sum_S e^(m_S - m) l_S,    m = max m_S,    lse = m + log(sum_S e^(m_S - m) l_S).
+// So three launches: o, m and l over the prefixes, for all queries of a group that a key/value head serves in one product; over
+// what rows have of their own, by the cache's attention from token P_g on (qpack_attend.cuh); and the joins.
+//
+// What bounds it. A group has R = rows x query heads a key/value head queries, for which each element of its prefix is
+// multiplied and added R times: with 8-bit elements the tensor cores at their rate take as long as HBM at R = 142. Neither is
+// reached; what limits the prefix kernel is the chain scores -> maximum -> weights -> values: for two blocks of 128 queries
+// 5.2k clocks a tile of 128 tokens, of which the softmax of 128 scores a thread is 2.7k, each product 0.65k (128 x 128 x 128),
+// the rest hand-overs between warps; the tensor pipe is 29% busy, the schedulers 50%. 32 rows of 65531 tokens, 64 heads over
+// 8, 8 bits: 111 us for 68.7 GFLOP, 32% of the measured bf16 rate; 64 rows of 7999, 32 over 8: 26 us, of which some 12 are the
+// call's start (plan, queries, first tiles) and the results' way out. A call of a few rows takes three launches' latency, 20
+// us.
+//
+// Layout. One block an SM, 17 warps: loaders bring tiles of keys and values into a ring of 128-byte-swizzled operands (8-bit codes
+// are unpacked to fp16(scale code) on the way, which is what the cache stands for), one warp issues the products on tcgen05, two
+// groups of four hold a query a thread, take scores from tensor memory, and put the weights back over them as the A operand of the
+// second product, so that neither leaves the SM nor passes through shared memory. Units, a tile for one block of queries, are cut
+// evenly over the blocks whatever the groups' lengths; a block that gets part of a prefix leaves a piece.
+//   A tile at a time by all warps took 760 us for the 65531 tokens, roles of their own 226, codes staged asynchronously 180,
+// addresses by a lane a row 150, products issued by a converged warp and two teams of loaders 140. Slower: halves of 64 tokens
+// with two score buffers a group (149 against 137), one team (150), rows' own tokens attended to within the join (fp32, a lane
+// a token out of shared memory: 28 us more for 64 rows of up to 200).
+//
+// Terms. fp32 queries (and rotated ones of 16 bits) are two 16-bit terms over fp16 values, weights two where the output or the
+// cache asks for it; a second term of the queries doubles that product, and blocks of 128 queries are then taken one at a time.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
