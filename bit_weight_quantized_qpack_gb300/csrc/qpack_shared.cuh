@@ -10,11 +10,11 @@
 // What bounds it. A group has R = rows x query heads a key/value head queries, for which each element of its prefix is
 // multiplied and added R times: with 8-bit elements the tensor cores at their rate take as long as HBM at R = 142. Neither is
 // reached; what limits the prefix kernel is the chain scores -> maximum -> weights -> values: for two blocks of 128 queries
-// 5.2k clocks a tile of 128 tokens, of which the softmax of 128 scores a thread is 2.7k, each product 0.65k (128 x 128 x 128),
-// the rest hand-overs between warps; the tensor pipe is 29% busy, the schedulers 50%. 32 rows of 65531 tokens, 64 heads over
-// 8, 8 bits: 111 us for 68.7 GFLOP, 32% of the measured bf16 rate; 64 rows of 7999, 32 over 8: 26 us, of which some 12 are the
-// call's start (plan, queries, first tiles) and the results' way out. A call of a few rows takes three launches' latency, 20
-// us.
+// some 4.6k clocks a tile of 128 tokens (5.2k where the maximum is found before the weights, of which those are 2.7k and each
+// product of 128 x 128 x 128 is 0.65k, the rest hand-overs between warps; the tensor pipe 29% busy then, the schedulers 50%).
+// 32 rows of 65531 tokens, 64 heads over 8, 8 bits: 103 us for 68.7 GFLOP, 35% of the measured bf16 rate; 64 rows of 7999, 32
+// over 8: 26 us, of which some 12 are the call's start (plan, queries, first tiles) and the results' way out. A call of a few
+// rows takes three launches' latency, 20 us.
 //
 // Layout. One block an SM, 17 warps: loaders bring tiles of keys and values into a ring of 128-byte-swizzled operands (8-bit codes
 // are unpacked to fp16(scale code) on the way, which is what the cache stands for), one warp issues the products on tcgen05, two
@@ -22,7 +22,8 @@
 // second product, so that neither leaves the SM nor passes through shared memory. Units, a tile for one block of queries, are cut
 // evenly over the blocks whatever the groups' lengths; a block that gets part of a prefix leaves a piece.
 //   A tile at a time by all warps took 760 us for the 65531 tokens, roles of their own 226, codes staged asynchronously 180,
-// addresses by a lane a row 150, products issued by a converged warp and two teams of loaders 140. Slower: halves of 64 tokens
+// addresses by a lane a row 150, products issued by a converged
+// warp and two teams of loaders 140, the joins' warps 132, weights by the maximum that there is 123. Slower: halves of 64 tokens
 // with two score buffers a group (149 against 137), one team (150), rows' own tokens attended to within the join (fp32, a lane
 // a token out of shared memory: 28 us more for 64 rows of up to 200).
 //
@@ -170,6 +171,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
           "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
         : "r"(taddr)
         : "memory");
 }
@@ -709,6 +717,7 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
             const uint32_t lanes = tmem + (uint32_t(32 * (warp % SOFT)) << 16);
             const uint32_t o = lanes + F::O_COL + (TWO ? wg * F::O_STEP : 0);
             bool any = false;                              // the accumulators hold something
+            const bool many = (TWO && !dual ? nt / 2 : nt) >= 8;
             const bool idle = (dual ? wg * ROWS : 0) + 32 * (warp % SOFT) >= live;     // no queries in this warp's lanes
             for (int j = TWO ? wg : wg * jobs; j < jobs; j += TWO ? 2 : 1) {
                 const int left = lim - (sg.tile0 + (dual ? j >> 1 : j)) * TOK;
@@ -728,6 +737,54 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     continue;
                 }
                 const bool all = __all_sync(0xffffffffu, left >= TOK);
+                // The maximum lags, so nearly every tile but the first is weighed by the one that there is: weights and the tile's
+                // maximum in one go, the weights kept until it is known that they hold (over the scores they could not be taken
+                // back). Where they do not, or are two terms, maximum first and weights then; so too where a group has few tiles, which do not
+                // pay for one more path's cold instructions (1.3 us; 0.35 us gained a tile of 2 x 128 queries: 32 rows of 65531 tokens 132 ->
+                // 122 us, 64 of 7999, with four tiles a group, 45.8 -> 47.1).
+                if (!BF && any && all && many && a.p_terms == 1) {
+                    const float by = m == -INFINITY ? 0.0f : m;
+                    float2 sum = make_float2(0.0f, 0.0f), sum1 = sum;
+                    float t0 = -INFINITY, t1 = -INFINITY;
+                    uint32_t h[TOK / 2], x[8], y[8];
+                    auto part = [&](int c, const uint32_t (&z)[8]) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 v = make_float2(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1]));
+                            if (i & 1) t1 = max3(t1, v.x, v.y); else t0 = max3(t0, v.x, v.y);
+                            float2 e = fma2(sub2(v, by), f, F::BIAS);
+                            e = make_float2(ex2(e.x), ex2(e.y));
+                            if (i & 1) sum1 = add2(sum1, e); else sum = add2(sum, e);
+                            h[c / 2 + i] = pack2<BF>(e.x, e.y);
+                        }
+                    };
+                    tmem_ld8(sc, x);
+#pragma unroll
+                    for (int c = 0; c < TOK; c += 16) {
+                        tmem_ld_wait();
+                        tmem_ld8(sc + c + 8, y);
+                        part(c, x);
+                        tmem_ld_wait();
+                        if (c + 16 < TOK) tmem_ld8(sc + c + 16, x);
+                        part(c + 8, y);
+                    }
+                    const float top = fmaxf(t0, t1);
+                    if (!__any_sync(0xffffffffu, top > m && !((top - m) * f <= F::GROW))) {
+#pragma unroll
+                        for (int c = 0; c < TOK; c += 32) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) w[i] = h[c / 2 + i];
+                            tmem_st16(sc + c, w);
+                        }
+                        l += sum.x + sum.y + (sum1.x + sum1.y);
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_full[j & 1]);
+                        continue;
+                    }
+                }
                 float top = -INFINITY;
 #pragma unroll 1
                 for (int c = 0; c < TOK; c += 64) {

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_paged import f64, make_pool
+from test_gpu_paged import DT, f64, make_pool
 from test_gpu_shared import check, forked, i32, tables_of
 
 pytestmark = pytest.mark.gpu
@@ -108,3 +108,30 @@ def test_not_finite(qpg, kind, D, bad):
     assert not bool(torch.isfinite(got[hit]).any()) and torch.equal(got[~hit], good[~hit])
     pool.v[0, page, 0, slot, 7] = 0
     assert qpg.qpack_fetch_fault_flags() == 0
+
+
+@pytest.mark.parametrize("kind", ["i8", "f16"])
+@pytest.mark.parametrize("rows,G,prefix,qdt", [(3, 2, 39990, "f32"), (9, 16, 20470, "f16")])
+def test_maxima_that_move_in_long_segments(qpg, kind, rows, G, prefix, qdt):
+    """Long runs of tiles a block, one and two blocks of queries: scores swell and ebb, so that the running maximum holds in some
+    tiles, moves a little in others and far in others, each query in its own."""
+    T, H, D = 64, 8, 64
+    first, pref, lens, tab, pages = forked(qpg, [rows], [prefix], [20, 3], T, seed=34)
+    pool = make_pool(qpg, kind, 1, pages, H, T, D, 34, 0, False)
+    t = torch.arange(lens[0], device="cuda")
+    ramp = 40 * torch.sin(t / 300.0) + t / 700.0
+    page = torch.from_numpy(tab[0]).cuda().long()[t // T]
+    for h in range(H):
+        x = ramp * (1 + h / 8)
+        if kind == "i8":
+            pool.k_scales[0, page, h, t % T, 0] = (x.abs() / 127).half()
+            pool.k[0, page, h, t % T, 5] = (127 * torch.sign(x)).to(torch.int8)
+        else:
+            pool.k[0, page, h, t % T, 5] = x.half()
+    q = torch.randn((rows, H * G, D), device="cuda") * 0.1
+    q[:, :, 5] = torch.linspace(-2, 2, rows * H * G, device="cuda").view(rows, H * G)
+    q = q.to(DT[qdt])
+    out, lse = torch.empty((rows, H * G, D), dtype=torch.float16, device="cuda"), torch.empty((rows, H * G), device="cuda")
+    qpg.qpack_kv_attend_shared(pool, 0, tables_of(qpg, tab, lens), q, i32(first), i32(pref), scale=1.0, out=out, lse=lse)
+    assert qpg.qpack_fetch_fault_flags() == 0
+    check(out, lse, "f16", kind, f64(q), pool, 0, tab, lens, range(rows), [0] * rows, pref * rows, 1.0, None)
