@@ -10,9 +10,9 @@
 // What bounds it. A group has R = rows x query heads a key/value head queries, for which each element of its prefix is
 // multiplied and added R times: with 8-bit elements the tensor cores at their rate take as long as HBM at R = 142. Neither is
 // reached; what limits the prefix kernel is the chain scores -> maximum -> weights -> values: for two blocks of 128 queries
-// some 4.6k clocks a tile of 128 tokens (5.2k where the maximum is found before the weights, of which those are 2.7k and each
+// some 4.5k clocks a tile of 128 tokens (5.2k where the maximum is found before the weights, of which those are 2.7k and each
 // product of 128 x 128 x 128 is 0.65k, the rest hand-overs between warps; the tensor pipe 29% busy then, the schedulers 50%).
-// 32 rows of 65531 tokens, 64 heads over 8, 8 bits: 103 us for 68.7 GFLOP, 35% of the measured bf16 rate; 64 rows of 7999, 32
+// 32 rows of 65531 tokens, 64 heads over 8, 8 bits: 99 us for 68.7 GFLOP, 36% of the measured bf16 rate; 64 rows of 7999, 32
 // over 8: 26 us, of which some 12 are the call's start (plan, queries, first tiles) and the results' way out. A call of a few
 // rows takes three launches' latency, 20 us.
 //
@@ -23,7 +23,8 @@
 // evenly over the blocks whatever the groups' lengths; a block that gets part of a prefix leaves a piece.
 //   A tile at a time by all warps took 760 us for the 65531 tokens, roles of their own 226, codes staged asynchronously 180,
 // addresses by a lane a row 150, products issued by a converged
-// warp and two teams of loaders 140, the joins' warps 132, weights by the maximum that there is 123. Slower: halves of 64 tokens
+// warp and two teams of loaders 140, the joins' warps 132, weights by the maximum that there is 123, queries' lines
+// asked for ahead 119. Slower: halves of 64 tokens
 // with two score buffers a group (149 against 137), one team (150), rows' own tokens attended to within the join (fp32, a lane
 // a token out of shared memory: 28 us more for 64 rows of up to 200).
 //
@@ -223,6 +224,7 @@ __device__ __forceinline__ int row_len(const SharedArgs &a, int seq) {
     const int64_t len = a.t.lens[seq];
     return int(len < 0 ? 0 : len > cap ? cap : len);
 }
+__device__ __forceinline__ void prefetch_line(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
@@ -440,6 +442,23 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                         my_pos = -1;
                     }
                 }
+                // all passes' lines are asked for first: registers for their loads there are not (heads of 256: nothing gained)
+                if (D <= 128)
+#pragma unroll 1
+                for (int it = 0; it * 32 < top; ++it) {
+                    const int pos = __shfl_sync(0xffffffffu, my_pos, it * 4 + (lane >> 3));
+                    const int64_t at = __shfl_sync(0xffffffffu, my_at, it * 4 + (lane >> 3)) + sub * N;
+                    if (it * 32 + warp * 4 + (lane >> 3) < live) {
+                        const char *from = static_cast<const char *>(a.q) + at * (a.qdt == DT_F32 ? 4 : 2);
+                        prefetch_line(from);
+                        prefetch_line(from + D / 2 * (a.qdt == DT_F32 ? 4 : 2));
+                    }
+                    if (pos >= 0) {
+                        const float *t = a.rope + int64_t(pos) * D + sub * N;
+                        prefetch_line(t);
+                        prefetch_line(t + D / 2);
+                    }
+                }
 #pragma unroll 1
                 for (int it = 0; it * 32 < top; ++it) {
                     const int r = it * 32 + warp * 4 + (lane >> 3);
@@ -618,8 +637,8 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                 }
             };
             if constexpr (I8) {
-                // A tile's codes come asynchronously into places of this thread's own, while it converts the tile before from its
-                // registers; a row's scales come to the lane that found the row.
+                // A tile's codes come asynchronously into places of this thread's own, as soon as it has converted the team's tile
+                // before, while the other team's is converted; a row's scales come to the lane that found the row.
                 constexpr int WPR = D / 64;                // pairs of scales a row
                 const uint8_t *const codes = raw + team * F::RAW_BYTES + t * 16;
                 const uint32_t codes32 = smem_u32(codes);
@@ -657,8 +676,6 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     for (int i = 0; i < NC; ++i) code[i] = *reinterpret_cast<const uint4 *>(codes + i * (F::TEAM * 16));
 #pragma unroll
                     for (int e = 0; e < WPR; ++e) pair[e] = next[e];
-                    fetch(n + F::TEAMS, page);
-                    page = page_of(n + 2 * F::TEAMS, lane);
                     wait_empty();
                     if (dead) break;
                     uint8_t *to = ring + load.at * F::TILE_BYTES;
@@ -680,6 +697,8 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     }
                     arrive(load);
                     load.forward(F::TEAMS, R);
+                    fetch(n + F::TEAMS, page);
+                    page = page_of(n + 2 * F::TEAMS, lane);
                 }
                 cp_wait<0>();
             } else {
