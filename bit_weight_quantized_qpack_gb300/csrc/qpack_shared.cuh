@@ -22,11 +22,10 @@
 // second product, so that neither leaves the SM nor passes through shared memory. Units, a tile for one block of queries, are cut
 // evenly over the blocks whatever the groups' lengths; a block that gets part of a prefix leaves a piece.
 //   A tile at a time by all warps took 760 us for the 65531 tokens, roles of their own 226, codes staged asynchronously 180,
-// addresses by a lane a row 150, products issued by a converged
-// warp and two teams of loaders 140, the joins' warps 132, weights by the maximum that there is 123, queries' lines
-// asked for ahead 119. Slower: halves of 64 tokens
-// with two score buffers a group (149 against 137), one team (150), rows' own tokens attended to within the join (fp32, a lane
-// a token out of shared memory: 28 us more for 64 rows of up to 200).
+// addresses by a lane a row 150, products issued by a converged warp and two teams of loaders 140, the joins' warps 132,
+// weights by the maximum that there is 123, queries' lines asked for ahead 119. Slower: halves of 64 tokens with two score
+// buffers a group (149 against 137), one team (150), rows' own tokens attended to within the join (fp32, a lane a token out of
+// shared memory: 28 us more for 64 rows of up to 200).
 //
 // Terms. fp32 queries (and rotated ones of 16 bits) are two 16-bit terms over fp16 values, weights two where the output or the
 // cache asks for it; a second term of the queries doubles that product, and blocks of 128 queries are then taken one at a time.
