@@ -294,6 +294,11 @@ template <int N> __device__ __forceinline__ void load_q(const void *p, int dt, i
     }
 }
 
+// A bounded wait of a whole warp, which gives up together: lanes that did alone would leave the others in the shuffles behind it.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+}
+
 template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_kernel(const __grid_constant__ Params p) {
     using F = Cfg<KT, D>;
     constexpr int TOK = F::TOK, PS = F::PS;
@@ -528,7 +533,7 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
             {
                 auto scores = [&](int j) {
                     const int mb = dual ? j & 1 : 0;
-                    if (!dual || mb == 0) dead = dead || !mbar_wait_bounded(&full[keys.at], keys.phase);
+                    if (!dual || mb == 0) dead = dead || !warp_wait(&full[keys.at], keys.phase);
                     if (dead) return;
                     tc_fence_after();
                     const uint32_t kd = desc_k(ring32 + keys.at * F::TILE_BYTES);
@@ -554,8 +559,8 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                 if (jobs > 1) scores(1);
                 for (int j = 0; j < jobs && !dead; ++j) {
                     const int mb = dual ? j & 1 : 0, t = dual ? j >> 1 : j;
-                    if (!dual || mb == 0) dead = dead || !mbar_wait_bounded(&full[values.at], values.phase);
-                    dead = dead || !mbar_wait_bounded(&p_full[j & 1], j & 1 ? p_phase1 : p_phase);
+                    if (!dual || mb == 0) dead = dead || !warp_wait(&full[values.at], values.phase);
+                    dead = dead || !warp_wait(&p_full[j & 1], j & 1 ? p_phase1 : p_phase);
                     if (j & 1) p_phase1 ^= 1; else p_phase ^= 1;
                     if (dead) break;
                     tc_fence_after();
@@ -617,7 +622,7 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                 return -1;
             };
             auto slot_of = [&](int t0, int j) -> unsigned { return slots + (unsigned(t0 + row_of(j)) & within); };
-            auto wait_empty = [&] { dead = dead || !mbar_wait_bounded(&empty[load.at], load.phase ^ 1); };
+            auto wait_empty = [&] { dead = dead || !warp_wait(&empty[load.at], load.phase ^ 1); };
             auto arrive = [&](const Slot &at) {
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -742,12 +747,9 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                 const uint32_t sc = lanes + F::S_COL + (j & 1) * F::S_STEP;
                 // (a group that has its own score buffer keeps its phase in s_phase)
                 const int phase = TWO || !(j & 1) ? s_phase : s_phase1;
-                const bool seen = !dead && mbar_wait_bounded(&s_full[j & 1], phase);
+                dead = dead || !warp_wait(&s_full[j & 1], phase);
                 if (TWO || !(j & 1)) s_phase ^= 1; else s_phase1 ^= 1;
-                if (!__all_sync(0xffffffffu, seen)) {
-                    dead = true;
-                    break;
-                }
+                if (dead) break;
                 tc_fence_after();
                 if (!TWO) pv_phase ^= 1;
                 if (idle) {
@@ -832,11 +834,8 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     if (any) {
                         l *= shrink;
                         if (!TWO) {                        // the previous tile's product may still be adding
-                            const bool there = mbar_wait_bounded(pv_done, pv_phase);
-                            if (!__all_sync(0xffffffffu, there)) {
-                                dead = true;
-                                break;
-                            }
+                            dead = !warp_wait(pv_done, pv_phase);
+                            if (dead) break;
                             tc_fence_after();
                         }
 #pragma unroll 1
@@ -905,7 +904,7 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[j & 1]);
             }
-            if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_bounded(o_done, o_phase));
+            dead = dead || !warp_wait(o_done, o_phase);
             tc_fence_after();
         }
         o_phase ^= 1;
