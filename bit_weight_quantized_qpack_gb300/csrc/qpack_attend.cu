@@ -13,6 +13,9 @@ template <> cudaError_t launch<QPACK_KV_BF16>(const AttendArgs &, cudaStream_t);
 template <> int64_t workspace<QPACK_KV_I8>(const qpack_kv_pool_t &, int, int);
 template <> int64_t workspace<QPACK_KV_F16>(const qpack_kv_pool_t &, int, int);
 template <> int64_t workspace<QPACK_KV_BF16>(const qpack_kv_pool_t &, int, int);
+template <> bool fits<QPACK_KV_I8>(const qpack_kv_pool_t &, const qpack_kv_tables_t &, int);
+template <> bool fits<QPACK_KV_F16>(const qpack_kv_pool_t &, const qpack_kv_tables_t &, int);
+template <> bool fits<QPACK_KV_BF16>(const qpack_kv_pool_t &, const qpack_kv_tables_t &, int);
 template <> cudaError_t fault_word<QPACK_KV_I8>(int **);
 template <> cudaError_t fault_word<QPACK_KV_F16>(int **);
 template <> cudaError_t fault_word<QPACK_KV_BF16>(int **);
@@ -25,6 +28,12 @@ int64_t kv_attend_workspace(const qpack_kv_pool_t &pool, int q_heads) {
     else if (pool.type == QPACK_KV_F16) parts = attend::workspace<QPACK_KV_F16>(pool, q_heads, grid);
     else parts = attend::workspace<QPACK_KV_BF16>(pool, q_heads, grid);
     return int64_t(attend::MAX_COUNTERS) * 4 + parts;
+}
+
+bool kv_attend_fits(const qpack_kv_pool_t &pool, const qpack_kv_tables_t &t, int q_heads) {
+    if (pool.type == QPACK_KV_I8) return attend::fits<QPACK_KV_I8>(pool, t, q_heads);
+    if (pool.type == QPACK_KV_F16) return attend::fits<QPACK_KV_F16>(pool, t, q_heads);
+    return attend::fits<QPACK_KV_BF16>(pool, t, q_heads);
 }
 
 cudaError_t launch_kv_attend(const AttendArgs &a, cudaStream_t s) {

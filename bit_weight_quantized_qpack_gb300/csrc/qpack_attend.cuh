@@ -1094,6 +1094,16 @@ inline int groups(const qpack_kv_pool_t &pool, int q_heads) {
     return q_heads / pool.heads > 8 && pool.dim <= 128 ? 2 : 1;
 }
 
+// Rows a launch: bounded by the kernel's tables, and tile numbers stay below 2^31 whatever the lengths are (0: one row's do not).
+template <int KT, int D, int NT> int rows_a_launch(const qpack_kv_pool_t &pool, const qpack_kv_tables_t &t, int q_heads) {
+    using F = Cfg<KT, D, NT>;
+    const int G = q_heads / pool.heads, HC = pool.heads * ((G + 8 * NT - 1) / (8 * NT));
+    const int64_t most = (int64_t(t.max_pages) * pool.page_tokens + F::TOK - 1) / F::TOK + 1 + SETUP;
+    const int64_t fit = 0x7FFF0000 / (most * HC);
+    const int rows = MAX_COUNTERS / (HC * F::SLICES) < MAX_ROWS ? MAX_COUNTERS / (HC * F::SLICES) : MAX_ROWS;
+    return fit < rows ? int(fit) : rows;
+}
+
 template <int KT, int D, int NT> int64_t part_bytes(int grid) {
     using F = Cfg<KT, D, NT>;
     return int64_t(grid) * (2 * F::VEC * 24 + F::W * F::PF * 4);
@@ -1101,6 +1111,8 @@ template <int KT, int D, int NT> int64_t part_bytes(int grid) {
 
 template <int KT, int D, int NT> cudaError_t run(const AttendArgs &a, cudaStream_t s) {
     using F = Cfg<KT, D, NT>;
+    const int rows = rows_a_launch<KT, D, NT>(a.pool, a.t, a.q_heads);
+    if (rows < 1) return cudaErrorNotSupported;
     static int opted[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1118,17 +1130,10 @@ template <int KT, int D, int NT> cudaError_t run(const AttendArgs &a, cudaStream
     p.a = a;
     p.G = a.q_heads / a.pool.heads;
     p.C = (p.G + 8 * NT - 1) / (8 * NT);
-    const int HC = a.pool.heads * p.C;
     p.counters = static_cast<int *>(a.ws);
     p.block_parts = reinterpret_cast<float4 *>(p.counters + MAX_COUNTERS);
     p.block_sums = reinterpret_cast<float2 *>(p.block_parts + int64_t(grid) * 2 * F::VEC);
     p.warp_parts = reinterpret_cast<float *>(p.block_sums + int64_t(grid) * 2 * F::VEC);
-    // Rows a launch: bounded by the kernel's tables, and tile numbers stay below 2^31 whatever the lengths are.
-    const int64_t most = (int64_t(a.t.max_pages) * a.pool.page_tokens + F::TOK - 1) / F::TOK + 1 + SETUP;
-    const int64_t fit = 0x7FFF0000 / (most * HC);
-    if (fit < 1) return cudaErrorNotSupported;
-    int rows = MAX_COUNTERS / (HC * F::SLICES) < MAX_ROWS ? MAX_COUNTERS / (HC * F::SLICES) : MAX_ROWS;
-    if (fit < rows) rows = int(fit);
     for (int r = 0; r < a.B; r += rows) {
         p.row0 = r;
         p.B = a.B - r < rows ? a.B - r : rows;
@@ -1151,6 +1156,7 @@ template <int KT, int D, int NT> cudaError_t run(const AttendArgs &a, cudaStream
 // What each cache type's translation unit defines.
 template <int KT> cudaError_t launch(const AttendArgs &a, cudaStream_t s);
 template <int KT> int64_t workspace(const qpack_kv_pool_t &pool, int q_heads, int grid);
+template <int KT> bool fits(const qpack_kv_pool_t &pool, const qpack_kv_tables_t &t, int q_heads);
 template <int KT> cudaError_t fault_word(int **word);
 
 #define QPACK_ATTEND_TYPE(KT)                                                                                         \
@@ -1167,6 +1173,13 @@ template <int KT> cudaError_t fault_word(int **word);
         if (pool.dim == 64) return nt == 2 ? part_bytes<KT, 64, 2>(grid) : part_bytes<KT, 64, 1>(grid);               \
         if (pool.dim == 128) return nt == 2 ? part_bytes<KT, 128, 2>(grid) : part_bytes<KT, 128, 1>(grid);            \
         return part_bytes<KT, 256, 1>(grid);                                                                          \
+    }                                                                                                                 \
+    template <> bool fits<KT>(const qpack_kv_pool_t &pool, const qpack_kv_tables_t &t, int q_heads) {                 \
+        const int nt = groups(pool, q_heads);                                                                         \
+        auto *const rows = pool.dim == 64 ? (nt == 2 ? rows_a_launch<KT, 64, 2> : rows_a_launch<KT, 64, 1>)           \
+                           : pool.dim == 128 ? (nt == 2 ? rows_a_launch<KT, 128, 2> : rows_a_launch<KT, 128, 1>)      \
+                                             : rows_a_launch<KT, 256, 1>;                                             \
+        return rows(pool, t, q_heads) > 0;                                                                            \
     }                                                                                                                 \
     template <> cudaError_t fault_word<KT>(int **word) {                                                              \
         return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_fault_attend);                                 \

@@ -109,6 +109,7 @@ struct AttendArgs {
     const int *from;             // null, or each row's first token (on the device)
 };
 cudaError_t launch_kv_attend(const AttendArgs &a, cudaStream_t s);
+bool kv_attend_fits(const qpack_kv_pool_t &pool, const qpack_kv_tables_t &t, int q_heads);  // else launch_kv_attend refuses
 int64_t kv_attend_workspace(const qpack_kv_pool_t &pool, int q_heads);
 
 // Attention where groups of rows share a prefix (qpack_shared.cu).

@@ -59,6 +59,7 @@ cudaError_t launch_kv_attend_shared(const SharedArgs &a, cudaStream_t s) {
     const int64_t tokens = int64_t(a.t.max_pages) * a.pool.page_tokens, tiles = (tokens + 63) / 64;
     const int64_t items = (int64_t(a.B) * p.G / shared::ROWS + 1 + a.groups) * a.pool.heads;
     if (tokens > 0x7FFFFF00 || items * tiles >= (int64_t(1) << 30)) return cudaErrorNotSupported;
+    if (!kv_attend_fits(a.pool, a.t, a.q_heads)) return cudaErrorNotSupported;      // before anything is launched
     if (a.pool.type == QPACK_KV_I8) return shared::launch<QPACK_KV_I8>(p, s);
     if (a.pool.type == QPACK_KV_F16) return shared::launch<QPACK_KV_F16>(p, s);
     return shared::launch<QPACK_KV_BF16>(p, s);
