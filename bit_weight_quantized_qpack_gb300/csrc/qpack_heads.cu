@@ -18,6 +18,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
+
 #include "qpack_dev.cuh"
 #include "qpack_launch.h"
 #include "qpack_paged.cuh"
@@ -91,6 +93,16 @@ __device__ __forceinline__ int position(const HeadsArgs &a, int64_t i, bool repo
     return max(len, 0) - 1;
 }
 
+// The sum of a head's squares.
+template <int RUN, int G> __device__ __forceinline__ float squares(const float (&y)[2 * RUN]) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 2 * RUN; ++e) sum = fmaf(y[e], y[e], sum);
+#pragma unroll
+    for (int o = G / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
 // G lanes a head: dim <= 2 RUN G. NEAR: pairs are neighbours.
 template <int XT, int OT, int RUN, int G, bool NEAR>
 __global__ void __launch_bounds__(WARPS * 32) heads_kernel(HeadsArgs a, int64_t first, unsigned items, unsigned q_groups,
@@ -149,12 +161,26 @@ __global__ void __launch_bounds__(WARPS * 32) heads_kernel(HeadsArgs a, int64_t 
         widen<XT, RUN>(raw[u][0], y);
         widen<XT, RUN>(raw[u][1], y + RUN);
         if (x.weight) {                                    // the same for the whole warp
-            float sum = 0.0f;
+            float mean = __fdiv_rn(squares<RUN, G>(y), float(D)) + a.eps;
+            const bool low = mean < 0x1p-100f;
+            const bool rare = low || !(mean <= FLT_MAX);
+            if (__any_sync(0xffffffffu, rare)) {
+                // Squares that pass fp32, or vanish in it beside an eps that is as small: the head by a power of two that brings its
+                // largest element to 1, eps by the square of it. (With an eps, 2^-149 or more, 2^74 is enough: what is small then
+                // is small beside eps.) A head without a largest element, or with an infinite or NaN one, stays.
+                float big = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 2 * RUN; ++e) sum = fmaf(y[e], y[e], sum);
+                for (int e = 0; e < 2 * RUN; ++e) big = fmaxf(big, fabsf(y[e]));
 #pragma unroll
-            for (int o = G / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float r = __frsqrt_rn(__fdiv_rn(sum, float(D)) + a.eps);
+                for (int o = G / 2; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                const int ex = __float_as_int(big) >> 23;
+                const int up = min(max(254 - ex, 1), low && a.eps > 0.0f ? 127 + 74 : 254);
+                const float g = !rare || big == 0.0f || ex == 255 ? 1.0f : __int_as_float(up << 23);
+#pragma unroll
+                for (int e = 0; e < 2 * RUN; ++e) y[e] *= g;
+                mean = __fdiv_rn(squares<RUN, G>(y), float(D)) + a.eps * g * g;
+            }
+            const float r = __frsqrt_rn(mean);
 #pragma unroll
             for (int e = 0; e < 2 * RUN; ++e) y[e] = y[e] * r * w[e];
         }

@@ -362,7 +362,8 @@ int qpack_kv_page_workspace(const qpack_kv_pool_t *pool, const qpack_kv_tables_t
  *              the outputs overlap nothing.
  *    weight    [dim] fp32, 16-byte aligned, or NULL
  *  dim         elements of a head, a multiple of 8, 8 to 256
- *  eps         >= 0, finite (used with a weight only)
+ *  eps         >= 0, finite (used with a weight only; a head of zeros with an eps of 0 is NaN). The mean of squares may lie outside
+ *              fp32's range: a head for which it does is scaled by a power of two for it.
  *  rope        NULL (no rotation), or [rope_rows, rope_dim] fp32, 16-byte aligned: row p holds cos (rope_dim / 2) and sin
  *              (rope_dim / 2) of position p (whatever scaling a long context asks for is in the table)
  *  rope_dim    a multiple of 8, at most dim (0 without rope)
