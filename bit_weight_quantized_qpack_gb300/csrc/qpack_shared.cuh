@@ -928,7 +928,7 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                 const float2 him = ml[(wg ^ 1) * ROWS + row];
                 const float both = fmaxf(m, him.x), at = both == -INFINITY ? 0.0f : both;
                 mine = m == -INFINITY ? 0.0f : ex2((m - at) * f);
-                l = l * mine + (him.x == -INFINITY ? 0.0f : him.y * ex2((him.x - at) * f));
+                l = l * mine + (him.y == 0.0f ? 0.0f : him.y * ex2((him.x - at) * f));    // (a sum of NaN counts)
                 m = both;
                 named_bar_sync(2, 2 * SOFT * 32);
             }
