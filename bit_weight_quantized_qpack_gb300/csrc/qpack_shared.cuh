@@ -502,7 +502,8 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     const float g = __int_as_float((up << 23) | (__float_as_int(a.scale) & 0x80000000));
                     const float back = __int_as_float(max(254 - up, 1) << 23);
                     const float factor = fabsf(a.scale) * 1.4426950408889634f * back * (up == 254 ? 0.5f : 1.0f);
-                    if (sub == 0) x_scale[r] = factor == 0.0f ? 0x1p-126f : factor;
+                    // An infinite query is NaN, whatever signs its scores have: were all of them -inf, they would count as none.
+                    if (sub == 0) x_scale[r] = ex == 255 ? __int_as_float(0x7FC00000) : factor == 0.0f ? 0x1p-126f : factor;
                     const int block = r / ROWS, row = r % ROWS;
 #pragma unroll
                     for (int s = 0; s < 2; ++s)

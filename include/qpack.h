@@ -302,8 +302,9 @@ int qpack_kv_attend_workspace(const qpack_kv_pool_t *pool, int B, int q_heads, i
  * Scores, maxima, sums and accumulators are fp32. Over the prefix, queries enter the tensor cores as two 16-bit terms (22 bits
  * where the pool is 8-bit or fp16, 16 where it is bf16; one term where that holds them whole), probabilities as one (11 bits)
  * where the pool is 8-bit or fp16 and the output has 16 bits, else as two. Own tokens are attended to as by qpack_kv_attend.
- * A prefix's key that is not finite makes the heads of its group that see it NaN, a value its own element (that element may be NaN
- * in rows that end before it too); everything else keeps its bits.
+ * A prefix's key that is not finite may make the heads of its group that see it NaN, a value that is not makes its own element
+ * infinite or NaN (NaN, perhaps, in rows that end before it too); everything else keeps its bits. A query that is not finite
+ * makes its own head NaN.
  * The other arguments, limits and errors are qpack_kv_attend's; QPACK_ERR_UNSUPPORTED also where a row of the table could hold
  * more than 2^31 - 256 tokens, or its tiles of 64 tokens for all queries in blocks of 128 (one more a group) come to 2^30.
  *  ws      at least qpack_kv_shared_workspace bytes for this B or more, 16-byte aligned, the first QPACK_KV_ATTEND_ZEROED of
