@@ -472,7 +472,7 @@ int qpack_kv_attend_shared(const qpack_kv_pool_t *pool, int layer, const qpack_k
     if (!ws) return QPACK_ERR_ARG;
     if (ws_bytes < kv_shared_workspace(*pool, B, q_heads)) return QPACK_ERR_SHAPE;
     SharedArgs a = {*pool, *t, seqs, first, prefix, q, ldq, rope, rope_rows, out, ldo, lse, ws, scale, layer, B, groups, q_heads,
-                    qdt, odt, 0, 0};
+                    qdt, odt, 0};
     const cudaError_t e = launch_kv_attend_shared(a, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaErrorNotSupported ? QPACK_ERR_UNSUPPORTED : cuda_status(e);
 }

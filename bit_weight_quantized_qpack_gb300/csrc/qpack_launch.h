@@ -128,7 +128,7 @@ struct SharedArgs {
     void *ws;
     float scale;
     int layer, B, groups, q_heads, qdt, odt;
-    int q_terms, p_terms;        // 16-bit terms of queries and probabilities, set by the launcher
+    int q_terms;                 // 16-bit terms of queries, set by the launcher
 };
 cudaError_t launch_kv_attend_shared(const SharedArgs &a, cudaStream_t s);
 int64_t kv_shared_workspace(const qpack_kv_pool_t &pool, int64_t B, int q_heads);

@@ -48,12 +48,9 @@ cudaError_t launch_kv_attend_shared(const SharedArgs &a, cudaStream_t s) {
     p.a = a;
     p.G = a.q_heads / a.pool.heads;
     // Queries of the products' own type that are not rotated are one term as they stand (a power of two that they are scaled
-    // by changes no bit of an fp16 query that is not subnormal after it; see the kernel). Probabilities of one fp16 term are off by
-    // 2^-11 each, less than an output of 16 bits shows once they are averaged; of one bfloat16 term by 2^-8, so a bfloat16 cache
-    // takes two, and an fp32 output too.
+    // by changes no bit of an fp16 query that is not subnormal after it; see the kernel).
     const bool bf = a.pool.type == QPACK_KV_BF16;
     p.a.q_terms = !a.rope && a.qdt == (bf ? QPACK_BF16 : QPACK_F16) ? 1 : 2;
-    p.a.p_terms = bf || a.odt == QPACK_F32 ? 2 : 1;
     shared::lay_out(a.pool, a.B, a.q_heads, static_cast<unsigned char *>(a.ws), p.w);
     // tokens up to the end of a last tile and the units of a call are counted in 31 bits
     const int64_t tokens = int64_t(a.t.max_pages) * a.pool.page_tokens, tiles = (tokens + 63) / 64;

@@ -27,8 +27,10 @@
 // buffers a group (149 against 137), one team (150), rows' own tokens attended to within the join (fp32, a lane a token out of
 // shared memory: 28 us more for 64 rows of up to 200).
 //
-// Terms. fp32 queries (and rotated ones of 16 bits) are two 16-bit terms over fp16 values, weights two where the output or the
-// cache asks for it; a second term of the queries doubles that product, and blocks of 128 queries are then taken one at a time.
+// Terms. fp32 queries (and rotated ones of 16 bits) are two 16-bit terms; a second term of the queries doubles that product, and
+// blocks of 128 queries are then taken one at a time. Weights are always two: of one (fp16: 11 bits, off by up to 2^-11 against
+// the sum, which is of unrounded weights) a 16-bit output showed the error, 2.3e-4 to 2.5e-4 of it where its own rounding alone is
+// 2.1e-4. us a call, one term / two: 64 rows of 7999 tokens 49.2 / 50.2, 32 of 65531 124 / 141, heads of 256 45.1 / 45.9.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -88,7 +90,7 @@ template <int KT, int D> struct Cfg {
     // columns of first terms, 16 of second ones.
     static constexpr int O_COL = 0, O_STEP = D, S_COL = 256, S_STEP = TOK;
     // Probabilities are held as 2^(x - m + BIAS), at most 2^(BIAS + GROW): m is a maximum that lags behind by up to GROW.
-    static constexpr float BIAS = BF ? 0.0f : 7.0f, GROW = 8.0f;
+    static constexpr float BIAS = BF ? 0.0f : 7.0f, GROW = 8.0f;      // (fp16 ends at 2^16)
     // Shared memory: the queries (one or two operands), 8-bit codes on their way (a tile a team), a ring of tiles of 16-bit keys or
     // values, the plan and the barriers. The results of a segment are put together over the first three.
     static constexpr int SMEM = 227 * 1024, REST = (MAX_GROUPS + 1) * 4 + (TWO ? 2 : 1) * ROWS * 4 + 256;
@@ -568,7 +570,7 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     const uint32_t vd = desc_mn(ring32 + values.at * F::TILE_BYTES, F::KB);
                     const uint32_t o = tmem + F::O_COL + (TWO ? (j & 1) * F::O_STEP : 0), w = tmem + F::S_COL + (j & 1) * F::S_STEP;
                     const bool more = TWO ? j > 1 : j > 0; // the accumulators hold something
-                    for (int term = 0; term < a.p_terms; ++term)
+                    for (int term = 0; term < 2; ++term)
 #pragma unroll
                         for (int k = 0; k < TOK / 16; ++k)
                             umma_ts(one, o, w + (k / 2) * 32 + term * 16 + (k % 2) * 8, vd + k * (2048 / 16), kIdesc<BF, D, true>,
@@ -741,7 +743,6 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
             const uint32_t lanes = tmem + (uint32_t(32 * (warp % SOFT)) << 16);
             const uint32_t o = lanes + F::O_COL + (TWO ? wg * F::O_STEP : 0);
             bool any = false;                              // the accumulators hold something
-            const bool many = (TWO && !dual ? nt / 2 : nt) >= 8;
             const bool idle = (dual ? wg * ROWS : 0) + 32 * (warp % SOFT) >= live;     // no queries in this warp's lanes
             for (int j = TWO ? wg : wg * jobs; j < jobs; j += TWO ? 2 : 1) {
                 const int left = lim - (sg.tile0 + (dual ? j >> 1 : j)) * TOK;
@@ -758,54 +759,6 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     continue;
                 }
                 const bool all = __all_sync(0xffffffffu, left >= TOK);
-                // The maximum lags, so nearly every tile but the first is weighed by the one that there is: weights and the tile's
-                // maximum in one go, the weights kept until it is known that they hold (over the scores they could not be taken
-                // back). Where they do not, or are two terms, maximum first and weights then; so too where a group has few tiles, which do not
-                // pay for one more path's cold instructions (1.3 us; 0.35 us gained a tile of 2 x 128 queries: 32 rows of 65531 tokens 132 ->
-                // 122 us, 64 of 7999, with four tiles a group, 45.8 -> 47.1).
-                if (!BF && any && all && many && a.p_terms == 1) {
-                    const float by = m == -INFINITY ? 0.0f : m;
-                    float2 sum = make_float2(0.0f, 0.0f), sum1 = sum;
-                    float t0 = -INFINITY, t1 = -INFINITY;
-                    uint32_t h[TOK / 2], x[8], y[8];
-                    auto part = [&](int c, const uint32_t (&z)[8]) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 v = make_float2(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1]));
-                            if (i & 1) t1 = max3(t1, v.x, v.y); else t0 = max3(t0, v.x, v.y);
-                            float2 e = fma2(sub2(v, by), f, F::BIAS);
-                            e = make_float2(ex2(e.x), ex2(e.y));
-                            if (i & 1) sum1 = add2(sum1, e); else sum = add2(sum, e);
-                            h[c / 2 + i] = pack2<BF>(e.x, e.y);
-                        }
-                    };
-                    tmem_ld8(sc, x);
-#pragma unroll
-                    for (int c = 0; c < TOK; c += 16) {
-                        tmem_ld_wait();
-                        tmem_ld8(sc + c + 8, y);
-                        part(c, x);
-                        tmem_ld_wait();
-                        if (c + 16 < TOK) tmem_ld8(sc + c + 16, x);
-                        part(c + 8, y);
-                    }
-                    const float top = fmaxf(t0, t1);
-                    if (!__any_sync(0xffffffffu, top > m && !((top - m) * f <= F::GROW))) {
-#pragma unroll
-                        for (int c = 0; c < TOK; c += 32) {
-                            uint32_t w[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) w[i] = h[c / 2 + i];
-                            tmem_st16(sc + c, w);
-                        }
-                        l += sum.x + sum.y + (sum1.x + sum1.y);
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&p_full[j & 1]);
-                        continue;
-                    }
-                }
                 float top = -INFINITY;
 #pragma unroll 1
                 for (int c = 0; c < TOK; c += 64) {
@@ -860,44 +813,31 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     if (!all) e = make_float2(c < left ? e.x : 0.0f, c + 1 < left ? e.y : 0.0f);
                     return e;
                 };
-                if (BF || a.p_terms == 2) {
-#pragma unroll 1
-                    for (int c = 0; c < TOK; c += 32) {
-                        uint32_t x[32], h[16], g[16];
-                        tmem_ld32(sc + c, x);
-                        tmem_ld_wait();
+                // two terms, 16 scores' loads under the weights of the 16 before: those of 32 tokens go over their scores, the
+                // second terms of the first 16 once the other 16 scores are here
+                uint32_t x[16], y[16], h[8], g[8];
+                auto half = [&](int c, const uint32_t (&z)[16]) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 e = weigh(c + 2 * i, x[2 * i], x[2 * i + 1]);
-                            if (i & 1) sum1 = add2(sum1, e); else sum = add2(sum, e);
-                            h[i] = pack2<BF>(e.x, e.y);
-                            g[i] = rest2<BF>(e.x, e.y, h[i]);
-                        }
-                        tmem_st16(sc + c, h);
-                        tmem_st16(sc + c + 16, g);
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 e = weigh(c + 2 * i, z[2 * i], z[2 * i + 1]);
+                        if (i & 1) sum1 = add2(sum1, e); else sum = add2(sum, e);
+                        h[i] = pack2<BF>(e.x, e.y);
+                        g[i] = rest2<BF>(e.x, e.y, h[i]);
                     }
-                } else {                                   // 16 scores' loads under the weights of the 16 before
-                    uint32_t x[16], y[16];
-                    auto half = [&](int c, const uint32_t (&z)[16]) {
-                        uint32_t h[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float2 e = weigh(c + 2 * i, z[2 * i], z[2 * i + 1]);
-                            if (i & 1) sum1 = add2(sum1, e); else sum = add2(sum, e);
-                            h[i] = pack2<BF>(e.x, e.y);
-                        }
-                        tmem_st8(sc + c / 32 * 32 + c % 32 / 2, h);
-                    };
-                    tmem_ld16(sc, x);
+                };
+                tmem_ld16(sc, x);
 #pragma unroll 1
-                    for (int c = 0; c < TOK; c += 32) {
-                        tmem_ld_wait();
-                        tmem_ld16(sc + c + 16, y);
-                        half(c, x);
-                        tmem_ld_wait();
-                        if (c + 32 < TOK) tmem_ld16(sc + c + 32, x);
-                        half(c + 16, y);
-                    }
+                for (int c = 0; c < TOK; c += 32) {
+                    tmem_ld_wait();
+                    tmem_ld16(sc + c + 16, y);
+                    half(c, x);
+                    tmem_st8(sc + c, h);
+                    tmem_ld_wait();
+                    tmem_st8(sc + c + 16, g);
+                    if (c + 32 < TOK) tmem_ld16(sc + c + 32, x);
+                    half(c + 16, y);
+                    tmem_st8(sc + c + 8, h);
+                    tmem_st8(sc + c + 24, g);
                 }
                 l += sum.x + sum.y + (sum1.x + sum1.y);
                 tmem_st_wait();

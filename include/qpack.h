@@ -294,14 +294,15 @@ int qpack_kv_attend_workspace(const qpack_kv_pool_t *pool, int B, int q_heads, i
  * Rows first[g] .. first[g + 1] - 1 are group g; they share the first prefix[g] tokens, which are read from the pages of the
  * group's first row. Of a row's sequence (seqs as above, L = lens) the tokens t < min(L, prefix[g]) are those, and the tokens
  * prefix[g] <= t < L are its own. Rows of no group have no prefix. With sequences that share their prefixes by
- * qpack_kv_fork (full pages are the same, a last page that is not full is a copy) the result is qpack_kv_attend's.
+ * qpack_kv_fork (full pages are the same, a last page that is not full is a copy) the result is qpack_kv_attend's but for
+ * the terms below and the order of sums.
  *  first   [groups + 1] int32, rising from 0 or more to at most B (equal neighbours: a group without rows); anything else sets
  *          QPACK_FAULT_PAGE, and all rows go without a prefix. May be NULL where groups is 0.
  *  prefix  [groups] int32, 0 to the length of the group's first row; others are cut to that and set QPACK_FAULT_PAGE
  *  groups  at most 512
- * Scores, maxima, sums and accumulators are fp32. Over the prefix, queries enter the tensor cores as two 16-bit terms (22 bits
- * where the pool is 8-bit or fp16, 16 where it is bf16; one term where that holds them whole), probabilities as one (11 bits)
- * where the pool is 8-bit or fp16 and the output has 16 bits, else as two. Own tokens are attended to as by qpack_kv_attend.
+ * Scores, maxima, sums and accumulators are fp32. Over the prefix, queries and probabilities enter the tensor cores as two 16-bit
+ * terms each (22 bits where the pool is 8-bit or fp16, 16 where it is bf16; a query is one term where that holds it whole: fp16,
+ * or bf16 over a bf16 pool, without rope). Own tokens are attended to as by qpack_kv_attend.
  * A prefix's key that is not finite may make the heads of its group that see it NaN, a value that is not makes its own element
  * infinite or NaN (NaN, perhaps, in rows that end before it too); everything else keeps its bits. A query that is not finite
  * makes its own head NaN.
