@@ -104,6 +104,8 @@ def main(argv=None):
     ap.add_argument("--check", action="store_true")
     a = ap.parse_args(argv)
     n, per = len(a.prompts), a.samples
+    if min(per, a.steps, *a.prompts) < 1 or n * per > 16:
+        ap.error("prompts, samples and steps start at 1; prompts x samples go to 16, what qgemm_small takes")
     rows, top = n * per, max(a.prompts) + a.steps
     model = Model(a.layers, a.q_heads, a.kv_heads, a.dim, a.ffn, top, qp.Q4G32)
     d = Sampler(model, n * (per + 1), top, a.page, n * (per + 1) * -(-top // a.page), a.vocab, rows)
@@ -122,7 +124,7 @@ def main(argv=None):
     first_logits = d.logits(x[ends]).repeat_interleave(per, 0)
     qp.qpack_sample(first_logits, u[0], tokens=last, **sampling)
     answers[0] = last
-    graph, t0, logits = None, 0.0, None
+    graph, t0, logits, replayed = None, 0.0, None, max(0, a.steps - 3)
     for i in range(1, a.steps):
         next_u.copy_(u[i])
         if graph is None:
@@ -138,9 +140,9 @@ def main(argv=None):
         answers[i] = now
         last.copy_(now)
     torch.cuda.synchronize()
-    ms = (time.perf_counter() - t0) / max(1, a.steps - 3) * 1e3
+    speed = f"{(time.perf_counter() - t0) / replayed * 1e3:.2f} ms a replayed step" if replayed else "no step replayed"
     flags = qp.qpack_fetch_fault_flags()
-    print(f"{per} answers each to prompts of {a.prompts} tokens, {a.steps} tokens long, {a.layers} layers: {ms:.2f} ms a replayed step"
+    print(f"{per} answers each to prompts of {a.prompts} tokens, {a.steps} tokens long, {a.layers} layers: {speed}"
           + (f" (worst attention error {d.worst:.2e})" if a.check else "") + f", fault flags {flags}")
     return dict(answers=answers, logits=logits, u=u, last=last, worst=d.worst, flags=flags, decoder=d, first_logits=first_logits, seqs=seqs,
                 sampling=sampling, step=lambda t, uu, out: d.step(seqs, t, first, prefix, uu, out, sampling, True))

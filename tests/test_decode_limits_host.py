@@ -3,7 +3,10 @@ arguments."""
 import os
 import re
 
-CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_weight_quantized_qpack_gb300", "csrc")
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "bit_weight_quantized_qpack_gb300", "csrc")
 
 
 def library():
@@ -42,3 +45,15 @@ def test_shared_refuses_what_the_attention_behind_it_would():
     import torch
     if not torch.cuda.is_available():
         assert call_shared(qp, **{**many, "max_pages": (1 << 27) // 16 // 16}) not in (0, UNSUPPORTED)
+
+
+@pytest.mark.parametrize("args", [["--samples", "5"], ["--samples", "0"], ["--steps", "0"], ["--prompts", "4", "0"],
+                                  ["--prompts"] + ["1"] * 17 + ["--samples", "1"]])
+def test_example_refuses_what_it_cannot_run(args, capsys):
+    """More rows than qgemm_small takes, and nothing to do: said before anything is set up."""
+    import sys
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    import sampled_decode
+    with pytest.raises(SystemExit):
+        sampled_decode.main(args)
+    assert "prompts x samples" in capsys.readouterr().err
