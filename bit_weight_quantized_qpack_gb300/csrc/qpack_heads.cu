@@ -1,19 +1,20 @@
 // qpack_heads.cu — the root-mean-square norm of query and key heads with the position rotation in the same pass.
 //
-// The mathematics. A head x of `dim` elements becomes y = x / sqrt(mean(x^2) + eps) * w (or x where it has no weight), and
-// of its first `turn` elements the pairs (a, b) of position p become (a c - b s, b c + a s), c and s from row p of the
-// table: pairs (i, i + turn / 2), or neighbours (2i, 2i + 1). Every operation is fp32 and rounded by itself, products
-// before their sum, as the cache's append has it: without a weight the rotated keys are those that append would store.
+// The mathematics. A head x of `dim` elements becomes y = x / sqrt(mean(x^2) + eps) * w (or x where it has no weight;
+// a head whose squares leave fp32's range is scaled by a power of two for its mean), and of its first `turn` elements
+// the pairs (a, b) of position p become (a c - b s, b c + a s), c and s from row p of the table: pairs (i, i + turn /
+// 2), or neighbours (2i, 2i + 1). Every operation is fp32 and rounded by itself, products before their sum, as the
+// cache's append has it: without a weight the rotated keys are those that append would store.
 //
-// What bounds it. Each element is read and written once, and one row of the table is read for all heads of a token: the
-// copy rate at length (8191 bfloat16 tokens of 40 heads of 128: 38 us, 67% of it; the chain position -> table row -> store in
-// the warps that fit an SM), the launch and that chain at a decode step's few tokens (2.1 us in a graph, 10.5 by a call from
-// Python, whose host time that is).
+// What bounds it. Each element is read and written once, and one row of the table is read for all heads of a token:
+// the copy rate at length (8191 tokens of 40 heads of 128: bfloat16 38 us, 67% of it, fp32 53.5 us, 94%; the chain
+// position -> table row -> store in the warps that fit an SM), the launch and that chain at a decode step's few
+// tokens (2.1 us in a graph, 10.5 by a call from Python, whose host time that is).
 //
-// A lane holds two runs of RUN elements, 16 bytes each where the type and the sizes allow it: lane l of a half layout the
-// elements RUN l and on and their partners turn / 2 further, so that the rotation needs no shuffle and a lane writes what it has
-// read (in place is fine); behind the rotated part, and of neighbouring pairs, 2 RUN elements in a row. A head takes
-// dim / (2 RUN) lanes of a group of 4 to 32.
+// A lane holds two runs of RUN elements, 16 bytes each where the type and the sizes allow it: lane l of a half layout
+// the elements RUN l and on and their partners turn / 2 further, so that the rotation needs no shuffle and a lane
+// writes what it has read (in place is fine); behind the rotated part, and of neighbouring pairs, 2 RUN elements in a
+// row. A head takes dim / (2 RUN) lanes of a group of 4 to 32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -30,17 +31,18 @@ namespace {
 __device__ int g_fault_heads = 0;
 
 constexpr int WARPS = 4;        // a block
-// Heads in flight a group of lanes. us for 16 fp32 tokens / 8191 bfloat16 tokens of 40 heads of 128 (the latter in runs of
-// eight): 1 1.8 / 44.4, 2 2.1 / 38.6, 4 2.8 / 38.2; in runs of four 2 2.2 / 40.5, 4 2.8 / 37.6, 6 3.5 / 43.0. A grid that stays
-// and asks for the next position a pass ahead took 41 us.
+// Heads in flight a group of lanes. us for 16 fp32 tokens / 8191 bfloat16 tokens of 40 heads of 128 (the latter in
+// runs of eight): 1 1.8 / 44.4, 2 2.1 / 38.6, 4 2.8 / 38.2; in runs of four 2 2.2 / 40.5, 4 2.8 / 37.6, 6 3.5 / 43.0.
+// A grid that stays and asks for the next position a pass ahead took 41 us.
 constexpr int ROWS = 2;
 
-// RUN = 4 or 8 consecutive elements, aligned to 8 or 16 bytes. Plain loads: the previous grid may have written them, and in place
-// they are written here.
+// RUN = 4 or 8 consecutive elements, aligned to 8 or 16 bytes. Plain loads: the previous grid may have written them,
+// and in place they are written here.
 template <int DT, int RUN> struct Raw { uint32_t w[DT == DT_F32 ? RUN : RUN / 2]; };
 template <int DT, int RUN> __device__ __forceinline__ void load_run(const void *p, int64_t i, Raw<DT, RUN> &r) {
     constexpr int WORDS = DT == DT_F32 ? RUN : RUN / 2;
-    const uint32_t *q = DT == DT_F32 ? static_cast<const uint32_t *>(p) + i : reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + i);
+    const uint32_t *q = DT == DT_F32 ? static_cast<const uint32_t *>(p) + i
+                                     : reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + i);
     if constexpr (WORDS == 2) {
         const uint2 v = *reinterpret_cast<const uint2 *>(q);
         r.w[0] = v.x, r.w[1] = v.y;
@@ -82,7 +84,8 @@ template <int DT, int RUN> __device__ __forceinline__ void store_run(void *p, in
     else *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[RUN / 2 - 2], w[RUN / 2 - 1]);
 }
 
-// The token's position: -1 where it is skipped (a negative position, an empty sequence) or its sequence is out of range.
+// The token's position: -1 where it is skipped (a negative position, an empty sequence) or its sequence is out of
+// range.
 __device__ __forceinline__ int position(const HeadsArgs &a, int64_t i, bool report) {
     if (a.pos) return max(a.pos[i], -1);
     if (!a.has_tables) return 0;                           // no rotation: any position will do
@@ -151,7 +154,8 @@ __global__ void __launch_bounds__(WARPS * 32) heads_kernel(HeadsArgs a, int64_t 
     if (x.weight && holds)
 #pragma unroll
         for (int e = 0; e < RUN; e += 4) {
-            const float4 lo = *reinterpret_cast<const float4 *>(x.weight + at0 + e), hi = *reinterpret_cast<const float4 *>(x.weight + at1 + e);
+            const float4 lo = *reinterpret_cast<const float4 *>(x.weight + at0 + e);
+            const float4 hi = *reinterpret_cast<const float4 *>(x.weight + at1 + e);
             w[e] = lo.x, w[e + 1] = lo.y, w[e + 2] = lo.z, w[e + 3] = lo.w;
             w[RUN + e] = hi.x, w[RUN + e + 1] = hi.y, w[RUN + e + 2] = hi.z, w[RUN + e + 3] = hi.w;
         }
@@ -165,9 +169,10 @@ __global__ void __launch_bounds__(WARPS * 32) heads_kernel(HeadsArgs a, int64_t 
             const bool low = mean < 0x1p-100f;
             const bool rare = low || !(mean <= FLT_MAX);
             if (__any_sync(0xffffffffu, rare)) {
-                // Squares that pass fp32, or vanish in it beside an eps that is as small: the head by a power of two that brings its
-                // largest element to 1, eps by the square of it. (With an eps, 2^-149 or more, 2^74 is enough: what is small then
-                // is small beside eps.) A head without a largest element, or with an infinite or NaN one, stays.
+                // Squares that pass fp32, or vanish in it beside an eps that is as small: the head by a power of two
+                // that brings its largest element to 1, eps by the square of it. (With an eps, 2^-149 or more, 2^74
+                // is enough: what is small then is small beside eps.) A head without a largest element, or with an
+                // infinite or NaN one, stays.
                 float big = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 2 * RUN; ++e) big = fmaxf(big, fabsf(y[e]));
@@ -228,11 +233,17 @@ template <int XT, int OT> cudaError_t run_dim(const HeadsArgs &a, cudaStream_t s
     // runs of eight where they are 16 bytes on the way in, and both parts of a head are made of pairs of runs
     if constexpr (XT != DT_F32)
         if (a.dim % 16 == 0 && a.turn % 16 == 0)
-            return a.dim <= 64 ? run_pairs<XT, OT, 8, 4>(a, s) : a.dim <= 128 ? run_pairs<XT, OT, 8, 8>(a, s) : run_pairs<XT, OT, 8, 16>(a, s);
-    return a.dim <= 64 ? run_pairs<XT, OT, 4, 8>(a, s) : a.dim <= 128 ? run_pairs<XT, OT, 4, 16>(a, s) : run_pairs<XT, OT, 4, 32>(a, s);
+            return a.dim <= 64    ? run_pairs<XT, OT, 8, 4>(a, s)
+                   : a.dim <= 128 ? run_pairs<XT, OT, 8, 8>(a, s)
+                                  : run_pairs<XT, OT, 8, 16>(a, s);
+    return a.dim <= 64    ? run_pairs<XT, OT, 4, 8>(a, s)
+           : a.dim <= 128 ? run_pairs<XT, OT, 4, 16>(a, s)
+                          : run_pairs<XT, OT, 4, 32>(a, s);
 }
 template <int XT> cudaError_t run_out(const HeadsArgs &a, cudaStream_t s) {
-    return a.odt == DT_F32 ? run_dim<XT, DT_F32>(a, s) : a.odt == DT_F16 ? run_dim<XT, DT_F16>(a, s) : run_dim<XT, DT_BF16>(a, s);
+    return a.odt == DT_F32   ? run_dim<XT, DT_F32>(a, s)
+           : a.odt == DT_F16 ? run_dim<XT, DT_F16>(a, s)
+                             : run_dim<XT, DT_BF16>(a, s);
 }
 
 }  // namespace

@@ -1,30 +1,38 @@
-// qpack_sample.cu — the draw of the next token from its logits: temperature, top-k, top-p, min-p and a given random number.
+// qpack_sample.cu — the draw of the next token from its logits: temperature, top-k, top-p, min-p and a given random
+// number.
 //
-// The mathematics. With m the row's maximum, w_i = e^{(x_i - m) / T}. Tokens are ordered by falling logit, the lowest index
-// first among equals. Kept are: of the first k tokens, the shortest run from the top whose weights reach p of the sum over
-// those k; of these, the ones with w_i >= min_p. The token drawn is the first one in order of index where the sum of kept
-// weights passes u times their total.
+// The mathematics. With m the row's maximum, w_i = e^{(x_i - m) / T}. Tokens are ordered by falling logit, the lowest
+// index first among equals. Kept are: of the first k tokens, the shortest run from the top whose weights reach p of
+// the sum over those k; of these, the ones with w_i >= min_p. The token drawn is the first one in order of index
+// where the sum of kept weights passes u times their total.
 //
-// A token is told from its neighbour by the last place of a sum, so weights are integers: W_i = round(w_i 2^S), S = 46 or
-// as many bits fewer as keep the sum of a row below 2^63. Sums of integers do not depend on their order: the same row
-// gives the same token whatever the blocks do, and a draw differs from the one in exact arithmetic only where u lies
-// within some 2^-44 of a border between two tokens. w itself comes from 2^y by a table of 2^(j / 256) and a polynomial in two-float
-// arithmetic (a pair of fp32 whose sum is the value), to about 2^-43: fp64 would take some 20 operations of a unit that does
-// 1/64 of fp32's rate.
+// A token is told from its neighbour by the last place of a sum, so weights are integers: W_i = round(w_i 2^S), S =
+// 46 or as many bits fewer as keep the sum of a row below 2^63. Sums of integers do not depend on their order: the
+// same row gives the same token whatever the blocks do, and a draw differs from the one in exact arithmetic only
+// where u lies within some 2^-44 of a border between two tokens. w itself comes from 2^y by a table of 2^(j / 256)
+// and a polynomial in two-float arithmetic (a pair of fp32 whose sum is the value), to about 2^-43: fp64 would take
+// some 20 operations of a unit that does 1/64 of fp32's rate.
 //
-// The kept tokens are found without sorting: a histogram of counts and weights over 2048 intervals of m - x shows the interval
-// in which the k-th token or the p-th part of the sum lies, its tokens are gathered and ranked among each other; an
-// interval of too many tokens is divided again by the bits of the logits, until its tokens are few or all equal.
+// The kept tokens are found without sorting: a histogram of counts and weights over 2048 intervals of m - x shows the
+// interval in which the k-th token or the p-th part of the sum lies, its tokens are gathered and ranked among each
+// other; an interval of too many tokens is divided again by the bits of the logits, until its tokens are few or all
+// equal.
 //
-// What bounds it. A row is read from HBM once and from L2 some four times more (maximum, histogram, gathering, the sums of the
-// draw), 64 rows of 128256 fp32 logits 33 MB (156 MB through L2): 5 us at the copy rate, 70 us as it is. The passes are bound by the
-// weights' instructions (schedulers 57% busy) and by what stands between them: two barriers of the row's blocks a pass, sums over
-// 2048 intervals, a launch's cold instruction cache. One row of 32000 is all latency: 25 us.
+// What bounds it. A row is read from HBM once and from L2 some four times more (maximum, histogram, gathering, the
+// sums of the draw), 64 rows of 128256 fp32 logits 33 MB (156 MB through L2): 5 us at the copy rate, 70 to 86 us as
+// it is, by how many tokens the temperatures leave of weight. Schedulers are 57% busy, with some 220
+// thread-instructions a token, of which a weight is some 50; the rest are passes over the tokens, shared atomics, two
+// barriers of the row's blocks a pass, sums over 2048 intervals, and a launch's cold instruction cache. One row of
+// 32000 is all latency: 25 us.
 //
-// A row is split over up to 8 blocks of a cluster, which read each other's totals in shared memory, as long as all rows' blocks run
-// at once; rows enough to fill the GPU take a block of 512 threads each, two an SM (us for one row of 32000 / 64 of 128256 / 256 of
-// 32000 unfiltered / 33 of 50257 of all kinds: a block of 1024 a row 48 / 213 / 64 / 78, split 29 / 90 / 55 / 43, as it is 25 / 70 / 33 /
-// 31; as it is but with twice the blocks, of 512 threads, where a row is split 25 / 73 / 33 / 61).
+// A row is split over up to 8 blocks of a cluster, of 1024 threads, which read each other's totals in shared memory,
+// as long as there are no more blocks than SMs; other rows take one block of 512 threads, two of which fit an SM (us
+// for one row of 32000 / 64 of 128256 / 256 of 32000 unfiltered / 33 of 50257 of all kinds: a block of 1024 a row 48
+// / 213 / 64 / 78, split 29 / 90 / 55 / 43, as it is 25 / 70 / 33 / 31; as it is but with twice the blocks, of 512
+// threads, where a row is split 25 / 73 / 33 / 61). The rule has steps. us for rows of 32000 / 128256 without a
+// filter: 38 rows 30 / 41 and 39 rows 15 / 32 (152 blocks in clusters of four seem not to find their SMs all at once;
+// 78 in pairs do); 76 rows 16 / 33 and 77 rows 20 / 82 (from there on half of the SMs have a block of 512 until rows
+// fill them all); 304 rows 31 / 123 and 305 rows 45 / 164.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -72,7 +80,8 @@ struct Heat {
 };
 // round(2^places e^{(x - top) / T}) for x <= top.
 __device__ __forceinline__ unsigned long long weight(const Heat &h, const float *pow2, float x) {
-    // d = x - top in two floats, exactly; y = d log2(e) / T. Products and sums are written out, so that none is contracted.
+    // d = x - top in two floats, exactly; y = d log2(e) / T. Products and sums are written out, so that none is
+    // contracted.
     const float d = __fsub_rn(x, h.top);
     const float full = __fmul_rn(d, h.hi), y = fmaxf(full, -60.0f);
     float tail = __fmul_rn(d, h.lo);
@@ -87,7 +96,9 @@ __device__ __forceinline__ unsigned long long weight(const Heat &h, const float 
     const float *entry = pow2 + (nj & (STEPS - 1)) * 32;
     const float2 t = make_float2(entry[0], entry[STEPS * 32]);
     const int n = (nj + STEPS / 2) >> 8;
-    // 2^(r + y_lo) - 1 = a + b: ln2 z + ln2^2 / 2 z^2 + ln2^3 / 6 z^3, |z| < 2^-8.9; the next term is below 2^-42
+    // 2^(r + y_lo) - 1 = a + b: ln2 z + ln2^2 / 2 z^2 + ln2^3 / 6 z^3 + ln2^4 / 24 z^4, |z| < 2^-8.9; the next term
+    // is below 2^-54, and the limit is the rounding of the square and what follows it, together below 2^-19, to fp32:
+    // some 2^-43
     constexpr float ln2_hi = 0.693147182464599609375f, ln2_lo = -1.904654299957767e-9f;
     const float z = __fadd_rn(r, y_lo);
     const float a = __fmul_rn(ln2_hi, r);
@@ -98,8 +109,8 @@ __device__ __forceinline__ unsigned long long weight(const Heat &h, const float 
     const float c = __fmul_rn(t.x, a), sum = __fadd_rn(t.x, c);
     const float low = __fadd_rn(__fmaf_rn(t.x, a, -c), __fmaf_rn(t.x, b, __fmaf_rn(t.y, a, t.y)));
     const float rest = __fadd_rn(__fsub_rn(c, __fsub_rn(sum, t.x)), low);
-    // (sum + rest) 2^e: sum's 24 bits (from 2^-1 or 2^0 on) are a whole number where e is 24 or more, |rest| 2^e is below 2^30;
-    // where e is less the sum of both is rounded at once
+    // (sum + rest) 2^e: sum's 24 bits (from 2^-1 or 2^0 on) are a whole number where e is 24 or more, |rest| 2^e is
+    // below 2^30; where e is less the sum of both is rounded at once
     const int e = h.places + n;
     const bool whole = e >= 24;
     const float part = (whole ? 0.0f : sum) + rest;
@@ -301,9 +312,11 @@ template <int DT, int THREADS> struct Row {
     const float *pow2;          // the lane's table
 
     __device__ __forceinline__ unsigned long long weigh(float x) const { return weight(heat, pow2, x); }
-    __device__ __forceinline__ unsigned long long weigh_rare(float x) const { return weight_call(heat.hi, heat.lo, heat.top, heat.places, pow2, x); }
-    // 16 elements a thread and pass, whose loads are under way together: the passes behind the first read L2, and wait for it
-    // more than they compute.
+    __device__ __forceinline__ unsigned long long weigh_rare(float x) const {
+        return weight_call(heat.hi, heat.lo, heat.top, heat.places, pow2, x);
+    }
+    // 16 elements a thread and pass, whose loads are under way together: the passes behind the first read L2, and
+    // wait for it more than they compute.
     static constexpr int FLIGHT = 16 / VE;
     // batch(first vector, elements): from vector v on, `step` apart, to `end`
     template <class B> __device__ __forceinline__ void batches(int v, int step, int end, B batch) const {
@@ -333,8 +346,8 @@ template <int DT, int THREADS> struct Row {
         for (int i = 0; i < 16; ++i) m |= x[i / VE][i % VE] >= limit && x[i / VE][i % VE] <= most ? 1u << i : 0u;
         return m;
     }
-    // f(vector, element of it, x) of those elements, one after the other: few of many are looked at, and a branch an element
-    // cost more than all else
+    // f(vector, element of it, x) of those elements, one after the other: few of many are looked at, and a branch an
+    // element cost more than all else
     template <class F> __device__ __forceinline__ void pick(unsigned m, int v, int step, F f) const {
         while (m) {
             const int i = __ffs(m) - 1, vec = v + i / VE * step;
@@ -343,8 +356,8 @@ template <int DT, int THREADS> struct Row {
         }
     }
 
-    // Counts the intervals' tokens, or (WEIGH) adds up their weights, of which those below `least` are left out. Returns the
-    // thread's sum of all weights above iv.floor.
+    // Counts the intervals' tokens, or (WEIGH) adds up their weights, of which those below `least` are left out.
+    // Returns the thread's sum of all weights above iv.floor.
     template <bool WEIGH> __device__ __forceinline__ unsigned long long fill(const Intervals &iv, unsigned long long least) {
         for (int i = threadIdx.x; i < BINS; i += THREADS) {
             if (WEIGH) s.sums[i] = make_uint2(0, 0);
@@ -382,13 +395,15 @@ template <int DT, int THREADS> struct Row {
         return sum;
     }
 
-    // The thread's intervals of all blocks: counts, or weights. All blocks' words are asked for before the first is added.
+    // The thread's intervals of all blocks: counts, or weights. All blocks' words are asked for before the first is
+    // added.
     __device__ __forceinline__ void counts_of(unsigned long long (&n)[PER]) const {
 #pragma unroll
         for (int i = 0; i < PER; i += 2) {
             uint2 x[MOST_BLOCKS];
 #pragma unroll
-            for (unsigned r = 0; r < MOST_BLOCKS; ++r) x[r] = r < c.size ? c.read2(&s.count[PER * threadIdx.x + i], r) : make_uint2(0, 0);
+            for (unsigned r = 0; r < MOST_BLOCKS; ++r)
+                x[r] = r < c.size ? c.read2(&s.count[PER * threadIdx.x + i], r) : make_uint2(0, 0);
             n[i] = n[i + 1] = 0;
 #pragma unroll
             for (unsigned r = 0; r < MOST_BLOCKS; ++r) n[i] += x[r].x, n[i + 1] += x[r].y;
@@ -399,17 +414,19 @@ template <int DT, int THREADS> struct Row {
         for (int i = 0; i < PER; ++i) {
             uint2 x[MOST_BLOCKS];
 #pragma unroll
-            for (unsigned r = 0; r < MOST_BLOCKS; ++r) x[r] = r < c.size ? c.read2(&s.sums[PER * threadIdx.x + i].x, r) : make_uint2(0, 0);
+            for (unsigned r = 0; r < MOST_BLOCKS; ++r)
+                x[r] = r < c.size ? c.read2(&s.sums[PER * threadIdx.x + i].x, r) : make_uint2(0, 0);
             n[i] = 0;
 #pragma unroll
             for (unsigned r = 0; r < MOST_BLOCKS; ++r) n[i] += static_cast<unsigned long long>(x[r].y) << 32 | x[r].x;
         }
     }
 
-    // Finds the token at which the running count (or weight) from the top reaches `goal`: its key, and how many of the tokens of
-    // that key are kept (s.found_key, s.found_ties). The intervals are filled. Every thread of all blocks calls it.
-    // `apart`: the blocks have not met since.
-    template <bool WEIGH> __device__ __forceinline__ void select(Intervals iv, unsigned long long goal, unsigned long long least, bool apart) {
+    // Finds the token at which the running count (or weight) from the top reaches `goal`: its key, and how many of
+    // the tokens of that key are kept (s.found_key, s.found_ties). The intervals are filled. Every thread of all
+    // blocks calls it. `apart`: the blocks have not met since.
+    template <bool WEIGH>
+    __device__ __forceinline__ void select(Intervals iv, unsigned long long goal, unsigned long long least, bool apart) {
         const int tid = threadIdx.x;
         unsigned long long above = 0;                      // counts or weights above the intervals
         for (;; apart = true) {
@@ -480,7 +497,8 @@ template <int DT, int THREADS> struct Row {
                         same += o == k;
                     }
                     const unsigned long long w = WEIGH ? s.weights[t] : 1;
-                    if (over < goal && goal <= over + same * w) s.found_key = k, s.found_ties = unsigned((goal - over + w - 1) / w);
+                    if (over < goal && goal <= over + same * w)
+                        s.found_key = k, s.found_ties = unsigned((goal - over + w - 1) / w);
                 }
                 break;
             }
@@ -509,12 +527,14 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
     if (tid == 0) s.best = 0, s.bad = 0, s.first = 0xFFFFFFFFu, s.share = -1;
     pdl_launch_dependents();
     pdl_wait();
-    Row<DT, THREADS> row = {s, c, Logits<DT>(static_cast<const unsigned char *>(a.logits) + b * a.ld * Logits<DT>::ES, int(a.vocab)), 0, 0, {}, &s.pow2[0][0][lane]};
+    const unsigned char *const logits = static_cast<const unsigned char *>(a.logits) + b * a.ld * Logits<DT>::ES;
+    Row<DT, THREADS> row = {s, c, Logits<DT>(logits, int(a.vocab)), 0, 0, {}, &s.pow2[0][0][lane]};
     const int share = (row.logits.vectors + int(c.size) - 1) / int(c.size);
     row.v0 = min(int(c.rank) * share, row.logits.vectors), row.v1 = min(row.v0 + share, row.logits.vectors);
     const float given = a.temperature ? a.temperature[b] : 1.0f, heat_t = given > 0x1p64f ? 0x1p64f : given;
     const int k = a.top_k ? a.top_k[b] : 0;
-    const float p = a.top_p ? a.top_p[b] : 1.0f, min_p = a.min_p ? a.min_p[b] : 0.0f, u = fminf(fmaxf(a.u[b], 0.0f), 0x1.fffffep-1f);
+    const float p = a.top_p ? a.top_p[b] : 1.0f, min_p = a.min_p ? a.min_p[b] : 0.0f;
+    const float u = fminf(fmaxf(a.u[b], 0.0f), 0x1.fffffep-1f);
     __syncthreads();
 
     // -- the maximum ----------------------------------------------------------------------------------------------
@@ -537,7 +557,9 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
         // a token without a draw: none, or the lowest index of the maximum
         if (!bad && best) {
             row.batches(row.v0 + tid, THREADS, row.v1, [&](int v, const float (&x)[Row<DT, THREADS>::FLIGHT][VE]) {
-                row.pick(row.reach(top, x), v, THREADS, [&](int vec, int e, float) { atomicMin(&s.first, unsigned(row.logits.index(vec) + e)); });
+                row.pick(row.reach(top, x), v, THREADS, [&](int vec, int e, float) {
+                    atomicMin(&s.first, unsigned(row.logits.index(vec) + e));
+                });
             });
             c.sync();
         }
@@ -551,7 +573,7 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
         if (c.size > 1) c.sync();                          // none leaves while another reads its memory
         return;
     }
-    {                                                      // log2(e) / T in two floats: fp64 would take 4 us of a block's threads
+    {                                      // log2(e) / T in two floats: fp64 would take 4 us of a block's threads
         constexpr float log2e_hi = 1.44269502162933349609375f, log2e_lo = 1.925963033500e-8f;
         row.heat.hi = __fdiv_rn(log2e_hi, heat_t);
         row.heat.lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-row.heat.hi, heat_t, log2e_hi), log2e_lo), heat_t);
@@ -563,7 +585,7 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
     // -- the last token kept by top-k and top-p ---------------------------------------------------------------
     bool cut_k = k > 0 && k < a.vocab;
     const bool cut_p = p < 1.0f;
-    unsigned last_ties = 0;                                // kept: logits above the last one, and so many equal to it (0: nothing cut)
+    unsigned last_ties = 0;                // kept: logits above the last one, and so many equal to it (0: nothing cut)
     float last = -INFINITY;
     if (cut_k || cut_p) {
         Intervals iv = {row.heat.top, BINS / fmaxf(32.0f, 32.0f * heat_t), 0, 0, -1, -INFINITY};
@@ -584,10 +606,11 @@ template <int DT, int THREADS> __global__ void __launch_bounds__(THREADS, 1024 /
             }
         }
         if (cut_p) {
-            // The sum of the tokens kept so far, and their weights by intervals. Tokens whose weight is below (1 - p) / 2 of the
-            // largest over their number stay below (1 - p) / 2 of the sum all together: they are behind the last one kept, and
-            // are left out.
-            const unsigned long long least = max(1ull, part_of(fminf((1.0f - fmaxf(p, 0.0f)) * 0.5f, 0.5f), one, false) / a.vocab);
+            // The sum of the tokens kept so far, and their weights by intervals. Tokens whose weight is below (1 - p)
+            // / 2 of the largest over their number stay below (1 - p) / 2 of the sum all together: they are behind
+            // the last one kept, and are left out.
+            const float beyond = fminf((1.0f - fmaxf(p, 0.0f)) * 0.5f, 0.5f);
+            const unsigned long long least = max(1ull, part_of(beyond, one, false) / a.vocab);
             unsigned long long sum = row.template fill<true>(iv, least), total;
             block_sum<WARPS>(sum, s.scan64, &total);
             if (tid == 0) s.sum = total;

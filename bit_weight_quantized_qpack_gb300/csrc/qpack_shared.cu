@@ -47,8 +47,8 @@ cudaError_t launch_kv_attend_shared(const SharedArgs &a, cudaStream_t s) {
     shared::Params p = {};
     p.a = a;
     p.G = a.q_heads / a.pool.heads;
-    // Queries of the products' own type that are not rotated are one term as they stand (a power of two that they are scaled
-    // by changes no bit of an fp16 query that is not subnormal after it; see the kernel).
+    // Queries of the products' own type that are not rotated are one term as they stand (a power of two that they are
+    // scaled by changes no bit of an fp16 query that is not subnormal after it; see the kernel).
     const bool bf = a.pool.type == QPACK_KV_BF16;
     p.a.q_terms = !a.rope && a.qdt == (bf ? QPACK_BF16 : QPACK_F16) ? 1 : 2;
     shared::lay_out(a.pool, a.B, a.q_heads, static_cast<unsigned char *>(a.ws), p.w);

@@ -1,36 +1,43 @@
-// qpack_shared.cuh — attention of one new token a row where groups of rows share a prefix: the kernels over the prefixes and
-// for the joins, instantiated per cache type in qpack_shared_i8.cu, qpack_shared_f16.cu and qpack_shared_bf16.cu.
+// qpack_shared.cuh — attention of one new token a row where groups of rows share a prefix: the kernels over the
+// prefixes and for the joins, instantiated per cache type in qpack_shared_i8.cu, qpack_shared_f16.cu and
+// qpack_shared_bf16.cu.
 //
-// The mathematics. Row b of group g sees the tokens 0 .. L_b - 1, of which the first P_g are those of the group's first row. For
-// any split of a row's tokens into sets S with m_S = max s_t, l_S = sum e^(s_t - m_S), o_S = sum e^(s_t - m_S) v_t, the whole is
+// The mathematics. Row b of group g sees the tokens 0 .. L_b - 1, of which the first P_g are those of the group's
+// first row. For any split of a row's tokens into sets S with m_S = max s_t, l_S = sum e^(s_t - m_S), o_S = sum
+// e^(s_t - m_S) v_t, the whole is
 //     out = sum_S e^(m_S - m) o_S / sum_S e^(m_S - m) l_S,    m = max m_S,    lse = m + log(sum_S e^(m_S - m) l_S).
-// So three launches: o, m and l over the prefixes, for all queries of a group that a key/value head serves in one product; over
-// what rows have of their own, by the cache's attention from token P_g on (qpack_attend.cuh); and the joins.
+// So three launches: o, m and l over the prefixes, for all queries of a group that a key/value head serves in one
+// product; over what rows have of their own, by the cache's attention from token P_g on (qpack_attend.cuh); and the
+// joins.
 //
-// What bounds it. A group has R = rows x query heads a key/value head queries, for which each element of its prefix is
-// multiplied and added R times: with 8-bit elements the tensor cores at their rate take as long as HBM at R = 142. Neither is
-// reached; what limits the prefix kernel is the chain scores -> maximum -> weights -> values: for two blocks of 128 queries
-// some 4.5k clocks a tile of 128 tokens (5.2k where the maximum is found before the weights, of which those are 2.7k and each
-// product of 128 x 128 x 128 is 0.65k, the rest hand-overs between warps; the tensor pipe 29% busy then, the schedulers 50%).
-// 32 rows of 65531 tokens, 64 heads over 8, 8 bits: 99 us for 68.7 GFLOP, 36% of the measured bf16 rate; 64 rows of 7999, 32
-// over 8: 26 us, of which some 12 are the call's start (plan, queries, first tiles) and the results' way out. A call of a few
-// rows takes three launches' latency, 20 us.
+// What bounds it. A group has R = rows x query heads a key/value head queries, for which each element of its prefix
+// is multiplied and added R times: with 8-bit elements the tensor cores at their rate take as long as HBM at R = 142.
+// Neither is reached; what limits the prefix kernel is the chain scores -> maximum -> weights -> values: for two
+// blocks of 128 queries some 3.8 us a tile of 128 tokens (products of 128 x 128 x 128 are 0.65k clocks each, two for
+// the scores and, of two terms, four for the values; weights with their maximum some 2.7k; the rest hand-overs
+// between warps; the tensor pipe is 42% busy, the schedulers 58%). 32 rows of 65531 tokens, 64 heads over 8, 8 bits:
+// 115 us for 68.7 GFLOP, 32% of the measured bf16 rate; 64 rows of 7999, 32 over 8: 26 us, of which some 12 are the
+// call's start (plan, queries, first tiles) and the results' way out. A call of a few rows takes three launches'
+// latency, 20 us.
 //
-// Layout. One block an SM, 17 warps: loaders bring tiles of keys and values into a ring of 128-byte-swizzled operands (8-bit codes
-// are unpacked to fp16(scale code) on the way, which is what the cache stands for), one warp issues the products on tcgen05, two
-// groups of four hold a query a thread, take scores from tensor memory, and put the weights back over them as the A operand of the
-// second product, so that neither leaves the SM nor passes through shared memory. Units, a tile for one block of queries, are cut
-// evenly over the blocks whatever the groups' lengths; a block that gets part of a prefix leaves a piece.
-//   A tile at a time by all warps took 760 us for the 65531 tokens, roles of their own 226, codes staged asynchronously 180,
-// addresses by a lane a row 150, products issued by a converged warp and two teams of loaders 140, the joins' warps 132,
-// weights by the maximum that there is 123, queries' lines asked for ahead 119. Slower: halves of 64 tokens with two score
-// buffers a group (149 against 137), one team (150), rows' own tokens attended to within the join (fp32, a lane a token out of
-// shared memory: 28 us more for 64 rows of up to 200).
+// Layout. One block an SM, 17 warps: loaders bring tiles of keys and values into a ring of 128-byte-swizzled operands
+// (8-bit codes are unpacked to fp16(scale code) on the way, which is what the cache stands for), one warp issues the
+// products on tcgen05, two groups of four hold a query a thread, take scores from tensor memory, and put the weights
+// back over them as the A operand of the second product, so that neither leaves the SM nor passes through shared
+// memory. Units, a tile for one block of queries, are cut evenly over the blocks whatever the groups' lengths; a
+// block that gets part of a prefix leaves a piece.
+//   A tile at a time by all warps took 760 us for the 65531 tokens, roles of their own 226, codes staged
+// asynchronously 180, addresses by a lane a row 150, products issued by a converged warp and two teams of loaders
+// 140, the joins' warps 132 (weights of one term); with weights of two terms and queries' lines asked for ahead it is
+// 137. Slower, with one term: halves of 64 tokens with two score buffers a group (149 against 137), one team (150),
+// rows' own tokens attended to within the join (fp32, a lane a token out of shared memory: 28 us more for 64 rows of
+// up to 200).
 //
-// Terms. fp32 queries (and rotated ones of 16 bits) are two 16-bit terms; a second term of the queries doubles that product, and
-// blocks of 128 queries are then taken one at a time. Weights are always two: of one (fp16: 11 bits, off by up to 2^-11 against
-// the sum, which is of unrounded weights) a 16-bit output showed the error, 2.3e-4 to 2.5e-4 of it where its own rounding alone is
-// 2.1e-4. us a call, one term / two: 64 rows of 7999 tokens 49.2 / 50.2, 32 of 65531 124 / 141, heads of 256 45.1 / 45.9.
+// Terms. fp32 queries (and rotated ones of 16 bits) are two 16-bit terms; a second term of the queries doubles that
+// product, and blocks of 128 queries are then taken one at a time. Weights are always two: of one (fp16: 11 bits, off
+// by up to 2^-11 against the sum, which is of unrounded weights) a 16-bit output showed the error, 2.3e-4 to 2.5e-4
+// of it where its own rounding alone is 2.1e-4. us a call, one term / two: 64 rows of 7999 tokens 49.2 / 50.2, 32 of
+// 65531 124 / 141, heads of 256 45.1 / 45.9.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -44,16 +51,16 @@
 namespace qpack {
 namespace shared {
 
-constexpr int ROWS = 128;                   // queries of a product: (row, query head) pairs of a group and key/value head
+constexpr int ROWS = 128;           // queries of a product: (row, query head) pairs of a group and key/value head
 constexpr int MAX_GROUPS = 512;
 constexpr int MAX_BATCH = 4096;
 
-// Warps: two softmax groups of four (a warp reads the quarter of the tensor memory's lanes that its number mod 4 gives), the
-// loaders, the one that issues the products.
+// Warps: two softmax groups of four (a warp reads the quarter of the tensor memory's lanes that its number mod 4
+// gives), the loaders, the one that issues the products.
 constexpr int SOFT = 4, LOADERS = 8, MMA_WARP = 2 * SOFT + LOADERS;
 constexpr int THREADS = (MMA_WARP + 1) * 32, LOAD_THREADS = LOADERS * 32;
 
-// Where results go between the launches of a call. Written by the prefix kernel's first block: the plan of the call.
+// Where results go between the launches of a call. Written by the prefix kernel's last block: the plan of the call.
 struct Plan {
     int size, item;                         // units of a block; queries that a block takes together
     int cum[MAX_GROUPS + 1];                // units before group g
@@ -80,19 +87,21 @@ template <int KT, int D> struct Cfg {
     static constexpr bool BF = KT == QPACK_KV_BF16, I8 = KT == QPACK_KV_I8;
     static constexpr bool TWO = D <= 128;                  // two accumulators fit the tensor memory beside two tiles' scores
     static constexpr int TOK = D == 256 ? 64 : 128;        // tokens of a tile
-    // Loaders take a tile together, or, where they convert it, in two teams that take them in turn: with one, the waits and
-    // latencies of a tile had nothing to pass under.
+    // Loaders take a tile together, or, where they convert it, in two teams that take them in turn: with one, the
+    // waits and latencies of a tile had nothing to pass under.
     static constexpr int TEAMS = I8 ? 2 : 1, TEAM = LOAD_THREADS / TEAMS;
     static constexpr int BLOCKS = D / 64;                  // 128-byte columns of an operand
     static constexpr int QB = ROWS * 128, KB = TOK * 128;  // bytes of a column of queries, of a tile
     static constexpr int Q_BYTES = BLOCKS * QB, TILE_BYTES = BLOCKS * KB;
-    // TMEM columns: accumulators of the output, two tiles' scores. The probabilities of 32 tokens go over their scores: 16
-    // columns of first terms, 16 of second ones.
+    // TMEM columns: accumulators of the output, two tiles' scores. The probabilities of 32 tokens go over their
+    // scores: 16 columns of first terms, 16 of second ones.
     static constexpr int O_COL = 0, O_STEP = D, S_COL = 256, S_STEP = TOK;
-    // Probabilities are held as 2^(x - m + BIAS), at most 2^(BIAS + GROW): m is a maximum that lags behind by up to GROW.
+    // Probabilities are held as 2^(x - m + BIAS), at most 2^(BIAS + GROW): m is a maximum that lags behind by up to
+    // GROW.
     static constexpr float BIAS = BF ? 0.0f : 7.0f, GROW = 8.0f;      // (fp16 ends at 2^16)
-    // Shared memory: the queries (one or two operands), 8-bit codes on their way (a tile a team), a ring of tiles of 16-bit keys or
-    // values, the plan and the barriers. The results of a segment are put together over the first three.
+    // Shared memory: the queries (one or two operands), 8-bit codes on their way (a tile a team), a ring of tiles of
+    // 16-bit keys or values, the plan and the barriers. The results of a segment are put together over the first
+    // three.
     static constexpr int SMEM = 227 * 1024, REST = (MAX_GROUPS + 1) * 4 + (TWO ? 2 : 1) * ROWS * 4 + 256;
     static constexpr int RAW_BYTES = TOK * D, RAW_ALL = I8 ? TEAMS * RAW_BYTES : 0;
     static constexpr int ring(int operands) {
@@ -111,18 +120,20 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// The products are issued by one lane of a warp that runs through their code as a whole: all they are given is the same for
-// the warp then, and lies where the instruction wants it (one lane alone in a branch took 135 clocks a product).
+// The products are issued by one lane of a warp that runs through their code as a whole: all they are given is the
+// same for the warp then, and lies where the instruction wants it (one lane alone in a branch took 135 clocks a
+// product).
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r;
 }
-// Descriptors are given by their low words: between operands and steps only the address field there changes, and one addition
-// a descriptor is what the issuing warp can do beside a product. High word: 1024 bytes between groups of rows, version 1,
-// 128-byte swizzle.
+// Descriptors are given by their low words: between operands and steps only the address field there changes, and one
+// addition a descriptor is what the issuing warp can do beside a product. High word: 1024 bytes between groups of
+// rows, version 1, 128-byte swizzle.
 constexpr uint32_t DESC_HI = 1024 >> 4 | 1u << 14 | 2u << 29;
-__device__ __forceinline__ void umma_ss(uint32_t one, uint32_t d_tmem, uint32_t adesc, uint32_t bdesc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void umma_ss(uint32_t one, uint32_t d_tmem, uint32_t adesc, uint32_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
@@ -134,7 +145,8 @@ __device__ __forceinline__ void umma_ss(uint32_t one, uint32_t d_tmem, uint32_t 
         : "memory");
 }
 // A (128 x 16, in TMEM) times B.
-__device__ __forceinline__ void umma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint32_t bdesc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void umma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint32_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
@@ -191,14 +203,17 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Low words of operand descriptors with 128-byte swizzle, groups of eight rows of 128 bytes 1024 bytes apart: rows of 64
-// elements of the product's sum (queries, keys); rows that run along the sum themselves (values by tokens), whose columns of 64
-// elements lie `column` bytes apart.
+// Low words of operand descriptors with 128-byte swizzle, groups of eight rows of 128 bytes 1024 bytes apart: rows of
+// 64 elements of the product's sum (queries, keys); rows that run along the sum themselves (values by tokens), whose
+// columns of 64 elements lie `column` bytes apart.
 __device__ __forceinline__ uint32_t desc_k(uint32_t smem_addr) { return (smem_addr >> 4 & 0x3FFFu) | 1u << 16; }
-__device__ __forceinline__ uint32_t desc_mn(uint32_t smem_addr, uint32_t column) { return (smem_addr >> 4 & 0x3FFFu) | column >> 4 << 16; }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t smem_addr, uint32_t column) {
+    return (smem_addr >> 4 & 0x3FFFu) | column >> 4 << 16;
+}
 // Instruction descriptors, kind::f16: fp32 sums, M = 128, N, B's layout.
 template <bool BF, int N, bool MN> constexpr uint32_t kIdesc =
-    (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (MN ? 1u << 16 : 0u) | (uint32_t(N >> 3) << 17) | (uint32_t(ROWS >> 4) << 24);
+    (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (MN ? 1u << 16 : 0u) | (uint32_t(N >> 3) << 17) |
+    (uint32_t(ROWS >> 4) << 24);
 
 // A pair of fp32 as a pair of 16-bit terms, x in the low half, and what they leave.
 template <bool BF> __device__ __forceinline__ uint32_t pack2(float x, float y) {
@@ -296,7 +311,8 @@ template <int N> __device__ __forceinline__ void load_q(const void *p, int dt, i
     }
 }
 
-// A bounded wait of a whole warp, which gives up together: lanes that did alone would leave the others in the shuffles behind it.
+// A bounded wait of a whole warp, which gives up together: lanes that did alone would leave the others in the
+// shuffles behind it.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
 }
@@ -355,10 +371,12 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
         }
     }
     const int tiles = (length + TOK - 1) / TOK, queries = rows * p.G;
-    // Two blocks of queries at a time share a tile's conversion and its way from L2, where queries are one term each (with two
-    // the products take longer than either) and every block gets enough tiles to pay for twice the queries and results.
-    const int most = TWO && a.q_terms == 1 ? __syncthreads_or(queries > ROWS && int64_t(tiles) * ((queries + 2 * ROWS - 1) / (2 * ROWS)) *
-                                                              a.pool.heads >= 6 * int64_t(gridDim.x)) : (__syncthreads(), 0);
+    // Two blocks of queries at a time share a tile's conversion and its way from L2, where queries are one term each
+    // (with two the products take longer than either) and every block gets enough tiles to pay for twice the queries
+    // and results.
+    const bool pays = queries > ROWS && int64_t(tiles) * ((queries + 2 * ROWS - 1) / (2 * ROWS)) * a.pool.heads >=
+                                            6 * int64_t(gridDim.x);
+    const int most = TWO && a.q_terms == 1 ? __syncthreads_or(pays) : (__syncthreads(), 0);
     const int item = most ? 2 * ROWS : ROWS;
     const bool ok = *s_ok;
     const int units = ok ? tiles * ((queries + item - 1) / item) * a.pool.heads : 0;
@@ -415,7 +433,8 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
     uint8_t *const ring = raw + F::RAW_ALL;
     const uint32_t ring32 = smem_u32(ring);
     const int shift = 31 - __clz(a.pool.page_tokens);
-    Slot load = {I8 && warp >= 2 * SOFT + LOADERS / 2 ? 1 : 0, 0}, keys = {0, 0}, values = {0, 0};    // of the loaders; of the products
+    Slot load = {I8 && warp >= 2 * SOFT + LOADERS / 2 ? 1 : 0, 0};         // of the loaders
+    Slot keys = {0, 0}, values = {0, 0};                   // of the products
     int s_phase = 0, s_phase1 = 0, p_phase = 0, p_phase1 = 0, pv_phase = 0, o_phase = 0;
     bool dead = false;
     for (int unit = unit0;;) {
@@ -427,7 +446,8 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
         }
         const int live = min(item, sg.rows * p.G - sg.mb * item);   // queries there are
         const bool dual = live > ROWS;                     // two blocks of queries, each with its softmax group; else one, whose
-                                                           // tiles the groups take in turn (where there are two accumulators)
+                                                           // tiles the groups take in turn (where there are two
+                                                           // accumulators)
         const int nt = sg.nt, jobs = dual ? 2 * nt : nt;
         int lim = sg.length;                               // tokens that this thread's query sees (softmax groups)
         float f = 0.0f, m = -INFINITY, l = 0.0f;           // its scale, running maximum and sum
@@ -448,7 +468,8 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                         my_pos = -1;
                     }
                 }
-                // all passes' lines are asked for first: registers for their loads there are not (heads of 256: nothing gained)
+                // all passes' lines are asked for first: registers for their loads there are not (heads of 256:
+                // nothing gained)
                 if (D <= 128)
 #pragma unroll 1
                 for (int it = 0; it * 32 < top; ++it) {
@@ -497,22 +518,26 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     for (int e = 0; e < N; ++e) big = fmaxf(big, fmaxf(fabsf(x[0][e]), fabsf(x[1][e])));
 #pragma unroll
                     for (int o = 4; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-                    // a power of two that brings the maximum to [2^13, 2^14), within fp32's normal range; 1 for zero, inf and NaN,
-                    // and for bfloat16 terms. The scale's sign goes with it, so that the largest score is the largest sum.
+                    // a power of two that brings the maximum to [2^13, 2^14), within fp32's normal range; 1 for zero,
+                    // inf and NaN, and for bfloat16 terms. The scale's sign goes with it, so that the largest score
+                    // is the largest sum.
                     const int ex = __float_as_int(big) >> 23;
                     const int up = BF || big == 0.0f || ex == 255 ? 127 : min(254, 267 - ex);
                     const float g = __int_as_float((up << 23) | (__float_as_int(a.scale) & 0x80000000));
                     const float back = __int_as_float(max(254 - up, 1) << 23);
                     const float factor = fabsf(a.scale) * 1.4426950408889634f * back * (up == 254 ? 0.5f : 1.0f);
-                    // An infinite query is NaN, whatever signs its scores have: were all of them -inf, they would count as none.
-                    if (sub == 0) x_scale[r] = ex == 255 ? __int_as_float(0x7FC00000) : factor == 0.0f ? 0x1p-126f : factor;
+                    // An infinite query is NaN, whatever signs its scores have: were all of them -inf, they would
+                    // count as none.
+                    if (sub == 0)
+                        x_scale[r] = ex == 255 ? __int_as_float(0x7FC00000) : factor == 0.0f ? 0x1p-126f : factor;
                     const int block = r / ROWS, row = r % ROWS;
 #pragma unroll
                     for (int s = 0; s < 2; ++s)
 #pragma unroll
                         for (int e = 0; e < N; e += 4) {
                             const int d = s * (D / 2) + sub * N + e;
-                            uint8_t *to = sm + block * F::Q_BYTES + (d / 64) * F::QB + sw128_off(row, (d % 64) / 8) + (d % 8) * 2;
+                            uint8_t *to = sm + block * F::Q_BYTES + (d / 64) * F::QB + sw128_off(row, (d % 64) / 8) +
+                                          (d % 8) * 2;
                             const float y[4] = {x[s][e] * g, x[s][e + 1] * g, x[s][e + 2] * g, x[s][e + 3] * g};
                             const uint2 h = make_uint2(pack2<BF>(y[0], y[1]), pack2<BF>(y[2], y[3]));
                             *reinterpret_cast<uint2 *>(to) = h;
@@ -545,8 +570,8 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                         const uint32_t qd = desc_k(base + (term + mb) * F::Q_BYTES);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            umma_ss(one, to, qd + ((k / 4) * F::QB + (k % 4) * 32) / 16, kd + ((k / 4) * F::KB + (k % 4) * 32) / 16,
-                                     kIdesc<BF, TOK, false>, term || k);
+                            umma_ss(one, to, qd + ((k / 4) * F::QB + (k % 4) * 32) / 16,
+                                    kd + ((k / 4) * F::KB + (k % 4) * 32) / 16, kIdesc<BF, TOK, false>, term || k);
                     }
                     commit(one, &s_full[j & 1]);
                     if (!dual || mb == 1) {
@@ -568,13 +593,14 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     if (dead) break;
                     tc_fence_after();
                     const uint32_t vd = desc_mn(ring32 + values.at * F::TILE_BYTES, F::KB);
-                    const uint32_t o = tmem + F::O_COL + (TWO ? (j & 1) * F::O_STEP : 0), w = tmem + F::S_COL + (j & 1) * F::S_STEP;
+                    const uint32_t o = tmem + F::O_COL + (TWO ? (j & 1) * F::O_STEP : 0);
+                    const uint32_t w = tmem + F::S_COL + (j & 1) * F::S_STEP;
                     const bool more = TWO ? j > 1 : j > 0; // the accumulators hold something
                     for (int term = 0; term < 2; ++term)
 #pragma unroll
                         for (int k = 0; k < TOK / 16; ++k)
-                            umma_ts(one, o, w + (k / 2) * 32 + term * 16 + (k % 2) * 8, vd + k * (2048 / 16), kIdesc<BF, D, true>,
-                                        more || term || k);
+                            umma_ts(one, o, w + (k / 2) * 32 + term * 16 + (k % 2) * 8, vd + k * (2048 / 16),
+                                    kIdesc<BF, D, true>, more || term || k);
                     if (!dual || mb == 1) {
                         commit(one, &empty[values.at]);
                         // the last values come right behind their predecessor where tiles are taken in turn
@@ -591,8 +617,8 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
             // ------------------------------------- loaders -------------------------------------
             const int team = (warp - 2 * SOFT) / (LOADERS / F::TEAMS), t = tid - 2 * SOFT * 32 - team * F::TEAM;
             const int *table = a.t.tables + int64_t(sg.page_row) * a.t.stride;
-            // a segment's tiles in the order of the products: keys of the next tile before values of this one where tiles are
-            // taken in turn, keys and values of a tile else
+            // a segment's tiles in the order of the products: keys of the next tile before values of this one where
+            // tiles are taken in turn, keys and values of a tile else
             const int steps = 2 * nt;
             auto place = [&](int n, int &t0) -> bool {     // whether the n-th are values; the tile's first token
                 int tile;
@@ -603,9 +629,9 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                 t0 = (sg.tile0 + tile) * TOK;
                 return v;
             };
-            // A thread has 16 bytes of NC rows of a tile, STEP rows apart; a warp has WR rows. Where a row lies is found by one lane
-            // (lane j: the warp's j-th row) and handed to the others by shuffles: by every lane for itself it was most of the
-            // loaders' instructions.
+            // A thread has 16 bytes of NC rows of a tile, STEP rows apart; a warp has WR rows. Where a row lies is
+            // found by one lane (lane j: the warp's j-th row) and handed to the others by shuffles: by every lane for
+            // itself it was most of the loaders' instructions.
             constexpr int CPR = I8 ? D / 16 : D / 8, NC = TOK * CPR / F::TEAM, STEP = F::TEAM / CPR;
             constexpr int SUB = 32 / CPR, WR = SUB * NC;
             static_assert(WR <= 32 && STEP % 8 == 0, "a lane a row; a thread's rows lie alike in the swizzle");
@@ -635,8 +661,10 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
             auto copy = [&](int n, int page, uint32_t to, int step) {
                 int t0;
                 const bool v = place(n, t0);
-                const char *from = static_cast<const char *>(v ? a.pool.v : a.pool.k) + a.layer * a.pool.layer_stride * (I8 ? 1 : 2) + c * 16;
-                const int64_t mine = page < 0 ? -1 : (page * a.pool.page_stride + int64_t(slot_of(t0, lane)) * D) * (I8 ? 1 : 2);
+                constexpr int SIZE = I8 ? 1 : 2;
+                const char *from = static_cast<const char *>(v ? a.pool.v : a.pool.k) +
+                                   a.layer * a.pool.layer_stride * SIZE + c * 16;
+                const int64_t mine = page < 0 ? -1 : (page * a.pool.page_stride + int64_t(slot_of(t0, lane)) * D) * SIZE;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
                     const int64_t off = __shfl_sync(0xffffffffu, mine, i * SUB + lane / CPR);
@@ -644,8 +672,9 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                 }
             };
             if constexpr (I8) {
-                // A tile's codes come asynchronously into places of this thread's own, as soon as it has converted the team's tile
-                // before, while the other team's is converted; a row's scales come to the lane that found the row.
+                // A tile's codes come asynchronously into places of this thread's own, as soon as it has converted
+                // the team's tile before, while the other team's is converted; a row's scales come to the lane that
+                // found the row.
                 constexpr int WPR = D / 64;                // pairs of scales a row
                 const uint8_t *const codes = raw + team * F::RAW_BYTES + t * 16;
                 const uint32_t codes32 = smem_u32(codes);
@@ -695,12 +724,15 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                             two = c / 4 == e ? x : two;
                         }
                         const uint32_t s = __byte_perm(two, two, c & 2 ? 0x3232u : 0x1010u);
-                        const uint32_t w[4] = {(flip ? code[i].z : code[i].x) ^ 0x80808080u, (flip ? code[i].w : code[i].y) ^ 0x80808080u,
-                                               (flip ? code[i].x : code[i].z) ^ 0x80808080u, (flip ? code[i].y : code[i].w) ^ 0x80808080u};
-                        *reinterpret_cast<uint4 *>(to + off + i * (STEP * 128)) = make_uint4(
-                            dequant2(w[0], 0x4140u, s), dequant2(w[0], 0x4342u, s), dequant2(w[1], 0x4140u, s), dequant2(w[1], 0x4342u, s));
-                        *reinterpret_cast<uint4 *>(to + (off ^ 16) + i * (STEP * 128)) = make_uint4(
-                            dequant2(w[2], 0x4140u, s), dequant2(w[2], 0x4342u, s), dequant2(w[3], 0x4140u, s), dequant2(w[3], 0x4342u, s));
+                        const uint32_t w[4] = {
+                            (flip ? code[i].z : code[i].x) ^ 0x80808080u, (flip ? code[i].w : code[i].y) ^ 0x80808080u,
+                            (flip ? code[i].x : code[i].z) ^ 0x80808080u, (flip ? code[i].y : code[i].w) ^ 0x80808080u};
+                        *reinterpret_cast<uint4 *>(to + off + i * (STEP * 128)) =
+                            make_uint4(dequant2(w[0], 0x4140u, s), dequant2(w[0], 0x4342u, s),
+                                       dequant2(w[1], 0x4140u, s), dequant2(w[1], 0x4342u, s));
+                        *reinterpret_cast<uint4 *>(to + (off ^ 16) + i * (STEP * 128)) =
+                            make_uint4(dequant2(w[2], 0x4140u, s), dequant2(w[2], 0x4342u, s),
+                                       dequant2(w[3], 0x4140u, s), dequant2(w[3], 0x4342u, s));
                     }
                     arrive(load);
                     load.forward(F::TEAMS, R);
@@ -743,7 +775,7 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
             const uint32_t lanes = tmem + (uint32_t(32 * (warp % SOFT)) << 16);
             const uint32_t o = lanes + F::O_COL + (TWO ? wg * F::O_STEP : 0);
             bool any = false;                              // the accumulators hold something
-            const bool idle = (dual ? wg * ROWS : 0) + 32 * (warp % SOFT) >= live;     // no queries in this warp's lanes
+            const bool idle = (dual ? wg * ROWS : 0) + 32 * (warp % SOFT) >= live;     // no queries in its lanes
             for (int j = TWO ? wg : wg * jobs; j < jobs; j += TWO ? 2 : 1) {
                 const int left = lim - (sg.tile0 + (dual ? j >> 1 : j)) * TOK;
                 const uint32_t sc = lanes + F::S_COL + (j & 1) * F::S_STEP;
@@ -813,8 +845,8 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     if (!all) e = make_float2(c < left ? e.x : 0.0f, c + 1 < left ? e.y : 0.0f);
                     return e;
                 };
-                // two terms, 16 scores' loads under the weights of the 16 before: those of 32 tokens go over their scores, the
-                // second terms of the first 16 once the other 16 scores are here
+                // two terms, 16 scores' loads under the weights of the 16 before: those of 32 tokens go over their
+                // scores, the second terms of the first 16 once the other 16 scores are here
                 uint32_t x[16], y[16], h[8], g[8];
                 auto half = [&](int c, const uint32_t (&z)[16]) {
 #pragma unroll
@@ -856,10 +888,16 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
         // -- the segment's results: rows of shared memory, then as whole rows to the workspace ----------------------
         float *const rows_out = reinterpret_cast<float *>(sm);
         const bool whole = sg.tile0 == 0 && nt == sg.tiles;
+        auto place_of = [&](int r) -> int64_t {            // a query's row there
+            const int rr = sg.mb * item + r, b = rr / p.G, head = sg.h * p.G + rr - b * p.G;
+            return whole ? int64_t(sg.row0 + b) * a.q_heads + head
+                         : (int64_t(blockIdx.x) * 2 + (sg.tile0 == 0)) * (2 * ROWS) + r;
+        };
         if (warp < 2 * SOFT) {
             const int wg = warp / SOFT, row = tid % ROWS, r = dual ? tid : row;
             const uint32_t o = tmem + (uint32_t(32 * (warp % SOFT)) << 16) + F::O_COL + (TWO ? wg * F::O_STEP : 0);
-            // one block of queries in two accumulators: each group puts down half of the columns, then adds the other half
+            // one block of queries in two accumulators: each group puts down half of the columns, then adds the other
+            // half
             const bool merge = TWO && !dual && jobs > 1;
             float mine = 1.0f;
             if (merge) {
@@ -884,11 +922,12 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                         float4 *to = reinterpret_cast<float4 *>(rows_out + r * PS + c);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            float4 v = make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]), __uint_as_float(x[4 * i + 2]),
-                                                   __uint_as_float(x[4 * i + 3]));
+                            float4 v = make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]),
+                                                   __uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3]));
                             if (merge) {
                                 const float4 w = half ? to[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                                v = make_float4(fmaf(v.x, mine, w.x), fmaf(v.y, mine, w.y), fmaf(v.z, mine, w.z), fmaf(v.w, mine, w.w));
+                                v = make_float4(fmaf(v.x, mine, w.x), fmaf(v.y, mine, w.y), fmaf(v.z, mine, w.z),
+                                                fmaf(v.w, mine, w.w));
                             }
                             to[i] = v;
                         }
@@ -896,19 +935,17 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
                     if (merge && half == 0) named_bar_sync(2, 2 * SOFT * 32);
                 }
             // the maximum as a power of two, the probabilities' height taken off
-            if (r < live && (dual || wg == 0)) {
-                const int rr = sg.mb * item + r, b = rr / p.G, head = sg.h * p.G + rr - b * p.G;
-                const int64_t at = whole ? int64_t(sg.row0 + b) * a.q_heads + head : (int64_t(blockIdx.x) * 2 + (sg.tile0 == 0)) * (2 * ROWS) + r;
-                (whole ? p.w.direct_ml : p.w.piece_ml)[at] = make_float2(m == -INFINITY ? -INFINITY : m * f - F::BIAS, l);
-            }
+            if (r < live && (dual || wg == 0))
+                (whole ? p.w.direct_ml : p.w.piece_ml)[place_of(r)] =
+                    make_float2(m == -INFINITY ? -INFINITY : m * f - F::BIAS, l);
             tc_fence_before();
         }
         __syncthreads();
 #pragma unroll 1
         for (int i = tid; i < live * (D / 4); i += THREADS) {
-            const int r = i / (D / 4), c = i % (D / 4) * 4, rr = sg.mb * item + r, b = rr / p.G, head = sg.h * p.G + rr - b * p.G;
-            const int64_t at = whole ? int64_t(sg.row0 + b) * a.q_heads + head : (int64_t(blockIdx.x) * 2 + (sg.tile0 == 0)) * (2 * ROWS) + r;
-            *reinterpret_cast<float4 *>((whole ? p.w.direct : p.w.piece) + at * D + c) = *reinterpret_cast<const float4 *>(rows_out + r * PS + c);
+            const int r = i / (D / 4), c = i % (D / 4) * 4;
+            *reinterpret_cast<float4 *>((whole ? p.w.direct : p.w.piece) + place_of(r) * D + c) =
+                *reinterpret_cast<const float4 *>(rows_out + r * PS + c);
         }
         unit += nt;
         if (unit >= unit1) break;
@@ -931,12 +968,12 @@ template <int KT, int D> __global__ void __launch_bounds__(THREADS, 1) prefix_ke
     }
 }
 
-// The parts of a row's query head joined: prefix pieces in the order of their blocks, then what the row has of its own. A block a
-// query head: every warp finds the common maximum and sum, a part a lane, and adds up every JOIN-th part's accumulators, four
-// parts' loads at a time and the first four's under way meanwhile; the warps' sums are added in shared memory. It is bound by the
-// chain plan -> maxima -> accumulators and by how many blocks pass through an SM. us at 1 / 2 / 4 / 8 warps: 64 rows of 32 heads of
-// 128, 10 parts 6.8 / 6.5 / 7.9 / 12.5; 17 rows of 16 heads of 256, 28 parts 10.4 / 7.9 / 6.1 / 6.0 (19 by a warp that took one
-// part after another).
+// The parts of a row's query head joined: prefix pieces in the order of their blocks, then what the row has of its
+// own. A block a query head: every warp finds the common maximum and sum, a part a lane, and adds up every JOIN-th
+// part's accumulators, four parts' loads at a time and the first four's under way meanwhile; the warps' sums are
+// added in shared memory. It is bound by the chain plan -> maxima -> accumulators and by how many blocks pass through
+// an SM. us at 1 / 2 / 4 / 8 warps: 64 rows of 32 heads of 128, 10 parts 6.8 / 6.5 / 7.9 / 12.5; 17 rows of 16 heads
+// of 256, 28 parts 10.4 / 7.9 / 6.1 / 6.0 (19 by a warp that took one part after another).
 template <int D> constexpr int JOIN_WARPS = D == 256 ? 4 : 2;
 template <int D> __global__ void __launch_bounds__(JOIN_WARPS<D> * 32) join_kernel(const __grid_constant__ Params p, int tok) {
     constexpr int JOIN = JOIN_WARPS<D>, N = D / 32;        // elements a lane
@@ -950,13 +987,15 @@ template <int D> __global__ void __launch_bounds__(JOIN_WARPS<D> * 32) join_kern
     const Plan &pl = *p.w.plan;
     const float own = p.w.own_lse[i];
     const int g = pl.group[b];
-    // parts: n prefix pieces, of which the first block's is in its second place, the others' in their first; then the own one
+    // parts: n prefix pieces, of which the first block's is in its second place, the others' in their first; then the
+    // own one
     int n = 0;
     const float *piece = p.w.direct + i * D;
     const float2 *ml = p.w.direct_ml + i;
     int64_t step = 0, skip = 0;
     if (g >= 0 && pl.length[g] > 0) {
-        const int item = pl.item, size = pl.size, row0 = a.first[g], rows = a.first[g + 1] - row0, tiles = (pl.length[g] + tok - 1) / tok;
+        const int item = pl.item, size = pl.size, tiles = (pl.length[g] + tok - 1) / tok;
+        const int row0 = a.first[g], rows = a.first[g + 1] - row0;
         const int rr = (b - row0) * p.G + head - h * p.G, mb = rr / item, blocks = (rows * p.G + item - 1) / item;
         const int u0 = pl.cum[g] + (h * blocks + mb) * tiles, f0 = u0 / size;
         n = (u0 + tiles - 1) / size - f0 + 1;
@@ -1048,7 +1087,7 @@ template <int KT, int D> cudaError_t run(const Params &p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(num_sms());
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = F::SMEM;                        // above half of an SM's: one block an SM, which takes all of the tensor memory
+    cfg.dynamicSmemBytes = F::SMEM;        // above half of an SM's: one block an SM, which takes all of the tensor memory
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -1056,14 +1095,16 @@ template <int KT, int D> cudaError_t run(const Params &p, cudaStream_t s) {
     // what the rows have of their own: the cache's attention from each row's prefix on
     AttendArgs own = {};
     const SharedArgs &a = p.a;
-    own.pool = a.pool, own.t = a.t, own.seqs = a.seqs, own.q = a.q, own.ldq = a.ldq, own.rope = a.rope, own.rope_rows = a.rope_rows;
+    own.pool = a.pool, own.t = a.t, own.seqs = a.seqs, own.q = a.q, own.ldq = a.ldq;
+    own.rope = a.rope, own.rope_rows = a.rope_rows;
     own.out = p.w.own_out, own.ldo = int64_t(a.q_heads) * D, own.lse = p.w.own_lse, own.ws = a.ws, own.window = 0;
     own.scale = a.scale, own.layer = a.layer, own.B = a.B, own.q_heads = a.q_heads, own.qdt = a.qdt, own.odt = DT_F32;
     own.from = p.w.plan->from;
     if ((e = launch_kv_attend(own, s)) != cudaSuccess) return e;
-    // One after the other: blocks that come early, while their predecessors' still run, gather on the SMs that are done first and
-    // then wait there for one another's loads (64 samples / 32 rows of 65531 / 17 rows with heads of 256, us in a graph: both
-    // early 52.3 / 150.5 / 107, the attention alone 48.5 / 141 / 54.6, neither 46.5 / 135 / 54.5).
+    // One after the other: blocks that come early, while their predecessors' still run, gather on the SMs that are
+    // done first and then wait there for one another's loads (64 samples / 32 rows of 65531 / 17 rows with heads of
+    // 256, us in a graph: both early 52.3 / 150.5 / 107, the attention alone 48.5 / 141 / 54.6, neither 46.5 / 135 /
+    // 54.5).
     cfg.gridDim = dim3(unsigned(int64_t(a.B) * a.q_heads));
     cfg.blockDim = dim3(JOIN_WARPS<D> * 32);
     cfg.dynamicSmemBytes = 0;

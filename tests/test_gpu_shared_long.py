@@ -1,9 +1,9 @@
 """Attention over shared prefixes that are long enough for every form of its inner loop, against 64 bits.
 
 Which form runs goes by the queries of a group, their type and the tiles that a block of the GPU gets: two blocks of 128 queries
-at a time, or one; weights and a tile's maximum in one go, or one after the other. Lengths here are derived from the number of
-SMs, and each test states the conditions of the form that it is about, so that it cannot stop reaching it unnoticed. Tolerances
-are those of test_gpu_shared.py."""
+at a time, or one; one accumulator, or two that tiles go to in turn. Lengths here are derived from the number of SMs, and each test
+states the conditions of the form that it is about, so that it cannot stop reaching it unnoticed. Tolerances are those of
+test_gpu_shared.py."""
 import pytest
 import torch
 
@@ -63,8 +63,7 @@ def forms(D, H, G, rows, prefix, one_term):
     return pair, share if pair or not two else share // 2
 
 
-# queries' type, output's type: one term of queries where the first is the cache's own product type; one of weights where the second
-# has 16 bits and the cache is not bfloat16
+# queries' type, output's type: queries are one term where the first is the cache's own product type
 @pytest.mark.parametrize("kind,D,G,rows,qdt,odt,pair", [
     ("i8", 64, 64, 3, "f16", "f16", True), ("f16", 64, 64, 3, "f16", "f32", True), ("bf16", 64, 64, 3, "bf16", "bf16", True),
     ("i8", 128, 64, 3, "f16", "f16", True), ("f16", 128, 64, 4, "f16", "bf16", True), ("i8", 128, 33, 5, "f16", "f32", True),
