@@ -586,7 +586,8 @@ def qpack_kv_attend_shared(pool, layer, tables, q, first, prefix, seqs=None, sca
                            workspace=None, stream=None):
     """qpack_kv_attend for rows in groups that share a prefix: rows first[g] .. first[g + 1] - 1 (int32 [groups + 1]) have
     the first prefix[g] tokens (int32 [groups]) in common, which are read once, from the pages of the group's first row; the
-    rest of a row's tokens are its own. The other arguments and the result are qpack_kv_attend's. A kept workspace
+    rest of a row's tokens are its own. The other arguments and the result are qpack_kv_attend's. Faster than that call for
+    groups of some eight rows and more whose rows times prefix pass some 50000 tokens (qpack.h has times). A kept workspace
     (alloc_kv_shared_workspace) saves its allocation."""
     D, shape = pool.dim, q.shape
     q_heads = shape[1] if len(shape) == 3 else shape[-1] // D
